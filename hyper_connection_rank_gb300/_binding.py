@@ -25,11 +25,13 @@ PATH_NAMES = {0: "none", 1: "decode", 2: "prefill", 3: "general"}
 
 DTYPE_CODES = {torch.float32: HC_F32, torch.float16: HC_F16, torch.bfloat16: HC_BF16}
 
-# Every symbol include/hc_lowrank_mix.h declares.
+# Every symbol the headers in include/ declare.
 EXPORTS = ("hc_attrs_default", "hc_lowrank_mix_path", "hc_lowrank_mix_workspace_size", "hc_lowrank_mix",
            "hc_status_string", "hc_last_error", "hc_debug_wait_timeouts", "hc_debug_sigmoid_exact",
            "hc_debug_sigmoid_table", "hc_debug_sigmoid_table_f16", "hc_debug_sigmoid_table_f16_bytes", "hc_debug_wait_timeout", "hc_debug_phase_clocks", "hc_debug_sync_probe", "hc_lowrank_mix_decode_noalloc", "hc_inv_rms",
-           "hc_engram_gate")
+           "hc_engram_gate", "hc_rotary", "hc_rotary_append", "hc_paged_attention", "hc_paged_attention_workspace_size",
+           "hc_pages_workspace_size", "hc_page_copy", "hc_page_fork", "hc_page_extend", "hc_page_release",
+           "hc_page_compact")
 
 
 class HcAttrs(ctypes.Structure):
@@ -87,6 +89,21 @@ def load_library(path: str = LIB_PATH):
         L.hc_inv_rms.restype = ci
         L.hc_engram_gate.argtypes = [vp] * 5 + [i64, ci, i64, f32, ci, vp, vp]
         L.hc_engram_gate.restype = ci
+        # argument structs (include/hc_paged.h) are passed packed, as bytes
+        cp = ctypes.c_char_p
+        L.hc_rotary.argtypes = L.hc_rotary_append.argtypes = L.hc_paged_attention.argtypes = [cp, vp]
+        L.hc_paged_attention_workspace_size.argtypes = [cp]
+        L.hc_paged_attention_workspace_size.restype = sz
+        L.hc_pages_workspace_size.argtypes = [i64, ctypes.c_int32]
+        L.hc_pages_workspace_size.restype = sz
+        L.hc_page_copy.argtypes = [vp, i64, i64, i64, vp, vp, i64, vp]
+        L.hc_page_fork.argtypes = [cp, vp, ctypes.c_int32, vp, vp, i64, i64, vp, sz, vp]
+        L.hc_page_extend.argtypes = [cp, vp, vp, vp, sz, vp]
+        L.hc_page_release.argtypes = [cp, vp, vp]
+        L.hc_page_compact.argtypes = [cp, vp, vp, vp, i64, i64, vp, sz, vp]
+        for f in ("hc_rotary", "hc_rotary_append", "hc_paged_attention", "hc_page_copy", "hc_page_fork", "hc_page_extend",
+                  "hc_page_release", "hc_page_compact"):
+            getattr(L, f).restype = ci
         _lib = L
         return L
 

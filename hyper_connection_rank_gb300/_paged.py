@@ -1,0 +1,361 @@
+"""Binding of the paged-cache operators (include/hc_paged.h).
+
+Argument checks and marshalling only, as in _binding.py: every step runs in
+the CUDA kernels of libhc_lowrank_mix.so, PyTorch supplies memory and streams.
+
+Tensors of a batch, in all functions that take one:
+
+  page_table (seqs, max_pages) int32, kv_lens (seqs,) int32, cu_q (seqs + 1,) int32 or None,
+  k_cache, v_cache (num_pages, page_size, kv_heads, head_dim), any strides but a contiguous last axis
+
+``kv_lens`` counts the new tokens of the call too. ``cu_q`` bounds each sequence's rows of q; None means one new token
+for every sequence. All calls are asynchronous and may be captured in a CUDA graph.
+"""
+from __future__ import annotations
+
+import math
+import struct
+
+import torch
+
+from ._binding import DTYPE_CODES, check, lib
+
+__all__ = ["rotary_frequencies", "rotary", "rotary_append", "paged_attention", "paged_attention_workspace_size",
+           "page_copy", "page_fork", "page_extend", "page_release", "page_compact"]
+
+# The argument structs of include/hc_paged.h, field by field ("0q": padded to 8 bytes as in C).
+_ROTARY = struct.Struct("@4P5q7if0q")
+_APPEND = struct.Struct("@10P3q6q2q3q3i4iiif0q")
+_ATTENTION = struct.Struct("@9PN3q4q3q3i3i2iiiI2f0q")
+_PAGES = struct.Struct("@6P2q3i0q")
+
+
+def _is(name, t, dtype, ndim):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.dim() != ndim:
+        raise ValueError(f"{name} must be a {ndim}-dimensional CUDA tensor of dtype {dtype}")
+
+
+def _heads(name, t, dtype):
+    """A tensor of rows of heads, the last axis contiguous."""
+    _is(name, t, dtype, 3)
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+
+
+def _flat(name, t, dtype):
+    _is(name, t, dtype, 1)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _dtype_code(t):
+    code = DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _table(t):
+    _is("page_table", t, torch.int32, 2)
+    if t.shape[1] < 1:
+        raise ValueError("page_table needs at least one column")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError("rows of page_table must be contiguous")
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _batch(page_table, kv_lens, cu_q, tokens):
+    stride = _table(page_table)
+    seqs = page_table.shape[0]
+    _flat("kv_lens", kv_lens, torch.int32)
+    if kv_lens.shape[0] != seqs:
+        raise ValueError("kv_lens and page_table differ in sequences")
+    if cu_q is None:
+        if tokens != seqs:
+            raise ValueError("without cu_q every sequence has one new token")
+        return stride, seqs, 0
+    _flat("cu_q", cu_q, torch.int32)
+    if cu_q.shape[0] != seqs + 1:
+        raise ValueError("cu_q must have one entry more than there are sequences")
+    return stride, seqs, cu_q.data_ptr()
+
+
+def _caches(k_cache, v_cache, dtype):
+    _is("k_cache", k_cache, dtype, 4)
+    _is("v_cache", v_cache, dtype, 4)
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    if k_cache.stride(3) != 1 and k_cache.shape[3] > 1:
+        raise ValueError("the last axis of the caches must be contiguous")
+
+
+def _stream(t, stream, *temporaries):
+    """The stream to launch on. Memory that this call allocated on the current stream and uses on another one must not be
+    handed out again before that one is done with it."""
+    if stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    for x in temporaries:
+        if x is not None:
+            x.record_stream(stream)
+    return stream.cuda_stream
+
+
+def rotary_frequencies(rot_dim, theta=10000.0, *, scaling=None, factor=1.0, original_length=None, slow=1.0, fast=32.0,
+                       device="cuda"):
+    """The frequencies of a rotation, radians per token, and the amplitude that goes with them: (inv_freq, amplitude) for
+    ``rotary`` and ``rotary_append``. inv_freq[i] = theta ** (-2 i / rot_dim), and for contexts ``factor`` times as long as
+    those of ``original_length`` tokens that a model was trained with
+
+      scaling="linear"    every frequency divided by factor (positions are interpolated)
+      scaling="base"      theta multiplied by factor ** (rot_dim / (rot_dim - 2)): the slowest pair is interpolated, the
+                          fastest is left as it is
+      scaling="by_parts"  pairs that make fewer than ``slow`` turns in original_length are interpolated, those that make
+                          more than ``fast`` are left, those between go over from one to the other linearly in their turns;
+                          amplitude 0.1 ln(factor) + 1 (Peng et al., "YaRN: Efficient Context Window Extension of Large
+                          Language Models", section 3.2 and 3.4, whose temperature is 1 / amplitude^2)
+    """
+    if rot_dim < 2 or rot_dim % 2 or not theta > 0 or not factor >= 1:
+        raise ValueError("rot_dim must be even and positive, theta positive, factor at least 1")
+    exponent = torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim
+    amplitude = 1.0
+    if scaling == "base":
+        if rot_dim == 2:
+            raise ValueError("a single pair has no base to scale")
+        theta = theta * factor ** (rot_dim / (rot_dim - 2))
+    f = theta ** -exponent
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        if original_length is None or not 0 < slow < fast:
+            raise ValueError("by_parts needs original_length and 0 < slow < fast")
+        turns = original_length * f / (2 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device), amplitude
+
+
+def rotary(x, positions, inv_freq, *, amplitude=1.0, interleaved=False, inverse=False, out=None, stream=None):
+    """Rotate heads by their positions (hc_rotary). x: (tokens, heads, head_dim), float32, float16 or bfloat16, any token and
+    head stride; positions: (tokens,) int64 or int32; inv_freq: (rot_dim / 2,) float64 from ``rotary_frequencies``. Features
+    from rot_dim on are copied. ``inverse=True`` turns back, which also takes the gradient of the result to that of x.
+    ``out`` may be x itself."""
+    code = _dtype_code(x)
+    _heads("x", x, x.dtype)
+    _flat("inv_freq", inv_freq, torch.float64)
+    _flat("positions", positions, torch.int32 if positions.dtype == torch.int32 else torch.int64)
+    tokens, heads, dim = x.shape
+    if positions.shape[0] != tokens:
+        raise ValueError("positions and x differ in tokens")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _heads("out", out, x.dtype)
+        if out.shape != x.shape:
+            raise ValueError("out must have the shape of x")
+    xs, os = x.stride(), out.stride()
+    args = _ROTARY.pack(x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr(), tokens, xs[0], xs[1], os[0],
+                        os[1], heads, dim, 2 * inv_freq.shape[0], bool(interleaved), bool(inverse),
+                        positions.dtype == torch.int32, code, amplitude)
+    check(lib().hc_rotary(args, _stream(x, stream, out)))
+    return out
+
+
+def rotary_append(q, k, v, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, inv_freq, amplitude=1.0, interleaved=False,
+                  out=None, stream=None):
+    """Rotate a batch's new queries, and rotate its new keys and write them with the values into the cache
+    (hc_rotary_append). q: (tokens, heads, head_dim); k, v: (tokens, kv_heads, head_dim), which may be parts of one matrix.
+    Positions follow from kv_lens and cu_q. Returns the rotated queries (``out``, which may be q itself)."""
+    code = _dtype_code(q)
+    _heads("q", q, q.dtype)
+    _heads("k", k, q.dtype)
+    _heads("v", v, q.dtype)
+    _caches(k_cache, v_cache, q.dtype)
+    _flat("inv_freq", inv_freq, torch.float64)
+    tokens, heads, dim = q.shape
+    pages, page, kv_heads, cdim = k_cache.shape
+    if k.shape != v.shape or k.shape[0] != tokens or k.shape[1] != kv_heads or k.shape[2] != dim or cdim != dim:
+        raise ValueError("q, k, v and the caches differ in tokens, kv_heads or head_dim")
+    ts, seqs, cu = _batch(page_table, kv_lens, cu_q, tokens)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _heads("out", out, q.dtype)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    qs, ks, vs, os, cs = q.stride(), k.stride(), v.stride(), out.stride(), k_cache.stride()
+    args = _APPEND.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                        inv_freq.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cu, tokens, pages, ts, qs[0], qs[1],
+                        ks[0], ks[1], vs[0], vs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, page_table.shape[1], page, heads,
+                        kv_heads, dim, 2 * inv_freq.shape[0], bool(interleaved), code, amplitude)
+    check(lib().hc_rotary_append(args, _stream(q, stream, out)))
+    return out
+
+
+def _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, out, lse,
+                    workspace):
+    code = _dtype_code(q)
+    _heads("q", q, q.dtype)
+    _caches(k_cache, v_cache, q.dtype)
+    tokens, heads, dim = q.shape
+    pages, page, kv_heads, cdim = k_cache.shape
+    if cdim != dim or kv_heads < 1 or heads % kv_heads:
+        raise ValueError("heads must be a multiple of kv_heads, and head_dim that of the caches")
+    ts, seqs, cu = _batch(page_table, kv_lens, cu_q, tokens)
+    qs, cs = q.stride(), k_cache.stride()
+    os = (heads * dim, dim) if out is None else out.stride()
+    at, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return _ATTENTION.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cu,
+                           0 if out is None else out.data_ptr(), 0 if lse is None else lse.data_ptr(), at, size, tokens, pages,
+                           ts, qs[0], qs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, page_table.shape[1], page, heads,
+                           kv_heads, dim, max_q or 0, max_kv or 0, window or 0, code, flags,
+                           1.0 / math.sqrt(dim) if scale is None else scale, softcap or 0.0)
+
+
+def paged_attention_workspace_size(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, max_q=None, max_kv=None, window=0,
+                                   flags=0):
+    """Bytes of workspace that ``paged_attention`` needs for these tensors (their contents do not matter)."""
+    return lib().hc_paged_attention_workspace_size(
+        _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, None, window, 0.0, max_q, max_kv, flags, None, None,
+                        None))
+
+
+def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, scale=None, window=0, softcap=0.0, max_q=None,
+                    max_kv=None, return_lse=False, out=None, workspace=None, flags=0, stream=None):
+    """Causal attention of a batch's new tokens over their sequences in the cache (hc_paged_attention). q: (tokens, heads,
+    head_dim), any token and head stride. scale: 1 / sqrt(head_dim) by default; window > 0: only the last ``window``
+    positions are seen; softcap > 0: scores go through softcap * tanh(score / softcap). max_q, max_kv: upper bounds of the
+    new tokens of a sequence and of kv_lens, if known; they only steer speed. Returns out (tokens, heads, head_dim), and with
+    return_lse also the float32 logarithms (tokens, heads) of the sums of weights. A token that sees nothing gets zeros, and
+    minus infinity. ``workspace``: a CUDA tensor of at least ``paged_attention_workspace_size`` bytes, allocated here if
+    omitted."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _heads("out", out, q.dtype)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+    L = lib()
+    if workspace is None:
+        need = L.hc_paged_attention_workspace_size(
+            _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, out,
+                            lse, None))
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    args = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, out,
+                           lse, workspace)
+    check(L.hc_paged_attention(args, _stream(q, stream, out, lse, workspace)))
+    return (out, lse) if return_lse else out
+
+
+# ------------------------------------------------------------------------------------------------ pages --
+
+def _pool(cache):
+    """(planes, pages, bytes of a page) of a pool (planes, num_pages, ...)."""
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda or cache.dim() < 3 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous CUDA tensor (planes, num_pages, ...)")
+    planes, pages = cache.shape[:2]
+    if cache.numel() == 0:
+        raise ValueError("cache is empty")
+    return planes, pages, cache.numel() // (planes * pages) * cache.element_size()
+
+
+def _pages(page_table, lens, refs, page_size, seqs_out, need_lens=True):
+    """The new tables and counts, and the packed arguments."""
+    ts = _table(page_table)
+    seqs, width = page_table.shape
+    _flat("lens", lens, torch.int32)
+    _flat("refs", refs, torch.int32)
+    if lens.shape[0] != seqs:
+        raise ValueError("lens and page_table differ in sequences")
+    if page_size < 1:
+        raise ValueError("page_size must be positive")
+    dev = refs.device
+    table_out = torch.empty((seqs_out, width), dtype=torch.int32, device=dev)
+    lens_out = torch.empty((seqs_out,), dtype=torch.int32, device=dev) if need_lens else None
+    refs_out = torch.empty(refs.shape, dtype=torch.int32, device=dev)
+    args = _PAGES.pack(page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), table_out.data_ptr(),
+                       lens_out.data_ptr() if need_lens else 0, refs_out.data_ptr(), refs.shape[0], ts, seqs, width, page_size)
+    return args, table_out, lens_out, refs_out
+
+
+def _pages_workspace(refs, seqs):
+    n = lib().hc_pages_workspace_size(refs.shape[0], seqs)
+    return torch.empty(n, dtype=torch.uint8, device=refs.device), n
+
+
+def page_copy(cache, src, dst, *, stream=None):
+    """Copy pages within a pool (hc_page_copy): cache[:, dst[i]] = cache[:, src[i]]. cache: (planes, num_pages, ...), where
+    the planes are the layers' keys and values; src, dst: int32. The dst are distinct and none is a src; entries outside the
+    pool are passed over. Returns cache."""
+    planes, pages, size = _pool(cache)
+    _flat("src", src, torch.int32)
+    _flat("dst", dst, torch.int32)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst differ in length")
+    check(lib().hc_page_copy(cache.data_ptr(), planes, pages, size, src.data_ptr(), dst.data_ptr(), src.shape[0],
+                             _stream(cache, stream)))
+    return cache
+
+
+def page_fork(cache, page_table, lens, refs, parents, *, page_size=None, stream=None):
+    """New sequences that go on from others, as after a step of beam search (hc_page_fork): new sequence i continues
+    parents[i] (-1: it is empty), the old ones are given up. Full pages are shared; of a last page that is not full every
+    child but the first gets a copy. refs (num_pages,) int32 counts the tables' entries and whoever else holds a page.
+    Returns (page_table, lens, refs, missing), all new; missing (1,) counts the children that no free page was left for."""
+    planes, pages, size = _pool(cache)
+    _flat("parents", parents, torch.int32)
+    n = parents.shape[0]
+    args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, cache.shape[2] if page_size is None else page_size, n)
+    if refs.shape[0] != pages:
+        raise ValueError("refs must have an entry for every page of cache")
+    missing = torch.empty((1,), dtype=torch.int32, device=refs.device)
+    ws, bytes_ = _pages_workspace(refs, max(n, page_table.shape[0]))
+    check(lib().hc_page_fork(args, parents.data_ptr(), n, missing.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(),
+                             bytes_, _stream(refs, stream, table_out, lens_out, refs_out, missing, ws)))
+    return table_out, lens_out, refs_out, missing
+
+
+def page_extend(page_table, lens, refs, new_tokens, *, page_size, stream=None):
+    """Pages for new_tokens[s] more tokens of every sequence (hc_page_extend). Returns (page_table, lens, refs, missing)."""
+    _flat("new_tokens", new_tokens, torch.int32)
+    seqs = page_table.shape[0]
+    if new_tokens.shape[0] != seqs:
+        raise ValueError("new_tokens and page_table differ in sequences")
+    args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, page_size, seqs)
+    missing = torch.empty((1,), dtype=torch.int32, device=refs.device)
+    ws, bytes_ = _pages_workspace(refs, seqs)
+    check(lib().hc_page_extend(args, new_tokens.data_ptr(), missing.data_ptr(), ws.data_ptr(), bytes_,
+                               _stream(refs, stream, table_out, lens_out, refs_out, missing, ws)))
+    return table_out, lens_out, refs_out, missing
+
+
+def page_release(page_table, lens, refs, drop, *, page_size, stream=None):
+    """Sequences with drop[s] (uint8 or bool) give up their pages (hc_page_release). Returns (page_table, lens, refs)."""
+    _flat("drop", drop, torch.bool if drop.dtype == torch.bool else torch.uint8)
+    seqs = page_table.shape[0]
+    if drop.shape[0] != seqs:
+        raise ValueError("drop and page_table differ in sequences")
+    args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, page_size, seqs)
+    check(lib().hc_page_release(args, drop.data_ptr(), _stream(refs, stream, table_out, lens_out, refs_out)))
+    return table_out, lens_out, refs_out
+
+
+def page_compact(cache, page_table, lens, refs, *, page_size=None, stream=None):
+    """Move the live pages of a pool to its front (hc_page_compact). Returns (page_table, refs, remap, live): the new tables
+    and counts, where each page went (-1: nowhere), and the number of live pages."""
+    planes, pages, size = _pool(cache)
+    seqs = page_table.shape[0]
+    args, table_out, _, refs_out = _pages(page_table, lens, refs, cache.shape[2] if page_size is None else page_size, seqs,
+                                          need_lens=False)
+    if refs.shape[0] != pages:
+        raise ValueError("refs must have an entry for every page of cache")
+    remap = torch.empty(refs.shape, dtype=torch.int32, device=refs.device)
+    live = torch.empty((1,), dtype=torch.int32, device=refs.device)
+    ws, bytes_ = _pages_workspace(refs, seqs)
+    check(lib().hc_page_compact(args, remap.data_ptr(), live.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(), bytes_,
+                                _stream(refs, stream, table_out, refs_out, remap, live, ws)))
+    return table_out, refs_out, remap, live

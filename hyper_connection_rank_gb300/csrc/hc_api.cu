@@ -98,6 +98,7 @@ size_t workspace_for(int path, int64_t rows, int C, int H, int R, hc_dtype_t dt,
 
 namespace hc {
 hc_status_t set_error(hc_status_t s, const char* msg) { return fail(s, "%s", msg); }
+hc_status_t current_device_sms(int* num_sms) { return device_info(num_sms); }
 }  // namespace hc
 
 extern "C" {

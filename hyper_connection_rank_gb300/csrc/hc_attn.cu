@@ -1,0 +1,398 @@
+// Attention of new tokens over a paged cache (include/hc_paged.h): the choice
+// of kernels, the general kernel, and the kernel that joins splits.
+//
+// General kernel (every type, head size, page size, stride and alignment, and
+// all of float32): fp32 arithmetic on the CUDA cores. A CTA holds `ROWS` rows of
+// queries in shared memory and passes once over the split's keys in steps of
+// kKeys: scores into shared memory, running maximum m and sum l of each row
+//   m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m')
+// with s in base-2 exponents, and the sums of values scaled alike in
+// registers. Bound by its multiply-adds (2 * dim for each visible pair and
+// product); 16 rows to a tile where a sequence has no more than that (single
+// tokens), else 64.
+#include <algorithm>
+
+#include "hc_attn.cuh"
+#include "hc_paged_internal.h"
+
+namespace hc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 32;
+
+// DP: head_dim padded to a multiple of 64.
+template <int ROWS, int DP>
+struct GeneralSmem {
+  float q[ROWS][DP + 4];
+  float k[kKeys][DP + 4];
+  float v[kKeys][DP];
+  float p[ROWS][kKeys + 1];
+  float alpha[ROWS];
+  float m[ROWS], l[ROWS];
+  int64_t place[kKeys];  // element offset of a key's row in the pool, -1: no such key
+};
+
+// Threads are 16 x 16: thread (ty, tx) forms the scores of rows ty + 16 i and
+// keys tx, tx + 16, and the sums of rows ty + 16 i and features 4 tx + 64 c ..
+// + 3.
+template <typename T, int ROWS, int DP>
+__global__ void __launch_bounds__(kThreads) general_kernel(AttnArgs a) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  auto& sm = *reinterpret_cast<GeneralSmem<ROWS, DP>*>(raw);
+  constexpr int RI = ROWS / 16, CI = DP / 64;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
+  const int z = blockIdx.z, kvh = blockIdx.y;
+  AttnTile t;
+  tile_of_slot(a, blockIdx.x, &t);
+  if (t.rows == 0 || z >= t.splits) return;
+  int64_t k0, k1;
+  split_range(a.g, t, z, &k0, &k1);
+  const T* kp = static_cast<const T*>(a.k);
+  const T* vp = static_cast<const T*>(a.v);
+
+  for (int r = warp; r < ROWS; r += kThreads / 32) {
+    const T* src = nullptr;
+    if (r < t.rows) {
+      int64_t token;
+      int head;
+      row_owner(a, t, kvh, r, &token, &head);
+      src = static_cast<const T*>(a.q) + token * a.q_ts + head * a.q_hs;
+    }
+    for (int d = lane; d < DP; d += 32) sm.q[r][d] = src != nullptr && d < a.dim ? ldf(src + d) : 0.0f;
+  }
+  if (tid < ROWS) {
+    sm.m[tid] = neg_inf();
+    sm.l[tid] = 0.0f;
+  }
+  float acc[RI][CI][4] = {};
+
+  for (int64_t kb = k0; kb < k1; kb += kKeys) {
+    __syncthreads();
+    if (tid < kKeys) {
+      const int64_t j = kb + tid;
+      int64_t at = -1;
+      if (j >= t.lo && j < k1) {
+        const int page = page_of(a.b, t.s, j / a.b.page_size);
+        if (page >= 0) at = page * a.c_ps + j % a.b.page_size * a.c_ts + kvh * a.c_hs;
+      }
+      sm.place[tid] = at;
+    }
+    __syncthreads();
+    for (int j = warp; j < kKeys; j += kThreads / 32) {
+      const int64_t at = sm.place[j];
+#pragma unroll
+      for (int d = lane; d < DP; d += 32) {
+        const bool in = at >= 0 && d < a.dim;
+        sm.k[j][d] = in ? ldf(kp + at + d) : 0.0f;
+        sm.v[j][d] = in ? ldf(vp + at + d) : 0.0f;
+      }
+    }
+    __syncthreads();
+    float s[RI][2] = {};
+#pragma unroll 4
+    for (int d = 0; d < DP; d += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(&sm.k[tx][d]);
+      const float4 y = *reinterpret_cast<const float4*>(&sm.k[tx + 16][d]);
+#pragma unroll
+      for (int i = 0; i < RI; ++i) {
+        const float4 q = *reinterpret_cast<const float4*>(&sm.q[ty + 16 * i][d]);
+        s[i][0] = fmaf(q.x, x.x, fmaf(q.y, x.y, fmaf(q.z, x.z, fmaf(q.w, x.w, s[i][0]))));
+        s[i][1] = fmaf(q.x, y.x, fmaf(q.y, y.y, fmaf(q.z, y.z, fmaf(q.w, y.w, s[i][1]))));
+      }
+    }
+    // running maximum and sum: the 16 threads of a row are half a warp
+    bool masked = false;
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      const int r = ty + 16 * i;
+      const int64_t p = row_position(t, t.row0 + r, a.group);
+      float top = neg_inf();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int64_t j = kb + tx + 16 * c;
+        float x = s[i][c] * a.scale;
+        if (a.softcap > 0.0f) x = a.softcap * tanhf(x / a.softcap);
+        x *= kLog2e;
+        const bool seen = r < t.rows && j < k1 && j <= p && (a.window <= 0 || j > p - a.window);
+        masked |= !seen;
+        s[i][c] = seen ? x : neg_inf();
+        top = fmaxf(top, s[i][c]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float old = sm.m[r];
+      const float now = fmaxf(old, top);
+      const float ref = now == neg_inf() ? 0.0f : now;  // nothing seen yet
+      float sum = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float w = exp2f(s[i][c] - ref);
+        sum += w;
+        sm.p[r][tx + 16 * c] = w;
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      __syncwarp();
+      if (tx == 0) {
+        const float scale = exp2f(old - ref);
+        sm.alpha[r] = scale;
+        sm.m[r] = now;
+        sm.l[r] = sm.l[r] * scale + sum;
+      }
+    }
+    masked = __syncthreads_or(masked);
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      const float f = sm.alpha[ty + 16 * i];
+#pragma unroll
+      for (int c = 0; c < CI; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][c][e] *= f;
+    }
+#pragma unroll 4
+    for (int j = 0; j < kKeys; ++j) {
+      float4 v[CI];
+#pragma unroll
+      for (int c = 0; c < CI; ++c) v[c] = *reinterpret_cast<const float4*>(&sm.v[j][4 * tx + 64 * c]);
+#pragma unroll
+      for (int i = 0; i < RI; ++i) {
+        const float w = sm.p[ty + 16 * i][j];
+        // a weight of zero adds nothing, whatever the value at a key that the row does not see
+        if (masked && w == 0.0f) continue;
+#pragma unroll
+        for (int c = 0; c < CI; ++c) {
+          acc[i][c][0] = fmaf(w, v[c].x, acc[i][c][0]);
+          acc[i][c][1] = fmaf(w, v[c].y, acc[i][c][1]);
+          acc[i][c][2] = fmaf(w, v[c].z, acc[i][c][2]);
+          acc[i][c][3] = fmaf(w, v[c].w, acc[i][c][3]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < RI; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= t.rows) continue;
+    int64_t token;
+    int head;
+    row_owner(a, t, kvh, r, &token, &head);
+    const float l = sm.l[r], m = sm.m[r];
+    if (t.splits > 1) {
+      const int64_t at = part_index(a, z, token, head);
+      for (int c = 0; c < CI; ++c)
+        for (int e = 0; e < 4; ++e) {
+          const int d = 4 * tx + 64 * c + e;
+          if (d < a.dim) a.part_o[at * a.dim + d] = acc[i][c][e];
+        }
+      if (tx == 0) a.part_ml[at] = make_float2(m, l);
+    } else {
+      T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs;
+      const float f = l == 0.0f ? 0.0f : 1.0f / l;  // no weight at all: the row sees nothing
+      for (int c = 0; c < CI; ++c)
+        for (int e = 0; e < 4; ++e) {
+          const int d = 4 * tx + 64 * c + e;
+          if (d < a.dim) stf(dst + d, acc[i][c][e] * f);
+        }
+      if (tx == 0 && a.lse) a.lse[token * a.heads + head] = l == 0.0f ? neg_inf() : m * kLn2 + logf(l);
+    }
+  }
+}
+
+// Joins the splits of every row that has more than one: with M = max_z m_z,
+//   out = sum_z 2^(m_z - M) o_z / sum_z 2^(m_z - M) l_z.
+// A warp to a row, its lanes along the features; bound by the bytes of the
+// partial results, which the L2 holds.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) combine_kernel(AttnArgs a, AttnGeometry small, int64_t small_rows,
+                                                           AttnGeometry large) {
+  pdl_wait();
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= a.tokens * a.heads) return;
+  const int64_t token = row / a.heads;
+  const int head = static_cast<int>(row - token * a.heads);
+  const int s = a.b.cu_q ? warp_last_le(a.b.seqs, token, [&](int i) { return static_cast<int64_t>(a.b.cu_q[i]); })
+                         : static_cast<int>(token);
+  const int64_t first = first_row(a.b, s), all = (first_row(a.b, s + 1) - first) * a.group;
+  const AttnGeometry& g = all <= small_rows ? small : large;
+  AttnTile t;
+  tile_at(a, g, s, ((token - first) * a.group + head % a.group) / g.rows, &t);
+  if (t.rows == 0 || t.splits == 1) return;
+  float top = neg_inf();
+  for (int z = lane; z < t.splits; z += 32) top = fmaxf(top, a.part_ml[part_index(a, z, token, head)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top == neg_inf() ? 0.0f : top;
+  float sum = 0.0f;
+  for (int z = lane; z < t.splits; z += 32) {
+    const float2 ml = a.part_ml[part_index(a, z, token, head)];
+    sum += ml.y * exp2f(ml.x - ref);
+  }
+  sum = warp_sum(sum);
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs;
+  for (int d = lane; d < a.dim; d += 32) {
+    float o = 0.0f;
+    for (int z = 0; z < t.splits; ++z) {
+      const int64_t at = part_index(a, z, token, head);
+      const float m = a.part_ml[at].x;
+      if (m != neg_inf()) o = fmaf(a.part_o[at * a.dim + d], exp2f(m - ref), o);
+    }
+    stf(dst + d, o * f);
+  }
+  if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+}
+
+// ------------------------------------------------------------------- host --
+
+struct Plan {
+  AttnGeometry small, large;
+  int64_t small_rows;  // sequences with at most so many rows go to the small tiles
+  bool use_small, use_large;
+  int splits;          // the larger of the two
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int64_t slots_of(const hc_paged_attention_t& a, int rows) {
+  const int64_t group = a.heads / a.kv_heads;
+  return a.tokens * group / rows + a.seqs;
+}
+
+// Keys of a split: the longest piece that still gives every SM `per_sm` CTAs,
+// if all sequences were as long as the longest can be.
+void set_splits(AttnGeometry* g, const hc_paged_attention_t& a, int64_t keys, int64_t tiles, int num_sms, int per_sm,
+                int64_t shortest) {
+  const int64_t want = std::max<int64_t>(1, ceil_div(static_cast<int64_t>(num_sms) * per_sm, tiles * a.kv_heads));
+  int64_t len = std::max<int64_t>(shortest, ceil_div(keys, want));
+  len = ceil_div(len, g->align) * g->align;
+  g->split_len = static_cast<int>(std::min<int64_t>(len, int64_t{1} << 30));
+  g->splits = static_cast<int>(std::max<int64_t>(1, ceil_div(keys + g->align, g->split_len)));
+  if (g->splits > 256) {
+    g->splits = 256;
+    g->split_len = static_cast<int>(std::min<int64_t>(ceil_div(ceil_div(keys, 256), g->align) * g->align, int64_t{1} << 30));
+  }
+}
+
+Plan plan_of(const hc_paged_attention_t& a, int num_sms) {
+  Plan p = {};
+  const int64_t group = a.heads / a.kv_heads;
+  const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
+  const int64_t max_kv = a.max_kv > 0 ? std::min<int64_t>(a.max_kv, cap) : cap;
+  const int64_t max_q = a.cu_q == nullptr ? 1 : a.max_q > 0 ? std::min<int64_t>(a.max_q, a.tokens) : a.tokens;
+  p.small_rows = 16;
+  p.use_small = true;
+  p.use_large = a.cu_q != nullptr || group > p.small_rows;
+  p.small = AttnGeometry{16, kKeys, 0, 0};
+  p.large = AttnGeometry{64, kKeys, 0, 0};
+  const auto keys_of = [&](int rows) {
+    const int64_t span = ceil_div(rows, group) + 1;
+    return a.window > 0 ? std::min<int64_t>(max_kv, a.window + span) : max_kv;
+  };
+  set_splits(&p.small, a, keys_of(16), a.seqs, num_sms, 4, 128);
+  set_splits(&p.large, a, keys_of(64), std::max<int64_t>(1, a.tokens * group / 64), num_sms, 2, 256);
+  (void)max_q;
+  p.splits = std::max(p.use_small ? p.small.splits : 1, p.use_large ? p.large.splits : 1);
+  return p;
+}
+
+size_t part_bytes(const hc_paged_attention_t& a, const Plan& p) {
+  if (p.splits <= 1) return 0;
+  const size_t rows = static_cast<size_t>(p.splits) * a.tokens * a.heads;
+  return align_up(rows * 8, 256) + align_up(rows * a.head_dim * 4, 256);
+}
+
+AttnArgs args_of(const hc_paged_attention_t& a) {
+  AttnArgs d = {};
+  d.q = a.q;
+  d.k = a.k_cache;
+  d.v = a.v_cache;
+  d.out = a.out;
+  d.lse = a.lse;
+  d.b = BatchView{a.page_table, a.kv_lens, a.cu_q, a.table_stride, a.num_pages, a.seqs, a.max_pages, a.page_size};
+  d.tokens = a.tokens;
+  d.q_ts = a.q_token_stride;
+  d.q_hs = a.q_head_stride;
+  d.o_ts = a.out_token_stride;
+  d.o_hs = a.out_head_stride;
+  d.c_ps = a.cache_page_stride;
+  d.c_ts = a.cache_token_stride;
+  d.c_hs = a.cache_head_stride;
+  d.heads = a.heads;
+  d.kv_heads = a.kv_heads;
+  d.group = a.heads / a.kv_heads;
+  d.dim = a.head_dim;
+  d.window = a.window;
+  d.scale = a.scale;
+  d.softcap = a.softcap;
+  return d;
+}
+
+template <typename T, int ROWS, int DP>
+cudaError_t general_t(const AttnArgs& d, int64_t slots, cudaStream_t s) {
+  constexpr size_t smem = sizeof(GeneralSmem<ROWS, DP>);
+  const cudaError_t e = ensure_smem<general_kernel<T, ROWS, DP>>(smem);
+  if (e != cudaSuccess) return e;
+  general_kernel<T, ROWS, DP>
+      <<<dim3(static_cast<unsigned>(slots), d.kv_heads, d.g.splits), kThreads, smem, s>>>(d);
+  return cudaGetLastError();
+}
+
+template <typename T, int ROWS>
+cudaError_t general_d(const AttnArgs& d, int64_t slots, cudaStream_t s) {
+  if (d.dim <= 64) return general_t<T, ROWS, 64>(d, slots, s);
+  if (d.dim <= 128) return general_t<T, ROWS, 128>(d, slots, s);
+  return general_t<T, ROWS, 256>(d, slots, s);
+}
+
+template <typename T>
+cudaError_t launch_t(const hc_paged_attention_t& a, int num_sms, cudaStream_t s) {
+  const Plan p = plan_of(a, num_sms);
+  AttnArgs d = args_of(a);
+  if (p.splits > 1) {
+    const size_t rows = static_cast<size_t>(p.splits) * a.tokens * a.heads;
+    d.part_ml = static_cast<float2*>(a.workspace);
+    d.part_o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + align_up(rows * 8, 256));
+  }
+  cudaError_t e = cudaSuccess;
+  if (p.use_small) {
+    d.g = p.small;
+    d.min_rows = 1;
+    d.max_rows = p.small_rows;
+    e = general_d<T, 16>(d, slots_of(a, p.small.rows), s);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.use_large) {
+    d.g = p.large;
+    d.min_rows = p.small_rows + 1;
+    d.max_rows = INT64_MAX;
+    e = general_d<T, 64>(d, slots_of(a, p.large.rows), s);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.splits > 1) {
+    const unsigned grid = static_cast<unsigned>(ceil_div(a.tokens * a.heads, kThreads / 32));
+    combine_kernel<T><<<grid, kThreads, 0, s>>>(d, p.small, p.small_rows, p.large);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t attention_workspace(const hc_paged_attention_t& a, bool aligned, int num_sms) {
+  (void)aligned;
+  return part_bytes(a, plan_of(a, num_sms));
+}
+
+cudaError_t launch_attention(const hc_paged_attention_t& a, bool aligned, int num_sms, cudaStream_t s) {
+  (void)aligned;
+  switch (a.dtype) {
+    case HC_F32: return launch_t<float>(a, num_sms, s);
+    case HC_F16: return launch_t<__half>(a, num_sms, s);
+    default: return launch_t<__nv_bfloat16>(a, num_sms, s);
+  }
+}
+
+}  // namespace hc

@@ -100,6 +100,8 @@ bool make_tmap_2d_sw128(CUtensorMap* m, const void* base, bool bf16, uint64_t in
 
 // Record `msg` as this thread's hc_last_error() text and return `s`.
 hc_status_t set_error(hc_status_t s, const char* msg);
+// HC_OK and the SM count if the current device is an sm_103.
+hc_status_t current_device_sms(int* num_sms);
 
 // Diagnostic counter of bounded device waits that gave up.
 unsigned int read_wait_timeouts(bool reset);

@@ -1,0 +1,261 @@
+// Rotary positions, alone and fused with the write of a batch's new tokens
+// into the paged cache (include/hc_paged.h).
+//
+// Mathematics: pair (a, b) of a head at position p turns by p * inv_freq. The
+// angle is wanted modulo one turn, and fp32 has lost it long before p reaches
+// the lengths in use (at p = 10^5 an fp32 angle is off by up to 0.004 rad).
+// So the frequency becomes a 64-bit fraction of a turn, u = 2^64 * frac(
+// inv_freq / 2 pi), and p * u modulo 2^64 is the exact fraction of a turn after
+// p tokens (negative p wrap the right way); its upper 32 bits, as a signed
+// number of half turns in [-1, 1), go to sincospif. What is left is u's own
+// rounding (2^-53 relative) and one fp32 rounding of the half turns.
+//
+// Bound: bytes; every element is read and written once. One CTA serves a few
+// tokens; their sines and cosines are formed once in shared memory (rot_dim/2
+// per token, against heads * rot_dim elements that use them), and each thread
+// then turns 16 bytes of each side of the pairs at a time. The half layout
+// takes the two sides from one head's two halves, the interleaved one has both
+// sides in one vector.
+#include "hc_common.cuh"
+#include "hc_paged_batch.cuh"
+#include "hc_paged_internal.h"
+
+namespace hc {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T e[V];
+};
+
+struct RotaryArgs {
+  // parts of a token's row: heads [0, hq) from q, [hq, hq + hk) from k, the next hk from v
+  const void *q, *k, *v;
+  void *q_out, *k_cache, *v_cache;
+  const void* positions;  // NULL: positions come from the batch
+  bool positions32;
+  const double* inv_freq;
+  int64_t tokens;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs, c_ps, c_ts, c_hs;
+  int hq, hk, dim, rot;
+  float amplitude, sign;
+  BatchView batch;
+};
+
+// Items of a head's work. V > 1: vectors of V features (interleaved), or pairs
+// of vectors from the two halves and then vectors that are copied; V == 1, for
+// any alignment: pairs, then single features that are copied.
+template <int V, bool INTER>
+__host__ __device__ __forceinline__ int items_of(int dim, int rot) {
+  if (V > 1 && INTER) return dim / V;
+  return rot / 2 / V + (dim - rot) / V;
+}
+
+// Item `it` of one head, `src` to `dst` (which may be the same place).
+template <typename T, int V, bool INTER>
+__device__ __forceinline__ void turn_item(const T* src, T* dst, int it, int rot, const float2* cs) {
+  using P = Pack<T, V>;
+  if (V > 1 && INTER) {
+    P x = *reinterpret_cast<const P*>(src + it * V);
+    if (it * V < rot) {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const float2 c = cs[(it * V + i) >> 1];
+        const float a = Ty<T>::to_f(x.e[i]), b = Ty<T>::to_f(x.e[i + 1]);
+        x.e[i] = Ty<T>::from_f(a * c.x - b * c.y);
+        x.e[i + 1] = Ty<T>::from_f(b * c.x + a * c.y);
+      }
+    }
+    *reinterpret_cast<P*>(dst + it * V) = x;
+  } else {
+    const int half = rot >> 1, turns = half / V;
+    if (it < turns) {
+      const int ia = INTER ? 2 * it : it * V, ib = INTER ? 2 * it + 1 : half + it * V;
+      P x = *reinterpret_cast<const P*>(src + ia);
+      P y = *reinterpret_cast<const P*>(src + ib);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 c = cs[it * V + i];
+        const float a = Ty<T>::to_f(x.e[i]), b = Ty<T>::to_f(y.e[i]);
+        x.e[i] = Ty<T>::from_f(a * c.x - b * c.y);
+        y.e[i] = Ty<T>::from_f(b * c.x + a * c.y);
+      }
+      *reinterpret_cast<P*>(dst + ia) = x;
+      *reinterpret_cast<P*>(dst + ib) = y;
+    } else {
+      const int d = rot + (it - turns) * V;
+      *reinterpret_cast<P*>(dst + d) = *reinterpret_cast<const P*>(src + d);
+    }
+  }
+}
+
+// V elements per access; TPB tokens per CTA. Dynamic shared memory: rot/2
+// 64-bit fractions, then TPB * rot/2 (cos, sin).
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int tpb) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int64_t s_pos[32];
+  __shared__ int64_t s_slot[32];  // element offset of the token in the pool, -1: nowhere
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int half = a.rot >> 1;
+  uint64_t* frac = reinterpret_cast<uint64_t*>(smem);
+  float2* cs = reinterpret_cast<float2*>(frac + half);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tpb;
+  const int nt = static_cast<int>(a.tokens - t0 < tpb ? a.tokens - t0 : tpb);
+
+  for (int i = tid; i < half; i += kThreads) {
+    double f = a.inv_freq[i] * 0.15915494309189535;  // turns per token
+    f -= floor(f);
+    frac[i] = __double2ull_rn(f * 18446744073709551616.0);
+  }
+  if (a.positions != nullptr) {
+    if (tid < nt)
+      s_pos[tid] = a.positions32 ? static_cast<const int32_t*>(a.positions)[t0 + tid]
+                                 : static_cast<const int64_t*>(a.positions)[t0 + tid];
+  } else {
+    for (int j = warp; j < nt; j += kThreads / 32) {
+      const int64_t t = t0 + j;
+      const BatchView& b = a.batch;
+      const int s = b.cu_q ? warp_last_le(b.seqs, t, [&](int i) { return static_cast<int64_t>(b.cu_q[i]); })
+                           : static_cast<int>(t);
+      if (lane == 0) {
+        const int64_t end = first_row(b, s + 1);
+        const int64_t pos = kv_len_of(b, s) - (end - t);
+        int page = -1;
+        if (pos >= 0) page = page_of(b, s, pos / b.page_size);
+        s_pos[j] = pos;
+        s_slot[j] = page < 0 ? -1 : page * a.c_ps + pos % b.page_size * a.c_ts;
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < nt * half; i += kThreads) {
+    const int j = i / half, f = i - j * half;
+    const int32_t turn = static_cast<int32_t>((static_cast<uint64_t>(s_pos[j]) * frac[f]) >> 32);
+    float s, c;
+    sincospif(static_cast<float>(turn) * 4.656612873077393e-10f, &s, &c);  // half turns: turn * 2^-31
+    cs[i] = make_float2(a.amplitude * c, a.amplitude * a.sign * s);
+  }
+  __syncthreads();
+
+  // threads: `items` to a head, as many heads at a time as fit
+  const int items = items_of<V, INTER>(a.dim, a.rot);
+  const int heads = a.hq + 2 * a.hk;
+  const int hpp = items < kThreads ? kThreads / items : 1;
+  const int ih = items < kThreads ? tid / items : 0;
+  if (ih >= hpp) return;
+  for (int it = items < kThreads ? tid - ih * items : tid; it < items; it += kThreads) {
+    for (int u = ih; u < nt * heads; u += hpp) {
+      const int j = u / heads, h = u - j * heads;
+      const int64_t t = t0 + j;
+      if (h < a.hq) {
+        turn_item<T, V, INTER>(static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs,
+                               static_cast<T*>(a.q_out) + t * a.o_ts + h * a.o_hs, it, a.rot, cs + j * half);
+      } else {
+        if (s_slot[j] < 0) continue;
+        const int kh = h < a.hq + a.hk ? h - a.hq : h - a.hq - a.hk;
+        const int64_t to = s_slot[j] + kh * a.c_hs;
+        if (h < a.hq + a.hk) {
+          turn_item<T, V, INTER>(static_cast<const T*>(a.k) + t * a.k_ts + kh * a.k_hs,
+                                 static_cast<T*>(a.k_cache) + to, it, a.rot, cs + j * half);
+        } else {
+          const T* src = static_cast<const T*>(a.v) + t * a.v_ts + kh * a.v_hs;
+          for (int c = it; c < a.dim / V; c += items)
+            *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(a.v_cache) + to + c * V) =
+                *reinterpret_cast<const Pack<T, V>*>(src + c * V);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int V, bool INTER>
+cudaError_t launch_t(const RotaryArgs& a, int num_sms, cudaStream_t s) {
+  // Few tokens: one per CTA, so that they spread over the SMs. Many: more per
+  // CTA, so that the frequencies are converted once for several tokens.
+  int tpb = 1;
+  while (tpb < 8 && a.tokens / (tpb * 2) >= num_sms * 8) tpb *= 2;
+  const int half = a.rot / 2;
+  const size_t smem = static_cast<size_t>(half) * 8 * (1 + tpb);
+  const unsigned grid = static_cast<unsigned>((a.tokens + tpb - 1) / tpb);
+  rotary_kernel<T, V, INTER><<<grid, kThreads, smem, s>>>(a, tpb);
+  return cudaGetLastError();
+}
+
+template <typename T, bool INTER>
+cudaError_t launch_v(const RotaryArgs& a, bool vec, int num_sms, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  // 16-byte vectors where every part of a head is whole ones, else element by element
+  const bool whole = vec && a.dim % V == 0 && a.rot % (INTER ? V : 2 * V) == 0;
+  return whole ? launch_t<T, V, INTER>(a, num_sms, s) : launch_t<T, 1, INTER>(a, num_sms, s);
+}
+
+cudaError_t launch_any(const RotaryArgs& a, int dtype, bool interleaved, bool vec, int num_sms, cudaStream_t s) {
+  if (a.tokens == 0) return cudaSuccess;
+  switch (dtype) {
+    case HC_F32:
+      return interleaved ? launch_v<float, true>(a, vec, num_sms, s) : launch_v<float, false>(a, vec, num_sms, s);
+    case HC_F16:
+      return interleaved ? launch_v<__half, true>(a, vec, num_sms, s) : launch_v<__half, false>(a, vec, num_sms, s);
+    default:
+      return interleaved ? launch_v<__nv_bfloat16, true>(a, vec, num_sms, s)
+                         : launch_v<__nv_bfloat16, false>(a, vec, num_sms, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const hc_rotary_t& r, bool vec, int num_sms, cudaStream_t s) {
+  RotaryArgs a = {};
+  a.q = r.x;
+  a.q_out = r.out;
+  a.positions = r.positions;
+  a.positions32 = r.positions32 != 0;
+  a.inv_freq = r.inv_freq;
+  a.tokens = r.tokens;
+  a.q_ts = r.x_token_stride;
+  a.q_hs = r.x_head_stride;
+  a.o_ts = r.out_token_stride;
+  a.o_hs = r.out_head_stride;
+  a.hq = r.heads;
+  a.dim = r.head_dim;
+  a.rot = r.rot_dim;
+  a.amplitude = r.amplitude;
+  a.sign = r.inverse ? -1.0f : 1.0f;
+  return launch_any(a, r.dtype, r.interleaved != 0, vec, num_sms, s);
+}
+
+cudaError_t launch_rotary_append(const hc_rotary_append_t& r, bool vec, int num_sms, cudaStream_t s) {
+  RotaryArgs a = {};
+  a.q = r.q;
+  a.k = r.k;
+  a.v = r.v;
+  a.q_out = r.q_out;
+  a.k_cache = r.k_cache;
+  a.v_cache = r.v_cache;
+  a.inv_freq = r.inv_freq;
+  a.tokens = r.tokens;
+  a.q_ts = r.q_token_stride;
+  a.q_hs = r.q_head_stride;
+  a.k_ts = r.k_token_stride;
+  a.k_hs = r.k_head_stride;
+  a.v_ts = r.v_token_stride;
+  a.v_hs = r.v_head_stride;
+  a.o_ts = r.out_token_stride;
+  a.o_hs = r.out_head_stride;
+  a.c_ps = r.cache_page_stride;
+  a.c_ts = r.cache_token_stride;
+  a.c_hs = r.cache_head_stride;
+  a.hq = r.heads;
+  a.hk = r.kv_heads;
+  a.dim = r.head_dim;
+  a.rot = r.rot_dim;
+  a.amplitude = r.amplitude;
+  a.sign = 1.0f;
+  a.batch = BatchView{r.page_table, r.kv_lens, r.cu_q, r.table_stride, r.num_pages, r.seqs, r.max_pages, r.page_size};
+  return launch_any(a, r.dtype, r.interleaved != 0, vec, num_sms, s);
+}
+
+}  // namespace hc
