@@ -12,7 +12,7 @@
 // tokens), else 64.
 #include <algorithm>
 
-#include "hc_attn.cuh"
+#include "hc_attn_internal.h"
 #include "hc_paged_internal.h"
 
 namespace hc {
@@ -251,6 +251,7 @@ struct Plan {
   AttnGeometry small, large;
   int64_t small_rows;  // sequences with at most so many rows go to the small tiles
   bool use_small, use_large;
+  bool rows_kernel;    // small tiles by hc_attn_rows.cu
   int splits;          // the larger of the two
 };
 
@@ -276,14 +277,16 @@ void set_splits(AttnGeometry* g, const hc_paged_attention_t& a, int64_t keys, in
   }
 }
 
-Plan plan_of(const hc_paged_attention_t& a, int num_sms) {
+Plan plan_of(const hc_paged_attention_t& a, bool aligned, int num_sms) {
   Plan p = {};
+  const bool fast = !(a.flags & HC_FLAG_FORCE_GENERAL);
   const int64_t group = a.heads / a.kv_heads;
   const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
   const int64_t max_kv = a.max_kv > 0 ? std::min<int64_t>(a.max_kv, cap) : cap;
   const int64_t max_q = a.cu_q == nullptr ? 1 : a.max_q > 0 ? std::min<int64_t>(a.max_q, a.tokens) : a.tokens;
   p.small_rows = 16;
   p.use_small = true;
+  p.rows_kernel = fast && attn_rows_supported(a.dtype, a.head_dim, aligned);
   p.use_large = a.cu_q != nullptr || group > p.small_rows;
   p.small = AttnGeometry{16, kKeys, 0, 0};
   p.large = AttnGeometry{64, kKeys, 0, 0};
@@ -348,8 +351,8 @@ cudaError_t general_d(const AttnArgs& d, int64_t slots, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_t(const hc_paged_attention_t& a, int num_sms, cudaStream_t s) {
-  const Plan p = plan_of(a, num_sms);
+cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, cudaStream_t s) {
+  const Plan p = plan_of(a, aligned, num_sms);
   AttnArgs d = args_of(a);
   if (p.splits > 1) {
     const size_t rows = static_cast<size_t>(p.splits) * a.tokens * a.heads;
@@ -361,7 +364,8 @@ cudaError_t launch_t(const hc_paged_attention_t& a, int num_sms, cudaStream_t s)
     d.g = p.small;
     d.min_rows = 1;
     d.max_rows = p.small_rows;
-    e = general_d<T, 16>(d, slots_of(a, p.small.rows), s);
+    const int64_t slots = slots_of(a, p.small.rows);
+    e = p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s) : general_d<T, 16>(d, slots, s);
     if (e != cudaSuccess) return e;
   }
   if (p.use_large) {
@@ -373,8 +377,7 @@ cudaError_t launch_t(const hc_paged_attention_t& a, int num_sms, cudaStream_t s)
   }
   if (p.splits > 1) {
     const unsigned grid = static_cast<unsigned>(ceil_div(a.tokens * a.heads, kThreads / 32));
-    combine_kernel<T><<<grid, kThreads, 0, s>>>(d, p.small, p.small_rows, p.large);
-    e = cudaGetLastError();
+    e = launch_pdl(combine_kernel<T>, dim3(grid), dim3(kThreads), 0, s, 1, d, p.small, p.small_rows, p.large);
   }
   return e;
 }
@@ -382,16 +385,14 @@ cudaError_t launch_t(const hc_paged_attention_t& a, int num_sms, cudaStream_t s)
 }  // namespace
 
 size_t attention_workspace(const hc_paged_attention_t& a, bool aligned, int num_sms) {
-  (void)aligned;
-  return part_bytes(a, plan_of(a, num_sms));
+  return part_bytes(a, plan_of(a, aligned, num_sms));
 }
 
 cudaError_t launch_attention(const hc_paged_attention_t& a, bool aligned, int num_sms, cudaStream_t s) {
-  (void)aligned;
   switch (a.dtype) {
-    case HC_F32: return launch_t<float>(a, num_sms, s);
-    case HC_F16: return launch_t<__half>(a, num_sms, s);
-    default: return launch_t<__nv_bfloat16>(a, num_sms, s);
+    case HC_F32: return launch_t<float>(a, aligned, num_sms, s);
+    case HC_F16: return launch_t<__half>(a, aligned, num_sms, s);
+    default: return launch_t<__nv_bfloat16>(a, aligned, num_sms, s);
   }
 }
 

@@ -119,4 +119,19 @@ __device__ __forceinline__ int64_t part_index(const AttnArgs& a, int z, int64_t 
   return (static_cast<int64_t>(z) * a.tokens + token) * a.heads + head;
 }
 
+// Score to base-2 exponent: scale * log2(e), and with a cap c on the scaled
+// score, c * log2(e) * tanh(scale / c * x) with tanh(y) = 1 - 2 / (exp(2y) + 1)
+// (absolute error some 1e-7, which the cap multiplies).
+struct ScoreMap {
+  float mul, cap;  // cap 0: none
+};
+__host__ __device__ __forceinline__ ScoreMap score_map(float scale, float softcap) {
+  return softcap > 0.0f ? ScoreMap{scale / softcap * 2.0f * kLog2e, softcap * kLog2e}
+                        : ScoreMap{scale * kLog2e, 0.0f};
+}
+__device__ __forceinline__ float map_score(const ScoreMap& m, float x) {
+  if (m.cap == 0.0f) return x * m.mul;
+  return m.cap - __fdividef(2.0f * m.cap, ex2(x * m.mul) + 1.0f);
+}
+
 }  // namespace hc

@@ -1,0 +1,14 @@
+// The specialised attention kernels, as hc_attn.cu dispatches them.
+#pragma once
+
+#include "hc_attn.cuh"
+#include "hc_internal.h"
+
+namespace hc {
+
+// Up to 16 rows to a key head (hc_attn_rows.cu). `aligned`: 16-byte accesses
+// are possible everywhere.
+bool attn_rows_supported(int dtype, int dim, bool aligned);
+cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, int64_t slots, cudaStream_t s);
+
+}  // namespace hc

@@ -1,0 +1,319 @@
+// Attention over a paged cache for few rows (fp16/bf16): sequences whose new
+// tokens and grouped heads make at most 16 rows to a key head, single tokens
+// above all.
+//
+// Bound: bytes. Every key and value is read once and used by at most 16 rows, 16
+// multiply-adds to the byte at most, so what counts is to keep enough loads in
+// flight (some 44 bytes/ns and SM, about 45 KB at a microsecond's latency).
+// Each warp runs for itself: blocks of 16 keys, every fourth of the split's,
+// come by 16-byte cp.async into a ring of its own, four blocks deep, so that
+// no barrier stands between the loads of one warp and the arithmetic of
+// another (two CTAs to an SM hold 192 KB in flight). The products are warp-level
+// MMAs (m16n8k16): a tile of 16 rows is what they are made for, where a
+// tcgen05 tile would be seven eighths empty and its tensor-memory round trips
+// would lie on the path of every block.
+//
+// Mathematics: the running maximum and sum of a softmax, held per warp, with the
+// sums of values in registers; they are rescaled only when a block raises the
+// maximum. The warps' results are joined once at the end:
+//   M = max_w m_w,  out = sum_w 2^(m_w - M) o_w / sum_w 2^(m_w - M) l_w.
+#include "hc_async.cuh"
+#include "hc_attn.cuh"
+#include "hc_attn_internal.h"
+#include "hc_mma.cuh"
+
+namespace hc {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kBlock = 16;  // keys of a block
+constexpr int kStages = 3;
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 16-byte chunk `c` of row `r` of a block of D-element rows: chunks are permuted
+// by the row's low three bits, so that the eight rows of an 8x8 matrix lie in
+// eight different groups of banks.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return static_cast<uint32_t>(r * (D * 2) + ((c ^ (r & 7)) << 4));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
+  constexpr int kChunks = D / 8;                 // 16-byte chunks of a row
+  constexpr int kHalf = kBlock * D * 2;          // bytes of a block's keys
+  constexpr int kStage = 2 * kHalf;              // and of its values
+  constexpr int kRowsPer = 32 / kChunks;         // rows that a warp copies at once
+  constexpr int kCopies = kBlock / kRowsPer;
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ float s_m[kWarps][16], s_l[kWarps][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+  const int z = blockIdx.z, kvh = blockIdx.y;
+  pdl_trigger();
+  AttnTile t;
+  tile_of_slot(a, blockIdx.x, &t);
+  if (t.rows == 0 || z >= t.splits) return;
+  int64_t k0, k1;
+  split_range(a.g, t, z, &k0, &k1);
+  const T* kp = static_cast<const T*>(a.k) + kvh * a.c_hs;
+  const T* vp = static_cast<const T*>(a.v) + kvh * a.c_hs;
+  const int blocks = k1 > k0 ? static_cast<int>((k1 - k0 + kBlock - 1) / kBlock) : 0;
+  const uint32_t base = smem_addr(ring) + warp * (kStages * kStage);
+
+  // place of key (lane & 15) of block b in the pool, -1: no such key
+  const auto place_of = [&](int b) -> int64_t {
+    const int64_t j = k0 + static_cast<int64_t>(b) * kBlock + (lane & 15);
+    if (b >= blocks || j < t.lo || j >= k1) return -1;
+    const uint32_t i = static_cast<uint32_t>(j) / static_cast<uint32_t>(a.b.page_size);
+    const int page = page_of(a.b, t.s, i);
+    return page < 0 ? -1 : page * a.c_ps + (static_cast<uint32_t>(j) - i * a.b.page_size) * a.c_ts;
+  };
+  const auto fetch = [&](int64_t place, int stage) {
+    const uint32_t to = base + stage * kStage;
+    const int c = lane % kChunks;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const int r = i * kRowsPer + lane / kChunks;
+      const int64_t at = __shfl_sync(0xffffffffu, place, r);
+      const int64_t off = (at < 0 ? 0 : at) + c * 8;
+      const uint32_t bytes = at < 0 ? 0 : 16;
+      cp_async16_zfill(to + chunk_at<D>(r, c), kp + off, bytes);
+      cp_async16_zfill(to + kHalf + chunk_at<D>(r, c), vp + off, bytes);
+    }
+  };
+
+  // the ring's first blocks, then the queries while those are on their way
+  int64_t place = place_of(warp);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    const int b = warp + i * kWarps;
+    const int64_t next = place_of(b + kWarps);
+    if (b < blocks) fetch(place, i);
+    cp_async_commit();
+    place = next;
+  }
+  uint32_t qf[D / 16][4];
+  {
+    const T* rows[2] = {nullptr, nullptr};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (g + 8 * i < t.rows) {
+        int64_t token;
+        int head;
+        row_owner(a, t, kvh, g + 8 * i, &token, &head);
+        rows[i] = static_cast<const T*>(a.q) + token * a.q_ts + head * a.q_hs;
+      }
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const T* src = rows[i & 1];
+        qf[ks][i] = src ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + (i >> 1) * 8 + q4 * 2) : 0u;
+      }
+  }
+  // keys that this thread's two rows see, relative to k0: [from, to)
+  int from[2], to[2], all_from = 0, all_to = 0;
+  const auto rel = [&](int64_t j) {
+    const int64_t d = j - k0, n = k1 - k0;
+    return static_cast<int>(d < 0 ? 0 : d > n ? n : d);
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t p = row_position(t, t.row0 + g + 8 * i, a.group);
+    const bool real = g + 8 * i < t.rows;
+    to[i] = real ? rel(p + 1) : 0;
+    from[i] = real && a.window > 0 ? rel(p - a.window + 1) : 0;
+  }
+  all_to = rel(row_position(t, t.row0, a.group) + 1);  // seen by every row: [all_from, all_to)
+  if (a.window > 0) all_from = rel(row_position(t, t.row0 + t.rows - 1, a.group) - a.window + 1);
+
+  const ScoreMap map = score_map(a.scale, a.softcap);
+  float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.0f, 0.0f};
+  float o[D / 8][4];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+
+  int stage = 0;
+  for (int b = warp; b < blocks; b += kWarps) {
+    {
+      const int ahead = b + (kStages - 1) * kWarps;
+      const int64_t next = place_of(ahead + kWarps);
+      if (ahead < blocks) fetch(place, stage == 0 ? kStages - 1 : stage - 1);
+      cp_async_commit();
+      place = next;
+    }
+    cp_async_wait_group<kStages - 1>();
+    __syncwarp();
+    const uint32_t ks_at = base + stage * kStage, vs_at = ks_at + kHalf;
+    // scores of 16 rows and 16 keys, as two 16 x 8 tiles
+    float s[2][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4(ks_at + chunk_at<D>(((lane >> 4) << 3) + (lane & 7), 2 * ks + ((lane >> 3) & 1)), b0, b1, b2, b3);
+      Mma<T>::run4(s[0], qf[ks], b0, b1);
+      Mma<T>::run4(s[1], qf[ks], b2, b3);
+    }
+    const int j0 = b * kBlock;
+    const bool whole = j0 >= all_from && j0 + kBlock <= all_to;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[n][e] = map_score(map, s[n][e]);
+        if (!whole) {
+          const int j = j0 + 8 * n + 2 * q4 + (e & 1), i = e >> 1;
+          if (j < from[i] || j >= to[i]) s[n][e] = neg_inf();
+        }
+      }
+    float top[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      top[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+    }
+    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+      float f[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float now = fmaxf(m[i], top[i]);
+        f[i] = now == neg_inf() ? 1.0f : ex2(m[i] - now);
+        m[i] = now;
+        l[i] *= f[i];
+      }
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d) {
+        o[d][0] *= f[0];
+        o[d][1] *= f[0];
+        o[d][2] *= f[1];
+        o[d][3] *= f[1];
+      }
+    }
+    float ref[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) ref[i] = m[i] == neg_inf() ? 0.0f : m[i];
+    uint32_t p[4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[n][e] = ex2(s[n][e] - ref[e >> 1]);
+        l[e >> 1] += s[n][e];
+      }
+      p[2 * n] = pack2<T>(s[n][0], s[n][1]);
+      p[2 * n + 1] = pack2<T>(s[n][2], s[n][3]);
+    }
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4_trans(vs_at + chunk_at<D>(lane & 15, 2 * d + (lane >> 4)), b0, b1, b2, b3);
+      Mma<T>::run4(o[2 * d], p, b0, b1);
+      Mma<T>::run4(o[2 * d + 1], p, b2, b3);
+    }
+    __syncwarp();
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  cp_async_wait_group<0>();
+
+  // join the four lanes of a row, then the warps
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    if (q4 == 0) {
+      s_m[warp][g + 8 * i] = m[i];
+      s_l[warp][g + 8 * i] = l[i];
+    }
+  }
+  __syncthreads();  // (every warp is done with its ring)
+  float f[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float top = neg_inf();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][g + 8 * i]);
+    f[i] = m[i] == neg_inf() ? 1.0f : ex2(m[i] - top);  // (no weights: sums of zero, or NaN from NaN scores)
+  }
+  constexpr int kPitch = D + 8;  // floats; rows g and g + 1 lie 8 banks apart
+  float* sums = reinterpret_cast<float*>(ring) + warp * 16 * kPitch;
+#pragma unroll
+  for (int d = 0; d < D / 8; ++d) {
+    *reinterpret_cast<float2*>(sums + g * kPitch + d * 8 + q4 * 2) = make_float2(o[d][0] * f[0], o[d][1] * f[0]);
+    *reinterpret_cast<float2*>(sums + (g + 8) * kPitch + d * 8 + q4 * 2) = make_float2(o[d][2] * f[1], o[d][3] * f[1]);
+  }
+  __syncthreads();
+  constexpr int kPerRow = D / 4;  // threads of a row, four features each
+  const float* all = reinterpret_cast<const float*>(ring);
+  for (int u = threadIdx.x; u < t.rows * kPerRow; u += kWarps * 32) {
+    const int r = u / kPerRow, d = (u - r * kPerRow) * 4;
+    float top = neg_inf(), sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += s_l[w][r] * (s_m[w][r] == neg_inf() ? 1.0f : ex2(s_m[w][r] - top));
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(all + (w * 16 + r) * kPitch + d);
+      x.x += y.x;
+      x.y += y.y;
+      x.z += y.z;
+      x.w += y.w;
+    }
+    int64_t token;
+    int head;
+    row_owner(a, t, kvh, r, &token, &head);
+    if (t.splits > 1) {
+      const int64_t at = part_index(a, z, token, head);
+      *reinterpret_cast<float4*>(a.part_o + at * D + d) = x;
+      if (d == 0) a.part_ml[at] = make_float2(top, sum);
+    } else {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + d;
+      stf(dst, x.x * inv);
+      stf(dst + 1, x.y * inv);
+      stf(dst + 2, x.z * inv);
+      stf(dst + 3, x.w * inv);
+      if (d == 0 && a.lse) a.lse[token * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+    }
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const AttnArgs& a, int64_t slots, cudaStream_t s) {
+  constexpr size_t ring = static_cast<size_t>(kWarps) * kStages * kBlock * D * 4;
+  constexpr size_t sums = static_cast<size_t>(kWarps) * 16 * (D + 8) * 4;
+  constexpr size_t smem = ring > sums ? ring : sums;
+  const cudaError_t e = ensure_smem<rows_kernel<T, D>>(smem);
+  if (e != cudaSuccess) return e;
+  rows_kernel<T, D><<<dim3(static_cast<unsigned>(slots), a.kv_heads, a.g.splits), kWarps * 32, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_rows_supported(int dtype, int dim, bool aligned) {
+  return aligned && (dtype == HC_F16 || dtype == HC_BF16) && (dim == 64 || dim == 128);
+}
+
+cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, int64_t slots, cudaStream_t s) {
+  if (dtype == HC_F16) return a.dim == 64 ? launch_t<__half, 64>(a, slots, s) : launch_t<__half, 128>(a, slots, s);
+  return a.dim == 64 ? launch_t<__nv_bfloat16, 64>(a, slots, s) : launch_t<__nv_bfloat16, 128>(a, slots, s);
+}
+
+}  // namespace hc
