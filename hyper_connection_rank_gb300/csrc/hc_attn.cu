@@ -202,14 +202,30 @@ __global__ void __launch_bounds__(kThreads) general_kernel(AttnArgs a) {
 
 // Joins the splits of every row that has more than one: with M = max_z m_z,
 //   out = sum_z 2^(m_z - M) o_z / sum_z 2^(m_z - M) l_z.
-// A warp to a row, its lanes along the features; bound by the bytes of the
-// partial results, which the L2 holds.
-template <typename T>
+// WARPS warps to a row: all weights first, at once, then each warp adds every
+// WARPS-th split, four loads in flight, and the warps' sums are added in order.
+// One warp where the splits are few and the rows many, a CTA of eight where a
+// row has many splits (two rows of 64 heads and 39 splits took 100 us with one
+// warp to a row, one load after another). Bound by the latency of three loads
+// in a row; the L2 holds the partial results.
+constexpr int kMaxSplits = 256;
+
+template <typename T, int WARPS>
 __global__ void __launch_bounds__(kThreads) combine_kernel(AttnArgs a, AttnGeometry small, int64_t small_rows,
                                                            AttnGeometry large) {
-  pdl_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  constexpr int kRows = kThreads / 32 / WARPS;  // rows of a CTA
+  __shared__ float s_w[kRows][kMaxSplits];
+  __shared__ float s_red[kRows][WARPS][2];
+  __shared__ float s_o[WARPS > 1 ? WARPS : 1][WARPS > 1 ? 256 : 1];
+  const int lane = threadIdx.x & 31, group = threadIdx.x / (32 * WARPS), tid = threadIdx.x % (32 * WARPS), warp = tid >> 5;
+  const auto sync = [] {
+    if (WARPS == 1) {
+      __syncwarp();
+    } else {
+      __syncthreads();
+    }
+  };
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group;
   if (row >= a.tokens * a.heads) return;
   const int64_t token = row / a.heads;
   const int head = static_cast<int>(row - token * a.heads);
@@ -220,29 +236,80 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(AttnArgs a, AttnGeome
   AttnTile t;
   tile_at(a, g, s, ((token - first) * a.group + head % a.group) / g.rows, &t);
   if (t.rows == 0 || t.splits == 1) return;
+  pdl_wait();  // (the lengths and tables are the caller's; only the partial results are the kernels' before)
+  const int64_t step = a.tokens * a.heads;  // from one split to the next
+  const float2* ml = a.part_ml + row;
   float top = neg_inf();
-  for (int z = lane; z < t.splits; z += 32) top = fmaxf(top, a.part_ml[part_index(a, z, token, head)].x);
+  for (int z = tid; z < t.splits; z += 32 * WARPS) top = fmaxf(top, ml[z * step].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float ref = top == neg_inf() ? 0.0f : top;
+  if (WARPS > 1) {
+    if (lane == 0) s_red[group][warp][0] = top;
+    sync();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_red[group][w][0]);
+  }
   float sum = 0.0f;
-  for (int z = lane; z < t.splits; z += 32) {
-    const float2 ml = a.part_ml[part_index(a, z, token, head)];
-    sum += ml.y * exp2f(ml.x - ref);
+  for (int z = tid; z < t.splits; z += 32 * WARPS) {
+    const float2 x = ml[z * step];
+    const float w = x.x == neg_inf() ? (x.y == 0.0f ? 0.0f : 1.0f) : exp2f(x.x - top);  // (NaN scores alone: m = -inf, l = NaN)
+    s_w[group][z] = w;
+    sum += x.y * w;
   }
   sum = warp_sum(sum);
+  if (WARPS > 1 && lane == 0) s_red[group][warp][1] = sum;
+  sync();
+  if (WARPS > 1) {
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) sum += s_red[group][w][1];
+  }
   const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
   T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs;
-  for (int d = lane; d < a.dim; d += 32) {
-    float o = 0.0f;
-    for (int z = 0; z < t.splits; ++z) {
-      const int64_t at = part_index(a, z, token, head);
-      const float m = a.part_ml[at].x;
-      if (m != neg_inf()) o = fmaf(a.part_o[at * a.dim + d], exp2f(m - ref), o);
+  if (a.dim % 4 == 0) {
+    for (int d = lane * 4; d < a.dim; d += 128) {
+      const float* src = a.part_o + row * a.dim + d;
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int z = warp; z < t.splits; z += WARPS) {
+        const float4 y = *reinterpret_cast<const float4*>(src + z * step * a.dim);
+        const float w = s_w[group][z];
+        x.x = fmaf(y.x, w, x.x);
+        x.y = fmaf(y.y, w, x.y);
+        x.z = fmaf(y.z, w, x.z);
+        x.w = fmaf(y.w, w, x.w);
+      }
+      if (WARPS > 1) {
+        *reinterpret_cast<float4*>(&s_o[warp][d]) = x;
+      } else {
+        stf(dst + d, x.x * f);
+        stf(dst + d + 1, x.y * f);
+        stf(dst + d + 2, x.z * f);
+        stf(dst + d + 3, x.w * f);
+      }
     }
-    stf(dst + d, o * f);
+  } else {
+    for (int d = lane; d < a.dim; d += 32) {
+      float x = 0.0f;
+#pragma unroll 4
+      for (int z = warp; z < t.splits; z += WARPS) x = fmaf(a.part_o[(z * step + row) * a.dim + d], s_w[group][z], x);
+      if (WARPS > 1) {
+        s_o[warp][d] = x;
+      } else {
+        stf(dst + d, x * f);
+      }
+    }
   }
-  if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+  if (WARPS > 1) {
+    sync();
+    for (int d = tid; d < a.dim; d += 32 * WARPS) {
+      float x = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) x += s_o[w][d];
+      stf(dst + d, x * f);
+    }
+  }
+  if (tid == 0 && a.lse) a.lse[row] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
 }
 
 // ------------------------------------------------------------------- host --
@@ -271,9 +338,10 @@ void set_splits(AttnGeometry* g, const hc_paged_attention_t& a, int64_t keys, in
   len = ceil_div(len, g->align) * g->align;
   g->split_len = static_cast<int>(std::min<int64_t>(len, int64_t{1} << 30));
   g->splits = static_cast<int>(std::max<int64_t>(1, ceil_div(keys + g->align, g->split_len)));
-  if (g->splits > 256) {
-    g->splits = 256;
-    g->split_len = static_cast<int>(std::min<int64_t>(ceil_div(ceil_div(keys, 256), g->align) * g->align, int64_t{1} << 30));
+  if (g->splits > kMaxSplits) {
+    g->splits = kMaxSplits;
+    g->split_len =
+        static_cast<int>(std::min<int64_t>(ceil_div(ceil_div(keys, kMaxSplits), g->align) * g->align, int64_t{1} << 30));
   }
 }
 
@@ -294,7 +362,7 @@ Plan plan_of(const hc_paged_attention_t& a, bool aligned, int num_sms) {
     const int64_t span = ceil_div(rows, group) + 1;
     return a.window > 0 ? std::min<int64_t>(max_kv, a.window + span) : max_kv;
   };
-  set_splits(&p.small, a, keys_of(16), a.seqs, num_sms, 4, 128);
+  set_splits(&p.small, a, keys_of(16), a.seqs, num_sms, 8, 64);
   set_splits(&p.large, a, keys_of(64), std::max<int64_t>(1, a.tokens * group / 64), num_sms, 2, 256);
   (void)max_q;
   p.splits = std::max(p.use_small ? p.small.splits : 1, p.use_large ? p.large.splits : 1);
@@ -376,8 +444,14 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
     if (e != cudaSuccess) return e;
   }
   if (p.splits > 1) {
-    const unsigned grid = static_cast<unsigned>(ceil_div(a.tokens * a.heads, kThreads / 32));
-    e = launch_pdl(combine_kernel<T>, dim3(grid), dim3(kThreads), 0, s, 1, d, p.small, p.small_rows, p.large);
+    const int64_t rows = a.tokens * a.heads;
+    if (p.splits > 8 && rows < 16384) {
+      e = launch_pdl(combine_kernel<T, 8>, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, s, 1, d, p.small,
+                     p.small_rows, p.large);
+    } else {
+      e = launch_pdl(combine_kernel<T, 1>, dim3(static_cast<unsigned>(ceil_div(rows, kThreads / 32))), dim3(kThreads), 0, s,
+                     1, d, p.small, p.small_rows, p.large);
+    }
   }
   return e;
 }
