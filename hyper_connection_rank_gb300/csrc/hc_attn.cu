@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(AttnArgs a, AttnGeome
   if (row >= a.tokens * a.heads) return;
   const int64_t token = row / a.heads;
   const int head = static_cast<int>(row - token * a.heads);
-  const int s = a.b.cu_q ? warp_last_le(a.b.seqs, token, [&](int i) { return static_cast<int64_t>(a.b.cu_q[i]); })
+  const int s = a.b.cu_q ? warp_last_le(a.b.seqs, token, [&](int i) { return first_row(a.b, i); })
                          : static_cast<int>(token);
   const int64_t first = first_row(a.b, s), all = (first_row(a.b, s + 1) - first) * a.group;
   const AttnGeometry& g = all <= small_rows ? small : large;
@@ -315,12 +315,14 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(AttnArgs a, AttnGeome
 // ------------------------------------------------------------------- host --
 
 struct Plan {
+  bool tile;           // all sequences by hc_attn_tile.cu; the rest does not matter then
   AttnGeometry small, large;
-  int64_t small_rows;  // sequences with at most so many rows go to the small tiles
-  bool use_small, use_large;
+  bool use_large;      // sequences of more than kSmallRows rows go to the large tiles
   bool rows_kernel;    // small tiles by hc_attn_rows.cu
   int splits;          // the larger of the two
 };
+
+constexpr int kSmallRows = 16;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -345,6 +347,12 @@ void set_splits(AttnGeometry* g, const hc_paged_attention_t& a, int64_t keys, in
   }
 }
 
+// Kernels for a call. Where no sequence has more than 16 rows (single tokens
+// of up to 16 grouped heads), the small tiles serve all: they read keys at the
+// rate of memory, and a tile of 256 rows would be empty. Anything longer goes
+// to the tile kernel with all sequences of the batch, where type, head size and
+// page size allow it; its single tokens cost it less than a second kernel.
+// Otherwise small and large general tiles share the sequences.
 Plan plan_of(const hc_paged_attention_t& a, bool aligned, int num_sms) {
   Plan p = {};
   const bool fast = !(a.flags & HC_FLAG_FORCE_GENERAL);
@@ -352,20 +360,21 @@ Plan plan_of(const hc_paged_attention_t& a, bool aligned, int num_sms) {
   const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
   const int64_t max_kv = a.max_kv > 0 ? std::min<int64_t>(a.max_kv, cap) : cap;
   const int64_t max_q = a.cu_q == nullptr ? 1 : a.max_q > 0 ? std::min<int64_t>(a.max_q, a.tokens) : a.tokens;
-  p.small_rows = 16;
-  p.use_small = true;
+  const bool few = max_q * group <= kSmallRows;
+  p.splits = 1;
+  p.tile = !few && fast && attn_tile_supported(a.dtype, a.head_dim, a.page_size, a.scale, aligned);
+  if (p.tile) return p;
   p.rows_kernel = fast && attn_rows_supported(a.dtype, a.head_dim, aligned);
-  p.use_large = a.cu_q != nullptr || group > p.small_rows;
-  p.small = AttnGeometry{16, kKeys, 0, 0};
+  p.use_large = !few;
+  p.small = AttnGeometry{kSmallRows, kKeys, 0, 0};
   p.large = AttnGeometry{64, kKeys, 0, 0};
   const auto keys_of = [&](int rows) {
     const int64_t span = ceil_div(rows, group) + 1;
     return a.window > 0 ? std::min<int64_t>(max_kv, a.window + span) : max_kv;
   };
-  set_splits(&p.small, a, keys_of(16), a.seqs, num_sms, 8, 64);
-  set_splits(&p.large, a, keys_of(64), std::max<int64_t>(1, a.tokens * group / 64), num_sms, 2, 256);
-  (void)max_q;
-  p.splits = std::max(p.use_small ? p.small.splits : 1, p.use_large ? p.large.splits : 1);
+  set_splits(&p.small, a, keys_of(p.small.rows), a.seqs, num_sms, 8, 64);
+  set_splits(&p.large, a, keys_of(p.large.rows), std::max<int64_t>(1, a.tokens * group / 64), num_sms, 2, 256);
+  p.splits = std::max(p.small.splits, p.use_large ? p.large.splits : 1);
   return p;
 }
 
@@ -382,7 +391,7 @@ AttnArgs args_of(const hc_paged_attention_t& a) {
   d.v = a.v_cache;
   d.out = a.out;
   d.lse = a.lse;
-  d.b = BatchView{a.page_table, a.kv_lens, a.cu_q, a.table_stride, a.num_pages, a.seqs, a.max_pages, a.page_size};
+  d.b = BatchView{a.page_table, a.kv_lens, a.cu_q, a.table_stride, a.num_pages, a.seqs, a.max_pages, a.page_size, a.tokens};
   d.tokens = a.tokens;
   d.q_ts = a.q_token_stride;
   d.q_hs = a.q_head_stride;
@@ -427,30 +436,29 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
     d.part_ml = static_cast<float2*>(a.workspace);
     d.part_o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + align_up(rows * 8, 256));
   }
-  cudaError_t e = cudaSuccess;
-  if (p.use_small) {
-    d.g = p.small;
-    d.min_rows = 1;
-    d.max_rows = p.small_rows;
-    const int64_t slots = slots_of(a, p.small.rows);
-    e = p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s) : general_d<T, 16>(d, slots, s);
-    if (e != cudaSuccess) return e;
-  }
+  if (p.tile) return launch_attn_tile(d, a.dtype, a.workspace, num_sms, s);
+  const int64_t slots = slots_of(a, p.small.rows);
+  d.g = p.small;
+  d.min_rows = 1;
+  d.max_rows = p.use_large ? kSmallRows : INT64_MAX;
+  cudaError_t e = p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s) : general_d<T, kSmallRows>(d, slots, s);
+  if (e != cudaSuccess) return e;
   if (p.use_large) {
     d.g = p.large;
-    d.min_rows = p.small_rows + 1;
+    d.min_rows = kSmallRows + 1;
     d.max_rows = INT64_MAX;
     e = general_d<T, 64>(d, slots_of(a, p.large.rows), s);
     if (e != cudaSuccess) return e;
   }
+  const int64_t small_rows = p.use_large ? kSmallRows : INT64_MAX;
   if (p.splits > 1) {
     const int64_t rows = a.tokens * a.heads;
     if (p.splits > 8 && rows < 16384) {
       e = launch_pdl(combine_kernel<T, 8>, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, s, 1, d, p.small,
-                     p.small_rows, p.large);
+                     small_rows, p.large);
     } else {
       e = launch_pdl(combine_kernel<T, 1>, dim3(static_cast<unsigned>(ceil_div(rows, kThreads / 32))), dim3(kThreads), 0, s,
-                     1, d, p.small, p.small_rows, p.large);
+                     1, d, p.small, small_rows, p.large);
     }
   }
   return e;
@@ -459,7 +467,9 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
 }  // namespace
 
 size_t attention_workspace(const hc_paged_attention_t& a, bool aligned, int num_sms) {
-  return part_bytes(a, plan_of(a, aligned, num_sms));
+  const Plan p = plan_of(a, aligned, num_sms);
+  if (p.tile) return attn_tile_workspace(a.tokens, a.heads / a.kv_heads, a.seqs, a.head_dim, num_sms);
+  return part_bytes(a, p);
 }
 
 cudaError_t launch_attention(const hc_paged_attention_t& a, bool aligned, int num_sms, cudaStream_t s) {

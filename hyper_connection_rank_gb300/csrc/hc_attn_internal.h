@@ -11,4 +11,10 @@ namespace hc {
 bool attn_rows_supported(int dtype, int dim, bool aligned);
 cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, int64_t slots, cudaStream_t s);
 
+// Any number of rows, on tcgen05 (hc_attn_tile.cu); takes a workspace of its
+// own and needs no splits.
+bool attn_tile_supported(int dtype, int dim, int page, float scale, bool aligned);
+size_t attn_tile_workspace(int64_t tokens, int group, int seqs, int dim, int num_sms);
+cudaError_t launch_attn_tile(const AttnArgs& a, int dtype, void* workspace, int num_sms, cudaStream_t s);
+
 }  // namespace hc

@@ -1,0 +1,836 @@
+// Attention over a paged cache for many rows (fp16/bf16, heads of 64 or 128,
+// pages that divide 128 keys or are whole multiples of them): chunks of a
+// prompt, and batches that mix chunks with single tokens.
+//
+// Mathematics: per tile of rows, over key blocks j of 128,
+//   S = Q K_j^T;  P = 2^(S c - m);  l += sum P;  O += P V_j
+// with the running maximum m of each row. O is rescaled (O, l *= 2^(m - m'))
+// only when a row's maximum has risen by more than 8 (a factor of 256) above
+// the m in use: until then weights up to 2^8 are exact in either type, so most
+// blocks touch O with nothing but the MMA. P is rounded to T for its product (the
+// tensor core's operands are 16 bits); l sums the weights before that.
+//
+// Bound: the tensor cores, 4 * head_dim flops for each pair of row and key.
+// One CTA per SM holds two tiles, A and B, of 128 rows. Both products run on
+// tcgen05: S = Q K^T from shared memory into tensor memory (128 columns for
+// each tile), and O += P V with P read from tensor memory, where it takes the
+// place of the S it came from. The MMA warp issues PV_A(j), QK_A(j+1),
+// PV_B(j), QK_B(j+1) in turn, so that while the softmax warps of one tile work,
+// the tensor core has the other tile's two products to do. Two warpgroups do
+// the softmax, a thread to a row (no exchange between lanes); one warp copies
+// keys and values by TMA, a box per page and 64 features, into a ring. Of the
+// 168 * 384 registers that the CTA starts with, the softmax threads take 216
+// each, so that a row's 128 scores stay in them, and the others 72
+// (2 * 128 * 216 + 128 * 72 = 384 * 168).
+//
+// Work: all tiles' key blocks, for all key heads, laid end to end, are cut into
+// equal runs, one for each SM (hc_attn.cuh's slots give the tiles, plan_kernel
+// their prefix sums). A tile that a cut goes through is written as partial
+// sums by every CTA that has a piece of it and joined by join_kernel; at most
+// two pieces to a CTA are of that kind. So a long prompt, many short ones and one
+// short chunk over a long context all fill the GPU, without a choice of split.
+#include <cuda.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "hc_async.cuh"
+#include "hc_attn_internal.h"
+#include "hc_tc.cuh"
+
+namespace hc {
+namespace {
+
+constexpr int kRows = 128;        // rows of a tile, an MMA's M
+constexpr int kPair = 2 * kRows;  // rows of a CTA's two tiles
+constexpr int kKeys = 128;        // keys of a block, N of the first product
+constexpr int kThreads = 384;     // two softmax warpgroups, and one with the copy warp and the MMA warp
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kMinBlocks = 4;     // key blocks that are worth a CTA
+constexpr float kLazy = 8.0f;     // rise of a row's maximum (base-2) that O is rescaled for
+
+__device__ unsigned int g_tile_wait_timeouts = 0;
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;             // boxes of 64 features
+  static constexpr int kHalf = kKeys * 128;          // bytes of one such box of 128 rows
+  static constexpr int kSlot = kHalves * kHalf;      // a block's keys or values
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kQ = kHalves * kRows * 128;   // one tile's queries
+  static constexpr int kSmem = 2 * kQ + kSlots * kSlot + 1024;
+};
+
+struct Work {
+  const int32_t* prefix;  // blocks of the tiles before each slot, per key head; [slots] = all
+  int slots, ctas;
+  float2* part_ml;        // [2 * ctas][kPair]
+  float* part_o;          // [2 * ctas][kPair][dim]
+};
+
+// --------------------------------------------------------------- schedule --
+
+__device__ __forceinline__ int64_t blocks_of(const AttnTile& t) {
+  const int64_t n = (t.hi - t.base + kKeys - 1) / kKeys;
+  return n < 1 ? 1 : n;  // a tile that sees nothing still writes its zeros
+}
+
+// Number of key blocks of every slot's tile, as an exclusive prefix.
+__global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, int32_t* prefix, int slots) {
+  __shared__ int red[33];
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < slots; i += 1024) prefix[i] = 0;
+  __syncthreads();
+  for (int s = warp; s < a.b.seqs; s += 32) {
+    const int64_t first = first_row(a.b, s), next = first_row(a.b, s + 1);
+    const int64_t lo = first * a.group / kPair + s, hi = next * a.group / kPair + s + 1;
+    for (int64_t i = lo + lane; i < hi; i += 32) {
+      AttnTile t;
+      tile_at(a, a.g, s, i - lo, &t);
+      if (i < slots) prefix[i] = t.rows == 0 ? 0 : static_cast<int>(blocks_of(t));
+    }
+  }
+  __syncthreads();
+  // exclusive prefix in place, 1024 slots at a time
+  int before = 0;
+  for (int i0 = 0; i0 <= slots; i0 += 1024) {
+    const int i = i0 + threadIdx.x;
+    const int v = i < slots ? prefix[i] : 0;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) red[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      const int w = red[lane];
+      int z = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, z, o);
+        if (lane >= o) z += y;
+      }
+      red[lane] = z - w;
+      if (lane == 31) red[32] = z;
+    }
+    __syncthreads();
+    if (i <= slots) prefix[i] = before + red[warp] + x - v;
+    before += red[32];
+    __syncthreads();
+  }
+}
+
+// The run of key blocks that CTA c has, out of all: [u0, u1).
+struct Run {
+  int64_t per_head, all;
+  int ctas;
+  __device__ Run(const Work& w, int kv_heads) {
+    per_head = w.prefix[w.slots];
+    all = per_head * kv_heads;
+    const int64_t most = (all + kMinBlocks - 1) / kMinBlocks;
+    ctas = static_cast<int>(most < 1 ? 1 : most < w.ctas ? most : w.ctas);
+  }
+  __device__ int64_t start(int c) const { return all * c / ctas; }
+};
+
+// A CTA's piece of one tile pair: blocks [j0, j1) of its n.
+struct Segment {
+  AttnTile t;
+  int kv_head, j0, j1, n;
+  int64_t at;  // of the tile's first block among all
+};
+
+// The segment that starts at block u of all, in a run that ends at u1 (full warps).
+__device__ __forceinline__ void segment_at(const AttnArgs& a, const Work& w, const Run& run, int64_t u, int64_t u1,
+                                           Segment* g) {
+  const int h = static_cast<int>(u / run.per_head);
+  const int64_t v = u - h * run.per_head;
+  const int slot = warp_last_le(w.slots, v, [&](int i) { return static_cast<int64_t>(w.prefix[i]); });
+  const auto start = [&](int s) { return first_row(a.b, s) * a.group / kPair + s; };
+  const int s = warp_last_le(a.b.seqs, slot, start);
+  tile_at(a, a.g, s, slot - start(s), &g->t);
+  g->kv_head = h;
+  g->at = h * run.per_head + w.prefix[slot];
+  g->n = w.prefix[slot + 1] - w.prefix[slot];
+  g->j0 = static_cast<int>(u - g->at);
+  const int64_t end = u1 - g->at;
+  g->j1 = end < g->n ? static_cast<int>(end) : g->n;
+}
+
+// Blocks of tile x (0: A, 1: B) of a pair: those up to the last key its last row sees.
+__device__ __forceinline__ int tile_rows(const AttnTile& t, int x) {
+  const int r = t.rows - x * kRows;
+  return r < 0 ? 0 : r < kRows ? r : kRows;
+}
+__device__ __forceinline__ int tile_blocks(const AttnArgs& a, const AttnTile& t, int x) {
+  const int rows = tile_rows(t, x);
+  if (rows == 0) return 0;
+  const int64_t end = row_position(t, t.row0 + x * kRows + rows - 1, a.group) + 1;
+  const int64_t n = (end - t.base + kKeys - 1) / kKeys;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+// ------------------------------------------------------------ tensor memory --
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Marks registers that an asynchronous load filled as written here, after its wait.
+__device__ __forceinline__ void landed32(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile(""
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                   "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], issued by one thread; A holds pairs of
+// 16-bit elements of a row in each 32-bit column.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// x * y + z on two floats at once.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return d;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ----------------------------------------------------------------- kernel --
+
+struct Bars {
+  uint64_t q_full[2];   // a tile's queries lie in shared memory
+  uint64_t s_full[2];   // its scores lie in tensor memory
+  uint64_t p_full[2];   // its weights do, and O may be added to
+  uint64_t o_done[2];   // the product with the values is done
+  uint64_t kv_full[8], kv_empty[8];
+  uint32_t tmem;
+};
+
+// A wait that gave up ends its role's loop; the other roles' next waits give
+// up in turn, and the rows of the tile at hand become NaN.
+#define HC_WAIT(bar, parity)                                               \
+  do {                                                                     \
+    if (!mbar_wait((bar), (parity), &g_tile_wait_timeouts)) return false;  \
+  } while (0)
+
+template <typename T, int D, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Work w,
+                const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+  using C = Cfg<D>;
+  extern __shared__ unsigned char raw[];
+  __shared__ Bars bars;
+  __shared__ Segment s_seg[8];  // each softmax warp's segment at hand (held here, not in registers)
+  unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  unsigned char* const ring = smem + 2 * C::kQ;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars.q_full[x], kRows);
+      mbar_init(&bars.s_full[x], 1);
+      mbar_init(&bars.p_full[x], kRows);
+      mbar_init(&bars.o_done[x], 1);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&bars.kv_full[i], 1);
+      mbar_init(&bars.kv_empty[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars.tmem, 512);
+    tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&k_map);
+    tma_prefetch_desc(&v_map);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  pdl_trigger();
+  pdl_wait();
+  const Run run(w, a.kv_heads);
+  const bool mine = static_cast<int>(blockIdx.x) < run.ctas;
+  const int64_t u0 = mine ? run.start(blockIdx.x) : 0, u1 = mine ? run.start(blockIdx.x + 1) : 0;
+  // tensor memory: S (and P) of A and B, then O of A and B
+  constexpr uint32_t kO = 2 * kKeys;
+
+  if (warp >= kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kLoadWarp) {
+      // ---- copies: for each segment K(j0), V(j0), K(j0+1), ... ----
+      const int page = a.b.page_size;
+      const int box = page < kKeys ? page : kKeys;       // tokens of a copy
+      const int boxes = kKeys / box * C::kHalves;        // copies of a block's keys
+      int slot = 0;
+      uint32_t round = 0;
+      const auto copy_all = [&]() -> bool {
+        for (int64_t u = u0; u < u1;) {
+          Segment g;
+          segment_at(a, w, run, u, u1, &g);
+          for (int j = g.j0; j < g.j1; ++j) {
+            const int64_t key0 = g.t.base + static_cast<int64_t>(j) * kKeys;
+            // pages of this lane's copies; a box without a key that any row sees lies outside the pool, and reads zeros
+            int at[2] = {-1, -1};
+            int off[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int b = (lane + 32 * i) / C::kHalves;
+              const int64_t key = key0 + b * box;
+              if (lane + 32 * i < boxes && key < g.t.hi && key + box > g.t.lo) {
+                const uint32_t e = static_cast<uint32_t>(key) / static_cast<uint32_t>(page);
+                at[i] = page_of(a.b, g.t.s, e);
+                off[i] = static_cast<int>(static_cast<uint32_t>(key) - e * page);
+              }
+            }
+            for (int kind = 0; kind < 2; ++kind) {
+              HC_WAIT(&bars.kv_empty[slot], (round & 1) ^ 1);
+              if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[slot], C::kSlot);
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int e = lane + 32 * i;
+                if (e < boxes) {
+                  const int h = e % C::kHalves, b = e / C::kHalves;
+                  tma_load_4d(smem_addr(ring + slot * C::kSlot + h * C::kHalf) + b * box * 128, kind ? &v_map : &k_map,
+                              h * 64, off[i], g.kv_head, at[i] < 0 ? static_cast<int>(a.b.num_pages) : at[i],
+                              &bars.kv_full[slot]);
+                }
+              }
+              if (++slot == C::kSlots) {
+                slot = 0;
+                ++round;
+              }
+            }
+          }
+          u = g.at + g.j1;
+        }
+        return true;
+      };
+      const bool ok = copy_all();
+      // the CTA keeps its memory until the last copies have landed and the last products have read them
+      for (int i = 0; i < C::kSlots; ++i) {
+        const uint32_t used = i < slot ? round : round - 1;
+        if (i < slot || round > 0) {
+          mbar_wait(&bars.kv_full[i], used & 1, nullptr);
+          if (ok) mbar_wait(&bars.kv_empty[i], used & 1, &g_tile_wait_timeouts);
+        }
+      }
+    } else if (warp == kMmaWarp) {
+      // ---- products ----
+      constexpr uint32_t kQk = idesc_f16(std::is_same<T, __nv_bfloat16>::value, kRows, kKeys, false, false);
+      constexpr uint32_t kPv = idesc_f16(std::is_same<T, __nv_bfloat16>::value, kRows, D, false, true);
+      int slot = 0;
+      uint32_t round = 0, q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
+      const auto advance = [&] {
+        if (++slot == C::kSlots) {
+          slot = 0;
+          ++round;
+        }
+      };
+      const auto issue_qk = [&](int x, int k_slot) {
+        if (lane == 0) {
+          const uint32_t q = smem_addr(smem + x * C::kQ), k = smem_addr(ring + k_slot * C::kSlot);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t o = (ks / 4) * C::kHalf + (ks % 4) * 32;
+            mma_f16(tmem + x * kKeys, smem_desc_sw128(q + o, 16, 1024), smem_desc_sw128(k + o, 16, 1024), kQk, ks > 0);
+          }
+          mma_commit(&bars.s_full[x]);
+        }
+        __syncwarp();
+      };
+      const auto multiply_all = [&]() -> bool {
+        for (int64_t u = u0; u < u1;) {
+          Segment g;
+          segment_at(a, w, run, u, u1, &g);
+          const int ends[2] = {min(tile_blocks(a, g.t, 0), g.j1), min(tile_blocks(a, g.t, 1), g.j1)};
+          // first scores of both tiles
+          HC_WAIT(&bars.kv_full[slot], round & 1);
+          for (int x = 0; x < 2; ++x)
+            if (g.j0 < ends[x]) {
+              HC_WAIT(&bars.q_full[x], q_seen[x] & 1);
+              ++q_seen[x];
+              tc_fence_after();
+              issue_qk(x, slot);
+            }
+          if (lane == 0) mma_commit(&bars.kv_empty[slot]);
+          advance();
+          for (int j = g.j0; j < g.j1; ++j) {
+            const int v_slot = slot;
+            HC_WAIT(&bars.kv_full[slot], round & 1);
+            advance();
+            const int k_slot = slot;
+            const bool more = j + 1 < g.j1;
+            if (more) HC_WAIT(&bars.kv_full[slot], round & 1);
+            // values beside the keys that the tile sees may be anything; a weight of zero must meet a zero
+            const int64_t key0 = g.t.base + static_cast<int64_t>(j) * kKeys;
+            if (key0 < g.t.lo || key0 + kKeys > g.t.hi) {
+              const int lo = static_cast<int>(g.t.lo > key0 ? min(g.t.lo - key0, static_cast<int64_t>(kKeys)) : 0);
+              const int hi = static_cast<int>(g.t.hi > key0 ? min(g.t.hi - key0, static_cast<int64_t>(kKeys)) : 0);
+              const int n = (lo + kKeys - hi) * 8 * C::kHalves;
+              for (int e = lane; e < n; e += 32) {
+                const int c = e & 7, h = (e >> 3) % C::kHalves, i = (e >> 3) / C::kHalves;
+                const int r = i < lo ? i : hi + (i - lo);
+                *reinterpret_cast<uint4*>(ring + v_slot * C::kSlot + h * C::kHalf + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_async_smem();
+              __syncwarp();
+            }
+            for (int x = 0; x < 2; ++x) {
+              if (j < ends[x]) {
+                HC_WAIT(&bars.p_full[x], p_seen[x] & 1);
+                ++p_seen[x];
+                tc_fence_after();
+                if (lane == 0) {
+                  const uint32_t v = smem_addr(ring + v_slot * C::kSlot);
+#pragma unroll
+                  for (int ks = 0; ks < kKeys / 16; ++ks)
+                    mma_f16_ts(tmem + kO + x * D, tmem + x * kKeys + ks * 8, smem_desc_sw128(v + ks * 2048, C::kHalf, 1024),
+                               kPv, j > g.j0 || ks > 0);
+                  mma_commit(&bars.o_done[x]);
+                }
+                __syncwarp();
+              }
+              if (more && j + 1 < ends[x]) issue_qk(x, k_slot);
+            }
+            if (lane == 0) {
+              mma_commit(&bars.kv_empty[v_slot]);
+              if (more) mma_commit(&bars.kv_empty[k_slot]);
+            }
+            __syncwarp();
+            if (more) advance();
+          }
+          u = g.at + g.j1;
+        }
+        return true;
+      };
+      multiply_all();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ---- softmax: warpgroup x has tile x, a thread to a row ----
+    const int x = warp >> 2, row = threadIdx.x & (kRows - 1);
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // this warp's 32 lanes
+    const uint32_t s_at = lanes + x * kKeys, o_at = lanes + kO + x * D;
+    const ScoreMap map = score_map(a.scale, a.softcap);
+    uint32_t s_seen = 0, o_seen = 0;
+    Segment& g = s_seg[warp];
+    const auto keep = [&](const Segment& sg) {
+      __syncwarp();
+      if (lane == 0) g = sg;
+      __syncwarp();
+    };
+    const auto load_q = [&](const Segment& sg) {
+      if (sg.j0 >= min(tile_blocks(a, sg.t, x), sg.j1)) return;
+      const uint4* src = nullptr;
+      if (row < tile_rows(sg.t, x)) {
+        int64_t token;
+        int head;
+        row_owner(a, sg.t, sg.kv_head, x * kRows + row, &token, &head);
+        src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + token * a.q_ts + head * a.q_hs);
+      }
+      unsigned char* dst = smem + x * C::kQ + row * 128;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4)) =
+            src ? src[c] : make_uint4(0, 0, 0, 0);
+      fence_async_smem();
+      mbar_arrive(&bars.q_full[x]);
+    };
+    float m = neg_inf(), l = 0.0f;
+    const auto softmax_all = [&]() -> bool {
+      if (u0 < u1) {
+        Segment first;
+        segment_at(a, w, run, u0, u1, &first);
+        load_q(first);
+        keep(first);
+      }
+      for (int64_t u = u0; u < u1;) {
+        const int end = min(tile_blocks(a, g.t, x), g.j1);
+        const int rows = tile_rows(g.t, x);
+        const int64_t u_next = g.at + g.j1;
+        // keys that this row sees, from the tile's first block on: [from, to); those that every row sees: [all_from, all_to)
+        int from = 0, to = 0, all_from = 0, all_to = 0;
+        if (rows > 0) {
+          const int64_t r0 = g.t.row0 + x * kRows;
+          const int64_t p0 = row_position(g.t, r0, a.group) - g.t.base, p1 = row_position(g.t, r0 + rows - 1, a.group) - g.t.base;
+          const int64_t p = row_position(g.t, r0 + row, a.group) - g.t.base;
+          const auto cut = [](int64_t v) { return static_cast<int>(v < 0 ? 0 : v); };
+          // (rows past the last are computed along and never written; they are not masked)
+          to = row < rows ? cut(p + 1) : INT32_MAX;
+          from = row < rows && a.window > 0 ? cut(p - a.window + 1) : 0;
+          all_to = cut(p0 + 1);
+          all_from = a.window > 0 ? cut(p1 - a.window + 1) : 0;
+        }
+        m = neg_inf();
+        l = 0.0f;
+        for (int j = g.j0; j < end; ++j) {
+          uint32_t s[kKeys];
+          HC_WAIT(&bars.s_full[x], s_seen & 1);
+          ++s_seen;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_at + c, s + c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) landed32(s + c);
+          float* f = reinterpret_cast<float*>(s);
+          if (CAP) {
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c) f[c] = map_score(map, f[c]);
+          }
+          const int j0 = j * kKeys;
+          if (j0 < all_from || j0 + kKeys > all_to) {
+            const int lo = from - j0, hi = to - j0;
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c)
+              if (c < lo || c >= hi) f[c] = neg_inf();
+          }
+          float top0 = fmaxf(f[0], f[1]), top1 = fmaxf(f[2], f[3]);
+#pragma unroll
+          for (int c = 4; c < kKeys; c += 4) {
+            top0 = fmaxf(top0, fmaxf(f[c], f[c + 1]));
+            top1 = fmaxf(top1, fmaxf(f[c + 2], f[c + 3]));
+          }
+          const float mul = CAP ? 1.0f : map.mul;
+          const float top = fmaxf(top0, top1) * mul;
+          if (j == g.j0) {
+            m = top;
+          } else if (__any_sync(0xffffffffu, top > m + kLazy || (m == neg_inf() && top > m))) {
+            const float now = fmaxf(m, top);
+            const float scale = now == neg_inf() ? 1.0f : ex2(m - now);
+            m = now;
+            l *= scale;
+            // O holds the products up to block j-1
+            HC_WAIT(&bars.o_done[x], (o_seen - 1) & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_at + c, o);
+              tmem_wait_ld();
+              landed32(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
+              tmem_st32(o_at + c, o);
+            }
+            tmem_wait_st();
+          }
+          const float ref = m == neg_inf() ? 0.0f : m;
+          const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(-ref, -ref);
+          float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+          for (int h = 0; h < kKeys; h += 64) {
+            uint32_t p[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+              float2 y0 = fma2(make_float2(f[h + c], f[h + c + 1]), mul2, ref2);
+              float2 y1 = fma2(make_float2(f[h + c + 2], f[h + c + 3]), mul2, ref2);
+              y0 = make_float2(ex2(y0.x), ex2(y0.y));
+              y1 = make_float2(ex2(y1.x), ex2(y1.y));
+              sum0 = add2(sum0, y0);
+              sum1 = add2(sum1, y1);
+              p[c / 2] = pack2<T>(y0.x, y0.y);
+              p[c / 2 + 1] = pack2<T>(y1.x, y1.y);
+            }
+            tmem_st32(s_at + h / 2, p);
+          }
+          sum0 = add2(sum0, sum1);
+          l += sum0.x + sum0.y;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars.p_full[x]);
+          ++o_seen;
+        }
+        // the tile's scores are all formed, so its queries make room for the next segment's
+        Segment next;
+        if (u_next < u1) {
+          segment_at(a, w, run, u_next, u1, &next);
+          load_q(next);
+        }
+        if (rows > 0) {
+          const bool partial = g.j0 > 0 || g.j1 < g.n;
+          const bool some = end > g.j0;
+          if (some) {
+            HC_WAIT(&bars.o_done[x], (o_seen - 1) & 1);
+            tc_fence_after();
+          }
+          if (partial) {
+            const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + (g.j0 > 0 ? 0 : 1)) * kPair + x * kRows + row;
+            w.part_ml[at] = some ? make_float2(m, l) : make_float2(neg_inf(), 0.0f);
+            if (some) {
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_at + c, o);
+                tmem_wait_ld();
+                landed32(o);
+                uint4* dst = reinterpret_cast<uint4*>(w.part_o + at * D + c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              }
+            }
+          } else {
+            int64_t token = 0;
+            int head = 0;
+            if (row < rows) row_owner(a, g.t, g.kv_head, x * kRows + row, &token, &head);
+            T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs;
+            const bool wide = ((a.o_ts | a.o_hs) & 7) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_at + c, o);
+              tmem_wait_ld();
+              landed32(o);
+              if (row < rows) {
+                uint32_t y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  y[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                if (wide) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4*>(dst + c + 8 * i) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    reinterpret_cast<uint16_t*>(dst)[c + i] = static_cast<uint16_t>(y[i / 2] >> (16 * (i & 1)));
+                }
+              }
+            }
+            if (row < rows && a.lse) a.lse[token * a.heads + head] = l == 0.0f ? neg_inf() : m * kLn2 + logf(l);
+          }
+          tc_fence_before();  // O has been read before the next segment's weights let it be written
+        }
+        if (u_next < u1) keep(next);
+        u = u_next;
+      }
+      return true;
+    };
+    if (!softmax_all() && u0 < u1 && row < tile_rows(g.t, x)) {
+      int64_t token;
+      int head;
+      row_owner(a, g.t, g.kv_head, x * kRows + row, &token, &head);
+      for (int d = 0; d < D; ++d)
+        stf(static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + d, __int_as_float(0x7fffffff));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of the tile that cut c + 1 goes through, if that is the
+// first cut in it; a warp to a row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) join_kernel(AttnArgs a, Work w) {
+  __shared__ float s_w[8][160];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  const Run run(w, a.kv_heads);
+  const int c0 = blockIdx.x;
+  if (c0 + 1 >= run.ctas) return;
+  const int64_t u = run.start(c0 + 1);
+  if (u >= run.all) return;
+  Segment g;
+  segment_at(a, w, run, u, run.all, &g);
+  if (g.at == u || run.start(c0) > g.at) return;
+  const int64_t end = g.at + g.n;
+  int pieces = 1;
+  while (c0 + pieces < run.ctas && run.start(c0 + pieces) < end) ++pieces;
+  const int r = blockIdx.y * 8 + warp;
+  if (r >= g.t.rows) return;
+  // piece 0 is the last of its CTA's segments, the others are the first of theirs
+  const auto index = [&](int i) { return (2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0)) * kPair + r; };
+  float top = neg_inf();
+  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, w.part_ml[index(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.0f;
+  for (int i = lane; i < pieces; i += 32) {
+    const float2 ml = w.part_ml[index(i)];
+    const float f = ml.x == neg_inf() ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - top);
+    s_w[warp][i] = f;
+    sum += ml.y * f;
+  }
+  sum = warp_sum(sum);
+  __syncwarp();
+  constexpr int V = D / 32;
+  float o[V] = {};
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const float f = s_w[warp][i];
+    if (f != 0.0f) {
+      const float* src = w.part_o + index(i) * D + lane * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = fmaf(src[e], f, o[e]);
+    }
+  }
+  int64_t token;
+  int head;
+  row_owner(a, g.t, g.kv_head, r, &token, &head);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + lane * V;
+#pragma unroll
+  for (int e = 0; e < V; ++e) stf(dst + e, o[e] * inv);
+  if (lane == 0 && a.lse) a.lse[token * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+}
+
+// ------------------------------------------------------------------- host --
+
+// The pool as (features, tokens of a page, key heads, pages), boxes of 64
+// features and a page's tokens (128 at most) of one head.
+bool make_pool_map(CUtensorMap* m, const void* base, bool bf16, const AttnArgs& a) {
+  auto fn = tmap_encoder();
+  if (fn == nullptr) return false;
+  // strides of axes with one entry are never used, but must be valid
+  const int64_t row = a.dim, ts = a.b.page_size > 1 ? a.c_ts : row, hs = a.kv_heads > 1 ? a.c_hs : row,
+                ps = a.b.num_pages > 1 ? a.c_ps : row;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(a.b.page_size),
+                              static_cast<cuuint64_t>(a.kv_heads), static_cast<cuuint64_t>(a.b.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ts) * 2, static_cast<cuuint64_t>(hs) * 2,
+                                 static_cast<cuuint64_t>(ps) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(std::min(a.b.page_size, kKeys)), 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base),
+            dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, bool CAP>
+cudaError_t launch_t(const AttnArgs& a, const Work& w, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+  constexpr size_t smem = Cfg<D>::kSmem;
+  cudaError_t e = ensure_smem<tile_kernel<T, D, CAP>>(smem);
+  if (e != cudaSuccess) return e;
+  plan_kernel<<<1, 1024, 0, s>>>(a, const_cast<int32_t*>(w.prefix), w.slots);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(tile_kernel<T, D, CAP>, dim3(w.ctas), dim3(kThreads), smem, s, 1, a, w, k, v);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(join_kernel<T, D>, dim3(w.ctas, kPair / 8), dim3(256), 0, s, 1, a, w);
+}
+
+template <typename T>
+cudaError_t launch_d(const AttnArgs& a, const Work& w, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+  if (a.dim == 64)
+    return a.softcap > 0.0f ? launch_t<T, 64, true>(a, w, k, v, s) : launch_t<T, 64, false>(a, w, k, v, s);
+  return a.softcap > 0.0f ? launch_t<T, 128, true>(a, w, k, v, s) : launch_t<T, 128, false>(a, w, k, v, s);
+}
+
+size_t prefix_bytes(int64_t slots) { return align_up(static_cast<size_t>(slots + 1) * 4, 256); }
+
+int64_t slots_of(int64_t tokens, int group, int seqs) { return tokens * group / kPair + seqs; }
+
+}  // namespace
+
+unsigned int read_tile_wait_timeouts(bool reset) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_tile_wait_timeouts, sizeof(v)) != cudaSuccess) return 0xffffffffu;
+  if (reset) {
+    const unsigned int z = 0;
+    cudaMemcpyToSymbol(g_tile_wait_timeouts, &z, sizeof(z));
+  }
+  return v;
+}
+
+bool attn_tile_supported(int dtype, int dim, int page, float scale, bool aligned) {
+  return aligned && (dtype == HC_F16 || dtype == HC_BF16) && (dim == 64 || dim == 128) && scale > 0.0f && page >= 8 &&
+         (kKeys % page == 0 || page % kKeys == 0) && tmap_encoder() != nullptr;
+}
+
+size_t attn_tile_workspace(int64_t tokens, int group, int seqs, int dim, int num_sms) {
+  const size_t rows = 2 * static_cast<size_t>(num_sms) * kPair;
+  return prefix_bytes(slots_of(tokens, group, seqs)) + align_up(rows * 8, 256) + rows * dim * 4;
+}
+
+cudaError_t launch_attn_tile(const AttnArgs& args, int dtype, void* workspace, int num_sms, cudaStream_t s) {
+  AttnArgs a = args;
+  a.g = AttnGeometry{kPair, kKeys, 1 << 30, 1};
+  Work w;
+  w.slots = static_cast<int>(slots_of(a.tokens, a.group, a.b.seqs));
+  w.ctas = std::min(num_sms, 160);
+  char* p = static_cast<char*>(workspace);
+  w.prefix = reinterpret_cast<const int32_t*>(p);
+  p += prefix_bytes(w.slots);
+  w.part_ml = reinterpret_cast<float2*>(p);
+  p += align_up(2 * static_cast<size_t>(num_sms) * kPair * 8, 256);
+  w.part_o = reinterpret_cast<float*>(p);
+  CUtensorMap k, v;
+  const bool bf16 = dtype == HC_BF16;
+  if (!make_pool_map(&k, a.k, bf16, a) || !make_pool_map(&v, a.v, bf16, a)) return cudaErrorInvalidValue;
+  return bf16 ? launch_d<__nv_bfloat16>(a, w, k, v, s) : launch_d<__half>(a, w, k, v, s);
+}
+
+}  // namespace hc

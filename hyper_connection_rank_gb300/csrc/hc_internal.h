@@ -88,6 +88,8 @@ bool prefill_supported(int64_t rows, int C, int H, int R, hc_dtype_t dt);
 size_t prefill_workspace(int64_t rows, int C, int H, int R, hc_dtype_t dt);
 cudaError_t launch_prefill(const Problem& p);
 unsigned int read_pf_wait_timeouts(bool reset);
+// Attention over a paged cache (hc_attn_tile.cu).
+unsigned int read_tile_wait_timeouts(bool reset);
 
 // Tensor (TMA) maps (hc_tmap.cu): the driver's encoder (nullptr if the
 // driver lacks it), and a map over a row-major [outer, inner] matrix of 16-bit

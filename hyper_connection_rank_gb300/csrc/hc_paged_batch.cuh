@@ -12,10 +12,15 @@ struct BatchView {
   const int32_t *page_table, *kv_lens, *cu_q;  // cu_q NULL: one new token per sequence
   int64_t table_stride, num_pages;
   int32_t seqs, max_pages, page_size;
+  int64_t tokens;
 };
 
+// First new token of sequence s, as a row of q (within the call's rows,
+// whatever cu_q says).
 __device__ __forceinline__ int64_t first_row(const BatchView& b, int s) {
-  return b.cu_q ? static_cast<int64_t>(b.cu_q[s]) : s;
+  if (!b.cu_q) return s;
+  const int64_t t = b.cu_q[s];
+  return t < 0 ? 0 : t < b.tokens ? t : b.tokens;
 }
 // Length of sequence s with its new tokens, cut to what its table row can hold.
 __device__ __forceinline__ int64_t kv_len_of(const BatchView& b, int s) {

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int tpb)
     for (int j = warp; j < nt; j += kThreads / 32) {
       const int64_t t = t0 + j;
       const BatchView& b = a.batch;
-      const int s = b.cu_q ? warp_last_le(b.seqs, t, [&](int i) { return static_cast<int64_t>(b.cu_q[i]); })
+      const int s = b.cu_q ? warp_last_le(b.seqs, t, [&](int i) { return first_row(b, i); })
                            : static_cast<int>(t);
       if (lane == 0) {
         const int64_t end = first_row(b, s + 1);
@@ -254,7 +254,7 @@ cudaError_t launch_rotary_append(const hc_rotary_append_t& r, bool vec, int num_
   a.rot = r.rot_dim;
   a.amplitude = r.amplitude;
   a.sign = 1.0f;
-  a.batch = BatchView{r.page_table, r.kv_lens, r.cu_q, r.table_stride, r.num_pages, r.seqs, r.max_pages, r.page_size};
+  a.batch = BatchView{r.page_table, r.kv_lens, r.cu_q, r.table_stride, r.num_pages, r.seqs, r.max_pages, r.page_size, r.tokens};
   return launch_any(a, r.dtype, r.interleaved != 0, vec, num_sms, s);
 }
 
