@@ -14,9 +14,11 @@
 // One CTA per SM holds two tiles, A and B, of 128 rows. Both products run on
 // tcgen05: S = Q K^T from shared memory into tensor memory (128 columns for
 // each tile), and O += P V with P read from tensor memory, where it takes the
-// place of the S it came from. The MMA warp issues PV_A(j), QK_A(j+1),
-// PV_B(j), QK_B(j+1) in turn, so that while the softmax warps of one tile work,
-// the tensor core has the other tile's two products to do. Two warpgroups do
+// place of the S it came from (the MMAs of one thread run in the order of their
+// issue, so QK(j+1) does not overtake PV(j)). While the softmax warps of one tile
+// work, the tensor core has the other tile's two products to do. Each tile has
+// an MMA warp of its own: one thread gets an instruction out every 76 cycles at
+// best, and these take 64. Two warpgroups do
 // the softmax, a thread to a row (no exchange between lanes); one warp copies
 // keys and values by TMA, a box per page and 64 features, into a ring. Of the
 // 168 * 384 registers that the CTA starts with, the softmax threads take 216
@@ -44,8 +46,8 @@ namespace {
 constexpr int kRows = 128;        // rows of a tile, an MMA's M
 constexpr int kPair = 2 * kRows;  // rows of a CTA's two tiles
 constexpr int kKeys = 128;        // keys of a block, N of the first product
-constexpr int kThreads = 384;     // two softmax warpgroups, and one with the copy warp and the MMA warp
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384;     // two softmax warpgroups, and one of the other warps
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 11;  // (an MMA warp for each tile)
 constexpr int kMinBlocks = 4;     // key blocks that are worth a CTA
 constexpr float kLazy = 8.0f;     // rise of a row's maximum (base-2) that O is rescaled for
 
@@ -173,6 +175,11 @@ __device__ __forceinline__ int tile_blocks(const AttnArgs& a, const AttnTile& t,
   return n < 1 ? 1 : static_cast<int>(n);
 }
 
+// Whether a block of keys holds some that no row of the tile sees.
+__device__ __forceinline__ bool at_edge(const AttnTile& t, int64_t key0) {
+  return key0 < t.lo || key0 + kKeys > t.hi;
+}
+
 // ------------------------------------------------------------ tensor memory --
 
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
@@ -267,15 +274,24 @@ struct Bars {
   uint64_t p_full[2];   // its weights do, and O may be added to
   uint64_t o_done[2];   // the product with the values is done
   uint64_t kv_full[8], kv_empty[8];
+  uint64_t edge[8];     // values at a tile's edge have landed and are yet to be cleaned
   uint32_t tmem;
 };
 
 // A wait that gave up ends its role's loop; the other roles' next waits give
 // up in turn, and the rows of the tile at hand become NaN.
-#define HC_WAIT(bar, parity)                                               \
-  do {                                                                     \
-    if (!mbar_wait((bar), (parity), &g_tile_wait_timeouts)) return false;  \
+#define HC_WAIT(bar, parity)                                                                         \
+  do {                                                                                               \
+    if (!__all_sync(0xffffffffu, mbar_wait((bar), (parity), &g_tile_wait_timeouts))) return false;   \
   } while (0)
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 template <typename T, int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -287,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Segment s_seg[8];  // each softmax warp's segment at hand (held here, not in registers)
   unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   unsigned char* const ring = smem + 2 * C::kQ;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (through a shuffle the compiler knows that a warp's threads agree on it, and keeps what follows from it in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -298,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&bars.kv_full[i], 1);
-      mbar_init(&bars.kv_empty[i], 1);
+      mbar_init(&bars.kv_empty[i], 2);  // both tiles' products
+      mbar_init(&bars.edge[i], 1);
     }
     fence_mbar_init();
   }
@@ -352,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int kind = 0; kind < 2; ++kind) {
               HC_WAIT(&bars.kv_empty[slot], (round & 1) ^ 1);
-              if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[slot], C::kSlot);
+              uint64_t* const full = kind == 1 && at_edge(g.t, key0) ? &bars.edge[slot] : &bars.kv_full[slot];
+            if (lane == 0) mbar_arrive_expect_tx(full, C::kSlot);
               __syncwarp();
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
@@ -361,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const int h = e % C::kHalves, b = e / C::kHalves;
                   tma_load_4d(smem_addr(ring + slot * C::kSlot + h * C::kHalf) + b * box * 128, kind ? &v_map : &k_map,
                               h * 64, off[i], g.kv_head, at[i] < 0 ? static_cast<int>(a.b.num_pages) : at[i],
-                              &bars.kv_full[slot]);
+                              full);
                 }
               }
               if (++slot == C::kSlots) {
@@ -383,96 +402,117 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) mbar_wait(&bars.kv_empty[i], used & 1, &g_tile_wait_timeouts);
         }
       }
-    } else if (warp == kMmaWarp) {
-      // ---- products ----
+    } else if (warp < kFixWarp) {
+      // ---- products of tile x ----
       constexpr uint32_t kQk = idesc_f16(std::is_same<T, __nv_bfloat16>::value, kRows, kKeys, false, false);
       constexpr uint32_t kPv = idesc_f16(std::is_same<T, __nv_bfloat16>::value, kRows, D, false, true);
+      const int x = warp - kMmaWarp;
+      const uint32_t s_tmem = tmem + x * kKeys, o_tmem = tmem + kO + x * D;
+      const uint64_t q_desc = smem_desc_sw128(smem_addr(smem + x * C::kQ), 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(smem_addr(ring), 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(smem_addr(ring), C::kHalf, 1024);
       int slot = 0;
-      uint32_t round = 0, q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
+      uint32_t round = 0, q_seen = 0, p_seen = 0;
       const auto advance = [&] {
         if (++slot == C::kSlots) {
           slot = 0;
           ++round;
         }
       };
-      const auto issue_qk = [&](int x, int k_slot) {
-        if (lane == 0) {
-          const uint32_t q = smem_addr(smem + x * C::kQ), k = smem_addr(ring + k_slot * C::kSlot);
+      // (descriptors count addresses in 16 bytes)
+      const auto issue_qk = [&](int k_slot) {
+        const uint64_t k = k_desc + static_cast<uint32_t>(k_slot * (C::kSlot / 16));
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t o = (ks / 4) * C::kHalf + (ks % 4) * 32;
-            mma_f16(tmem + x * kKeys, smem_desc_sw128(q + o, 16, 1024), smem_desc_sw128(k + o, 16, 1024), kQk, ks > 0);
-          }
-          mma_commit(&bars.s_full[x]);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t o = ((ks / 4) * C::kHalf + (ks % 4) * 32) / 16;
+          mma_f16(s_tmem, q_desc + o, k + o, kQk, ks > 0);
         }
-        __syncwarp();
+        mma_commit(&bars.s_full[x]);
+      };
+      const auto issue_pv = [&](int v_slot, bool add) {
+        const uint64_t v = v_desc + static_cast<uint32_t>(v_slot * (C::kSlot / 16));
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          mma_f16_ts(o_tmem, s_tmem + ks * 8, v + ks * (2048 / 16), kPv, add || ks > 0);
+        mma_commit(&bars.o_done[x]);
       };
       const auto multiply_all = [&]() -> bool {
         for (int64_t u = u0; u < u1;) {
           Segment g;
           segment_at(a, w, run, u, u1, &g);
-          const int ends[2] = {min(tile_blocks(a, g.t, 0), g.j1), min(tile_blocks(a, g.t, 1), g.j1)};
-          // first scores of both tiles
+          const int end = min(tile_blocks(a, g.t, x), g.j1);
+          const int j0 = g.j0, j1 = g.j1;
+          u = g.at + j1;
           HC_WAIT(&bars.kv_full[slot], round & 1);
-          for (int x = 0; x < 2; ++x)
-            if (g.j0 < ends[x]) {
-              HC_WAIT(&bars.q_full[x], q_seen[x] & 1);
-              ++q_seen[x];
-              tc_fence_after();
-              issue_qk(x, slot);
-            }
-          if (lane == 0) mma_commit(&bars.kv_empty[slot]);
+          if (j0 < end) {
+            HC_WAIT(&bars.q_full[x], q_seen & 1);
+            ++q_seen;
+            tc_fence_after();
+            if (elect_one()) issue_qk(slot);
+          }
+          if (elect_one()) mma_commit(&bars.kv_empty[slot]);
+          __syncwarp();
           advance();
-          for (int j = g.j0; j < g.j1; ++j) {
+          for (int j = j0; j < j1; ++j) {
             const int v_slot = slot;
             HC_WAIT(&bars.kv_full[slot], round & 1);
             advance();
             const int k_slot = slot;
-            const bool more = j + 1 < g.j1;
+            const bool more = j + 1 < j1;
             if (more) HC_WAIT(&bars.kv_full[slot], round & 1);
-            // values beside the keys that the tile sees may be anything; a weight of zero must meet a zero
-            const int64_t key0 = g.t.base + static_cast<int64_t>(j) * kKeys;
-            if (key0 < g.t.lo || key0 + kKeys > g.t.hi) {
-              const int lo = static_cast<int>(g.t.lo > key0 ? min(g.t.lo - key0, static_cast<int64_t>(kKeys)) : 0);
-              const int hi = static_cast<int>(g.t.hi > key0 ? min(g.t.hi - key0, static_cast<int64_t>(kKeys)) : 0);
-              const int n = (lo + kKeys - hi) * 8 * C::kHalves;
-              for (int e = lane; e < n; e += 32) {
-                const int c = e & 7, h = (e >> 3) % C::kHalves, i = (e >> 3) / C::kHalves;
-                const int r = i < lo ? i : hi + (i - lo);
-                *reinterpret_cast<uint4*>(ring + v_slot * C::kSlot + h * C::kHalf + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+            if (j < end) {
+              HC_WAIT(&bars.p_full[x], p_seen & 1);
+              ++p_seen;
+              tc_fence_after();
+              if (elect_one()) {
+                issue_pv(v_slot, j > j0);
+                if (j + 1 < end) issue_qk(k_slot);
               }
-              fence_async_smem();
-              __syncwarp();
             }
-            for (int x = 0; x < 2; ++x) {
-              if (j < ends[x]) {
-                HC_WAIT(&bars.p_full[x], p_seen[x] & 1);
-                ++p_seen[x];
-                tc_fence_after();
-                if (lane == 0) {
-                  const uint32_t v = smem_addr(ring + v_slot * C::kSlot);
-#pragma unroll
-                  for (int ks = 0; ks < kKeys / 16; ++ks)
-                    mma_f16_ts(tmem + kO + x * D, tmem + x * kKeys + ks * 8, smem_desc_sw128(v + ks * 2048, C::kHalf, 1024),
-                               kPv, j > g.j0 || ks > 0);
-                  mma_commit(&bars.o_done[x]);
-                }
-                __syncwarp();
-              }
-              if (more && j + 1 < ends[x]) issue_qk(x, k_slot);
-            }
-            if (lane == 0) {
+            if (elect_one()) {
               mma_commit(&bars.kv_empty[v_slot]);
               if (more) mma_commit(&bars.kv_empty[k_slot]);
             }
             __syncwarp();
             if (more) advance();
           }
-          u = g.at + g.j1;
         }
         return true;
       };
       multiply_all();
+    } else {
+      // ---- values beside the keys that a tile sees may be anything; a weight of zero must meet a zero ----
+      int slot = 0;
+      uint32_t edges = 0;  // parity of each slot's edge barrier
+      const auto fix_all = [&]() -> bool {
+        for (int64_t u = u0; u < u1;) {
+          Segment g;
+          segment_at(a, w, run, u, u1, &g);
+          for (int j = g.j0; j < g.j1; ++j) {
+            const int v_slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+            slot = v_slot + 1 == C::kSlots ? 0 : v_slot + 1;
+            const int64_t key0 = g.t.base + static_cast<int64_t>(j) * kKeys;
+            if (!at_edge(g.t, key0)) continue;
+            HC_WAIT(&bars.edge[v_slot], edges >> v_slot & 1);
+            edges ^= 1u << v_slot;
+            const int lo = static_cast<int>(g.t.lo > key0 ? min(g.t.lo - key0, static_cast<int64_t>(kKeys)) : 0);
+            const int hi = static_cast<int>(g.t.hi > key0 ? min(g.t.hi - key0, static_cast<int64_t>(kKeys)) : 0);
+            const int n = (lo + kKeys - hi) * 8 * C::kHalves;
+            for (int e = lane; e < n; e += 32) {
+              const int c = e & 7, h = (e >> 3) % C::kHalves, i = (e >> 3) / C::kHalves;
+              const int r = i < lo ? i : hi + (i - lo);
+              *reinterpret_cast<uint4*>(ring + v_slot * C::kSlot + h * C::kHalf + r * 128 + c * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.kv_full[v_slot]);
+          }
+          u = g.at + g.j1;
+        }
+        return true;
+      };
+      fix_all();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
