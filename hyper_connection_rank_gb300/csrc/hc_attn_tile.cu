@@ -15,10 +15,10 @@
 // tcgen05: S = Q K^T from shared memory into tensor memory (128 columns for
 // each tile), and O += P V with P read from tensor memory, where it takes the
 // place of the S it came from (the MMAs of one thread run in the order of their
-// issue, so QK(j+1) does not overtake PV(j)). While the softmax warps of one tile
-// work, the tensor core has the other tile's two products to do. Each tile has
-// an MMA warp of its own: one thread gets an instruction out every 76 cycles at
-// best, and these take 64. Two warpgroups do
+// issue, so QK(j+1) does not overtake PV(j)). The MMA warp issues PV_A(j), QK_A(j+1),
+// PV_B(j), QK_B(j+1) in turn, so that while the softmax warps of one tile work,
+// the tensor core has the other tile's two products to do (with a warp for each
+// tile the two fell into step, and products and softmax took turns). Two warpgroups do
 // the softmax, a thread to a row (no exchange between lanes); one warp copies
 // keys and values by TMA, a box per page and 64 features, into a ring. Of the
 // 168 * 384 registers that the CTA starts with, the softmax threads take 216
@@ -47,7 +47,7 @@ constexpr int kRows = 128;        // rows of a tile, an MMA's M
 constexpr int kPair = 2 * kRows;  // rows of a CTA's two tiles
 constexpr int kKeys = 128;        // keys of a block, N of the first product
 constexpr int kThreads = 384;     // two softmax warpgroups, and one of the other warps
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 11;  // (an MMA warp for each tile)
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10;
 constexpr int kMinBlocks = 4;     // key blocks that are worth a CTA
 constexpr float kLazy = 8.0f;     // rise of a row's maximum (base-2) that O is rescaled for
 
@@ -234,6 +234,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
+  return d;
+}
 // x * y + z on two floats at once.
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
   float2 d;
@@ -310,12 +315,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars.q_full[x], kRows);
       mbar_init(&bars.s_full[x], 1);
-      mbar_init(&bars.p_full[x], kRows);
+      mbar_init(&bars.p_full[x], 4);  // a warp each
       mbar_init(&bars.o_done[x], 1);
     }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&bars.kv_full[i], 1);
-      mbar_init(&bars.kv_empty[i], 2);  // both tiles' products
+      mbar_init(&bars.kv_empty[i], 1);
       mbar_init(&bars.edge[i], 1);
     }
     fence_mbar_init();
@@ -332,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // (after the wait: join_kernel may read the plan before its own)
   const Run run(w, a.kv_heads);
   const bool mine = static_cast<int>(blockIdx.x) < run.ctas;
   const int64_t u0 = mine ? run.start(blockIdx.x) : 0, u1 = mine ? run.start(blockIdx.x + 1) : 0;
@@ -402,17 +407,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) mbar_wait(&bars.kv_empty[i], used & 1, &g_tile_wait_timeouts);
         }
       }
-    } else if (warp < kFixWarp) {
-      // ---- products of tile x ----
+    } else if (warp == kMmaWarp) {
+      // ---- products ----
       constexpr uint32_t kQk = idesc_f16(std::is_same<T, __nv_bfloat16>::value, kRows, kKeys, false, false);
       constexpr uint32_t kPv = idesc_f16(std::is_same<T, __nv_bfloat16>::value, kRows, D, false, true);
-      const int x = warp - kMmaWarp;
-      const uint32_t s_tmem = tmem + x * kKeys, o_tmem = tmem + kO + x * D;
-      const uint64_t q_desc = smem_desc_sw128(smem_addr(smem + x * C::kQ), 16, 1024);
+      const uint64_t q_desc = smem_desc_sw128(smem_addr(smem), 16, 1024);
       const uint64_t k_desc = smem_desc_sw128(smem_addr(ring), 16, 1024);
       const uint64_t v_desc = smem_desc_sw128(smem_addr(ring), C::kHalf, 1024);
       int slot = 0;
-      uint32_t round = 0, q_seen = 0, p_seen = 0;
+      uint32_t round = 0, q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
       const auto advance = [&] {
         if (++slot == C::kSlots) {
           slot = 0;
@@ -420,67 +423,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       // (descriptors count addresses in 16 bytes)
-      const auto issue_qk = [&](int k_slot) {
+      const auto issue_qk = [&](int x, int k_slot) {
+        const uint64_t q = q_desc + static_cast<uint32_t>(x * (C::kQ / 16));
         const uint64_t k = k_desc + static_cast<uint32_t>(k_slot * (C::kSlot / 16));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t o = ((ks / 4) * C::kHalf + (ks % 4) * 32) / 16;
-          mma_f16(s_tmem, q_desc + o, k + o, kQk, ks > 0);
+          mma_f16(tmem + x * kKeys, q + o, k + o, kQk, ks > 0);
         }
         mma_commit(&bars.s_full[x]);
       };
-      const auto issue_pv = [&](int v_slot, bool add) {
+      const auto issue_pv = [&](int x, int v_slot, bool add) {
         const uint64_t v = v_desc + static_cast<uint32_t>(v_slot * (C::kSlot / 16));
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_f16_ts(o_tmem, s_tmem + ks * 8, v + ks * (2048 / 16), kPv, add || ks > 0);
+          mma_f16_ts(tmem + kO + x * D, tmem + x * kKeys + ks * 8, v + ks * (2048 / 16), kPv, add || ks > 0);
         mma_commit(&bars.o_done[x]);
       };
       const auto multiply_all = [&]() -> bool {
         for (int64_t u = u0; u < u1;) {
           Segment g;
           segment_at(a, w, run, u, u1, &g);
-          const int end = min(tile_blocks(a, g.t, x), g.j1);
           const int j0 = g.j0, j1 = g.j1;
+          const int ends[2] = {min(tile_blocks(a, g.t, 0), j1), min(tile_blocks(a, g.t, 1), j1)};
           u = g.at + j1;
           HC_WAIT(&bars.kv_full[slot], round & 1);
-          if (j0 < end) {
-            HC_WAIT(&bars.q_full[x], q_seen & 1);
-            ++q_seen;
-            tc_fence_after();
-            if (elect_one()) issue_qk(slot);
-          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (j0 < ends[x]) {
+              HC_WAIT(&bars.q_full[x], q_seen[x] & 1);
+              ++q_seen[x];
+              tc_fence_after();
+              if (elect_one()) issue_qk(x, slot);
+              __syncwarp();
+            }
           if (elect_one()) mma_commit(&bars.kv_empty[slot]);
           __syncwarp();
           advance();
+          HC_WAIT(&bars.kv_full[slot], round & 1);
           for (int j = j0; j < j1; ++j) {
+            // block j's values are there, block j+1's keys and values are waited for while products are queued
             const int v_slot = slot;
-            HC_WAIT(&bars.kv_full[slot], round & 1);
             advance();
             const int k_slot = slot;
+            const uint32_t k_round = round;
             const bool more = j + 1 < j1;
-            if (more) HC_WAIT(&bars.kv_full[slot], round & 1);
-            if (j < end) {
-              HC_WAIT(&bars.p_full[x], p_seen & 1);
-              ++p_seen;
-              tc_fence_after();
-              if (elect_one()) {
-                issue_pv(v_slot, j > j0);
-                if (j + 1 < end) issue_qk(k_slot);
+            if (more) advance();
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (j < ends[x]) {
+                HC_WAIT(&bars.p_full[x], p_seen[x] & 1);
+                ++p_seen[x];
+                tc_fence_after();
+                if (elect_one()) issue_pv(x, v_slot, j > j0);
+              }
+              if (x == 1 && elect_one()) mma_commit(&bars.kv_empty[v_slot]);
+              __syncwarp();
+              if (more) {
+                if (x == 0) HC_WAIT(&bars.kv_full[k_slot], k_round & 1);
+                if (j + 1 < ends[x] && elect_one()) issue_qk(x, k_slot);
+                if (x == 1 && elect_one()) mma_commit(&bars.kv_empty[k_slot]);
+                __syncwarp();
+                if (x == 1) HC_WAIT(&bars.kv_full[slot], round & 1);
               }
             }
-            if (elect_one()) {
-              mma_commit(&bars.kv_empty[v_slot]);
-              if (more) mma_commit(&bars.kv_empty[k_slot]);
-            }
-            __syncwarp();
-            if (more) advance();
           }
         }
         return true;
       };
       multiply_all();
-    } else {
+    } else if (warp == kFixWarp) {
       // ---- values beside the keys that a tile sees may be anything; a weight of zero must meet a zero ----
       int slot = 0;
       uint32_t edges = 0;  // parity of each slot's edge barrier
@@ -594,14 +606,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kKeys; ++c)
               if (c < lo || c >= hi) f[c] = neg_inf();
           }
-          float top0 = fmaxf(f[0], f[1]), top1 = fmaxf(f[2], f[3]);
+          float tops[4];
 #pragma unroll
-          for (int c = 4; c < kKeys; c += 4) {
-            top0 = fmaxf(top0, fmaxf(f[c], f[c + 1]));
-            top1 = fmaxf(top1, fmaxf(f[c + 2], f[c + 3]));
-          }
+          for (int i = 0; i < 4; ++i) tops[i] = fmaxf(f[2 * i], f[2 * i + 1]);
+#pragma unroll
+          for (int c = 8; c < kKeys; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tops[i] = max3(tops[i], f[c + 2 * i], f[c + 2 * i + 1]);
           const float mul = CAP ? 1.0f : map.mul;
-          const float top = fmaxf(top0, top1) * mul;
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mul;
           if (j == g.j0) {
             m = top;
           } else if (__any_sync(0xffffffffu, top > m + kLazy || (m == neg_inf() && top > m))) {
@@ -632,8 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t p[32];
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
-              float2 y0 = fma2(make_float2(f[h + c], f[h + c + 1]), mul2, ref2);
-              float2 y1 = fma2(make_float2(f[h + c + 2], f[h + c + 3]), mul2, ref2);
+              const float* y = f + h + c;
+              float2 y0 = fma2(make_float2(y[0], y[1]), mul2, ref2);
+              float2 y1 = fma2(make_float2(y[2], y[3]), mul2, ref2);
               y0 = make_float2(ex2(y0.x), ex2(y0.y));
               y1 = make_float2(ex2(y1.x), ex2(y1.y));
               sum0 = add2(sum0, y0);
@@ -643,11 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st32(s_at + h / 2, p);
           }
-          sum0 = add2(sum0, sum1);
-          l += sum0.x + sum0.y;
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&bars.p_full[x]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.p_full[x]);
+          sum0 = add2(sum0, sum1);
+          l += sum0.x + sum0.y;
           ++o_seen;
         }
         // the tile's scores are all formed, so its queries make room for the next segment's
@@ -733,59 +748,89 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of the tile that cut c + 1 goes through, if that is the
-// first cut in it; a warp to a row.
+// first cut in it: kJoinRows rows to a CTA. First every row's weights, 2^(m_i -
+// M) / sum, eight threads to a row; then the sums, a thread to four features.
+// Bound by the latency of its chain of loads (schedule, then maxima and sums, then
+// partial results), so a CTA has many rows in flight at once; the schedule is
+// read while the tile kernel still runs.
+constexpr int kJoinRows = 32;
+constexpr int kMaxCtas = 160;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kernel(AttnArgs a, Work w) {
-  __shared__ float s_w[8][160];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
+  __shared__ float s_w[kJoinRows][kMaxCtas + 1];
   const Run run(w, a.kv_heads);
   const int c0 = blockIdx.x;
   if (c0 + 1 >= run.ctas) return;
   const int64_t u = run.start(c0 + 1);
-  if (u >= run.all) return;
   Segment g;
   segment_at(a, w, run, u, run.all, &g);
   if (g.at == u || run.start(c0) > g.at) return;
+  const int row0 = blockIdx.y * kJoinRows;
+  const int rows = min(g.t.rows - row0, kJoinRows);
+  if (rows <= 0) return;
   const int64_t end = g.at + g.n;
   int pieces = 1;
   while (c0 + pieces < run.ctas && run.start(c0 + pieces) < end) ++pieces;
-  const int r = blockIdx.y * 8 + warp;
-  if (r >= g.t.rows) return;
   // piece 0 is the last of its CTA's segments, the others are the first of theirs
-  const auto index = [&](int i) { return (2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0)) * kPair + r; };
-  float top = neg_inf();
-  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, w.part_ml[index(i)].x);
+  const auto index = [&](int i, int r) { return (2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0)) * kPair + row0 + r; };
+  pdl_wait();
+  {
+    const int r = threadIdx.x >> 3, e = threadIdx.x & 7;
+    float top = neg_inf(), sum = 0.0f;
+    if (r < rows)
+      for (int i = e; i < pieces; i += 8) top = fmaxf(top, w.part_ml[index(i, r)].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float sum = 0.0f;
-  for (int i = lane; i < pieces; i += 32) {
-    const float2 ml = w.part_ml[index(i)];
-    const float f = ml.x == neg_inf() ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - top);
-    s_w[warp][i] = f;
-    sum += ml.y * f;
-  }
-  sum = warp_sum(sum);
-  __syncwarp();
-  constexpr int V = D / 32;
-  float o[V] = {};
-#pragma unroll 4
-  for (int i = 0; i < pieces; ++i) {
-    const float f = s_w[warp][i];
-    if (f != 0.0f) {
-      const float* src = w.part_o + index(i) * D + lane * V;
+    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (r < rows)
+      for (int i = e; i < pieces; i += 8) {
+        const float2 ml = w.part_ml[index(i, r)];
+        // (scores that are all NaN: m = -inf, l = NaN)
+        const float f = ml.x == neg_inf() ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - top);
+        s_w[r][i] = f;
+        sum += ml.y * f;
+      }
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = fmaf(src[e], f, o[e]);
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (r < rows) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      for (int i = e; i < pieces; i += 8) s_w[r][i] *= inv;
+      if (e == 0 && a.lse) {
+        int64_t token;
+        int head;
+        row_owner(a, g.t, g.kv_head, row0 + r, &token, &head);
+        a.lse[token * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+      }
     }
   }
-  int64_t token;
-  int head;
-  row_owner(a, g.t, g.kv_head, r, &token, &head);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + lane * V;
+  __syncthreads();
+  constexpr int kPer = D / 4;          // threads of a row
+  constexpr int kAtOnce = 256 / kPer;  // rows at once
+  const int d = threadIdx.x % kPer * 4;
 #pragma unroll
-  for (int e = 0; e < V; ++e) stf(dst + e, o[e] * inv);
-  if (lane == 0 && a.lse) a.lse[token * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+  for (int r0 = 0; r0 < kJoinRows; r0 += kAtOnce) {
+    const int r = r0 + threadIdx.x / kPer;
+    if (r >= rows) continue;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+      const float f = s_w[r][i];
+      if (f == 0.0f) continue;  // (a piece without a key of this row has no sums)
+      const float4 y = *reinterpret_cast<const float4*>(w.part_o + index(i, r) * D + d);
+      o.x = fmaf(y.x, f, o.x);
+      o.y = fmaf(y.y, f, o.y);
+      o.z = fmaf(y.z, f, o.z);
+      o.w = fmaf(y.w, f, o.w);
+    }
+    int64_t token;
+    int head;
+    row_owner(a, g.t, g.kv_head, row0 + r, &token, &head);
+    T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + d;
+    stf(dst, o.x);
+    stf(dst + 1, o.y);
+    stf(dst + 2, o.z);
+    stf(dst + 3, o.w);
+  }
 }
 
 // ------------------------------------------------------------------- host --
@@ -819,7 +864,7 @@ cudaError_t launch_t(const AttnArgs& a, const Work& w, const CUtensorMap& k, con
   if (e != cudaSuccess) return e;
   e = launch_pdl(tile_kernel<T, D, CAP>, dim3(w.ctas), dim3(kThreads), smem, s, 1, a, w, k, v);
   if (e != cudaSuccess) return e;
-  return launch_pdl(join_kernel<T, D>, dim3(w.ctas, kPair / 8), dim3(256), 0, s, 1, a, w);
+  return launch_pdl(join_kernel<T, D>, dim3(w.ctas, kPair / kJoinRows), dim3(256), 0, s, 1, a, w);
 }
 
 template <typename T>
@@ -860,7 +905,7 @@ cudaError_t launch_attn_tile(const AttnArgs& args, int dtype, void* workspace, i
   a.g = AttnGeometry{kPair, kKeys, 1 << 30, 1};
   Work w;
   w.slots = static_cast<int>(slots_of(a.tokens, a.group, a.b.seqs));
-  w.ctas = std::min(num_sms, 160);
+  w.ctas = std::min(num_sms, kMaxCtas);
   char* p = static_cast<char*>(workspace);
   w.prefix = reinterpret_cast<const int32_t*>(p);
   p += prefix_bytes(w.slots);
