@@ -47,7 +47,9 @@ constexpr int kRows = 128;        // rows of a tile, an MMA's M
 constexpr int kPair = 2 * kRows;  // rows of a CTA's two tiles
 constexpr int kKeys = 128;        // keys of a block, N of the first product
 constexpr int kThreads = 384;     // two softmax warpgroups, and one of the other warps
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10, kPlanWarp = 11;
+constexpr int kSegs = 4;          // segments at hand
+constexpr int kSegUsers = 11;     // warps that read them
 constexpr int kMinBlocks = 4;     // key blocks that are worth a CTA
 constexpr float kLazy = 8.0f;     // rise of a row's maximum (base-2) that O is rescaled for
 
@@ -239,6 +241,11 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
   return d;
 }
+__device__ __forceinline__ float min3(float x, float y, float z) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
+  return d;
+}
 // x * y + z on two floats at once.
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
   float2 d;
@@ -258,6 +265,52 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
       : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return d;
 }
+// A row's scores through the cap, c log2(e) tanh(y) with y = scale / c * score.
+// Where all of a warp's |y| are below 3/4 (scores well inside the cap, the usual
+// case), tanh(y) = y P(y^2) with P of degree 5, fitted to tanh(sqrt(u)) /
+// sqrt(u) for the least error over that range (1.4e-8 with these coefficients
+// in float32), seven operations on pairs of floats that leave the
+// exponential unit to the softmax; else by exponential and quotient.
+__device__ __forceinline__ void cap_scores(float* f, const ScoreMap& map, float to_y) {
+  float hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = fmaxf(f[2 * i], f[2 * i + 1]);
+    lo[i] = fminf(f[2 * i], f[2 * i + 1]);
+  }
+#pragma unroll
+  for (int c = 8; c < kKeys; c += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hi[i] = max3(hi[i], f[c + 2 * i], f[c + 2 * i + 1]);
+      lo[i] = min3(lo[i], f[c + 2 * i], f[c + 2 * i + 1]);
+    }
+  const float far = fmaxf(fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])), -fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3])));
+  if (__any_sync(0xffffffffu, far * to_y > 0.75f)) {
+#pragma unroll
+    for (int c = 0; c < kKeys; ++c) f[c] = map_score(map, f[c]);
+    return;
+  }
+  const auto twice = [](float v) { return make_float2(v, v); };
+  const float2 k = twice(to_y), zero = twice(0.0f);
+  const float2 p0 = twice(map.cap * 0.999999832f), p1 = twice(map.cap * -0.333324709f), p2 = twice(map.cap * 0.133205797f),
+               p3 = twice(map.cap * -0.0531492611f), p4 = twice(map.cap * 0.0192372364f),
+               p5 = twice(map.cap * -0.00449345569f);
+#pragma unroll
+  for (int c = 0; c < kKeys; c += 2) {
+    const float2 y = fma2(make_float2(f[c], f[c + 1]), k, zero);
+    const float2 u = fma2(y, y, zero);
+    float2 p = fma2(p5, u, p4);
+    p = fma2(p, u, p3);
+    p = fma2(p, u, p2);
+    p = fma2(p, u, p1);
+    p = fma2(p, u, p0);
+    p = fma2(p, y, zero);
+    f[c] = p.x;
+    f[c + 1] = p.y;
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float x, float y);
 template <>
@@ -279,6 +332,7 @@ struct Bars {
   uint64_t p_full[2];   // its weights do, and O may be added to
   uint64_t o_done[2];   // the product with the values is done
   uint64_t kv_full[8], kv_empty[8];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t edge[8];     // values at a tile's edge have landed and are yet to be cleaned
   uint32_t tmem;
 };
@@ -305,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   extern __shared__ unsigned char raw[];
   __shared__ Bars bars;
-  __shared__ Segment s_seg[8];  // each softmax warp's segment at hand (held here, not in registers)
+  __shared__ Segment segs[kSegs];
   unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   unsigned char* const ring = smem + 2 * C::kQ;
   // (through a shuffle the compiler knows that a warp's threads agree on it, and keeps what follows from it in uniform registers)
@@ -317,6 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.s_full[x], 1);
       mbar_init(&bars.p_full[x], 4);  // a warp each
       mbar_init(&bars.o_done[x], 1);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&bars.seg_full[i], 1);
+      mbar_init(&bars.seg_empty[i], kSegUsers);
     }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&bars.kv_full[i], 1);
@@ -345,6 +403,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tensor memory: S (and P) of A and B, then O of A and B
   constexpr uint32_t kO = 2 * kKeys;
 
+  // Segment i of this CTA's run, worked out by the plan warp ahead of the others
+  // (a chain of loads through the schedule and the batch that nobody else waits for).
+  const auto done_with = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.seg_empty[i % kSegs]);
+  };
+#define HC_SEGMENT(i) HC_WAIT(&bars.seg_full[(i) % kSegs], ((i) / kSegs) & 1)
+
   if (warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kLoadWarp) {
@@ -355,9 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot = 0;
       uint32_t round = 0;
       const auto copy_all = [&]() -> bool {
-        for (int64_t u = u0; u < u1;) {
-          Segment g;
-          segment_at(a, w, run, u, u1, &g);
+        int seg = 0;
+        for (int64_t u = u0; u < u1; ++seg) {
+          HC_SEGMENT(seg);
+          const Segment& g = segs[seg % kSegs];
           for (int j = g.j0; j < g.j1; ++j) {
             const int64_t key0 = g.t.base + static_cast<int64_t>(j) * kKeys;
             // pages of this lane's copies; a box without a key that any row sees lies outside the pool, and reads zeros
@@ -376,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kind = 0; kind < 2; ++kind) {
               HC_WAIT(&bars.kv_empty[slot], (round & 1) ^ 1);
               uint64_t* const full = kind == 1 && at_edge(g.t, key0) ? &bars.edge[slot] : &bars.kv_full[slot];
-            if (lane == 0) mbar_arrive_expect_tx(full, C::kSlot);
+              if (lane == 0) mbar_arrive_expect_tx(full, C::kSlot);
               __syncwarp();
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
@@ -395,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           u = g.at + g.j1;
+          done_with(seg);
         }
         return true;
       };
@@ -441,12 +509,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&bars.o_done[x]);
       };
       const auto multiply_all = [&]() -> bool {
-        for (int64_t u = u0; u < u1;) {
-          Segment g;
-          segment_at(a, w, run, u, u1, &g);
+        int seg = 0;
+        for (int64_t u = u0; u < u1; ++seg) {
+          HC_SEGMENT(seg);
+          const Segment& g = segs[seg % kSegs];
           const int j0 = g.j0, j1 = g.j1;
           const int ends[2] = {min(tile_blocks(a, g.t, 0), j1), min(tile_blocks(a, g.t, 1), j1)};
           u = g.at + j1;
+          done_with(seg);
           HC_WAIT(&bars.kv_full[slot], round & 1);
 #pragma unroll
           for (int x = 0; x < 2; ++x)
@@ -497,9 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot = 0;
       uint32_t edges = 0;  // parity of each slot's edge barrier
       const auto fix_all = [&]() -> bool {
-        for (int64_t u = u0; u < u1;) {
-          Segment g;
-          segment_at(a, w, run, u, u1, &g);
+        int seg = 0;
+        for (int64_t u = u0; u < u1; ++seg) {
+          HC_SEGMENT(seg);
+          const Segment& g = segs[seg % kSegs];
           for (int j = g.j0; j < g.j1; ++j) {
             const int v_slot = slot + 1 == C::kSlots ? 0 : slot + 1;
             slot = v_slot + 1 == C::kSlots ? 0 : v_slot + 1;
@@ -521,10 +592,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bars.kv_full[v_slot]);
           }
           u = g.at + g.j1;
+          done_with(seg);
         }
         return true;
       };
       fix_all();
+    } else {
+      // ---- the run's segments, one after another ----
+      const auto plan_all = [&]() -> bool {
+        int seg = 0;
+        for (int64_t u = u0; u < u1; ++seg) {
+          Segment g;
+          segment_at(a, w, run, u, u1, &g);
+          HC_WAIT(&bars.seg_empty[seg % kSegs], ((seg / kSegs) & 1) ^ 1);
+          if (lane == 0) {
+            segs[seg % kSegs] = g;
+            mbar_arrive(&bars.seg_full[seg % kSegs]);
+          }
+          __syncwarp();
+          u = g.at + g.j1;
+        }
+        return true;
+      };
+      plan_all();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -534,12 +624,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = lanes + x * kKeys, o_at = lanes + kO + x * D;
     const ScoreMap map = score_map(a.scale, a.softcap);
     uint32_t s_seen = 0, o_seen = 0;
-    Segment& g = s_seg[warp];
-    const auto keep = [&](const Segment& sg) {
-      __syncwarp();
-      if (lane == 0) g = sg;
-      __syncwarp();
-    };
     const auto load_q = [&](const Segment& sg) {
       if (sg.j0 >= min(tile_blocks(a, sg.t, x), sg.j1)) return;
       const uint4* src = nullptr;
@@ -558,14 +642,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&bars.q_full[x]);
     };
     float m = neg_inf(), l = 0.0f;
+    int seg = 0;
     const auto softmax_all = [&]() -> bool {
       if (u0 < u1) {
-        Segment first;
-        segment_at(a, w, run, u0, u1, &first);
-        load_q(first);
-        keep(first);
+        HC_SEGMENT(0);
+        load_q(segs[0]);
       }
-      for (int64_t u = u0; u < u1;) {
+      for (int64_t u = u0; u < u1; ++seg) {
+        const Segment& g = segs[seg % kSegs];
         const int end = min(tile_blocks(a, g.t, x), g.j1);
         const int rows = tile_rows(g.t, x);
         const int64_t u_next = g.at + g.j1;
@@ -595,10 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kKeys; c += 32) landed32(s + c);
           float* f = reinterpret_cast<float*>(s);
-          if (CAP) {
-#pragma unroll
-            for (int c = 0; c < kKeys; ++c) f[c] = map_score(map, f[c]);
-          }
+          if (CAP) cap_scores(f, map, a.scale / a.softcap);
           const int j0 = j * kKeys;
           if (j0 < all_from || j0 + kKeys > all_to) {
             const int lo = from - j0, hi = to - j0;
@@ -666,10 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++o_seen;
         }
         // the tile's scores are all formed, so its queries make room for the next segment's
-        Segment next;
         if (u_next < u1) {
-          segment_at(a, w, run, u_next, u1, &next);
-          load_q(next);
+          HC_SEGMENT(seg + 1);
+          load_q(segs[(seg + 1) % kSegs]);
         }
         if (rows > 0) {
           const bool partial = g.j0 > 0 || g.j1 < g.n;
@@ -726,19 +806,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_before();  // O has been read before the next segment's weights let it be written
         }
-        if (u_next < u1) keep(next);
         u = u_next;
+        done_with(seg);
       }
       return true;
     };
-    if (!softmax_all() && u0 < u1 && row < tile_rows(g.t, x)) {
-      int64_t token;
-      int head;
-      row_owner(a, g.t, g.kv_head, x * kRows + row, &token, &head);
-      for (int d = 0; d < D; ++d)
-        stf(static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + d, __int_as_float(0x7fffffff));
+    if (!softmax_all() && u0 < u1) {
+      const Segment& g = segs[seg % kSegs];
+      const float nan = __int_as_float(0x7fffffff);
+      for (int i = 0; i < 2; ++i)
+        w.part_ml[(2 * static_cast<int64_t>(blockIdx.x) + i) * kPair + x * kRows + row] = make_float2(0.0f, nan);
+      if (mbar_test(&bars.seg_full[seg % kSegs], (seg / kSegs) & 1) && row < tile_rows(g.t, x)) {
+        int64_t token;
+        int head;
+        row_owner(a, g.t, g.kv_head, x * kRows + row, &token, &head);
+        for (int d = 0; d < D; ++d) stf(static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + d, nan);
+      }
     }
   }
+#undef HC_SEGMENT
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
