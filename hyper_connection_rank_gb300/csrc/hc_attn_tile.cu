@@ -25,9 +25,10 @@
 // each, so that a row's 128 scores stay in them, and the others 72
 // (2 * 128 * 216 + 128 * 72 = 384 * 168).
 //
-// Work: all tiles' key blocks, for all key heads, laid end to end, are cut into
-// equal runs, one for each SM (hc_attn.cuh's slots give the tiles, plan_kernel
-// their prefix sums). A tile that a cut goes through is written as partial
+// Work: all tiles' key blocks, for all key heads, laid end to end with four
+// units before each tile for its queries and results, are cut into equal runs,
+// one for each SM (hc_attn.cuh's slots give the tiles, plan_kernel their prefix
+// sums); a cut among those units moves to the tile's start. A tile that a cut goes through is written as partial
 // sums by every CTA that has a piece of it and joined by join_kernel; at most
 // two pieces to a CTA are of that kind. So a long prompt, many short ones and one
 // short chunk over a long context all fill the GPU, without a choice of split.
@@ -50,7 +51,7 @@ constexpr int kThreads = 384;     // two softmax warpgroups, and one of the othe
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10, kPlanWarp = 11;
 constexpr int kSegs = 4;          // segments at hand
 constexpr int kSegUsers = 11;     // warps that read them
-constexpr int kMinBlocks = 4;     // key blocks that are worth a CTA
+constexpr int kTileCost = 4;      // what a tile costs beside its key blocks (queries in, results out), in blocks
 constexpr float kLazy = 8.0f;     // rise of a row's maximum (base-2) that O is rescaled for
 
 __device__ unsigned int g_tile_wait_timeouts = 0;
@@ -66,7 +67,7 @@ struct Cfg {
 };
 
 struct Work {
-  const int32_t* prefix;  // blocks of the tiles before each slot, per key head; [slots] = all
+  const int32_t* prefix;  // units of the tiles before each slot, per key head; [slots] = all
   int slots, ctas;
   float2* part_ml;        // [2 * ctas][kPair]
   float* part_o;          // [2 * ctas][kPair][dim]
@@ -79,7 +80,7 @@ __device__ __forceinline__ int64_t blocks_of(const AttnTile& t) {
   return n < 1 ? 1 : n;  // a tile that sees nothing still writes its zeros
 }
 
-// Number of key blocks of every slot's tile, as an exclusive prefix.
+// Units of every slot's tile, as an exclusive prefix.
 __global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, int32_t* prefix, int slots) {
   __shared__ int red[33];
   pdl_trigger();
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, int32_t* prefix,
     for (int64_t i = lo + lane; i < hi; i += 32) {
       AttnTile t;
       tile_at(a, a.g, s, i - lo, &t);
-      if (i < slots) prefix[i] = t.rows == 0 ? 0 : static_cast<int>(blocks_of(t));
+      if (i < slots) prefix[i] = t.rows == 0 ? 0 : kTileCost + static_cast<int>(blocks_of(t));
     }
   }
   __syncthreads();
@@ -127,27 +128,27 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, int32_t* prefix,
   }
 }
 
-// The run of key blocks that CTA c has, out of all: [u0, u1).
+// The run of units that CTA c has, out of all: [start(c), start(c + 1)).
 struct Run {
   int64_t per_head, all;
   int ctas;
   __device__ Run(const Work& w, int kv_heads) {
     per_head = w.prefix[w.slots];
     all = per_head * kv_heads;
-    const int64_t most = (all + kMinBlocks - 1) / kMinBlocks;
+    const int64_t most = all / (kTileCost + 1);  // a tile of one block to a CTA, where there is no more
     ctas = static_cast<int>(most < 1 ? 1 : most < w.ctas ? most : w.ctas);
   }
   __device__ int64_t start(int c) const { return all * c / ctas; }
 };
 
-// A CTA's piece of one tile pair: blocks [j0, j1) of its n.
+// A CTA's piece of one tile pair: blocks [j0, j1) of its n; none: the run's end.
 struct Segment {
   AttnTile t;
   int kv_head, j0, j1, n;
-  int64_t at;  // of the tile's first block among all
+  int64_t at;  // unit of the tile's first block
 };
 
-// The segment that starts at block u of all, in a run that ends at u1 (full warps).
+// The segment that unit u of all lies in, of a run that ends at u1 (full warps).
 __device__ __forceinline__ void segment_at(const AttnArgs& a, const Work& w, const Run& run, int64_t u, int64_t u1,
                                            Segment* g) {
   const int h = static_cast<int>(u / run.per_head);
@@ -157,11 +158,11 @@ __device__ __forceinline__ void segment_at(const AttnArgs& a, const Work& w, con
   const int s = warp_last_le(a.b.seqs, slot, start);
   tile_at(a, a.g, s, slot - start(s), &g->t);
   g->kv_head = h;
-  g->at = h * run.per_head + w.prefix[slot];
-  g->n = w.prefix[slot + 1] - w.prefix[slot];
-  g->j0 = static_cast<int>(u - g->at);
-  const int64_t end = u1 - g->at;
-  g->j1 = end < g->n ? static_cast<int>(end) : g->n;
+  g->at = h * run.per_head + w.prefix[slot] + kTileCost;
+  g->n = w.prefix[slot + 1] - w.prefix[slot] - kTileCost;
+  const int64_t from = u - g->at, to = u1 - g->at;
+  g->j0 = from < 0 ? 0 : static_cast<int>(from);
+  g->j1 = to < 0 ? 0 : to < g->n ? static_cast<int>(to) : g->n;
 }
 
 // Blocks of tile x (0: A, 1: B) of a pair: those up to the last key its last row sees.
@@ -265,50 +266,27 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
       : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return d;
 }
-// A row's scores through the cap, c log2(e) tanh(y) with y = scale / c * score.
-// Where all of a warp's |y| are below 3/4 (scores well inside the cap, the usual
-// case), tanh(y) = y P(y^2) with P of degree 5, fitted to tanh(sqrt(u)) /
-// sqrt(u) for the least error over that range (1.4e-8 with these coefficients
-// in float32), seven operations on pairs of floats that leave the
-// exponential unit to the softmax; else by exponential and quotient.
-__device__ __forceinline__ void cap_scores(float* f, const ScoreMap& map, float to_y) {
-  float hi[4], lo[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hi[i] = fmaxf(f[2 * i], f[2 * i + 1]);
-    lo[i] = fminf(f[2 * i], f[2 * i + 1]);
-  }
-#pragma unroll
-  for (int c = 8; c < kKeys; c += 8)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hi[i] = max3(hi[i], f[c + 2 * i], f[c + 2 * i + 1]);
-      lo[i] = min3(lo[i], f[c + 2 * i], f[c + 2 * i + 1]);
-    }
-  const float far = fmaxf(fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])), -fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3])));
-  if (__any_sync(0xffffffffu, far * to_y > 0.75f)) {
-#pragma unroll
-    for (int c = 0; c < kKeys; ++c) f[c] = map_score(map, f[c]);
-    return;
-  }
+// Scores inside a cap: c log2(e) tanh(k x) with k = scale / c as x P(x^2), where
+// |k x| <= 3/4. P is a polynomial of degree 4, fitted to tanh(sqrt(u)) / sqrt(u)
+// for the least error of tanh over that range (2.1e-7 with coefficients in float32),
+// k and c worked into its coefficients: five operations on pairs of floats
+// that leave the exponential unit to the softmax.
+struct CapPoly {
+  float c[5];
+  float most;  // largest |x|
+};
+__device__ __forceinline__ CapPoly cap_poly(float scale, float softcap) {
+  const float k = scale / softcap, k2 = k * k, k4 = k2 * k2, c = softcap * kLog2e * k;
+  return CapPoly{{c * 0.999997199f, c * k2 * -0.333230764f, c * k4 * 0.132260919f, c * k4 * k2 * -0.0492804497f, c * k4 * k4 * 0.0123188356f},
+                 k < 1e3f && softcap < 1e9f ? 0.75f / k : -1.0f};  // (a cap beyond these: none is inside)
+}
+__device__ __forceinline__ float2 cap_factor(const CapPoly& p, float2 x) {
   const auto twice = [](float v) { return make_float2(v, v); };
-  const float2 k = twice(to_y), zero = twice(0.0f);
-  const float2 p0 = twice(map.cap * 0.999999832f), p1 = twice(map.cap * -0.333324709f), p2 = twice(map.cap * 0.133205797f),
-               p3 = twice(map.cap * -0.0531492611f), p4 = twice(map.cap * 0.0192372364f),
-               p5 = twice(map.cap * -0.00449345569f);
-#pragma unroll
-  for (int c = 0; c < kKeys; c += 2) {
-    const float2 y = fma2(make_float2(f[c], f[c + 1]), k, zero);
-    const float2 u = fma2(y, y, zero);
-    float2 p = fma2(p5, u, p4);
-    p = fma2(p, u, p3);
-    p = fma2(p, u, p2);
-    p = fma2(p, u, p1);
-    p = fma2(p, u, p0);
-    p = fma2(p, y, zero);
-    f[c] = p.x;
-    f[c + 1] = p.y;
-  }
+  const float2 u = fma2(x, x, twice(0.0f));
+  float2 y = fma2(twice(p.c[4]), u, twice(p.c[3]));
+  y = fma2(y, u, twice(p.c[2]));
+  y = fma2(y, u, twice(p.c[1]));
+  return fma2(y, u, twice(p.c[0]));
 }
 
 template <typename T>
@@ -397,9 +375,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars.tmem;
   pdl_wait();
   pdl_trigger();  // (after the wait: join_kernel may read the plan before its own)
-  const Run run(w, a.kv_heads);
-  const bool mine = static_cast<int>(blockIdx.x) < run.ctas;
-  const int64_t u0 = mine ? run.start(blockIdx.x) : 0, u1 = mine ? run.start(blockIdx.x + 1) : 0;
   // tensor memory: S (and P) of A and B, then O of A and B
   constexpr uint32_t kO = 2 * kKeys;
 
@@ -421,10 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot = 0;
       uint32_t round = 0;
       const auto copy_all = [&]() -> bool {
-        int seg = 0;
-        for (int64_t u = u0; u < u1; ++seg) {
+        for (int seg = 0;; ++seg) {
           HC_SEGMENT(seg);
           const Segment& g = segs[seg % kSegs];
+          if (g.j1 <= g.j0) return true;
           for (int j = g.j0; j < g.j1; ++j) {
             const int64_t key0 = g.t.base + static_cast<int64_t>(j) * kKeys;
             // pages of this lane's copies; a box without a key that any row sees lies outside the pool, and reads zeros
@@ -461,10 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          u = g.at + g.j1;
           done_with(seg);
         }
-        return true;
       };
       const bool ok = copy_all();
       // the CTA keeps its memory until the last copies have landed and the last products have read them
@@ -509,13 +482,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&bars.o_done[x]);
       };
       const auto multiply_all = [&]() -> bool {
-        int seg = 0;
-        for (int64_t u = u0; u < u1; ++seg) {
+        for (int seg = 0;; ++seg) {
           HC_SEGMENT(seg);
           const Segment& g = segs[seg % kSegs];
           const int j0 = g.j0, j1 = g.j1;
+          if (j1 <= j0) return true;
           const int ends[2] = {min(tile_blocks(a, g.t, 0), j1), min(tile_blocks(a, g.t, 1), j1)};
-          u = g.at + j1;
           done_with(seg);
           HC_WAIT(&bars.kv_full[slot], round & 1);
 #pragma unroll
@@ -559,7 +531,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        return true;
       };
       multiply_all();
     } else if (warp == kFixWarp) {
@@ -567,10 +538,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot = 0;
       uint32_t edges = 0;  // parity of each slot's edge barrier
       const auto fix_all = [&]() -> bool {
-        int seg = 0;
-        for (int64_t u = u0; u < u1; ++seg) {
+        for (int seg = 0;; ++seg) {
           HC_SEGMENT(seg);
           const Segment& g = segs[seg % kSegs];
+          if (g.j1 <= g.j0) return true;
           for (int j = g.j0; j < g.j1; ++j) {
             const int v_slot = slot + 1 == C::kSlots ? 0 : slot + 1;
             slot = v_slot + 1 == C::kSlots ? 0 : v_slot + 1;
@@ -591,28 +562,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.kv_full[v_slot]);
           }
-          u = g.at + g.j1;
           done_with(seg);
         }
-        return true;
       };
       fix_all();
     } else {
       // ---- the run's segments, one after another ----
       const auto plan_all = [&]() -> bool {
-        int seg = 0;
-        for (int64_t u = u0; u < u1; ++seg) {
-          Segment g;
-          segment_at(a, w, run, u, u1, &g);
+        const Run run(w, a.kv_heads);
+        const bool mine = static_cast<int>(blockIdx.x) < run.ctas;
+        int64_t u = mine ? run.start(blockIdx.x) : 0;
+        const int64_t u1 = mine ? run.start(blockIdx.x + 1) : 0;
+        for (int seg = 0;; ++seg) {
+          Segment g = {};
+          if (u < u1) segment_at(a, w, run, u, u1, &g);
           HC_WAIT(&bars.seg_empty[seg % kSegs], ((seg / kSegs) & 1) ^ 1);
           if (lane == 0) {
             segs[seg % kSegs] = g;
             mbar_arrive(&bars.seg_full[seg % kSegs]);
           }
           __syncwarp();
-          u = g.at + g.j1;
+          if (g.j1 <= g.j0) return true;
+          u = g.at + g.n;
         }
-        return true;
       };
       plan_all();
     }
@@ -623,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // this warp's 32 lanes
     const uint32_t s_at = lanes + x * kKeys, o_at = lanes + kO + x * D;
     const ScoreMap map = score_map(a.scale, a.softcap);
+    const CapPoly poly = cap_poly(a.scale, CAP ? a.softcap : 1.0f);
     uint32_t s_seen = 0, o_seen = 0;
     const auto load_q = [&](const Segment& sg) {
       if (sg.j0 >= min(tile_blocks(a, sg.t, x), sg.j1)) return;
@@ -644,15 +617,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = neg_inf(), l = 0.0f;
     int seg = 0;
     const auto softmax_all = [&]() -> bool {
-      if (u0 < u1) {
-        HC_SEGMENT(0);
-        load_q(segs[0]);
-      }
-      for (int64_t u = u0; u < u1; ++seg) {
+      HC_SEGMENT(0);
+      load_q(segs[0]);
+      for (;; ++seg) {
         const Segment& g = segs[seg % kSegs];
+        if (g.j1 <= g.j0) return true;
         const int end = min(tile_blocks(a, g.t, x), g.j1);
         const int rows = tile_rows(g.t, x);
-        const int64_t u_next = g.at + g.j1;
         // keys that this row sees, from the tile's first block on: [from, to); those that every row sees: [all_from, all_to)
         int from = 0, to = 0, all_from = 0, all_to = 0;
         if (rows > 0) {
@@ -679,23 +650,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kKeys; c += 32) landed32(s + c);
           float* f = reinterpret_cast<float*>(s);
-          if (CAP) cap_scores(f, map, a.scale / a.softcap);
+          // largest (and, to see whether all are inside the cap, smallest) score
+          float tops[4], lows[4];
+          const auto extremes = [&] {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tops[i] = fmaxf(f[2 * i], f[2 * i + 1]);
+#pragma unroll
+            for (int c = 8; c < kKeys; c += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) tops[i] = max3(tops[i], f[c + 2 * i], f[c + 2 * i + 1]);
+            return fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+          };
           const int j0 = j * kKeys;
-          if (j0 < all_from || j0 + kKeys > all_to) {
+          const bool masked = j0 < all_from || j0 + kKeys > all_to;
+          bool inside = false;  // scores are still to go through the cap, all well within it
+          float top;
+          if (CAP) {
+            top = extremes();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lows[i] = fminf(f[2 * i], f[2 * i + 1]);
+#pragma unroll
+            for (int c = 8; c < kKeys; c += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) lows[i] = min3(lows[i], f[c + 2 * i], f[c + 2 * i + 1]);
+            const float low = fminf(fminf(lows[0], lows[1]), fminf(lows[2], lows[3]));
+            const bool far = __any_sync(0xffffffffu, fmaxf(top, -low) > poly.most);
+            inside = !far && !masked;
+            if (far) {
+#pragma unroll
+              for (int c = 0; c < kKeys; ++c) f[c] = map_score(map, f[c]);
+            } else if (masked) {
+#pragma unroll
+              for (int c = 0; c < kKeys; c += 2) {
+                const float2 v = make_float2(f[c], f[c + 1]);
+                const float2 y = fma2(v, cap_factor(poly, v), make_float2(0.0f, 0.0f));
+                f[c] = y.x;
+                f[c + 1] = y.y;
+              }
+            }
+          }
+          if (masked) {
             const int lo = from - j0, hi = to - j0;
 #pragma unroll
             for (int c = 0; c < kKeys; ++c)
               if (c < lo || c >= hi) f[c] = neg_inf();
           }
-          float tops[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tops[i] = fmaxf(f[2 * i], f[2 * i + 1]);
-#pragma unroll
-          for (int c = 8; c < kKeys; c += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tops[i] = max3(tops[i], f[c + 2 * i], f[c + 2 * i + 1]);
           const float mul = CAP ? 1.0f : map.mul;
-          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mul;
+          top = inside ? map_score(map, top) : extremes() * mul;
           if (j == g.j0) {
             m = top;
           } else if (__any_sync(0xffffffffu, top > m + kLazy || (m == neg_inf() && top > m))) {
@@ -721,22 +722,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float ref = m == neg_inf() ? 0.0f : m;
           const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(-ref, -ref);
           float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+          const auto weights = [&](auto factor) {
 #pragma unroll
-          for (int h = 0; h < kKeys; h += 64) {
-            uint32_t p[32];
+            for (int h = 0; h < kKeys; h += 64) {
+              uint32_t p[32];
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-              const float* y = f + h + c;
-              float2 y0 = fma2(make_float2(y[0], y[1]), mul2, ref2);
-              float2 y1 = fma2(make_float2(y[2], y[3]), mul2, ref2);
-              y0 = make_float2(ex2(y0.x), ex2(y0.y));
-              y1 = make_float2(ex2(y1.x), ex2(y1.y));
-              sum0 = add2(sum0, y0);
-              sum1 = add2(sum1, y1);
-              p[c / 2] = pack2<T>(y0.x, y0.y);
-              p[c / 2 + 1] = pack2<T>(y1.x, y1.y);
+              for (int c = 0; c < 64; c += 4) {
+                const float2 v0 = make_float2(f[h + c], f[h + c + 1]), v1 = make_float2(f[h + c + 2], f[h + c + 3]);
+                float2 y0 = fma2(v0, factor(v0), ref2);
+                float2 y1 = fma2(v1, factor(v1), ref2);
+                y0 = make_float2(ex2(y0.x), ex2(y0.y));
+                y1 = make_float2(ex2(y1.x), ex2(y1.y));
+                sum0 = add2(sum0, y0);
+                sum1 = add2(sum1, y1);
+                p[c / 2] = pack2<T>(y0.x, y0.y);
+                p[c / 2 + 1] = pack2<T>(y1.x, y1.y);
+              }
+              tmem_st32(s_at + h / 2, p);
             }
-            tmem_st32(s_at + h / 2, p);
+          };
+          if (CAP && inside) {
+            weights([&](float2 v) { return cap_factor(poly, v); });
+          } else {
+            weights([&](float2) { return mul2; });
           }
           tmem_wait_st();
           tc_fence_before();
@@ -747,10 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++o_seen;
         }
         // the tile's scores are all formed, so its queries make room for the next segment's
-        if (u_next < u1) {
-          HC_SEGMENT(seg + 1);
-          load_q(segs[(seg + 1) % kSegs]);
-        }
+        HC_SEGMENT(seg + 1);
+        load_q(segs[(seg + 1) % kSegs]);
         if (rows > 0) {
           const bool partial = g.j0 > 0 || g.j1 < g.n;
           const bool some = end > g.j0;
@@ -806,17 +812,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_before();  // O has been read before the next segment's weights let it be written
         }
-        u = u_next;
         done_with(seg);
       }
-      return true;
     };
-    if (!softmax_all() && u0 < u1) {
+    if (!softmax_all()) {
       const Segment& g = segs[seg % kSegs];
       const float nan = __int_as_float(0x7fffffff);
       for (int i = 0; i < 2; ++i)
         w.part_ml[(2 * static_cast<int64_t>(blockIdx.x) + i) * kPair + x * kRows + row] = make_float2(0.0f, nan);
-      if (mbar_test(&bars.seg_full[seg % kSegs], (seg / kSegs) & 1) && row < tile_rows(g.t, x)) {
+      if (mbar_test(&bars.seg_full[seg % kSegs], (seg / kSegs) & 1) && g.j1 > g.j0 && row < tile_rows(g.t, x)) {
         int64_t token;
         int head;
         row_owner(a, g.t, g.kv_head, x * kRows + row, &token, &head);
@@ -851,7 +855,7 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a, Work w) {
   const int64_t u = run.start(c0 + 1);
   Segment g;
   segment_at(a, w, run, u, run.all, &g);
-  if (g.at == u || run.start(c0) > g.at) return;
+  if (g.j0 == 0 || run.start(c0) > g.at) return;
   const int row0 = blockIdx.y * kJoinRows;
   const int rows = min(g.t.rows - row0, kJoinRows);
   if (rows <= 0) return;
