@@ -61,12 +61,14 @@ struct Cfg {
   static constexpr int kHalves = D / 64;             // boxes of 64 features
   static constexpr int kHalf = kKeys * 128;          // bytes of one such box of 128 rows
   static constexpr int kSlot = kHalves * kHalf;      // a block's keys or values
-  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kSlots = D == 128 ? 4 : 6;
   static constexpr int kQ = kHalves * kRows * 128;   // one tile's queries
-  static constexpr int kSmem = 2 * kQ + kSlots * kSlot + 1024;
+  static constexpr int kStage = 8 * 32 * 128;        // results on their way out, 128 bytes of each row
+  static constexpr int kSmem = 2 * kQ + kSlots * kSlot + kStage + 1024;
 };
 
 struct Work {
+  const AttnTile* tiles;  // tile of each slot
   const int32_t* prefix;  // units of the tiles before each slot, per key head; [slots] = all
   int slots, ctas;
   float2* part_ml;        // [2 * ctas][kPair]
@@ -80,8 +82,8 @@ __device__ __forceinline__ int64_t blocks_of(const AttnTile& t) {
   return n < 1 ? 1 : n;  // a tile that sees nothing still writes its zeros
 }
 
-// Units of every slot's tile, as an exclusive prefix.
-__global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, int32_t* prefix, int slots) {
+// The tile of every slot, and the units of all before it.
+__global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, int32_t* prefix, AttnTile* tiles, int slots) {
   __shared__ int red[33];
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, int32_t* prefix,
     for (int64_t i = lo + lane; i < hi; i += 32) {
       AttnTile t;
       tile_at(a, a.g, s, i - lo, &t);
+      if (i < slots) tiles[i] = t;
       if (i < slots) prefix[i] = t.rows == 0 ? 0 : kTileCost + static_cast<int>(blocks_of(t));
     }
   }
@@ -149,14 +152,12 @@ struct Segment {
 };
 
 // The segment that unit u of all lies in, of a run that ends at u1 (full warps).
-__device__ __forceinline__ void segment_at(const AttnArgs& a, const Work& w, const Run& run, int64_t u, int64_t u1,
+__device__ __forceinline__ void segment_at(const Work& w, const Run& run, int64_t u, int64_t u1,
                                            Segment* g) {
   const int h = static_cast<int>(u / run.per_head);
   const int64_t v = u - h * run.per_head;
   const int slot = warp_last_le(w.slots, v, [&](int i) { return static_cast<int64_t>(w.prefix[i]); });
-  const auto start = [&](int s) { return first_row(a.b, s) * a.group / kPair + s; };
-  const int s = warp_last_le(a.b.seqs, slot, start);
-  tile_at(a, a.g, s, slot - start(s), &g->t);
+  g->t = w.tiles[slot];
   g->kv_head = h;
   g->at = h * run.per_head + w.prefix[slot] + kTileCost;
   g->n = w.prefix[slot + 1] - w.prefix[slot] - kTileCost;
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t u1 = mine ? run.start(blockIdx.x + 1) : 0;
         for (int seg = 0;; ++seg) {
           Segment g = {};
-          if (u < u1) segment_at(a, w, run, u, u1, &g);
+          if (u < u1) segment_at(w, run, u, u1, &g);
           HC_WAIT(&bars.seg_empty[seg % kSegs], ((seg / kSegs) & 1) ^ 1);
           if (lane == 0) {
             segs[seg % kSegs] = g;
@@ -597,28 +598,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     const ScoreMap map = score_map(a.scale, a.softcap);
     const CapPoly poly = cap_poly(a.scale, CAP ? a.softcap : 1.0f);
     uint32_t s_seen = 0, o_seen = 0;
-    const auto load_q = [&](const Segment& sg) {
-      if (sg.j0 >= min(tile_blocks(a, sg.t, x), sg.j1)) return;
-      const uint4* src = nullptr;
+    // Queries of a segment's tile: a warp copies its 32 rows, whole rows side by side, and hands them over when they have landed.
+    const auto fetch_q = [&](const Segment& sg) {
+      if (sg.j0 >= min(tile_blocks(a, sg.t, x), sg.j1)) return false;
+      int64_t at = -1;
       if (row < tile_rows(sg.t, x)) {
         int64_t token;
         int head;
         row_owner(a, sg.t, sg.kv_head, x * kRows + row, &token, &head);
-        src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + token * a.q_ts + head * a.q_hs);
+        at = token * a.q_ts + head * a.q_hs;
       }
-      unsigned char* dst = smem + x * C::kQ + row * 128;
+      constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;
+      const int c = lane % kChunks;
+      const uint32_t dst = smem_addr(smem + x * C::kQ + (c >> 3) * (kRows * 128));
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c)
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4)) =
-            src ? src[c] : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 32; i += kAtOnce) {
+        const int from = i + lane / kChunks, r = (warp & 3) * 32 + from;
+        const int64_t off = __shfl_sync(0xffffffffu, at, from);
+        cp_async16_zfill(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                         static_cast<const T*>(a.q) + (off < 0 ? 0 : off) + c * 8, off < 0 ? 0 : 16);
+      }
+      cp_async_commit();
+      return true;
+    };
+    const auto hand_q = [&] {
+      cp_async_wait_all();
       fence_async_smem();
       mbar_arrive(&bars.q_full[x]);
+    };
+    // 128 bytes of each of the warp's rows, held a row to a lane, to where `place` says (element offset, -1: nowhere): through
+    // shared memory, so that a store writes four rows' 128 bytes and not 16 bytes of 32 rows.
+    unsigned char* const stage = ring + C::kSlots * C::kSlot + warp * (32 * 128);
+    const auto write_out = [&](const uint32_t* y, unsigned char* base, int64_t place, bool wide) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+            make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+      __syncwarp();
+      const int c = lane & 7;
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const int r = i + (lane >> 3);
+        const int64_t off = __shfl_sync(0xffffffffu, place, r);
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+        if (off < 0) continue;
+        unsigned char* dst = base + off + c * 16;
+        if (wide) {
+          *reinterpret_cast<uint4*>(dst) = v;
+        } else {
+          const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint16_t*>(dst)[e] = static_cast<uint16_t>(w4[e / 2] >> (16 * (e & 1)));
+        }
+      }
+      __syncwarp();
     };
     float m = neg_inf(), l = 0.0f;
     int seg = 0;
     const auto softmax_all = [&]() -> bool {
       HC_SEGMENT(0);
-      load_q(segs[0]);
+      if (fetch_q(segs[0])) hand_q();
       for (;; ++seg) {
         const Segment& g = segs[seg % kSegs];
         if (g.j1 <= g.j0) return true;
@@ -756,14 +796,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the tile's scores are all formed, so its queries make room for the next segment's
         HC_SEGMENT(seg + 1);
-        load_q(segs[(seg + 1) % kSegs]);
+        const bool fetched = fetch_q(segs[(seg + 1) % kSegs]);
+        const bool some = end > g.j0;
+        if (some) {
+          HC_WAIT(&bars.o_done[x], (o_seen - 1) & 1);
+          tc_fence_after();
+        }
+        if (fetched) hand_q();
         if (rows > 0) {
           const bool partial = g.j0 > 0 || g.j1 < g.n;
-          const bool some = end > g.j0;
-          if (some) {
-            HC_WAIT(&bars.o_done[x], (o_seen - 1) & 1);
-            tc_fence_after();
-          }
+          const bool real = row < rows;
           if (partial) {
             const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + (g.j0 > 0 ? 0 : 1)) * kPair + x * kRows + row;
             w.part_ml[at] = some ? make_float2(m, l) : make_float2(neg_inf(), 0.0f);
@@ -774,41 +816,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(o_at + c, o);
                 tmem_wait_ld();
                 landed32(o);
-                uint4* dst = reinterpret_cast<uint4*>(w.part_o + at * D + c);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                write_out(o, reinterpret_cast<unsigned char*>(w.part_o), real ? (at * D + c) * 4 : -1, true);
               }
             }
           } else {
             int64_t token = 0;
             int head = 0;
-            if (row < rows) row_owner(a, g.t, g.kv_head, x * kRows + row, &token, &head);
-            T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs;
+            if (real) row_owner(a, g.t, g.kv_head, x * kRows + row, &token, &head);
+            const int64_t at = token * a.o_ts + head * a.o_hs;
             const bool wide = ((a.o_ts | a.o_hs) & 7) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_at + c, o);
-              tmem_wait_ld();
-              landed32(o);
-              if (row < rows) {
-                uint32_t y[16];
+            for (int c = 0; c < D; c += 64) {
+              uint32_t y[32];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t o[32];
+                tmem_ld32(o_at + c + 32 * h, o);
+                tmem_wait_ld();
+                landed32(o);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                  y[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                if (wide) {
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4*>(dst + c + 8 * i) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-                } else {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    reinterpret_cast<uint16_t*>(dst)[c + i] = static_cast<uint16_t>(y[i / 2] >> (16 * (i & 1)));
-                }
+                  y[16 * h + i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
               }
+              write_out(y, static_cast<unsigned char*>(a.out), real ? (at + c) * 2 : -1, wide);
             }
-            if (row < rows && a.lse) a.lse[token * a.heads + head] = l == 0.0f ? neg_inf() : m * kLn2 + logf(l);
+            if (real && a.lse) a.lse[token * a.heads + head] = l == 0.0f ? neg_inf() : m * kLn2 + logf(l);
           }
           tc_fence_before();  // O has been read before the next segment's weights let it be written
         }
@@ -854,7 +887,7 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a, Work w) {
   if (c0 + 1 >= run.ctas) return;
   const int64_t u = run.start(c0 + 1);
   Segment g;
-  segment_at(a, w, run, u, run.all, &g);
+  segment_at(w, run, u, run.all, &g);
   if (g.j0 == 0 || run.start(c0) > g.at) return;
   const int row0 = blockIdx.y * kJoinRows;
   const int rows = min(g.t.rows - row0, kJoinRows);
@@ -949,7 +982,7 @@ cudaError_t launch_t(const AttnArgs& a, const Work& w, const CUtensorMap& k, con
   constexpr size_t smem = Cfg<D>::kSmem;
   cudaError_t e = ensure_smem<tile_kernel<T, D, CAP>>(smem);
   if (e != cudaSuccess) return e;
-  plan_kernel<<<1, 1024, 0, s>>>(a, const_cast<int32_t*>(w.prefix), w.slots);
+  plan_kernel<<<1, 1024, 0, s>>>(a, const_cast<int32_t*>(w.prefix), const_cast<AttnTile*>(w.tiles), w.slots);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = launch_pdl(tile_kernel<T, D, CAP>, dim3(w.ctas), dim3(kThreads), smem, s, 1, a, w, k, v);
@@ -965,6 +998,7 @@ cudaError_t launch_d(const AttnArgs& a, const Work& w, const CUtensorMap& k, con
 }
 
 size_t prefix_bytes(int64_t slots) { return align_up(static_cast<size_t>(slots + 1) * 4, 256); }
+size_t tiles_bytes(int64_t slots) { return align_up(static_cast<size_t>(slots) * sizeof(AttnTile), 256); }
 
 int64_t slots_of(int64_t tokens, int group, int seqs) { return tokens * group / kPair + seqs; }
 
@@ -987,7 +1021,8 @@ bool attn_tile_supported(int dtype, int dim, int page, float scale, bool aligned
 
 size_t attn_tile_workspace(int64_t tokens, int group, int seqs, int dim, int num_sms) {
   const size_t rows = 2 * static_cast<size_t>(num_sms) * kPair;
-  return prefix_bytes(slots_of(tokens, group, seqs)) + align_up(rows * 8, 256) + rows * dim * 4;
+  const int64_t slots = slots_of(tokens, group, seqs);
+  return prefix_bytes(slots) + tiles_bytes(slots) + align_up(rows * 8, 256) + rows * dim * 4;
 }
 
 cudaError_t launch_attn_tile(const AttnArgs& args, int dtype, void* workspace, int num_sms, cudaStream_t s) {
@@ -999,6 +1034,8 @@ cudaError_t launch_attn_tile(const AttnArgs& args, int dtype, void* workspace, i
   char* p = static_cast<char*>(workspace);
   w.prefix = reinterpret_cast<const int32_t*>(p);
   p += prefix_bytes(w.slots);
+  w.tiles = reinterpret_cast<const AttnTile*>(p);
+  p += tiles_bytes(w.slots);
   w.part_ml = reinterpret_cast<float2*>(p);
   p += align_up(2 * static_cast<size_t>(num_sms) * kPair * 8, 256);
   w.part_o = reinterpret_cast<float*>(p);
