@@ -271,7 +271,8 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
 // |k x| <= 3/4. P is a polynomial of degree 4, fitted to tanh(sqrt(u)) / sqrt(u)
 // for the least error of tanh over that range (2.1e-7 with coefficients in float32),
 // k and c worked into its coefficients: five operations on pairs of floats
-// that leave the exponential unit to the softmax.
+// that leave the exponential unit to the softmax. A score of minus infinity, which
+// stands for a key that is not seen, stays one: P's highest coefficient is positive.
 struct CapPoly {
   float c[5];
   float most;  // largest |x|
@@ -279,7 +280,7 @@ struct CapPoly {
 __device__ __forceinline__ CapPoly cap_poly(float scale, float softcap) {
   const float k = scale / softcap, k2 = k * k, k4 = k2 * k2, c = softcap * kLog2e * k;
   return CapPoly{{c * 0.999997199f, c * k2 * -0.333230764f, c * k4 * 0.132260919f, c * k4 * k2 * -0.0492804497f, c * k4 * k4 * 0.0123188356f},
-                 k < 1e3f && softcap < 1e9f ? 0.75f / k : -1.0f};  // (a cap beyond these: none is inside)
+                 k > 1e-4f && k < 1e3f && softcap < 1e9f ? 0.75f / k : -1.0f};  // (a cap beyond these: none is inside)
 }
 __device__ __forceinline__ float2 cap_factor(const CapPoly& p, float2 x) {
   const auto twice = [](float v) { return make_float2(v, v); };
@@ -714,19 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) lows[i] = min3(lows[i], f[c + 2 * i], f[c + 2 * i + 1]);
             const float low = fminf(fminf(lows[0], lows[1]), fminf(lows[2], lows[3]));
-            const bool far = __any_sync(0xffffffffu, fmaxf(top, -low) > poly.most);
-            inside = !far && !masked;
-            if (far) {
+            inside = !__any_sync(0xffffffffu, fmaxf(top, -low) > poly.most);
+            if (!inside) {
 #pragma unroll
               for (int c = 0; c < kKeys; ++c) f[c] = map_score(map, f[c]);
-            } else if (masked) {
-#pragma unroll
-              for (int c = 0; c < kKeys; c += 2) {
-                const float2 v = make_float2(f[c], f[c + 1]);
-                const float2 y = fma2(v, cap_factor(poly, v), make_float2(0.0f, 0.0f));
-                f[c] = y.x;
-                f[c + 1] = y.y;
-              }
             }
           }
           if (masked) {
@@ -736,7 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c < lo || c >= hi) f[c] = neg_inf();
           }
           const float mul = CAP ? 1.0f : map.mul;
-          top = inside ? map_score(map, top) : extremes() * mul;
+          if (!CAP || !inside || masked) top = extremes();
+          top = inside ? (top == neg_inf() ? top : map_score(map, top)) : top * mul;
           if (j == g.j0) {
             m = top;
           } else if (__any_sync(0xffffffffu, top > m + kLazy || (m == neg_inf() && top > m))) {
