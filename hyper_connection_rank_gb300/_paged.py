@@ -30,22 +30,23 @@ _ATTENTION = struct.Struct("@9PN3q4q3q3i3i2iiiI2f0q")
 _PAGES = struct.Struct("@6P2q3i0q")
 
 
-def _is(name, t, dtype, ndim):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.dim() != ndim:
-        raise ValueError(f"{name} must be a {ndim}-dimensional CUDA tensor of dtype {dtype}")
-
+# (A call costs the host as much as a small kernel costs the GPU, so the checks below ask each tensor for as little as they
+# can; what the library checks itself is left to it.)
 
 def _heads(name, t, dtype):
-    """A tensor of rows of heads, the last axis contiguous."""
-    _is(name, t, dtype, 3)
-    if t.stride(2) != 1 and t.shape[2] > 1:
-        raise ValueError(f"the last axis of {name} must be contiguous")
+    """A tensor of rows of heads, the last axis contiguous: (shape, strides)."""
+    if t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of dtype {dtype}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1):
+        raise ValueError(f"{name} must have three axes, the last one contiguous")
+    return shape, strides
 
 
 def _flat(name, t, dtype):
-    _is(name, t, dtype, 1)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-dimensional CUDA tensor of dtype {dtype}")
+    return t.shape[0]
 
 
 def _dtype_code(t):
@@ -56,48 +57,64 @@ def _dtype_code(t):
 
 
 def _table(t):
-    _is("page_table", t, torch.int32, 2)
-    if t.shape[1] < 1:
-        raise ValueError("page_table needs at least one column")
-    if t.stride(1) != 1 and t.shape[1] > 1:
-        raise ValueError("rows of page_table must be contiguous")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    """(sequences, columns, entries from one row to the next)"""
+    if t.dtype is not torch.int32 or not t.is_cuda or t.dim() != 2:
+        raise ValueError("page_table must be a 2-dimensional CUDA tensor of dtype torch.int32")
+    (seqs, width), (step, inner) = t.shape, t.stride()
+    if width < 1 or (inner != 1 and width > 1):
+        raise ValueError("page_table needs at least one column, and contiguous rows")
+    return seqs, width, step if seqs > 1 else max(step, width)
 
 
 def _batch(page_table, kv_lens, cu_q, tokens):
-    stride = _table(page_table)
-    seqs = page_table.shape[0]
-    _flat("kv_lens", kv_lens, torch.int32)
-    if kv_lens.shape[0] != seqs:
+    """(sequences, columns, row step of the table, address of cu_q)"""
+    seqs, width, step = _table(page_table)
+    if _flat("kv_lens", kv_lens, torch.int32) != seqs:
         raise ValueError("kv_lens and page_table differ in sequences")
     if cu_q is None:
         if tokens != seqs:
             raise ValueError("without cu_q every sequence has one new token")
-        return stride, seqs, 0
-    _flat("cu_q", cu_q, torch.int32)
-    if cu_q.shape[0] != seqs + 1:
+        return seqs, width, step, 0
+    if _flat("cu_q", cu_q, torch.int32) != seqs + 1:
         raise ValueError("cu_q must have one entry more than there are sequences")
-    return stride, seqs, cu_q.data_ptr()
+    return seqs, width, step, cu_q.data_ptr()
 
 
 def _caches(k_cache, v_cache, dtype):
-    _is("k_cache", k_cache, dtype, 4)
-    _is("v_cache", v_cache, dtype, 4)
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    """(shape, strides) of both."""
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype or not k_cache.is_cuda or not v_cache.is_cuda:
+        raise ValueError(f"k_cache and v_cache must be CUDA tensors of dtype {dtype}")
+    shape, strides = k_cache.shape, k_cache.stride()
+    if shape != v_cache.shape or strides != v_cache.stride():
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    if k_cache.stride(3) != 1 and k_cache.shape[3] > 1:
-        raise ValueError("the last axis of the caches must be contiguous")
+    if len(shape) != 4 or (strides[3] != 1 and shape[3] > 1):
+        raise ValueError("the caches must have four axes, the last one contiguous")
+    return shape, strides
+
+
+def _out(out, like, name):
+    """(out, its strides): the one given, or a new one of the shape of `like`."""
+    if out is None:
+        out = torch.empty_like(like)
+    elif out.shape != like.shape or out.dtype is not like.dtype:
+        raise ValueError(f"out must have the shape and dtype of {name}")
+    return out, _heads("out", out, like.dtype)[1]
 
 
 def _stream(t, stream, *temporaries):
     """The stream to launch on. Memory that this call allocated on the current stream and uses on another one must not be
     handed out again before that one is done with it."""
     if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
+        return _current_stream(t.get_device())
     for x in temporaries:
         if x is not None:
             x.record_stream(stream)
     return stream.cuda_stream
+
+
+# The current stream's handle without a Python object around it, where this build of torch has that.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def rotary_frequencies(rot_dim, theta=10000.0, *, scaling=None, factor=1.0, original_length=None, slow=1.0, fast=32.0,
@@ -143,22 +160,14 @@ def rotary(x, positions, inv_freq, *, amplitude=1.0, interleaved=False, inverse=
     from rot_dim on are copied. ``inverse=True`` turns back, which also takes the gradient of the result to that of x.
     ``out`` may be x itself."""
     code = _dtype_code(x)
-    _heads("x", x, x.dtype)
-    _flat("inv_freq", inv_freq, torch.float64)
-    _flat("positions", positions, torch.int32 if positions.dtype == torch.int32 else torch.int64)
-    tokens, heads, dim = x.shape
-    if positions.shape[0] != tokens:
+    (tokens, heads, dim), xs = _heads("x", x, x.dtype)
+    half = _flat("inv_freq", inv_freq, torch.float64)
+    narrow = positions.dtype is torch.int32
+    if _flat("positions", positions, torch.int32 if narrow else torch.int64) != tokens:
         raise ValueError("positions and x differ in tokens")
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    else:
-        _heads("out", out, x.dtype)
-        if out.shape != x.shape:
-            raise ValueError("out must have the shape of x")
-    xs, os = x.stride(), out.stride()
+    out, os = _out(out, x, "x")
     args = _ROTARY.pack(x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr(), tokens, xs[0], xs[1], os[0],
-                        os[1], heads, dim, 2 * inv_freq.shape[0], bool(interleaved), bool(inverse),
-                        positions.dtype == torch.int32, code, amplitude)
+                        os[1], heads, dim, 2 * half, bool(interleaved), bool(inverse), narrow, code, amplitude)
     check(lib().hc_rotary(args, _stream(x, stream, out)))
     return out
 
@@ -168,58 +177,45 @@ def rotary_append(q, k, v, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, 
     """Rotate a batch's new queries, and rotate its new keys and write them with the values into the cache
     (hc_rotary_append). q: (tokens, heads, head_dim); k, v: (tokens, kv_heads, head_dim), which may be parts of one matrix.
     Positions follow from kv_lens and cu_q. Returns the rotated queries (``out``, which may be q itself)."""
-    code = _dtype_code(q)
-    _heads("q", q, q.dtype)
-    _heads("k", k, q.dtype)
-    _heads("v", v, q.dtype)
-    _caches(k_cache, v_cache, q.dtype)
-    _flat("inv_freq", inv_freq, torch.float64)
-    tokens, heads, dim = q.shape
-    pages, page, kv_heads, cdim = k_cache.shape
-    if k.shape != v.shape or k.shape[0] != tokens or k.shape[1] != kv_heads or k.shape[2] != dim or cdim != dim:
+    code, dtype = _dtype_code(q), q.dtype
+    (tokens, heads, dim), qs = _heads("q", q, dtype)
+    kshape, ks = _heads("k", k, dtype)
+    vshape, vs = _heads("v", v, dtype)
+    (pages, page, kv_heads, cdim), cs = _caches(k_cache, v_cache, dtype)
+    half = _flat("inv_freq", inv_freq, torch.float64)
+    if kshape != vshape or kshape != (tokens, kv_heads, dim) or cdim != dim:
         raise ValueError("q, k, v and the caches differ in tokens, kv_heads or head_dim")
-    ts, seqs, cu = _batch(page_table, kv_lens, cu_q, tokens)
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        _heads("out", out, q.dtype)
-        if out.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-    qs, ks, vs, os, cs = q.stride(), k.stride(), v.stride(), out.stride(), k_cache.stride()
+    seqs, width, step, cu = _batch(page_table, kv_lens, cu_q, tokens)
+    out, os = _out(out, q, "q")
     args = _APPEND.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                        inv_freq.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cu, tokens, pages, ts, qs[0], qs[1],
-                        ks[0], ks[1], vs[0], vs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, page_table.shape[1], page, heads,
-                        kv_heads, dim, 2 * inv_freq.shape[0], bool(interleaved), code, amplitude)
+                        inv_freq.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cu, tokens, pages, step, qs[0], qs[1],
+                        ks[0], ks[1], vs[0], vs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, width, page, heads, kv_heads, dim,
+                        2 * half, bool(interleaved), code, amplitude)
     check(lib().hc_rotary_append(args, _stream(q, stream, out)))
     return out
 
 
-def _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, out, lse,
-                    workspace):
+def _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, os):
+    """The packed arguments before out, lse and workspace, and those after."""
     code = _dtype_code(q)
-    _heads("q", q, q.dtype)
-    _caches(k_cache, v_cache, q.dtype)
-    tokens, heads, dim = q.shape
-    pages, page, kv_heads, cdim = k_cache.shape
+    (tokens, heads, dim), qs = _heads("q", q, q.dtype)
+    (pages, page, kv_heads, cdim), cs = _caches(k_cache, v_cache, q.dtype)
     if cdim != dim or kv_heads < 1 or heads % kv_heads:
         raise ValueError("heads must be a multiple of kv_heads, and head_dim that of the caches")
-    ts, seqs, cu = _batch(page_table, kv_lens, cu_q, tokens)
-    qs, cs = q.stride(), k_cache.stride()
-    os = (heads * dim, dim) if out is None else out.stride()
-    at, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    return _ATTENTION.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cu,
-                           0 if out is None else out.data_ptr(), 0 if lse is None else lse.data_ptr(), at, size, tokens, pages,
-                           ts, qs[0], qs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, page_table.shape[1], page, heads,
-                           kv_heads, dim, max_q or 0, max_kv or 0, window or 0, code, flags,
-                           1.0 / math.sqrt(dim) if scale is None else scale, softcap or 0.0)
+    seqs, width, step, cu = _batch(page_table, kv_lens, cu_q, tokens)
+    front = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cu)
+    back = (tokens, pages, step, qs[0], qs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, width, page, heads, kv_heads, dim,
+            max_q or 0, max_kv or 0, window or 0, code, flags, 1.0 / math.sqrt(dim) if scale is None else scale, softcap or 0.0)
+    return front, back
 
 
 def paged_attention_workspace_size(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, max_q=None, max_kv=None, window=0,
                                    flags=0):
     """Bytes of workspace that ``paged_attention`` needs for these tensors (their contents do not matter)."""
-    return lib().hc_paged_attention_workspace_size(
-        _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, None, window, 0.0, max_q, max_kv, flags, None, None,
-                        None))
+    heads, dim = q.shape[1:]
+    front, back = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, None, window, 0.0, max_q, max_kv, flags,
+                                  (heads * dim, dim))
+    return lib().hc_paged_attention_workspace_size(_ATTENTION.pack(*front, 0, 0, 0, 0, *back))
 
 
 def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, scale=None, window=0, softcap=0.0, max_q=None,
@@ -231,23 +227,21 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, scal
     return_lse also the float32 logarithms (tokens, heads) of the sums of weights. A token that sees nothing gets zeros, and
     minus infinity. ``workspace``: a CUDA tensor of at least ``paged_attention_workspace_size`` bytes, allocated here if
     omitted."""
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        _heads("out", out, q.dtype)
-        if out.shape != q.shape:
-            raise ValueError("out must have the shape of q")
+    out, os = _out(out, q, "q")
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+    front, back = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags,
+                                  os)
+    results = (out.data_ptr(), 0 if lse is None else lse.data_ptr())
     L = lib()
+    at = size = 0
     if workspace is None:
-        need = L.hc_paged_attention_workspace_size(
-            _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, out,
-                            lse, None))
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    args = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, out,
-                           lse, workspace)
-    check(L.hc_paged_attention(args, _stream(q, stream, out, lse, workspace)))
+        size = L.hc_paged_attention_workspace_size(_ATTENTION.pack(*front, *results, 0, 0, *back))
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            at = workspace.data_ptr()
+    else:
+        at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    check(L.hc_paged_attention(_ATTENTION.pack(*front, *results, at, size, *back), _stream(q, stream, out, lse, workspace)))
     return (out, lse) if return_lse else out
 
 
@@ -265,26 +259,23 @@ def _pool(cache):
 
 def _pages(page_table, lens, refs, page_size, seqs_out, need_lens=True):
     """The new tables and counts, and the packed arguments."""
-    ts = _table(page_table)
-    seqs, width = page_table.shape
-    _flat("lens", lens, torch.int32)
-    _flat("refs", refs, torch.int32)
-    if lens.shape[0] != seqs:
+    seqs, width, step = _table(page_table)
+    pages = _flat("refs", refs, torch.int32)
+    if _flat("lens", lens, torch.int32) != seqs:
         raise ValueError("lens and page_table differ in sequences")
     if page_size < 1:
         raise ValueError("page_size must be positive")
-    dev = refs.device
-    table_out = torch.empty((seqs_out, width), dtype=torch.int32, device=dev)
-    lens_out = torch.empty((seqs_out,), dtype=torch.int32, device=dev) if need_lens else None
-    refs_out = torch.empty(refs.shape, dtype=torch.int32, device=dev)
+    table_out = refs.new_empty((seqs_out, width))
+    lens_out = refs.new_empty(seqs_out) if need_lens else None
+    refs_out = refs.new_empty(pages)
     args = _PAGES.pack(page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), table_out.data_ptr(),
-                       lens_out.data_ptr() if need_lens else 0, refs_out.data_ptr(), refs.shape[0], ts, seqs, width, page_size)
+                       lens_out.data_ptr() if need_lens else 0, refs_out.data_ptr(), pages, step, seqs, width, page_size)
     return args, table_out, lens_out, refs_out
 
 
 def _pages_workspace(refs, seqs):
     n = lib().hc_pages_workspace_size(refs.shape[0], seqs)
-    return torch.empty(n, dtype=torch.uint8, device=refs.device), n
+    return refs.new_empty((n + 3) // 4), n
 
 
 def page_copy(cache, src, dst, *, stream=None):
@@ -312,7 +303,7 @@ def page_fork(cache, page_table, lens, refs, parents, *, page_size=None, stream=
     args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, cache.shape[2] if page_size is None else page_size, n)
     if refs.shape[0] != pages:
         raise ValueError("refs must have an entry for every page of cache")
-    missing = torch.empty((1,), dtype=torch.int32, device=refs.device)
+    missing = refs.new_empty(1)
     ws, bytes_ = _pages_workspace(refs, max(n, page_table.shape[0]))
     check(lib().hc_page_fork(args, parents.data_ptr(), n, missing.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(),
                              bytes_, _stream(refs, stream, table_out, lens_out, refs_out, missing, ws)))
@@ -326,7 +317,7 @@ def page_extend(page_table, lens, refs, new_tokens, *, page_size, stream=None):
     if new_tokens.shape[0] != seqs:
         raise ValueError("new_tokens and page_table differ in sequences")
     args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, page_size, seqs)
-    missing = torch.empty((1,), dtype=torch.int32, device=refs.device)
+    missing = refs.new_empty(1)
     ws, bytes_ = _pages_workspace(refs, seqs)
     check(lib().hc_page_extend(args, new_tokens.data_ptr(), missing.data_ptr(), ws.data_ptr(), bytes_,
                                _stream(refs, stream, table_out, lens_out, refs_out, missing, ws)))
@@ -353,8 +344,8 @@ def page_compact(cache, page_table, lens, refs, *, page_size=None, stream=None):
                                           need_lens=False)
     if refs.shape[0] != pages:
         raise ValueError("refs must have an entry for every page of cache")
-    remap = torch.empty(refs.shape, dtype=torch.int32, device=refs.device)
-    live = torch.empty((1,), dtype=torch.int32, device=refs.device)
+    remap = refs.new_empty(pages)
+    live = refs.new_empty(1)
     ws, bytes_ = _pages_workspace(refs, seqs)
     check(lib().hc_page_compact(args, remap.data_ptr(), live.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(), bytes_,
                                 _stream(refs, stream, table_out, refs_out, remap, live, ws)))
