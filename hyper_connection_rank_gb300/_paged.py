@@ -265,9 +265,10 @@ def _pages(page_table, lens, refs, page_size, seqs_out, need_lens=True):
         raise ValueError("lens and page_table differ in sequences")
     if page_size < 1:
         raise ValueError("page_size must be positive")
-    table_out = refs.new_empty((seqs_out, width))
-    lens_out = refs.new_empty(seqs_out) if need_lens else None
-    refs_out = refs.new_empty(pages)
+    device = refs.device
+    table_out = torch.empty((seqs_out, width), dtype=torch.int32, device=device)
+    lens_out = torch.empty(seqs_out, dtype=torch.int32, device=device) if need_lens else None
+    refs_out = torch.empty_like(refs)
     args = _PAGES.pack(page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), table_out.data_ptr(),
                        lens_out.data_ptr() if need_lens else 0, refs_out.data_ptr(), pages, step, seqs, width, page_size)
     return args, table_out, lens_out, refs_out
@@ -275,7 +276,7 @@ def _pages(page_table, lens, refs, page_size, seqs_out, need_lens=True):
 
 def _pages_workspace(refs, seqs):
     n = lib().hc_pages_workspace_size(refs.shape[0], seqs)
-    return refs.new_empty((n + 3) // 4), n
+    return torch.empty(n, dtype=torch.uint8, device=refs.device), n
 
 
 def page_copy(cache, src, dst, *, stream=None):
@@ -303,7 +304,7 @@ def page_fork(cache, page_table, lens, refs, parents, *, page_size=None, stream=
     args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, cache.shape[2] if page_size is None else page_size, n)
     if refs.shape[0] != pages:
         raise ValueError("refs must have an entry for every page of cache")
-    missing = refs.new_empty(1)
+    missing = torch.empty(1, dtype=torch.int32, device=refs.device)
     ws, bytes_ = _pages_workspace(refs, max(n, page_table.shape[0]))
     check(lib().hc_page_fork(args, parents.data_ptr(), n, missing.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(),
                              bytes_, _stream(refs, stream, table_out, lens_out, refs_out, missing, ws)))
@@ -317,7 +318,7 @@ def page_extend(page_table, lens, refs, new_tokens, *, page_size, stream=None):
     if new_tokens.shape[0] != seqs:
         raise ValueError("new_tokens and page_table differ in sequences")
     args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, page_size, seqs)
-    missing = refs.new_empty(1)
+    missing = torch.empty(1, dtype=torch.int32, device=refs.device)
     ws, bytes_ = _pages_workspace(refs, seqs)
     check(lib().hc_page_extend(args, new_tokens.data_ptr(), missing.data_ptr(), ws.data_ptr(), bytes_,
                                _stream(refs, stream, table_out, lens_out, refs_out, missing, ws)))
@@ -344,8 +345,8 @@ def page_compact(cache, page_table, lens, refs, *, page_size=None, stream=None):
                                           need_lens=False)
     if refs.shape[0] != pages:
         raise ValueError("refs must have an entry for every page of cache")
-    remap = refs.new_empty(pages)
-    live = refs.new_empty(1)
+    remap = torch.empty_like(refs)
+    live = torch.empty(1, dtype=torch.int32, device=refs.device)
     ws, bytes_ = _pages_workspace(refs, seqs)
     check(lib().hc_page_compact(args, remap.data_ptr(), live.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(), bytes_,
                                 _stream(refs, stream, table_out, refs_out, remap, live, ws)))
