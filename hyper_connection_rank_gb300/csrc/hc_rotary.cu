@@ -19,7 +19,7 @@
 // forms that held two or four vectors of the next heads in registers ran at
 // half the occupancy and took 76 to 113 us where this takes 57.
 //
-// Measured (bf16, 13635 tokens of 32 + 2 * 8 heads of 128 written into pages of
+// Measured (bf16, 13638 tokens of 32 + 2 * 8 heads of 128 written into pages of
 // 64): 57 us, 5.9 TB/s, 88% of the measured copy bandwidth; the angles read
 // with bank conflicts cost 66 us. float32, 4099 tokens of 20 heads: 19.7 us, 4.3
 // TB/s (6.5 us of that is what a single token takes: a launch and a chain of
