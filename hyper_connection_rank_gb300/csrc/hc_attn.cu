@@ -7,11 +7,15 @@
 // kKeys: scores into shared memory, running maximum m and sum l of each row
 //   m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m')
 // with s in base-2 exponents, and the sums of values scaled alike in
-// registers. Bound by its multiply-adds (2 * dim for each visible pair and
-// product); 16 rows to a tile where a sequence has no more than that (single
-// tokens), else 64.
+// registers. 16 rows to a tile where a sequence has no more than that (single
+// tokens), else 64. Bound, for many rows, by the loads of its operands from shared
+// memory (a 16-byte load takes four cycles of the SM for 16 multiply-adds of
+// each of 32 threads): float32, three chunks of up to 131 tokens of 20 heads
+// of 128 behind up to 901, 162 us, 18.6 TFLOP/s.
 #include <algorithm>
+#include <type_traits>
 
+#include "hc_async.cuh"
 #include "hc_attn_internal.h"
 #include "hc_paged_internal.h"
 
@@ -21,25 +25,27 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kKeys = 32;
 
-// DP: head_dim padded to a multiple of 64.
-template <int ROWS, int DP>
+// DP: head_dim padded to a multiple of 64. BUFS: buffers of keys and values, two
+// where the next step's come by cp.async while this one is worked on.
+template <int ROWS, int DP, int BUFS>
 struct GeneralSmem {
   float q[ROWS][DP + 4];
-  float k[kKeys][DP + 4];
-  float v[kKeys][DP];
-  float p[ROWS][kKeys + 1];
+  float k[BUFS][kKeys][DP + 4];
+  float v[BUFS][kKeys][DP];
+  float p[ROWS][kKeys + 4];
   float alpha[ROWS];
   float m[ROWS], l[ROWS];
-  int64_t place[kKeys];  // element offset of a key's row in the pool, -1: no such key
 };
 
 // Threads are 16 x 16: thread (ty, tx) forms the scores of rows ty + 16 i and
 // keys tx, tx + 16, and the sums of rows ty + 16 i and features 4 tx + 64 c ..
-// + 3.
-template <typename T, int ROWS, int DP>
+// + 3. Keys j of a step belong to warp j % 8, which finds their places in the
+// pool and copies their rows.
+template <typename T, int ROWS, int DP, bool ASYNC>
 __global__ void __launch_bounds__(kThreads) general_kernel(AttnArgs a) {
+  constexpr int BUFS = ASYNC ? 2 : 1;
   extern __shared__ __align__(16) unsigned char raw[];
-  auto& sm = *reinterpret_cast<GeneralSmem<ROWS, DP>*>(raw);
+  auto& sm = *reinterpret_cast<GeneralSmem<ROWS, DP, BUFS>*>(raw);
   constexpr int RI = ROWS / 16, CI = DP / 64;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
   const int z = blockIdx.z, kvh = blockIdx.y;
@@ -51,6 +57,42 @@ __global__ void __launch_bounds__(kThreads) general_kernel(AttnArgs a) {
   const T* kp = static_cast<const T*>(a.k);
   const T* vp = static_cast<const T*>(a.v);
 
+  const auto bring = [&](int64_t kb, int buf) {
+    int64_t at[kKeys / 8];
+#pragma unroll
+    for (int i = 0; i < kKeys / 8; ++i) {
+      const int64_t j = kb + warp + 8 * i;
+      at[i] = -1;
+      if (j >= t.lo && j < k1) {
+        const int page = page_of(a.b, t.s, j / a.b.page_size);
+        if (page >= 0) at[i] = page * a.c_ps + j % a.b.page_size * a.c_ts + kvh * a.c_hs;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kKeys / 8; ++i) {
+      const int j = warp + 8 * i;
+      if (ASYNC) {
+#pragma unroll
+        for (int d = lane * 4; d < DP; d += 128) {
+          const bool in = at[i] >= 0 && d < a.dim;
+          const int64_t off = in ? at[i] + d : 0;
+          cp_async16_zfill(smem_addr(&sm.k[buf][j][d]), kp + off, in ? 16 : 0);
+          cp_async16_zfill(smem_addr(&sm.v[buf][j][d]), vp + off, in ? 16 : 0);
+        }
+      } else {
+#pragma unroll
+        for (int d = lane; d < DP; d += 32) {
+          const bool in = at[i] >= 0 && d < a.dim;
+          sm.k[buf][j][d] = in ? ldf(kp + at[i] + d) : 0.0f;
+          sm.v[buf][j][d] = in ? ldf(vp + at[i] + d) : 0.0f;
+        }
+      }
+    }
+  };
+  if (ASYNC) {
+    bring(k0, 0);
+    cp_async_commit();
+  }
   for (int r = warp; r < ROWS; r += kThreads / 32) {
     const T* src = nullptr;
     if (r < t.rows) {
@@ -67,33 +109,22 @@ __global__ void __launch_bounds__(kThreads) general_kernel(AttnArgs a) {
   }
   float acc[RI][CI][4] = {};
 
+  int buf = 0;
   for (int64_t kb = k0; kb < k1; kb += kKeys) {
     __syncthreads();
-    if (tid < kKeys) {
-      const int64_t j = kb + tid;
-      int64_t at = -1;
-      if (j >= t.lo && j < k1) {
-        const int page = page_of(a.b, t.s, j / a.b.page_size);
-        if (page >= 0) at = page * a.c_ps + j % a.b.page_size * a.c_ts + kvh * a.c_hs;
-      }
-      sm.place[tid] = at;
-    }
-    __syncthreads();
-    for (int j = warp; j < kKeys; j += kThreads / 32) {
-      const int64_t at = sm.place[j];
-#pragma unroll
-      for (int d = lane; d < DP; d += 32) {
-        const bool in = at >= 0 && d < a.dim;
-        sm.k[j][d] = in ? ldf(kp + at + d) : 0.0f;
-        sm.v[j][d] = in ? ldf(vp + at + d) : 0.0f;
-      }
+    if (ASYNC) {
+      if (kb + kKeys < k1) bring(kb + kKeys, buf ^ 1);
+      cp_async_commit();
+      cp_async_wait_group1();
+    } else {
+      bring(kb, 0);
     }
     __syncthreads();
     float s[RI][2] = {};
 #pragma unroll 4
     for (int d = 0; d < DP; d += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(&sm.k[tx][d]);
-      const float4 y = *reinterpret_cast<const float4*>(&sm.k[tx + 16][d]);
+      const float4 x = *reinterpret_cast<const float4*>(&sm.k[buf][tx][d]);
+      const float4 y = *reinterpret_cast<const float4*>(&sm.k[buf][tx + 16][d]);
 #pragma unroll
       for (int i = 0; i < RI; ++i) {
         const float4 q = *reinterpret_cast<const float4*>(&sm.q[ty + 16 * i][d]);
@@ -150,25 +181,40 @@ __global__ void __launch_bounds__(kThreads) general_kernel(AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][c][e] *= f;
     }
-#pragma unroll 4
-    for (int j = 0; j < kKeys; ++j) {
-      float4 v[CI];
+    // four keys at a time, so that a row's weights come in one load
+    const auto add_values = [&](auto skip_zeros) {
+#pragma unroll 2
+      for (int j0 = 0; j0 < kKeys; j0 += 4) {
+        float4 w4[RI];
 #pragma unroll
-      for (int c = 0; c < CI; ++c) v[c] = *reinterpret_cast<const float4*>(&sm.v[j][4 * tx + 64 * c]);
+        for (int i = 0; i < RI; ++i) w4[i] = *reinterpret_cast<const float4*>(&sm.p[ty + 16 * i][j0]);
 #pragma unroll
-      for (int i = 0; i < RI; ++i) {
-        const float w = sm.p[ty + 16 * i][j];
-        // a weight of zero adds nothing, whatever the value at a key that the row does not see
-        if (masked && w == 0.0f) continue;
+        for (int jj = 0; jj < 4; ++jj) {
+          float4 v[CI];
 #pragma unroll
-        for (int c = 0; c < CI; ++c) {
-          acc[i][c][0] = fmaf(w, v[c].x, acc[i][c][0]);
-          acc[i][c][1] = fmaf(w, v[c].y, acc[i][c][1]);
-          acc[i][c][2] = fmaf(w, v[c].z, acc[i][c][2]);
-          acc[i][c][3] = fmaf(w, v[c].w, acc[i][c][3]);
+          for (int c = 0; c < CI; ++c) v[c] = *reinterpret_cast<const float4*>(&sm.v[buf][j0 + jj][4 * tx + 64 * c]);
+#pragma unroll
+          for (int i = 0; i < RI; ++i) {
+            const float w = jj == 0 ? w4[i].x : jj == 1 ? w4[i].y : jj == 2 ? w4[i].z : w4[i].w;
+            if (decltype(skip_zeros)::value && w == 0.0f) continue;
+#pragma unroll
+            for (int c = 0; c < CI; ++c) {
+              acc[i][c][0] = fmaf(w, v[c].x, acc[i][c][0]);
+              acc[i][c][1] = fmaf(w, v[c].y, acc[i][c][1]);
+              acc[i][c][2] = fmaf(w, v[c].z, acc[i][c][2]);
+              acc[i][c][3] = fmaf(w, v[c].w, acc[i][c][3]);
+            }
+          }
         }
       }
+    };
+    // a weight of zero adds nothing, whatever the value at a key that the row does not see
+    if (masked) {
+      add_values(std::true_type());
+    } else {
+      add_values(std::false_type());
     }
+    if (ASYNC) buf ^= 1;
   }
   __syncthreads();
 #pragma unroll
@@ -373,7 +419,7 @@ Plan plan_of(const hc_paged_attention_t& a, bool aligned, int num_sms) {
     return a.window > 0 ? std::min<int64_t>(max_kv, a.window + span) : max_kv;
   };
   set_splits(&p.small, a, keys_of(p.small.rows), a.seqs, num_sms, 8, 64);
-  set_splits(&p.large, a, keys_of(p.large.rows), std::max<int64_t>(1, a.tokens * group / 64), num_sms, 2, 256);
+  set_splits(&p.large, a, keys_of(p.large.rows), std::max<int64_t>(1, a.tokens * group / 64), num_sms, 4, 128);
   p.splits = std::max(p.small.splits, p.use_large ? p.large.splits : 1);
   return p;
 }
@@ -410,21 +456,30 @@ AttnArgs args_of(const hc_paged_attention_t& a) {
   return d;
 }
 
-template <typename T, int ROWS, int DP>
-cudaError_t general_t(const AttnArgs& d, int64_t slots, cudaStream_t s) {
-  constexpr size_t smem = sizeof(GeneralSmem<ROWS, DP>);
-  const cudaError_t e = ensure_smem<general_kernel<T, ROWS, DP>>(smem);
+template <typename T, int ROWS, int DP, bool ASYNC>
+cudaError_t general_a(const AttnArgs& d, int64_t slots, cudaStream_t s) {
+  constexpr size_t smem = sizeof(GeneralSmem<ROWS, DP, ASYNC ? 2 : 1>);
+  const cudaError_t e = ensure_smem<general_kernel<T, ROWS, DP, ASYNC>>(smem);
   if (e != cudaSuccess) return e;
-  general_kernel<T, ROWS, DP>
+  general_kernel<T, ROWS, DP, ASYNC>
       <<<dim3(static_cast<unsigned>(slots), d.kv_heads, d.g.splits), kThreads, smem, s>>>(d);
   return cudaGetLastError();
 }
 
+// float32 needs no conversion on its way in, so aligned rows come asynchronously.
+template <typename T, int ROWS, int DP>
+cudaError_t general_t(const AttnArgs& d, bool aligned, int64_t slots, cudaStream_t s) {
+  if constexpr (std::is_same<T, float>::value) {
+    if (aligned && d.dim % 4 == 0) return general_a<T, ROWS, DP, true>(d, slots, s);
+  }
+  return general_a<T, ROWS, DP, false>(d, slots, s);
+}
+
 template <typename T, int ROWS>
-cudaError_t general_d(const AttnArgs& d, int64_t slots, cudaStream_t s) {
-  if (d.dim <= 64) return general_t<T, ROWS, 64>(d, slots, s);
-  if (d.dim <= 128) return general_t<T, ROWS, 128>(d, slots, s);
-  return general_t<T, ROWS, 256>(d, slots, s);
+cudaError_t general_d(const AttnArgs& d, bool aligned, int64_t slots, cudaStream_t s) {
+  if (d.dim <= 64) return general_t<T, ROWS, 64>(d, aligned, slots, s);
+  if (d.dim <= 128) return general_t<T, ROWS, 128>(d, aligned, slots, s);
+  return general_t<T, ROWS, 256>(d, aligned, slots, s);
 }
 
 template <typename T>
@@ -437,23 +492,26 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
     d.part_o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + align_up(rows * 8, 256));
   }
   if (p.tile) return launch_attn_tile(d, a.dtype, a.workspace, num_sms, s);
-  const int64_t slots = slots_of(a, p.small.rows);
+  // (where longer sequences go to the large tiles, a sequence's one small tile is the slot of its number)
+  const int64_t slots = p.use_large ? a.seqs : slots_of(a, p.small.rows);
   d.g = p.small;
   d.min_rows = 1;
   d.max_rows = p.use_large ? kSmallRows : INT64_MAX;
-  cudaError_t e = p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s) : general_d<T, kSmallRows>(d, slots, s);
+  d.slot_is_seq = p.use_large;
+  cudaError_t e = p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s) : general_d<T, kSmallRows>(d, aligned, slots, s);
   if (e != cudaSuccess) return e;
   if (p.use_large) {
     d.g = p.large;
+    d.slot_is_seq = false;
     d.min_rows = kSmallRows + 1;
     d.max_rows = INT64_MAX;
-    e = general_d<T, 64>(d, slots_of(a, p.large.rows), s);
+    e = general_d<T, 64>(d, aligned, slots_of(a, p.large.rows), s);
     if (e != cudaSuccess) return e;
   }
   const int64_t small_rows = p.use_large ? kSmallRows : INT64_MAX;
   if (p.splits > 1) {
     const int64_t rows = a.tokens * a.heads;
-    if (p.splits > 8 && rows < 16384) {
+    if (p.splits > 8 && rows < 4096) {
       e = launch_pdl(combine_kernel<T, 8>, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, s, 1, d, p.small,
                      small_rows, p.large);
     } else {

@@ -42,6 +42,7 @@ struct AttnArgs {
   float scale, softcap;
   AttnGeometry g;
   int64_t min_rows, max_rows;  // only sequences with that many rows (q_len * group)
+  bool slot_is_seq;            // slot s is the first tile of sequence s
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -93,8 +94,8 @@ __device__ __forceinline__ void tile_at(const AttnArgs& a, const AttnGeometry& g
 // The tile of a slot, found by a full warp; rows == 0 if the slot is not used.
 __device__ __forceinline__ void tile_of_slot(const AttnArgs& a, int64_t slot, AttnTile* t) {
   const auto start = [&](int s) { return first_row(a.b, s) * a.group / a.g.rows + s; };
-  const int s = warp_last_le(a.b.seqs, slot, start);
-  const int64_t index = slot - start(s);
+  const int s = a.slot_is_seq ? static_cast<int>(slot) : warp_last_le(a.b.seqs, slot, start);
+  const int64_t index = a.slot_is_seq ? 0 : slot - start(s);
   tile_at(a, a.g, s, index < 0 ? 0 : index, t);
   const int64_t all = (first_row(a.b, s + 1) - t->token0) * a.group;
   if (all < a.min_rows || all > a.max_rows) t->rows = 0;
