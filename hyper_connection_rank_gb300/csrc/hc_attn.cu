@@ -365,6 +365,7 @@ struct Plan {
   AttnGeometry small, large;
   bool use_large;      // sequences of more than kSmallRows rows go to the large tiles
   bool rows_kernel;    // small tiles by hc_attn_rows.cu
+  bool f32_kernel;     // both by hc_attn_f32.cu
   int splits;          // the larger of the two
 };
 
@@ -411,6 +412,7 @@ Plan plan_of(const hc_paged_attention_t& a, bool aligned, int num_sms) {
   p.tile = !few && fast && attn_tile_supported(a.dtype, a.head_dim, a.page_size, a.scale, aligned);
   if (p.tile) return p;
   p.rows_kernel = fast && attn_rows_supported(a.dtype, a.head_dim, aligned);
+  p.f32_kernel = fast && attn_f32_supported(a.dtype, a.head_dim, aligned);
   p.use_large = !few;
   p.small = AttnGeometry{kSmallRows, kKeys, 0, 0};
   p.large = AttnGeometry{64, kKeys, 0, 0};
@@ -498,14 +500,17 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
   d.min_rows = 1;
   d.max_rows = p.use_large ? kSmallRows : INT64_MAX;
   d.slot_is_seq = p.use_large;
-  cudaError_t e = p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s) : general_d<T, kSmallRows>(d, aligned, slots, s);
+  cudaError_t e = p.f32_kernel    ? launch_attn_f32(d, slots, s)
+                  : p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s)
+                                  : general_d<T, kSmallRows>(d, aligned, slots, s);
   if (e != cudaSuccess) return e;
   if (p.use_large) {
     d.g = p.large;
     d.slot_is_seq = false;
     d.min_rows = kSmallRows + 1;
     d.max_rows = INT64_MAX;
-    e = general_d<T, 64>(d, aligned, slots_of(a, p.large.rows), s);
+    const int64_t large_slots = slots_of(a, p.large.rows);
+    e = p.f32_kernel ? launch_attn_f32(d, large_slots, s) : general_d<T, 64>(d, aligned, large_slots, s);
     if (e != cudaSuccess) return e;
   }
   const int64_t small_rows = p.use_large ? kSmallRows : INT64_MAX;

@@ -11,6 +11,10 @@ namespace hc {
 bool attn_rows_supported(int dtype, int dim, bool aligned);
 cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, int64_t slots, cudaStream_t s);
 
+// float32 (hc_attn_f32.cu), tiles of 16 or 64 rows by a.g.rows.
+bool attn_f32_supported(int dtype, int dim, bool aligned);
+cudaError_t launch_attn_f32(const AttnArgs& a, int64_t slots, cudaStream_t s);
+
 // Any number of rows, on tcgen05 (hc_attn_tile.cu); takes a workspace of its
 // own and needs no splits.
 bool attn_tile_supported(int dtype, int dim, int page, float scale, bool aligned);
