@@ -272,7 +272,11 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(AttnArgs a, AttnGeome
     }
   };
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group;
-  if (row >= a.tokens * a.heads) return;
+  // (every thread waits for the kernels before, whatever it finds: later kernels on the stream count on this one's end alone)
+  if (row >= a.tokens * a.heads) {
+    pdl_wait();
+    return;
+  }
   const int64_t token = row / a.heads;
   const int head = static_cast<int>(row - token * a.heads);
   const int s = a.b.cu_q ? warp_last_le(a.b.seqs, token, [&](int i) { return first_row(a.b, i); })
@@ -281,8 +285,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(AttnArgs a, AttnGeome
   const AttnGeometry& g = all <= small_rows ? small : large;
   AttnTile t;
   tile_at(a, g, s, ((token - first) * a.group + head % a.group) / g.rows, &t);
-  if (t.rows == 0 || t.splits == 1) return;
   pdl_wait();  // (the lengths and tables are the caller's; only the partial results are the kernels' before)
+  if (t.rows == 0 || t.splits == 1) return;
   const int64_t step = a.tokens * a.heads;  // from one split to the next
   const float2* ml = a.part_ml + row;
   float top = neg_inf();
@@ -365,6 +369,7 @@ struct Plan {
   AttnGeometry small, large;
   bool use_large;      // sequences of more than kSmallRows rows go to the large tiles
   bool rows_kernel;    // small tiles by hc_attn_rows.cu
+  RowsSchedule pieces; // which splits single-token sequences itself; units 0: the splits below
   bool f32_kernel;     // both by hc_attn_f32.cu
   int splits;          // the larger of the two
 };
@@ -386,7 +391,7 @@ void set_splits(AttnGeometry* g, const hc_paged_attention_t& a, int64_t keys, in
   int64_t len = std::max<int64_t>(shortest, ceil_div(keys, want));
   len = ceil_div(len, g->align) * g->align;
   g->split_len = static_cast<int>(std::min<int64_t>(len, int64_t{1} << 30));
-  g->splits = static_cast<int>(std::max<int64_t>(1, ceil_div(keys + g->align, g->split_len)));
+  g->splits = static_cast<int>(std::max<int64_t>(1, ceil_div(keys + (a.window > 0 ? g->align : 0), g->split_len)));
   if (g->splits > kMaxSplits) {
     g->splits = kMaxSplits;
     g->split_len =
@@ -420,15 +425,27 @@ Plan plan_of(const hc_paged_attention_t& a, bool aligned, int num_sms) {
     const int64_t span = ceil_div(rows, group) + 1;
     return a.window > 0 ? std::min<int64_t>(max_kv, a.window + span) : max_kv;
   };
-  set_splits(&p.small, a, keys_of(p.small.rows), a.seqs, num_sms, 8, 64);
+  if (p.rows_kernel && a.cu_q == nullptr)
+    p.pieces = attn_rows_schedule(a.seqs, a.kv_heads, keys_of(p.small.rows), num_sms);
+  if (p.pieces.units > 0) {
+    p.small.split_len = 1 << 30;
+    p.small.splits = 1;
+    return p;
+  }
+  set_splits(&p.small, a, keys_of(p.small.rows), a.seqs, num_sms, 8, 128);
   set_splits(&p.large, a, keys_of(p.large.rows), std::max<int64_t>(1, a.tokens * group / 64), num_sms, 4, 128);
   p.splits = std::max(p.small.splits, p.use_large ? p.large.splits : 1);
   return p;
 }
 
+// Rows of partial results.
+size_t part_rows(const hc_paged_attention_t& a, const Plan& p) {
+  if (p.pieces.units > 0) return static_cast<size_t>(p.pieces.units) * a.kv_heads * kSmallRows;
+  return p.splits <= 1 ? 0 : static_cast<size_t>(p.splits) * a.tokens * a.heads;
+}
+
 size_t part_bytes(const hc_paged_attention_t& a, const Plan& p) {
-  if (p.splits <= 1) return 0;
-  const size_t rows = static_cast<size_t>(p.splits) * a.tokens * a.heads;
+  const size_t rows = part_rows(a, p);
   return align_up(rows * 8, 256) + align_up(rows * a.head_dim * 4, 256);
 }
 
@@ -488,8 +505,7 @@ template <typename T>
 cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, cudaStream_t s) {
   const Plan p = plan_of(a, aligned, num_sms);
   AttnArgs d = args_of(a);
-  if (p.splits > 1) {
-    const size_t rows = static_cast<size_t>(p.splits) * a.tokens * a.heads;
+  if (const size_t rows = part_rows(a, p)) {
     d.part_ml = static_cast<float2*>(a.workspace);
     d.part_o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + align_up(rows * 8, 256));
   }
@@ -500,6 +516,8 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
   d.min_rows = 1;
   d.max_rows = p.use_large ? kSmallRows : INT64_MAX;
   d.slot_is_seq = p.use_large;
+  d.spare_ctas = p.pieces.spare_ctas;
+  d.units = p.pieces.units;
   cudaError_t e = p.f32_kernel    ? launch_attn_f32(d, slots, s)
                   : p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s)
                                   : general_d<T, kSmallRows>(d, aligned, slots, s);

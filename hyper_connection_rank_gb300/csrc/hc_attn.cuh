@@ -24,7 +24,7 @@ namespace hc {
 
 struct AttnGeometry {
   int rows;       // rows of a tile
-  int align;      // a tile's first key is a multiple of it
+  int align;      // a tile's first key is a multiple of it (a power of two)
   int split_len;  // keys of a split, a multiple of align
   int splits;     // splits of the grid; the last one takes what is left
 };
@@ -43,6 +43,9 @@ struct AttnArgs {
   AttnGeometry g;
   int64_t min_rows, max_rows;  // only sequences with that many rows (q_len * group)
   bool slot_is_seq;            // slot s is the first tile of sequence s
+  // hc_attn_rows.cu, where it splits single-token sequences itself: CTAs that there may be beside one for each tile, and pieces at
+  // most (0: the splits above)
+  int spare_ctas, units;
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -67,8 +70,13 @@ struct AttnTile {
   int splits;       // splits with keys; at least 1
 };
 
+// a / b for a >= 0, in 32 bits where a has no more (a 64-bit division is a hundred instructions).
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return (a >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 __device__ __forceinline__ int64_t row_position(const AttnTile& t, int64_t row, int group) {
-  return t.pos0 + row / group;
+  return t.pos0 + quotient(row, group);
 }
 
 // Fills in a tile of sequence s, `index` tiles into it.
@@ -86,14 +94,14 @@ __device__ __forceinline__ void tile_at(const AttnArgs& a, const AttnGeometry& g
   t->hi = p_last + 1 < 0 ? 0 : p_last + 1;
   t->lo = a.window > 0 && p_first - a.window + 1 > 0 ? p_first - a.window + 1 : 0;
   if (t->lo > t->hi) t->lo = t->hi;
-  t->base = t->lo / g.align * g.align;
-  const int64_t want = (t->hi - t->base + g.split_len - 1) / g.split_len;
+  t->base = t->lo & -static_cast<int64_t>(g.align);
+  const int64_t want = quotient(t->hi - t->base + g.split_len - 1, g.split_len);
   t->splits = want < 1 ? 1 : want < g.splits ? static_cast<int>(want) : g.splits;
 }
 
 // The tile of a slot, found by a full warp; rows == 0 if the slot is not used.
 __device__ __forceinline__ void tile_of_slot(const AttnArgs& a, int64_t slot, AttnTile* t) {
-  const auto start = [&](int s) { return first_row(a.b, s) * a.group / a.g.rows + s; };
+  const auto start = [&](int s) { return quotient(first_row(a.b, s) * a.group, a.g.rows) + s; };
   const int s = a.slot_is_seq ? static_cast<int>(slot) : warp_last_le(a.b.seqs, slot, start);
   const int64_t index = a.slot_is_seq ? 0 : slot - start(s);
   tile_at(a, a.g, s, index < 0 ? 0 : index, t);
@@ -111,7 +119,7 @@ __device__ __forceinline__ void split_range(const AttnGeometry& g, const AttnTil
 __device__ __forceinline__ void row_owner(const AttnArgs& a, const AttnTile& t, int kv_head, int r, int64_t* token,
                                           int* head) {
   const int64_t row = t.row0 + r;
-  const int64_t i = row / a.group;
+  const int64_t i = quotient(row, a.group);
   *token = t.token0 + i;
   *head = kv_head * a.group + static_cast<int>(row - i * a.group);
 }

@@ -9,6 +9,13 @@ namespace hc {
 // Up to 16 rows to a key head (hc_attn_rows.cu). `aligned`: 16-byte accesses
 // are possible everywhere.
 bool attn_rows_supported(int dtype, int dim, bool aligned);
+// Its own split of sequences of one new token: CTAs beside one for each tile, and
+// pieces (of all sequences) at most; none where splits by the host are as good.
+// `keys`: the longest sequence's.
+struct RowsSchedule {
+  int spare_ctas, units;
+};
+RowsSchedule attn_rows_schedule(int64_t seqs, int kv_heads, int64_t keys, int num_sms);
 cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, int64_t slots, cudaStream_t s);
 
 // float32 (hc_attn_f32.cu), tiles of 16 or 64 rows by a.g.rows.

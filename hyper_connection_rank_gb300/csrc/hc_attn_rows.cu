@@ -13,6 +13,18 @@
 // tcgen05 tile would be seven eighths empty and its tensor-memory round trips
 // would lie on the path of every block.
 //
+// Work: where every sequence has one new token (no cu_q) and there are too few of
+// them to fill half the GPU, the kernel splits them itself, by their lengths: with
+// T CTAs, two for each SM, all that run at once, and as many extra pieces as
+// rounding up may make, all are cut into pieces of
+//   L = sum of keys * kv_heads / (T - seqs * kv_heads)
+// keys, so that they fill the GPU once, evenly, whatever the lengths are. Every
+// warp works that out for itself from kv_lens, 32 sequences at a time. (Against
+// pieces that the host chose by the longest: two contexts of 130002 and 34402
+// tokens, 8 key heads, 121 -> 112 us; one of 30002, 4 key heads, 35 -> 21 us;
+// eight of up to 4002, 25 -> 17 us. With more sequences the host's splits are
+// as good, and 64 contexts of up to 8192 take 231 us where these took 240.)
+//
 // Mathematics: the running maximum and sum of a softmax, held per warp, with the
 // sums of values in registers; they are rescaled only when a block raises the
 // maximum. The warps' results are joined once at the end:
@@ -28,6 +40,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kBlock = 16;  // keys of a block
 constexpr int kStages = 3;
+constexpr int kShortest = 128;  // keys that are worth a piece
+constexpr int kMaxPieces = 512; // of a sequence
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float x, float y);
@@ -50,7 +64,77 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return static_cast<uint32_t>(r * (D * 2) + ((c ^ (r & 7)) << 4));
 }
 
-template <typename T, int D>
+// Pieces of a batch of single tokens, one tile to a sequence.
+struct Pieces {
+  int len;          // keys of a piece
+  int s, z;         // sequence and piece of the unit asked for; s = -1: there is no such unit
+  int unit0, count; // the sequence's first unit, and its pieces
+};
+
+// Keys of a sequence's one tile, from its first block on (as tile_at has them).
+__device__ __forceinline__ int64_t keys_of(const AttnArgs& a, int s) {
+  const int64_t n = kv_len_of(a.b, s), lo = a.window > 0 && n > a.window ? n - a.window : 0;
+  return n - (lo & -static_cast<int64_t>(a.g.align));
+}
+__device__ __forceinline__ int pieces_of(int64_t keys, int len) {
+  return keys <= len ? 1 : static_cast<int>(quotient(keys + len - 1, len));
+}
+
+// Place of row r of a unit among the partial results.
+__device__ __forceinline__ int64_t piece_row(const AttnArgs& a, int kvh, int unit, int r) {
+  return (static_cast<int64_t>(kvh) * a.units + unit) * 16 + r;
+}
+
+// By a full warp: the piece that is unit `unit`, or with `seq` >= 0 the units of that sequence.
+__device__ __forceinline__ Pieces find_pieces(const AttnArgs& a, int unit, int seq) {
+  const int lane = threadIdx.x & 31, seqs = a.b.seqs;
+  const int64_t early = lane < seqs ? keys_of(a, lane) : 0;  // of the first 32 sequences
+  int64_t total = early, most = early;
+  for (int s = lane + 32; s < seqs; s += 32) {
+    const int64_t k = keys_of(a, s);
+    total += k;
+    most = k > most ? k : most;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    const int64_t other = __shfl_xor_sync(0xffffffffu, most, o);
+    most = other > most ? other : most;
+  }
+  Pieces p;
+  int64_t len = quotient(total * a.kv_heads + a.spare_ctas - 1, a.spare_ctas);
+  const int64_t least = (most + kMaxPieces - 1) / kMaxPieces;
+  len = len < kShortest ? kShortest : len;
+  len = len < least ? least : len;
+  // (2^30 keys to a piece are more than the memory of a GPU holds)
+  p.len = static_cast<int>(len < (1 << 30) ? (len + kBlock - 1) / kBlock * kBlock : 1 << 30);
+  int before = 0;
+  p.s = -1;
+  for (int s0 = 0; s0 < seqs; s0 += 32) {
+    const int n = s0 + lane < seqs ? pieces_of(s0 == 0 ? early : keys_of(a, s0 + lane), p.len) : 0;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int first = before + x - n;
+    const unsigned hit = __ballot_sync(0xffffffffu, seq >= 0 ? s0 + lane == seq : unit >= first && unit < first + n);
+    if (hit != 0) {
+      const int at = __ffs(hit) - 1;
+      p.s = s0 + at;
+      p.unit0 = __shfl_sync(0xffffffffu, first, at);
+      p.count = __shfl_sync(0xffffffffu, n, at);
+      p.z = unit - p.unit0;
+      return p;
+    }
+    before += __shfl_sync(0xffffffffu, x, 31);
+  }
+  return p;
+}
+
+// PIECES: units of single-token sequences along x; else slots along x and splits along z.
+template <typename T, int D, bool PIECES>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
   constexpr int kChunks = D / 8;                 // 16-byte chunks of a row
   constexpr int kHalf = kBlock * D * 2;          // bytes of a block's keys
@@ -60,13 +144,24 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ float s_m[kWarps][16], s_l[kWarps][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
-  const int z = blockIdx.z, kvh = blockIdx.y;
+  const int kvh = blockIdx.y;
+  int z = blockIdx.z;
   pdl_trigger();
   AttnTile t;
-  tile_of_slot(a, blockIdx.x, &t);
-  if (t.rows == 0 || z >= t.splits) return;
   int64_t k0, k1;
-  split_range(a.g, t, z, &k0, &k1);
+  if (PIECES) {
+    const Pieces p = find_pieces(a, blockIdx.x, -1);
+    if (p.s < 0) return;
+    tile_at(a, a.g, p.s, 0, &t);
+    t.splits = p.count;
+    z = p.z;
+    k0 = t.base + static_cast<int64_t>(z) * p.len;
+    k1 = z == p.count - 1 ? t.hi : k0 + p.len;
+  } else {
+    tile_of_slot(a, blockIdx.x, &t);
+    if (t.rows == 0 || z >= t.splits) return;
+    split_range(a.g, t, z, &k0, &k1);
+  }
   const T* kp = static_cast<const T*>(a.k) + kvh * a.c_hs;
   const T* vp = static_cast<const T*>(a.v) + kvh * a.c_hs;
   const int blocks = k1 > k0 ? static_cast<int>((k1 - k0 + kBlock - 1) / kBlock) : 0;
@@ -279,7 +374,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
     int head;
     row_owner(a, t, kvh, r, &token, &head);
     if (t.splits > 1) {
-      const int64_t at = part_index(a, z, token, head);
+      const int64_t at = PIECES ? piece_row(a, kvh, blockIdx.x, r) : part_index(a, z, token, head);
       *reinterpret_cast<float4*>(a.part_o + at * D + d) = x;
       if (d == 0) a.part_ml[at] = make_float2(top, sum);
     } else {
@@ -294,14 +389,81 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
   }
 }
 
+// Joins the pieces of every sequence that has more than one (as combine_kernel of
+// hc_attn.cu does splits), a CTA to a row: all weights first, then each warp
+// adds every eighth piece. The pieces are worked out while the other kernel still
+// runs.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) rows_join_kernel(AttnArgs a) {
+  __shared__ float s_w[kMaxPieces];
+  __shared__ float s_red[8][2];
+  __shared__ float s_o[8][D];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, s = blockIdx.x, head = blockIdx.y;
+  const int kvh = head / a.group, r = head - kvh * a.group;
+  const Pieces p = find_pieces(a, 0, s);
+  pdl_wait();  // (in every thread, whatever it finds: later kernels on the stream count on this one's end alone)
+  if (p.count == 1) return;
+  const int64_t first = piece_row(a, kvh, p.unit0, r);  // the next piece's row is 16 on
+  float top = neg_inf(), sum = 0.0f;
+  for (int i = tid; i < p.count; i += 256) top = fmaxf(top, a.part_ml[first + i * 16].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s_red[warp][0] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, s_red[w][0]);
+  for (int i = tid; i < p.count; i += 256) {
+    const float2 ml = a.part_ml[first + i * 16];
+    const float w = ml.x == neg_inf() ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - top);  // (NaN scores alone: m = -inf, l = NaN)
+    s_w[i] = w;
+    sum += ml.y * w;
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) s_red[warp][1] = sum;
+  __syncthreads();
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) sum += s_red[w][1];
+  if (lane < D / 4) {
+    const float* src = a.part_o + first * D + lane * 4;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = warp; i < p.count; i += 8) {
+      const float4 y = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * 16 * D);
+      const float w = s_w[i];
+      x.x = fmaf(y.x, w, x.x);
+      x.y = fmaf(y.y, w, x.y);
+      x.z = fmaf(y.z, w, x.z);
+      x.w = fmaf(y.w, w, x.w);
+    }
+    *reinterpret_cast<float4*>(&s_o[warp][lane * 4]) = x;
+  }
+  __syncthreads();
+  if (tid < D) {
+    float x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) x += s_o[w][tid];
+    stf(static_cast<T*>(a.out) + s * a.o_ts + head * a.o_hs + tid, sum == 0.0f ? 0.0f : x / sum);
+  }
+  if (tid == 0 && a.lse) a.lse[static_cast<int64_t>(s) * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+}
+
 template <typename T, int D>
 cudaError_t launch_t(const AttnArgs& a, int64_t slots, cudaStream_t s) {
   constexpr size_t ring = static_cast<size_t>(kWarps) * kStages * kBlock * D * 4;
   constexpr size_t sums = static_cast<size_t>(kWarps) * 16 * (D + 8) * 4;
   constexpr size_t smem = ring > sums ? ring : sums;
-  const cudaError_t e = ensure_smem<rows_kernel<T, D>>(smem);
+  if (a.units > 0) {
+    const cudaError_t e = ensure_smem<rows_kernel<T, D, true>>(smem);
+    if (e != cudaSuccess) return e;
+    rows_kernel<T, D, true><<<dim3(a.units, a.kv_heads), kWarps * 32, smem, s>>>(a);
+    const cudaError_t e2 = cudaGetLastError();
+    if (e2 != cudaSuccess) return e2;
+    return launch_pdl(rows_join_kernel<T, D>, dim3(a.b.seqs, a.heads), dim3(256), 0, s, 1, a);
+  }
+  const cudaError_t e = ensure_smem<rows_kernel<T, D, false>>(smem);
   if (e != cudaSuccess) return e;
-  rows_kernel<T, D><<<dim3(static_cast<unsigned>(slots), a.kv_heads, a.g.splits), kWarps * 32, smem, s>>>(a);
+  rows_kernel<T, D, false><<<dim3(static_cast<unsigned>(slots), a.kv_heads, a.g.splits), kWarps * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -309,6 +471,12 @@ cudaError_t launch_t(const AttnArgs& a, int64_t slots, cudaStream_t s) {
 
 bool attn_rows_supported(int dtype, int dim, bool aligned) {
   return aligned && (dtype == HC_F16 || dtype == HC_BF16) && (dim == 64 || dim == 128);
+}
+
+RowsSchedule attn_rows_schedule(int64_t seqs, int kv_heads, int64_t keys, int num_sms) {
+  const int64_t tiles = seqs * kv_heads, wave = 2 * static_cast<int64_t>(num_sms);
+  if (keys <= kShortest || tiles * 2 > wave) return RowsSchedule{0, 0};
+  return RowsSchedule{static_cast<int>(wave - tiles), static_cast<int>((wave - tiles) / kv_heads + seqs)};
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, int64_t slots, cudaStream_t s) {

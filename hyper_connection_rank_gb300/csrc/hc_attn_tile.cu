@@ -48,7 +48,7 @@ constexpr int kRows = 128;        // rows of a tile, an MMA's M
 constexpr int kPair = 2 * kRows;  // rows of a CTA's two tiles
 constexpr int kKeys = 128;        // keys of a block, N of the first product
 constexpr int kThreads = 384;     // two softmax warpgroups, and one of the other warps
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10, kPlanWarp = 11;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10;  // (and 11 plans)
 constexpr int kSegs = 4;          // segments at hand
 constexpr int kSegUsers = 11;     // warps that read them
 constexpr int kTileCost = 4;      // what a tile costs beside its key blocks (queries in, results out), in blocks
@@ -877,20 +877,19 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a, Work w) {
   __shared__ float s_w[kJoinRows][kMaxCtas + 1];
   const Run run(w, a.kv_heads);
   const int c0 = blockIdx.x;
-  if (c0 + 1 >= run.ctas) return;
-  const int64_t u = run.start(c0 + 1);
-  Segment g;
-  segment_at(w, run, u, run.all, &g);
-  if (g.j0 == 0 || run.start(c0) > g.at) return;
+  Segment g = {};
+  int pieces = 0;
+  if (c0 + 1 < run.ctas) {
+    segment_at(w, run, run.start(c0 + 1), run.all, &g);
+    if (g.j0 > 0 && run.start(c0) <= g.at)
+      for (pieces = 1; c0 + pieces < run.ctas && run.start(c0 + pieces) < g.at + g.n;) ++pieces;
+  }
   const int row0 = blockIdx.y * kJoinRows;
   const int rows = min(g.t.rows - row0, kJoinRows);
-  if (rows <= 0) return;
-  const int64_t end = g.at + g.n;
-  int pieces = 1;
-  while (c0 + pieces < run.ctas && run.start(c0 + pieces) < end) ++pieces;
   // piece 0 is the last of its CTA's segments, the others are the first of theirs
   const auto index = [&](int i, int r) { return (2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0)) * kPair + row0 + r; };
-  pdl_wait();
+  pdl_wait();  // (in every thread, whatever it found: later kernels on the stream count on this one's end alone)
+  if (pieces == 0 || rows <= 0) return;
   {
     const int r = threadIdx.x >> 3, e = threadIdx.x & 7;
     float top = neg_inf(), sum = 0.0f;
