@@ -370,7 +370,7 @@ struct Plan {
   bool use_large;      // sequences of more than kSmallRows rows go to the large tiles
   bool rows_kernel;    // small tiles by hc_attn_rows.cu
   RowsSchedule pieces; // which splits single-token sequences itself; units 0: the splits below
-  bool f32_kernel;     // both by hc_attn_f32.cu
+  bool f32_kernel;     // large tiles by hc_attn_f32.cu
   int splits;          // the larger of the two
 };
 
@@ -416,7 +416,7 @@ Plan plan_of(const hc_paged_attention_t& a, bool aligned, int num_sms) {
   p.splits = 1;
   p.tile = !few && fast && attn_tile_supported(a.dtype, a.head_dim, a.page_size, a.scale, aligned);
   if (p.tile) return p;
-  p.rows_kernel = fast && attn_rows_supported(a.dtype, a.head_dim, aligned);
+  p.rows_kernel = fast && attn_rows_supported(a.dtype, a.head_dim, a.cu_q == nullptr, static_cast<int>(group), aligned);
   p.f32_kernel = fast && attn_f32_supported(a.dtype, a.head_dim, aligned);
   p.use_large = !few;
   p.small = AttnGeometry{kSmallRows, kKeys, 0, 0};
@@ -425,7 +425,7 @@ Plan plan_of(const hc_paged_attention_t& a, bool aligned, int num_sms) {
     const int64_t span = ceil_div(rows, group) + 1;
     return a.window > 0 ? std::min<int64_t>(max_kv, a.window + span) : max_kv;
   };
-  if (p.rows_kernel && a.cu_q == nullptr)
+  if (p.rows_kernel && few && a.cu_q == nullptr)
     p.pieces = attn_rows_schedule(a.seqs, a.kv_heads, keys_of(p.small.rows), num_sms);
   if (p.pieces.units > 0) {
     p.small.split_len = 1 << 30;
@@ -518,9 +518,7 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
   d.slot_is_seq = p.use_large;
   d.spare_ctas = p.pieces.spare_ctas;
   d.units = p.pieces.units;
-  cudaError_t e = p.f32_kernel    ? launch_attn_f32(d, slots, s)
-                  : p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s)
-                                  : general_d<T, kSmallRows>(d, aligned, slots, s);
+  cudaError_t e = p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s) : general_d<T, kSmallRows>(d, aligned, slots, s);
   if (e != cudaSuccess) return e;
   if (p.use_large) {
     d.g = p.large;

@@ -1,32 +1,30 @@
-// Attention over a paged cache in float32 (heads of 64 or 128, aligned rows), on
-// the tensor cores at float32's precision.
+// Attention over a paged cache in float32 for many rows (heads of 64 or 128,
+// aligned rows), on the tensor cores at float32's precision.
 //
-// Mathematics: a float32 x is cut into parts of fewer bits that sum to it
-// exactly, and a product into the MMAs of its parts that matter, with fp32
-// accumulation:
-//   three bf16 of 8 bits each (tile_kernel), x y = x0 y0 + x0 y1 + x1 y0 +
-//     x1 y1 + x0 y2 + x2 y0, and at most 2^-23 |x y| left out;
-//   a tf32 of 11 bits and the rest, of which the MMA reads 11 bits more
-//     (rows_kernel), x y = hi hi + hi lo + lo hi, and at most 3 * 2^-22 |x y|.
-// Scores, weights and sums of values keep float32's accuracy: what is left out is
-// below the dim * 2^-24 of a sum in float32. Softmax as in hc_attn.cu, with
+// Mathematics: a float32 x is cut into three bf16 of 8 bits each that sum to it
+// exactly, and a product into the MMAs of its parts that matter,
+//   x y = x0 y0 + x0 y1 + x1 y0 + x1 y1 + x0 y2 + x2 y0
+// and at most 2^-23 |x y| left out, with fp32 accumulation. What is left out is below
+// the dim * 2^-24 of a sum in float32. An MMA cuts its sums off rather than rounding
+// them, so a block's values are summed by MMAs from zero and added to the running
+// sums by a rounded addition (sums run through the MMAs were 1.7e-6 off on the case
+// below, these are 5e-7, plain float32 sums 9e-7). Softmax as in hc_attn.cu, with
 // CUDA's accurate exponential and tanh. An infinite key or value takes part in the
 // product of the first parts alone (its rest would be NaN, and so would a zero part
 // times infinity), so each has its first part a second time, zero if infinite,
 // for the corrections.
 //
-// Bound: for many rows the warp-level MMAs (an m16n8k16 takes 8 cycles of a
-// quarter SM, so six for a product make 170 multiply-adds a cycle and SM, where
-// the CUDA cores have 128 and reach a third of that for want of operands);
-// for few rows, bytes.
-//
-// tile_kernel: a tile of 64 rows, 16 to a warp. Blocks of 16 keys go from global
+// Work: a tile of 64 rows, 16 to a warp. Blocks of 16 keys go from global
 // memory to registers, are cut into parts, once for the four warps, and stored
 // in shared memory in the layout that ldmatrix reads without conflicts; while a
 // block is multiplied, the next is cut and the one after is on its way.
-// rows_kernel, for sequences of at most 16 rows: all warps have the same rows, and
-// each its own blocks of keys in a cp.async ring of its own (as in
-// hc_attn_rows.cu); their results are joined at the end.
+//
+// Bound: the warp-level MMAs, of which an m16n8k16 takes 8 cycles of a quarter
+// SM, so that six for a product make 170 multiply-adds a cycle and SM (the CUDA
+// cores have 128, and reached a third of that for want of operands). Three chunks
+// of up to 131 tokens, 20 heads of 128, behind up to 901: XXX us; 1000 tokens
+// behind 2000: 36 TFLOP/s, 40% of the MMAs' rate; the rest is cutting and
+// waiting, with two CTAs of four warps to an SM.
 #include "hc_async.cuh"
 #include "hc_attn.cuh"
 #include "hc_attn_internal.h"
@@ -36,293 +34,6 @@ namespace hc {
 namespace {
 
 constexpr int kWarps = 4;
-
-template <int D>
-struct RowsCfg {
-  // rows lie 4 banks apart, so that the MMA operands' loads (8 rows by 4
-  // neighbours, or 8 neighbours by rows two apart) touch 32 banks
-  static constexpr int kPitch = D + 4;
-  static constexpr int kKeys = 16;  // keys of a block
-  static constexpr int kStages = 3;
-  static constexpr int kRows = 16;
-  static constexpr int kBlock = 2 * kKeys * kPitch;  // floats of a block's keys and values
-  static constexpr int kRing = kWarps * kStages * kBlock;
-  static constexpr int kSums = kWarps * 16 * (D + 8);  // (joined in the ring's place)
-  static constexpr size_t kSmem = static_cast<size_t>(kRows * kPitch + (kRing > kSums ? kRing : kSums)) * 4;
-};
-
-struct Split {
-  uint32_t hi, lo;
-};
-__device__ __forceinline__ Split split(float x) {
-  const uint32_t hi = __float_as_uint(x) & 0xffffe000u;
-  return Split{hi, __float_as_uint(x - __uint_as_float(hi))};
-}
-// The same for keys and values, which may be infinite: such a number takes part in the product of the upper halves alone, for
-// its rest would be NaN, and so would a lower half of zero times infinity. `cor` is the upper half for the correction.
-struct SplitAny {
-  uint32_t hi, cor, lo;
-};
-__device__ __forceinline__ SplitAny split_any(float x) {
-  const uint32_t hi = __float_as_uint(x) & 0xffffe000u;
-  const float lo = x - __uint_as_float(hi);
-  const bool fine = lo == lo;
-  return SplitAny{hi, fine ? hi : 0u, fine ? __float_as_uint(lo) : 0u};
-}
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) f32_rows_kernel(AttnArgs a) {
-  using C = RowsCfg<D>;
-  constexpr int kKeys = C::kKeys, kPitch = C::kPitch, kTiles = kKeys / 8;
-  extern __shared__ __align__(128) float smem[];
-  __shared__ float s_m[kWarps][16], s_l[kWarps][16];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
-  const int z = blockIdx.z, kvh = blockIdx.y;
-  float* const queries = smem;
-  float* const ring = smem + C::kRows * kPitch + warp * C::kStages * C::kBlock;
-  pdl_trigger();
-  AttnTile t;
-  tile_of_slot(a, blockIdx.x, &t);
-  if (t.rows == 0 || z >= t.splits) return;
-  int64_t k0, k1;
-  split_range(a.g, t, z, &k0, &k1);
-  const float* kp = static_cast<const float*>(a.k) + kvh * a.c_hs;
-  const float* vp = static_cast<const float*>(a.v) + kvh * a.c_hs;
-  const int blocks = k1 > k0 ? static_cast<int>((k1 - k0 + kKeys - 1) / kKeys) : 0;
-
-  // Block b into a stage: the lanes take a row's 16-byte pieces side by side; a row that does not exist is zeros.
-  constexpr int kPieces = D / 4, kAtOnce = 32 / kPieces;
-  static_assert(kAtOnce >= 1, "a row at a time at least");
-  const int piece = lane % kPieces, row_of = lane / kPieces;
-  const auto bring = [&](int b, int stage) {
-    if (b >= blocks) return;
-    float* to = ring + stage * C::kBlock;
-#pragma unroll
-    for (int i = 0; i < kKeys / kAtOnce; ++i) {
-      const int r = i * kAtOnce + row_of;
-      const int64_t j = k0 + static_cast<int64_t>(b) * kKeys + r;
-      int64_t at = -1;
-      if (j >= t.lo && j < k1) {
-        const uint32_t e = static_cast<uint32_t>(j) / static_cast<uint32_t>(a.b.page_size);
-        const int page = page_of(a.b, t.s, e);
-        if (page >= 0) at = page * a.c_ps + (static_cast<uint32_t>(j) - e * a.b.page_size) * a.c_ts;
-      }
-      const int64_t off = (at < 0 ? 0 : at) + piece * 4;
-      const uint32_t bytes = at < 0 ? 0 : 16;
-      cp_async16_zfill(smem_addr(to + r * kPitch + piece * 4), kp + off, bytes);
-      cp_async16_zfill(smem_addr(to + (kKeys + r) * kPitch + piece * 4), vp + off, bytes);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) {
-    bring(warp + i * kWarps, i);
-    cp_async_commit();
-  }
-  // queries, rows past the last as zeros
-  for (int r = warp; r < C::kRows; r += kWarps) {
-    const float* src = nullptr;
-    if (r < t.rows) {
-      int64_t token;
-      int head;
-      row_owner(a, t, kvh, r, &token, &head);
-      src = static_cast<const float*>(a.q) + token * a.q_ts + head * a.q_hs;
-    }
-    for (int d = lane; d < D; d += 32) queries[r * kPitch + d] = src ? src[d] : 0.0f;
-  }
-  __syncthreads();
-  const float* const qa = queries + g * kPitch + q4;
-
-  // keys that this thread's two rows see, relative to k0: [from, to)
-  int from[2], to[2], all_from = 0, all_to = 0;
-  const auto rel = [&](int64_t j) {
-    const int64_t d = j - k0, n = k1 - k0;
-    return static_cast<int>(d < 0 ? 0 : d > n ? n : d);
-  };
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = g + 8 * i;
-    const int64_t p = row_position(t, t.row0 + r, a.group);
-    to[i] = r < t.rows ? rel(p + 1) : 0;
-    from[i] = r < t.rows && a.window > 0 ? rel(p - a.window + 1) : 0;
-  }
-  all_to = rel(row_position(t, t.row0, a.group) + 1);  // seen by every row: [all_from, all_to)
-  if (a.window > 0) all_from = rel(row_position(t, t.row0 + t.rows - 1, a.group) - a.window + 1);
-
-  float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.0f, 0.0f};
-  float o[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
-
-  int stage = 0;
-  for (int b = warp; b < blocks; b += kWarps) {
-    cp_async_wait_group<C::kStages - 2>();
-    __syncwarp();
-    bring(b + (C::kStages - 1) * kWarps, stage == 0 ? C::kStages - 1 : stage - 1);
-    cp_async_commit();
-    const float* keys = ring + stage * C::kBlock;
-    const float* values = keys + kKeys * kPitch;
-    stage = stage + 1 == C::kStages ? 0 : stage + 1;
-    float s[kTiles][4] = {}, c[kTiles][4] = {};  // products of the upper halves, and the corrections
-#pragma unroll 4
-    for (int ks = 0; ks < D; ks += 8) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Split x = split(qa[(i & 1) * 8 * kPitch + ks + (i >> 1) * 4]);
-        hi[i] = x.hi;
-        lo[i] = x.lo;
-      }
-#pragma unroll
-      for (int n = 0; n < kTiles; ++n) {
-        const float* kb = keys + (n * 8 + g) * kPitch + ks + q4;
-        const SplitAny x = split_any(kb[0]), y = split_any(kb[4]);
-        mma_tf32(c[n], lo, x.cor, y.cor);
-        mma_tf32(s[n], hi, x.hi, y.hi);
-        mma_tf32(c[n], hi, x.lo, y.lo);
-      }
-    }
-    const int j0 = b * kKeys;
-    const bool whole = j0 >= all_from && j0 + kKeys <= all_to;
-    float top[2] = {neg_inf(), neg_inf()};
-#pragma unroll
-    for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = (s[n][e] + c[n][e]) * a.scale;
-        if (a.softcap > 0.0f) x = a.softcap * tanhf(x / a.softcap);
-        x *= kLog2e;
-        const int j = j0 + 8 * n + 2 * q4 + (e & 1), i = e >> 1;
-        if (!whole && (j < from[i] || j >= to[i])) x = neg_inf();
-        s[n][e] = x;
-        top[i] = fmaxf(top[i], x);
-      }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-    }
-    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
-      float f[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float now = fmaxf(m[i], top[i]);
-        f[i] = now == neg_inf() ? 1.0f : exp2f(m[i] - now);
-        m[i] = now;
-        l[i] *= f[i];
-      }
-#pragma unroll
-      for (int d = 0; d < D / 8; ++d) {
-        o[d][0] *= f[0];
-        o[d][1] *= f[0];
-        o[d][2] *= f[1];
-        o[d][3] *= f[1];
-      }
-    }
-    const float ref[2] = {m[0] == neg_inf() ? 0.0f : m[0], m[1] == neg_inf() ? 0.0f : m[1]};
-    // The scores' places (rows g, g + 8; keys 2 q4, 2 q4 + 1) are those of the second product's A operand (columns q4, q4 + 4) if
-    // its column q4 stands for key 2 q4 and q4 + 4 for 2 q4 + 1.
-#pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float w = exp2f(s[n][e] - ref[e >> 1]);
-        l[e >> 1] += w;
-        const Split x = split(w);
-        const int i = (e >> 1) | ((e & 1) << 1);
-        hi[i] = x.hi;
-        lo[i] = x.lo;
-      }
-      const float* vb = values + (n * 8 + 2 * q4) * kPitch + g;
-#pragma unroll
-      for (int d = 0; d < D / 8; ++d) {
-        const SplitAny x = split_any(vb[d * 8]), y = split_any(vb[kPitch + d * 8]);
-        mma_tf32(o[d], lo, x.cor, y.cor);
-        mma_tf32(o[d], hi, x.lo, y.lo);
-        mma_tf32(o[d], hi, x.hi, y.hi);
-      }
-    }
-    __syncwarp();
-  }
-  cp_async_wait_group<0>();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-  }
-
-  // a row's four features to the partial results, or divided to out
-  const auto write = [&](int r, int d, float4 x, float top, float sum) {
-    int64_t token;
-    int head;
-    row_owner(a, t, kvh, r, &token, &head);
-    if (t.splits > 1) {
-      const int64_t at = part_index(a, z, token, head);
-      *reinterpret_cast<float4*>(a.part_o + at * D + d) = x;
-      if (d == 0) a.part_ml[at] = make_float2(top, sum);
-    } else {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      float* dst = static_cast<float*>(a.out) + token * a.o_ts + head * a.o_hs + d;
-      dst[0] = x.x * inv;
-      dst[1] = x.y * inv;
-      dst[2] = x.z * inv;
-      dst[3] = x.w * inv;
-      if (d == 0 && a.lse) a.lse[token * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
-    }
-  };
-  if (q4 == 0)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      s_m[warp][g + 8 * i] = m[i];
-      s_l[warp][g + 8 * i] = l[i];
-    }
-  __syncthreads();  // (every warp is done with its ring)
-  float f[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float top = neg_inf();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][g + 8 * i]);
-    f[i] = m[i] == neg_inf() ? 1.0f : exp2f(m[i] - top);
-  }
-  constexpr int kSumPitch = D + 8;
-  float* const all = smem + C::kRows * kPitch;
-  float* const sums = all + warp * 16 * kSumPitch;
-#pragma unroll
-  for (int d = 0; d < D / 8; ++d) {
-    *reinterpret_cast<float2*>(sums + g * kSumPitch + d * 8 + q4 * 2) = make_float2(o[d][0] * f[0], o[d][1] * f[0]);
-    *reinterpret_cast<float2*>(sums + (g + 8) * kSumPitch + d * 8 + q4 * 2) = make_float2(o[d][2] * f[1], o[d][3] * f[1]);
-  }
-  __syncthreads();
-  for (int u = threadIdx.x; u < t.rows * kPieces; u += kWarps * 32) {
-    const int r = u / kPieces, d = (u - r * kPieces) * 4;
-    float top = neg_inf(), sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += s_l[w][r] * (s_m[w][r] == neg_inf() ? 1.0f : exp2f(s_m[w][r] - top));
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 y = *reinterpret_cast<const float4*>(all + (w * 16 + r) * kSumPitch + d);
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
-    }
-    write(r, d, x, top, sum);
-  }
-}
-
-// ------------------------------------------------------------------- tiles --
 
 constexpr int kTileRows = 16 * kWarps;
 constexpr int kTileKeys = 16;
@@ -554,13 +265,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
           ldsm_x4_trans(v_at + i * C::kPart + chunk_at<D>(lane & 15, 2 * d + (lane >> 4)), v[i][0], v[i][1], v[i][2], v[i][3]);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          float(&y)[4] = o[2 * d + n];
+          float y[4] = {};
           M::run4(y, p[2], v[1][2 * n], v[1][2 * n + 1]);
           M::run4(y, p[0], v[3][2 * n], v[3][2 * n + 1]);
           M::run4(y, p[1], v[2][2 * n], v[2][2 * n + 1]);
           M::run4(y, p[1], v[1][2 * n], v[1][2 * n + 1]);
           M::run4(y, p[0], v[2][2 * n], v[2][2 * n + 1]);
           M::run4(y, p[0], v[0][2 * n], v[0][2 * n + 1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[2 * d + n][e] += y[e];
         }
       }
     }
@@ -612,18 +325,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
 
 template <int D>
 cudaError_t launch_t(const AttnArgs& a, int64_t slots, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(slots), a.kv_heads, a.g.splits);
-  if (a.g.rows == 16) {
-    constexpr size_t smem = RowsCfg<D>::kSmem;
-    const cudaError_t e = ensure_smem<f32_rows_kernel<D>>(smem);
-    if (e != cudaSuccess) return e;
-    f32_rows_kernel<D><<<grid, kWarps * 32, smem, s>>>(a);
-  } else {
-    constexpr size_t smem = TileCfg<D>::kSmem;
-    const cudaError_t e = ensure_smem<f32_tile_kernel<D>>(smem);
-    if (e != cudaSuccess) return e;
-    f32_tile_kernel<D><<<grid, kWarps * 32, smem, s>>>(a);
-  }
+  constexpr size_t smem = TileCfg<D>::kSmem;
+  const cudaError_t e = ensure_smem<f32_tile_kernel<D>>(smem);
+  if (e != cudaSuccess) return e;
+  f32_tile_kernel<D><<<dim3(static_cast<unsigned>(slots), a.kv_heads, a.g.splits), kWarps * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 

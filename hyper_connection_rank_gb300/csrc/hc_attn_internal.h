@@ -6,9 +6,9 @@
 
 namespace hc {
 
-// Up to 16 rows to a key head (hc_attn_rows.cu). `aligned`: 16-byte accesses
-// are possible everywhere.
-bool attn_rows_supported(int dtype, int dim, bool aligned);
+// Up to 16 rows to a key head (hc_attn_rows.cu). `single`: every sequence has one
+// new token; `aligned`: 16-byte accesses are possible everywhere.
+bool attn_rows_supported(int dtype, int dim, bool single, int group, bool aligned);
 // Its own split of sequences of one new token: CTAs beside one for each tile, and
 // pieces (of all sequences) at most; none where splits by the host are as good.
 // `keys`: the longest sequence's.
@@ -18,7 +18,7 @@ struct RowsSchedule {
 RowsSchedule attn_rows_schedule(int64_t seqs, int kv_heads, int64_t keys, int num_sms);
 cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, int64_t slots, cudaStream_t s);
 
-// float32 (hc_attn_f32.cu), tiles of 16 or 64 rows by a.g.rows.
+// float32, tiles of 64 rows (hc_attn_f32.cu).
 bool attn_f32_supported(int dtype, int dim, bool aligned);
 cudaError_t launch_attn_f32(const AttnArgs& a, int64_t slots, cudaStream_t s);
 

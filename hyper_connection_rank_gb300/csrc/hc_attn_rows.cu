@@ -1,4 +1,4 @@
-// Attention over a paged cache for few rows (fp16/bf16): sequences whose new
+// Attention over a paged cache for few rows: sequences whose new
 // tokens and grouped heads make at most 16 rows to a key head, single tokens
 // above all.
 //
@@ -29,6 +29,8 @@
 // sums of values in registers; they are rescaled only when a block raises the
 // maximum. The warps' results are joined once at the end:
 //   M = max_w m_w,  out = sum_w 2^(m_w - M) o_w / sum_w 2^(m_w - M) l_w.
+#include <type_traits>
+
 #include "hc_async.cuh"
 #include "hc_attn.cuh"
 #include "hc_attn_internal.h"
@@ -133,7 +135,68 @@ __device__ __forceinline__ Pieces find_pieces(const AttnArgs& a, int unit, int s
   return p;
 }
 
-// PIECES: units of single-token sequences along x; else slots along x and splits along z.
+// What a CTA has to do: tile, piece or split z, and its keys [k0, k1). PIECES: units of single-token sequences along x; else
+// slots along x and splits along z.
+template <bool PIECES>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, AttnTile* t, int* z, int64_t* k0, int64_t* k1) {
+  if (PIECES) {
+    const Pieces p = find_pieces(a, blockIdx.x, -1);
+    if (p.s < 0) return false;
+    tile_at(a, a.g, p.s, 0, t);
+    t->splits = p.count;
+    *z = p.z;
+    *k0 = t->base + static_cast<int64_t>(p.z) * p.len;
+    *k1 = p.z == p.count - 1 ? t->hi : *k0 + p.len;
+    return true;
+  }
+  tile_of_slot(a, blockIdx.x, t);
+  if (t->rows == 0 || *z >= t->splits) return false;
+  split_range(a.g, *t, *z, k0, k1);
+  return true;
+}
+
+// Joins the warps' sums `all` ([warp][16 rows][D + 8], each scaled to the largest
+// maximum) of a tile's rows, and writes them as a piece's or as the result.
+template <typename T, int D, bool PIECES>
+__device__ __forceinline__ void write_rows(const AttnArgs& a, const AttnTile& t, int z, int kvh, const float* all,
+                                           const float (*s_m)[16], const float (*s_l)[16]) {
+  constexpr int kPitch = D + 8;
+  constexpr int kPerRow = D / 4;  // threads of a row, four features each
+  for (int u = threadIdx.x; u < t.rows * kPerRow; u += kWarps * 32) {
+    const int r = u / kPerRow, d = (u - r * kPerRow) * 4;
+    float top = neg_inf(), sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += s_l[w][r] * (s_m[w][r] == neg_inf() ? 1.0f : exp2f(s_m[w][r] - top));
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(all + (w * 16 + r) * kPitch + d);
+      x.x += y.x;
+      x.y += y.y;
+      x.z += y.z;
+      x.w += y.w;
+    }
+    int64_t token;
+    int head;
+    row_owner(a, t, kvh, r, &token, &head);
+    if (t.splits > 1) {
+      const int64_t at = PIECES ? piece_row(a, kvh, blockIdx.x, r) : part_index(a, z, token, head);
+      *reinterpret_cast<float4*>(a.part_o + at * D + d) = x;
+      if (d == 0) a.part_ml[at] = make_float2(top, sum);
+    } else {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + d;
+      stf(dst, x.x * inv);
+      stf(dst + 1, x.y * inv);
+      stf(dst + 2, x.z * inv);
+      stf(dst + 3, x.w * inv);
+      if (d == 0 && a.lse) a.lse[token * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+    }
+  }
+}
+
 template <typename T, int D, bool PIECES>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
   constexpr int kChunks = D / 8;                 // 16-byte chunks of a row
@@ -149,19 +212,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
   pdl_trigger();
   AttnTile t;
   int64_t k0, k1;
-  if (PIECES) {
-    const Pieces p = find_pieces(a, blockIdx.x, -1);
-    if (p.s < 0) return;
-    tile_at(a, a.g, p.s, 0, &t);
-    t.splits = p.count;
-    z = p.z;
-    k0 = t.base + static_cast<int64_t>(z) * p.len;
-    k1 = z == p.count - 1 ? t.hi : k0 + p.len;
-  } else {
-    tile_of_slot(a, blockIdx.x, &t);
-    if (t.rows == 0 || z >= t.splits) return;
-    split_range(a.g, t, z, &k0, &k1);
-  }
+  if (!find_work<PIECES>(a, &t, &z, &k0, &k1)) return;
   const T* kp = static_cast<const T*>(a.k) + kvh * a.c_hs;
   const T* vp = static_cast<const T*>(a.v) + kvh * a.c_hs;
   const int blocks = k1 > k0 ? static_cast<int>((k1 - k0 + kBlock - 1) / kBlock) : 0;
@@ -352,41 +403,168 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
     *reinterpret_cast<float2*>(sums + (g + 8) * kPitch + d * 8 + q4 * 2) = make_float2(o[d][2] * f[1], o[d][3] * f[1]);
   }
   __syncthreads();
-  constexpr int kPerRow = D / 4;  // threads of a row, four features each
-  const float* all = reinterpret_cast<const float*>(ring);
-  for (int u = threadIdx.x; u < t.rows * kPerRow; u += kWarps * 32) {
-    const int r = u / kPerRow, d = (u - r * kPerRow) * 4;
-    float top = neg_inf(), sum = 0.0f;
+  write_rows<T, D, PIECES>(a, t, z, kvh, reinterpret_cast<const float*>(ring), s_m, s_l);
+}
+
+// The same for float32 and at most 8 rows, on the CUDA cores. A key's or a value's row
+// goes straight from global memory to registers, D / 32 features to a lane (512
+// bytes side by side for a head of 128), 32 / R keys at a time, the values on
+// their way while the keys are worked on and the next keys while the values
+// are. Each lane forms its features' part of the block's 32 scores; a butterfly
+// that halves the scores a lane keeps at each of its five steps leaves each
+// lane with one whole score. Weights go back to all lanes by shuffles. All sums are
+// float32. Bound by its instructions, some 140 for a key and a value of 1 KB with
+// eight rows. One context of 100001 tokens, 20 heads on 4: 189 us, 2.2 TB/s
+// (342 us by the general kernel); 32 of up to 8001: 451 us against 490.
+template <int D, int R, bool PIECES>
+__global__ void __launch_bounds__(kWarps * 32, 3) f32_rows_kernel(AttnArgs a) {
+  constexpr int V = D / 32, kKeys = 32 / R;  // features of a lane; keys of a block
+  struct alignas(4 * V) Vec {
+    float e[V];
+  };
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ float s_m[kWarps][16], s_l[kWarps][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kvh = blockIdx.y;
+  int z = blockIdx.z;
+  pdl_trigger();
+  AttnTile t;
+  int64_t k0, k1;
+  if (!find_work<PIECES>(a, &t, &z, &k0, &k1)) return;
+  const float* kp = static_cast<const float*>(a.k) + kvh * a.c_hs + lane * V;
+  const float* vp = static_cast<const float*>(a.v) + kvh * a.c_hs + lane * V;
+  const int blocks = k1 > k0 ? static_cast<int>((k1 - k0 + kKeys - 1) / kKeys) : 0;
+
+  // place of key lane % kKeys of block b in the pool, -1: no such key
+  const auto place_of = [&](int b) -> int64_t {
+    const int64_t j = k0 + static_cast<int64_t>(b) * kKeys + lane % kKeys;
+    if (b >= blocks || j < t.lo || j >= k1) return -1;
+    const uint32_t i = static_cast<uint32_t>(j) / static_cast<uint32_t>(a.b.page_size);
+    const int page = page_of(a.b, t.s, i);
+    return page < 0 ? -1 : page * a.c_ps + (static_cast<uint32_t>(j) - i * a.b.page_size) * a.c_ts;
+  };
+  const auto fetch = [&](Vec* x, const float* base, int64_t place) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+    for (int j = 0; j < kKeys; ++j) {
+      const int64_t at = __shfl_sync(0xffffffffu, place, j);
+      if (at >= 0) {
+        x[j] = *reinterpret_cast<const Vec*>(base + at);
+      } else {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += s_l[w][r] * (s_m[w][r] == neg_inf() ? 1.0f : ex2(s_m[w][r] - top));
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 y = *reinterpret_cast<const float4*>(all + (w * 16 + r) * kPitch + d);
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
+        for (int e = 0; e < V; ++e) x[j].e[e] = 0.0f;
+      }
     }
-    int64_t token;
-    int head;
-    row_owner(a, t, kvh, r, &token, &head);
-    if (t.splits > 1) {
-      const int64_t at = PIECES ? piece_row(a, kvh, blockIdx.x, r) : part_index(a, z, token, head);
-      *reinterpret_cast<float4*>(a.part_o + at * D + d) = x;
-      if (d == 0) a.part_ml[at] = make_float2(top, sum);
-    } else {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + d;
-      stf(dst, x.x * inv);
-      stf(dst + 1, x.y * inv);
-      stf(dst + 2, x.z * inv);
-      stf(dst + 3, x.w * inv);
-      if (d == 0 && a.lse) a.lse[token * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+  };
+  Vec keys[kKeys], values[kKeys];
+  int64_t place = place_of(warp), next = place_of(warp + kWarps);
+  fetch(keys, kp, place);
+  float q[R][V], o[R][V];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) q[r][e] = o[r][e] = 0.0f;
+    if (r < t.rows) {
+      int64_t token;
+      int head;
+      row_owner(a, t, kvh, r, &token, &head);
+      const Vec x = *reinterpret_cast<const Vec*>(static_cast<const float*>(a.q) + token * a.q_ts + head * a.q_hs + lane * V);
+#pragma unroll
+      for (int e = 0; e < V; ++e) q[r][e] = x.e[e];
     }
   }
+  // this lane's score of a block: row `mine`, key my_key; and the keys that the row sees, relative to k0
+  const int mine = lane / kKeys, my_key = lane % kKeys;
+  int from = 0, to = 0;
+  {
+    const auto rel = [&](int64_t j) {
+      const int64_t d = j - k0, n = k1 - k0;
+      return static_cast<int>(d < 0 ? 0 : d > n ? n : d);
+    };
+    const int64_t p = row_position(t, t.row0 + mine, a.group);
+    to = mine < t.rows ? rel(p + 1) : 0;
+    from = mine < t.rows && a.window > 0 ? rel(p - a.window + 1) : 0;
+  }
+  float m = neg_inf(), l = 0.0f;  // of row `mine`, l over this lane's keys
+
+  for (int b = warp; b < blocks; b += kWarps) {
+    fetch(values, vp, place);
+    float s[32];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) {
+        float x = q[r][0] * keys[j].e[0];
+#pragma unroll
+        for (int e = 1; e < V; ++e) x = fmaf(q[r][e], keys[j].e[e], x);
+        s[r * kKeys + j] = x;
+      }
+    fetch(keys, kp, next);
+    place = next;
+    next = place_of(b + 2 * kWarps);
+#pragma unroll
+    for (int step = 0; step < 5; ++step) {
+      const int n = 16 >> step, bit = n;
+      const bool upper = lane & bit;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i >= n) break;
+        const float give = upper ? s[i] : s[i + n], have = upper ? s[i + n] : s[i];
+        s[i] = have + __shfl_xor_sync(0xffffffffu, give, bit);
+      }
+    }
+    float x = s[0] * a.scale;
+    if (a.softcap > 0.0f) x = a.softcap * tanhf(x / a.softcap);
+    const int at = b * kKeys + my_key;
+    x = at >= from && at < to ? x * kLog2e : neg_inf();
+    float top = x;
+#pragma unroll
+    for (int bit = 1; bit < kKeys; bit *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, bit));
+    if (__any_sync(0xffffffffu, top > m)) {
+      const float now = fmaxf(m, top);
+      const float f = now == neg_inf() ? 1.0f : exp2f(m - now);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float x = __shfl_sync(0xffffffffu, f, r * kKeys);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[r][e] *= x;
+      }
+    }
+    const float weight = exp2f(x - (m == neg_inf() ? 0.0f : m));
+    l += weight;
+    // (keys that only some rows see, in a tile of more than one token: a weight of zero adds nothing, whatever the value)
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) {
+        const float w = __shfl_sync(0xffffffffu, weight, r * kKeys + j);
+        if (w == 0.0f) continue;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[r][e] = fmaf(w, values[j].e[e], o[r][e]);
+      }
+  }
+#pragma unroll
+  for (int bit = 1; bit < kKeys; bit *= 2) l += __shfl_xor_sync(0xffffffffu, l, bit);
+  if (my_key == 0) {
+    s_m[warp][mine] = m;
+    s_l[warp][mine] = l;
+  }
+  __syncthreads();
+  constexpr int kPitch = D + 8;
+  float* sums = reinterpret_cast<float*>(ring) + warp * 16 * kPitch;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float top = neg_inf();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+    const float f = s_m[warp][r] == neg_inf() ? 1.0f : exp2f(s_m[warp][r] - top);
+    Vec x;
+#pragma unroll
+    for (int e = 0; e < V; ++e) x.e[e] = o[r][e] * f;
+    *reinterpret_cast<Vec*>(sums + r * kPitch + lane * V) = x;
+  }
+  __syncthreads();
+  write_rows<float, D, PIECES>(a, t, z, kvh, reinterpret_cast<const float*>(ring), s_m, s_l);
 }
 
 // Joins the pieces of every sequence that has more than one (as combine_kernel of
@@ -448,29 +626,41 @@ __global__ void __launch_bounds__(256) rows_join_kernel(AttnArgs a) {
   if (tid == 0 && a.lse) a.lse[static_cast<int64_t>(s) * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
 }
 
+template <auto Kernel>
+cudaError_t launch_kernel(const AttnArgs& a, int64_t slots, size_t smem, cudaStream_t s) {
+  const cudaError_t e = ensure_smem<Kernel>(smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid = a.units > 0 ? dim3(a.units, a.kv_heads) : dim3(static_cast<unsigned>(slots), a.kv_heads, a.g.splits);
+  Kernel<<<grid, kWarps * 32, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, int D>
 cudaError_t launch_t(const AttnArgs& a, int64_t slots, cudaStream_t s) {
   constexpr size_t ring = static_cast<size_t>(kWarps) * kStages * kBlock * D * 4;
   constexpr size_t sums = static_cast<size_t>(kWarps) * 16 * (D + 8) * 4;
-  constexpr size_t smem = ring > sums ? ring : sums;
-  if (a.units > 0) {
-    const cudaError_t e = ensure_smem<rows_kernel<T, D, true>>(smem);
-    if (e != cudaSuccess) return e;
-    rows_kernel<T, D, true><<<dim3(a.units, a.kv_heads), kWarps * 32, smem, s>>>(a);
-    const cudaError_t e2 = cudaGetLastError();
-    if (e2 != cudaSuccess) return e2;
-    return launch_pdl(rows_join_kernel<T, D>, dim3(a.b.seqs, a.heads), dim3(256), 0, s, 1, a);
+  cudaError_t e;
+  if constexpr (std::is_same<T, float>::value) {
+    if (a.group <= 4) {
+      e = a.units > 0 ? launch_kernel<f32_rows_kernel<D, 4, true>>(a, slots, sums, s)
+                      : launch_kernel<f32_rows_kernel<D, 4, false>>(a, slots, sums, s);
+    } else {
+      e = a.units > 0 ? launch_kernel<f32_rows_kernel<D, 8, true>>(a, slots, sums, s)
+                      : launch_kernel<f32_rows_kernel<D, 8, false>>(a, slots, sums, s);
+    }
+  } else {
+    constexpr size_t smem = ring > sums ? ring : sums;
+    e = a.units > 0 ? launch_kernel<rows_kernel<T, D, true>>(a, slots, smem, s)
+                    : launch_kernel<rows_kernel<T, D, false>>(a, slots, smem, s);
   }
-  const cudaError_t e = ensure_smem<rows_kernel<T, D, false>>(smem);
-  if (e != cudaSuccess) return e;
-  rows_kernel<T, D, false><<<dim3(static_cast<unsigned>(slots), a.kv_heads, a.g.splits), kWarps * 32, smem, s>>>(a);
-  return cudaGetLastError();
+  if (e != cudaSuccess || a.units == 0) return e;
+  return launch_pdl(rows_join_kernel<T, D>, dim3(a.b.seqs, a.heads), dim3(256), 0, s, 1, a);
 }
 
 }  // namespace
 
-bool attn_rows_supported(int dtype, int dim, bool aligned) {
-  return aligned && (dtype == HC_F16 || dtype == HC_BF16) && (dim == 64 || dim == 128);
+bool attn_rows_supported(int dtype, int dim, bool single, int group, bool aligned) {
+  return aligned && (dim == 64 || dim == 128) && (dtype != HC_F32 || (single && group <= 8));
 }
 
 RowsSchedule attn_rows_schedule(int64_t seqs, int kv_heads, int64_t keys, int num_sms) {
@@ -480,6 +670,7 @@ RowsSchedule attn_rows_schedule(int64_t seqs, int kv_heads, int64_t keys, int nu
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, int64_t slots, cudaStream_t s) {
+  if (dtype == HC_F32) return a.dim == 64 ? launch_t<float, 64>(a, slots, s) : launch_t<float, 128>(a, slots, s);
   if (dtype == HC_F16) return a.dim == 64 ? launch_t<__half, 64>(a, slots, s) : launch_t<__half, 128>(a, slots, s);
   return a.dim == 64 ? launch_t<__nv_bfloat16, 64>(a, slots, s) : launch_t<__nv_bfloat16, 128>(a, slots, s);
 }
