@@ -6,24 +6,31 @@
 // multiply-adds to the byte at most, so what counts is to keep enough loads in
 // flight (some 44 bytes/ns and SM, about 45 KB at a microsecond's latency).
 // Each warp runs for itself: blocks of 16 keys, every fourth of the split's,
-// come by 16-byte cp.async into a ring of its own, four blocks deep, so that
+// come by 16-byte cp.async into a ring of its own, two blocks deep, so that
 // no barrier stands between the loads of one warp and the arithmetic of
-// another (two CTAs to an SM hold 192 KB in flight). The products are warp-level
-// MMAs (m16n8k16): a tile of 16 rows is what they are made for, where a
-// tcgen05 tile would be seven eighths empty and its tensor-memory round trips
-// would lie on the path of every block.
+// another; three CTAs of four warps to an SM have up to 192 KB on their way (a
+// ring of three blocks leaves room for two CTAs: 112 us where this takes 104, of
+// four for one: 146). The products are warp-level MMAs (m16n8k16): a tile of 16
+// rows is what they are made for, where a tcgen05 tile would be seven eighths
+// empty and its tensor-memory round trips would lie on the path of every block.
+//
+// Measured: two contexts of 130002 and 34402 tokens, 32 heads of 128 on 8, fp16:
+// 104 us, 6.5 TB/s, 97% of the measured copy bandwidth; 61 ragged contexts of up
+// to 8192 in bf16: 231 us, 6.1 TB/s, 92%; one of 700, 20 heads on 4: 10.6 us, the
+// latency of two kernels.
 //
 // Work: where every sequence has one new token (no cu_q) and there are too few of
 // them to fill half the GPU, the kernel splits them itself, by their lengths: with
-// T CTAs, two for each SM, all that run at once, and as many extra pieces as
+// T CTAs, two for each SM, which all run at once, and as many extra pieces as
 // rounding up may make, all are cut into pieces of
 //   L = sum of keys * kv_heads / (T - seqs * kv_heads)
 // keys, so that they fill the GPU once, evenly, whatever the lengths are. Every
 // warp works that out for itself from kv_lens, 32 sequences at a time. (Against
-// pieces that the host chose by the longest: two contexts of 130002 and 34402
-// tokens, 8 key heads, 121 -> 112 us; one of 30002, 4 key heads, 35 -> 21 us;
-// eight of up to 4002, 25 -> 17 us. With more sequences the host's splits are
-// as good, and 64 contexts of up to 8192 take 231 us where these took 240.)
+// pieces that the host chose by the longest, with a ring of three blocks: two
+// contexts of 130002 and 34402 tokens, 8 key heads, 121 -> 112 us; one of 30002, 4
+// key heads, 35 -> 21 us; eight of up to 4002, 25 -> 17 us. With more sequences
+// the host's splits are as good, and 64 contexts of up to 8192 took 231 us where
+// these took 240.)
 //
 // Mathematics: the running maximum and sum of a softmax, held per warp, with the
 // sums of values in registers; they are rescaled only when a block raises the
@@ -41,7 +48,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kBlock = 16;  // keys of a block
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kShortest = 128;  // keys that are worth a piece
 constexpr int kMaxPieces = 512; // of a sequence
 
