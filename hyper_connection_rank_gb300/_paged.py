@@ -27,6 +27,9 @@ __all__ = ["rotary_frequencies", "rotary", "rotary_append", "paged_attention", "
 _ROTARY = struct.Struct("@4P5q7if0q")
 _APPEND = struct.Struct("@10P3q6q2q3q3i4iiif0q")
 _ATTENTION = struct.Struct("@9PN3q4q3q3i3i2iiiI2f0q")
+# (in three parts, of which the middle one, workspace and its size, is known last)
+_ATTENTION_FRONT, _ATTENTION_WORK, _ATTENTION_BACK = struct.Struct("@8P"), struct.Struct("@PN"), struct.Struct("@3q4q3q3i3i2iiiI2f0q")
+_NO_WORK = _ATTENTION_WORK.pack(0, 0)
 _PAGES = struct.Struct("@6P2q3i0q")
 
 
@@ -96,7 +99,8 @@ def _out(out, like, name):
     """(out, its strides): the one given, or a new one of the shape of `like`."""
     if out is None:
         out = torch.empty_like(like)
-    elif out.shape != like.shape or out.dtype is not like.dtype:
+        return out, out.stride()
+    if out.shape != like.shape or out.dtype is not like.dtype:
         raise ValueError(f"out must have the shape and dtype of {name}")
     return out, _heads("out", out, like.dtype)[1]
 
@@ -195,17 +199,19 @@ def rotary_append(q, k, v, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, 
     return out
 
 
-def _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, os):
-    """The packed arguments before out, lse and workspace, and those after."""
+def _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, out, lse, os):
+    """The packed arguments before the workspace, and those after."""
     code = _dtype_code(q)
     (tokens, heads, dim), qs = _heads("q", q, q.dtype)
     (pages, page, kv_heads, cdim), cs = _caches(k_cache, v_cache, q.dtype)
     if cdim != dim or kv_heads < 1 or heads % kv_heads:
         raise ValueError("heads must be a multiple of kv_heads, and head_dim that of the caches")
     seqs, width, step, cu = _batch(page_table, kv_lens, cu_q, tokens)
-    front = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cu)
-    back = (tokens, pages, step, qs[0], qs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, width, page, heads, kv_heads, dim,
-            max_q or 0, max_kv or 0, window or 0, code, flags, 1.0 / math.sqrt(dim) if scale is None else scale, softcap or 0.0)
+    front = _ATTENTION_FRONT.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+                                  kv_lens.data_ptr(), cu, out, lse)
+    back = _ATTENTION_BACK.pack(tokens, pages, step, qs[0], qs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, width, page, heads,
+                                kv_heads, dim, max_q or 0, max_kv or 0, window or 0, code, flags,
+                                1.0 / math.sqrt(dim) if scale is None else scale, softcap or 0.0)
     return front, back
 
 
@@ -213,9 +219,9 @@ def paged_attention_workspace_size(q, k_cache, v_cache, page_table, kv_lens, cu_
                                    flags=0):
     """Bytes of workspace that ``paged_attention`` needs for these tensors (their contents do not matter)."""
     heads, dim = q.shape[1:]
-    front, back = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, None, window, 0.0, max_q, max_kv, flags,
+    front, back = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, None, window, 0.0, max_q, max_kv, flags, 0, 0,
                                   (heads * dim, dim))
-    return lib().hc_paged_attention_workspace_size(_ATTENTION.pack(*front, 0, 0, 0, 0, *back))
+    return lib().hc_paged_attention_workspace_size(front + _NO_WORK + back)
 
 
 def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, scale=None, window=0, softcap=0.0, max_q=None,
@@ -230,18 +236,17 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, scal
     out, os = _out(out, q, "q")
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
     front, back = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags,
-                                  os)
-    results = (out.data_ptr(), 0 if lse is None else lse.data_ptr())
+                                  out.data_ptr(), 0 if lse is None else lse.data_ptr(), os)
     L = lib()
-    at = size = 0
+    work = _NO_WORK
     if workspace is None:
-        size = L.hc_paged_attention_workspace_size(_ATTENTION.pack(*front, *results, 0, 0, *back))
+        size = L.hc_paged_attention_workspace_size(front + _NO_WORK + back)
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-            at = workspace.data_ptr()
+            work = _ATTENTION_WORK.pack(workspace.data_ptr(), size)
     else:
-        at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    check(L.hc_paged_attention(_ATTENTION.pack(*front, *results, at, size, *back), _stream(q, stream, out, lse, workspace)))
+        work = _ATTENTION_WORK.pack(workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    check(L.hc_paged_attention(front + work + back, _stream(q, stream, out, lse, workspace)))
     return (out, lse) if return_lse else out
 
 
