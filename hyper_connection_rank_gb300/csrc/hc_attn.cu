@@ -427,7 +427,7 @@ Plan plan_of(const hc_paged_attention_t& a, bool aligned, int num_sms) {
   };
   if (p.rows_kernel && few && a.cu_q == nullptr)
     p.pieces = attn_rows_schedule(a.seqs, a.kv_heads, keys_of(p.small.rows), num_sms);
-  if (p.pieces.units > 0) {
+  if (p.pieces.units > 0 || p.pieces.clusters) {
     p.small.split_len = 1 << 30;
     p.small.splits = 1;
     return p;
@@ -518,6 +518,7 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
   d.slot_is_seq = p.use_large;
   d.spare_ctas = p.pieces.spare_ctas;
   d.units = p.pieces.units;
+  d.clusters = p.pieces.clusters;
   cudaError_t e = p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s) : general_d<T, kSmallRows>(d, aligned, slots, s);
   if (e != cudaSuccess) return e;
   if (p.use_large) {

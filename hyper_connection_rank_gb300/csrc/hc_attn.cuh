@@ -46,6 +46,7 @@ struct AttnArgs {
   // hc_attn_rows.cu, where it splits single-token sequences itself: CTAs that there may be beside one for each tile, and pieces at
   // most (0: the splits above)
   int spare_ctas, units;
+  bool clusters;  // there, a cluster to a sequence
 };
 
 constexpr float kLog2e = 1.4426950408889634f;

@@ -14,6 +14,7 @@ bool attn_rows_supported(int dtype, int dim, bool single, int group, bool aligne
 // `keys`: the longest sequence's.
 struct RowsSchedule {
   int spare_ctas, units;
+  bool clusters;  // no pieces, but a cluster to a sequence
 };
 RowsSchedule attn_rows_schedule(int64_t seqs, int kv_heads, int64_t keys, int num_sms);
 cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, int64_t slots, cudaStream_t s);

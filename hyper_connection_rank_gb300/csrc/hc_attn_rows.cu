@@ -16,8 +16,8 @@
 //
 // Measured: two contexts of 130002 and 34402 tokens, 32 heads of 128 on 8, fp16:
 // 104 us, 6.5 TB/s, 97% of the measured copy bandwidth; 61 ragged contexts of up
-// to 8192 in bf16: 231 us, 6.1 TB/s, 92%; one of 700, 20 heads on 4: 10.6 us, the
-// latency of two kernels.
+// to 8192 in bf16: 231 us, 6.1 TB/s, 92%; one of 700, 20 heads on 4: 8.6 us, the latency
+// of its chain of loads.
 //
 // Work: where every sequence has one new token (no cu_q) and there are too few of
 // them to fill half the GPU, the kernel splits them itself, by their lengths: with
@@ -30,7 +30,11 @@
 // contexts of 130002 and 34402 tokens, 8 key heads, 121 -> 112 us; one of 30002, 4
 // key heads, 35 -> 21 us; eight of up to 4002, 25 -> 17 us. With more sequences
 // the host's splits are as good, and 64 contexts of up to 8192 took 231 us where
-// these took 240.)
+// these took 240.) Contexts of up to kClusterKeys, where eight CTAs to each tile
+// still run at once, go to clusters of eight, which join their sums through
+// shared memory: one kernel and no workspace (one context of 700, 20 heads on 4:
+// 8.6 us where pieces take 10.7, of 2002 10.6 against 12.6; of 4002 14.7 against
+// 12.2).
 //
 // Mathematics: the running maximum and sum of a softmax, held per warp, with the
 // sums of values in registers; they are rescaled only when a block raises the
@@ -51,6 +55,7 @@ constexpr int kBlock = 16;  // keys of a block
 constexpr int kStages = 2;
 constexpr int kShortest = 128;  // keys that are worth a piece
 constexpr int kMaxPieces = 512; // of a sequence
+constexpr int kClusterKeys = 2560;  // the longest context that a cluster takes
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float x, float y);
@@ -142,11 +147,16 @@ __device__ __forceinline__ Pieces find_pieces(const AttnArgs& a, int unit, int s
   return p;
 }
 
-// What a CTA has to do: tile, piece or split z, and its keys [k0, k1). PIECES: units of single-token sequences along x; else
-// slots along x and splits along z.
-template <bool PIECES>
+// How a sequence's keys are shared out: slots along x and splits along z
+// (hc_attn.cuh); pieces of single-token sequences along x, as above; or a cluster
+// of kCluster CTAs along x to each single-token sequence.
+enum Share { kBySplit, kByPiece, kByCluster };
+constexpr int kCluster = 8;
+
+// What a CTA has to do: tile, split, piece or rank z, and its keys [k0, k1).
+template <int SHARE>
 __device__ __forceinline__ bool find_work(const AttnArgs& a, AttnTile* t, int* z, int64_t* k0, int64_t* k1) {
-  if (PIECES) {
+  if (SHARE == kByPiece) {
     const Pieces p = find_pieces(a, blockIdx.x, -1);
     if (p.s < 0) return false;
     tile_at(a, a.g, p.s, 0, t);
@@ -156,19 +166,66 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, AttnTile* t, int* z
     *k1 = p.z == p.count - 1 ? t->hi : *k0 + p.len;
     return true;
   }
+  if (SHARE == kByCluster) {
+    tile_at(a, a.g, blockIdx.x / kCluster, 0, t);
+    *z = blockIdx.x % kCluster;
+    const int64_t len = (t->hi - t->base + kCluster * kBlock - 1) / (kCluster * kBlock) * kBlock;
+    *k0 = t->base + *z * len;
+    *k0 = *k0 < t->hi ? *k0 : t->hi;
+    *k1 = *k0 + len < t->hi ? *k0 + len : t->hi;
+    return true;
+  }
   tile_of_slot(a, blockIdx.x, t);
   if (t->rows == 0 || *z >= t->splits) return false;
   split_range(a.g, *t, *z, k0, k1);
   return true;
 }
 
+__device__ __forceinline__ float4 peer_load4(const void* p, int rank) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(mapa_shared(smem_addr(p), rank)));
+  return x;
+}
+__device__ __forceinline__ float2 peer_load2(const void* p, int rank) {
+  float2 x;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(x.x), "=f"(x.y)
+               : "r"(mapa_shared(smem_addr(p), rank)));
+  return x;
+}
+
+// Floats of shared memory for a tile's sums on their way out: each warp's, and, in a cluster, the CTA's with its maxima and sums
+// of weights.
+template <int D>
+constexpr int sum_floats(bool cluster) {
+  return kWarps * 16 * (D + 8) + (cluster ? 16 * D + 32 : 0);
+}
+
 // Joins the warps' sums `all` ([warp][16 rows][D + 8], each scaled to the largest
-// maximum) of a tile's rows, and writes them as a piece's or as the result.
-template <typename T, int D, bool PIECES>
-__device__ __forceinline__ void write_rows(const AttnArgs& a, const AttnTile& t, int z, int kvh, const float* all,
+// maximum) of a tile's rows, and writes them as partial results or as the result.
+// The CTAs of a cluster join theirs through one another's shared memory, each for
+// its share of the rows' features.
+template <typename T, int D, int SHARE>
+__device__ __forceinline__ void write_rows(const AttnArgs& a, const AttnTile& t, int z, int kvh, float* all,
                                            const float (*s_m)[16], const float (*s_l)[16]) {
   constexpr int kPitch = D + 8;
   constexpr int kPerRow = D / 4;  // threads of a row, four features each
+  const auto write = [&](int r, int d, float4 x, float top, float sum) {
+    int64_t token;
+    int head;
+    row_owner(a, t, kvh, r, &token, &head);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + d;
+    stf(dst, x.x * inv);
+    stf(dst + 1, x.y * inv);
+    stf(dst + 2, x.z * inv);
+    stf(dst + 3, x.w * inv);
+    if (d == 0 && a.lse) a.lse[token * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+  };
+  float* const cta_sums = all + kWarps * 16 * kPitch;
+  float2* const cta_ml = reinterpret_cast<float2*>(cta_sums + 16 * D);
   for (int u = threadIdx.x; u < t.rows * kPerRow; u += kWarps * 32) {
     const int r = u / kPerRow, d = (u - r * kPerRow) * 4;
     float top = neg_inf(), sum = 0.0f;
@@ -185,26 +242,57 @@ __device__ __forceinline__ void write_rows(const AttnArgs& a, const AttnTile& t,
       x.z += y.z;
       x.w += y.w;
     }
-    int64_t token;
-    int head;
-    row_owner(a, t, kvh, r, &token, &head);
-    if (t.splits > 1) {
-      const int64_t at = PIECES ? piece_row(a, kvh, blockIdx.x, r) : part_index(a, z, token, head);
+    if (SHARE == kByCluster) {
+      *reinterpret_cast<float4*>(cta_sums + r * D + d) = x;
+      if (d == 0) cta_ml[r] = make_float2(top, sum);
+    } else if (t.splits > 1) {
+      int64_t at;
+      if (SHARE == kByPiece) {
+        at = piece_row(a, kvh, blockIdx.x, r);
+      } else {
+        int64_t token;
+        int head;
+        row_owner(a, t, kvh, r, &token, &head);
+        at = part_index(a, z, token, head);
+      }
       *reinterpret_cast<float4*>(a.part_o + at * D + d) = x;
       if (d == 0) a.part_ml[at] = make_float2(top, sum);
     } else {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      T* dst = static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + d;
-      stf(dst, x.x * inv);
-      stf(dst + 1, x.y * inv);
-      stf(dst + 2, x.z * inv);
-      stf(dst + 3, x.w * inv);
-      if (d == 0 && a.lse) a.lse[token * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
+      write(r, d, x, top, sum);
     }
+  }
+  if (SHARE == kByCluster) {
+    cluster_sync_all();
+    for (int u = z * kWarps * 32 + threadIdx.x; u < t.rows * kPerRow; u += kCluster * kWarps * 32) {
+      const int r = u / kPerRow, d = (u - r * kPerRow) * 4;
+      float2 ml[kCluster];
+      float4 y[kCluster];
+#pragma unroll
+      for (int k = 0; k < kCluster; ++k) {
+        ml[k] = peer_load2(cta_ml + r, k);
+        y[k] = peer_load4(cta_sums + r * D + d, k);
+      }
+      float top = neg_inf(), sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kCluster; ++k) top = fmaxf(top, ml[k].x);
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < kCluster; ++k) {
+        // (no weights: sums of zero, or NaN from NaN scores)
+        const float w = ml[k].x == neg_inf() ? 1.0f : exp2f(ml[k].x - top);
+        sum += ml[k].y * w;
+        x.x = fmaf(y[k].x, w, x.x);
+        x.y = fmaf(y[k].y, w, x.y);
+        x.z = fmaf(y[k].z, w, x.z);
+        x.w = fmaf(y[k].w, w, x.w);
+      }
+      write(r, d, x, top, sum);
+    }
+    cluster_sync_all();  // (no CTA leaves while another reads its memory)
   }
 }
 
-template <typename T, int D, bool PIECES>
+template <typename T, int D, int SHARE>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
   constexpr int kChunks = D / 8;                 // 16-byte chunks of a row
   constexpr int kHalf = kBlock * D * 2;          // bytes of a block's keys
@@ -219,7 +307,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
   pdl_trigger();
   AttnTile t;
   int64_t k0, k1;
-  if (!find_work<PIECES>(a, &t, &z, &k0, &k1)) return;
+  if (!find_work<SHARE>(a, &t, &z, &k0, &k1)) return;
   const T* kp = static_cast<const T*>(a.k) + kvh * a.c_hs;
   const T* vp = static_cast<const T*>(a.v) + kvh * a.c_hs;
   const int blocks = k1 > k0 ? static_cast<int>((k1 - k0 + kBlock - 1) / kBlock) : 0;
@@ -410,7 +498,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
     *reinterpret_cast<float2*>(sums + (g + 8) * kPitch + d * 8 + q4 * 2) = make_float2(o[d][2] * f[1], o[d][3] * f[1]);
   }
   __syncthreads();
-  write_rows<T, D, PIECES>(a, t, z, kvh, reinterpret_cast<const float*>(ring), s_m, s_l);
+  write_rows<T, D, SHARE>(a, t, z, kvh, reinterpret_cast<float*>(ring), s_m, s_l);
 }
 
 // The same for float32 and at most 8 rows, on the CUDA cores. A key's or a value's row
@@ -423,7 +511,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
 // float32. Bound by its instructions, some 140 for a key and a value of 1 KB with
 // eight rows. One context of 100001 tokens, 20 heads on 4: 189 us, 2.2 TB/s
 // (342 us by the general kernel); 32 of up to 8001: 451 us against 490.
-template <int D, int R, bool PIECES>
+template <int D, int R, int SHARE>
 __global__ void __launch_bounds__(kWarps * 32, 3) f32_rows_kernel(AttnArgs a) {
   constexpr int V = D / 32, kKeys = 32 / R;  // features of a lane; keys of a block
   struct alignas(4 * V) Vec {
@@ -436,7 +524,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) f32_rows_kernel(AttnArgs a) {
   pdl_trigger();
   AttnTile t;
   int64_t k0, k1;
-  if (!find_work<PIECES>(a, &t, &z, &k0, &k1)) return;
+  if (!find_work<SHARE>(a, &t, &z, &k0, &k1)) return;
   const float* kp = static_cast<const float*>(a.k) + kvh * a.c_hs + lane * V;
   const float* vp = static_cast<const float*>(a.v) + kvh * a.c_hs + lane * V;
   const int blocks = k1 > k0 ? static_cast<int>((k1 - k0 + kKeys - 1) / kKeys) : 0;
@@ -571,7 +659,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) f32_rows_kernel(AttnArgs a) {
     *reinterpret_cast<Vec*>(sums + r * kPitch + lane * V) = x;
   }
   __syncthreads();
-  write_rows<float, D, PIECES>(a, t, z, kvh, reinterpret_cast<const float*>(ring), s_m, s_l);
+  write_rows<float, D, SHARE>(a, t, z, kvh, reinterpret_cast<float*>(ring), s_m, s_l);
 }
 
 // Joins the pieces of every sequence that has more than one (as combine_kernel of
@@ -633,34 +721,48 @@ __global__ void __launch_bounds__(256) rows_join_kernel(AttnArgs a) {
   if (tid == 0 && a.lse) a.lse[static_cast<int64_t>(s) * a.heads + head] = sum == 0.0f ? neg_inf() : top * kLn2 + logf(sum);
 }
 
-template <auto Kernel>
+template <int SHARE, auto Kernel>
 cudaError_t launch_kernel(const AttnArgs& a, int64_t slots, size_t smem, cudaStream_t s) {
   const cudaError_t e = ensure_smem<Kernel>(smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid = a.units > 0 ? dim3(a.units, a.kv_heads) : dim3(static_cast<unsigned>(slots), a.kv_heads, a.g.splits);
+  if (SHARE == kByCluster) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.b.seqs * kCluster, a.kv_heads);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kCluster;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, Kernel, a);
+  }
+  const dim3 grid = SHARE == kByPiece ? dim3(a.units, a.kv_heads) : dim3(static_cast<unsigned>(slots), a.kv_heads, a.g.splits);
   Kernel<<<grid, kWarps * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 
+template <typename T, int D, int SHARE>
+cudaError_t launch_share(const AttnArgs& a, int64_t slots, cudaStream_t s) {
+  constexpr size_t ring = static_cast<size_t>(kWarps) * kStages * kBlock * D * 4;
+  constexpr size_t sums = static_cast<size_t>(sum_floats<D>(SHARE == kByCluster)) * 4;
+  if constexpr (std::is_same<T, float>::value) {
+    return a.group <= 4 ? launch_kernel<SHARE, f32_rows_kernel<D, 4, SHARE>>(a, slots, sums, s)
+                        : launch_kernel<SHARE, f32_rows_kernel<D, 8, SHARE>>(a, slots, sums, s);
+  } else {
+    return launch_kernel<SHARE, rows_kernel<T, D, SHARE>>(a, slots, ring > sums ? ring : sums, s);
+  }
+}
+
 template <typename T, int D>
 cudaError_t launch_t(const AttnArgs& a, int64_t slots, cudaStream_t s) {
-  constexpr size_t ring = static_cast<size_t>(kWarps) * kStages * kBlock * D * 4;
-  constexpr size_t sums = static_cast<size_t>(kWarps) * 16 * (D + 8) * 4;
-  cudaError_t e;
-  if constexpr (std::is_same<T, float>::value) {
-    if (a.group <= 4) {
-      e = a.units > 0 ? launch_kernel<f32_rows_kernel<D, 4, true>>(a, slots, sums, s)
-                      : launch_kernel<f32_rows_kernel<D, 4, false>>(a, slots, sums, s);
-    } else {
-      e = a.units > 0 ? launch_kernel<f32_rows_kernel<D, 8, true>>(a, slots, sums, s)
-                      : launch_kernel<f32_rows_kernel<D, 8, false>>(a, slots, sums, s);
-    }
-  } else {
-    constexpr size_t smem = ring > sums ? ring : sums;
-    e = a.units > 0 ? launch_kernel<rows_kernel<T, D, true>>(a, slots, smem, s)
-                    : launch_kernel<rows_kernel<T, D, false>>(a, slots, smem, s);
-  }
-  if (e != cudaSuccess || a.units == 0) return e;
+  if (a.clusters) return launch_share<T, D, kByCluster>(a, slots, s);
+  if (a.units == 0) return launch_share<T, D, kBySplit>(a, slots, s);
+  const cudaError_t e = launch_share<T, D, kByPiece>(a, slots, s);
+  if (e != cudaSuccess) return e;
   return launch_pdl(rows_join_kernel<T, D>, dim3(a.b.seqs, a.heads), dim3(256), 0, s, 1, a);
 }
 
@@ -672,8 +774,9 @@ bool attn_rows_supported(int dtype, int dim, bool single, int group, bool aligne
 
 RowsSchedule attn_rows_schedule(int64_t seqs, int kv_heads, int64_t keys, int num_sms) {
   const int64_t tiles = seqs * kv_heads, wave = 2 * static_cast<int64_t>(num_sms);
-  if (keys <= kShortest || tiles * 2 > wave) return RowsSchedule{0, 0};
-  return RowsSchedule{static_cast<int>(wave - tiles), static_cast<int>((wave - tiles) / kv_heads + seqs)};
+  if (keys <= kShortest || tiles * 2 > wave) return RowsSchedule{0, 0, false};
+  if (keys <= kClusterKeys && tiles * kCluster <= wave) return RowsSchedule{0, 0, true};
+  return RowsSchedule{static_cast<int>(wave - tiles), static_cast<int>((wave - tiles) / kv_heads + seqs), false};
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, int64_t slots, cudaStream_t s) {
