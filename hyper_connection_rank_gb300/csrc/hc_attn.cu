@@ -370,7 +370,7 @@ struct Plan {
   bool use_large;      // sequences of more than kSmallRows rows go to the large tiles
   bool rows_kernel;    // small tiles by hc_attn_rows.cu
   RowsSchedule pieces; // which splits single-token sequences itself; units 0: the splits below
-  bool f32_kernel;     // large tiles by hc_attn_f32.cu
+  bool f32_kernel;     // large tiles by hc_attn_f32.cu, and then no small ones
   int splits;          // the larger of the two
 };
 
@@ -510,27 +510,31 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
     d.part_o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + align_up(rows * 8, 256));
   }
   if (p.tile) return launch_attn_tile(d, a.dtype, a.workspace, num_sms, s);
-  // (where longer sequences go to the large tiles, a sequence's one small tile is the slot of its number)
-  const int64_t slots = p.use_large ? a.seqs : slots_of(a, p.small.rows);
-  d.g = p.small;
-  d.min_rows = 1;
-  d.max_rows = p.use_large ? kSmallRows : INT64_MAX;
-  d.slot_is_seq = p.use_large;
-  d.spare_ctas = p.pieces.spare_ctas;
-  d.units = p.pieces.units;
-  d.clusters = p.pieces.clusters;
-  cudaError_t e = p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s) : general_d<T, kSmallRows>(d, aligned, slots, s);
-  if (e != cudaSuccess) return e;
+  // Sequences of at most small_rows rows go to the small tiles, the others to the large ones (hc_attn_f32.cu takes all of a batch
+  // that has any longer). Where there are both kinds, a sequence's one small tile is the slot of its number.
+  const int64_t small_rows = !p.use_large ? INT64_MAX : p.f32_kernel ? 0 : kSmallRows;
+  cudaError_t e = cudaSuccess;
+  if (small_rows > 0) {
+    const int64_t slots = p.use_large ? a.seqs : slots_of(a, p.small.rows);
+    d.g = p.small;
+    d.min_rows = 1;
+    d.max_rows = small_rows;
+    d.slot_is_seq = p.use_large;
+    d.spare_ctas = p.pieces.spare_ctas;
+    d.units = p.pieces.units;
+    d.clusters = p.pieces.clusters;
+    e = p.rows_kernel ? launch_attn_rows(d, a.dtype, slots, s) : general_d<T, kSmallRows>(d, aligned, slots, s);
+    if (e != cudaSuccess) return e;
+  }
   if (p.use_large) {
     d.g = p.large;
     d.slot_is_seq = false;
-    d.min_rows = kSmallRows + 1;
+    d.min_rows = small_rows + 1;
     d.max_rows = INT64_MAX;
-    const int64_t large_slots = slots_of(a, p.large.rows);
-    e = p.f32_kernel ? launch_attn_f32(d, large_slots, s) : general_d<T, 64>(d, aligned, large_slots, s);
+    const int64_t slots = slots_of(a, p.large.rows);
+    e = p.f32_kernel ? launch_attn_f32(d, slots, s) : general_d<T, 64>(d, aligned, slots, s);
     if (e != cudaSuccess) return e;
   }
-  const int64_t small_rows = p.use_large ? kSmallRows : INT64_MAX;
   if (p.splits > 1) {
     const int64_t rows = a.tokens * a.heads;
     if (p.splits > 8 && rows < 4096) {

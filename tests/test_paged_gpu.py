@@ -311,6 +311,15 @@ def test_attention_chunks(hc, dtype, case):
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page", [1, 4, 8, 24, 128, 384, 512])
+def test_attention_page_sizes(hc, dtype, dim, page):
+    """Pages that divide the kernels' blocks of keys, are multiples of them, or neither."""
+    Batch(67, [(70, 700), (1, 513), (3, 3)], 4, 2, dim, page, dtype).check(hc, window=300)
+    Batch(71, [(1, 700), (1, 513)], 4, 2, dim, page, dtype, cu=False).check(hc)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
 @pytest.mark.parametrize("layout", ["head", "gaps"])
 def test_attention_layouts(hc, dtype, layout):
     Batch(19, [(1, 300), (1, 45)], 8, 2, 128, 16, dtype, cu=False, layout=layout).check(hc)
