@@ -17,6 +17,8 @@
 // them; a single one writes the result itself.
 #pragma once
 
+#include <type_traits>
+
 #include "hc_common.cuh"
 #include "hc_paged_batch.cuh"
 
@@ -127,6 +129,13 @@ __device__ __forceinline__ void row_owner(const AttnArgs& a, const AttnTile& t, 
 
 __device__ __forceinline__ int64_t part_index(const AttnArgs& a, int z, int64_t token, int head) {
   return (static_cast<int64_t>(z) * a.tokens + token) * a.heads + head;
+}
+
+// Whether either of two 16-bit numbers is infinite or NaN.
+template <typename T>
+__device__ __forceinline__ bool not_finite2(uint32_t w) {
+  constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+  return __vcmpeq2(w & kExp, kExp) != 0;
 }
 
 // Score to base-2 exponent: scale * log2(e), and with a cap c on the scaled

@@ -73,11 +73,56 @@ __device__ __forceinline__ Parts cut(float x, float y) {
                upper_pair(__float_as_uint(x2), __float_as_uint(y2))};
 }
 
+// Infinite and NaN values at keys that only some of a tile's rows see, which go
+// into the products as zeros (a weight of zero must meet a finite value) and are
+// added at the end to the rows that see them, where any weight above zero gives
+// the same. Past kMost of them (a token whose whole value is NaN has as many as
+// features) the rows that see any of these keys become NaN.
+struct OddValues {
+  static constexpr int kMost = 32;
+  static constexpr int kSide = 96;  // keys where the rows' views begin, or end: 64 rows' and a block's rest
+  static constexpr int kWords = 2 * kSide / 32;
+  int count, lower, all_from, all_to;  // (keys are relative to the split's first)
+  int key[kMost], feature[kMost];
+  float value[kMost];
+  uint32_t keys[kWords];  // keys with such values: from `lower` on, and from all_to on
+};
+__device__ __forceinline__ int odd_place(const OddValues& s, int key) {
+  return key < s.all_from ? min(key - s.lower, OddValues::kSide - 1) : OddValues::kSide + min(key - s.all_to, OddValues::kSide - 1);
+}
+__device__ __noinline__ float4 odd_taken(OddValues& s, float4 x, int key, int feature) {
+  float v[4] = {x.x, x.y, x.z, x.w};
+  for (int e = 0; e < 4; ++e) {
+    if (isfinite(v[e])) continue;
+    const int n = atomicAdd(&s.count, 1), at = odd_place(s, key);
+    atomicOr(&s.keys[at >> 5], 1u << (at & 31));
+    if (n < OddValues::kMost) {
+      s.key[n] = key;
+      s.feature[n] = feature + e;
+      s.value[n] = v[e];
+    }
+    v[e] = 0.0f;
+  }
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void set_odd_aside(OddValues& s, float4& x, int key, int feature) {
+  if (key < s.all_from || key >= s.all_to) x = odd_taken(s, x, key, feature);
+}
+__device__ __noinline__ bool sees_odd(const OddValues& s, int from, int to) {
+  for (int i = 0; i < OddValues::kSide; ++i) {
+    if ((s.keys[i >> 5] >> (i & 31) & 1) && s.lower + i >= from && s.lower + i < to) return true;
+    const int at = OddValues::kSide + i;
+    if ((s.keys[at >> 5] >> (at & 31) & 1) && s.all_to + i >= from && s.all_to + i < to) return true;
+  }
+  return false;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
   using C = TileCfg<D>;
   using M = Mma<__nv_bfloat16>;
   extern __shared__ __align__(128) unsigned char tile_smem[];
+  __shared__ OddValues aside;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
   const int z = blockIdx.z, kvh = blockIdx.y;
   pdl_trigger();
@@ -108,7 +153,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
       held[1][i] = *reinterpret_cast<const float4*>(vp + at);
     }
   };
-  const auto store = [&](unsigned char* to) {
+  const auto store = [&](int b) {
+    unsigned char* const to = parts + (b & 1) * C::kBlock;
 #pragma unroll
     for (int i = 0; i < C::kLoads; ++i) {
       const uint32_t at = chunk_at<D>(i * C::kAtOnce + row_of, piece >> 1) + (piece & 1) * 8;
@@ -116,6 +162,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
       for (int kind = 0; kind < 2; ++kind) {
         float4 x = held[kind][i];
         unsigned char* dst = to + kind * 4 * C::kPart + at;
+        if (kind == 1 && !(isfinite(x.x) && isfinite(x.y) && isfinite(x.z) && isfinite(x.w)))
+          set_odd_aside(aside, x, b * kTileKeys + i * C::kAtOnce + row_of, piece * 4);
         const auto put = [&](int part, uint32_t lo, uint32_t hi) {
           *reinterpret_cast<uint2*>(dst + part * C::kPart) = make_uint2(lo, hi);
         };
@@ -131,6 +179,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
       }
     }
   };
+  {
+    // keys that all of the tile's rows see, relative to k0
+    const int64_t first = row_position(t, t.row0, a.group), last = row_position(t, t.row0 + t.rows - 1, a.group);
+    const auto rel = [&](int64_t j) { return static_cast<int>(max(min(j - k0, k1 - k0), int64_t{0})); };
+    if (threadIdx.x < OddValues::kWords) aside.keys[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+      aside.count = 0;
+      aside.lower = rel(t.lo);
+      aside.all_from = a.window > 0 ? rel(last - a.window + 1) : 0;
+      aside.all_to = rel(first + 1);
+    }
+    __syncthreads();
+  }
   if (blocks > 0) load(0);
   // queries: a warp cuts its own 16 rows (those past the last are zeros)
   const int row0 = warp * 16;
@@ -149,7 +210,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
     *reinterpret_cast<uint2*>(dst + kTileRows * C::kRow) = make_uint2(lo.p1, hi.p1);
     *reinterpret_cast<uint2*>(dst + 2 * kTileRows * C::kRow) = make_uint2(lo.p2, hi.p2);
   }
-  if (blocks > 0) store(parts);
+  if (blocks > 0) store(0);
   if (blocks > 1) load(1);
   __syncthreads();
 
@@ -182,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
   for (int b = 0; b < blocks; ++b) {
     const uint32_t k_at = parts_at + (b & 1) * C::kBlock, v_at = k_at + 4 * C::kPart;
     // the next block into the other buffer (all warps are done with it), the one after on its way
-    if (b + 1 < blocks) store(parts + ((b + 1) & 1) * C::kBlock);
+    if (b + 1 < blocks) store(b + 1);
     if (b + 2 < blocks) load(b + 2);
     if (row0 < t.rows) {
       float s[2][4] = {}, c[2][4] = {};  // first parts' products, and the corrections
@@ -280,6 +341,25 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
     __syncthreads();
   }
   if (row0 >= t.rows) return;
+  if (aside.count > 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool all = aside.count > OddValues::kMost && sees_odd(aside, from[i], to[i]);
+      for (int n = 0; n < min(aside.count, OddValues::kMost); ++n) {
+        const int key = aside.key[n], d0 = aside.feature[n];
+        if (key < from[i] || key >= to[i] || (d0 & 7) >> 1 != q4) continue;
+        const float v = aside.value[n];
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) {
+          if (d0 == d * 8 + q4 * 2) o[d][2 * i] += v;
+          if (d0 == d * 8 + q4 * 2 + 1) o[d][2 * i + 1] += v;
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d)
+        if (all) o[d][2 * i] = o[d][2 * i + 1] = __int_as_float(0x7fffffff);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);

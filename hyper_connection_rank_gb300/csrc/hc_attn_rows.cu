@@ -293,7 +293,7 @@ __device__ __forceinline__ void write_rows(const AttnArgs& a, const AttnTile& t,
 }
 
 template <typename T, int D, int SHARE>
-__global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 3) rows_kernel(AttnArgs a) {
   constexpr int kChunks = D / 8;                 // 16-byte chunks of a row
   constexpr int kHalf = kBlock * D * 2;          // bytes of a block's keys
   constexpr int kStage = 2 * kHalf;              // and of its values
@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
   }
   all_to = rel(row_position(t, t.row0, a.group) + 1);  // seen by every row: [all_from, all_to)
   if (a.window > 0) all_from = rel(row_position(t, t.row0 + t.rows - 1, a.group) - a.window + 1);
+  const bool uneven = row_position(t, t.row0, a.group) != row_position(t, t.row0 + t.rows - 1, a.group);
 
   const ScoreMap map = score_map(a.scale, a.softcap);
   float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.0f, 0.0f};
@@ -459,12 +460,57 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(AttnArgs a) {
       p[2 * n] = pack2<T>(s[n][0], s[n][1]);
       p[2 * n + 1] = pack2<T>(s[n][2], s[n][3]);
     }
+    const auto load_values = [&](int d, uint32_t(&v)[4]) {
+      ldsm_x4_trans(vs_at + chunk_at<D>(lane & 15, 2 * d + (lane >> 4)), v[0], v[1], v[2], v[3]);
+    };
+    // Keys that only some of the rows see: for the others their weight is zero, which only a finite value takes to zero.
+    bool care = false;
+    if (SHARE == kBySplit && uneven && !whole) {  // (else all rows are one token's)
+      bool bad = false;
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) {
-      uint32_t b0, b1, b2, b3;
-      ldsm_x4_trans(vs_at + chunk_at<D>(lane & 15, 2 * d + (lane >> 4)), b0, b1, b2, b3);
-      Mma<T>::run4(o[2 * d], p, b0, b1);
-      Mma<T>::run4(o[2 * d + 1], p, b2, b3);
+      for (int d = 0; d < D / 16; ++d) {
+        uint32_t v[4];
+        load_values(d, v);
+        bad |= not_finite2<T>(v[0]) || not_finite2<T>(v[1]) || not_finite2<T>(v[2]) || not_finite2<T>(v[3]);
+      }
+      care = __any_sync(0xffffffffu, bad);
+    }
+    if (!care) {
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        uint32_t v[4];
+        load_values(d, v);
+        Mma<T>::run4(o[2 * d], p, v[0], v[1]);
+        Mma<T>::run4(o[2 * d + 1], p, v[2], v[3]);
+      }
+    } else {
+      // row by row, with the values that the row does not see at zero
+      for (int r = 0; r < t.rows; ++r) {
+        const int owner = (r & 7) * 4;
+        const int f0 = __shfl_sync(0xffffffffu, from[0], owner), f1 = __shfl_sync(0xffffffffu, from[1], owner);
+        const int t0 = __shfl_sync(0xffffffffu, to[0], owner), t1 = __shfl_sync(0xffffffffu, to[1], owner);
+        const int lo = (r < 8 ? f0 : f1) - j0 - 2 * q4, hi = (r < 8 ? t0 : t1) - j0 - 2 * q4;
+        const uint32_t m0 = (0 >= lo && 0 < hi ? 0xffffu : 0u) | (1 >= lo && 1 < hi ? 0xffff0000u : 0u);
+        const uint32_t m1 = (8 >= lo && 8 < hi ? 0xffffu : 0u) | (9 >= lo && 9 < hi ? 0xffff0000u : 0u);
+        const bool mine = g == (r & 7);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t v[4];
+          load_values(d, v);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float y[4] = {};
+            Mma<T>::run4(y, p, v[2 * n] & m0, v[2 * n + 1] & m1);
+            if (mine && r < 8) {
+              o[2 * d + n][0] += y[0];
+              o[2 * d + n][1] += y[1];
+            } else if (mine) {
+              o[2 * d + n][2] += y[2];
+              o[2 * d + n][3] += y[3];
+            }
+          }
+        }
+      }
     }
     __syncwarp();
     stage = stage + 1 == kStages ? 0 : stage + 1;

@@ -148,8 +148,13 @@ struct Run {
 struct Segment {
   AttnTile t;
   int kv_head, j0, j1, n;
-  int64_t at;  // unit of the tile's first block
+  int all_from, all_to;  // keys that every row of the pair sees, from the tile's first block on
+  int64_t at;            // unit of the tile's first block
 };
+// Whether a block of keys holds some that not every row of the tile pair sees.
+__device__ __forceinline__ bool at_edge(const Segment& g, int j) {
+  return j * kKeys < g.all_from || (j + 1) * kKeys > g.all_to;
+}
 
 // The segment that unit u of all lies in, of a run that ends at u1 (full warps).
 __device__ __forceinline__ void segment_at(const Work& w, const Run& run, int64_t u, int64_t u1,
@@ -177,11 +182,6 @@ __device__ __forceinline__ int tile_blocks(const AttnArgs& a, const AttnTile& t,
   const int64_t end = row_position(t, t.row0 + x * kRows + rows - 1, a.group) + 1;
   const int64_t n = (end - t.base + kKeys - 1) / kKeys;
   return n < 1 ? 1 : static_cast<int>(n);
-}
-
-// Whether a block of keys holds some that no row of the tile sees.
-__device__ __forceinline__ bool at_edge(const AttnTile& t, int64_t key0) {
-  return key0 < t.lo || key0 + kKeys > t.hi;
 }
 
 // ------------------------------------------------------------ tensor memory --
@@ -306,6 +306,33 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
 
 // ----------------------------------------------------------------- kernel --
 
+// Infinite or NaN values at keys that only some of a tile's rows see. The copy of the
+// values that the product reads has zeros in their place (a weight of zero must
+// meet a finite value); the rows that see them add them at the end, where any
+// weight above zero gives the same infinity or NaN. Past kOdd of them (a token
+// whose whole value is NaN has as many as features) the rows that see any of
+// these keys become NaN.
+constexpr int kOdd = 8;
+constexpr int kOddBlocks = 8;  // of a tile: its rows' views begin within three blocks, and end within three
+struct OddValues {
+  int count, blocks;
+  int key[kOdd];       // from the tile's first block on
+  uint32_t at[kOdd];   // feature in the upper half, the value's 16 bits in the lower
+  int block[kOddBlocks];               // blocks that not all rows see
+  uint32_t keys[kOddBlocks][4];        // and their keys with such values
+};
+// Whether a row that sees the keys [from, to) sees one with an odd value.
+__device__ __forceinline__ bool sees_odd(const OddValues& list, int from, int to) {
+  bool any = false;
+  for (int b = 0; b < list.blocks; ++b)
+    for (int w = 0; w < 4; ++w) {
+      const int k0 = list.block[b] * kKeys + 32 * w, lo = max(from - k0, 0), hi = min(to - k0, 32);
+      if (lo >= hi) continue;
+      any |= (list.keys[b][w] & (0xffffffffu >> (32 - (hi - lo)) << lo)) != 0;
+    }
+  return any;
+}
+
 struct Bars {
   uint64_t q_full[2];   // a tile's queries lie in shared memory
   uint64_t s_full[2];   // its scores lie in tensor memory
@@ -313,7 +340,8 @@ struct Bars {
   uint64_t o_done[2];   // the product with the values is done
   uint64_t kv_full[8], kv_empty[8];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t edge[8];     // values at a tile's edge have landed and are yet to be cleaned
+  uint64_t odd_full[kSegs];  // a segment's odd values are all listed
+  uint64_t edge[8];     // values that not all rows see have landed and are yet to be cleaned
   uint32_t tmem;
 };
 
@@ -340,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char raw[];
   __shared__ Bars bars;
   __shared__ Segment segs[kSegs];
+  __shared__ OddValues odd[kSegs];
   unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   unsigned char* const ring = smem + 2 * C::kQ;
   // (through a shuffle the compiler knows that a warp's threads agree on it, and keeps what follows from it in uniform registers)
@@ -355,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&bars.seg_full[i], 1);
       mbar_init(&bars.seg_empty[i], kSegUsers);
+      mbar_init(&bars.odd_full[i], 1);
     }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&bars.kv_full[i], 1);
@@ -419,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int kind = 0; kind < 2; ++kind) {
               HC_WAIT(&bars.kv_empty[slot], (round & 1) ^ 1);
-              uint64_t* const full = kind == 1 && at_edge(g.t, key0) ? &bars.edge[slot] : &bars.kv_full[slot];
+              uint64_t* const full = kind == 1 && at_edge(g, j) ? &bars.edge[slot] : &bars.kv_full[slot];
               if (lane == 0) mbar_arrive_expect_tx(full, C::kSlot);
               __syncwarp();
 #pragma unroll
@@ -536,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       multiply_all();
     } else if (warp == kFixWarp) {
-      // ---- values beside the keys that a tile sees may be anything; a weight of zero must meet a zero ----
+      // ---- values that not all rows see: zeros for those that none sees, and for what is not finite ----
       int slot = 0;
       uint32_t edges = 0;  // parity of each slot's edge barrier
       const auto fix_all = [&]() -> bool {
@@ -544,25 +574,78 @@ __global__ void __launch_bounds__(kThreads, 1)
           HC_SEGMENT(seg);
           const Segment& g = segs[seg % kSegs];
           if (g.j1 <= g.j0) return true;
+          OddValues& list = odd[seg % kSegs];
+          if (lane == 0) list.count = list.blocks = 0;
+          int blocks = 0;
+          __syncwarp();
           for (int j = g.j0; j < g.j1; ++j) {
             const int v_slot = slot + 1 == C::kSlots ? 0 : slot + 1;
             slot = v_slot + 1 == C::kSlots ? 0 : v_slot + 1;
             const int64_t key0 = g.t.base + static_cast<int64_t>(j) * kKeys;
-            if (!at_edge(g.t, key0)) continue;
+            if (!at_edge(g, j)) continue;
             HC_WAIT(&bars.edge[v_slot], edges >> v_slot & 1);
             edges ^= 1u << v_slot;
-            const int lo = static_cast<int>(g.t.lo > key0 ? min(g.t.lo - key0, static_cast<int64_t>(kKeys)) : 0);
-            const int hi = static_cast<int>(g.t.hi > key0 ? min(g.t.hi - key0, static_cast<int64_t>(kKeys)) : 0);
-            const int n = (lo + kKeys - hi) * 8 * C::kHalves;
-            for (int e = lane; e < n; e += 32) {
-              const int c = e & 7, h = (e >> 3) % C::kHalves, i = (e >> 3) / C::kHalves;
-              const int r = i < lo ? i : hi + (i - lo);
-              *reinterpret_cast<uint4*>(ring + v_slot * C::kSlot + h * C::kHalf + r * 128 + c * 16) =
-                  make_uint4(0, 0, 0, 0);
+            uint32_t* const odd_keys = list.keys[min(blocks, kOddBlocks - 1)];
+            if (lane < 4) odd_keys[lane] = 0;
+            if (lane == 0) list.block[min(blocks, kOddBlocks - 1)] = j;
+            ++blocks;
+            __syncwarp();
+            // rows of the block: none sees those before lo and from hi on, not all those before sure_lo and from sure_hi on
+            const auto in_block = [&](int64_t key) { return static_cast<int>(max(min(key, static_cast<int64_t>(kKeys)), int64_t{0})); };
+            const int lo = in_block(g.t.lo - key0), hi = in_block(g.t.hi - key0);
+            const int sure_lo = in_block(g.all_from - j * kKeys), sure_hi = max(in_block(g.all_to - j * kKeys), sure_lo);
+            constexpr int kPer = 8 * C::kHalves;  // 16-byte chunks of a row
+            const int rows = sure_lo + kKeys - sure_hi;
+            const auto place = [&](int e, int* r, int* feature) {
+              const int i = e / kPer, c = e & 7, h = (e >> 3) % C::kHalves;
+              *r = i < sure_lo ? i : sure_hi + (i - sure_lo);
+              *feature = h * 64 + c * 8;
+              return reinterpret_cast<uint4*>(ring + v_slot * C::kSlot + h * C::kHalf + *r * 128 + ((c ^ (*r & 7)) << 4));
+            };
+            // a half whose exponent is all ones carries into its sign's place
+            constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+            constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+            uint32_t carry = 0;
+#pragma unroll 8
+            for (int e = lane; e < rows * kPer; e += 32) {
+              int r, feature;
+              uint4* const at = place(e, &r, &feature);
+              if (r < lo || r >= hi) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else {
+                const uint4 v = *at;
+                carry |= (v.x & kExp) + kOne | (v.y & kExp) + kOne | (v.z & kExp) + kOne | (v.w & kExp) + kOne;
+              }
+            }
+            if (__any_sync(0xffffffffu, carry & 0x80008000u)) {
+              for (int e = lane; e < rows * kPer; e += 32) {
+                int r, feature;
+                uint4* const at = place(e, &r, &feature);
+                const uint4 v = *at;
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint32_t half = w[i / 2] >> (16 * (i & 1)) & 0xffffu;
+                  if (!not_finite2<T>(half)) continue;
+                  const int n = atomicAdd(&list.count, 1);
+                  atomicOr(&odd_keys[r >> 5], 1u << (r & 31));
+                  if (n < kOdd) {
+                    list.key[n] = j * kKeys + r;
+                    list.at[n] = static_cast<uint32_t>(feature + i) << 16 | half;
+                  }
+                  w[i / 2] &= (i & 1) ? 0xffffu : 0xffff0000u;
+                }
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
+              }
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.kv_full[v_slot]);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            list.blocks = min(blocks, kOddBlocks);
+            mbar_arrive(&bars.odd_full[seg % kSegs]);
           }
           done_with(seg);
         }
@@ -577,7 +660,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t u1 = mine ? run.start(blockIdx.x + 1) : 0;
         for (int seg = 0;; ++seg) {
           Segment g = {};
-          if (u < u1) segment_at(w, run, u, u1, &g);
+          if (u < u1) {
+            segment_at(w, run, u, u1, &g);
+            const int64_t first = row_position(g.t, g.t.row0, a.group) - g.t.base;
+            const int64_t last = row_position(g.t, g.t.row0 + g.t.rows - 1, a.group) - g.t.base;
+            g.all_to = static_cast<int>(first + 1 < 0 ? 0 : first + 1);
+            g.all_from = static_cast<int>(a.window <= 0 || last - a.window + 1 < 0 ? 0 : last - a.window + 1);
+          }
           HC_WAIT(&bars.seg_empty[seg % kSegs], ((seg / kSegs) & 1) ^ 1);
           if (lane == 0) {
             segs[seg % kSegs] = g;
@@ -796,6 +885,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
         }
         if (fetched) hand_q();
+        // what is to be added to features c .. c + 31 of this row's sums
+        HC_WAIT(&bars.odd_full[seg % kSegs], (seg / kSegs) & 1);
+        const OddValues& list = odd[seg % kSegs];
+        const int odds = list.count;
+        const auto add_odd = [&](int c, uint32_t* o) {
+          for (int e = 0; e < min(odds, kOdd); ++e) {
+            const int key = list.key[e], d = static_cast<int>(list.at[e] >> 16) - c;
+            if (d < 0 || d >= 32 || key < from || key >= to) continue;
+            const uint16_t bits = static_cast<uint16_t>(list.at[e]);
+            const float v = Ty<T>::to_f(*reinterpret_cast<const T*>(&bits));
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i == d) o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
+          }
+          if (odds > kOdd && sees_odd(list, from, to))
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0x7fffffffu;
+        };
         if (rows > 0) {
           const bool partial = g.j0 > 0 || g.j1 < g.n;
           const bool real = row < rows;
@@ -809,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(o_at + c, o);
                 tmem_wait_ld();
                 landed32(o);
+                if (odds > 0) add_odd(c, o);
                 write_out(o, reinterpret_cast<unsigned char*>(w.part_o), real ? (at * D + c) * 4 : -1, true);
               }
             }
@@ -828,6 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(o_at + c + 32 * h, o);
                 tmem_wait_ld();
                 landed32(o);
+                if (odds > 0) add_odd(c + 32 * h, o);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                   y[16 * h + i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);

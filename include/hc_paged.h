@@ -109,9 +109,10 @@ hc_status_t hc_rotary_append(const hc_rotary_append_t* args, struct CUstream_st*
  * A token that sees nothing gets out = 0 and lse = -inf. Scores, softmax and
  * sums are fp32; in the fp16/bf16 kernels the weights are rounded to T for the
  * product with the values (the sum of weights is not), out is rounded to T
- * once, lse is fp32. Keys and values that no new token of the sequence sees
- * are not touched by the result, whatever they hold; a NaN or an infinity at
- * a visible position may reach every new token of its sequence.
+ * once, lse is fp32. What a token does not see does not touch its result,
+ * whatever it holds; an infinity or a NaN among what it sees does (more than a
+ * few such values near the end of a token's view may make all its features
+ * NaN).
  *
  * max_q, max_kv: the longest row of new tokens and the longest kv_lens, if the
  * caller knows them (0: unknown). They steer the choice of kernels and how far

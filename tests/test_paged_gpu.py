@@ -415,6 +415,30 @@ def test_attention_nan_reaches_only_its_own(hc, dtype):
     assert torch.equal(got, base)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim,page,flags", [(64, 16, 0), (128, 32, 0), (128, 7, 0), (128, 16, 2)])
+@pytest.mark.parametrize("window", [0, 40])
+def test_attention_unseen_values_may_be_anything(hc, dtype, dim, page, flags, window):
+    """Infinities and NaN in values (and NaN in keys) of tokens that only some of the new tokens see reach those alone: the last
+    new tokens' own, and, with a window, some that only the first of them still see. Few new tokens and many."""
+    for both, at in (([(5, 60)], [58, 59, 17]), ([(3, 3), (2, 130)], [129]), ([(150, 333)], [330, 300, 250, 190, 150])):
+        for what in ("one value", "whole values", "keys"):
+            b = Batch(73, both, 4, 2, dim, page, dtype)
+            s, n = len(both) - 1, both[-1][1]
+            for i, j in enumerate(at):
+                place = (int(b.table[s, j // page]), j % page)
+                if what == "keys":
+                    b.k[place] = math.nan
+                elif what == "whole values":
+                    b.v[place] = math.nan
+                else:
+                    b.v[place][i % 2, (7 * i + 3) % dim] = [math.inf, math.nan, -math.inf][i % 3]
+            out, lse, tol, ltol = R.attention(b.q, b.k, b.v, b.table, b.lens, b.cu, window=window)
+            got, glse = b.run(hc, window=window, flags=flags)
+            within(got, out, tol, what)
+            within(glse, lse, ltol, what + " lse")
+
+
 def test_attention_long_offsets(hc):
     """A pool of more than 2^31 elements, its pages far apart: offsets pass 32 bits."""
     page, kv_heads, dim = 16, 1, 64
