@@ -22,7 +22,7 @@
 // Bound: the warp-level MMAs, of which an m16n8k16 takes 8 cycles of a quarter
 // SM, so that six for a product make 170 multiply-adds a cycle and SM (the CUDA
 // cores have 128, and reached a third of that for want of operands). Three chunks
-// of up to 131 tokens, 20 heads of 128, behind up to 901: XXX us; 1000 tokens
+// of up to 131 tokens, 20 heads of 128, behind up to 901: 113 us; 1000 tokens
 // behind 2000: 36 TFLOP/s, 40% of the MMAs' rate; the rest is cutting and
 // waiting, with two CTAs of four warps to an SM.
 #include "hc_async.cuh"
