@@ -28,7 +28,7 @@
 // Measured: 2047 tokens behind 28001, 32 heads of 128 on 8, bf16: 567 us, 1.72
 // PFLOP/s, 89% of the measured burst rate (640 us where it runs on for long and meets
 // the power limit: 87% of the sustained rate). 17 sequences of 1 to 301 tokens,
-// window 1000, scores capped, 20 heads of 64 on 4, fp16: 79 us, of which some 15
+// window 1000, scores capped, 20 heads of 64 on 4, fp16: 71 us, of which some 15
 // are plan, start and joining; a block of keys takes a tile pair of 64 features
 // about 2 us then, the capped scores' multiply-adds and exponentials of two warps to a
 // scheduler.
@@ -819,10 +819,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (masked) {
+            // (a bit for each key, so that a score costs one test: with two comparisons a score, the
+            // batch of 17 sequences above took 79 us and not 71)
             const int lo = from - j0, hi = to - j0;
 #pragma unroll
-            for (int c = 0; c < kKeys; ++c)
-              if (c < lo || c >= hi) f[c] = neg_inf();
+            for (int h = 0; h < kKeys; h += 32) {
+              const int below = min(max(lo - h, 0), 32), upto = min(max(hi - h, 0), 32);
+              const uint32_t seen = upto > below ? 0xffffffffu >> (32 - (upto - below)) << below : 0u;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(seen >> c & 1)) f[h + c] = neg_inf();
+            }
           }
           const float mul = CAP ? 1.0f : map.mul;
           if (!CAP || !inside || masked) top = extremes();
