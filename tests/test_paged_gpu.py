@@ -364,6 +364,20 @@ def test_attention_magnitudes(hc, dtype, dim):
         b.check(hc, "no scale", scale=0.0)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("scale", [0.001, 0.02, 0.05, 0.2, 2.0])
+def test_attention_caps(hc, dtype, dim, scale):
+    """Scores that are small against the cap, near it, beyond it, and in one block all of these."""
+    for both in ([(1, 300)], [(140, 700), (9, 20)]):
+        b = Batch(83, both, 4, 2, dim, 16, dtype, cu=both[0][0] > 1)
+        b.check(hc, "whole", softcap=5.0, scale=scale)
+        b.check(hc, "window", softcap=5.0, scale=scale, window=90)
+        b.q[::3] *= 0.05
+        b.k[:, 5] *= 4
+        b.check(hc, "mixed", softcap=5.0, scale=scale)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=ids)
 def test_attention_split_and_not_split_agree(hc, dtype):
     """One sequence is split over the GPU, a hundred are not; both within the bound, so the split's joining is exact."""
