@@ -390,6 +390,41 @@ def test_attention_split_and_not_split_agree(hc, dtype):
     Batch(43, [(90, 2000)], 8, 2, 128, 16, dtype).check(hc, "low bounds", max_kv=64, max_q=1)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("hints", [(0, 0), (1, 1), (7, 30), (10 ** 6, 10 ** 9)], ids=lambda h: f"q{h[0]}kv{h[1]}")
+def test_attention_wrong_hints(hc, dtype, dim, hints):
+    """Bounds that are too low or too high choose the kernel and the split, not the result."""
+    kw = dict(max_q=hints[0], max_kv=hints[1])
+    Batch(101, [(1, 700), (1, 0), (1, 33)], 8, 2, dim, 16, dtype, cu=False).check(hc, "single", **kw)
+    Batch(103, [(1, 700), (40, 600), (0, 9), (5, 5)], 8, 2, dim, 16, dtype).check(hc, "chunks", window=70, **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("both", [[(1, 320), (1, 160)], [(70, 320), (1, 160)]], ids=["single", "chunk"])
+def test_attention_lengths_and_pages_out_of_range(hc, dtype, dim, both):
+    """A length past what the table's row holds is cut to it; a negative one counts as none; a sequence with pages outside the
+    pool disturbs no other."""
+    b = Batch(107, both, 8, 2, dim, 16, dtype, cu=both[0][0] > 1)
+    b.table = b.table[:, :20].contiguous()
+    out, lse, tol, ltol = R.attention(b.q, b.k, b.v, b.table, b.lens, b.cu)
+    b.lens = torch.tensor([2 ** 31 - 1, 160], dtype=torch.int32)
+    got, glse = b.run(hc)
+    within(got, out, tol, "long")
+    within(glse, lse, ltol, "long lse")
+    b.table[0, 3], b.table[0, 4] = -1, 10 ** 9
+    n = both[0][0]
+    got, glse = b.run(hc)
+    within(got[n:], out[n:], tol[n:], "beside missing pages")
+    within(glse[n:], lse[n:], ltol[n:], "beside missing pages, lse")
+    b.lens = torch.tensor([-5, 160], dtype=torch.int32)
+    got, glse = b.run(hc)
+    assert bool((got[:n] == 0).all()) and bool((glse[:n] == -math.inf).all())
+    within(got[n:], out[n:], tol[n:], "beside none")
+    assert hc.debug_wait_timeouts() == 0
+
+
 def test_attention_chunk_by_chunk(hc):
     """A prompt read at once and in pieces gives every token the same result, within the bounds of both."""
     f, _ = hc.rotary_frequencies(128)
