@@ -151,11 +151,11 @@ hc_status_t hc_rotary(const hc_rotary_t* args, cudaStream_t stream) {
       span("x", in_place ? nullptr : a.x, es * extent(a.tokens, a.x_token_stride, a.heads, a.x_head_stride, a.head_dim)),
       span("positions", a.positions, a.tokens * (a.positions32 ? 4 : 8)), span("inv_freq", a.inv_freq, a.rot_dim * 4)};
   HC_RETURN_IF(check_apart(&out, 1, ins, 3));
-  int sms = 0;
+  int sms = 0;  // (only to refuse other devices)
   HC_RETURN_IF(hc::current_device_sms(&sms));
   const bool vec = aligned16(a.x) && aligned16(a.out) &&
                    vec_strides(a.dtype, {a.x_token_stride, a.x_head_stride, a.out_token_stride, a.out_head_stride});
-  return launched(hc::launch_rotary(a, vec, sms, stream));
+  return launched(hc::launch_rotary(a, vec, stream));
 }
 
 hc_status_t hc_rotary_append(const hc_rotary_append_t* args, cudaStream_t stream) {
@@ -203,14 +203,14 @@ hc_status_t hc_rotary_append(const hc_rotary_append_t* args, cudaStream_t stream
   HC_RETURN_IF(check_apart(&kc, 1, ins, 4));
   HC_RETURN_IF(check_apart(&vc, 1, ins, 4));
   if (a.k_cache == a.v_cache) return fail(HC_ERR_INVALID_ARG, "k_cache is v_cache");
-  int sms = 0;
+  int sms = 0;  // (only to refuse other devices)
   HC_RETURN_IF(hc::current_device_sms(&sms));
   const bool vec = aligned16(a.q) && aligned16(a.k) && aligned16(a.v) && aligned16(a.q_out) && aligned16(a.k_cache) &&
                    aligned16(a.v_cache) &&
                    vec_strides(a.dtype, {a.q_token_stride, a.q_head_stride, a.k_token_stride, a.k_head_stride,
                                          a.v_token_stride, a.v_head_stride, a.out_token_stride, a.out_head_stride,
                                          a.cache_page_stride, a.cache_token_stride, a.cache_head_stride});
-  return launched(hc::launch_rotary_append(a, vec, sms, stream));
+  return launched(hc::launch_rotary_append(a, vec, stream));
 }
 
 namespace {

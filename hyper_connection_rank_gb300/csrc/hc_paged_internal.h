@@ -10,8 +10,8 @@ namespace hc {
 
 // Rotary positions (hc_rotary.cu). `vec`: pointers and strides allow 16-byte
 // accesses.
-cudaError_t launch_rotary(const hc_rotary_t& a, bool vec, int num_sms, cudaStream_t s);
-cudaError_t launch_rotary_append(const hc_rotary_append_t& a, bool vec, int num_sms, cudaStream_t s);
+cudaError_t launch_rotary(const hc_rotary_t& a, bool vec, cudaStream_t s);
+cudaError_t launch_rotary_append(const hc_rotary_append_t& a, bool vec, cudaStream_t s);
 
 // Attention (hc_attn.cu). `aligned`: every pointer is 16-byte aligned and the
 // strides are multiples of 16 bytes.

@@ -10,18 +10,20 @@
 // number of half turns in [-1, 1), go to sincospif. What is left is u's own
 // rounding (2^-53 relative) and one fp32 rounding of the half turns.
 //
-// Bound: bytes; every element is read and written once. One CTA serves one or
-// two tokens; their sines and cosines are formed once in shared memory (rot_dim/2
-// per token, against heads * rot_dim elements that use them), and each thread
+// Bound: bytes; every element is read and written once. A CTA of 128 threads
+// serves a token; its sines and cosines are formed once in shared memory (rot_dim/2,
+// against heads * rot_dim elements that use them), and each thread
 // then turns 16 bytes of each side of the pairs at a time. The half layout
 // takes the two sides from one head's two halves, the interleaved one has both
-// sides in one vector. Eight CTAs of 32 registers a thread share an SM;
+// sides in one vector. Sixteen CTAs of 32 registers a thread share an SM;
 // forms that held two or four vectors of the next heads in registers ran at
-// half the occupancy and took 76 to 113 us where this takes 57.
+// half the occupancy and took 76 to 113 us where the form without took 57. Small CTAs
+// keep the last wave short: two tokens to 256 threads took 20.1 and 57.4 us for the sizes
+// below, one token to 256 threads 20.8 and 61.9, to 64 threads 21.3 and 63.7.
 //
 // Measured (bf16, 13638 tokens of 32 + 2 * 8 heads of 128 written into pages of
-// 64): 57 us, 5.9 TB/s, 88% of the measured copy bandwidth; the angles read
-// with bank conflicts cost 66 us. float32, 4099 tokens of 20 heads: 19.7 us, 4.3
+// 64): 55.4 us, 6.05 TB/s, 90% of the measured copy bandwidth; the angles read
+// with bank conflicts cost 9 us more. float32, 4099 tokens of 20 heads: 18.8 us, 4.5
 // TB/s (6.5 us of that is what a single token takes: a launch and a chain of
 // four loads).
 #include "hc_common.cuh"
@@ -31,7 +33,7 @@
 namespace hc {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Pack {
@@ -110,93 +112,78 @@ __device__ __forceinline__ void turn_item(const T* src, T* dst, int it, int rot,
   }
 }
 
-// V elements per access; TPB tokens per CTA. Dynamic shared memory: rot/2
-// 64-bit fractions, then TPB * rot/2 (cos, sin).
+// V elements per access; a CTA to a token. Dynamic shared memory: rot/2 (cos, sin).
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int tpb) {
+__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ int64_t s_pos[32];
-  __shared__ int64_t s_slot[32];  // element offset of the token in the pool, -1: nowhere
+  __shared__ int64_t s_pos;
+  __shared__ int64_t s_slot;  // element offset of the token in the pool, -1: nowhere
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int half = a.rot >> 1;
-  uint64_t* frac = reinterpret_cast<uint64_t*>(smem);
-  float2* cs = reinterpret_cast<float2*>(frac + half);
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tpb;
-  const int nt = static_cast<int>(a.tokens - t0 < tpb ? a.tokens - t0 : tpb);
+  const int half = a.rot >> 1, heads = a.hq + 2 * a.hk;
+  float2* cs = reinterpret_cast<float2*>(smem);
+  const int64_t t = blockIdx.x;
 
-  // the tokens' rows are on their way to the L2 while the angles are formed: one prefetch to a head of 128 bytes and more
+  // the token's rows are on their way to the L2 while the angles are formed: one prefetch to a head of 128 bytes and more
   {
-    const int lines = (a.dim * static_cast<int>(sizeof(T)) + 127) / 128, all = a.hq + 2 * a.hk;
-    for (int i = tid; i < nt * all * lines; i += kThreads) {
-      const int u = i / lines, j = u / all, h = u - j * all;
-      const int64_t t = t0 + j;
+    const int lines = (a.dim * static_cast<int>(sizeof(T)) + 127) / 128;
+    for (int i = tid; i < heads * lines; i += kThreads) {
+      const int h = i / lines;
       const T* src = h < a.hq           ? static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs
                      : h < a.hq + a.hk  ? static_cast<const T*>(a.k) + t * a.k_ts + (h - a.hq) * a.k_hs
                                         : static_cast<const T*>(a.v) + t * a.v_ts + (h - a.hq - a.hk) * a.v_hs;
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (i - u * lines) * (128 / static_cast<int>(sizeof(T)))));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (i - h * lines) * (128 / static_cast<int>(sizeof(T)))));
     }
   }
-  for (int i = tid; i < half; i += kThreads) {
+  // frequencies as fractions of a turn, the first of each thread while the position is on its way
+  const auto fraction = [&](int i) {
     double f = a.inv_freq[i] * 0.15915494309189535;  // turns per token
     f -= floor(f);
-    frac[i] = __double2ull_rn(f * 18446744073709551616.0);
-  }
+    return __double2ull_rn(f * 18446744073709551616.0);
+  };
+  const uint64_t first = tid < half ? fraction(tid) : 0;
   if (a.positions != nullptr) {
-    if (tid < nt)
-      s_pos[tid] = a.positions32 ? static_cast<const int32_t*>(a.positions)[t0 + tid]
-                                 : static_cast<const int64_t*>(a.positions)[t0 + tid];
-  } else {
-    for (int j = warp; j < nt; j += kThreads / 32) {
-      const int64_t t = t0 + j;
-      const BatchView& b = a.batch;
-      const int s = b.cu_q ? warp_last_le(b.seqs, t, [&](int i) { return first_row(b, i); })
-                           : static_cast<int>(t);
-      if (lane == 0) {
-        const int64_t end = first_row(b, s + 1);
-        const int64_t pos = kv_len_of(b, s) - (end - t);
-        int page = -1;
-        if (pos >= 0) page = page_of(b, s, pos / b.page_size);
-        s_pos[j] = pos;
-        s_slot[j] = page < 0 ? -1 : page * a.c_ps + pos % b.page_size * a.c_ts;
-      }
+    if (tid == 0)
+      s_pos = a.positions32 ? static_cast<const int32_t*>(a.positions)[t] : static_cast<const int64_t*>(a.positions)[t];
+  } else if (warp == kThreads / 32 - 1) {
+    const BatchView& b = a.batch;
+    const int s = b.cu_q ? warp_last_le(b.seqs, t, [&](int i) { return first_row(b, i); })
+                         : static_cast<int>(t);
+    if (lane == 0) {
+      const int64_t end = first_row(b, s + 1);
+      const int64_t pos = kv_len_of(b, s) - (end - t);
+      int page = -1;
+      if (pos >= 0) page = page_of(b, s, pos / b.page_size);
+      s_pos = pos;
+      s_slot = page < 0 ? -1 : page * a.c_ps + pos % b.page_size * a.c_ts;
     }
   }
   __syncthreads();
-  for (int i = tid; i < nt * half; i += kThreads) {
-    const int j = i / half, f = i - j * half;
-    const int32_t turn = static_cast<int32_t>((static_cast<uint64_t>(s_pos[j]) * frac[f]) >> 32);
+  for (int i = tid; i < half; i += kThreads) {
+    const int32_t turn = static_cast<int32_t>((static_cast<uint64_t>(s_pos) * (i == tid ? first : fraction(i))) >> 32);
     float s, c;
     sincospif(static_cast<float>(turn) * 4.656612873077393e-10f, &s, &c);  // half turns: turn * 2^-31
     constexpr int kPairs = Angles<V, INTER>::kPairs;
-    cs[j * half + Angles<V, INTER>::at(f / kPairs, f % kPairs, half)] =
-        make_float2(a.amplitude * c, a.amplitude * a.sign * s);
+    cs[Angles<V, INTER>::at(i / kPairs, i % kPairs, half)] = make_float2(a.amplitude * c, a.amplitude * a.sign * s);
   }
   __syncthreads();
 
   // threads: `items` to a head, as many heads at a time as fit
   const int items = items_of<V, INTER>(a.dim, a.rot);
-  const int heads = a.hq + 2 * a.hk;
   const int hpp = items < kThreads ? kThreads / items : 1;
   const int ih = items < kThreads ? tid / items : 0;
   if (ih >= hpp) return;
   for (int it = items < kThreads ? tid - ih * items : tid; it < items; it += kThreads) {
-    for (int j = 0, h = ih; j < nt; h += hpp) {
-      while (h >= heads && j < nt) {
-        h -= heads;
-        ++j;
-      }
-      if (j >= nt) break;
-      const int64_t t = t0 + j;
+    for (int h = ih; h < heads; h += hpp) {
       if (h < a.hq) {
         turn_item<T, V, INTER>(static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs,
-                               static_cast<T*>(a.q_out) + t * a.o_ts + h * a.o_hs, it, a.rot, cs + j * half);
+                               static_cast<T*>(a.q_out) + t * a.o_ts + h * a.o_hs, it, a.rot, cs);
       } else {
-        if (s_slot[j] < 0) continue;
+        if (s_slot < 0) break;
         const int kh = h < a.hq + a.hk ? h - a.hq : h - a.hq - a.hk;
-        const int64_t to = s_slot[j] + kh * a.c_hs;
+        const int64_t to = s_slot + kh * a.c_hs;
         if (h < a.hq + a.hk) {
           turn_item<T, V, INTER>(static_cast<const T*>(a.k) + t * a.k_ts + kh * a.k_hs,
-                                 static_cast<T*>(a.k_cache) + to, it, a.rot, cs + j * half);
+                                 static_cast<T*>(a.k_cache) + to, it, a.rot, cs);
         } else {
           const T* src = static_cast<const T*>(a.v) + t * a.v_ts + kh * a.v_hs;
           for (int c = it; c < a.dim / V; c += items)
@@ -209,42 +196,35 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, int tpb)
 }
 
 template <typename T, int V, bool INTER>
-cudaError_t launch_t(const RotaryArgs& a, int num_sms, cudaStream_t s) {
-  // Few tokens: one per CTA, so that they spread over the SMs. Many: more per
-  // CTA, so that the frequencies are converted once for several tokens.
-  int tpb = 1;
-  while (tpb < 2 && a.tokens / (tpb * 2) >= num_sms * 8) tpb *= 2;
-  const int half = a.rot / 2;
-  const size_t smem = static_cast<size_t>(half) * 8 * (1 + tpb);
-  const unsigned grid = static_cast<unsigned>((a.tokens + tpb - 1) / tpb);
-  rotary_kernel<T, V, INTER><<<grid, kThreads, smem, s>>>(a, tpb);
+cudaError_t launch_t(const RotaryArgs& a, cudaStream_t s) {
+  rotary_kernel<T, V, INTER><<<static_cast<unsigned>(a.tokens), kThreads, static_cast<size_t>(a.rot / 2) * 8, s>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T, bool INTER>
-cudaError_t launch_v(const RotaryArgs& a, bool vec, int num_sms, cudaStream_t s) {
+cudaError_t launch_v(const RotaryArgs& a, bool vec, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   // 16-byte vectors where every part of a head is whole ones, else element by element
   const bool whole = vec && a.dim % V == 0 && a.rot % (INTER ? V : 2 * V) == 0;
-  return whole ? launch_t<T, V, INTER>(a, num_sms, s) : launch_t<T, 1, INTER>(a, num_sms, s);
+  return whole ? launch_t<T, V, INTER>(a, s) : launch_t<T, 1, INTER>(a, s);
 }
 
-cudaError_t launch_any(const RotaryArgs& a, int dtype, bool interleaved, bool vec, int num_sms, cudaStream_t s) {
+cudaError_t launch_any(const RotaryArgs& a, int dtype, bool interleaved, bool vec, cudaStream_t s) {
   if (a.tokens == 0) return cudaSuccess;
   switch (dtype) {
     case HC_F32:
-      return interleaved ? launch_v<float, true>(a, vec, num_sms, s) : launch_v<float, false>(a, vec, num_sms, s);
+      return interleaved ? launch_v<float, true>(a, vec, s) : launch_v<float, false>(a, vec, s);
     case HC_F16:
-      return interleaved ? launch_v<__half, true>(a, vec, num_sms, s) : launch_v<__half, false>(a, vec, num_sms, s);
+      return interleaved ? launch_v<__half, true>(a, vec, s) : launch_v<__half, false>(a, vec, s);
     default:
-      return interleaved ? launch_v<__nv_bfloat16, true>(a, vec, num_sms, s)
-                         : launch_v<__nv_bfloat16, false>(a, vec, num_sms, s);
+      return interleaved ? launch_v<__nv_bfloat16, true>(a, vec, s)
+                         : launch_v<__nv_bfloat16, false>(a, vec, s);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_rotary(const hc_rotary_t& r, bool vec, int num_sms, cudaStream_t s) {
+cudaError_t launch_rotary(const hc_rotary_t& r, bool vec, cudaStream_t s) {
   RotaryArgs a = {};
   a.q = r.x;
   a.q_out = r.out;
@@ -261,10 +241,10 @@ cudaError_t launch_rotary(const hc_rotary_t& r, bool vec, int num_sms, cudaStrea
   a.rot = r.rot_dim;
   a.amplitude = r.amplitude;
   a.sign = r.inverse ? -1.0f : 1.0f;
-  return launch_any(a, r.dtype, r.interleaved != 0, vec, num_sms, s);
+  return launch_any(a, r.dtype, r.interleaved != 0, vec, s);
 }
 
-cudaError_t launch_rotary_append(const hc_rotary_append_t& r, bool vec, int num_sms, cudaStream_t s) {
+cudaError_t launch_rotary_append(const hc_rotary_append_t& r, bool vec, cudaStream_t s) {
   RotaryArgs a = {};
   a.q = r.q;
   a.k = r.k;
@@ -292,7 +272,7 @@ cudaError_t launch_rotary_append(const hc_rotary_append_t& r, bool vec, int num_
   a.amplitude = r.amplitude;
   a.sign = 1.0f;
   a.batch = BatchView{r.page_table, r.kv_lens, r.cu_q, r.table_stride, r.num_pages, r.seqs, r.max_pages, r.page_size, r.tokens};
-  return launch_any(a, r.dtype, r.interleaved != 0, vec, num_sms, s);
+  return launch_any(a, r.dtype, r.interleaved != 0, vec, s);
 }
 
 }  // namespace hc
