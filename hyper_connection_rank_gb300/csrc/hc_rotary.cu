@@ -15,14 +15,14 @@
 // against heads * rot_dim elements that use them), and each thread
 // then turns 16 bytes of each side of the pairs at a time. The half layout
 // takes the two sides from one head's two halves, the interleaved one has both
-// sides in one vector. Sixteen CTAs of 32 registers a thread share an SM;
+// sides in one vector. Up to sixteen CTAs share an SM;
 // forms that held two or four vectors of the next heads in registers ran at
 // half the occupancy and took 76 to 113 us where the form without took 57. Small CTAs
 // keep the last wave short: two tokens to 256 threads took 20.1 and 57.4 us for the sizes
 // below, one token to 256 threads 20.8 and 61.9, to 64 threads 21.3 and 63.7.
 //
 // Measured (bf16, 13638 tokens of 32 + 2 * 8 heads of 128 written into pages of
-// 64): 55.4 us, 6.05 TB/s, 90% of the measured copy bandwidth; the angles read
+// 64): 54.6 us, 6.14 TB/s, 92% of the measured copy bandwidth; the angles read
 // with bank conflicts cost 9 us more. float32, 4099 tokens of 20 heads: 18.8 us, 4.5
 // TB/s (6.5 us of that is what a single token takes: a launch and a chain of
 // four loads).
@@ -173,25 +173,25 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
   const int ih = items < kThreads ? tid / items : 0;
   if (ih >= hpp) return;
   for (int it = items < kThreads ? tid - ih * items : tid; it < items; it += kThreads) {
-    for (int h = ih; h < heads; h += hpp) {
-      if (h < a.hq) {
-        turn_item<T, V, INTER>(static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs,
-                               static_cast<T*>(a.q_out) + t * a.o_ts + h * a.o_hs, it, a.rot, cs);
-      } else {
-        if (s_slot < 0) break;
-        const int kh = h < a.hq + a.hk ? h - a.hq : h - a.hq - a.hk;
-        const int64_t to = s_slot + kh * a.c_hs;
-        if (h < a.hq + a.hk) {
-          turn_item<T, V, INTER>(static_cast<const T*>(a.k) + t * a.k_ts + kh * a.k_hs,
-                                 static_cast<T*>(a.k_cache) + to, it, a.rot, cs);
-        } else {
-          const T* src = static_cast<const T*>(a.v) + t * a.v_ts + kh * a.v_hs;
-          for (int c = it; c < a.dim / V; c += items)
-            *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(a.v_cache) + to + c * V) =
-                *reinterpret_cast<const Pack<T, V>*>(src + c * V);
-        }
-      }
+    int h = ih;
+    {
+      const T* src = static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs;
+      T* dst = static_cast<T*>(a.q_out) + t * a.o_ts + h * a.o_hs;
+      for (; h < a.hq; h += hpp, src += hpp * a.q_hs, dst += hpp * a.o_hs) turn_item<T, V, INTER>(src, dst, it, a.rot, cs);
     }
+    if (h >= heads || s_slot < 0) continue;
+    {
+      const T* src = static_cast<const T*>(a.k) + t * a.k_ts + (h - a.hq) * a.k_hs;
+      T* dst = static_cast<T*>(a.k_cache) + s_slot + (h - a.hq) * a.c_hs;
+      for (; h < a.hq + a.hk; h += hpp, src += hpp * a.k_hs, dst += hpp * a.c_hs)
+        turn_item<T, V, INTER>(src, dst, it, a.rot, cs);
+    }
+    const int kh = h - a.hq - a.hk;
+    const T* src = static_cast<const T*>(a.v) + t * a.v_ts + kh * a.v_hs;
+    T* dst = static_cast<T*>(a.v_cache) + s_slot + kh * a.c_hs;
+    for (; h < heads; h += hpp, src += hpp * a.v_hs, dst += hpp * a.c_hs)
+      for (int c = it; c < a.dim / V; c += items)
+        *reinterpret_cast<Pack<T, V>*>(dst + c * V) = *reinterpret_cast<const Pack<T, V>*>(src + c * V);
   }
 }
 
