@@ -15,7 +15,8 @@
 // against heads * rot_dim elements that use them), and each thread
 // then turns 16 bytes of each side of the pairs at a time. The half layout
 // takes the two sides from one head's two halves, the interleaved one has both
-// sides in one vector. Up to sixteen CTAs share an SM;
+// sides in one vector. Ten to sixteen CTAs share an SM (46 to 32
+// registers a thread; held to twelve or sixteen, the first size below takes 1 and 4 us more);
 // forms that held two or four vectors of the next heads in registers ran at
 // half the occupancy and took 76 to 113 us where the form without took 57. Small CTAs
 // keep the last wave short: two tokens to 256 threads took 20.1 and 57.4 us for the sizes
