@@ -275,26 +275,22 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
       : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return d;
 }
-// Scores inside a cap: c log2(e) tanh(k x) with k = scale / c as x P(x^2), where
-// |k x| <= 3/4. P is a polynomial of degree 4, fitted to tanh(sqrt(u)) / sqrt(u)
-// for the least error of tanh over that range (2.7e-7 in float32),
-// k and c worked into its coefficients: five operations on pairs of floats
-// that leave the exponential unit to the softmax. A score of minus infinity, which
-// stands for a key that is not seen, stays one: P's highest coefficient is positive.
-// Where a warp's scores are all within |k x| <= 3/10, degree 2 has no larger an error (1.9e-7)
-// and takes two operations less: 66 us instead of 71 for the batch of 17 sequences above.
+// Scores inside a cap: map_score's polynomial in x, scale / c worked into its
+// coefficients: five operations on pairs of floats that leave the exponential
+// unit to the softmax. A score of minus infinity, which stands for a key that
+// is not seen, stays one: the highest coefficient is positive. Where a
+// coefficient may have lost its precision below float32's normal range, or pass
+// the range, scores go through map_score: with |x| <= 1.8e4 what is lost of the
+// smallest (2^-149 x^8) is below 1e-7 of scale.
 struct CapPoly {
   float c[5];
   float most;  // largest |x|
-  float b[3];
-  float most_b;
 };
 __device__ __forceinline__ CapPoly cap_poly(float scale, float softcap) {
-  const float k = scale / softcap, k2 = k * k, k4 = k2 * k2, c = softcap * kLog2e * k;
-  return CapPoly{{c * 0.999997199f, c * k2 * -0.333230764f, c * k4 * 0.132260919f, c * k4 * k2 * -0.0492804497f, c * k4 * k4 * 0.0123188356f},
-                 k > 1e-4f && k < 1e3f && softcap < 1e9f ? 0.75f / k : -1.0f,  // (a cap beyond these: none is inside)
-                 {c * 0.99999601f, c * k2 * -0.33297479f, c * k4 * 0.12522586f},
-                 0.3f / k};
+  const float k = scale / softcap, k2 = k * k, k4 = k2 * k2, c = scale * kLog2e;
+  const bool fits = scale >= 1e-4f && scale <= 1e4f && k <= 1e3f;
+  return CapPoly{{c * kCap0, c * k2 * kCap1, c * k4 * kCap2, c * k4 * k2 * kCap3, fmaxf(c * k4 * k4 * kCap4, 1e-45f)},
+                 fits ? fminf(kCapTurn / k, 1.8e4f) : -1.0f};
 }
 __device__ __forceinline__ float2 cap_factor(const CapPoly& p, float2 x) {
   const auto twice = [](float v) { return make_float2(v, v); };
@@ -303,11 +299,6 @@ __device__ __forceinline__ float2 cap_factor(const CapPoly& p, float2 x) {
   y = fma2(y, u, twice(p.c[2]));
   y = fma2(y, u, twice(p.c[1]));
   return fma2(y, u, twice(p.c[0]));
-}
-__device__ __forceinline__ float2 cap_factor_near(const CapPoly& p, float2 x) {
-  const auto twice = [](float v) { return make_float2(v, v); };
-  const float2 u = fma2(x, x, twice(0.0f));
-  return fma2(fma2(twice(p.b[2]), u, twice(p.b[1])), u, twice(p.b[0]));
 }
 
 template <typename T>
@@ -793,11 +784,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           HC_WAIT(&bars.s_full[x], s_seen & 1);
           ++s_seen;
           tc_fence_after();
+          const auto load_scores = [&] {
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_at + c, s + c);
-          tmem_wait_ld();
+            for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_at + c, s + c);
+            tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) landed32(s + c);
+            for (int c = 0; c < kKeys; c += 32) landed32(s + c);
+          };
+          load_scores();
           float* f = reinterpret_cast<float*>(s);
           // largest (and, to see whether all are inside the cap, smallest) score
           float tops[4], lows[4];
@@ -813,7 +807,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int j0 = j * kKeys;
           const bool masked = j0 < all_from || j0 + kKeys > all_to;
           bool inside = false;  // scores are still to go through the cap, all well within it
-          bool near = false;    // and are small against it
           float top;
           if (CAP) {
             top = extremes();
@@ -825,10 +818,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 4; ++i) lows[i] = min3(lows[i], f[c + 2 * i], f[c + 2 * i + 1]);
             const float low = fminf(fminf(lows[0], lows[1]), fminf(lows[2], lows[3]));
             inside = !__any_sync(0xffffffffu, fmaxf(top, -low) > poly.most);
-            near = !__any_sync(0xffffffffu, fmaxf(top, -low) > poly.most_b);
             if (!inside) {
+              // (32 at a time from tensor memory and back, in a loop: all 128 in registers spill)
+#pragma unroll 1
+              for (int c = 0; c < kKeys; c += 32) {
+                uint32_t y[32];
+                tmem_ld32(s_at + c, y);
+                tmem_wait_ld();
+                landed32(y);
 #pragma unroll
-              for (int c = 0; c < kKeys; ++c) f[c] = map_score(map, f[c]);
+                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(map_score(map, __uint_as_float(y[i])));
+                tmem_st32(s_at + c, y);
+              }
+              tmem_wait_st();
+              load_scores();
             }
           }
           if (masked) {
@@ -846,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float mul = CAP ? 1.0f : map.mul;
           if (!CAP || !inside || masked) top = extremes();
-          top = inside ? (top == neg_inf() ? top : map_score(map, top)) : top * mul;
+          top *= inside ? cap_factor(poly, make_float2(top, top)).x : mul;
           if (j == g.j0) {
             m = top;
           } else if (__any_sync(0xffffffffu, top > m + kLazy || (m == neg_inf() && top > m))) {
@@ -891,9 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st32(s_at + h / 2, p);
             }
           };
-          if (CAP && inside && near) {
-            weights([&](float2 v) { return cap_factor_near(poly, v); });
-          } else if (CAP && inside) {
+          if (CAP && inside) {
             weights([&](float2 v) { return cap_factor(poly, v); });
           } else {
             weights([&](float2) { return mul2; });

@@ -1,0 +1,80 @@
+"""The paged-cache operators at the ends of their ranges, on the GPU: caps of every size, bytes that nobody sees, streams,
+bounds that end early, values that are not finite."""
+import math
+import random
+
+import pytest
+import torch
+
+import _paged_ref as R
+from test_paged_gpu import BF16, F16, F32, Batch, hc, ids, rnd, within  # noqa: F401 (hc is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+V = 2.0 ** -24
+
+
+# ---------------------------------------------------------------------------------------------- caps --
+
+def one_feature(dtype, heads, kv_heads, dim, tokens, reach, seed):
+    """Queries and keys of one feature each, so that a score is one exact product, and all keys of a head alike: a token that
+    sees n of them has lse = s + log(n). Scores from 2^-9 to `reach` of either sign."""
+    r = random.Random(seed)
+    q = torch.zeros(tokens, heads, dim, dtype=dtype)
+    for t in range(tokens):
+        for h in range(heads):
+            q[t, h, 7] = r.choice([-1, 1]) * 2.0 ** r.uniform(-6, math.log2(reach)) if (t + h) % 5 else 0.0
+    k = torch.zeros(kv_heads, dim, dtype=dtype)
+    k[:, 7] = torch.tensor([1.0 + 0.25 * (i % 3) for i in range(kv_heads)])
+    return q, k
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("cap", [1e-3, 5.0, 50.0, 1e3, 1e4, 1e5, 1e6, 1e8, 1e30])
+@pytest.mark.parametrize("both", [[(1, 1), (1, 300)], [(20, 20), (40, 300)]], ids=["single", "chunk"])
+def test_caps_of_every_size(hc, dtype, dim, cap, both):
+    """c tanh(s / c) to a few units of its own size, whatever c is. Bound of lse = F(s) + log(n): the cap's argument, the cap and
+    its place in a base-2 exponent round some 16 times in all (16 v |F|), the sum of weights and its logarithm as in _paged_ref."""
+    heads, kv_heads, page, scale = 6, 2, 16, 0.125
+    b = Batch(3, both, heads, kv_heads, dim, page, dtype, cu=both[0][0] > 1)
+    b.q, k = one_feature(dtype, heads, kv_heads, dim, b.tokens, 2.0 ** 14, 5)
+    b.k[b.held] = k
+    out, lse = b.run(hc, scale=scale, softcap=cap)
+    s = b.q.double()[:, :, 7] * k[:, 7].double().repeat_interleave(heads // kv_heads) * scale
+    f = cap * torch.tanh(s / cap)
+    n = torch.tensor([m - nq + i + 1 for nq, m in both for i in range(nq)], dtype=torch.float64)[:, None]
+    want = f + n.log()
+    within(lse, want, 16 * V * f.abs() + (n + 16) * V + 2.0 ** -21 + 2 * V * want.abs(), "lse")
+    # all weights are alike: the values' mean
+    mean, _, tol, _ = R.attention(torch.zeros_like(b.q), b.k, b.v, b.table, b.lens, b.cu)
+    within(out, mean, tol, "out")
+
+
+def cap_bounds(b, out, lse, scale):
+    """Bounds as in _paged_ref, with 16 v |s| for the cap in place of 4 v c, and coarser: |s| <= scale |q| |k| for every score,
+    and the values' largest for their weighted mean."""
+    n, dim, u = max(m for _, m in b.both), b.q.shape[2], R.U[b.dtype]
+    big = scale * b.q.double().norm(dim=-1) * b.k[b.held].double().norm(dim=-1).max()
+    v = b.v[b.held].double().abs()
+    e = (dim + 8 + 16 + 4) * V * big + 2.0 ** -21
+    tol = (2 * e + (n + 16) * V)[..., None] * v.max() + u * out.abs()
+    if b.dtype != F32:
+        tol = tol + u * v.max()
+    if b.dtype == F16:
+        tol = tol + 2.0 ** -25 * (n * v.max() + 1)
+    return tol, e + (n + 16) * V + 2 * V * lse.abs()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("cap", [20.0, 50.0, 1e3, 1e6, 1e30])
+@pytest.mark.parametrize("scale", [0.1, 1.0])
+def test_large_caps_over_ordinary_scores(hc, dtype, dim, cap, scale):
+    for both in ([(1, 700), (1, 33)], [(70, 700), (1, 33)]):
+        b = Batch(211, both, 8, 2, dim, 16, dtype, cu=both[0][0] > 1)
+        out, lse, _, _ = R.attention(b.q, b.k, b.v, b.table, b.lens, b.cu, scale=scale, softcap=cap)
+        tol, ltol = cap_bounds(b, out, lse, scale)
+        got, glse = b.run(hc, scale=scale, softcap=cap)
+        within(got, out, tol, "out")
+        within(glse, lse, ltol, "lse")
