@@ -156,12 +156,15 @@ __host__ __device__ __forceinline__ ScoreMap score_map(float scale, float softca
   return softcap > 0.0f ? ScoreMap{scale * kLog2e, fmaxf(fminf(scale / softcap, 3e38f), -3e38f), softcap * kLog2e}
                         : ScoreMap{scale * kLog2e, 0.0f, 0.0f};
 }
+__device__ __forceinline__ float cap_beyond(const ScoreMap& m, float y) {  // for |y| > kCapTurn
+  const float e = ex2(-2.0f * kLog2e * fabsf(y));
+  return copysignf(__fdividef(m.cap * (1.0f - e), 1.0f + e), y);
+}
 __device__ __forceinline__ float map_score(const ScoreMap& m, float x) {
   if (m.cap == 0.0f) return x * m.mul;
   const float y = x * m.k, u = y * y;
   const float p = fmaf(fmaf(fmaf(fmaf(kCap4, u, kCap3), u, kCap2), u, kCap1), u, kCap0);
-  const float e = ex2(-2.0f * kLog2e * fabsf(y));
-  const float far = copysignf(__fdividef(m.cap * (1.0f - e), 1.0f + e), y);
+  const float far = cap_beyond(m, y);
   return fabsf(y) <= kCapTurn ? x * m.mul * p : far;
 }
 

@@ -499,14 +499,15 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rows_kernel(AttnArgs a) {
           load_values(d, v);
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            float y[4] = {};
+            float (&sums)[4] = o[2 * d + n];
+            float y[4] = {sums[0], sums[1], sums[2], sums[3]};  // (from the sums on: the bits of the row are those of the product above)
             Mma<T>::run4(y, p, v[2 * n] & m0, v[2 * n + 1] & m1);
             if (mine && r < 8) {
-              o[2 * d + n][0] += y[0];
-              o[2 * d + n][1] += y[1];
+              sums[0] = y[0];
+              sums[1] = y[1];
             } else if (mine) {
-              o[2 * d + n][2] += y[2];
-              o[2 * d + n][3] += y[3];
+              sums[2] = y[2];
+              sums[3] = y[3];
             }
           }
         }

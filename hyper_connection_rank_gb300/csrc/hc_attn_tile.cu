@@ -285,12 +285,14 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
 struct CapPoly {
   float c[5];
   float most;  // largest |x|
+  bool all;    // that is, all that have |y| <= kCapTurn
 };
 __device__ __forceinline__ CapPoly cap_poly(float scale, float softcap) {
   const float k = scale / softcap, k2 = k * k, k4 = k2 * k2, c = scale * kLog2e;
   const bool fits = scale >= 1e-4f && scale <= 1e4f && k <= 1e3f;
   return CapPoly{{c * kCap0, c * k2 * kCap1, c * k4 * kCap2, c * k4 * k2 * kCap3, fmaxf(c * k4 * k4 * kCap4, 1e-45f)},
-                 fits ? fminf(kCapTurn / k, 1.8e4f) : -1.0f};
+                 fits ? fminf(kCapTurn / k, 1.8e4f) : -1.0f,
+                 fits && kCapTurn / k <= 1.8e4f};
 }
 __device__ __forceinline__ float2 cap_factor(const CapPoly& p, float2 x) {
   const auto twice = [](float v) { return make_float2(v, v); };
@@ -299,6 +301,14 @@ __device__ __forceinline__ float2 cap_factor(const CapPoly& p, float2 x) {
   y = fma2(y, u, twice(p.c[2]));
   y = fma2(y, u, twice(p.c[1]));
   return fma2(y, u, twice(p.c[0]));
+}
+
+// Any score, less `ref`: the bits of fma2(x, cap_factor(x), -ref) where that holds.
+template <bool ALL>  // poly.all
+__device__ __forceinline__ float cap_exponent(const CapPoly& p, const ScoreMap& m, float x, float ref) {
+  const float near = fmaf(x, cap_factor(p, make_float2(x, x)).x, -ref);
+  const float far = (ALL ? cap_beyond(m, x * m.k) : map_score(m, x)) - ref;
+  return fabsf(x) <= p.most ? near : far;
 }
 
 template <typename T>
@@ -806,37 +816,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           const int j0 = j * kKeys;
           const bool masked = j0 < all_from || j0 + kKeys > all_to;
-          bool inside = false;  // scores are still to go through the cap, all well within it
-          float top;
-          if (CAP) {
-            top = extremes();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) lows[i] = fminf(f[2 * i], f[2 * i + 1]);
-#pragma unroll
-            for (int c = 8; c < kKeys; c += 8)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) lows[i] = min3(lows[i], f[c + 2 * i], f[c + 2 * i + 1]);
-            const float low = fminf(fminf(lows[0], lows[1]), fminf(lows[2], lows[3]));
-            inside = !__any_sync(0xffffffffu, fmaxf(top, -low) > poly.most);
-            if (!inside) {
-              // (32 at a time from tensor memory and back, in a loop: all 128 in registers spill)
-#pragma unroll 1
-              for (int c = 0; c < kKeys; c += 32) {
-                uint32_t y[32];
-                tmem_ld32(s_at + c, y);
-                tmem_wait_ld();
-                landed32(y);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(map_score(map, __uint_as_float(y[i])));
-                tmem_st32(s_at + c, y);
-              }
-              tmem_wait_st();
-              load_scores();
-            }
-          }
-          if (masked) {
-            // (a bit for each key, so that a score costs one test: with two comparisons a score, the
-            // batch of 17 sequences above took 79 us and not 71)
+          // (a bit for each key, so that a score costs one test: with two comparisons a score, the
+          // batch of 17 sequences above took 79 us and not 71)
+          const auto mask = [&] {
             const int lo = from - j0, hi = to - j0;
 #pragma unroll
             for (int h = 0; h < kKeys; h += 32) {
@@ -846,14 +828,34 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < 32; ++c)
                 if (!(seen >> c & 1)) f[h + c] = neg_inf();
             }
+          };
+          // Whether a warp's scores are all well inside the cap chooses between two ways to the same bits: scores that a row
+          // does not see have a say in it.
+          bool inside = false;
+          float top = CAP || !masked ? extremes() : 0.0f;
+          if (CAP) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lows[i] = fminf(f[2 * i], f[2 * i + 1]);
+#pragma unroll
+            for (int c = 8; c < kKeys; c += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) lows[i] = min3(lows[i], f[c + 2 * i], f[c + 2 * i + 1]);
+            const float low = fminf(fminf(lows[0], lows[1]), fminf(lows[2], lows[3]));
+            inside = poly.most > 0.0f && !__any_sync(0xffffffffu, fmaxf(top, -low) > poly.most);
           }
-          const float mul = CAP ? 1.0f : map.mul;
-          if (!CAP || !inside || masked) top = extremes();
-          top *= inside ? cap_factor(poly, make_float2(top, top)).x : mul;
+          if (masked) {
+            mask();
+            top = extremes();
+          }
+          if (!CAP) {
+            top *= map.mul;
+          } else if (top != neg_inf()) {
+            top = cap_exponent<false>(poly, map, top, 0.0f);
+          }
           if (j == g.j0) {
             m = top;
-          } else if (__any_sync(0xffffffffu, top > m + kLazy || (m == neg_inf() && top > m))) {
-            const float now = fmaxf(m, top);
+          } else if (const bool rise = top > m + kLazy || (m == neg_inf() && top > m); __any_sync(0xffffffffu, rise)) {
+            const float now = rise ? top : m;  // (each row by its own scores)
             const float scale = now == neg_inf() ? 1.0f : ex2(m - now);
             m = now;
             l *= scale;
@@ -873,17 +875,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
           }
           const float ref = m == neg_inf() ? 0.0f : m;
-          const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(-ref, -ref);
+          if (CAP && !inside) {
+            // (32 at a time from tensor memory and back, in a loop: all 128 in registers spill)
+            const auto exponents = [&](auto all) {
+#pragma unroll 1
+              for (int c = 0; c < kKeys; c += 32) {
+                uint32_t y[32];
+                tmem_ld32(s_at + c, y);
+                tmem_wait_ld();
+                landed32(y);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(cap_exponent<decltype(all)::value>(poly, map, __uint_as_float(y[i]), ref));
+                tmem_st32(s_at + c, y);
+              }
+            };
+            if (poly.all) {
+              exponents(std::true_type());
+            } else {
+              exponents(std::false_type());
+            }
+            tmem_wait_st();
+            load_scores();
+            if (masked) mask();
+          }
+          const float2 mul2 = make_float2(map.mul, map.mul), ref2 = make_float2(-ref, -ref);
           float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
-          const auto weights = [&](auto factor) {
+          const auto weights = [&](auto exponent) {
 #pragma unroll
             for (int h = 0; h < kKeys; h += 64) {
               uint32_t p[32];
 #pragma unroll
               for (int c = 0; c < 64; c += 4) {
                 const float2 v0 = make_float2(f[h + c], f[h + c + 1]), v1 = make_float2(f[h + c + 2], f[h + c + 3]);
-                float2 y0 = fma2(v0, factor(v0), ref2);
-                float2 y1 = fma2(v1, factor(v1), ref2);
+                float2 y0 = exponent(v0), y1 = exponent(v1);
                 y0 = make_float2(ex2(y0.x), ex2(y0.y));
                 y1 = make_float2(ex2(y1.x), ex2(y1.y));
                 sum0 = add2(sum0, y0);
@@ -894,10 +918,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st32(s_at + h / 2, p);
             }
           };
-          if (CAP && inside) {
-            weights([&](float2 v) { return cap_factor(poly, v); });
+          if (!CAP) {
+            weights([&](float2 v) { return fma2(v, mul2, ref2); });
+          } else if (inside) {
+            weights([&](float2 v) { return fma2(v, cap_factor(poly, v), ref2); });
           } else {
-            weights([&](float2) { return mul2; });
+            weights([&](float2 v) { return v; });
           }
           tmem_wait_st();
           tc_fence_before();

@@ -78,3 +78,43 @@ def test_large_caps_over_ordinary_scores(hc, dtype, dim, cap, scale):
         got, glse = b.run(hc, scale=scale, softcap=cap)
         within(got, out, tol, "out")
         within(glse, lse, ltol, "lse")
+
+
+# ------------------------------------------------------------------------------------- what is not seen --
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("cap", [0.0, 8.0, 30.0])
+@pytest.mark.parametrize("both", [[(1, 700), (1, 37)], [(5, 300), (2, 37)], [(140, 700), (9, 37)]], ids=["single", "few", "chunk"])
+def test_bits_do_not_follow_what_is_not_seen(hc, dtype, dim, cap, both):
+    """The same bits whatever lies in the rest of a sequence's last page, in the pool's other pages, in keys that the window has
+    left, and, for a token, in the keys and values of those after it."""
+    b = Batch(31, both, 4, 2, dim, 16, dtype, cu=both[0][0] > 1, stale=0.0)
+    kw = dict(softcap=cap, scale=0.3, window=100)
+    base, lse = b.run(hc, **kw)
+    for stale in (0.01, -300.0, 6e4, math.inf, -math.inf, math.nan):
+        b.k[~b.held] = stale
+        b.v[~b.held] = stale
+        got, glse = b.run(hc, **kw)
+        assert torch.equal(got, base) and torch.equal(glse, lse), f"stale {stale}"
+    places = {(s, j): (int(b.table[s, j // 16]), j % 16) for s, (_, n) in enumerate(both) for j in range(n)}
+    for huge in (-300.0, 6e4, math.inf):
+        keep = b.k.clone(), b.v.clone()
+        for (s, j), place in places.items():
+            if j <= both[s][1] - both[s][0] - 100:  # no new token sees it
+                b.k[place], b.v[place] = huge, -huge
+        got, glse = b.run(hc, **kw)
+        assert torch.equal(got, base) and torch.equal(glse, lse), f"left keys {huge}"
+        b.k, b.v = keep
+    for last in (1, 3):
+        if last >= both[0][0]:
+            continue
+        for key, value in ((3.0, 3.0), (-300.0, 300.0), (6e4, 6e4), (math.nan, math.inf)):
+            keep = b.k.clone(), b.v.clone()
+            n, nq = both[0][1], both[0][0]
+            for j in range(n - last, n):
+                b.k[places[0, j]], b.v[places[0, j]] = key, value
+            got, glse = b.run(hc, **kw)
+            seen = [t for t in range(b.tokens) if not nq - last <= t < nq]
+            assert torch.equal(got[seen], base[seen]) and torch.equal(glse[seen], lse[seen]), f"later key {key}"
+            b.k, b.v = keep
