@@ -160,12 +160,15 @@ __device__ __forceinline__ float cap_beyond(const ScoreMap& m, float y) {  // fo
   const float e = ex2(-2.0f * kLog2e * fabsf(y));
   return copysignf(__fdividef(m.cap * (1.0f - e), 1.0f + e), y);
 }
+__device__ __forceinline__ bool cap_far(const ScoreMap& m, float x) { return fabsf(x * m.k) > kCapTurn; }
+__device__ __forceinline__ float cap_near(const ScoreMap& m, float x) {
+  const float y = x * m.k, u = y * y;
+  return x * m.mul * fmaf(fmaf(fmaf(fmaf(kCap4, u, kCap3), u, kCap2), u, kCap1), u, kCap0);
+}
 __device__ __forceinline__ float map_score(const ScoreMap& m, float x) {
   if (m.cap == 0.0f) return x * m.mul;
-  const float y = x * m.k, u = y * y;
-  const float p = fmaf(fmaf(fmaf(fmaf(kCap4, u, kCap3), u, kCap2), u, kCap1), u, kCap0);
-  const float far = cap_beyond(m, y);
-  return fabsf(y) <= kCapTurn ? x * m.mul * p : far;
+  const float near = cap_near(m, x), far = cap_beyond(m, x * m.k);
+  return cap_far(m, x) ? far : near;
 }
 
 }  // namespace hc

@@ -412,11 +412,30 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rows_kernel(AttnArgs a) {
     }
     const int j0 = b * kBlock;
     const bool whole = j0 >= all_from && j0 + kBlock <= all_to;
+    const auto map_all = [&](auto exponent) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = exponent(s[n][e]);
+    };
+    if (map.cap == 0.0f) {
+      map_all([&](float x) { return x * map.mul; });
+    } else {
+      bool far = false;
+      map_all([&](float x) {
+        far |= cap_far(map, x);
+        return x;
+      });
+      if (__any_sync(0xffffffffu, far)) {
+        map_all([&](float x) { return map_score(map, x); });
+      } else {  // (the same bits)
+        map_all([&](float x) { return cap_near(map, x); });
+      }
+    }
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[n][e] = map_score(map, s[n][e]);
         if (!whole) {
           const int j = j0 + 8 * n + 2 * q4 + (e & 1), i = e >> 1;
           if (j < from[i] || j >= to[i]) s[n][e] = neg_inf();
