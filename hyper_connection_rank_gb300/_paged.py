@@ -105,20 +105,25 @@ def _out(out, like, name):
     return out, _heads("out", out, like.dtype)[1]
 
 
-def _stream(t, stream, *temporaries):
-    """The stream to launch on. Memory that this call allocated on the current stream and uses on another one must not be
-    handed out again before that one is done with it."""
-    if stream is None:
-        return _current_stream(t.get_device())
-    for x in temporaries:
-        if x is not None:
-            x.record_stream(stream)
-    return stream.cuda_stream
-
-
 # The current stream's handle without a Python object around it, where this build of torch has that.
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on_stream(stream, f, *args, out=None, workspace=None, **kw):
+    """f's call with another stream as the current one, so that what it allocates comes from that stream's memory: a block that
+    was freed on this stream may still be in use by kernels queued here. Results are the caller's, who may free them on this
+    stream; memory that the caller gave is not handed out again before the other stream is done with it."""
+    for name, t in (("out", out), ("workspace", workspace)):
+        if t is not None:
+            t.record_stream(stream)
+            kw[name] = t
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        got = f(*args, **kw)
+    for t in got if isinstance(got, tuple) else (got,):
+        t.record_stream(here)
+    return got
 
 
 def rotary_frequencies(rot_dim, theta=10000.0, *, scaling=None, factor=1.0, original_length=None, slow=1.0, fast=32.0,
@@ -163,6 +168,9 @@ def rotary(x, positions, inv_freq, *, amplitude=1.0, interleaved=False, inverse=
     head stride; positions: (tokens,) int64 or int32; inv_freq: (rot_dim / 2,) float64 from ``rotary_frequencies``. Features
     from rot_dim on are copied. ``inverse=True`` turns back, which also takes the gradient of the result to that of x.
     ``out`` may be x itself."""
+    if stream is not None:
+        return _on_stream(stream, rotary, x, positions, inv_freq, amplitude=amplitude, interleaved=interleaved, inverse=inverse,
+                          out=out)
     code = _dtype_code(x)
     (tokens, heads, dim), xs = _heads("x", x, x.dtype)
     half = _flat("inv_freq", inv_freq, torch.float64)
@@ -172,7 +180,7 @@ def rotary(x, positions, inv_freq, *, amplitude=1.0, interleaved=False, inverse=
     out, os = _out(out, x, "x")
     args = _ROTARY.pack(x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr(), tokens, xs[0], xs[1], os[0],
                         os[1], heads, dim, 2 * half, bool(interleaved), bool(inverse), narrow, code, amplitude)
-    check(lib().hc_rotary(args, _stream(x, stream, out)))
+    check(lib().hc_rotary(args, _current_stream(x.get_device())))
     return out
 
 
@@ -181,6 +189,9 @@ def rotary_append(q, k, v, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, 
     """Rotate a batch's new queries, and rotate its new keys and write them with the values into the cache
     (hc_rotary_append). q: (tokens, heads, head_dim); k, v: (tokens, kv_heads, head_dim), which may be parts of one matrix.
     Positions follow from kv_lens and cu_q. Returns the rotated queries (``out``, which may be q itself)."""
+    if stream is not None:
+        return _on_stream(stream, rotary_append, q, k, v, k_cache, v_cache, page_table, kv_lens, cu_q, inv_freq=inv_freq,
+                          amplitude=amplitude, interleaved=interleaved, out=out)
     code, dtype = _dtype_code(q), q.dtype
     (tokens, heads, dim), qs = _heads("q", q, dtype)
     kshape, ks = _heads("k", k, dtype)
@@ -195,7 +206,7 @@ def rotary_append(q, k, v, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, 
                         inv_freq.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cu, tokens, pages, step, qs[0], qs[1],
                         ks[0], ks[1], vs[0], vs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, width, page, heads, kv_heads, dim,
                         2 * half, bool(interleaved), code, amplitude)
-    check(lib().hc_rotary_append(args, _stream(q, stream, out)))
+    check(lib().hc_rotary_append(args, _current_stream(q.get_device())))
     return out
 
 
@@ -233,6 +244,10 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, scal
     return_lse also the float32 logarithms (tokens, heads) of the sums of weights. A token that sees nothing gets zeros, and
     minus infinity. ``workspace``: a CUDA tensor of at least ``paged_attention_workspace_size`` bytes, allocated here if
     omitted."""
+    if stream is not None:
+        return _on_stream(stream, paged_attention, q, k_cache, v_cache, page_table, kv_lens, cu_q, scale=scale, window=window,
+                          softcap=softcap, max_q=max_q, max_kv=max_kv, return_lse=return_lse, out=out, workspace=workspace,
+                          flags=flags)
     out, os = _out(out, q, "q")
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
     front, back = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags,
@@ -246,7 +261,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, scal
             work = _ATTENTION_WORK.pack(workspace.data_ptr(), size)
     else:
         work = _ATTENTION_WORK.pack(workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    check(L.hc_paged_attention(front + work + back, _stream(q, stream, out, lse, workspace)))
+    check(L.hc_paged_attention(front + work + back, _current_stream(q.get_device())))
     return (out, lse) if return_lse else out
 
 
@@ -288,13 +303,15 @@ def page_copy(cache, src, dst, *, stream=None):
     """Copy pages within a pool (hc_page_copy): cache[:, dst[i]] = cache[:, src[i]]. cache: (planes, num_pages, ...), where
     the planes are the layers' keys and values; src, dst: int32. The dst are distinct and none is a src; entries outside the
     pool are passed over. Returns cache."""
+    if stream is not None:
+        return _on_stream(stream, page_copy, cache, src, dst)
     planes, pages, size = _pool(cache)
     _flat("src", src, torch.int32)
     _flat("dst", dst, torch.int32)
     if src.shape != dst.shape:
         raise ValueError("src and dst differ in length")
     check(lib().hc_page_copy(cache.data_ptr(), planes, pages, size, src.data_ptr(), dst.data_ptr(), src.shape[0],
-                             _stream(cache, stream)))
+                             _current_stream(cache.get_device())))
     return cache
 
 
@@ -303,6 +320,8 @@ def page_fork(cache, page_table, lens, refs, parents, *, page_size=None, stream=
     parents[i] (-1: it is empty), the old ones are given up. Full pages are shared; of a last page that is not full every
     child but the first gets a copy. refs (num_pages,) int32 counts the tables' entries and whoever else holds a page.
     Returns (page_table, lens, refs, missing), all new; missing (1,) counts the children that no free page was left for."""
+    if stream is not None:
+        return _on_stream(stream, page_fork, cache, page_table, lens, refs, parents, page_size=page_size)
     planes, pages, size = _pool(cache)
     _flat("parents", parents, torch.int32)
     n = parents.shape[0]
@@ -312,12 +331,14 @@ def page_fork(cache, page_table, lens, refs, parents, *, page_size=None, stream=
     missing = torch.empty(1, dtype=torch.int32, device=refs.device)
     ws, bytes_ = _pages_workspace(refs, max(n, page_table.shape[0]))
     check(lib().hc_page_fork(args, parents.data_ptr(), n, missing.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(),
-                             bytes_, _stream(refs, stream, table_out, lens_out, refs_out, missing, ws)))
+                             bytes_, _current_stream(refs.get_device())))
     return table_out, lens_out, refs_out, missing
 
 
 def page_extend(page_table, lens, refs, new_tokens, *, page_size, stream=None):
     """Pages for new_tokens[s] more tokens of every sequence (hc_page_extend). Returns (page_table, lens, refs, missing)."""
+    if stream is not None:
+        return _on_stream(stream, page_extend, page_table, lens, refs, new_tokens, page_size=page_size)
     _flat("new_tokens", new_tokens, torch.int32)
     seqs = page_table.shape[0]
     if new_tokens.shape[0] != seqs:
@@ -326,24 +347,28 @@ def page_extend(page_table, lens, refs, new_tokens, *, page_size, stream=None):
     missing = torch.empty(1, dtype=torch.int32, device=refs.device)
     ws, bytes_ = _pages_workspace(refs, seqs)
     check(lib().hc_page_extend(args, new_tokens.data_ptr(), missing.data_ptr(), ws.data_ptr(), bytes_,
-                               _stream(refs, stream, table_out, lens_out, refs_out, missing, ws)))
+                               _current_stream(refs.get_device())))
     return table_out, lens_out, refs_out, missing
 
 
 def page_release(page_table, lens, refs, drop, *, page_size, stream=None):
     """Sequences with drop[s] (uint8 or bool) give up their pages (hc_page_release). Returns (page_table, lens, refs)."""
+    if stream is not None:
+        return _on_stream(stream, page_release, page_table, lens, refs, drop, page_size=page_size)
     _flat("drop", drop, torch.bool if drop.dtype == torch.bool else torch.uint8)
     seqs = page_table.shape[0]
     if drop.shape[0] != seqs:
         raise ValueError("drop and page_table differ in sequences")
     args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, page_size, seqs)
-    check(lib().hc_page_release(args, drop.data_ptr(), _stream(refs, stream, table_out, lens_out, refs_out)))
+    check(lib().hc_page_release(args, drop.data_ptr(), _current_stream(refs.get_device())))
     return table_out, lens_out, refs_out
 
 
 def page_compact(cache, page_table, lens, refs, *, page_size=None, stream=None):
     """Move the live pages of a pool to its front (hc_page_compact). Returns (page_table, refs, remap, live): the new tables
     and counts, where each page went (-1: nowhere), and the number of live pages."""
+    if stream is not None:
+        return _on_stream(stream, page_compact, cache, page_table, lens, refs, page_size=page_size)
     planes, pages, size = _pool(cache)
     seqs = page_table.shape[0]
     args, table_out, _, refs_out = _pages(page_table, lens, refs, cache.shape[2] if page_size is None else page_size, seqs,
@@ -354,5 +379,5 @@ def page_compact(cache, page_table, lens, refs, *, page_size=None, stream=None):
     live = torch.empty(1, dtype=torch.int32, device=refs.device)
     ws, bytes_ = _pages_workspace(refs, seqs)
     check(lib().hc_page_compact(args, remap.data_ptr(), live.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(), bytes_,
-                                _stream(refs, stream, table_out, refs_out, remap, live, ws)))
+                                _current_stream(refs.get_device())))
     return table_out, refs_out, remap, live

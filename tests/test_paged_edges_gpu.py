@@ -118,3 +118,78 @@ def test_bits_do_not_follow_what_is_not_seen(hc, dtype, dim, cap, both):
             seen = [t for t in range(b.tokens) if not nq - last <= t < nq]
             assert torch.equal(got[seen], base[seen]) and torch.equal(glse[seen], lse[seen]), f"later key {key}"
             b.k, b.v = keep
+
+
+# -------------------------------------------------------------------------------------------- streams --
+
+def calls_with_streams(hc):
+    """Every entry point that takes a stream: (what, call(stream=...)), each giving a tuple of tensors. No call changes its
+    inputs in a way that a second one would see."""
+    b = Batch(61, [(40, 300), (1, 35)], 8, 2, 128, 16, BF16, stale=0.0)
+    f, _ = hc.rotary_frequencies(128)
+    q, k, v, table, lens, cu = (x.cuda() for x in (b.q, b.k, b.v, b.table, b.lens, b.cu))
+    kv = rnd(5, b.tokens, 2, 128, dtype=BF16).cuda()
+    kc, vc = k.clone(), v.clone()
+    at = torch.arange(b.tokens, device="cuda")
+    pool = torch.stack((k, v))
+    refs = torch.zeros(k.shape[0], dtype=torch.int32)
+    for row, (_, n) in zip(b.table, b.both):
+        refs[row[: -(-n // 16)].long()] += 1
+    refs = refs.cuda()
+    parents = torch.tensor([0, 0, 1], dtype=torch.int32, device="cuda")
+    one = torch.ones(2, dtype=torch.int32, device="cuda")
+    ids_ = torch.tensor([int(b.table[0, 0])], dtype=torch.int32, device="cuda")
+    free = (refs == 0).nonzero()[:1, 0].int()
+    tup = lambda x: x if isinstance(x, tuple) else (x,)  # noqa: E731
+    rest = (table, lens, cu)
+    return [
+        ("rotary", lambda **kw: tup(hc.rotary(q, at, f, **kw))),
+        ("rotary_append", lambda **kw: tup(hc.rotary_append(q, kv, kv, kc, vc, *rest, inv_freq=f, **kw)) + (kc, vc)),
+        ("paged_attention", lambda **kw: hc.paged_attention(q, k, v, *rest, return_lse=True, **kw)),
+        ("page_copy", lambda **kw: tup(hc.page_copy(pool, ids_, free, **kw))),
+        ("page_fork", lambda **kw: hc.page_fork(pool, table, lens, refs, parents, **kw)),
+        ("page_extend", lambda **kw: hc.page_extend(table, lens, refs, one, page_size=16, **kw)),
+        ("page_release", lambda **kw: hc.page_release(table, lens, refs, one.byte(), page_size=16, **kw)),
+        ("page_compact", lambda **kw: hc.page_compact(pool, table, lens, refs, **kw)),
+    ]
+
+
+def test_other_streams_do_not_take_memory_that_is_still_in_use(hc):
+    """Blocks freed on the current stream, whose kernels there have yet to write them, must not hold another stream's results
+    or workspace: the current stream is kept busy, and then fills every block that the call might have been handed."""
+    for what, call in calls_with_streams(hc):
+        want = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        torch.cuda._sleep(200_000_000)  # a tenth of a second
+        blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (4, 64, 500, 2000, 60000, 10 ** 6, 5 * 10 ** 6, 10 ** 8)
+                  for _ in range(8)]
+        for x in blocks:
+            x.fill_(255)
+        del blocks, x
+        got = call(stream=side)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), what
+
+
+def test_results_of_another_stream_are_not_handed_out_too_early(hc):
+    """The caller may free a result on its own stream while that one's kernels still read it."""
+    for what, call in calls_with_streams(hc):
+        if what == "page_copy":
+            continue  # (gives back its input)
+        want = call()[0].clone()
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        got = call(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(200_000_000)
+        kept = got[0].clone()
+        del got
+        for _ in range(4):
+            call(stream=side)
+            with torch.cuda.stream(side):
+                junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (64, 500, 2000, 60000, 10 ** 6)]
+        torch.cuda.synchronize()
+        assert torch.equal(kept, want), what
+        del junk
