@@ -36,19 +36,27 @@ _PAGES = struct.Struct("@6P2q3i0q")
 # (A call costs the host as much as a small kernel costs the GPU, so the checks below ask each tensor for as little as they
 # can; what the library checks itself is left to it.)
 
-def _heads(name, t, dtype):
+def _device(t):
+    """The index of the GPU that a call's first tensor lies on, which all the others must share."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError("expected CUDA tensors")
+    return device
+
+
+def _heads(name, t, dtype, device):
     """A tensor of rows of heads, the last axis contiguous: (shape, strides)."""
-    if t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor of dtype {dtype}")
+    if t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor of dtype {dtype} on device {device}")
     shape, strides = t.shape, t.stride()
     if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1):
         raise ValueError(f"{name} must have three axes, the last one contiguous")
     return shape, strides
 
 
-def _flat(name, t, dtype):
-    if t.dtype is not dtype or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous 1-dimensional CUDA tensor of dtype {dtype}")
+def _flat(name, t, dtype, device):
+    if t.dtype is not dtype or t.get_device() != device or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-dimensional CUDA tensor of dtype {dtype} on device {device}")
     return t.shape[0]
 
 
@@ -59,34 +67,35 @@ def _dtype_code(t):
     return code
 
 
-def _table(t):
+def _table(t, device):
     """(sequences, columns, entries from one row to the next)"""
-    if t.dtype is not torch.int32 or not t.is_cuda or t.dim() != 2:
-        raise ValueError("page_table must be a 2-dimensional CUDA tensor of dtype torch.int32")
+    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 2:
+        raise ValueError(f"page_table must be a 2-dimensional CUDA tensor of dtype torch.int32 on device {device}")
     (seqs, width), (step, inner) = t.shape, t.stride()
     if width < 1 or (inner != 1 and width > 1):
         raise ValueError("page_table needs at least one column, and contiguous rows")
     return seqs, width, step if seqs > 1 else max(step, width)
 
 
-def _batch(page_table, kv_lens, cu_q, tokens):
+def _batch(page_table, kv_lens, cu_q, tokens, device):
     """(sequences, columns, row step of the table, address of cu_q)"""
-    seqs, width, step = _table(page_table)
-    if _flat("kv_lens", kv_lens, torch.int32) != seqs:
+    seqs, width, step = _table(page_table, device)
+    if _flat("kv_lens", kv_lens, torch.int32, device) != seqs:
         raise ValueError("kv_lens and page_table differ in sequences")
     if cu_q is None:
         if tokens != seqs:
             raise ValueError("without cu_q every sequence has one new token")
         return seqs, width, step, 0
-    if _flat("cu_q", cu_q, torch.int32) != seqs + 1:
+    if _flat("cu_q", cu_q, torch.int32, device) != seqs + 1:
         raise ValueError("cu_q must have one entry more than there are sequences")
     return seqs, width, step, cu_q.data_ptr()
 
 
-def _caches(k_cache, v_cache, dtype):
+def _caches(k_cache, v_cache, dtype, device):
     """(shape, strides) of both."""
-    if k_cache.dtype is not dtype or v_cache.dtype is not dtype or not k_cache.is_cuda or not v_cache.is_cuda:
-        raise ValueError(f"k_cache and v_cache must be CUDA tensors of dtype {dtype}")
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.get_device() != device or \
+            v_cache.get_device() != device:
+        raise ValueError(f"k_cache and v_cache must be CUDA tensors of dtype {dtype} on device {device}")
     shape, strides = k_cache.shape, k_cache.stride()
     if shape != v_cache.shape or strides != v_cache.stride():
         raise ValueError("k_cache and v_cache must have the same shape and strides")
@@ -95,25 +104,45 @@ def _caches(k_cache, v_cache, dtype):
     return shape, strides
 
 
-def _out(out, like, name):
+def _out(out, like, name, device):
     """(out, its strides): the one given, or a new one of the shape of `like`."""
     if out is None:
         out = torch.empty_like(like)
         return out, out.stride()
     if out.shape != like.shape or out.dtype is not like.dtype:
         raise ValueError(f"out must have the shape and dtype of {name}")
-    return out, _heads("out", out, like.dtype)[1]
+    return out, _heads("out", out, like.dtype, device)[1]
 
 
-# The current stream's handle without a Python object around it, where this build of torch has that.
+# The current stream's handle and device without Python objects around them, where this build of torch has that.
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(device, f, *args):
+    """A library call on the current stream of a device, which the library takes to be the current one."""
+    if device == _current_device():
+        check(f(*args, _current_stream(device)))
+    else:
+        with torch.cuda.device(device):
+            check(f(*args, _current_stream(device)))
+
+
+def _sized(device, f, *args):
+    """A size that the library gives for the current device."""
+    if device == _current_device():
+        return f(*args)
+    with torch.cuda.device(device):
+        return f(*args)
 
 
 def _on_stream(stream, f, *args, out=None, workspace=None, **kw):
     """f's call with another stream as the current one, so that what it allocates comes from that stream's memory: a block that
     was freed on this stream may still be in use by kernels queued here. Results are the caller's, who may free them on this
     stream; memory that the caller gave is not handed out again before the other stream is done with it."""
+    if stream.device.index != args[0].get_device():
+        raise ValueError("the stream and the tensors are on different devices")
     for name, t in (("out", out), ("workspace", workspace)):
         if t is not None:
             t.record_stream(stream)
@@ -171,16 +200,16 @@ def rotary(x, positions, inv_freq, *, amplitude=1.0, interleaved=False, inverse=
     if stream is not None:
         return _on_stream(stream, rotary, x, positions, inv_freq, amplitude=amplitude, interleaved=interleaved, inverse=inverse,
                           out=out)
-    code = _dtype_code(x)
-    (tokens, heads, dim), xs = _heads("x", x, x.dtype)
-    half = _flat("inv_freq", inv_freq, torch.float64)
+    code, device = _dtype_code(x), _device(x)
+    (tokens, heads, dim), xs = _heads("x", x, x.dtype, device)
+    half = _flat("inv_freq", inv_freq, torch.float64, device)
     narrow = positions.dtype is torch.int32
-    if _flat("positions", positions, torch.int32 if narrow else torch.int64) != tokens:
+    if _flat("positions", positions, torch.int32 if narrow else torch.int64, device) != tokens:
         raise ValueError("positions and x differ in tokens")
-    out, os = _out(out, x, "x")
+    out, os = _out(out, x, "x", device)
     args = _ROTARY.pack(x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr(), tokens, xs[0], xs[1], os[0],
                         os[1], heads, dim, 2 * half, bool(interleaved), bool(inverse), narrow, code, amplitude)
-    check(lib().hc_rotary(args, _current_stream(x.get_device())))
+    _launch(device, lib().hc_rotary, args)
     return out
 
 
@@ -192,32 +221,33 @@ def rotary_append(q, k, v, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, 
     if stream is not None:
         return _on_stream(stream, rotary_append, q, k, v, k_cache, v_cache, page_table, kv_lens, cu_q, inv_freq=inv_freq,
                           amplitude=amplitude, interleaved=interleaved, out=out)
-    code, dtype = _dtype_code(q), q.dtype
-    (tokens, heads, dim), qs = _heads("q", q, dtype)
-    kshape, ks = _heads("k", k, dtype)
-    vshape, vs = _heads("v", v, dtype)
-    (pages, page, kv_heads, cdim), cs = _caches(k_cache, v_cache, dtype)
-    half = _flat("inv_freq", inv_freq, torch.float64)
+    code, dtype, device = _dtype_code(q), q.dtype, _device(q)
+    (tokens, heads, dim), qs = _heads("q", q, dtype, device)
+    kshape, ks = _heads("k", k, dtype, device)
+    vshape, vs = _heads("v", v, dtype, device)
+    (pages, page, kv_heads, cdim), cs = _caches(k_cache, v_cache, dtype, device)
+    half = _flat("inv_freq", inv_freq, torch.float64, device)
     if kshape != vshape or kshape != (tokens, kv_heads, dim) or cdim != dim:
         raise ValueError("q, k, v and the caches differ in tokens, kv_heads or head_dim")
-    seqs, width, step, cu = _batch(page_table, kv_lens, cu_q, tokens)
-    out, os = _out(out, q, "q")
+    seqs, width, step, cu = _batch(page_table, kv_lens, cu_q, tokens, device)
+    out, os = _out(out, q, "q", device)
     args = _APPEND.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                         inv_freq.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cu, tokens, pages, step, qs[0], qs[1],
                         ks[0], ks[1], vs[0], vs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, width, page, heads, kv_heads, dim,
                         2 * half, bool(interleaved), code, amplitude)
-    check(lib().hc_rotary_append(args, _current_stream(q.get_device())))
+    _launch(device, lib().hc_rotary_append, args)
     return out
 
 
-def _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, out, lse, os):
+def _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags, out, lse, os,
+                    device):
     """The packed arguments before the workspace, and those after."""
     code = _dtype_code(q)
-    (tokens, heads, dim), qs = _heads("q", q, q.dtype)
-    (pages, page, kv_heads, cdim), cs = _caches(k_cache, v_cache, q.dtype)
+    (tokens, heads, dim), qs = _heads("q", q, q.dtype, device)
+    (pages, page, kv_heads, cdim), cs = _caches(k_cache, v_cache, q.dtype, device)
     if cdim != dim or kv_heads < 1 or heads % kv_heads:
         raise ValueError("heads must be a multiple of kv_heads, and head_dim that of the caches")
-    seqs, width, step, cu = _batch(page_table, kv_lens, cu_q, tokens)
+    seqs, width, step, cu = _batch(page_table, kv_lens, cu_q, tokens, device)
     front = _ATTENTION_FRONT.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
                                   kv_lens.data_ptr(), cu, out, lse)
     back = _ATTENTION_BACK.pack(tokens, pages, step, qs[0], qs[1], os[0], os[1], cs[0], cs[1], cs[2], seqs, width, page, heads,
@@ -230,9 +260,10 @@ def paged_attention_workspace_size(q, k_cache, v_cache, page_table, kv_lens, cu_
                                    flags=0):
     """Bytes of workspace that ``paged_attention`` needs for these tensors (their contents do not matter)."""
     heads, dim = q.shape[1:]
+    device = _device(q)
     front, back = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, None, window, 0.0, max_q, max_kv, flags, 0, 0,
-                                  (heads * dim, dim))
-    return lib().hc_paged_attention_workspace_size(front + _NO_WORK + back)
+                                  (heads * dim, dim), device)
+    return _sized(device, lib().hc_paged_attention_workspace_size, front + _NO_WORK + back)
 
 
 def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, scale=None, window=0, softcap=0.0, max_q=None,
@@ -248,40 +279,43 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, scal
         return _on_stream(stream, paged_attention, q, k_cache, v_cache, page_table, kv_lens, cu_q, scale=scale, window=window,
                           softcap=softcap, max_q=max_q, max_kv=max_kv, return_lse=return_lse, out=out, workspace=workspace,
                           flags=flags)
-    out, os = _out(out, q, "q")
+    device = _device(q)
+    out, os = _out(out, q, "q", device)
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
     front, back = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, softcap, max_q, max_kv, flags,
-                                  out.data_ptr(), 0 if lse is None else lse.data_ptr(), os)
+                                  out.data_ptr(), 0 if lse is None else lse.data_ptr(), os, device)
     L = lib()
     work = _NO_WORK
     if workspace is None:
-        size = L.hc_paged_attention_workspace_size(front + _NO_WORK + back)
+        size = _sized(device, L.hc_paged_attention_workspace_size, front + _NO_WORK + back)
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
             work = _ATTENTION_WORK.pack(workspace.data_ptr(), size)
     else:
+        if workspace.get_device() != device:
+            raise ValueError(f"workspace must be a CUDA tensor on device {device}")
         work = _ATTENTION_WORK.pack(workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    check(L.hc_paged_attention(front + work + back, _current_stream(q.get_device())))
+    _launch(device, L.hc_paged_attention, front + work + back)
     return (out, lse) if return_lse else out
 
 
 # ------------------------------------------------------------------------------------------------ pages --
 
 def _pool(cache):
-    """(planes, pages, bytes of a page) of a pool (planes, num_pages, ...)."""
+    """(planes, pages, bytes of a page, device) of a pool (planes, num_pages, ...)."""
     if not isinstance(cache, torch.Tensor) or not cache.is_cuda or cache.dim() < 3 or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous CUDA tensor (planes, num_pages, ...)")
     planes, pages = cache.shape[:2]
     if cache.numel() == 0:
         raise ValueError("cache is empty")
-    return planes, pages, cache.numel() // (planes * pages) * cache.element_size()
+    return planes, pages, cache.numel() // (planes * pages) * cache.element_size(), cache.get_device()
 
 
-def _pages(page_table, lens, refs, page_size, seqs_out, need_lens=True):
+def _pages(page_table, lens, refs, page_size, seqs_out, index, need_lens=True):
     """The new tables and counts, and the packed arguments."""
-    seqs, width, step = _table(page_table)
-    pages = _flat("refs", refs, torch.int32)
-    if _flat("lens", lens, torch.int32) != seqs:
+    seqs, width, step = _table(page_table, index)
+    pages = _flat("refs", refs, torch.int32, index)
+    if _flat("lens", lens, torch.int32, index) != seqs:
         raise ValueError("lens and page_table differ in sequences")
     if page_size < 1:
         raise ValueError("page_size must be positive")
@@ -305,13 +339,12 @@ def page_copy(cache, src, dst, *, stream=None):
     pool are passed over. Returns cache."""
     if stream is not None:
         return _on_stream(stream, page_copy, cache, src, dst)
-    planes, pages, size = _pool(cache)
-    _flat("src", src, torch.int32)
-    _flat("dst", dst, torch.int32)
+    planes, pages, size, device = _pool(cache)
+    _flat("src", src, torch.int32, device)
+    _flat("dst", dst, torch.int32, device)
     if src.shape != dst.shape:
         raise ValueError("src and dst differ in length")
-    check(lib().hc_page_copy(cache.data_ptr(), planes, pages, size, src.data_ptr(), dst.data_ptr(), src.shape[0],
-                             _current_stream(cache.get_device())))
+    _launch(device, lib().hc_page_copy, cache.data_ptr(), planes, pages, size, src.data_ptr(), dst.data_ptr(), src.shape[0])
     return cache
 
 
@@ -322,16 +355,17 @@ def page_fork(cache, page_table, lens, refs, parents, *, page_size=None, stream=
     Returns (page_table, lens, refs, missing), all new; missing (1,) counts the children that no free page was left for."""
     if stream is not None:
         return _on_stream(stream, page_fork, cache, page_table, lens, refs, parents, page_size=page_size)
-    planes, pages, size = _pool(cache)
-    _flat("parents", parents, torch.int32)
+    planes, pages, size, device = _pool(cache)
+    _flat("parents", parents, torch.int32, device)
     n = parents.shape[0]
-    args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, cache.shape[2] if page_size is None else page_size, n)
+    args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, cache.shape[2] if page_size is None else page_size, n,
+                                                 device)
     if refs.shape[0] != pages:
         raise ValueError("refs must have an entry for every page of cache")
     missing = torch.empty(1, dtype=torch.int32, device=refs.device)
     ws, bytes_ = _pages_workspace(refs, max(n, page_table.shape[0]))
-    check(lib().hc_page_fork(args, parents.data_ptr(), n, missing.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(),
-                             bytes_, _current_stream(refs.get_device())))
+    _launch(device, lib().hc_page_fork, args, parents.data_ptr(), n, missing.data_ptr(), cache.data_ptr(), planes, size,
+            ws.data_ptr(), bytes_)
     return table_out, lens_out, refs_out, missing
 
 
@@ -339,15 +373,15 @@ def page_extend(page_table, lens, refs, new_tokens, *, page_size, stream=None):
     """Pages for new_tokens[s] more tokens of every sequence (hc_page_extend). Returns (page_table, lens, refs, missing)."""
     if stream is not None:
         return _on_stream(stream, page_extend, page_table, lens, refs, new_tokens, page_size=page_size)
-    _flat("new_tokens", new_tokens, torch.int32)
+    device = _device(refs)
+    _flat("new_tokens", new_tokens, torch.int32, device)
     seqs = page_table.shape[0]
     if new_tokens.shape[0] != seqs:
         raise ValueError("new_tokens and page_table differ in sequences")
-    args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, page_size, seqs)
+    args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, page_size, seqs, device)
     missing = torch.empty(1, dtype=torch.int32, device=refs.device)
     ws, bytes_ = _pages_workspace(refs, seqs)
-    check(lib().hc_page_extend(args, new_tokens.data_ptr(), missing.data_ptr(), ws.data_ptr(), bytes_,
-                               _current_stream(refs.get_device())))
+    _launch(device, lib().hc_page_extend, args, new_tokens.data_ptr(), missing.data_ptr(), ws.data_ptr(), bytes_)
     return table_out, lens_out, refs_out, missing
 
 
@@ -355,12 +389,13 @@ def page_release(page_table, lens, refs, drop, *, page_size, stream=None):
     """Sequences with drop[s] (uint8 or bool) give up their pages (hc_page_release). Returns (page_table, lens, refs)."""
     if stream is not None:
         return _on_stream(stream, page_release, page_table, lens, refs, drop, page_size=page_size)
-    _flat("drop", drop, torch.bool if drop.dtype == torch.bool else torch.uint8)
+    device = _device(refs)
+    _flat("drop", drop, torch.bool if drop.dtype == torch.bool else torch.uint8, device)
     seqs = page_table.shape[0]
     if drop.shape[0] != seqs:
         raise ValueError("drop and page_table differ in sequences")
-    args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, page_size, seqs)
-    check(lib().hc_page_release(args, drop.data_ptr(), _current_stream(refs.get_device())))
+    args, table_out, lens_out, refs_out = _pages(page_table, lens, refs, page_size, seqs, device)
+    _launch(device, lib().hc_page_release, args, drop.data_ptr())
     return table_out, lens_out, refs_out
 
 
@@ -369,15 +404,15 @@ def page_compact(cache, page_table, lens, refs, *, page_size=None, stream=None):
     and counts, where each page went (-1: nowhere), and the number of live pages."""
     if stream is not None:
         return _on_stream(stream, page_compact, cache, page_table, lens, refs, page_size=page_size)
-    planes, pages, size = _pool(cache)
+    planes, pages, size, device = _pool(cache)
     seqs = page_table.shape[0]
     args, table_out, _, refs_out = _pages(page_table, lens, refs, cache.shape[2] if page_size is None else page_size, seqs,
-                                          need_lens=False)
+                                          device, need_lens=False)
     if refs.shape[0] != pages:
         raise ValueError("refs must have an entry for every page of cache")
     remap = torch.empty_like(refs)
     live = torch.empty(1, dtype=torch.int32, device=refs.device)
     ws, bytes_ = _pages_workspace(refs, seqs)
-    check(lib().hc_page_compact(args, remap.data_ptr(), live.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(), bytes_,
-                                _current_stream(refs.get_device())))
+    _launch(device, lib().hc_page_compact, args, remap.data_ptr(), live.data_ptr(), cache.data_ptr(), planes, size, ws.data_ptr(),
+            bytes_)
     return table_out, refs_out, remap, live

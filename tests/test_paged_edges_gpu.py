@@ -193,3 +193,72 @@ def test_results_of_another_stream_are_not_handed_out_too_early(hc):
         torch.cuda.synchronize()
         assert torch.equal(kept, want), what
         del junk
+
+
+# -------------------------------------------------------------------------------------------- devices --
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it lies on another GPU."""
+
+    def get_device(self):
+        return 1
+
+
+def test_tensors_of_different_devices_are_refused(hc):
+    b = Batch(61, [(40, 300), (1, 35)], 8, 2, 128, 16, BF16, stale=0.0)
+    f, _ = hc.rotary_frequencies(128)
+    q, k, v, table, lens, cu = (x.cuda() for x in (b.q, b.k, b.v, b.table, b.lens, b.cu))
+    kv = rnd(5, b.tokens, 2, 128, dtype=BF16).cuda()
+    at = torch.arange(b.tokens, device="cuda")
+    pool = torch.stack((k, v))
+    refs = torch.ones(k.shape[0], dtype=torch.int32, device="cuda")
+    one = torch.ones(2, dtype=torch.int32, device="cuda")
+    ids_ = torch.tensor([0], dtype=torch.int32, device="cuda")
+    work = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    calls = [
+        (lambda a: hc.rotary(a[0], a[1], a[2], out=a[3]), [q, at, f, torch.empty_like(q)]),
+        (lambda a: hc.rotary_append(*a[:8], inv_freq=a[8], out=a[9]), [q, kv, kv.clone(), k, v, table, lens, cu, f, q.clone()]),
+        (lambda a: hc.paged_attention(*a[:6], out=a[6], workspace=a[7]), [q, k, v, table, lens, cu, q.clone(), work]),
+        (lambda a: hc.paged_attention_workspace_size(*a), [q, k, v, table, lens, cu]),
+        (lambda a: hc.page_copy(*a), [pool, ids_, ids_ + 1]),
+        (lambda a: hc.page_fork(*a), [pool, table, lens, refs, one]),
+        (lambda a: hc.page_extend(*a, page_size=16), [table, lens, refs, one]),
+        (lambda a: hc.page_release(*a, page_size=16), [table, lens, refs, one.byte()]),
+        (lambda a: hc.page_compact(*a), [pool, table, lens, refs]),
+    ]
+    for n, (call, args) in enumerate(calls):
+        call(args)
+        for i in range(len(args)):
+            bad = [t.as_subclass(Elsewhere) if j == i else t for j, t in enumerate(args)]
+            with pytest.raises(ValueError):
+                call(bad)
+                pytest.fail(f"call {n}: tensor {i} was taken")
+
+
+def test_a_stream_of_another_device_is_refused(hc):
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+    at = torch.zeros(2, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        hc.rotary(torch.zeros(2, 1, 8, device="cuda"), at, hc.rotary_frequencies(8)[0], stream=Stream())
+
+
+def test_tensors_of_another_device_than_the_current_one(hc, monkeypatch):
+    """The call makes the tensors' device the current one (here, where there is but one, the current one is said to be another)."""
+    from hyper_connection_rank_gb300 import _paged
+    entered = []
+    real = torch.cuda.device
+
+    def device(index):
+        entered.append(index)
+        return real(index)
+    for what, call in calls_with_streams(hc):
+        want = [t.clone() for t in call()]
+        monkeypatch.setattr(_paged, "_current_device", lambda: 3)
+        monkeypatch.setattr(torch.cuda, "device", device)
+        got = call()
+        monkeypatch.undo()
+        assert entered and set(entered) == {0}, what
+        entered.clear()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), what
