@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
       const int64_t end = first_row(b, s + 1);
       const int64_t pos = kv_len_of(b, s) - (end - t);
       int page = -1;
-      if (pos >= 0) page = page_of(b, s, pos / b.page_size);
+      // (a row past the last bound, or before the first, is no sequence's and has no place in its table)
+      if (pos >= 0 && t >= first_row(b, s) && t < end) page = page_of(b, s, pos / b.page_size);
       s_pos = pos;
       s_slot = page < 0 ? -1 : page * a.c_ps + pos % b.page_size * a.c_ts;
     }

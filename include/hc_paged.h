@@ -10,13 +10,16 @@
  * (strides in elements, the same for keys and values; d is contiguous). Row s
  * of page_table lists the pages of sequence s in order. kv_lens[s] counts its
  * tokens, the new ones of the call among them; what pages hold past that is
- * never read. With cu_q (seqs + 1 ascending offsets, cu_q[0] = 0 and
- * cu_q[seqs] = tokens) the new tokens of sequence s are the rows cu_q[s] ..
+ * never read. With cu_q (seqs + 1 ascending offsets, as a rule from
+ * 0 to tokens) the new tokens of sequence s are the rows cu_q[s] ..
  * cu_q[s+1] - 1 of the call; without it (NULL) every sequence has one. The
  * last new token of a sequence has position kv_lens[s] - 1, those before it
  * the positions before. A new token whose position would be negative (an
  * unused slot of a batch has kv_lens[s] = 0) sees nothing and is written
- * nowhere.
+ * nowhere. Rows before cu_q[0] and from cu_q[seqs] on, where a buffer of a
+ * fixed size has more rows than the sequences have new tokens, are no
+ * sequence's: they are written nowhere either (what q_out holds for them is of
+ * no use).
  *
  * Memory: all pointers are DEVICE pointers of the caller, except the argument
  * structs, which are read before the call returns. The calls allocate nothing,

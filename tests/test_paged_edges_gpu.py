@@ -262,3 +262,32 @@ def test_tensors_of_another_device_than_the_current_one(hc, monkeypatch):
         assert entered and set(entered) == {0}, what
         entered.clear()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), what
+
+
+# ------------------------------------------------------------------------- rows that no sequence has --
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("pad", [(0, 5), (0, 300), (3, 0), (4, 70)], ids=str)
+def test_append_writes_nothing_for_rows_past_the_bounds(hc, dtype, interleaved, pad):
+    """cu_q that begins past the first row or ends before the last (a buffer of a fixed size): those rows go nowhere, and the
+    others go where they would without them."""
+    f, _ = hc.rotary_frequencies(64)
+    front, back = pad
+    b = Batch(3, [(2, 40), (7, 47), (3, 160)], 2, 1, 64, 16, dtype, stale=None)
+    b.table = b.table[:, :10].contiguous()  # the last sequence fills its row: a place further on is past the table
+    k, v = (rnd(s, front + b.tokens + back, 1, 64, dtype=dtype).cuda() for s in (1, 2))
+    q = rnd(4, front + b.tokens + back, 2, 64, dtype=dtype).cuda()
+    rest = (b.table.cuda(), b.lens.cuda())
+    want = [b.k.cuda(), b.v.cuda()]
+    inner = slice(front, front + b.tokens)
+    wq = hc.rotary_append(q[inner], k[inner], v[inner], *want, *rest, b.cu.cuda(), inv_freq=f, interleaved=interleaved)
+    got = [b.k.cuda(), b.v.cuda()]
+    gq = hc.rotary_append(q, k, v, *got, *rest, (b.cu + front).cuda(), inv_freq=f, interleaved=interleaved)
+    assert torch.equal(gq[inner], wq)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool(torch.isfinite(gq.float()).all())
+    # bounds that leave no row to any sequence
+    none = [b.k.cuda(), b.v.cuda()]
+    hc.rotary_append(q, k, v, *none, *rest, torch.zeros_like(b.cu).cuda(), inv_freq=f, interleaved=interleaved)
+    assert torch.equal(none[0].cpu(), b.k) and torch.equal(none[1].cpu(), b.v)
