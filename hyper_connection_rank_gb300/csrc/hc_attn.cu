@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kThreads) general_kernel(AttnArgs a) {
   constexpr int RI = ROWS / 16, CI = DP / 64;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
   const int z = blockIdx.z, kvh = blockIdx.y;
+  if (a.clears && blockIdx.x == gridDim.x - 1) clear_unowned<T>(a, z * gridDim.y + kvh, gridDim.y * gridDim.z);
   AttnTile t;
   tile_of_slot(a, blockIdx.x, &t);
   if (t.rows == 0 || z >= t.splits) return;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(AttnArgs a, AttnGeome
   AttnTile t;
   tile_at(a, g, s, ((token - first) * a.group + head % a.group) / g.rows, &t);
   pdl_wait();  // (the lengths and tables are the caller's; only the partial results are the kernels' before)
-  if (t.rows == 0 || t.splits == 1) return;
+  if (token < first || (token - first) * a.group >= all || t.rows == 0 || t.splits == 1) return;  // (some rows are no sequence's)
   const int64_t step = a.tokens * a.heads;  // from one split to the next
   const float2* ml = a.part_ml + row;
   float top = neg_inf();
@@ -520,6 +521,7 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
     d.min_rows = 1;
     d.max_rows = small_rows;
     d.slot_is_seq = p.use_large;
+    d.clears = !p.use_large && a.cu_q != nullptr;
     d.spare_ctas = p.pieces.spare_ctas;
     d.units = p.pieces.units;
     d.clusters = p.pieces.clusters;
@@ -529,6 +531,7 @@ cudaError_t launch_t(const hc_paged_attention_t& a, bool aligned, int num_sms, c
   if (p.use_large) {
     d.g = p.large;
     d.slot_is_seq = false;
+    d.clears = a.cu_q != nullptr;
     d.min_rows = small_rows + 1;
     d.max_rows = INT64_MAX;
     const int64_t slots = slots_of(a, p.large.rows);

@@ -45,6 +45,7 @@ struct AttnArgs {
   AttnGeometry g;
   int64_t min_rows, max_rows;  // only sequences with that many rows (q_len * group)
   bool slot_is_seq;            // slot s is the first tile of sequence s
+  bool clears;                 // the last slot's CTAs clear the rows that no sequence has
   // hc_attn_rows.cu, where it splits single-token sequences itself: CTAs that there may be beside one for each tile, and pieces at
   // most (0: the splits above)
   int spare_ctas, units;
@@ -129,6 +130,24 @@ __device__ __forceinline__ void row_owner(const AttnArgs& a, const AttnTile& t, 
 
 __device__ __forceinline__ int64_t part_index(const AttnArgs& a, int z, int64_t token, int head) {
   return (static_cast<int64_t>(z) * a.tokens + token) * a.heads + head;
+}
+
+// Rows before the first bound and from the last one on are no sequence's and see nothing: zeros, and minus infinity, by CTA `part`
+// of `parts`.
+template <typename T>
+__device__ __forceinline__ void clear_unowned(const AttnArgs& a, int part, int parts) {
+  if (!a.b.cu_q) return;
+  const int64_t lo = first_row(a.b, 0), end = first_row(a.b, a.b.seqs), hi = end < lo ? lo : end;
+  const int n = a.heads * a.dim;
+  for (int64_t i = part; i < lo + a.tokens - hi; i += parts) {
+    const int64_t token = i < lo ? i : hi + (i - lo);
+    for (int e = threadIdx.x; e < n; e += blockDim.x) {
+      const int head = e / a.dim;
+      stf(static_cast<T*>(a.out) + token * a.o_ts + head * a.o_hs + (e - head * a.dim), 0.0f);
+    }
+    if (a.lse)
+      for (int h = threadIdx.x; h < a.heads; h += blockDim.x) a.lse[token * a.heads + h] = neg_inf();
+  }
 }
 
 // Whether either of two 16-bit numbers is infinite or NaN.

@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
   const int z = blockIdx.z, kvh = blockIdx.y;
   pdl_trigger();
+  if (a.clears && blockIdx.x == gridDim.x - 1) clear_unowned<float>(a, z * gridDim.y + kvh, gridDim.y * gridDim.z);
   AttnTile t;
   tile_of_slot(a, blockIdx.x, &t);
   if (t.rows == 0 || z >= t.splits) return;

@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rows_kernel(AttnArgs a) {
   const int kvh = blockIdx.y;
   int z = blockIdx.z;
   pdl_trigger();
+  if (SHARE == kBySplit && a.clears && blockIdx.x == gridDim.x - 1) clear_unowned<T>(a, z * gridDim.y + kvh, gridDim.y * gridDim.z);
   AttnTile t;
   int64_t k0, k1;
   if (!find_work<SHARE>(a, &t, &z, &k0, &k1)) return;

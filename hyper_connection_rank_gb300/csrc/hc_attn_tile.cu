@@ -1055,6 +1055,7 @@ __global__ void __launch_bounds__(256) join_kernel(AttnArgs a, Work w) {
   // piece 0 is the last of its CTA's segments, the others are the first of theirs
   const auto index = [&](int i, int r) { return (2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0)) * kPair + row0 + r; };
   pdl_wait();  // (in every thread, whatever it found: later kernels on the stream count on this one's end alone)
+  if (c0 == static_cast<int>(gridDim.x) - 1) clear_unowned<T>(a, blockIdx.y, gridDim.y);  // (no cut lies behind the last CTA's run)
   if (pieces == 0 || rows <= 0) return;
   {
     const int r = threadIdx.x >> 3, e = threadIdx.x & 7;

@@ -18,8 +18,8 @@
  * unused slot of a batch has kv_lens[s] = 0) sees nothing and is written
  * nowhere. Rows before cu_q[0] and from cu_q[seqs] on, where a buffer of a
  * fixed size has more rows than the sequences have new tokens, are no
- * sequence's: they are written nowhere either (what q_out holds for them is of
- * no use).
+ * sequence's: they see nothing and are written nowhere either (what q_out
+ * holds for them is of no use).
  *
  * Memory: all pointers are DEVICE pointers of the caller, except the argument
  * structs, which are read before the call returns. The calls allocate nothing,

@@ -291,3 +291,26 @@ def test_append_writes_nothing_for_rows_past_the_bounds(hc, dtype, interleaved, 
     none = [b.k.cuda(), b.v.cuda()]
     hc.rotary_append(q, k, v, *none, *rest, torch.zeros_like(b.cu).cuda(), inv_freq=f, interleaved=interleaved)
     assert torch.equal(none[0].cpu(), b.k) and torch.equal(none[1].cpu(), b.v)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("both", [[(1, 700), (2, 30)], [(5, 60), (1, 300)], [(130, 700), (1, 90), (17, 40)]], ids=["few", "some", "chunk"])
+@pytest.mark.parametrize("max_q", [None, 1])
+def test_attention_gives_zeros_for_rows_past_the_bounds(hc, dtype, dim, both, max_q):
+    for front, back in ((0, 1), (0, 333), (2, 0), (150, 40)):
+        b = Batch(47, both, 4, 2, dim, 16, dtype)
+        want, lse, tol, ltol = R.attention(b.q, b.k, b.v, b.table, b.lens, b.cu)
+        n = front + b.tokens + back
+        q = torch.full((n, 4, dim), 1.0, dtype=dtype, device="cuda")
+        inner = slice(front, front + b.tokens)
+        q[inner] = b.q.cuda()
+        out = torch.full((n, 4, dim), 7.0, dtype=dtype, device="cuda")
+        rest = (b.k.cuda(), b.v.cuda(), b.table.cuda(), b.lens.cuda())
+        got, glse = hc.paged_attention(q, *rest, (b.cu + front).cuda(), max_q=max_q, return_lse=True, out=out)
+        within(got[inner], want, tol, "out")
+        within(glse[inner], lse, ltol, "lse")
+        for rows in (slice(0, front), slice(n - back, n)):
+            assert bool((got[rows] == 0).all()) and bool((glse[rows] == -math.inf).all()), (front, back)
+        got, glse = hc.paged_attention(q, *rest, torch.zeros_like(b.cu).cuda(), max_q=max_q, return_lse=True, out=out)
+        assert bool((got == 0).all()) and bool((glse == -math.inf).all())
