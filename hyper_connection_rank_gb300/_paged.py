@@ -256,12 +256,13 @@ def _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, windo
     return front, back
 
 
-def paged_attention_workspace_size(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, max_q=None, max_kv=None, window=0,
-                                   flags=0):
-    """Bytes of workspace that ``paged_attention`` needs for these tensors (their contents do not matter)."""
+def paged_attention_workspace_size(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, *, scale=None, max_q=None, max_kv=None,
+                                   window=0, flags=0):
+    """Bytes of workspace that ``paged_attention`` needs for these tensors (their contents do not matter) and these arguments,
+    which steer the choice of kernels: give those of the call."""
     heads, dim = q.shape[1:]
     device = _device(q)
-    front, back = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, None, window, 0.0, max_q, max_kv, flags, 0, 0,
+    front, back = _attention_args(q, k_cache, v_cache, page_table, kv_lens, cu_q, scale, window, 0.0, max_q, max_kv, flags, 0, 0,
                                   (heads * dim, dim), device)
     return _sized(device, lib().hc_paged_attention_workspace_size, front + _NO_WORK + back)
 

@@ -140,8 +140,9 @@ typedef struct {
   float scale, softcap;
 } hc_paged_attention_t;
 
-/* Bytes of workspace for these sizes (pointers and lengths are not looked at
- * but for alignment, out and lse not at all); 0 if none is needed. */
+/* Bytes of workspace for these sizes, strides, hints, scale and flags, which
+ * steer the choice of kernels (pointers and lengths are not looked at but for
+ * alignment, out and lse not at all); 0 if none is needed. */
 size_t hc_paged_attention_workspace_size(const hc_paged_attention_t* args);
 hc_status_t hc_paged_attention(const hc_paged_attention_t* args, struct CUstream_st* stream);
 
