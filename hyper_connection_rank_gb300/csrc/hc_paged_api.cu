@@ -9,6 +9,12 @@
 
 #include "hc_paged_internal.h"
 
+#define HC_RETURN_IF(expr)                \
+  do {                                    \
+    const hc_status_t st_ = (expr);       \
+    if (st_ != HC_OK) return st_;         \
+  } while (0)
+
 namespace {
 
 using hc::dtype_size;
@@ -51,7 +57,25 @@ hc_status_t check_apart(const Span* outs, int n_out, const Span* ins, int n_in) 
   return HC_OK;
 }
 
-// Rows of heads: (tokens, heads, dim) with element strides. Heads of a token
+constexpr int64_t kMaxElems = int64_t{1} << 46;
+bool sane(int64_t v) { return v >= 0 && v <= kMaxElems; }
+// Whether the last of n entries lies within 2^46 elements of the first, so that no sum or product of extents passes 64 bits.
+bool within(int64_t n, int64_t stride) { return sane(stride) && (n <= 1 || stride <= kMaxElems / (n - 1)); }
+
+// The largest count of tokens, of which all products below are formed.
+hc_status_t check_tokens(int64_t tokens) {
+  if (tokens < 0) return fail(HC_ERR_INVALID_ARG, "invalid tokens=%lld", ll(tokens));
+  if (tokens >= int64_t{1} << 31) return fail(HC_ERR_UNSUPPORTED, "tokens=%lld beyond 2^31", ll(tokens));
+  return HC_OK;
+}
+
+hc_status_t check_extent(const char* name, int64_t tokens, int64_t ts, int heads, int64_t hs) {
+  if (!sane(ts) || !sane(hs)) return fail(HC_ERR_INVALID_ARG, "invalid strides of %s", name);
+  if (!within(tokens, ts) || !within(heads, hs)) return fail(HC_ERR_UNSUPPORTED, "%s beyond 2^46 elements", name);
+  return HC_OK;
+}
+
+// Rows of heads: (tokens, heads, dim) with element strides, within the extents above. Heads of a token
 // must not overlap one another, nor tokens; either may be the outer one.
 bool strides_valid(int64_t tokens, int64_t ts, int heads, int64_t hs, int dim) {
   if (tokens <= 0 || heads <= 0) return true;
@@ -72,14 +96,11 @@ bool on_elements(int dtype, std::initializer_list<const void*> pointers) {
   return true;
 }
 
-constexpr int64_t kMaxElems = int64_t{1} << 46;
-bool sane(int64_t v) { return v >= 0 && v <= kMaxElems; }
-
 hc_status_t check_cache(int64_t pages, int64_t ps, int page, int64_t ts, int kv_heads, int64_t hs, int dim) {
   if (pages < 1 || pages > (int64_t{1} << 31) - 1 || page < 1 || page > (1 << 20))
     return fail(HC_ERR_INVALID_ARG, "invalid pool: num_pages=%lld page_size=%d", ll(pages), page);
-  if (!sane(ps) || !sane(ts) || !sane(hs) || !strides_valid(page, ts, kv_heads, hs, dim) ||
-      (pages > 1 && ps < 1))
+  HC_RETURN_IF(check_extent("a page", page, ts, kv_heads, hs));
+  if (!sane(ps) || !strides_valid(page, ts, kv_heads, hs, dim) || (pages > 1 && ps < 1))
     return fail(HC_ERR_INVALID_ARG, "cache strides (page %lld, token %lld, head %lld) do not fit heads of %d", ll(ps),
                 ll(ts), ll(hs), dim);
   if (pages - 1 > kMaxElems / std::max<int64_t>(ps, 1)) return fail(HC_ERR_UNSUPPORTED, "pool beyond 2^46 elements");
@@ -88,11 +109,13 @@ hc_status_t check_cache(int64_t pages, int64_t ps, int page, int64_t ts, int kv_
 
 hc_status_t check_batch(const int32_t* table, const int32_t* lens, const int32_t* cu, int64_t tokens, int seqs,
                         int max_pages, int64_t table_stride) {
-  if (seqs < 0 || tokens < 0 || max_pages < 1 || max_pages > (1 << 20))
+  HC_RETURN_IF(check_tokens(tokens));
+  if (seqs < 0 || max_pages < 1 || max_pages > (1 << 20))
     return fail(HC_ERR_INVALID_ARG, "invalid batch: seqs=%d tokens=%lld max_pages=%d", seqs, ll(tokens), max_pages);
   if (table_stride < max_pages && seqs > 1)
     return fail(HC_ERR_INVALID_ARG, "table_stride %lld is below max_pages %d", ll(table_stride), max_pages);
-  if (table_stride < 0 || table_stride > kMaxElems) return fail(HC_ERR_INVALID_ARG, "invalid table_stride");
+  if (!sane(table_stride)) return fail(HC_ERR_INVALID_ARG, "invalid table_stride");
+  if (!within(seqs, table_stride)) return fail(HC_ERR_UNSUPPORTED, "page_table beyond 2^46 entries");
   if (tokens > 0 && (seqs < 1 || table == nullptr || lens == nullptr))
     return fail(HC_ERR_INVALID_ARG, "tokens without sequences, page_table or kv_lens");
   if (cu == nullptr && tokens != seqs)
@@ -121,24 +144,19 @@ hc_status_t check_rot(int rot, int dim) {
 
 }  // namespace
 
-#define HC_RETURN_IF(expr)                \
-  do {                                    \
-    const hc_status_t st_ = (expr);       \
-    if (st_ != HC_OK) return st_;         \
-  } while (0)
-
 extern "C" {
 
 hc_status_t hc_rotary(const hc_rotary_t* args, cudaStream_t stream) {
   if (args == nullptr) return fail(HC_ERR_INVALID_ARG, "null args");
   const hc_rotary_t& a = *args;
   if (!dtype_valid(a.dtype)) return fail(HC_ERR_INVALID_ARG, "invalid dtype %d", a.dtype);
-  if (a.tokens < 0) return fail(HC_ERR_INVALID_ARG, "invalid tokens=%lld", ll(a.tokens));
+  HC_RETURN_IF(check_tokens(a.tokens));
   HC_RETURN_IF(check_heads(a.heads, a.head_dim, 1024));
   HC_RETURN_IF(check_rot(a.rot_dim, a.head_dim));
-  if (!sane(a.x_token_stride) || !sane(a.x_head_stride) || !sane(a.out_token_stride) || !sane(a.out_head_stride) ||
-      !strides_valid(a.tokens, a.out_token_stride, a.heads, a.out_head_stride, a.head_dim))
-    return fail(HC_ERR_INVALID_ARG, "invalid strides");
+  HC_RETURN_IF(check_extent("x", a.tokens, a.x_token_stride, a.heads, a.x_head_stride));
+  HC_RETURN_IF(check_extent("out", a.tokens, a.out_token_stride, a.heads, a.out_head_stride));
+  if (!strides_valid(a.tokens, a.out_token_stride, a.heads, a.out_head_stride, a.head_dim))
+    return fail(HC_ERR_INVALID_ARG, "invalid strides of out");
   if (a.tokens * a.heads >= (int64_t{1} << 31)) return fail(HC_ERR_UNSUPPORTED, "tokens * heads beyond 2^31");
   if (a.tokens == 0) return HC_OK;
   if (a.x == nullptr || a.out == nullptr || a.positions == nullptr || (a.inv_freq == nullptr && a.rot_dim > 0))
@@ -168,9 +186,10 @@ hc_status_t hc_rotary_append(const hc_rotary_append_t* args, cudaStream_t stream
   HC_RETURN_IF(check_batch(a.page_table, a.kv_lens, a.cu_q, a.tokens, a.seqs, a.max_pages, a.table_stride));
   HC_RETURN_IF(check_cache(a.num_pages, a.cache_page_stride, a.page_size, a.cache_token_stride, a.kv_heads,
                            a.cache_head_stride, a.head_dim));
-  for (const int64_t v : {a.q_token_stride, a.q_head_stride, a.k_token_stride, a.k_head_stride, a.v_token_stride,
-                          a.v_head_stride, a.out_token_stride, a.out_head_stride})
-    if (!sane(v)) return fail(HC_ERR_INVALID_ARG, "invalid strides");
+  HC_RETURN_IF(check_extent("q", a.tokens, a.q_token_stride, a.heads, a.q_head_stride));
+  HC_RETURN_IF(check_extent("k", a.tokens, a.k_token_stride, a.kv_heads, a.k_head_stride));
+  HC_RETURN_IF(check_extent("v", a.tokens, a.v_token_stride, a.kv_heads, a.v_head_stride));
+  HC_RETURN_IF(check_extent("q_out", a.tokens, a.out_token_stride, a.heads, a.out_head_stride));
   if (!strides_valid(a.tokens, a.out_token_stride, a.heads, a.out_head_stride, a.head_dim))
     return fail(HC_ERR_INVALID_ARG, "invalid strides of q_out");
   if (a.tokens * (a.heads + 2 * static_cast<int64_t>(a.kv_heads)) >= (int64_t{1} << 31))
@@ -228,9 +247,10 @@ hc_status_t check_attention(const hc_paged_attention_t& a) {
   HC_RETURN_IF(check_batch(a.page_table, a.kv_lens, a.cu_q, a.tokens, a.seqs, a.max_pages, a.table_stride));
   HC_RETURN_IF(check_cache(a.num_pages, a.cache_page_stride, a.page_size, a.cache_token_stride, a.kv_heads,
                            a.cache_head_stride, a.head_dim));
-  if (!sane(a.q_token_stride) || !sane(a.q_head_stride) || !sane(a.out_token_stride) || !sane(a.out_head_stride) ||
-      !strides_valid(a.tokens, a.out_token_stride, a.heads, a.out_head_stride, a.head_dim))
-    return fail(HC_ERR_INVALID_ARG, "invalid strides of q or out");
+  HC_RETURN_IF(check_extent("q", a.tokens, a.q_token_stride, a.heads, a.q_head_stride));
+  HC_RETURN_IF(check_extent("out", a.tokens, a.out_token_stride, a.heads, a.out_head_stride));
+  if (!strides_valid(a.tokens, a.out_token_stride, a.heads, a.out_head_stride, a.head_dim))
+    return fail(HC_ERR_INVALID_ARG, "invalid strides of out");
   if (a.tokens * a.heads >= (int64_t{1} << 31) || a.seqs > (1 << 24))
     return fail(HC_ERR_UNSUPPORTED, "tokens * heads beyond 2^31 or more than 2^24 sequences");
   return HC_OK;
@@ -292,10 +312,11 @@ hc_status_t check_pages(const hc_pages_t* p, bool tables_out, bool lens_out, int
   if (p == nullptr) return fail(HC_ERR_INVALID_ARG, "null pages");
   if (p->num_pages < 1 || p->num_pages >= (int64_t{1} << 31) || p->seqs < 0 || p->max_pages < 1 ||
       p->max_pages > (1 << 20) || p->page_size < 1 || (p->seqs > 1 && p->table_stride < p->max_pages) ||
-      p->table_stride < 0 || p->table_stride > kMaxElems)
+      !sane(p->table_stride))
     return fail(HC_ERR_INVALID_ARG, "invalid sizes: num_pages=%lld seqs=%d max_pages=%d page_size=%d",
                 ll(p->num_pages), p->seqs, p->max_pages, p->page_size);
   if (p->seqs > (1 << 24) || seqs_out > (1 << 24)) return fail(HC_ERR_UNSUPPORTED, "more than 2^24 sequences");
+  if (!within(p->seqs, p->table_stride)) return fail(HC_ERR_UNSUPPORTED, "page_table beyond 2^46 entries");
   if (p->refs == nullptr || p->refs_out == nullptr || (p->seqs > 0 && (!p->page_table || !p->lens)) ||
       (seqs_out > 0 && ((tables_out && !p->page_table_out) || (lens_out && !p->lens_out))))
     return fail(HC_ERR_INVALID_ARG, "null pointer");
@@ -318,7 +339,7 @@ hc_status_t check_pool(const void* cache, int64_t planes, int64_t num_pages, int
       planes > (int64_t{1} << 31))
     return fail(HC_ERR_INVALID_ARG, "invalid pool: planes=%lld num_pages=%lld page_bytes=%lld", ll(planes),
                 ll(num_pages), ll(page_bytes));
-  if (planes > 0 && num_pages * page_bytes > (int64_t{1} << 50) / planes)
+  if (planes > 0 && num_pages > (int64_t{1} << 50) / planes / page_bytes)
     return fail(HC_ERR_UNSUPPORTED, "pool beyond 2^50 bytes");
   if (planes > 0 && cache == nullptr) return fail(HC_ERR_INVALID_ARG, "null cache");
   return HC_OK;

@@ -1,0 +1,54 @@
+"""The paged-cache entry points on the host at the ends of their ranges (CPU only; no compute calls): sizes whose products
+pass 64 bits, and outputs that overlap."""
+import pytest
+
+from hyper_connection_rank_gb300 import _binding as B
+from test_abi_paged import APP, ATT, LIST, ONE, PAG, POOL, ROT, WS, L, pack  # noqa: F401 (L is a fixture)
+
+BIG, FAR = 2 ** 62, 2 ** 45  # tokens; a stride within the limit of one
+
+
+def refused(status):
+    return status in (B.HC_ERR_INVALID_ARG, B.HC_ERR_UNSUPPORTED)
+
+
+@pytest.mark.parametrize("over", [dict(tokens=BIG), dict(tokens=2 ** 31), dict(tokens=2 ** 61 + 1, heads=8),
+                                  dict(tokens=2 ** 29, heads=1, x_token_stride=FAR, out_token_stride=64),
+                                  dict(tokens=2 ** 29, heads=1, out_token_stride=FAR),
+                                  dict(heads=65535, tokens=1, x_head_stride=FAR, out_head_stride=64),
+                                  dict(heads=65535, tokens=1, out_head_stride=FAR)], ids=str)
+def test_rotary_sizes_beyond_64_bits(L, over):  # noqa: F811
+    # (the outputs lie far above the inputs, so that no overlap is found by chance)
+    assert refused(L.hc_rotary(pack("hc_rotary_t", **{**ROT, "out": 2 ** 48, **over}), None))
+
+
+@pytest.mark.parametrize("over", [dict(tokens=BIG), dict(tokens=2 ** 60, cu_q=0, seqs=0), dict(tokens=2 ** 29, heads=1, q_token_stride=FAR),
+                                  dict(tokens=2 ** 29, heads=1, k_token_stride=FAR), dict(tokens=2 ** 29, heads=1, v_token_stride=FAR),
+                                  dict(tokens=2 ** 29, heads=1, out_token_stride=FAR),
+                                  dict(page_size=2 ** 20, cache_token_stride=FAR), dict(kv_heads=65535, cache_head_stride=FAR),
+                                  dict(seqs=2 ** 30, table_stride=FAR)], ids=str)
+def test_append_sizes_beyond_64_bits(L, over):  # noqa: F811
+    app = {**APP, "q_out": 2 ** 48, "k_cache": 2 ** 49, "v_cache": 2 ** 50}
+    assert refused(L.hc_rotary_append(pack("hc_rotary_append_t", **{**app, **over}), None))
+
+
+@pytest.mark.parametrize("over", [dict(tokens=BIG), dict(tokens=2 ** 61 + 4), dict(tokens=2 ** 29, heads=1, q_token_stride=FAR),
+                                  dict(tokens=2 ** 29, heads=1, out_token_stride=FAR), dict(heads=65535, q_head_stride=FAR, tokens=1),
+                                  dict(page_size=2 ** 20, cache_token_stride=FAR), dict(kv_heads=2, heads=2, cache_head_stride=2 ** 47),
+                                  dict(seqs=2 ** 24, table_stride=FAR)], ids=str)
+def test_attention_sizes_beyond_64_bits(L, over):  # noqa: F811
+    att = {**ATT, "out": 2 ** 48}
+    assert refused(L.hc_paged_attention(pack("hc_paged_attention_t", **{**att, **over}), None))
+    assert L.hc_paged_attention_workspace_size(pack("hc_paged_attention_t", **{**att, **over})) == 0
+
+
+def test_pools_beyond_64_bits(L):  # noqa: F811
+    many = 2 ** 31 - 1
+    assert refused(L.hc_page_copy(POOL, 1, many, 2 ** 36, LIST, LIST, 3, None))
+    assert refused(L.hc_page_copy(POOL, 2 ** 31, many, 2 ** 33, LIST, LIST, 3, None))
+    p = pack("hc_pages_t", **{**PAG, "num_pages": many, "refs": 2 ** 40, "refs_out": 2 ** 41})
+    need = L.hc_pages_workspace_size(many, 2)
+    assert refused(L.hc_page_fork(p, LIST, 2, ONE, 2 ** 44, 1, 2 ** 36, 2 ** 42, need, None))
+    assert refused(L.hc_page_compact(p, LIST, ONE, 2 ** 44, 1, 2 ** 36, 2 ** 42, need, None))
+    p = pack("hc_pages_t", **{**PAG, "seqs": 2 ** 24, "table_stride": FAR, "page_table_out": 2 ** 40, "lens_out": 2 ** 50})
+    assert refused(L.hc_page_release(p, 2 ** 51, None))
