@@ -308,7 +308,7 @@ hc_status_t hc_paged_attention(const hc_paged_attention_t* args, cudaStream_t st
 
 namespace {
 
-hc_status_t check_pages(const hc_pages_t* p, bool tables_out, bool lens_out, int64_t seqs_out) {
+hc_status_t check_pages(const hc_pages_t* p, bool lens_out, int64_t seqs_out) {
   if (p == nullptr) return fail(HC_ERR_INVALID_ARG, "null pages");
   if (p->num_pages < 1 || p->num_pages >= (int64_t{1} << 31) || p->seqs < 0 || p->max_pages < 1 ||
       p->max_pages > (1 << 20) || p->page_size < 1 || (p->seqs > 1 && p->table_stride < p->max_pages) ||
@@ -318,14 +318,23 @@ hc_status_t check_pages(const hc_pages_t* p, bool tables_out, bool lens_out, int
   if (p->seqs > (1 << 24) || seqs_out > (1 << 24)) return fail(HC_ERR_UNSUPPORTED, "more than 2^24 sequences");
   if (!within(p->seqs, p->table_stride)) return fail(HC_ERR_UNSUPPORTED, "page_table beyond 2^46 entries");
   if (p->refs == nullptr || p->refs_out == nullptr || (p->seqs > 0 && (!p->page_table || !p->lens)) ||
-      (seqs_out > 0 && ((tables_out && !p->page_table_out) || (lens_out && !p->lens_out))))
+      (seqs_out > 0 && (!p->page_table_out || (lens_out && !p->lens_out))))
     return fail(HC_ERR_INVALID_ARG, "null pointer");
-  const Span ins[3] = {span("page_table", p->page_table, ((p->seqs - 1) * p->table_stride + p->max_pages) * 4),
-                       span("lens", p->lens, p->seqs * int64_t{4}), span("refs", p->refs, p->num_pages * 4)};
-  const Span outs[3] = {span("page_table_out", tables_out ? p->page_table_out : nullptr, seqs_out * p->max_pages * 4),
-                        span("lens_out", lens_out ? p->lens_out : nullptr, seqs_out * 4),
-                        span("refs_out", p->refs_out, p->num_pages * 4)};
-  return check_apart(outs, 3, ins, 3);
+  return HC_OK;
+}
+
+// The tables and counts, and what a call has beside them: no output may overlap an input or another output. (With `list` an input
+// and `more` outputs; a span of no bytes overlaps nothing.)
+hc_status_t check_pages_apart(const hc_pages_t& p, bool lens_out, int64_t seqs_out, const Span& list,
+                              std::initializer_list<Span> more) {
+  const Span ins[4] = {span("page_table", p.page_table, p.seqs > 0 ? ((p.seqs - 1) * p.table_stride + p.max_pages) * 4 : 0),
+                       span("lens", p.lens, p.seqs * int64_t{4}), span("refs", p.refs, p.num_pages * 4), list};
+  Span outs[8] = {span("page_table_out", p.page_table_out, seqs_out * p.max_pages * 4),
+                  span("lens_out", lens_out ? p.lens_out : nullptr, seqs_out * 4),
+                  span("refs_out", p.refs_out, p.num_pages * 4)};
+  int n = 3;
+  for (const Span& o : more) outs[n++] = o;
+  return check_apart(outs, n, ins, 4);
 }
 
 hc_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
@@ -371,11 +380,14 @@ hc_status_t hc_page_fork(const hc_pages_t* pages, const int32_t* parents, int32_
                          int64_t planes, int64_t page_bytes, void* workspace, size_t workspace_bytes,
                          cudaStream_t stream) {
   if (children < 0) return fail(HC_ERR_INVALID_ARG, "invalid children=%d", children);
-  HC_RETURN_IF(check_pages(pages, true, true, children));
+  HC_RETURN_IF(check_pages(pages, true, children));
   HC_RETURN_IF(check_pool(cache, planes, pages->num_pages, page_bytes));
   if ((children > 0 && parents == nullptr) || missing == nullptr) return fail(HC_ERR_INVALID_ARG, "null pointer");
-  HC_RETURN_IF(check_workspace(workspace, workspace_bytes,
-                               hc::pages_workspace(pages->num_pages, std::max(pages->seqs, children))));
+  const size_t need = hc::pages_workspace(pages->num_pages, std::max(pages->seqs, children));
+  HC_RETURN_IF(check_workspace(workspace, workspace_bytes, need));
+  HC_RETURN_IF(check_pages_apart(*pages, true, children, span("parents", parents, children * int64_t{4}),
+                                 {span("missing", missing, 4), span("cache", cache, planes * pages->num_pages * page_bytes),
+                                  span("workspace", workspace, static_cast<int64_t>(need))}));
   int sms = 0;
   HC_RETURN_IF(hc::current_device_sms(&sms));
   return launched(hc::launch_page_fork(*pages, parents, children, missing, cache, planes, page_bytes, workspace, sms, stream));
@@ -383,17 +395,21 @@ hc_status_t hc_page_fork(const hc_pages_t* pages, const int32_t* parents, int32_
 
 hc_status_t hc_page_extend(const hc_pages_t* pages, const int32_t* new_tokens, int32_t* missing, void* workspace,
                            size_t workspace_bytes, cudaStream_t stream) {
-  HC_RETURN_IF(check_pages(pages, true, true, pages ? pages->seqs : 0));
+  HC_RETURN_IF(check_pages(pages, true, pages ? pages->seqs : 0));
   if ((pages->seqs > 0 && new_tokens == nullptr) || missing == nullptr) return fail(HC_ERR_INVALID_ARG, "null pointer");
-  HC_RETURN_IF(check_workspace(workspace, workspace_bytes, hc::pages_workspace(pages->num_pages, pages->seqs)));
+  const size_t need = hc::pages_workspace(pages->num_pages, pages->seqs);
+  HC_RETURN_IF(check_workspace(workspace, workspace_bytes, need));
+  HC_RETURN_IF(check_pages_apart(*pages, true, pages->seqs, span("new_tokens", new_tokens, pages->seqs * int64_t{4}),
+                                 {span("missing", missing, 4), span("workspace", workspace, static_cast<int64_t>(need))}));
   int sms = 0;
   HC_RETURN_IF(hc::current_device_sms(&sms));
   return launched(hc::launch_page_extend(*pages, new_tokens, missing, workspace, sms, stream));
 }
 
 hc_status_t hc_page_release(const hc_pages_t* pages, const uint8_t* drop, cudaStream_t stream) {
-  HC_RETURN_IF(check_pages(pages, true, true, pages ? pages->seqs : 0));
+  HC_RETURN_IF(check_pages(pages, true, pages ? pages->seqs : 0));
   if (pages->seqs > 0 && drop == nullptr) return fail(HC_ERR_INVALID_ARG, "null pointer");
+  HC_RETURN_IF(check_pages_apart(*pages, true, pages->seqs, span("drop", drop, pages->seqs), {}));
   int sms = 0;
   HC_RETURN_IF(hc::current_device_sms(&sms));
   return launched(hc::launch_page_release(*pages, drop, sms, stream));
@@ -401,10 +417,15 @@ hc_status_t hc_page_release(const hc_pages_t* pages, const uint8_t* drop, cudaSt
 
 hc_status_t hc_page_compact(const hc_pages_t* pages, int32_t* remap, int32_t* live, void* cache, int64_t planes,
                             int64_t page_bytes, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  HC_RETURN_IF(check_pages(pages, true, false, pages ? pages->seqs : 0));
+  HC_RETURN_IF(check_pages(pages, false, pages ? pages->seqs : 0));
   HC_RETURN_IF(check_pool(cache, planes, pages->num_pages, page_bytes));
   if (remap == nullptr || live == nullptr) return fail(HC_ERR_INVALID_ARG, "null pointer");
-  HC_RETURN_IF(check_workspace(workspace, workspace_bytes, hc::pages_workspace(pages->num_pages, pages->seqs)));
+  const size_t need = hc::pages_workspace(pages->num_pages, pages->seqs);
+  HC_RETURN_IF(check_workspace(workspace, workspace_bytes, need));
+  HC_RETURN_IF(check_pages_apart(*pages, false, pages->seqs, span("page_table", nullptr, 0),
+                                 {span("remap", remap, pages->num_pages * 4), span("live", live, 4),
+                                  span("cache", cache, planes * pages->num_pages * page_bytes),
+                                  span("workspace", workspace, static_cast<int64_t>(need))}));
   int sms = 0;
   HC_RETURN_IF(hc::current_device_sms(&sms));
   return launched(hc::launch_page_compact(*pages, remap, live, cache, planes, page_bytes, workspace, sms, stream));

@@ -52,3 +52,50 @@ def test_pools_beyond_64_bits(L):  # noqa: F811
     assert refused(L.hc_page_compact(p, LIST, ONE, 2 ** 44, 1, 2 ** 36, 2 ** 42, need, None))
     p = pack("hc_pages_t", **{**PAG, "seqs": 2 ** 24, "table_stride": FAR, "page_table_out": 2 ** 40, "lens_out": 2 ** 50})
     assert refused(L.hc_page_release(p, 2 ** 51, None))
+
+
+# ------------------------------------------------------------------------------- outputs that overlap --
+
+# Places apart from one another.
+AT = dict(table=0x1000000, lens=0x1100000, refs=0x1200000, table_out=0x1300000, lens_out=0x1400000, refs_out=0x1500000,
+          ws=0x2000000, cache=0x3000000, list=0x4000000, missing=0x5000000, remap=0x5100000, live=0x5200000)
+SIZE = dict(table=(5 + 5) * 4, lens=8, refs=36, table_out=40, lens_out=8, refs_out=36, cache=2 * 9 * 64, list=8, missing=4, remap=36,
+            live=4)
+
+
+def page_call(L, what, at):  # noqa: F811
+    p = pack("hc_pages_t", page_table=at["table"], lens=at["lens"], refs=at["refs"], page_table_out=at["table_out"],
+             lens_out=at["lens_out"], refs_out=at["refs_out"], num_pages=9, table_stride=5, seqs=2, max_pages=5, page_size=16)
+    n = L.hc_pages_workspace_size(9, 2)
+    if what == "fork":
+        return L.hc_page_fork(p, at["list"], 2, at["missing"], at["cache"], 2, 64, at["ws"], n, None)
+    if what == "extend":
+        return L.hc_page_extend(p, at["list"], at["missing"], at["ws"], n, None)
+    if what == "release":
+        return L.hc_page_release(p, at["list"], None)
+    return L.hc_page_compact(p, at["remap"], at["live"], at["cache"], 2, 64, at["ws"], n, None)
+
+
+INPUTS = ["table", "lens", "refs"]
+OUTPUTS = {"fork": ["table_out", "lens_out", "refs_out", "missing", "cache", "ws"],
+           "extend": ["table_out", "lens_out", "refs_out", "missing", "ws"],
+           "release": ["table_out", "lens_out", "refs_out"],
+           "compact": ["table_out", "refs_out", "remap", "live", "cache", "ws"]}
+READS = {"fork": ["list"], "extend": ["list"], "release": ["list"], "compact": []}
+
+
+@pytest.mark.parametrize("what", sorted(OUTPUTS))
+def test_page_operators_refuse_overlaps(L, what):  # noqa: F811
+    """Every output against every input and every other output: at the same place, and ending or beginning inside it."""
+    size = {**SIZE, "ws": L.hc_pages_workspace_size(9, 2)}
+    for out in OUTPUTS[what]:
+        for other in INPUTS + READS[what] + OUTPUTS[what]:
+            if other == out:
+                continue
+            last = 2 if what == "release" and other == "list" else size[other]  # (a byte to a sequence there)
+            for place in (AT[other], AT[other] + last - 1, AT[other] - size[out] + 1):
+                if out == "ws" and place % 256:
+                    continue  # refused for its alignment
+                got = page_call(L, what, {**AT, out: place})
+                assert got == B.HC_ERR_INVALID_ARG, (out, other, hex(place))
+                assert b"overlaps" in L.hc_last_error(), (out, other)
