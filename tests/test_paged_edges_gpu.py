@@ -320,11 +320,11 @@ def test_attention_gives_zeros_for_rows_past_the_bounds(hc, dtype, dim, both, ma
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
 @pytest.mark.parametrize("scale", [None, -0.2, 0.0, 1e-6])
-@pytest.mark.parametrize("both", [[(1, 3001)], [(90, 2000), (1, 90)]], ids=["single", "chunk"])
+@pytest.mark.parametrize("both", [[(1, 3001)], [(500, 4000), (1, 90)]], ids=["single", "chunk"])
 def test_a_workspace_of_the_size_asked_for_suffices(hc, dtype, scale, both):
     b = Batch(37, both, 8, 2, 128, 16, dtype, cu=both[0][0] > 1)
     t = [b.cuda(x) for x in (b.q, b.k, b.v, b.table, b.lens, b.cu)]
-    for kw in ({}, dict(window=500), dict(max_q=90, max_kv=3001), dict(flags=hc.HC_FLAG_FORCE_GENERAL)):
+    for kw in ({}, dict(window=500), dict(max_q=500, max_kv=4000), dict(flags=hc.HC_FLAG_FORCE_GENERAL)):
         n = hc.paged_attention_workspace_size(*t, scale=scale, **kw)
         work = torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda")
         got = hc.paged_attention(*t, scale=scale, workspace=work, **kw)
