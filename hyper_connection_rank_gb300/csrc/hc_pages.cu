@@ -39,12 +39,13 @@ constexpr int kCopyCtas = 64;     // CTAs to an SM, of which four run at once
 
 // Moves list[i]: page src[i] -> dst[i] of every plane, for i < *count (or
 // count_max where count is NULL). Units are pieces of kCopyThreads * kCopyVecs
-// vectors of one page of one plane; a CTA takes every gridDim.x-th.
+// vectors of one page of one plane; a CTA takes every gridDim.x-th. The lists and
+// the count may be the work of the kernel before, which still runs when this one
+// starts: they are read after the wait, and not as data that never changes.
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(V* cache, int64_t planes, int64_t num_pages,
-                                                            int64_t page_vecs, const int32_t* __restrict__ src,
-                                                            const int32_t* __restrict__ dst, int64_t count_max,
-                                                            const int32_t* __restrict__ count, int pieces) {
+                                                            int64_t page_vecs, const int32_t* src, const int32_t* dst,
+                                                            int64_t count_max, const int32_t* count, int pieces) {
   pdl_wait();
   const int64_t n = count ? min(static_cast<int64_t>(*count), count_max) : count_max;
   const int64_t units = n * planes * pieces;
