@@ -247,6 +247,13 @@ __global__ void __launch_bounds__(kThreads) general_kernel(AttnArgs a) {
   }
 }
 
+// Before its wait for the kernels whose splits it joins, the kernel below reads
+// nothing but the caller's lengths and bounds. They are no work of those kernels,
+// the first of which was launched to wait for everything before it, so they were
+// complete, and written back, before it began. Read after the wait they
+// lengthen the chain of loads: 46.3 -> 47.4 us for 64 contexts of 1000, 55.4 -> 57.6
+// for 40 sequences of up to 3 new tokens behind 8000.
+//
 // Joins the splits of every row that has more than one: with M = max_z m_z,
 //   out = sum_z 2^(m_z - M) o_z / sum_z 2^(m_z - M) l_z.
 // WARPS warps to a row: all weights first, at once, then each warp adds every
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(AttnArgs a, AttnGeome
   const AttnGeometry& g = all <= small_rows ? small : large;
   AttnTile t;
   tile_at(a, g, s, ((token - first) * a.group + head % a.group) / g.rows, &t);
-  pdl_wait();  // (the lengths and tables are the caller's; only the partial results are the kernels' before)
+  pdl_wait();
   if (token < first || (token - first) * a.group >= all || t.rows == 0 || t.splits == 1) return;  // (some rows are no sequence's)
   const int64_t step = a.tokens * a.heads;  // from one split to the next
   const float2* ml = a.part_ml + row;

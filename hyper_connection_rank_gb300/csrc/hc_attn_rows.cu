@@ -732,7 +732,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) f32_rows_kernel(AttnArgs a) {
 // Joins the pieces of every sequence that has more than one (as combine_kernel of
 // hc_attn.cu does splits), a CTA to a row: all weights first, then each warp
 // adds every eighth piece. The pieces are worked out while the other kernel still
-// runs.
+// runs, from the caller's lengths alone, which were complete before that kernel
+// began (its launch waits for everything before it). Worked out after the wait, or left
+// by the other kernel and read then, they cost 2 us: eight contexts of 4001, 20.6 -> 22.6.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) rows_join_kernel(AttnArgs a) {
   __shared__ float s_w[kMaxPieces];

@@ -75,10 +75,17 @@ struct Cfg {
   static constexpr int kSmem = 2 * kQ + kSlots * kSlot + kStage + 1024;
 };
 
+// A tile that a cut goes through, for the kernel that joins its pieces.
+struct JoinTile {
+  AttnTile t;
+  int kv_head, pieces;  // pieces of the CTAs from this one on; 0: none to join here
+};
+
 struct Work {
   const AttnTile* tiles;  // tile of each slot
   const int32_t* prefix;  // units of the tiles before each slot, per key head; [slots] = all
   int slots, ctas;
+  JoinTile* joins;        // of each CTA, the tile that its run ends in, if that is the first cut in it
   float2* part_ml;        // [2 * ctas][kPair]
   float* part_o;          // [2 * ctas][kPair][dim]
 };
@@ -177,6 +184,21 @@ __device__ __forceinline__ void segment_at(const Work& w, const Run& run, int64_
   const int64_t from = u - g->at, to = u1 - g->at;
   g->j0 = from < 0 ? 0 : static_cast<int>(from);
   g->j1 = to < 0 ? 0 : to < g->n ? static_cast<int>(to) : g->n;
+}
+
+// What is to be joined of the tile that cut c + 1 goes through, if that is the first cut in it (full warps).
+__device__ __forceinline__ JoinTile join_at(const Work& w, const Run& run, int c) {
+  JoinTile j = {};
+  if (c + 1 < run.ctas) {
+    Segment g;
+    segment_at(w, run, run.start(c + 1), run.all, &g);
+    if (g.j0 > 0 && run.start(c) <= g.at) {
+      j.t = g.t;
+      j.kv_head = g.kv_head;
+      for (j.pieces = 1; c + j.pieces < run.ctas && run.start(c + j.pieces) < g.at + g.n;) ++j.pieces;
+    }
+  }
+  return j;
 }
 
 // Blocks of tile x (0: A, 1: B) of a pair: those up to the last key its last row sees.
@@ -673,8 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       fix_all();
     } else {
       // ---- the run's segments, one after another ----
+      const Run run(w, a.kv_heads);
       const auto plan_all = [&]() -> bool {
-        const Run run(w, a.kv_heads);
         const bool mine = static_cast<int>(blockIdx.x) < run.ctas;
         int64_t u = mine ? run.start(blockIdx.x) : 0;
         const int64_t u1 = mine ? run.start(blockIdx.x + 1) : 0;
@@ -698,6 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       plan_all();
+      const JoinTile join = join_at(w, run, blockIdx.x);
+      if (lane == 0) w.joins[blockIdx.x] = join;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -1029,32 +1053,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of the tile that cut c + 1 goes through, if that is the
-// first cut in it: kJoinRows rows to a CTA. First every row's weights, 2^(m_i -
-// M) / sum, eight threads to a row; then the sums, a thread to four features.
-// Bound by the latency of its chain of loads (schedule, then maxima and sums, then
-// partial results), so a CTA has many rows in flight at once; the schedule is
-// read while the tile kernel still runs.
+// Joins the pieces of the tiles that cuts go through: kJoinRows rows to a CTA. First
+// every row's weights, 2^(m_i - M) / sum, eight threads to a row; then the sums, a
+// thread to four features. Bound by the latency of its chain of loads (what is to be
+// joined, then maxima and sums, then partial results), so a CTA has many rows in
+// flight at once.
 constexpr int kJoinRows = 32;
 constexpr int kMaxCtas = 160;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kernel(AttnArgs a, Work w) {
   __shared__ float s_w[kJoinRows][kMaxCtas + 1];
-  const Run run(w, a.kv_heads);
+  pdl_wait();  // (in every thread, before anything is read or left: later kernels on the stream count on this one's end alone)
   const int c0 = blockIdx.x;
-  Segment g = {};
-  int pieces = 0;
-  if (c0 + 1 < run.ctas) {
-    segment_at(w, run, run.start(c0 + 1), run.all, &g);
-    if (g.j0 > 0 && run.start(c0) <= g.at)
-      for (pieces = 1; c0 + pieces < run.ctas && run.start(c0 + pieces) < g.at + g.n;) ++pieces;
-  }
+  const JoinTile g = w.joins[c0];
+  const int pieces = g.pieces;
   const int row0 = blockIdx.y * kJoinRows;
   const int rows = min(g.t.rows - row0, kJoinRows);
   // piece 0 is the last of its CTA's segments, the others are the first of theirs
   const auto index = [&](int i, int r) { return (2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0)) * kPair + row0 + r; };
-  pdl_wait();  // (in every thread, whatever it found: later kernels on the stream count on this one's end alone)
   if (c0 == static_cast<int>(gridDim.x) - 1) clear_unowned<T>(a, blockIdx.y, gridDim.y);  // (no cut lies behind the last CTA's run)
   if (pieces == 0 || rows <= 0) return;
   {
@@ -1158,6 +1175,7 @@ cudaError_t launch_d(const AttnArgs& a, const Work& w, const CUtensorMap& k, con
 
 size_t prefix_bytes(int64_t slots) { return align_up(static_cast<size_t>(slots + 1) * 4, 256); }
 size_t tiles_bytes(int64_t slots) { return align_up(static_cast<size_t>(slots) * sizeof(AttnTile), 256); }
+size_t joins_bytes(int num_sms) { return align_up(static_cast<size_t>(num_sms) * sizeof(JoinTile), 256); }
 
 int64_t slots_of(int64_t tokens, int group, int seqs) { return tokens * group / kPair + seqs; }
 
@@ -1181,7 +1199,7 @@ bool attn_tile_supported(int dtype, int dim, int page, float scale, bool aligned
 size_t attn_tile_workspace(int64_t tokens, int group, int seqs, int dim, int num_sms) {
   const size_t rows = 2 * static_cast<size_t>(num_sms) * kPair;
   const int64_t slots = slots_of(tokens, group, seqs);
-  return prefix_bytes(slots) + tiles_bytes(slots) + align_up(rows * 8, 256) + rows * dim * 4;
+  return prefix_bytes(slots) + tiles_bytes(slots) + joins_bytes(num_sms) + align_up(rows * 8, 256) + rows * dim * 4;
 }
 
 cudaError_t launch_attn_tile(const AttnArgs& args, int dtype, void* workspace, int num_sms, cudaStream_t s) {
@@ -1195,6 +1213,8 @@ cudaError_t launch_attn_tile(const AttnArgs& args, int dtype, void* workspace, i
   p += prefix_bytes(w.slots);
   w.tiles = reinterpret_cast<const AttnTile*>(p);
   p += tiles_bytes(w.slots);
+  w.joins = reinterpret_cast<JoinTile*>(p);
+  p += joins_bytes(num_sms);
   w.part_ml = reinterpret_cast<float2*>(p);
   p += align_up(2 * static_cast<size_t>(num_sms) * kPair * 8, 256);
   w.part_o = reinterpret_cast<float*>(p);
