@@ -73,48 +73,27 @@ __device__ __forceinline__ Parts cut(float x, float y) {
                upper_pair(__float_as_uint(x2), __float_as_uint(y2))};
 }
 
-// Infinite and NaN values at keys that only some of a tile's rows see, which go
-// into the products as zeros (a weight of zero must meet a finite value) and are
-// added at the end to the rows that see them, where any weight above zero gives
-// the same. Past kMost of them (a token whose whole value is NaN has as many as
-// features) the rows that see any of these keys become NaN.
+// Infinite and NaN values at keys that only some of a tile's rows see go into the
+// products as zeros (a weight of zero must meet a finite value), and a bit stands
+// for each key that has any; the rows that see such a key read its value again at
+// the end and add what is not finite there, where any weight above zero gives the
+// same.
 struct OddValues {
-  static constexpr int kMost = 32;
   static constexpr int kSide = 96;  // keys where the rows' views begin, or end: 64 rows' and a block's rest
   static constexpr int kWords = 2 * kSide / 32;
-  int count, lower, all_from, all_to;  // (keys are relative to the split's first)
-  int key[kMost], feature[kMost];
-  float value[kMost];
+  int any, lower, all_from, all_to;  // (keys are relative to the split's first)
   uint32_t keys[kWords];  // keys with such values: from `lower` on, and from all_to on
 };
-__device__ __forceinline__ int odd_place(const OddValues& s, int key) {
-  return key < s.all_from ? min(key - s.lower, OddValues::kSide - 1) : OddValues::kSide + min(key - s.all_to, OddValues::kSide - 1);
+__device__ __noinline__ float4 odd_taken(OddValues& s, float4 x, int key) {
+  const int at = key < s.all_from ? min(key - s.lower, OddValues::kSide - 1)
+                                  : OddValues::kSide + min(key - s.all_to, OddValues::kSide - 1);
+  atomicOr(&s.keys[at >> 5], 1u << (at & 31));
+  s.any = 1;
+  return make_float4(isfinite(x.x) ? x.x : 0.0f, isfinite(x.y) ? x.y : 0.0f, isfinite(x.z) ? x.z : 0.0f,
+                     isfinite(x.w) ? x.w : 0.0f);
 }
-__device__ __noinline__ float4 odd_taken(OddValues& s, float4 x, int key, int feature) {
-  float v[4] = {x.x, x.y, x.z, x.w};
-  for (int e = 0; e < 4; ++e) {
-    if (isfinite(v[e])) continue;
-    const int n = atomicAdd(&s.count, 1), at = odd_place(s, key);
-    atomicOr(&s.keys[at >> 5], 1u << (at & 31));
-    if (n < OddValues::kMost) {
-      s.key[n] = key;
-      s.feature[n] = feature + e;
-      s.value[n] = v[e];
-    }
-    v[e] = 0.0f;
-  }
-  return make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void set_odd_aside(OddValues& s, float4& x, int key, int feature) {
-  if (key < s.all_from || key >= s.all_to) x = odd_taken(s, x, key, feature);
-}
-__device__ __noinline__ bool sees_odd(const OddValues& s, int from, int to) {
-  for (int i = 0; i < OddValues::kSide; ++i) {
-    if ((s.keys[i >> 5] >> (i & 31) & 1) && s.lower + i >= from && s.lower + i < to) return true;
-    const int at = OddValues::kSide + i;
-    if ((s.keys[at >> 5] >> (at & 31) & 1) && s.all_to + i >= from && s.all_to + i < to) return true;
-  }
-  return false;
+__device__ __forceinline__ void set_odd_aside(OddValues& s, float4& x, int key) {
+  if (key < s.all_from || key >= s.all_to) x = odd_taken(s, x, key);
 }
 
 template <int D>
@@ -164,7 +143,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
         float4 x = held[kind][i];
         unsigned char* dst = to + kind * 4 * C::kPart + at;
         if (kind == 1 && !(isfinite(x.x) && isfinite(x.y) && isfinite(x.z) && isfinite(x.w)))
-          set_odd_aside(aside, x, b * kTileKeys + i * C::kAtOnce + row_of, piece * 4);
+          set_odd_aside(aside, x, b * kTileKeys + i * C::kAtOnce + row_of);
         const auto put = [&](int part, uint32_t lo, uint32_t hi) {
           *reinterpret_cast<uint2*>(dst + part * C::kPart) = make_uint2(lo, hi);
         };
@@ -186,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
     const auto rel = [&](int64_t j) { return static_cast<int>(max(min(j - k0, k1 - k0), int64_t{0})); };
     if (threadIdx.x < OddValues::kWords) aside.keys[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
-      aside.count = 0;
+      aside.any = 0;
       aside.lower = rel(t.lo);
       aside.all_from = a.window > 0 ? rel(last - a.window + 1) : 0;
       aside.all_to = rel(first + 1);
@@ -342,24 +321,26 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
     __syncthreads();
   }
   if (row0 >= t.rows) return;
-  if (aside.count > 0) {
+  if (aside.any != 0) {
+    for (int side = 0; side < 2; ++side)
+      for (int w = 0; w < OddValues::kWords / 2; ++w)
+        for (uint32_t bits = aside.keys[side * (OddValues::kWords / 2) + w]; bits != 0; bits &= bits - 1) {
+          const int key = (side == 0 ? aside.lower : aside.all_to) + 32 * w + __ffs(bits) - 1;
+          const uint32_t j = static_cast<uint32_t>(k0 + key), e = j / static_cast<uint32_t>(a.b.page_size);
+          const int page = page_of(a.b, t.s, e);
+          if (page < 0) continue;
+          const float* v = vp + page * a.c_ps + (j - e * a.b.page_size) * a.c_ts + q4 * 2;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool all = aside.count > OddValues::kMost && sees_odd(aside, from[i], to[i]);
-      for (int n = 0; n < min(aside.count, OddValues::kMost); ++n) {
-        const int key = aside.key[n], d0 = aside.feature[n];
-        if (key < from[i] || key >= to[i] || (d0 & 7) >> 1 != q4) continue;
-        const float v = aside.value[n];
+          for (int i = 0; i < 2; ++i) {
+            if (key < from[i] || key >= to[i]) continue;
 #pragma unroll
-        for (int d = 0; d < D / 8; ++d) {
-          if (d0 == d * 8 + q4 * 2) o[d][2 * i] += v;
-          if (d0 == d * 8 + q4 * 2 + 1) o[d][2 * i + 1] += v;
+            for (int d = 0; d < D / 8; ++d) {
+              const float2 x = *reinterpret_cast<const float2*>(v + d * 8);
+              if (!isfinite(x.x)) o[d][2 * i] += x.x;
+              if (!isfinite(x.y)) o[d][2 * i + 1] += x.y;
+            }
+          }
         }
-      }
-#pragma unroll
-      for (int d = 0; d < D / 8; ++d)
-        if (all) o[d][2 * i] = o[d][2 * i + 1] = __int_as_float(0x7fffffff);
-    }
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {

@@ -350,30 +350,15 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
 
 // Infinite or NaN values at keys that only some of a tile's rows see. The copy of the
 // values that the product reads has zeros in their place (a weight of zero must
-// meet a finite value); the rows that see them add them at the end, where any
-// weight above zero gives the same infinity or NaN. Past kOdd of them (a token
-// whose whole value is NaN has as many as features) the rows that see any of
-// these keys become NaN.
-constexpr int kOdd = 8;
+// meet a finite value), and a bit stands for each key that has any; the rows that
+// see such a key read its value again at the end and add what is not finite there,
+// where any weight above zero gives the same infinity or NaN.
 constexpr int kOddBlocks = 8;  // of a tile: its rows' views begin within three blocks, and end within three
 struct OddValues {
-  int count, blocks;
-  int key[kOdd];       // from the tile's first block on
-  uint32_t at[kOdd];   // feature in the upper half, the value's 16 bits in the lower
+  int any, blocks;
   int block[kOddBlocks];               // blocks that not all rows see
   uint32_t keys[kOddBlocks][4];        // and their keys with such values
 };
-// Whether a row that sees the keys [from, to) sees one with an odd value.
-__device__ __forceinline__ bool sees_odd(const OddValues& list, int from, int to) {
-  bool any = false;
-  for (int b = 0; b < list.blocks; ++b)
-    for (int w = 0; w < 4; ++w) {
-      const int k0 = list.block[b] * kKeys + 32 * w, lo = max(from - k0, 0), hi = min(to - k0, 32);
-      if (lo >= hi) continue;
-      any |= (list.keys[b][w] & (0xffffffffu >> (32 - (hi - lo)) << lo)) != 0;
-    }
-  return any;
-}
 
 struct Bars {
   uint64_t q_full[2];   // a tile's queries lie in shared memory
@@ -617,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Segment& g = segs[seg % kSegs];
           if (g.j1 <= g.j0) return true;
           OddValues& list = odd[seg % kSegs];
-          if (lane == 0) list.count = list.blocks = 0;
+          if (lane == 0) list.any = list.blocks = 0;
           int blocks = 0;
           __syncwarp();
           for (int j = g.j0; j < g.j1; ++j) {
@@ -638,10 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int sure_lo = in_block(g.all_from - j * kKeys), sure_hi = max(in_block(g.all_to - j * kKeys), sure_lo);
             constexpr int kPer = 8 * C::kHalves;  // 16-byte chunks of a row
             const int rows = sure_lo + kKeys - sure_hi;
-            const auto place = [&](int e, int* r, int* feature) {
+            const auto place = [&](int e, int* r) {
               const int i = e / kPer, c = e & 7, h = (e >> 3) % C::kHalves;
               *r = i < sure_lo ? i : sure_hi + (i - sure_lo);
-              *feature = h * 64 + c * 8;
               return reinterpret_cast<uint4*>(ring + v_slot * C::kSlot + h * C::kHalf + *r * 128 + ((c ^ (*r & 7)) << 4));
             };
             // a half whose exponent is all ones carries into its sign's place
@@ -650,8 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t carry = 0;
 #pragma unroll 8
             for (int e = lane; e < rows * kPer; e += 32) {
-              int r, feature;
-              uint4* const at = place(e, &r, &feature);
+              int r;
+              uint4* const at = place(e, &r);
               if (r < lo || r >= hi) {
                 *at = make_uint4(0, 0, 0, 0);
               } else {
@@ -661,20 +645,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (__any_sync(0xffffffffu, carry & 0x80008000u)) {
               for (int e = lane; e < rows * kPer; e += 32) {
-                int r, feature;
-                uint4* const at = place(e, &r, &feature);
+                int r;
+                uint4* const at = place(e, &r);
                 const uint4 v = *at;
                 uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                   const uint32_t half = w[i / 2] >> (16 * (i & 1)) & 0xffffu;
                   if (!not_finite2<T>(half)) continue;
-                  const int n = atomicAdd(&list.count, 1);
+                  list.any = 1;
                   atomicOr(&odd_keys[r >> 5], 1u << (r & 31));
-                  if (n < kOdd) {
-                    list.key[n] = j * kKeys + r;
-                    list.at[n] = static_cast<uint32_t>(feature + i) << 16 | half;
-                  }
                   w[i / 2] &= (i & 1) ? 0xffffu : 0xffff0000u;
                 }
                 *at = make_uint4(w[0], w[1], w[2], w[3]);
@@ -969,20 +949,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // what is to be added to features c .. c + 31 of this row's sums
         HC_WAIT(&bars.odd_full[seg % kSegs], (seg / kSegs) & 1);
         const OddValues& list = odd[seg % kSegs];
-        const int odds = list.count;
+        const bool odds = list.any != 0;
         const auto add_odd = [&](int c, uint32_t* o) {
-          for (int e = 0; e < min(odds, kOdd); ++e) {
-            const int key = list.key[e], d = static_cast<int>(list.at[e] >> 16) - c;
-            if (d < 0 || d >= 32 || key < from || key >= to) continue;
-            const uint16_t bits = static_cast<uint16_t>(list.at[e]);
-            const float v = Ty<T>::to_f(*reinterpret_cast<const T*>(&bits));
+          for (int b = 0; b < list.blocks; ++b)
+            for (int w = 0; w < 4; ++w) {
+              const int k0 = list.block[b] * kKeys + 32 * w, lo = max(from - k0, 0), hi = min(to - k0, 32);
+              uint32_t keys = lo < hi ? list.keys[b][w] & (0xffffffffu >> (32 - (hi - lo)) << lo) : 0u;
+              for (; keys != 0; keys &= keys - 1) {
+                const uint32_t key = static_cast<uint32_t>(g.t.base + k0 + __ffs(keys) - 1), e = key / static_cast<uint32_t>(a.b.page_size);
+                const int page = page_of(a.b, g.t.s, e);
+                if (page < 0) continue;
+                const T* v = static_cast<const T*>(a.v) + page * a.c_ps + (key - e * a.b.page_size) * a.c_ts + g.kv_head * a.c_hs + c;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i == d) o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
-          }
-          if (odds > kOdd && sees_odd(list, from, to))
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0x7fffffffu;
+                for (int i = 0; i < 32; ++i) {
+                  const float x = ldf(v + i);
+                  if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                }
+              }
+            }
         };
         if (rows > 0) {
           const bool partial = g.j0 > 0 || g.j1 < g.n;
@@ -997,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(o_at + c, o);
                 tmem_wait_ld();
                 landed32(o);
-                if (odds > 0) add_odd(c, o);
+                if (odds) add_odd(c, o);
                 write_out(o, reinterpret_cast<unsigned char*>(w.part_o), real ? (at * D + c) * 4 : -1, true);
               }
             }
@@ -1017,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(o_at + c + 32 * h, o);
                 tmem_wait_ld();
                 landed32(o);
-                if (odds > 0) add_odd(c + 32 * h, o);
+                if (odds) add_odd(c + 32 * h, o);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                   y[16 * h + i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);

@@ -329,3 +329,24 @@ def test_a_workspace_of_the_size_asked_for_suffices(hc, dtype, scale, both):
         work = torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda")
         got = hc.paged_attention(*t, scale=scale, workspace=work, **kw)
         assert torch.equal(got, hc.paged_attention(*t, scale=scale, **kw))
+
+
+# ------------------------------------------------------------------------------ values that are not finite --
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim,page,flags", [(64, 16, 0), (128, 32, 0), (128, 16, 2)])
+@pytest.mark.parametrize("window", [0, 40, 200])
+def test_many_unseen_values_may_be_anything(hc, dtype, dim, page, flags, window):
+    """As many infinities and NaN as a chunk has tokens, one feature each: they reach those features of the tokens that see them,
+    and nothing else. With a window, the first tokens still see some that the others have left."""
+    for both in ([(150, 333)], [(1, 9), (290, 300), (5, 60)]):
+        b = Batch(79, both, 4, 2, dim, page, dtype)
+        s = max(range(len(both)), key=lambda i: both[i][0])
+        n = both[s][1]
+        for i, j in enumerate(range(n - both[s][0] - 60 if n > 320 else 5, n, 3)):
+            place = (int(b.table[s, j // page]), j % page)
+            b.v[place][i % 2, (11 * i + 3) % dim] = [math.inf, math.nan, -math.inf, math.inf][i % 4]
+        out, lse, tol, ltol = R.attention(b.q, b.k, b.v, b.table, b.lens, b.cu, window=window, scale=0.05)
+        got, glse = b.run(hc, window=window, flags=flags, scale=0.05)
+        within(got, out, tol, "out")
+        within(glse, lse, ltol, "lse")
