@@ -83,7 +83,7 @@ struct JoinTile {
 
 struct Work {
   const AttnTile* tiles;  // tile of each slot
-  const int32_t* prefix;  // units of the tiles before each slot, per key head; [slots] = all
+  const int64_t* prefix;  // units of the tiles before each slot, per key head; [slots] = all (4 million tokens of 16 grouped heads have 2^32)
   int slots, ctas;
   JoinTile* joins;        // of each CTA, the tile that its run ends in, if that is the first cut in it
   float2* part_ml;        // [2 * ctas][kPair]
@@ -98,8 +98,8 @@ __device__ __forceinline__ int64_t blocks_of(const AttnTile& t) {
 }
 
 // The tile of every slot, and the units of all before it.
-__global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, int32_t* prefix, AttnTile* tiles, int slots) {
-  __shared__ int red[33];
+__global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, int64_t* prefix, AttnTile* tiles, int slots) {
+  __shared__ int64_t red[33];
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < slots; i += 1024) prefix[i] = 0;
@@ -116,24 +116,24 @@ __global__ void __launch_bounds__(1024) plan_kernel(AttnArgs a, int32_t* prefix,
   }
   __syncthreads();
   // exclusive prefix in place, 1024 slots at a time
-  int before = 0;
+  int64_t before = 0;
   for (int i0 = 0; i0 <= slots; i0 += 1024) {
     const int i = i0 + threadIdx.x;
-    const int v = i < slots ? prefix[i] : 0;
-    int x = v;
+    const int64_t v = i < slots ? prefix[i] : 0;
+    int64_t x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) red[warp] = x;
     __syncthreads();
     if (warp == 0) {
-      const int w = red[lane];
-      int z = w;
+      const int64_t w = red[lane];
+      int64_t z = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, z, o);
+        const int64_t y = __shfl_up_sync(0xffffffffu, z, o);
         if (lane >= o) z += y;
       }
       red[lane] = z - w;
@@ -176,11 +176,11 @@ __device__ __forceinline__ void segment_at(const Work& w, const Run& run, int64_
                                            Segment* g) {
   const int h = static_cast<int>(u / run.per_head);
   const int64_t v = u - h * run.per_head;
-  const int slot = warp_last_le(w.slots, v, [&](int i) { return static_cast<int64_t>(w.prefix[i]); });
+  const int slot = warp_last_le(w.slots, v, [&](int i) { return w.prefix[i]; });
   g->t = w.tiles[slot];
   g->kv_head = h;
   g->at = h * run.per_head + w.prefix[slot] + kTileCost;
-  g->n = w.prefix[slot + 1] - w.prefix[slot] - kTileCost;
+  g->n = static_cast<int>(w.prefix[slot + 1] - w.prefix[slot]) - kTileCost;
   const int64_t from = u - g->at, to = u1 - g->at;
   g->j0 = from < 0 ? 0 : static_cast<int>(from);
   g->j1 = to < 0 ? 0 : to < g->n ? static_cast<int>(to) : g->n;
@@ -1142,7 +1142,7 @@ cudaError_t launch_t(const AttnArgs& a, const Work& w, const CUtensorMap& k, con
   constexpr size_t smem = Cfg<D>::kSmem;
   cudaError_t e = ensure_smem<tile_kernel<T, D, CAP>>(smem);
   if (e != cudaSuccess) return e;
-  plan_kernel<<<1, 1024, 0, s>>>(a, const_cast<int32_t*>(w.prefix), const_cast<AttnTile*>(w.tiles), w.slots);
+  plan_kernel<<<1, 1024, 0, s>>>(a, const_cast<int64_t*>(w.prefix), const_cast<AttnTile*>(w.tiles), w.slots);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = launch_pdl(tile_kernel<T, D, CAP>, dim3(w.ctas), dim3(kThreads), smem, s, 1, a, w, k, v);
@@ -1157,7 +1157,7 @@ cudaError_t launch_d(const AttnArgs& a, const Work& w, const CUtensorMap& k, con
   return a.softcap > 0.0f ? launch_t<T, 128, true>(a, w, k, v, s) : launch_t<T, 128, false>(a, w, k, v, s);
 }
 
-size_t prefix_bytes(int64_t slots) { return align_up(static_cast<size_t>(slots + 1) * 4, 256); }
+size_t prefix_bytes(int64_t slots) { return align_up(static_cast<size_t>(slots + 1) * 8, 256); }
 size_t tiles_bytes(int64_t slots) { return align_up(static_cast<size_t>(slots) * sizeof(AttnTile), 256); }
 size_t joins_bytes(int num_sms) { return align_up(static_cast<size_t>(num_sms) * sizeof(JoinTile), 256); }
 
@@ -1193,7 +1193,7 @@ cudaError_t launch_attn_tile(const AttnArgs& args, int dtype, void* workspace, i
   w.slots = static_cast<int>(slots_of(a.tokens, a.group, a.b.seqs));
   w.ctas = std::min(num_sms, kMaxCtas);
   char* p = static_cast<char*>(workspace);
-  w.prefix = reinterpret_cast<const int32_t*>(p);
+  w.prefix = reinterpret_cast<const int64_t*>(p);
   p += prefix_bytes(w.slots);
   w.tiles = reinterpret_cast<const AttnTile*>(p);
   p += tiles_bytes(w.slots);
