@@ -262,6 +262,11 @@ __global__ void __launch_bounds__(kMeta) fork_kernel(PagesArgs a, const int32_t*
   if (threadIdx.x == 0) *missing = want - got;
 }
 
+// Length of a sequence of `old` tokens with `more` new ones, within what a length can be.
+__device__ __forceinline__ int64_t grown(int old, int more) {
+  return min(static_cast<int64_t>(old) + max(0, more), static_cast<int64_t>(INT32_MAX));
+}
+
 // Extend. Workspace: need (seqs), free (num_pages).
 __global__ void __launch_bounds__(kMeta) extend_kernel(PagesArgs a, const int32_t* __restrict__ new_tokens,
                                                        int32_t* missing, int32_t* need, int32_t* free_list) {
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kMeta) extend_kernel(PagesArgs a, const int32_
     int more = 0;
     if (s < a.seqs) {
       const int old = max(0, a.lens[s]);
-      const int64_t len = static_cast<int64_t>(old) + max(0, new_tokens[s]);
+      const int64_t len = grown(old, new_tokens[s]);
       const int64_t to = len == 0 ? 0 : (len - 1) / a.page + 1;
       const int room = a.width - used_of(a, s);
       const int64_t grow = to - pages_for(old, a.page);
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(kMeta) extend_kernel(PagesArgs a, const int32_
   for (int s = threadIdx.x >> 5; s < a.seqs; s += kMeta / 32) {
     const int first = need[s], u = used_of(a, s);
     const int old = max(0, a.lens[s]);
-    const int64_t len = static_cast<int64_t>(old) + max(0, new_tokens[s]);
+    const int64_t len = grown(old, new_tokens[s]);
     const int64_t to = len == 0 ? 0 : (len - 1) / a.page + 1;
     const int more = static_cast<int>(min(to - pages_for(old, a.page), static_cast<int64_t>(max(0, a.width - u))));
     const int have = max(0, min(more, s_got - first));

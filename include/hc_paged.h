@@ -182,7 +182,8 @@ hc_status_t hc_page_fork(const hc_pages_t* pages, const int32_t* parents, int32_
 
 /* Pages for new_tokens[s] >= 0 more tokens of every sequence. Where pages or
  * the table's width run out, a sequence's new length ends with its pages;
- * missing[0] counts the pages that could not be had. */
+ * missing[0] counts the pages that could not be had. A length ends at 2^31 - 1
+ * tokens. */
 hc_status_t hc_page_extend(const hc_pages_t* pages, const int32_t* new_tokens, int32_t* missing, void* workspace,
                            size_t workspace_bytes, struct CUstream_st* stream);
 

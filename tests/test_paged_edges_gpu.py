@@ -350,3 +350,23 @@ def test_many_unseen_values_may_be_anything(hc, dtype, dim, page, flags, window)
         got, glse = b.run(hc, window=window, flags=flags, scale=0.05)
         within(got, out, tol, "out")
         within(glse, lse, ltol, "lse")
+
+
+# ---------------------------------------------------------------------------------------------- pages --
+
+@pytest.mark.parametrize("page,old", [(2 ** 30, 2 ** 31 - 5), (2 ** 30, 2 ** 30), (2 ** 29 + 1, 2 ** 31 - 1), (2 ** 31 - 1, 7)])
+def test_extend_ends_at_the_longest_length(hc, page, old):
+    used = -(-old // page)
+    table = torch.full((2, 6), -1, dtype=torch.int32)
+    table[0, :used] = torch.arange(used)
+    refs = torch.zeros(9, dtype=torch.int32)
+    refs[:used] = 1
+    most = 2 ** 31 - 1
+    for more in (0, 100, most):
+        n = min(old + more, most)
+        want = -(-n // page)
+        t, lens, k, missing = hc.page_extend(table.cuda(), torch.tensor([old, 0], dtype=torch.int32).cuda(), refs.cuda(),
+                                             torch.tensor([more, 1], dtype=torch.int32).cuda(), page_size=page)
+        assert lens.tolist() == [n, 1] and missing.tolist() == [0]
+        assert t.tolist() == [list(range(want)) + [-1] * (6 - want), [want] + [-1] * 5]
+        assert k.tolist() == [1] * (want + 1) + [0] * (9 - want - 1)
