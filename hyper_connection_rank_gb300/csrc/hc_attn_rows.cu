@@ -694,13 +694,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) f32_rows_kernel(AttnArgs a) {
     }
     const float weight = exp2f(x - (m == neg_inf() ? 0.0f : m));
     l += weight;
-    // (keys that only some rows see, in a tile of more than one token: a weight of zero adds nothing, whatever the value)
+    // (all rows are one token's: what it does not see has come as zeros)
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int j = 0; j < kKeys; ++j) {
         const float w = __shfl_sync(0xffffffffu, weight, r * kKeys + j);
-        if (w == 0.0f) continue;
 #pragma unroll
         for (int e = 0; e < V; ++e) o[r][e] = fmaf(w, values[j].e[e], o[r][e]);
       }
