@@ -40,6 +40,13 @@
 // sums of values in registers; they are rescaled only when a block raises the
 // maximum. The warps' results are joined once at the end:
 //   M = max_w m_w,  out = sum_w 2^(m_w - M) o_w / sum_w 2^(m_w - M) l_w.
+// The product with the values takes its weights in T, the operands' type. Up to eight
+// rows to a key head leave half of the MMA's sixteen free, and there goes what the
+// rounding leaves of each weight: for nothing, a weight keeps twice the bits, and
+// what is off in a result is its own rounding (64 contexts in bf16: 1.66e-3 against
+// 64 bits, where rounded weights gave 1.95e-3; an MMA of its own for the rest would
+// take 3 to 4% more time, so from nine rows on weights are rounded). The sum of
+// weights is taken before.
 #include <type_traits>
 
 #include "hc_async.cuh"
@@ -68,6 +75,19 @@ template <>
 __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// What a pair of numbers rounded to T leaves of the two, in T again.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2_rest(float x, float y, uint32_t packed);
+template <>
+__device__ __forceinline__ uint32_t pack2_rest<__half>(float x, float y, uint32_t packed) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&packed));
+  return pack2<__half>(x - f.x, y - f.y);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2_rest<__nv_bfloat16>(float x, float y, uint32_t packed) {
+  return pack2<__nv_bfloat16>(x - __uint_as_float(packed << 16), y - __uint_as_float(packed & 0xffff0000u));
 }
 
 // 16-byte chunk `c` of row `r` of a block of D-element rows: chunks are permuted
@@ -382,6 +402,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rows_kernel(AttnArgs a) {
   if (a.window > 0) all_from = rel(row_position(t, t.row0 + t.rows - 1, a.group) - a.window + 1);
   const bool uneven = row_position(t, t.row0, a.group) != row_position(t, t.row0 + t.rows - 1, a.group);
 
+  // Up to eight rows leave the upper half of the product's tile free for what rounding to T leaves of their weights.
+  const bool spare = t.rows <= 8;
   const ScoreMap map = score_map(a.scale, a.softcap);
   float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.0f, 0.0f};
   float o[D / 8][4];
@@ -458,6 +480,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rows_kernel(AttnArgs a) {
         m[i] = now;
         l[i] *= f[i];
       }
+      if (spare) f[1] = f[0];
 #pragma unroll
       for (int d = 0; d < D / 8; ++d) {
         o[d][0] *= f[0];
@@ -478,7 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rows_kernel(AttnArgs a) {
         l[e >> 1] += s[n][e];
       }
       p[2 * n] = pack2<T>(s[n][0], s[n][1]);
-      p[2 * n + 1] = pack2<T>(s[n][2], s[n][3]);
+      p[2 * n + 1] = spare ? pack2_rest<T>(s[n][0], s[n][1], p[2 * n]) : pack2<T>(s[n][2], s[n][3]);
     }
     const auto load_values = [&](int d, uint32_t(&v)[4]) {
       ldsm_x4_trans(vs_at + chunk_at<D>(lane & 15, 2 * d + (lane >> 4)), v[0], v[1], v[2], v[3]);
@@ -525,7 +548,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rows_kernel(AttnArgs a) {
             if (mine && r < 8) {
               sums[0] = y[0];
               sums[1] = y[1];
-            } else if (mine) {
+            }
+            if (mine && (r >= 8 || spare)) {
               sums[2] = y[2];
               sums[3] = y[3];
             }
@@ -538,6 +562,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rows_kernel(AttnArgs a) {
   }
   cp_async_wait_group<0>();
 
+  if (spare) {
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d) {
+      // (an infinite value is in the first sum as it should be; its product with a rest, of either sign or zero, is nothing)
+      if (isfinite(o[d][2])) o[d][0] += o[d][2];
+      if (isfinite(o[d][3])) o[d][1] += o[d][3];
+    }
+  }
   // join the four lanes of a row, then the warps
 #pragma unroll
   for (int i = 0; i < 2; ++i) {

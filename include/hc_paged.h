@@ -110,11 +110,11 @@ hc_status_t hc_rotary_append(const hc_rotary_append_t* args, struct CUstream_st*
  *   out = sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j)
  *
  * A token that sees nothing gets out = 0 and lse = -inf. Scores, softmax and
- * sums are fp32; in the fp16/bf16 kernels the weights are rounded to T for the
- * product with the values (the sum of weights is not), out is rounded to T
- * once, lse is fp32. What a token does not see does not touch its result,
- * whatever it holds; an infinity or a NaN among what it sees does, in its own
- * feature.
+ * sums are fp32; in the fp16/bf16 kernels the weights of more than eight rows
+ * to a key head are rounded to T for the product with the values (the sum of
+ * weights is not), out is rounded to T once, lse is fp32. What a token does
+ * not see does not touch its result, whatever it holds; an infinity or a NaN
+ * among what it sees does, in its own feature.
  *
  * max_q, max_kv: the longest row of new tokens and the longest kv_lens, if the
  * caller knows them (0: unknown). They steer the choice of kernels and how far

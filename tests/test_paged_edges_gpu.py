@@ -370,3 +370,24 @@ def test_extend_ends_at_the_longest_length(hc, page, old):
         assert lens.tolist() == [n, 1] and missing.tolist() == [0]
         assert t.tolist() == [list(range(want)) + [-1] * (6 - want), [want] + [-1] * 5]
         assert k.tolist() == [1] * (want + 1) + [0] * (9 - want - 1)
+
+
+# -------------------------------------------------------------------------------------------- weights --
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=ids)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("both,heads,kv_heads", [([(1, 40)], 4, 1), ([(1, 700), (1, 33)], 20, 4), ([(1, 4001)], 8, 1),
+                                                 ([(1, 100 + i) for i in range(60)], 8, 8), ([(5, 60), (3, 9)], 2, 2),
+                                                 ([(2, 500), (1, 20)], 8, 2)], ids=lambda v: str(len(v)) if isinstance(v, list) else None)
+def test_weights_of_up_to_eight_rows_keep_their_precision(hc, dtype, dim, both, heads, kv_heads):
+    """Values of 1 and -1, whose weighted mean nearly vanishes, so that what rounding takes off a weight shows: with up to eight
+    rows to a key head a weight goes into the product as two numbers of T, 2^-16 of it lost at most (in float16 what lies below
+    2^-25 of the largest too, as _paged_ref has it), where it is rounded to T else."""
+    b = Batch(89, both, heads, kv_heads, dim, 16, dtype, cu=any(q > 1 for q, _ in both))
+    b.v[b.held] = b.v[b.held].sign()
+    out, lse, tol, ltol = R.attention(b.q, b.k, b.v, b.table, b.lens, b.cu, scale=0.1)
+    if dtype != F32:
+        tol = tol - R.U[dtype] + 2.0 ** -16  # (the sum of weights times |values| is 1)
+    got, glse = b.run(hc, scale=0.1, max_q=max(q for q, _ in both))
+    within(got, out, tol, "out")
+    within(glse, lse, ltol, "lse")
