@@ -89,6 +89,16 @@ int64_t extent(int64_t tokens, int64_t ts, int heads, int64_t hs, int dim) {
   return (tokens - 1) * ts + (heads - 1) * hs + dim;
 }
 
+// Whether two tensors of rows (first element at a and b, `na` and `nb` elements from the first to the last of a row, one step
+// from row to row) share an element: b's rows must fit between a's.
+bool rows_meet(uintptr_t a, int64_t na, uintptr_t b, int64_t nb, int64_t step, int64_t rows, int64_t es) {
+  const Span x = span("", reinterpret_cast<const void*>(a), es * ((rows - 1) * step + na));
+  const Span y = span("", reinterpret_cast<const void*>(b), es * ((rows - 1) * step + nb));
+  if (!overlaps(x, y)) return false;
+  const int64_t at = static_cast<int64_t>(b - a) / es, in = step > 0 ? (at % step + step) % step : 0;
+  return rows == 1 || in < na || in + nb > step;
+}
+
 // Pointers to tensors lie at a multiple of their element's size.
 bool on_elements(int dtype, std::initializer_list<const void*> pointers) {
   for (const void* p : pointers)
@@ -213,15 +223,26 @@ hc_status_t hc_rotary_append(const hc_rotary_append_t* args, cudaStream_t stream
                          span("page_table", a.page_table, ((a.seqs - 1) * a.table_stride + a.max_pages) * 4)};
   const Span outs[3] = {qo, kc, vc};
   for (const Span& o : outs) HC_RETURN_IF(check_apart(&o, 1, small, 4));
-  // q, k and v may be parts of one matrix's rows, so an in-place q_out is not held against k and v
   if (!in_place) {
     const Span ins[3] = {q, k, v};
     HC_RETURN_IF(check_apart(&qo, 1, ins, 3));
+  } else {
+    // q, k and v may be parts of one matrix's rows
+    const auto meets = [&](const Span& other, const void* p, int64_t ts, int64_t hs) {
+      if (!overlaps(q, other)) return false;
+      return ts != a.q_token_stride || rows_meet(q.lo, extent(1, ts, a.heads, a.q_head_stride, a.head_dim),
+                                                 reinterpret_cast<uintptr_t>(p), extent(1, ts, a.kv_heads, hs, a.head_dim), ts,
+                                                 a.tokens, es);
+    };
+    if (meets(k, a.k, a.k_token_stride, a.k_head_stride)) return fail(HC_ERR_INVALID_ARG, "q_out overlaps k");
+    if (meets(v, a.v, a.v_token_stride, a.v_head_stride)) return fail(HC_ERR_INVALID_ARG, "q_out overlaps v");
   }
   const Span ins[4] = {q, k, v, qo};
   HC_RETURN_IF(check_apart(&kc, 1, ins, 4));
   HC_RETURN_IF(check_apart(&vc, 1, ins, 4));
-  if (a.k_cache == a.v_cache) return fail(HC_ERR_INVALID_ARG, "k_cache is v_cache");
+  // (the caches may be parts of one pool; heads that begin within one another's features are not)
+  if (kc.lo < vc.lo + static_cast<uintptr_t>(es * a.head_dim) && vc.lo < kc.lo + static_cast<uintptr_t>(es * a.head_dim))
+    return fail(HC_ERR_INVALID_ARG, "k_cache overlaps v_cache");
   int sms = 0;  // (only to refuse other devices)
   HC_RETURN_IF(hc::current_device_sms(&sms));
   const bool vec = aligned16(a.q) && aligned16(a.k) && aligned16(a.v) && aligned16(a.q_out) && aligned16(a.k_cache) &&

@@ -99,3 +99,28 @@ def test_page_operators_refuse_overlaps(L, what):  # noqa: F811
                 got = page_call(L, what, {**AT, out: place})
                 assert got == B.HC_ERR_INVALID_ARG, (out, other, hex(place))
                 assert b"overlaps" in L.hc_last_error(), (out, other)
+
+
+# q (2 heads of 64), k and v (one each) as the columns of one matrix's rows, q rotated in place
+ONE_MATRIX = {**APP, "q_out": APP["q"], "k": APP["q"] + 256, "v": APP["q"] + 384, "q_token_stride": 256, "k_token_stride": 256,
+              "v_token_stride": 256, "out_token_stride": 256}
+
+
+@pytest.mark.parametrize("over", [dict(k=APP["q"]), dict(v=APP["q"] + 128), dict(k=APP["q"] + 254), dict(v=APP["q"] + 2 * 512 + 128),
+                                  dict(k=APP["q"] - 126), dict(k=APP["q"] - 512 + 386), dict(v_token_stride=320),
+                                  dict(tokens=1, seqs=1, k=APP["q"] + 128), dict(k_cache=APP["v_cache"] + 64),
+                                  dict(k_cache=APP["v_cache"] - 126)], ids=str)
+def test_append_in_place_refuses_overlaps(L, over):  # noqa: F811
+    assert L.hc_rotary_append(pack("hc_rotary_append_t", **{**ONE_MATRIX, **over}), None) == B.HC_ERR_INVALID_ARG
+    assert b"overlaps" in L.hc_last_error()
+
+
+@pytest.mark.parametrize("over", [dict(), dict(k=APP["q"] - 512 + 256), dict(k=APP["q"] - 128, v=APP["q"] - 256),
+                                  dict(tokens=1, seqs=1), dict(k=0x2000000)], ids=str)
+def test_append_in_place_takes_one_matrix(L, over):  # noqa: F811
+    """What is refused of these is the check after it (so that nothing is launched where there is a GPU): the caches are one."""
+    args = {**ONE_MATRIX, **over, "k_cache": APP["v_cache"]}
+    if over.get("tokens") == 1:
+        args["cu_q"] = 0
+    assert L.hc_rotary_append(pack("hc_rotary_append_t", **args), None) == B.HC_ERR_INVALID_ARG
+    assert L.hc_last_error() == b"k_cache overlaps v_cache"
