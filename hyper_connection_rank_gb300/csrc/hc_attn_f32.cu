@@ -81,7 +81,8 @@ __device__ __forceinline__ Parts cut(float x, float y) {
 struct OddValues {
   static constexpr int kSide = 96;  // keys where the rows' views begin, or end: 64 rows' and a block's rest
   static constexpr int kWords = 2 * kSide / 32;
-  int any, lower, all_from, all_to;  // (keys are relative to the split's first)
+  int any, lower, all_from, all_to;  // (keys are relative to the split's first, k0)
+  uint32_t k0;
   uint32_t keys[kWords];  // keys with such values: from `lower` on, and from all_to on
 };
 __device__ __noinline__ float4 odd_taken(OddValues& s, float4 x, int key) {
@@ -166,6 +167,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
     if (threadIdx.x < OddValues::kWords) aside.keys[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
       aside.any = 0;
+      aside.k0 = static_cast<uint32_t>(k0);
       aside.lower = rel(t.lo);
       aside.all_from = a.window > 0 ? rel(last - a.window + 1) : 0;
       aside.all_to = rel(first + 1);
@@ -326,10 +328,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) f32_tile_kernel(AttnArgs a) {
       for (int w = 0; w < OddValues::kWords / 2; ++w)
         for (uint32_t bits = aside.keys[side * (OddValues::kWords / 2) + w]; bits != 0; bits &= bits - 1) {
           const int key = (side == 0 ? aside.lower : aside.all_to) + 32 * w + __ffs(bits) - 1;
-          const uint32_t j = static_cast<uint32_t>(k0 + key), e = j / static_cast<uint32_t>(a.b.page_size);
+          const uint32_t j = static_cast<uint32_t>(aside.k0 + key), e = j / static_cast<uint32_t>(a.b.page_size);
           const int page = page_of(a.b, t.s, e);
           if (page < 0) continue;
-          const float* v = vp + page * a.c_ps + (j - e * a.b.page_size) * a.c_ts + q4 * 2;
+          const float* v = static_cast<const float*>(a.v) + page * a.c_ps + (j - e * a.b.page_size) * a.c_ts + kvh * a.c_hs + q4 * 2;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (key < from[i] || key >= to[i]) continue;
