@@ -836,8 +836,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Whether a warp's scores are all well inside the cap chooses between two ways to the same bits: scores that a row
           // does not see have a say in it.
           bool inside = false;
-          float top = CAP || !masked ? extremes() : 0.0f;
+          float top = 0.0f;
           if (CAP) {
+            top = extremes();
 #pragma unroll
             for (int i = 0; i < 4; ++i) lows[i] = fminf(f[2 * i], f[2 * i + 1]);
 #pragma unroll
@@ -847,10 +848,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float low = fminf(fminf(lows[0], lows[1]), fminf(lows[2], lows[3]));
             inside = poly.most > 0.0f && !__any_sync(0xffffffffu, fmaxf(top, -low) > poly.most);
           }
-          if (masked) {
-            mask();
-            top = extremes();
-          }
+          if (masked) mask();
+          if (!CAP || masked) top = extremes();
           if (!CAP) {
             top *= map.mul;
           } else if (top != neg_inf()) {
