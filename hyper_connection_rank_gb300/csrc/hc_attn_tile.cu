@@ -852,6 +852,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!CAP || masked) top = extremes();
           if (!CAP) {
             top *= map.mul;
+          } else if (inside) {
+            top = fmaf(top, cap_factor(poly, make_float2(top, top)).x, 0.0f);
           } else if (top != neg_inf()) {
             top = cap_exponent<false>(poly, map, top, 0.0f);
           }
