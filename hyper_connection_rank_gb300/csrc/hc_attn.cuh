@@ -110,7 +110,7 @@ __device__ __forceinline__ void tile_of_slot(const AttnArgs& a, int64_t slot, At
   const int64_t index = a.slot_is_seq ? 0 : slot - start(s);
   tile_at(a, a.g, s, index < 0 ? 0 : index, t);
   const int64_t all = (first_row(a.b, s + 1) - t->token0) * a.group;
-  if (all < a.min_rows || all > a.max_rows) t->rows = 0;
+  if (index < 0 || all < a.min_rows || all > a.max_rows) t->rows = 0;  // (before the first bound there is no sequence)
 }
 
 // Keys of split z of a tile: [*k0, *k1).
