@@ -1,8 +1,10 @@
 // Attention of new tokens over a paged cache (include/hc_paged.h): the choice
 // of kernels, the general kernel, and the kernel that joins splits.
 //
-// General kernel (every type, head size, page size, stride and alignment, and
-// all of float32): fp32 arithmetic on the CUDA cores. A CTA holds `ROWS` rows of
+// General kernel, for what the specialised ones do not take (heads other than 64
+// and 128, operands off 16-byte boundaries, odd page sizes and scales of zero or
+// below for chunks in 16 bits, several tokens of few rows in float32): every type,
+// head size, page size, stride and alignment, fp32 arithmetic on the CUDA cores. A CTA holds `ROWS` rows of
 // queries in shared memory and passes once over the split's keys in steps of
 // kKeys: scores into shared memory, running maximum m and sum l of each row
 //   m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m')
@@ -10,8 +12,9 @@
 // registers. 16 rows to a tile where a sequence has no more than that (single
 // tokens), else 64. Bound, for many rows, by the loads of its operands from shared
 // memory (a 16-byte load takes four cycles of the SM for 16 multiply-adds of
-// each of 32 threads): float32, three chunks of up to 131 tokens of 20 heads
-// of 128 behind up to 901, 162 us, 18.6 TFLOP/s.
+// each of 32 threads): three chunks of up to 131 tokens of 20 heads behind up to
+// 901, heads of 96 in bf16 163 us, 14 TFLOP/s, of 256 371 us, 16 TFLOP/s; heads of
+// 128 in float32, if it is made to take them, 158 us, 19 TFLOP/s.
 #include <algorithm>
 #include <type_traits>
 

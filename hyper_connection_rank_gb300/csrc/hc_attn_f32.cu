@@ -4,8 +4,10 @@
 // Mathematics: a float32 x is cut into three bf16 of 8 bits each that sum to it
 // exactly, and a product into the MMAs of its parts that matter,
 //   x y = x0 y0 + x0 y1 + x1 y0 + x1 y1 + x0 y2 + x2 y0
-// and at most 2^-23 |x y| left out, with fp32 accumulation. What is left out is below
-// the dim * 2^-24 of a sum in float32. An MMA cuts its sums off rather than rounding
+// with fp32 accumulation. What is left out, x1 y2 + x2 y1 + x2 y2, is below 2^-21 |x y|
+// (the parts are cut off, so that x1 may come near 2^-7 of x and x2 near 2^-15; its sign
+// is that of x y), an eighth of the dim * 2^-24 of a float32 sum's bound at a head of 64.
+// An MMA cuts its sums off rather than rounding
 // them, so a block's values are summed by MMAs from zero and added to the running
 // sums by a rounded addition (sums run through the MMAs were 1.7e-6 off on the case
 // below, these are 5e-7, plain float32 sums 9e-7). Softmax as in hc_attn.cu, with
@@ -22,8 +24,8 @@
 // Bound: the warp-level MMAs, of which an m16n8k16 takes 8 cycles of a quarter
 // SM, so that six for a product make 170 multiply-adds a cycle and SM (the CUDA
 // cores have 128, and reached a third of that for want of operands). Three chunks
-// of up to 131 tokens, 20 heads of 128, behind up to 901: 113 us; 1000 tokens
-// behind 2000: 36 TFLOP/s, 40% of the MMAs' rate; the rest is cutting and
+// of up to 131 tokens, 20 heads of 128, behind up to 901: 112 us; 1000 tokens
+// behind 2000: 745 us, 34 TFLOP/s, 38% of the MMAs' rate; the rest is cutting and
 // waiting, with two CTAs of four warps to an SM.
 #include "hc_async.cuh"
 #include "hc_attn.cuh"

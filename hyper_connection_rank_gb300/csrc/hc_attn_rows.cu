@@ -16,7 +16,7 @@
 //
 // Measured: two contexts of 130002 and 34402 tokens, 32 heads of 128 on 8, fp16:
 // 104 us, 6.5 TB/s, 97% of the measured copy bandwidth; 61 ragged contexts of up
-// to 8192 in bf16: 231 us, 6.1 TB/s, 92%; one of 700, 20 heads on 4: 8.6 us, the latency
+// to 8192 in bf16: 232 us, 6.1 TB/s, 91%; one of 700, 20 heads on 4: 8.3 us, the latency
 // of its chain of loads.
 //
 // Work: where every sequence has one new token (no cu_q) and there are too few of
@@ -608,8 +608,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rows_kernel(AttnArgs a) {
 // that halves the scores a lane keeps at each of its five steps leaves each
 // lane with one whole score. Weights go back to all lanes by shuffles. All sums are
 // float32. Bound by its instructions, some 140 for a key and a value of 1 KB with
-// eight rows. One context of 100001 tokens, 20 heads on 4: 189 us, 2.2 TB/s
-// (342 us by the general kernel); 32 of up to 8001: 451 us against 490.
+// eight rows. One context of 100001 tokens, 20 heads on 4: 188 us, 2.2 TB/s
+// (341 us by the general kernel); 32 of up to 8001: 452 us against 488; 64 of up to 2001,
+// 32 heads on 8: 360 us.
 template <int D, int R, int SHARE>
 __global__ void __launch_bounds__(kWarps * 32, 3) f32_rows_kernel(AttnArgs a) {
   constexpr int V = D / 32, kKeys = 32 / R;  // features of a lane; keys of a block

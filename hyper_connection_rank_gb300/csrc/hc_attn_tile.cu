@@ -6,9 +6,12 @@
 //   S = Q K_j^T;  P = 2^(S c - m);  l += sum P;  O += P V_j
 // with the running maximum m of each row. O is rescaled (O, l *= 2^(m - m'))
 // only when a row's maximum has risen by more than 8 (a factor of 256) above
-// the m in use: until then weights up to 2^8 are exact in either type, so most
-// blocks touch O with nothing but the MMA. P is rounded to T for its product (the
-// tensor core's operands are 16 bits); l sums the weights before that.
+// the m in use: weights up to 2^8 are as precise in either type as weights up to
+// one, so most blocks touch O with nothing but the MMA. P is rounded to T for its
+// product (the tensor core's operands are 16 bits, and a second product with what
+// the rounding leaves would add half to the MMAs' time); l sums the weights before
+// that. So a result is off by 2.3e-3 of its size against 64 bits in bf16 (2.9e-4 in
+// fp16) where its own rounding is 1.7e-3 (2.1e-4).
 //
 // Bound: the tensor cores, 4 * head_dim flops for each pair of row and key.
 // One CTA per SM holds two tiles, A and B, of 128 rows. Both products run on
@@ -25,13 +28,15 @@
 // each, so that a row's 128 scores stay in them, and the others 72
 // (2 * 128 * 216 + 128 * 72 = 384 * 168).
 //
-// Measured: 2047 tokens behind 28001, 32 heads of 128 on 8, bf16: 567 us, 1.72
-// PFLOP/s, 89% of the measured burst rate (640 us where it runs on for long and meets
-// the power limit: 87% of the sustained rate). 17 sequences of 1 to 301 tokens,
-// window 1000, scores capped, 20 heads of 64 on 4, fp16: 66 us, of which some 15
-// are plan, start and joining; a block of keys takes a tile pair of 64 features
-// about 1.7 us then, the capped scores' multiply-adds and exponentials of two warps to a
-// scheduler.
+// Measured: 2047 tokens behind 28001, 32 heads of 128 on 8, bf16: 643 us call after
+// call, where it meets the power limit (1.51 PFLOP/s, 79% of the measured burst rate
+// and 87% of the sustained one; 640 to 680 from one GPU to the next), 567 us for a few
+// calls from rest (1.71 PFLOP/s, 89% of burst); with scores capped at 50 875 us. 17
+// sequences of 1 to 301 tokens, window 1000, scores capped at 30, 20 heads of 64 on 4,
+// fp16: 66 us, of which some 15 are plan, start and joining; a block of keys takes a
+// tile pair of 64 features about 1.7 us then, the capped scores' multiply-adds and
+// exponentials of two warps to a scheduler (47 us without the cap, 107 where scores
+// pass 3/5 of it).
 //
 // Work: all tiles' key blocks, for all key heads, laid end to end with four
 // units before each tile for its queries and results, are cut into equal runs,

@@ -23,10 +23,10 @@
 // below, one token to 256 threads 20.8 and 61.9, to 64 threads 21.3 and 63.7.
 //
 // Measured (bf16, 13638 tokens of 32 + 2 * 8 heads of 128 written into pages of
-// 64): 54.6 us, 6.14 TB/s, 92% of the measured copy bandwidth; the angles read
-// with bank conflicts cost 9 us more. float32, 4099 tokens of 20 heads: 18.8 us, 4.5
-// TB/s (6.5 us of that is what a single token takes: a launch and a chain of
-// four loads).
+// 64): 53.7 us, 6.25 TB/s, 93% of the measured copy bandwidth; the angles read
+// with bank conflicts cost 9 us more. float32, 4099 tokens of 20 heads: 18.3 us, 4.6
+// TB/s: they are two to three waves of CTAs, each of which begins with its chain of
+// four loads (position, frequencies, angles) before it moves a byte.
 #include "hc_common.cuh"
 #include "hc_paged_batch.cuh"
 #include "hc_paged_internal.h"
