@@ -31,7 +31,7 @@ EXPORTS = ("hc_attrs_default", "hc_lowrank_mix_path", "hc_lowrank_mix_workspace_
            "hc_debug_sigmoid_table", "hc_debug_sigmoid_table_f16", "hc_debug_sigmoid_table_f16_bytes", "hc_debug_wait_timeout", "hc_debug_phase_clocks", "hc_debug_sync_probe", "hc_lowrank_mix_decode_noalloc", "hc_inv_rms",
            "hc_engram_gate", "hc_rotary", "hc_rotary_append", "hc_paged_attention", "hc_paged_attention_workspace_size",
            "hc_pages_workspace_size", "hc_page_copy", "hc_page_fork", "hc_page_extend", "hc_page_release",
-           "hc_page_compact")
+           "hc_page_compact", "hc_expert_route", "hc_expert_mlp", "hc_expert_mlp_workspace_size", "hc_token_sample")
 
 
 class HcAttrs(ctypes.Structure):
@@ -89,7 +89,7 @@ def load_library(path: str = LIB_PATH):
         L.hc_inv_rms.restype = ci
         L.hc_engram_gate.argtypes = [vp] * 5 + [i64, ci, i64, f32, ci, vp, vp]
         L.hc_engram_gate.restype = ci
-        # argument structs (include/hc_paged.h) are passed packed, as bytes
+        # argument structs (include/hc_paged.h, hc_experts.h, hc_sample.h) are passed packed, as bytes
         cp = ctypes.c_char_p
         L.hc_rotary.argtypes = L.hc_rotary_append.argtypes = L.hc_paged_attention.argtypes = [cp, vp]
         L.hc_paged_attention_workspace_size.argtypes = [cp]
@@ -101,8 +101,11 @@ def load_library(path: str = LIB_PATH):
         L.hc_page_extend.argtypes = [cp, vp, vp, vp, sz, vp]
         L.hc_page_release.argtypes = [cp, vp, vp]
         L.hc_page_compact.argtypes = [cp, vp, vp, vp, i64, i64, vp, sz, vp]
+        L.hc_expert_route.argtypes = L.hc_expert_mlp.argtypes = L.hc_token_sample.argtypes = [cp, vp]
+        L.hc_expert_mlp_workspace_size.argtypes = [cp]
+        L.hc_expert_mlp_workspace_size.restype = sz
         for f in ("hc_rotary", "hc_rotary_append", "hc_paged_attention", "hc_page_copy", "hc_page_fork", "hc_page_extend",
-                  "hc_page_release", "hc_page_compact"):
+                  "hc_page_release", "hc_page_compact", "hc_expert_route", "hc_expert_mlp", "hc_token_sample"):
             getattr(L, f).restype = ci
         _lib = L
         return L

@@ -1,0 +1,260 @@
+// The experts' products (hc_expert_mlp): lists of the pairs by expert, the general
+// kernels for any shape, stride and type, and the sum over a token's experts.
+//
+//   lists_kernel    a CTA per expert: bounds and the sorted list of pairs
+//   inner_kernel    h = silu(x gate) * (x up), a row for each pair, in the list's order
+//   outer_kernel    o = h down, a row for each pair, at the pair's own place
+//   combine_kernel  out_t = sum_j weights[t, j] o[t top_k + j], in the order of j
+//
+// The general products run on the CUDA cores in fp32, in tiles of 32 pairs and 64
+// features with 16 inputs at a time in shared memory.
+#include <algorithm>
+
+#include "hc_async.cuh"
+#include "hc_common.cuh"
+#include "hc_experts.cuh"
+#include "hc_vec.cuh"
+
+namespace hc {
+namespace {
+
+// ------------------------------------------------------------------ lists --
+
+// CTA e counts the pairs of the experts before e, which is where its own begin, and its own in each warp's run of pairs;
+// then every warp writes its own. All CTAs read all experts (tokens * top_k numbers from L2), and none waits for another.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
+lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, ExpertLists lists) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int own[kWarps], less[kWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int run = (pairs + kThreads - 1) / kThreads * 32;
+  const int lo = min(pairs, warp * run), hi = min(pairs, lo + run);
+  int mine = 0, before = 0;
+#pragma unroll 8
+  for (int i = lo + lane; i < hi; i += 32) {
+    const int id = ids[i];
+    mine += id == e;
+    before += id >= 0 && id < e;
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) {
+    own[warp] = mine;
+    less[warp] = before;
+  }
+  __syncthreads();
+  int at = 0, end = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    at += less[w] + (w < warp ? own[w] : 0);
+    end += less[w] + own[w];
+  }
+  if (threadIdx.x == 0) {
+    lists.bounds[e] = at;
+    if (e == experts - 1) lists.bounds[experts] = end;
+  }
+  if (mine == 0) return;
+  for (int i0 = lo; i0 < hi; i0 += 32) {
+    const int i = i0 + lane;
+    const bool hit = i < hi && ids[i] == e;
+    const unsigned hits = __ballot_sync(0xffffffffu, hit);
+    if (hit) lists.order[at + __popc(hits & ((1u << lane) - 1u))] = i;
+    at += __popc(hits);
+  }
+}
+
+// ------------------------------------------------------- general products --
+
+constexpr int kTM = 32, kTN = 64, kTK = 16, kGenThreads = 256;
+
+// Element (row, col) of the tile that this thread holds: rows rm, rm + 16; columns cn .. cn + 3.
+struct Thread {
+  int rm, cn;
+};
+__device__ __forceinline__ Thread my_part() {
+  return Thread{static_cast<int>(threadIdx.x) >> 4, (static_cast<int>(threadIdx.x) & 15) * 4};
+}
+
+// A block of a weight, (kTK inputs, kTN outputs) from (k0, n0), zeros outside.
+template <typename T>
+__device__ __forceinline__ void load_weight(float (*b)[kTN + 4], const T* w, int64_t in_stride, int64_t out_stride, int k0, int n0,
+                                            int inputs, int outputs) {
+  for (int i = threadIdx.x; i < kTK * kTN; i += kGenThreads) {
+    const int k = out_stride == 1 ? i / kTN : i % kTK, n = out_stride == 1 ? i % kTN : i / kTK;
+    b[k][n] = k0 + k < inputs && n0 + n < outputs ? ldf(w + (k0 + k) * in_stride + (n0 + n) * out_stride) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ void multiply(float (*acc)[4], const float (*a)[kTM + 1], const float (*b)[kTN + 4], Thread me) {
+#pragma unroll
+  for (int k = 0; k < kTK; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(&b[k][me.cn]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float x = a[k][me.rm + 16 * i];
+      acc[i][0] = fmaf(x, v.x, acc[i][0]);
+      acc[i][1] = fmaf(x, v.y, acc[i][1]);
+      acc[i][2] = fmaf(x, v.z, acc[i][2]);
+      acc[i][3] = fmaf(x, v.w, acc[i][3]);
+    }
+  }
+}
+
+struct GeneralArgs {
+  hc_expert_mlp_t p;
+  ExpertLists lists;
+  float *h, *o;  // (pairs, inner) in the list's order, (pairs, hidden)
+};
+
+template <typename T> __global__ void __launch_bounds__(kGenThreads) inner_kernel(GeneralArgs g) {
+  __shared__ float a[kTK][kTM + 1];
+  __shared__ __align__(16) float b[2][kTK][kTN + 4];
+  __shared__ int64_t row[kTM];
+  const hc_expert_mlp_t& p = g.p;
+  pdl_wait();
+  pdl_trigger();
+  const ExpertTile t = expert_tile(g.lists.bounds, p.num_experts, kTM, blockIdx.x);
+  if (t.rows == 0) return;
+  if (threadIdx.x < kTM)
+    row[threadIdx.x] =
+        threadIdx.x < t.rows ? static_cast<int64_t>(g.lists.order[t.first + threadIdx.x] / p.top_k) * p.x_stride : -1;
+  __syncthreads();
+  const T* x = static_cast<const T*>(p.x);
+  const T* gate = static_cast<const T*>(p.gate) + t.expert * p.up_expert_stride;
+  const T* up = static_cast<const T*>(p.up) + t.expert * p.up_expert_stride;
+  const int n0 = blockIdx.y * kTN;
+  const Thread me = my_part();
+  float ga[2][4] = {}, ua[2][4] = {};
+  for (int k0 = 0; k0 < p.hidden; k0 += kTK) {
+    for (int i = threadIdx.x; i < kTM * kTK; i += kGenThreads) {
+      const int m = i / kTK, k = i % kTK;
+      a[k][m] = row[m] >= 0 && k0 + k < p.hidden ? ldf(x + row[m] + k0 + k) : 0.0f;
+    }
+    load_weight(b[0], gate, p.up_in_stride, p.up_out_stride, k0, n0, p.hidden, p.inner);
+    load_weight(b[1], up, p.up_in_stride, p.up_out_stride, k0, n0, p.hidden, p.inner);
+    __syncthreads();
+    multiply(ga, a, b[0], me);
+    multiply(ua, a, b[1], me);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = me.rm + 16 * i;
+    if (m >= t.rows) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n0 + me.cn + j < p.inner)
+        g.h[static_cast<int64_t>(t.first + m) * p.inner + n0 + me.cn + j] =
+            ga[i][j] / (1.0f + expf(-ga[i][j])) * ua[i][j];
+  }
+}
+
+template <typename T> __global__ void __launch_bounds__(kGenThreads) outer_kernel(GeneralArgs g) {
+  __shared__ float a[kTK][kTM + 1];
+  __shared__ __align__(16) float b[kTK][kTN + 4];
+  const hc_expert_mlp_t& p = g.p;
+  pdl_wait();
+  pdl_trigger();
+  const ExpertTile t = expert_tile(g.lists.bounds, p.num_experts, kTM, blockIdx.x);
+  if (t.rows == 0) return;
+  const T* down = static_cast<const T*>(p.down) + t.expert * p.down_expert_stride;
+  const int n0 = blockIdx.y * kTN;
+  const Thread me = my_part();
+  float acc[2][4] = {};
+  for (int k0 = 0; k0 < p.inner; k0 += kTK) {
+    for (int i = threadIdx.x; i < kTM * kTK; i += kGenThreads) {
+      const int m = i / kTK, k = i % kTK;
+      a[k][m] = m < t.rows && k0 + k < p.inner ? g.h[static_cast<int64_t>(t.first + m) * p.inner + k0 + k] : 0.0f;
+    }
+    load_weight(b, down, p.down_in_stride, p.down_out_stride, k0, n0, p.inner, p.hidden);
+    __syncthreads();
+    multiply(acc, a, b, me);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = me.rm + 16 * i;
+    if (m >= t.rows) continue;
+    const int64_t pair = g.lists.order[t.first + m];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n0 + me.cn + j < p.hidden) g.o[pair * p.hidden + n0 + me.cn + j] = acc[i][j];
+  }
+}
+
+// ---------------------------------------------------------------- combine --
+
+constexpr int kCombineThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(hc_expert_mlp_t p, const float* __restrict__ o) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t t = blockIdx.x;
+  T* out = static_cast<T*>(p.out) + t * p.out_stride;
+  const int32_t* ids = p.experts + t * p.top_k;
+  const float* w = p.weights + t * p.top_k;
+  for (int c = blockIdx.y * kCombineThreads + threadIdx.x; c < p.hidden; c += gridDim.y * kCombineThreads) {
+    float sum = 0.0f;
+    for (int j = 0; j < p.top_k; ++j)
+      if (ids[j] >= 0 && ids[j] < p.num_experts) sum = fmaf(w[j], o[(t * p.top_k + j) * p.hidden + c], sum);
+    stf(out + c, sum);
+  }
+}
+
+struct Layout {
+  size_t bounds, order, h, o, total;
+};
+Layout general_layout(const hc_expert_mlp_t& a) {
+  const size_t pairs = static_cast<size_t>(a.tokens) * a.top_k;
+  Layout l;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = align_up(at + bytes, 256);
+    return here;
+  };
+  l.bounds = take((a.num_experts + 1) * sizeof(int32_t));
+  l.order = take(pairs * sizeof(int32_t));
+  l.h = take(pairs * a.inner * sizeof(float));
+  l.o = take(pairs * a.hidden * sizeof(float));
+  l.total = at;
+  return l;
+}
+
+template <typename T> cudaError_t launch_general(const hc_expert_mlp_t& a, cudaStream_t s) {
+  const Layout l = general_layout(a);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const GeneralArgs g = {a,
+                         {reinterpret_cast<int32_t*>(ws + l.bounds), reinterpret_cast<int32_t*>(ws + l.order)},
+                         reinterpret_cast<float*>(ws + l.h),
+                         reinterpret_cast<float*>(ws + l.o)};
+  const int pairs = static_cast<int>(a.tokens * a.top_k);
+  const unsigned slots = static_cast<unsigned>(expert_slots(pairs, kTM, a.num_experts));
+  cudaError_t e = pairs > 4096 ? launch_pdl(lists_kernel<1024>, dim3(a.num_experts), dim3(1024), 0, s, 1, a.experts, pairs,
+                                            a.num_experts, g.lists)
+                               : launch_pdl(lists_kernel<128>, dim3(a.num_experts), dim3(128), 0, s, 1, a.experts, pairs,
+                                            a.num_experts, g.lists);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(inner_kernel<T>, dim3(slots, (a.inner + kTN - 1) / kTN), dim3(kGenThreads), 0, s, 1, g);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(outer_kernel<T>, dim3(slots, (a.hidden + kTN - 1) / kTN), dim3(kGenThreads), 0, s, 1, g);
+  if (e != cudaSuccess) return e;
+  const unsigned cols = static_cast<unsigned>(std::min<int64_t>((a.hidden + kCombineThreads - 1) / kCombineThreads, 4));
+  return launch_pdl(combine_kernel<T>, dim3(static_cast<unsigned>(a.tokens), cols), dim3(kCombineThreads), 0, s, 1, a,
+                    static_cast<const float*>(g.o));
+}
+
+}  // namespace
+
+size_t expert_mlp_workspace(const hc_expert_mlp_t& a, bool, int) { return general_layout(a).total; }
+
+cudaError_t launch_expert_mlp(const hc_expert_mlp_t& a, bool, int, cudaStream_t s) {
+  if (a.dtype == HC_F32) return launch_general<float>(a, s);
+  if (a.dtype == HC_F16) return launch_general<__half>(a, s);
+  return launch_general<__nv_bfloat16>(a, s);
+}
+
+}  // namespace hc
