@@ -24,12 +24,13 @@ namespace {
 // then every warp writes its own. All CTAs read all experts (tokens * top_k numbers from L2), and none waits for another.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads)
-lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, ExpertLists lists) {
+lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, ExpertLists lists, unsigned int* tickets, int num_tickets) {
   constexpr int kWarps = kThreads / 32;
   __shared__ int own[kWarps], less[kWarps];
   pdl_wait();
   pdl_trigger();
   const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = e * kThreads + threadIdx.x; i < num_tickets; i += experts * kThreads) tickets[i] = 0;
   const int run = (pairs + kThreads - 1) / kThreads * 32;
   const int lo = min(pairs, warp * run), hi = min(pairs, lo + run);
   int mine = 0, before = 0;
@@ -105,7 +106,8 @@ __device__ __forceinline__ void multiply(float (*acc)[4], const float (*a)[kTM +
 struct GeneralArgs {
   hc_expert_mlp_t p;
   ExpertLists lists;
-  float *h, *o;  // (pairs, inner) in the list's order, (pairs, hidden)
+  float *h, *o;  // (pairs, inner) in the list's order, (pairs, hidden) at the pairs' places
+  int64_t o_step;
 };
 
 template <typename T> __global__ void __launch_bounds__(kGenThreads) inner_kernel(GeneralArgs g) {
@@ -180,36 +182,81 @@ template <typename T> __global__ void __launch_bounds__(kGenThreads) outer_kerne
     const int64_t pair = g.lists.order[t.first + m];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (n0 + me.cn + j < p.hidden) g.o[pair * p.hidden + n0 + me.cn + j] = acc[i][j];
+      if (n0 + me.cn + j < p.hidden) g.o[pair * g.o_step + n0 + me.cn + j] = acc[i][j];
   }
 }
 
 // ---------------------------------------------------------------- combine --
 
-constexpr int kCombineThreads = 256;
+// Eight features to a thread; rows of o are padded to a multiple of eight. Bound: bytes, top_k + 1 rows a token.
+template <typename O> __device__ __forceinline__ void load8(const O* p, float* v) { V8<O>::unpack(ld16(p), v); }
+template <> __device__ __forceinline__ void load8<float>(const float* p, float* v) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
 
-template <typename T>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(hc_expert_mlp_t p, const float* __restrict__ o) {
+template <typename T, typename O>
+__global__ void __launch_bounds__(512) combine_kernel(hc_expert_mlp_t p, const O* __restrict__ o, int64_t o_step, bool vec) {
   pdl_wait();
   pdl_trigger();
   const int64_t t = blockIdx.x;
   T* out = static_cast<T*>(p.out) + t * p.out_stride;
   const int32_t* ids = p.experts + t * p.top_k;
   const float* w = p.weights + t * p.top_k;
-  for (int c = blockIdx.y * kCombineThreads + threadIdx.x; c < p.hidden; c += gridDim.y * kCombineThreads) {
-    float sum = 0.0f;
-    for (int j = 0; j < p.top_k; ++j)
-      if (ids[j] >= 0 && ids[j] < p.num_experts) sum = fmaf(w[j], o[(t * p.top_k + j) * p.hidden + c], sum);
-    stf(out + c, sum);
+  for (int c = threadIdx.x * 8; c < p.hidden; c += blockDim.x * 8) {
+    float sum[8] = {};
+#pragma unroll 4
+    for (int j = 0; j < p.top_k; ++j) {
+      if (ids[j] >= 0 && ids[j] < p.num_experts) {
+        float v[8];
+        load8(o + (t * p.top_k + j) * o_step + c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], v[i], sum[i]);
+      }
+    }
+    if (vec) {  // (out's rows are 16-byte aligned and hold whole vectors)
+      if constexpr (sizeof(T) == 2) {
+        st16(out + c, V8<T>::pack(sum));
+      } else {
+        reinterpret_cast<float4*>(out + c)[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        reinterpret_cast<float4*>(out + c)[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < p.hidden) stf(out + c + i, sum[i]);
+    }
   }
 }
 
-struct Layout {
-  size_t bounds, order, h, o, total;
+template <typename T, typename O>
+cudaError_t launch_combine(const hc_expert_mlp_t& a, const O* o, int64_t o_step, cudaStream_t s) {
+  const bool vec = a.hidden % 8 == 0 && a.out_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+  const int threads = std::min(512, (a.hidden + 255) / 256 * 32);
+  return launch_pdl(combine_kernel<T, O>, dim3(static_cast<unsigned>(a.tokens)), dim3(threads), 0, s, 1, a, o, o_step, vec);
+}
+
+// ---------------------------------------------------------------- layout --
+
+struct Plan {
+  int rows;  // pairs to a tile of the tensor cores' products; 0: the general ones
+  int64_t tickets, inner_tickets;
+  int64_t h_step, o_step;
+  size_t bounds, order, count, part, h, o, total;
 };
-Layout general_layout(const hc_expert_mlp_t& a) {
+
+// Which products run, and where their buffers lie in the workspace. Tiles of 32, 64 or 128 pairs by the pairs that an
+// expert has on average: REPLACE_RULE
+Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   const size_t pairs = static_cast<size_t>(a.tokens) * a.top_k;
-  Layout l;
+  Plan l = {};
+  // (TMA steps from row to row and from expert to expert, so strides of 0 are not for it)
+  const bool steps = (a.num_experts == 1 || (a.up_expert_stride > 0 && a.down_expert_stride > 0)) &&
+                     (a.tokens == 1 || a.x_stride >= a.hidden);
+  if (a.dtype != HC_F32 && aligned && steps && !(a.flags & HC_FLAG_FORCE_GENERAL)) {
+    const size_t mean = pairs / a.num_experts;
+    l.rows = mean <= 24 ? 32 : mean <= 48 ? 64 : 128;
+  }
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -218,43 +265,62 @@ Layout general_layout(const hc_expert_mlp_t& a) {
   };
   l.bounds = take((a.num_experts + 1) * sizeof(int32_t));
   l.order = take(pairs * sizeof(int32_t));
-  l.h = take(pairs * a.inner * sizeof(float));
-  l.o = take(pairs * a.hidden * sizeof(float));
+  l.h_step = l.rows ? static_cast<int64_t>(align_up(a.inner, 8)) : a.inner;
+  l.o_step = static_cast<int64_t>(align_up(a.hidden, 8));
+  const bool few = l.rows == 32 || l.rows == 64;
+  if (few) {
+    l.inner_tickets = experts_um_tiles(a, l.rows, true);
+    l.tickets = l.inner_tickets + experts_um_tiles(a, l.rows, false);
+    l.count = take(l.tickets * sizeof(unsigned int));
+    l.part = take(static_cast<size_t>(num_sms) * 2 * 2 * l.rows * 128 * sizeof(float));
+  }
+  l.h = take(pairs * l.h_step * (l.rows ? 2 : 4));
+  l.o = take(pairs * l.o_step * (l.rows && !few ? 2 : 4));
   l.total = at;
   return l;
 }
 
-template <typename T> cudaError_t launch_general(const hc_expert_mlp_t& a, cudaStream_t s) {
-  const Layout l = general_layout(a);
+template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned, int num_sms, cudaStream_t s) {
+  const Plan l = make_plan(a, aligned, num_sms);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  const GeneralArgs g = {a,
-                         {reinterpret_cast<int32_t*>(ws + l.bounds), reinterpret_cast<int32_t*>(ws + l.order)},
-                         reinterpret_cast<float*>(ws + l.h),
-                         reinterpret_cast<float*>(ws + l.o)};
-  const int pairs = static_cast<int>(a.tokens * a.top_k);
-  const unsigned slots = static_cast<unsigned>(expert_slots(pairs, kTM, a.num_experts));
+  const ExpertLists lists = {reinterpret_cast<int32_t*>(ws + l.bounds), reinterpret_cast<int32_t*>(ws + l.order)};
+  unsigned int* tickets = reinterpret_cast<unsigned int*>(ws + l.count);
+  const int pairs = static_cast<int>(a.tokens * a.top_k), count = static_cast<int>(l.tickets);
   cudaError_t e = pairs > 4096 ? launch_pdl(lists_kernel<1024>, dim3(a.num_experts), dim3(1024), 0, s, 1, a.experts, pairs,
-                                            a.num_experts, g.lists)
+                                            a.num_experts, lists, tickets, count)
                                : launch_pdl(lists_kernel<128>, dim3(a.num_experts), dim3(128), 0, s, 1, a.experts, pairs,
-                                            a.num_experts, g.lists);
+                                            a.num_experts, lists, tickets, count);
   if (e != cudaSuccess) return e;
+  const float* of = reinterpret_cast<const float*>(ws + l.o);
+  if constexpr (sizeof(T) == 2) {
+    if (l.rows) {
+      const ExpertUm u = {lists, ws + l.h, ws + l.o, l.h_step, l.o_step, reinterpret_cast<float*>(ws + l.part), tickets,
+                          l.inner_tickets, l.rows};
+      e = launch_experts_um(a, u, num_sms, s);
+      if (e != cudaSuccess) return e;
+      return l.rows == 128 ? launch_combine<T, T>(a, reinterpret_cast<const T*>(ws + l.o), l.o_step, s)
+                           : launch_combine<T, float>(a, of, l.o_step, s);
+    }
+  }
+  const GeneralArgs g = {a, lists, reinterpret_cast<float*>(ws + l.h), reinterpret_cast<float*>(ws + l.o), l.o_step};
+  const unsigned slots = static_cast<unsigned>(expert_slots(pairs, kTM, a.num_experts));
   e = launch_pdl(inner_kernel<T>, dim3(slots, (a.inner + kTN - 1) / kTN), dim3(kGenThreads), 0, s, 1, g);
   if (e != cudaSuccess) return e;
   e = launch_pdl(outer_kernel<T>, dim3(slots, (a.hidden + kTN - 1) / kTN), dim3(kGenThreads), 0, s, 1, g);
   if (e != cudaSuccess) return e;
-  const unsigned cols = static_cast<unsigned>(std::min<int64_t>((a.hidden + kCombineThreads - 1) / kCombineThreads, 4));
-  return launch_pdl(combine_kernel<T>, dim3(static_cast<unsigned>(a.tokens), cols), dim3(kCombineThreads), 0, s, 1, a,
-                    static_cast<const float*>(g.o));
+  return launch_combine<T, float>(a, of, l.o_step, s);
 }
 
 }  // namespace
 
-size_t expert_mlp_workspace(const hc_expert_mlp_t& a, bool, int) { return general_layout(a).total; }
+size_t expert_mlp_workspace(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
+  return make_plan(a, aligned, num_sms).total;
+}
 
-cudaError_t launch_expert_mlp(const hc_expert_mlp_t& a, bool, int, cudaStream_t s) {
-  if (a.dtype == HC_F32) return launch_general<float>(a, s);
-  if (a.dtype == HC_F16) return launch_general<__half>(a, s);
-  return launch_general<__nv_bfloat16>(a, s);
+cudaError_t launch_expert_mlp(const hc_expert_mlp_t& a, bool aligned, int num_sms, cudaStream_t s) {
+  if (a.dtype == HC_F32) return launch<float>(a, aligned, num_sms, s);
+  if (a.dtype == HC_F16) return launch<__half>(a, aligned, num_sms, s);
+  return launch<__nv_bfloat16>(a, aligned, num_sms, s);
 }
 
 }  // namespace hc

@@ -16,6 +16,19 @@ struct ExpertLists {
   int32_t* order;   // [pairs]
 };
 
+// The products on the tensor cores (hc_experts_um.cu), for fp16 and bf16.
+struct ExpertUm {
+  ExpertLists lists;
+  void *h, *o;             // (pairs, inner) of T in the list's order; (pairs, hidden) at the pairs' places, of T or float
+  int64_t h_step, o_step;  // elements from row to row, multiples of 8
+  float* part;             // partial sums
+  unsigned int* tickets;   // of the inner product's tiles, then of the outer one's; zero before the call
+  int64_t inner_tickets;
+  int rows;                // pairs to a tile: 32 and 64 (few, o is float), 128 (many, o is T)
+};
+int64_t experts_um_tiles(const hc_expert_mlp_t& p, int rows, bool inner);
+cudaError_t launch_experts_um(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s);
+
 // Tiles of up to `rows` rows of one expert's part of the list have numbers ("slots") that follow from the bounds without a
 // sum over experts: expert e's tiles are slots bounds[e] / rows + e, ... A slot past an expert's last tile is empty. There
 // are pairs / rows + num_experts slots.
