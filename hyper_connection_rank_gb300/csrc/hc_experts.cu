@@ -31,14 +31,22 @@ lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, ExpertList
   pdl_trigger();
   const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = e * kThreads + threadIdx.x; i < num_tickets; i += experts * kThreads) tickets[i] = 0;
-  const int run = (pairs + kThreads - 1) / kThreads * 32;
+  // four neighbouring pairs to a lane, 128 to a warp's step
+  const bool vec = (reinterpret_cast<uintptr_t>(ids) & 15u) == 0;
+  const auto load4 = [&](int i) {
+    if (vec && i + 4 <= pairs) return *reinterpret_cast<const int4*>(ids + i);
+    return make_int4(i < pairs ? ids[i] : -1, i + 1 < pairs ? ids[i + 1] : -1, i + 2 < pairs ? ids[i + 2] : -1,
+                     i + 3 < pairs ? ids[i + 3] : -1);
+  };
+  const int run = (pairs + kThreads * 4 - 1) / (kThreads * 4) * 128;
   const int lo = min(pairs, warp * run), hi = min(pairs, lo + run);
   int mine = 0, before = 0;
-#pragma unroll 8
-  for (int i = lo + lane; i < hi; i += 32) {
-    const int id = ids[i];
-    mine += id == e;
-    before += id >= 0 && id < e;
+#pragma unroll 4
+  for (int i = lo + lane * 4; i < hi; i += 128) {
+    const int4 v = load4(i);
+    mine += (v.x == e) + (v.y == e) + (v.z == e) + (v.w == e);
+    const auto less_than = [&](int id) { return id >= 0 && id < e; };
+    before += less_than(v.x) + less_than(v.y) + less_than(v.z) + less_than(v.w);
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
   before = __reduce_add_sync(0xffffffffu, before);
@@ -57,12 +65,28 @@ lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, ExpertList
     if (e == experts - 1) lists.bounds[experts] = end;
   }
   if (mine == 0) return;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const bool hit = i < hi && ids[i] == e;
-    const unsigned hits = __ballot_sync(0xffffffffu, hit);
-    if (hit) lists.order[at + __popc(hits & ((1u << lane) - 1u))] = i;
-    at += __popc(hits);
+  constexpr int kAhead = 4;
+  const unsigned below = (1u << lane) - 1u;
+  for (int i0 = lo; i0 < hi; i0 += 128 * kAhead) {
+    int4 v[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      v[j] = i0 + 128 * j + lane * 4 < hi ? load4(i0 + 128 * j + lane * 4) : make_int4(-1, -1, -1, -1);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const bool hit[4] = {v[j].x == e, v[j].y == e, v[j].z == e, v[j].w == e};
+      int rank = 0, all = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const unsigned hits = __ballot_sync(0xffffffffu, hit[c]);
+        rank += __popc(hits & below);
+        all += __popc(hits);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (hit[c]) lists.order[at + rank++] = i0 + 128 * j + lane * 4 + c;
+      at += all;
+    }
   }
 }
 
@@ -188,15 +212,11 @@ template <typename T> __global__ void __launch_bounds__(kGenThreads) outer_kerne
 
 // ---------------------------------------------------------------- combine --
 
-// Eight features to a thread; rows of o are padded to a multiple of eight. Bound: bytes, top_k + 1 rows a token.
-template <typename O> __device__ __forceinline__ void load8(const O* p, float* v) { V8<O>::unpack(ld16(p), v); }
-template <> __device__ __forceinline__ void load8<float>(const float* p, float* v) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
-template <typename T, typename O>
-__global__ void __launch_bounds__(512) combine_kernel(hc_expert_mlp_t p, const O* __restrict__ o, int64_t o_step, bool vec) {
+// Eight features to a thread; rows of o are padded to a multiple of sixteen. Bound: bytes, top_k + 1 rows a token.
+template <typename T, bool kInts>
+__global__ void __launch_bounds__(512)
+combine_kernel(hc_expert_mlp_t p, const void* __restrict__ o, int64_t o_step, const uint8_t* __restrict__ exps, int64_t exp_step,
+               bool vec) {
   pdl_wait();
   pdl_trigger();
   const int64_t t = blockIdx.x;
@@ -209,7 +229,14 @@ __global__ void __launch_bounds__(512) combine_kernel(hc_expert_mlp_t p, const O
     for (int j = 0; j < p.top_k; ++j) {
       if (ids[j] >= 0 && ids[j] < p.num_experts) {
         float v[8];
-        load8(o + (t * p.top_k + j) * o_step + c, v);
+        const int64_t pair = t * p.top_k + j, at = pair * o_step + c;
+        if constexpr (kInts) {
+          BlockFloat::unpack8(*reinterpret_cast<const uint4*>(static_cast<const int16_t*>(o) + at), exps[pair * exp_step + c / 16], v);
+        } else {
+          const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(o) + at);
+          const float4 a = f[0], b = f[1];
+          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], v[i], sum[i]);
       }
@@ -229,11 +256,13 @@ __global__ void __launch_bounds__(512) combine_kernel(hc_expert_mlp_t p, const O
   }
 }
 
-template <typename T, typename O>
-cudaError_t launch_combine(const hc_expert_mlp_t& a, const O* o, int64_t o_step, cudaStream_t s) {
+template <typename T, bool kInts>
+cudaError_t launch_combine(const hc_expert_mlp_t& a, const void* o, int64_t o_step, const uint8_t* exps, int64_t exp_step,
+                           cudaStream_t s) {
   const bool vec = a.hidden % 8 == 0 && a.out_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
   const int threads = std::min(512, (a.hidden + 255) / 256 * 32);
-  return launch_pdl(combine_kernel<T, O>, dim3(static_cast<unsigned>(a.tokens)), dim3(threads), 0, s, 1, a, o, o_step, vec);
+  return launch_pdl(combine_kernel<T, kInts>, dim3(static_cast<unsigned>(a.tokens)), dim3(threads), 0, s, 1, a, o, o_step, exps,
+                    exp_step, vec);
 }
 
 // ---------------------------------------------------------------- layout --
@@ -241,8 +270,8 @@ cudaError_t launch_combine(const hc_expert_mlp_t& a, const O* o, int64_t o_step,
 struct Plan {
   int rows;  // pairs to a tile of the tensor cores' products; 0: the general ones
   int64_t tickets, inner_tickets;
-  int64_t h_step, o_step;
-  size_t bounds, order, count, part, h, o, total;
+  int64_t h_step, o_step, exp_step;
+  size_t bounds, order, count, part, h, o, exps, total;
 };
 
 // Which products run, and where their buffers lie in the workspace. Tiles of 32, 64 or 128 pairs by the pairs that an
@@ -265,8 +294,8 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   };
   l.bounds = take((a.num_experts + 1) * sizeof(int32_t));
   l.order = take(pairs * sizeof(int32_t));
-  l.h_step = l.rows ? static_cast<int64_t>(align_up(a.inner, 8)) : a.inner;
-  l.o_step = static_cast<int64_t>(align_up(a.hidden, 8));
+  l.h_step = l.rows ? static_cast<int64_t>(align_up(a.inner, 16)) : a.inner;
+  l.o_step = static_cast<int64_t>(align_up(a.hidden, 16));
   const bool few = l.rows == 32 || l.rows == 64;
   if (few) {
     l.inner_tickets = experts_um_tiles(a, l.rows, true);
@@ -276,6 +305,10 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   }
   l.h = take(pairs * l.h_step * (l.rows ? 2 : 4));
   l.o = take(pairs * l.o_step * (l.rows && !few ? 2 : 4));
+  if (l.rows && !few) {
+    l.exp_step = static_cast<int64_t>(align_up(a.hidden, 256)) / 16;
+    l.exps = take(pairs * l.exp_step);
+  }
   l.total = at;
   return l;
 }
@@ -291,15 +324,14 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
                                : launch_pdl(lists_kernel<128>, dim3(a.num_experts), dim3(128), 0, s, 1, a.experts, pairs,
                                             a.num_experts, lists, tickets, count);
   if (e != cudaSuccess) return e;
-  const float* of = reinterpret_cast<const float*>(ws + l.o);
   if constexpr (sizeof(T) == 2) {
     if (l.rows) {
-      const ExpertUm u = {lists, ws + l.h, ws + l.o, l.h_step, l.o_step, reinterpret_cast<float*>(ws + l.part), tickets,
-                          l.inner_tickets, l.rows};
+      const ExpertUm u = {lists, ws + l.h, ws + l.o, ws + l.exps, l.h_step, l.o_step, l.exp_step,
+                          reinterpret_cast<float*>(ws + l.part), tickets, l.inner_tickets, l.rows};
       e = launch_experts_um(a, u, num_sms, s);
       if (e != cudaSuccess) return e;
-      return l.rows == 128 ? launch_combine<T, T>(a, reinterpret_cast<const T*>(ws + l.o), l.o_step, s)
-                           : launch_combine<T, float>(a, of, l.o_step, s);
+      return l.rows == 128 ? launch_combine<T, true>(a, ws + l.o, l.o_step, ws + l.exps, l.exp_step, s)
+                           : launch_combine<T, false>(a, ws + l.o, l.o_step, nullptr, 0, s);
     }
   }
   const GeneralArgs g = {a, lists, reinterpret_cast<float*>(ws + l.h), reinterpret_cast<float*>(ws + l.o), l.o_step};
@@ -308,7 +340,7 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
   if (e != cudaSuccess) return e;
   e = launch_pdl(outer_kernel<T>, dim3(slots, (a.hidden + kTN - 1) / kTN), dim3(kGenThreads), 0, s, 1, g);
   if (e != cudaSuccess) return e;
-  return launch_combine<T, float>(a, of, l.o_step, s);
+  return launch_combine<T, false>(a, ws + l.o, l.o_step, nullptr, 0, s);
 }
 
 }  // namespace

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "hc_experts_internal.h"
 
 namespace hc {
@@ -16,15 +18,69 @@ struct ExpertLists {
   int32_t* order;   // [pairs]
 };
 
+// Sixteen floats as 16-bit integers with one exponent, for results on their way to a sum in fp32: each is off by 2^-15 of
+// the largest of the sixteen at most, so that the sum's own rounding to fp16 or bf16 is what shows (rounding each to bf16
+// instead would add as much error as that does). With the largest below 2^(e - 126) the unit is 2^(e - 141) / (1 - 2^-14),
+// which keeps integers within 32766; infinities and NaN have integers of their own. e is at least 16, so values below
+// 2^-126 become 0.
+struct BlockFloat {
+  static constexpr int kMax = 32766, kInf = 32767, kNan = -32768;
+  static constexpr float kShrink = 0.99993896484375f;  // 1 - 2^-14
+
+  static __device__ __forceinline__ uint32_t pack(const float* v, uint32_t* q) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    const bool odd = top >= 0x7f800000u;
+    if (odd) {
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
+        if (u < 0x7f800000u) top = max(top, u);
+      }
+    }
+    const uint32_t e = max(top >> 23, 16u);
+    const float scale = __uint_as_float((268u - e) << 23) * kShrink;
+    // adding 1.5 * 2^23 rounds to an integer and leaves it in the low bits
+    int n[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) n[i] = __float_as_int(fmaf(v[i], scale, 12582912.0f));
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
+        if (u > 0x7f800000u) n[i] = kNan;
+        if (u == 0x7f800000u) n[i] = v[i] > 0.0f ? kInf : -kInf;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __byte_perm(n[2 * i], n[2 * i + 1], 0x5410);
+    return e;
+  }
+
+  static __device__ __forceinline__ void unpack8(const uint4& u, uint32_t e, float* v) {
+    const float scale = __uint_as_float((e - 14u) << 23) * (1.0f / kShrink);
+    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n = static_cast<int16_t>(i & 1 ? q[i >> 1] >> 16 : q[i >> 1] & 0xffffu);
+      v[i] = static_cast<float>(n) * scale;
+      if (n > kMax || n < -kMax) v[i] = n == kNan ? __int_as_float(0x7fc00000) : n > 0 ? INFINITY : -INFINITY;
+    }
+  }
+};
+
 // The products on the tensor cores (hc_experts_um.cu), for fp16 and bf16.
 struct ExpertUm {
   ExpertLists lists;
-  void *h, *o;             // (pairs, inner) of T in the list's order; (pairs, hidden) at the pairs' places, of T or float
-  int64_t h_step, o_step;  // elements from row to row, multiples of 8
+  void *h, *o;             // (pairs, inner) of T in the list's order; (pairs, hidden) at the pairs' places
+  uint8_t* exps;           // exponents of o's elements, where it holds 16-bit integers
+  int64_t h_step, o_step, exp_step;  // elements from row to row, multiples of 16
   float* part;             // partial sums
   unsigned int* tickets;   // of the inner product's tiles, then of the outer one's; zero before the call
   int64_t inner_tickets;
-  int rows;                // pairs to a tile: 32 and 64 (few, o is float), 128 (many, o is T)
+  int rows;                // pairs to a tile: 32 and 64 (few, o is float), 128 (many, o is 16-bit integers)
 };
 int64_t experts_um_tiles(const hc_expert_mlp_t& p, int rows, bool inner);
 cudaError_t launch_experts_um(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s);

@@ -46,6 +46,8 @@ constexpr int kHalf = 128;                 // features of half a tile
 constexpr int kBK = 64;                    // inputs of a stage: one 128-byte row
 constexpr int kWeightBytes = 2 * kHalf * kBK * 2;
 constexpr int kThreads = 192;              // warp 0 TMA, warp 1 MMA, warps 2..5 results
+constexpr int kGatherWarps = 4;            // (many, inner) and warps 6..9 the rows of x
+constexpr int kStageOut = 32 * 128;         // (many) results of a warp on their way out
 constexpr int kMaxExperts = 1024;
 
 struct UmArgs {
@@ -55,7 +57,11 @@ struct UmArgs {
   void* out;                // inner: h in the list's order; outer: o at the pairs' places
   float* part;              // [2 * CTAs][2 halves][kRows][128], for tiles that a cut goes through
   unsigned int* tickets;    // of each tile: pieces that have been written
-  int64_t out_step;         // elements from row to row of out
+  uint8_t* exps;            // (many, outer) an exponent for each 16 elements of o
+  int64_t out_step, exp_step;  // elements from row to row of out, and of exps
+  const void* x;            // (many, inner) rows that are gathered, and their step
+  int64_t x_step;
+  int inputs;
   int experts, top_k, kblocks, fblocks, features, k_major;
 };
 
@@ -70,11 +76,11 @@ struct Bars {
   uint64_t full[6], empty[6], acc_full[2], acc_empty[2];
   uint32_t tmem_base, last;
   int32_t bounds[kMaxExperts + 1], tiles[kMaxExperts + 1];  // tiles: of the experts before each
-  int32_t red[8];
+  int32_t red[16];
 };
 
 template <int kRows, bool kFew> constexpr size_t smem_bytes() {
-  return Cfg<kRows, kFew>::kStages * Cfg<kRows, kFew>::kStage + sizeof(Bars) + 1024;
+  return Cfg<kRows, kFew>::kStages * Cfg<kRows, kFew>::kStage + (kFew ? 0 : 4 * kStageOut) + sizeof(Bars) + 1024;
 }
 
 // Four rows of 64 elements (x a multiple of 64) into 512 bytes.
@@ -96,6 +102,13 @@ template <> __device__ __forceinline__ float saturate<__half>(float v) {
   const float m = fabsf(v);
   return m > 65504.0f && m < INFINITY ? copysignf(65504.0f, v) : v;
 }
+
+// Arrive on `bar` when this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Ordinary writes into shared memory (cp.async's among them) that this thread knows of, before the tensor core reads them.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // A CTA's pieces of work, the same for all its warps.
 template <int kRows, bool kFew> struct Pieces {
@@ -159,7 +172,7 @@ template <int kRows, bool kFew> struct Pieces {
 };
 
 // Tiles of each expert, summed up, and the bounds.
-template <int kRows> __device__ __forceinline__ void count_tiles(const UmArgs& a, Bars* b) {
+template <int kRows, int kThreads> __device__ __forceinline__ void count_tiles(const UmArgs& a, Bars* b) {
   constexpr int kEach = (kMaxExperts + kThreads - 1) / kThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int e = threadIdx.x; e <= a.experts; e += kThreads) b->bounds[e] = a.bounds[e];
@@ -190,19 +203,23 @@ template <int kRows> __device__ __forceinline__ void count_tiles(const UmArgs& a
   __syncthreads();
 }
 
+template <bool kFew, bool kInner> constexpr bool kGathers = kInner && !kFew;
+template <bool kFew, bool kInner> constexpr int kBlock = kThreads + (kGathers<kFew, kInner> ? 32 * kGatherWarps : 0);
+
 template <typename T, int kRows, bool kFew, bool kInner>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ UmArgs a) {
+__global__ void __launch_bounds__(kBlock<kFew, kInner>, 1) product_kernel(const __grid_constant__ UmArgs a) {
   using C = Cfg<kRows, kFew>;
+  constexpr bool kGather = kGathers<kFew, kInner>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int kStep = kInner ? kHalf : 2 * kHalf;  // features from tile to tile
   constexpr int kCols = 2 * C::kAccCols;             // (a power of two from 128 to 512)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  Bars* b = reinterpret_cast<Bars*>(smem + C::kStages * C::kStage);
+  Bars* b = reinterpret_cast<Bars*>(smem + C::kStages * C::kStage + (kFew ? 0 : 4 * kStageOut));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&b->full[i], 1);
+      mbar_init(&b->full[i], kGather ? 1 + 32 * kGatherWarps : 1);
       mbar_init(&b->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -224,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const uint32_t tmem = b->tmem_base;
   pdl_wait();
   pdl_trigger();
-  count_tiles<kRows>(a, b);
+  count_tiles<kRows, kBlock<kFew, kInner>>(a, b);
   Pieces<kRows, kFew> p(a, *b);
   bool ok = true;
 
@@ -233,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     while (ok && p.next(kStep)) {
       // the rows that this lane gathers (past the tile's last one any row will do: nobody looks at the results)
       int row[4];
-      if (kInner && lane * 4 < kRows) {
+      if (kInner && !kGather && lane * 4 < kRows) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) row[i] = a.order[p.first + min(lane * 4 + i, p.rows - 1)] / a.top_k;
       }
@@ -246,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         uint8_t* r = w + kWeightBytes;
         uint64_t* bar = &b->full[st];
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar, C::kStage);
+          mbar_arrive_expect_tx(bar, kGather ? kWeightBytes : C::kStage);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int n = p.feature + (kInner ? 0 : h * kHalf);
@@ -260,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           if (!kInner) tma_load_2d(r, &a.tm_rows, k * kBK, p.first, bar);
         }
         __syncwarp();
-        if (kInner && lane * 4 < kRows)
+        if (kInner && !kGather && lane * 4 < kRows)
           tma_gather4(r + lane * 4 * 128, &a.tm_rows, k * kBK, row[0], row[1], row[2], row[3], bar);
       }
     }
@@ -282,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           const int st = it % C::kStages;
           ok = mbar_wait(&b->full[st], (it / C::kStages) & 1, &g_experts_wait_timeouts);
           if (!ok) break;
+          if (kGather) fence_proxy_async();
           tc_fence_after();
           const uint64_t so = static_cast<uint64_t>((st * C::kStage) >> 4);
 #pragma unroll
@@ -300,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         mma_commit(&b->acc_full[buf]);
       }
     }
-  } else {
+  } else if (warp < 6) {
     const int quarter = warp & 3;  // of the lanes of tensor memory, which a warp's place decides
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int me = quarter * 32 + lane;
@@ -369,49 +387,113 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           const bool last = b->last != 0;
           if (last) {
             __threadfence();
-            for (int c = 0; c < p.rows; ++c) {
-              float v0 = 0.0f, v1 = 0.0f;
+            // (sixteen pairs' sums at a time, so that their loads overlap)
+            for (int b0 = 0; b0 < p.rows; b0 += 16) {
+              float v0[16] = {}, v1[16] = {};
               for (int q = c0; q <= c1; ++q) {
                 const int slot = p.first_unit(q) > unit ? 0 : 1;
-                const float* from =
-                    a.part + (2 * static_cast<int64_t>(q) + slot) * (2 * kRows * kHalf) + c * kHalf + me;
-                v0 += __ldcg(from);
-                v1 += __ldcg(from + kRows * kHalf);
+                const float* from = a.part + (2 * static_cast<int64_t>(q) + slot) * (2 * kRows * kHalf) + b0 * kHalf + me;
+                float w0[16], w1[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                  w0[c] = b0 + c < p.rows ? __ldcg(from + c * kHalf) : 0.0f;
+                  w1[c] = b0 + c < p.rows ? __ldcg(from + (kRows + c) * kHalf) : 0.0f;
+                }
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                  v0[c] += w0[c];
+                  v1[c] += w1[c];
+                }
               }
-              put(c, v0, v1);
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (b0 + c < p.rows) put(b0 + c, v0[c], v1[c]);
             }
           }
           named_bar_sync(1, 128);  // (`last` is read before it is written again)
         }
       } else {
-        // this thread has pair `me`, a column for each feature
-        T* to = static_cast<T*>(a.out) + static_cast<int64_t>(place[0]) * a.out_step + p.feature;
+        // This thread has pair `me`, a column for each feature. Sixty-four features of the warp's 32 pairs go through shared
+        // memory, so that eight lanes write 128 bytes of one row (a row for each lane would be 32 requests an instruction).
+        uint8_t* stage = smem + C::kStages * C::kStage + quarter * kStageOut;
         const bool have = me < p.rows;
-#pragma unroll 1
-        for (int c0 = 0; c0 < (kInner ? kHalf : 2 * kHalf); c0 += 16) {
-          float v[16];
-          if (kInner) {
-            uint32_t g[16], u[16];
-            tmem_ld16_nowait(d + c0, g);
-            tmem_ld16_nowait(d + kHalf + c0, u);
-            tmem_ld_wait_r(g);
-            tmem_ld_wait_r(u);
+        uint32_t exps[4] = {};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = saturate<T>(gated(__uint_as_float(g[i]), __uint_as_float(u[i])));
-          } else {
-            tmem_ld16(d + c0, v);
+        for (int h = 0; h < (kInner ? 2 : 4); ++h) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c0 = h * 64 + i * 16;
+            float v[16];
+            uint4 q[2];
+            if (kInner) {
+              uint32_t g[16], u[16];
+              tmem_ld16_nowait(d + c0, g);
+              tmem_ld16_nowait(d + kHalf + c0, u);
+              tmem_ld_wait_r(g);
+              tmem_ld_wait_r(u);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = saturate<T>(gated(__uint_as_float(g[j]), __uint_as_float(u[j])));
+              q[0] = V8<T>::pack(v);
+              q[1] = V8<T>::pack(v + 8);
+            } else {
+              tmem_ld16(d + c0, v);
+              exps[h] |= BlockFloat::pack(v, reinterpret_cast<uint32_t*>(q)) << (8 * i);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * i + j) ^ (lane & 7)) << 4)) = q[j];
           }
-          if (have) {
-            // (rows of out are 16-byte aligned and padded to a multiple of 8 elements)
-            if (p.feature + c0 < a.features) st16(to + c0, V8<T>::pack(v));
-            if (p.feature + c0 + 8 < a.features) st16(to + c0 + 8, V8<T>::pack(v + 8));
+          __syncwarp();
+          const int chunk = lane & 7, f = p.feature + h * 64 + chunk * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            const int64_t to = __shfl_sync(0xffffffffu, place[0], r);
+            const uint4 q = *reinterpret_cast<const uint4*>(stage + r * 128 + ((chunk ^ (r & 7)) << 4));
+            // (rows of out are 16-byte aligned and padded to a multiple of 16 elements)
+            if (quarter * 32 + r < p.rows && f < a.features) st16(static_cast<T*>(a.out) + to * a.out_step + f, q);
           }
+          __syncwarp();
         }
+        if (!kInner && have)  // (a row's exponents are padded to whole tiles)
+          *reinterpret_cast<uint4*>(a.exps + static_cast<int64_t>(place[0]) * a.exp_step + p.feature / 16) =
+              make_uint4(exps[0], exps[1], exps[2], exps[3]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->acc_empty[buf]);
       }
     }
+  } else if constexpr (kGather) {
+    // TMA's gather takes some 40 ns for four rows, so that 128 rows of 128 bytes would come at a third of the tensor cores'
+    // pace; four warps with 16-byte copies keep up. A lane has the same 16 bytes of eight rows.
+    const int g = warp - 6, chunk = lane & 7;
+    const uint32_t dst = smem_addr(smem) + kWeightBytes;
+    int it = 0;
+    while (ok && p.next(kStep)) {
+      const T* src[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = g * 32 + 4 * i + (lane >> 3);
+        src[i] = static_cast<const T*>(a.x) + static_cast<int64_t>(a.order[p.first + min(r, p.rows - 1)] / a.top_k) * a.x_step +
+                 chunk * 8;
+      }
+      for (int k = p.k0; k < p.k1; ++k, ++it) {
+        const int st = it % C::kStages;
+        if (lane == 0) ok = mbar_wait(&b->empty[st], ((it / C::kStages) & 1) ^ 1, &g_experts_wait_timeouts);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        const int left = a.inputs - (k * kBK + chunk * 8);  // elements of this chunk and after it
+        const uint32_t bytes = left <= 0 ? 0u : left >= 8 ? 16u : static_cast<uint32_t>(left * 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = g * 32 + 4 * i + (lane >> 3);
+          cp_async16_zfill(dst + st * C::kStage + r * 128 + ((chunk ^ (r & 7)) << 4), bytes ? src[i] + k * kBK : src[i] - chunk * 8,
+                           bytes);
+        }
+        cp_async_arrive(&b->full[st]);
+      }
+    }
+    cp_async_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -470,6 +552,11 @@ cudaError_t launch_products(const hc_expert_mlp_t& p, const ExpertUm& u, int num
   a.kblocks = (p.hidden + kBK - 1) / kBK;
   a.k_major = p.up_in_stride == 1;
   a.tickets = u.tickets;
+  a.exps = u.exps;
+  a.exp_step = u.exp_step;
+  a.x = p.x;
+  a.x_step = p.x_stride;
+  a.inputs = p.hidden;
   if (!map_2d(&a.tm_rows, p.x, kBf16, p.hidden, p.tokens, p.x_stride, 1) ||
       !map_weight(&a.tm_w[0], p.gate, kBf16, p.num_experts, p.hidden, p.inner, p.up_expert_stride, p.up_in_stride,
                   p.up_out_stride) ||
@@ -478,7 +565,7 @@ cudaError_t launch_products(const hc_expert_mlp_t& p, const ExpertUm& u, int num
   constexpr size_t smem = smem_bytes<kRows, kFew>();
   cudaError_t e = ensure_smem<product_kernel<T, kRows, kFew, true>>(smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(product_kernel<T, kRows, kFew, true>, dim3(grid(a.fblocks, a.kblocks)), dim3(kThreads), smem, s, 1, a);
+  e = launch_pdl(product_kernel<T, kRows, kFew, true>, dim3(grid(a.fblocks, a.kblocks)), dim3(kBlock<kFew, true>), smem, s, 1, a);
   if (e != cudaSuccess) return e;
   a.tickets += u.inner_tickets;
   a.out = u.o;
@@ -494,7 +581,7 @@ cudaError_t launch_products(const hc_expert_mlp_t& p, const ExpertUm& u, int num
   a.tm_w[1] = a.tm_w[0];
   e = ensure_smem<product_kernel<T, kRows, kFew, false>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(product_kernel<T, kRows, kFew, false>, dim3(grid(a.fblocks, a.kblocks)), dim3(kThreads), smem, s, 1, a);
+  return launch_pdl(product_kernel<T, kRows, kFew, false>, dim3(grid(a.fblocks, a.kblocks)), dim3(kBlock<kFew, false>), smem, s, 1, a);
 }
 
 template <typename T> cudaError_t launch_form(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s) {
