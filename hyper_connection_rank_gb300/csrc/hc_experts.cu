@@ -212,33 +212,58 @@ template <typename T> __global__ void __launch_bounds__(kGenThreads) outer_kerne
 
 // ---------------------------------------------------------------- combine --
 
-// Eight features to a thread; rows of o are padded to a multiple of sixteen. Bound: bytes, top_k + 1 rows a token.
+// A warp has 256 features of a token, eight to a lane, and loads four or eight experts' rows at a time (rows of o are padded to a
+// multiple of sixteen). Bound: bytes, top_k + 1 rows a token.
+constexpr int kCombineWarps = 4;
 template <typename T, bool kInts>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(32 * kCombineWarps, 7)
 combine_kernel(hc_expert_mlp_t p, const void* __restrict__ o, int64_t o_step, const uint8_t* __restrict__ exps, int64_t exp_step,
                bool vec) {
   pdl_wait();
   pdl_trigger();
-  const int64_t t = blockIdx.x;
-  T* out = static_cast<T*>(p.out) + t * p.out_stride;
-  const int32_t* ids = p.experts + t * p.top_k;
-  const float* w = p.weights + t * p.top_k;
-  for (int c = threadIdx.x * 8; c < p.hidden; c += blockDim.x * 8) {
+  const int lane = threadIdx.x & 31, blocks = (p.hidden + 255) / 256;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5), t = unit / blocks;
+  if (t >= p.tokens) return;
+  const int c = static_cast<int>(unit - t * blocks) * 256 + lane * 8;
+  // which of the token's experts take part
+  const int id = lane < p.top_k ? p.experts[t * p.top_k + lane] : -1;
+  const unsigned valid = __ballot_sync(0xffffffffu, id >= 0 && id < p.num_experts);
+  const int count = __popc(valid);
+  if (c < p.hidden) {
+    T* out = static_cast<T*>(p.out) + t * p.out_stride;
     float sum[8] = {};
-#pragma unroll 4
-    for (int j = 0; j < p.top_k; ++j) {
-      if (ids[j] >= 0 && ids[j] < p.num_experts) {
-        float v[8];
-        const int64_t pair = t * p.top_k + j, at = pair * o_step + c;
-        if constexpr (kInts) {
-          BlockFloat::unpack8(*reinterpret_cast<const uint4*>(static_cast<const int16_t*>(o) + at), exps[pair * exp_step + c / 16], v);
-        } else {
-          const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(o) + at);
-          const float4 a = f[0], b = f[1];
-          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        }
+    constexpr int kAhead = kInts ? 8 : 4;
+    unsigned left = valid;
+    for (int j0 = 0; j0 < count; j0 += kAhead) {
+      uint4 q[kAhead][kInts ? 1 : 2];
+      uint32_t exp[kAhead];
+      float by[kAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], v[i], sum[i]);
+      for (int j = 0; j < kAhead; ++j) {
+        if (j0 + j < count) {
+          const int64_t pair = t * p.top_k + (__ffs(left) - 1);
+          left &= left - 1;
+          by[j] = p.weights[pair];
+          if constexpr (kInts) {
+            q[j][0] = *reinterpret_cast<const uint4*>(static_cast<const int16_t*>(o) + pair * o_step + c);
+            exp[j] = exps[pair * exp_step + c / 16];
+          } else {
+            q[j][0] = reinterpret_cast<const uint4*>(static_cast<const float*>(o) + pair * o_step + c)[0];
+            q[j][1] = reinterpret_cast<const uint4*>(static_cast<const float*>(o) + pair * o_step + c)[1];
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (j0 + j < count) {
+          if constexpr (kInts) {
+            BlockFloat::add8(q[j][0], exp[j], by[j], sum);
+          } else {
+            const float* f = reinterpret_cast<const float*>(q[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = fmaf(by[j], f[i], sum[i]);
+          }
+        }
       }
     }
     if (vec) {  // (out's rows are 16-byte aligned and hold whole vectors)
@@ -260,9 +285,9 @@ template <typename T, bool kInts>
 cudaError_t launch_combine(const hc_expert_mlp_t& a, const void* o, int64_t o_step, const uint8_t* exps, int64_t exp_step,
                            cudaStream_t s) {
   const bool vec = a.hidden % 8 == 0 && a.out_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
-  const int threads = std::min(512, (a.hidden + 255) / 256 * 32);
-  return launch_pdl(combine_kernel<T, kInts>, dim3(static_cast<unsigned>(a.tokens)), dim3(threads), 0, s, 1, a, o, o_step, exps,
-                    exp_step, vec);
+  const int64_t units = a.tokens * ((a.hidden + 255) / 256);
+  return launch_pdl(combine_kernel<T, kInts>, dim3(static_cast<unsigned>((units + kCombineWarps - 1) / kCombineWarps)),
+                    dim3(32 * kCombineWarps), 0, s, 1, a, o, o_step, exps, exp_step, vec);
 }
 
 // ---------------------------------------------------------------- layout --

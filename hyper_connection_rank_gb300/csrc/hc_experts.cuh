@@ -59,14 +59,28 @@ struct BlockFloat {
     return e;
   }
 
-  static __device__ __forceinline__ void unpack8(const uint4& u, uint32_t e, float* v) {
+  // sum += by * (eight of them). An integer n is the low half of the float 2^23 + 2^15 + n, so that a subtraction makes a
+  // float of it (a conversion has a quarter of the rate).
+  static __device__ __forceinline__ void add8(const uint4& u, uint32_t e, float by, float* sum) {
     const float scale = __uint_as_float((e - 14u) << 23) * (1.0f / kShrink);
     const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+    uint32_t most = __vmaxs2(__vmaxs2(q[0], q[1]), __vmaxs2(q[2], q[3]));
+    uint32_t least = __vmins2(__vmins2(q[0], q[1]), __vmins2(q[2], q[3]));
+    if (__vmaxs2(most, 0x7ffe7ffeu) != 0x7ffe7ffeu || __vmins2(least, 0x80028002u) != 0x80028002u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int n = static_cast<int16_t>(i & 1 ? q[i >> 1] >> 16 : q[i >> 1] & 0xffffu);
+        const float v = n == kNan ? __int_as_float(0x7fc00000) : n == kInf ? INFINITY : n == -kInf ? -INFINITY
+                                                                                                 : static_cast<float>(n) * scale;
+        sum[i] = fmaf(by, v, sum[i]);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int n = static_cast<int16_t>(i & 1 ? q[i >> 1] >> 16 : q[i >> 1] & 0xffffu);
-      v[i] = static_cast<float>(n) * scale;
-      if (n > kMax || n < -kMax) v[i] = n == kNan ? __int_as_float(0x7fc00000) : n > 0 ? INFINITY : -INFINITY;
+      const uint32_t biased = q[i >> 1] ^ 0x80008000u;
+      const float n = __uint_as_float(__byte_perm(biased, 0x4b000000u, i & 1 ? 0x7432 : 0x7410)) - 8421376.0f;
+      sum[i] = fmaf(by, n * scale, sum[i]);
     }
   }
 };

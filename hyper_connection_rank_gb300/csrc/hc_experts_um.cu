@@ -45,9 +45,8 @@ namespace {
 constexpr int kHalf = 128;                 // features of half a tile
 constexpr int kBK = 64;                    // inputs of a stage: one 128-byte row
 constexpr int kWeightBytes = 2 * kHalf * kBK * 2;
-constexpr int kThreads = 192;              // warp 0 TMA, warp 1 MMA, warps 2..5 results
-constexpr int kGatherWarps = 4;            // (many, inner) and warps 6..9 the rows of x
-constexpr int kStageOut = 32 * 128;         // (many) results of a warp on their way out
+constexpr int kGatherWarps = 4;
+constexpr int kStageOut = 32 * 64;          // (many) results of a warp on their way out
 constexpr int kMaxExperts = 1024;
 
 struct UmArgs {
@@ -80,7 +79,7 @@ struct Bars {
 };
 
 template <int kRows, bool kFew> constexpr size_t smem_bytes() {
-  return Cfg<kRows, kFew>::kStages * Cfg<kRows, kFew>::kStage + (kFew ? 0 : 4 * kStageOut) + sizeof(Bars) + 1024;
+  return Cfg<kRows, kFew>::kStages * Cfg<kRows, kFew>::kStage + (kFew ? 0 : 8 * kStageOut) + sizeof(Bars) + 1024;
 }
 
 // Four rows of 64 elements (x a multiple of 64) into 512 bytes.
@@ -204,18 +203,22 @@ template <int kRows, int kThreads> __device__ __forceinline__ void count_tiles(c
 }
 
 template <bool kFew, bool kInner> constexpr bool kGathers = kInner && !kFew;
-template <bool kFew, bool kInner> constexpr int kBlock = kThreads + (kGathers<kFew, kInner> ? 32 * kGatherWarps : 0);
+// Warps that write results: a tile of the outer product has a quarter of the inner one's MMAs to a result, or less.
+template <bool kFew, bool kInner> constexpr int kResultWarps = !kFew && !kInner ? 8 : 4;
+template <bool kFew, bool kInner>
+constexpr int kBlock = 64 + 32 * kResultWarps<kFew, kInner> + (kGathers<kFew, kInner> ? 32 * kGatherWarps : 0);
 
 template <typename T, int kRows, bool kFew, bool kInner>
 __global__ void __launch_bounds__(kBlock<kFew, kInner>, 1) product_kernel(const __grid_constant__ UmArgs a) {
   using C = Cfg<kRows, kFew>;
   constexpr bool kGather = kGathers<kFew, kInner>;
+  constexpr int kResults = kResultWarps<kFew, kInner>;  // warps 2 .., after them those that gather
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int kStep = kInner ? kHalf : 2 * kHalf;  // features from tile to tile
   constexpr int kCols = 2 * C::kAccCols;             // (a power of two from 128 to 512)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  Bars* b = reinterpret_cast<Bars*>(smem + C::kStages * C::kStage + (kFew ? 0 : 4 * kStageOut));
+  Bars* b = reinterpret_cast<Bars*>(smem + C::kStages * C::kStage + (kFew ? 0 : 8 * kStageOut));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(kBlock<kFew, kInner>, 1) product_kernel(const 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b->acc_full[i], 1);
-      mbar_init(&b->acc_empty[i], 4);
+      mbar_init(&b->acc_empty[i], kResults);
     }
     fence_mbar_init();
     tma_prefetch_desc(&a.tm_rows);
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(kBlock<kFew, kInner>, 1) product_kernel(const 
         mma_commit(&b->acc_full[buf]);
       }
     }
-  } else if (warp < 6) {
+  } else if (warp < 2 + kResults) {
     const int quarter = warp & 3;  // of the lanes of tensor memory, which a warp's place decides
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int me = quarter * 32 + lane;
@@ -413,51 +416,56 @@ __global__ void __launch_bounds__(kBlock<kFew, kInner>, 1) product_kernel(const 
           named_bar_sync(1, 128);  // (`last` is read before it is written again)
         }
       } else {
-        // This thread has pair `me`, a column for each feature. Sixty-four features of the warp's 32 pairs go through shared
-        // memory, so that eight lanes write 128 bytes of one row (a row for each lane would be 32 requests an instruction).
-        uint8_t* stage = smem + C::kStages * C::kStage + quarter * kStageOut;
-        const bool have = me < p.rows;
-        uint32_t exps[4] = {};
+        // This thread has pair `me`, a column for each feature. Thirty-two features of the warp's 32 pairs at a time go through
+        // shared memory, so that four lanes write 64 bytes of one row (a row for each lane would be 32 requests an instruction).
+        constexpr int kCols32 = (kInner ? kHalf : 2 * kHalf) / 32 / (kResults / 4);  // that a warp has, from the first-th on
+        const int part = (warp - 2) / 4, first = part * kCols32;
+        uint8_t* stage = smem + C::kStages * C::kStage + (warp - 2) * kStageOut;
+        uint32_t exps[2] = {};
 #pragma unroll
-        for (int h = 0; h < (kInner ? 2 : 4); ++h) {
+        for (int h = 0; h < kCols32; ++h) {
+          const int c0 = (first + h) * 32;
+          uint32_t x[2][16], y[2][16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c0 = h * 64 + i * 16;
-            float v[16];
+          for (int i = 0; i < 2; ++i) {
+            tmem_ld16_nowait(d + c0 + 16 * i, x[i]);
+            if (kInner) tmem_ld16_nowait(d + kHalf + c0 + 16 * i, y[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
             uint4 q[2];
+            float v[16];
+            tmem_ld_wait_r(x[i]);
+            if (kInner) tmem_ld_wait_r(y[i]);
             if (kInner) {
-              uint32_t g[16], u[16];
-              tmem_ld16_nowait(d + c0, g);
-              tmem_ld16_nowait(d + kHalf + c0, u);
-              tmem_ld_wait_r(g);
-              tmem_ld_wait_r(u);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = saturate<T>(gated(__uint_as_float(g[j]), __uint_as_float(u[j])));
+              for (int j = 0; j < 16; ++j) v[j] = saturate<T>(gated(__uint_as_float(x[i][j]), __uint_as_float(y[i][j])));
               q[0] = V8<T>::pack(v);
               q[1] = V8<T>::pack(v + 8);
             } else {
-              tmem_ld16(d + c0, v);
-              exps[h] |= BlockFloat::pack(v, reinterpret_cast<uint32_t*>(q)) << (8 * i);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(x[i][j]);
+              exps[h >> 1] |= BlockFloat::pack(v, reinterpret_cast<uint32_t*>(q)) << (16 * (h & 1) + 8 * i);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * i + j) ^ (lane & 7)) << 4)) = q[j];
+              *reinterpret_cast<uint4*>(stage + lane * 64 + (((2 * i + j) ^ ((lane >> 1) & 3)) << 4)) = q[j];
           }
           __syncwarp();
-          const int chunk = lane & 7, f = p.feature + h * 64 + chunk * 8;
+          const int chunk = lane & 3, f = p.feature + c0 + chunk * 8;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3);
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
             const int64_t to = __shfl_sync(0xffffffffu, place[0], r);
-            const uint4 q = *reinterpret_cast<const uint4*>(stage + r * 128 + ((chunk ^ (r & 7)) << 4));
+            const uint4 q = *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
             // (rows of out are 16-byte aligned and padded to a multiple of 16 elements)
             if (quarter * 32 + r < p.rows && f < a.features) st16(static_cast<T*>(a.out) + to * a.out_step + f, q);
           }
           __syncwarp();
         }
-        if (!kInner && have)  // (a row's exponents are padded to whole tiles)
-          *reinterpret_cast<uint4*>(a.exps + static_cast<int64_t>(place[0]) * a.exp_step + p.feature / 16) =
-              make_uint4(exps[0], exps[1], exps[2], exps[3]);
+        if (!kInner && me < p.rows)  // (a row's exponents are padded to whole tiles)
+          *reinterpret_cast<uint2*>(a.exps + static_cast<int64_t>(place[0]) * a.exp_step + p.feature / 16 + 8 * part) =
+              make_uint2(exps[0], exps[1]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->acc_empty[buf]);
@@ -466,7 +474,7 @@ __global__ void __launch_bounds__(kBlock<kFew, kInner>, 1) product_kernel(const 
   } else if constexpr (kGather) {
     // TMA's gather takes some 40 ns for four rows, so that 128 rows of 128 bytes would come at a third of the tensor cores'
     // pace; four warps with 16-byte copies keep up. A lane has the same 16 bytes of eight rows.
-    const int g = warp - 6, chunk = lane & 7;
+    const int g = warp - 2 - kResults, chunk = lane & 7;
     const uint32_t dst = smem_addr(smem) + kWeightBytes;
     int it = 0;
     while (ok && p.next(kStep)) {
