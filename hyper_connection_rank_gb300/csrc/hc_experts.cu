@@ -299,7 +299,7 @@ struct Plan {
   size_t bounds, order, count, part, h, o, exps, total;
 };
 
-// Which products run, and where their buffers lie in the workspace. Tiles of 32, 64 or 128 pairs by the pairs that an
+// Which products run, and where their buffers lie in the workspace. Tiles of 32, 64, 128 or 256 pairs by the pairs that an
 // expert has on average: REPLACE_RULE
 Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   const size_t pairs = static_cast<size_t>(a.tokens) * a.top_k;
@@ -309,7 +309,7 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
                      (a.tokens == 1 || a.x_stride >= a.hidden);
   if (a.dtype != HC_F32 && aligned && steps && !(a.flags & HC_FLAG_FORCE_GENERAL)) {
     const size_t mean = pairs / a.num_experts;
-    l.rows = mean <= 24 ? 32 : mean <= 48 ? 64 : 128;
+    l.rows = mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 128 ? 128 : 256;
   }
   size_t at = 0;
   const auto take = [&](size_t bytes) {
@@ -321,7 +321,7 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   l.order = take(pairs * sizeof(int32_t));
   l.h_step = l.rows ? static_cast<int64_t>(align_up(a.inner, 16)) : a.inner;
   l.o_step = static_cast<int64_t>(align_up(a.hidden, 16));
-  const bool few = l.rows == 32 || l.rows == 64;
+  const bool few = l.rows > 0 && l.rows < 256;
   if (few) {
     l.inner_tickets = experts_um_tiles(a, l.rows, true);
     l.tickets = l.inner_tickets + experts_um_tiles(a, l.rows, false);
@@ -353,9 +353,9 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
     if (l.rows) {
       const ExpertUm u = {lists, ws + l.h, ws + l.o, ws + l.exps, l.h_step, l.o_step, l.exp_step,
                           reinterpret_cast<float*>(ws + l.part), tickets, l.inner_tickets, l.rows};
-      e = launch_experts_um(a, u, num_sms, s);
+      e = l.rows == 256 ? launch_experts_many(a, u, num_sms, s) : launch_experts_few(a, u, num_sms, s);
       if (e != cudaSuccess) return e;
-      return l.rows == 128 ? launch_combine<T, true>(a, ws + l.o, l.o_step, ws + l.exps, l.exp_step, s)
+      return l.rows == 256 ? launch_combine<T, true>(a, ws + l.o, l.o_step, ws + l.exps, l.exp_step, s)
                            : launch_combine<T, false>(a, ws + l.o, l.o_step, nullptr, 0, s);
     }
   }

@@ -85,7 +85,7 @@ struct BlockFloat {
   }
 };
 
-// The products on the tensor cores (hc_experts_um.cu), for fp16 and bf16.
+// The products on the tensor cores, for fp16 and bf16 (hc_experts_few.cu, hc_experts_many.cu).
 struct ExpertUm {
   ExpertLists lists;
   void *h, *o;             // (pairs, inner) of T in the list's order; (pairs, hidden) at the pairs' places
@@ -94,10 +94,11 @@ struct ExpertUm {
   float* part;             // partial sums
   unsigned int* tickets;   // of the inner product's tiles, then of the outer one's; zero before the call
   int64_t inner_tickets;
-  int rows;                // pairs to a tile: 32 and 64 (few, o is float), 128 (many, o is 16-bit integers)
+  int rows;                // pairs to a tile: 32, 64 and 128 (few, o is float), 256 (many, o is 16-bit integers)
 };
 int64_t experts_um_tiles(const hc_expert_mlp_t& p, int rows, bool inner);
-cudaError_t launch_experts_um(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s);
+cudaError_t launch_experts_few(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s);
+cudaError_t launch_experts_many(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s);
 
 // Tiles of up to `rows` rows of one expert's part of the list have numbers ("slots") that follow from the bounds without a
 // sum over experts: expert e's tiles are slots bounds[e] / rows + e, ... A slot past an expert's last tile is empty. There

@@ -1,0 +1,341 @@
+// The experts' products on the tensor cores where experts have few pairs (a serving
+// batch of single tokens): the weights are the MMA's A operand and the pairs its
+// columns, D (128 features x pairs) += W (128 x 64) R (64 x pairs), for both halves
+// of a tile. A weight's 128 rows fill the tensor core however few pairs there are.
+//
+// Bound: the bytes of the weights. All tiles' blocks of inputs, laid end to end, are
+// cut into equal runs, one for each SM, so that one token with eight experts and a
+// batch that hits all of them keep every SM's copies going. A tile that a cut goes
+// through is written as partial sums by every CTA that has a piece of it (at most
+// two to a CTA), and the CTA that finishes last adds them up in the order of the
+// runs, so that which one that is does not show in the result. REPLACE_MEASURED_FEW
+//
+// One warp copies weights, one issues MMAs, four write results, and for the inner
+// product a warp for every 32 pairs gathers rows; stages are handed over through
+// mbarriers (all waits bounded, see hc_async.cuh).
+#include <algorithm>
+
+#include "hc_experts_um.cuh"
+
+namespace hc {
+
+__device__ unsigned int g_few_wait_timeouts = 0;
+
+namespace {
+
+using namespace um;
+
+template <int kRows> struct Cfg {
+  static constexpr int kStage = 2 * kHalfBytes + kRows * kBK * 2;
+  static constexpr int kStages = kRows == 32 ? 6 : kRows == 64 ? 5 : 4;
+  static constexpr int kCols = 4 * kRows;  // of tensor memory: two accumulators of two halves each
+  static constexpr size_t kSmem = kStages * kStage + sizeof(Bars) + 1024;
+};
+template <int kRows, bool kInner> constexpr int kThreads = 192 + (kInner ? kRows : 0);
+
+template <typename T, int kRows, bool kInner>
+__global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const __grid_constant__ Args a) {
+  using C = Cfg<kRows>;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int kStep = kInner ? kHalf : 2 * kHalf;  // features from tile to tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  Bars* b = reinterpret_cast<Bars*>(smem + C::kStages * C::kStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&b->full[i], kInner ? 1 + kRows : 1);
+      mbar_init(&b->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b->acc_full[i], 1);
+      mbar_init(&b->acc_empty[i], 4);
+    }
+    fence_mbar_init();
+    if (!kInner) tma_prefetch_desc(&a.tm_rows);
+    tma_prefetch_desc(&a.tm_w[0]);
+    tma_prefetch_desc(&a.tm_w[1]);
+  }
+  if (warp == 1) {
+    tmem_alloc(&b->tmem_base, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = b->tmem_base;
+  pdl_wait();
+  pdl_trigger();
+  count_tiles<kRows, kThreads<kRows, kInner>>(a, b);
+  Pieces<kRows, true> p(a, *b, blockIdx.x, gridDim.x);
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      while (ok && p.next(kStep)) {
+        for (int k = p.k0; k < p.k1; ++k, ++it) {
+          const int st = it % C::kStages;
+          ok = mbar_wait(&b->empty[st], ((it / C::kStages) & 1) ^ 1, &g_few_wait_timeouts);
+          if (!ok) break;
+          uint8_t* w = smem + st * C::kStage;
+          mbar_arrive_expect_tx(&b->full[st], kInner ? 2 * kHalfBytes : C::kStage);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            load_half(w + h * kHalfBytes, &a.tm_w[h], a.k_major, k * kBK, p.feature + (kInner ? 0 : h * kHalf), p.expert,
+                      &b->full[st]);
+          if (!kInner) tma_load_2d(w + 2 * kHalfBytes, &a.tm_rows, k * kBK, p.first, &b->full[st]);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t w0 = smem_addr(smem), r0 = w0 + 2 * kHalfBytes;
+      const uint64_t wd = a.k_major ? smem_desc_sw128(w0, 16, 1024) : smem_desc_sw128(w0, kHalfBytes / 2, 1024);
+      const uint64_t wk = a.k_major ? 2 : 128;  // 16 inputs on, in 16 bytes
+      const uint64_t rd = smem_desc_sw128(r0, 16, 1024);
+      const uint32_t id = idesc_f16(kBf16, 128, kRows, !a.k_major, false);
+      int it = 0;
+      for (int acc = 0; ok && p.next(kStep); ++acc) {
+        const int buf = acc & 1;
+        ok = mbar_wait(&b->acc_empty[buf], ((acc >> 1) & 1) ^ 1, &g_few_wait_timeouts);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * 2 * kRows;
+        for (int k = p.k0; k < p.k1; ++k, ++it) {
+          const int st = it % C::kStages;
+          ok = mbar_wait(&b->full[st], (it / C::kStages) & 1, &g_few_wait_timeouts);
+          if (!ok) break;
+          if (kInner) fence_proxy_async();
+          tc_fence_after();
+          const uint64_t so = static_cast<uint64_t>((st * C::kStage) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk) {
+            const uint32_t add = k > p.k0 || kk > 0 ? 1u : 0u;
+            const uint64_t w = wd + so + kk * wk, r = rd + so + kk * 2;
+            mma_f16(d, w, r, id, add);
+            mma_f16(d + kRows, w + (kHalfBytes >> 4), r, id, add);
+          }
+          mma_commit(&b->empty[st]);
+        }
+        mma_commit(&b->acc_full[buf]);
+      }
+    }
+  } else if (warp < 6) {
+    const int quarter = warp & 3;  // of the lanes of tensor memory, which a warp's place decides
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const int me = quarter * 32 + lane;
+    for (int acc = 0; ok && p.next(kStep); ++acc) {
+      const int buf = acc & 1;
+      const uint32_t d = tmem + buf * 2 * kRows + lanes;
+      int place[kRows / 32];  // of the pairs' results, in out
+#pragma unroll
+      for (int i = 0; i < kRows / 32; ++i) {
+        const int at = p.first + min(32 * i + lane, p.rows - 1);
+        place[i] = kInner ? at : a.order[at];
+      }
+      ok = mbar_wait(&b->acc_full[buf], (acc >> 1) & 1, &g_few_wait_timeouts);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+              // this thread has feature `me` of both halves, a column for each pair
+              const bool whole = p.whole();
+              const int f = p.feature + me;
+              const auto put = [&](int c, float v0, float v1) {
+                const int64_t to = static_cast<int64_t>(__shfl_sync(0xffffffffu, place[c / 32], c % 32)) * a.out_step;
+                if (kInner) {
+                  if (f < a.features) stf(static_cast<T*>(a.out) + to + f, saturate<T>(gated(v0, v1)));
+                } else {
+                  if (f < a.features) static_cast<float*>(a.out)[to + f] = v0;
+                  if (f + kHalf < a.features) static_cast<float*>(a.out)[to + f + kHalf] = v1;
+                }
+              };
+              float* part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (p.k0 > 0 ? 0 : 1)) * (2 * kRows * kHalf) + me;
+      #pragma unroll
+              for (int c0 = 0; c0 < kRows; c0 += 16) {
+                if (c0 < p.rows) {
+                  float v[2][16];
+                  tmem_ld16(d + c0, v[0]);
+                  tmem_ld16(d + kRows + c0, v[1]);
+      #pragma unroll
+                  for (int c = 0; c < 16; ++c) {
+                    if (c0 + c < p.rows) {
+                      if (whole) {
+                        put(c0 + c, v[0][c], v[1][c]);
+                      } else {
+                        __stcg(part + (c0 + c) * kHalf, v[0][c]);
+                        __stcg(part + (kRows + c0 + c) * kHalf, v[1][c]);
+                      }
+                    }
+                  }
+                }
+              }
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&b->acc_empty[buf]);
+              if (!whole) {
+                const int64_t unit = static_cast<int64_t>(p.tile) * a.kblocks;
+                const int c0 = p.cta_of(unit), c1 = p.cta_of(unit + a.kblocks - 1);
+                __threadfence();
+                named_bar_sync(1, 128);
+                if (warp == 2 && lane == 0) b->last = atomicAdd(&a.tickets[p.tile], 1u) == static_cast<unsigned>(c1 - c0);
+                named_bar_sync(1, 128);
+                const bool last = b->last != 0;
+                if (last) {
+                  __threadfence();
+                  // (sixteen pairs' sums at a time, so that their loads overlap)
+                  for (int b0 = 0; b0 < p.rows; b0 += 16) {
+                    float v0[16] = {}, v1[16] = {};
+                    for (int q = c0; q <= c1; ++q) {
+                      const int slot = p.first_unit(q) > unit ? 0 : 1;
+                      const float* from = a.part + (2 * static_cast<int64_t>(q) + slot) * (2 * kRows * kHalf) + b0 * kHalf + me;
+                      float w0[16], w1[16];
+      #pragma unroll
+                      for (int c = 0; c < 16; ++c) {
+                        w0[c] = b0 + c < p.rows ? __ldcg(from + c * kHalf) : 0.0f;
+                        w1[c] = b0 + c < p.rows ? __ldcg(from + (kRows + c) * kHalf) : 0.0f;
+                      }
+      #pragma unroll
+                      for (int c = 0; c < 16; ++c) {
+                        v0[c] += w0[c];
+                        v1[c] += w1[c];
+                      }
+                    }
+      #pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                      if (b0 + c < p.rows) put(b0 + c, v0[c], v1[c]);
+                  }
+                }
+                named_bar_sync(1, 128);  // (`last` is read before it is written again)
+              }
+    }
+  } else if constexpr (kInner) {
+    const int group = warp - 6;
+    Gather<T> g;
+    int it = 0;
+    while (ok && p.next(kStep)) {
+      g.begin(a, p.first, p.rows, group);
+      for (int k = p.k0; k < p.k1; ++k, ++it) {
+        const int st = it % C::kStages;
+        if (lane == 0) ok = mbar_wait(&b->empty[st], ((it / C::kStages) & 1) ^ 1, &g_few_wait_timeouts);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        g.copy(a, smem_addr(smem) + st * C::kStage + 2 * kHalfBytes, k * kBK, group, &b->full[st]);
+      }
+    }
+    cp_async_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+template <typename T, int kRows, bool kInner>
+cudaError_t launch_product(Args a, const hc_expert_mlp_t& p, int num_sms, cudaStream_t s) {
+  // (no more CTAs than there can be units of work)
+  const int64_t units = experts_um_tiles(p, kRows, kInner) * a.kblocks;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(num_sms, units));
+  const cudaError_t e = ensure_smem<few_kernel<T, kRows, kInner>>(Cfg<kRows>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(few_kernel<T, kRows, kInner>, dim3(grid), dim3(kThreads<kRows, kInner>), Cfg<kRows>::kSmem, s, 1, a);
+}
+
+template <typename T, int kRows>
+cudaError_t launch_both(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  for (const bool inner : {true, false}) {
+    Args a;
+    if (!fill_args(&a, p, u, inner, kRows)) return cudaErrorInvalidValue;
+    a.part = u.part;
+    a.tickets = u.tickets + (inner ? 0 : u.inner_tickets);
+    e = inner ? launch_product<T, kRows, true>(a, p, num_sms, s) : launch_product<T, kRows, false>(a, p, num_sms, s);
+    if (e != cudaSuccess) break;
+  }
+  return e;
+}
+
+template <typename T> cudaError_t launch_rows(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s) {
+  if (u.rows == 32) return launch_both<T, 32>(p, u, num_sms, s);
+  if (u.rows == 64) return launch_both<T, 64>(p, u, num_sms, s);
+  return launch_both<T, 128>(p, u, num_sms, s);
+}
+
+}  // namespace
+
+namespace um {
+
+bool map_rows(CUtensorMap* m, const void* base, bool bf16, int64_t cols, int64_t rows, int64_t step, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(step) * 2};
+  const cuuint32_t box[2] = {kBK, static_cast<cuuint32_t>(box_rows)}, one[2] = {1, 1};
+  const auto fn = tmap_encoder();
+  return fn != nullptr &&
+         fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims,
+            strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map_weight(CUtensorMap* m, const void* base, bool bf16, int experts, int inputs, int outputs, int64_t es, int64_t is,
+                int64_t os) {
+  const bool k_major = is == 1;
+  const int64_t cols = k_major ? inputs : outputs, rows = k_major ? outputs : inputs, step = k_major ? os : is;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(experts)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(step) * 2, static_cast<cuuint64_t>(experts > 1 ? es : rows * step) * 2};
+  const cuuint32_t box[3] = {kBK, static_cast<cuuint32_t>(k_major ? kHalf : kBK), 1}, one[3] = {1, 1, 1};
+  const auto fn = tmap_encoder();
+  return fn != nullptr &&
+         fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims,
+            strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool fill_args(Args* a, const hc_expert_mlp_t& p, const ExpertUm& u, bool inner, int box_rows) {
+  const bool bf16 = p.dtype == HC_BF16;
+  *a = Args{};
+  a->bounds = u.lists.bounds;
+  a->order = u.lists.order;
+  a->x = p.x;
+  a->x_step = p.x_stride;
+  a->out = inner ? u.h : u.o;
+  a->out_step = inner ? u.h_step : u.o_step;
+  a->exps = u.exps;
+  a->exp_step = u.exp_step;
+  a->experts = p.num_experts;
+  a->top_k = p.top_k;
+  a->inputs = inner ? p.hidden : p.inner;
+  a->features = inner ? p.inner : p.hidden;
+  a->kblocks = (a->inputs + kBK - 1) / kBK;
+  a->fblocks = (a->features + (inner ? kHalf : 2 * kHalf) - 1) / (inner ? kHalf : 2 * kHalf);
+  const int64_t es = inner ? p.up_expert_stride : p.down_expert_stride, is = inner ? p.up_in_stride : p.down_in_stride,
+                os = inner ? p.up_out_stride : p.down_out_stride;
+  a->k_major = is == 1;
+  return (inner || map_rows(&a->tm_rows, u.h, bf16, p.inner, p.tokens * p.top_k, u.h_step, box_rows)) &&
+         map_weight(&a->tm_w[0], inner ? p.gate : p.down, bf16, p.num_experts, a->inputs, a->features, es, is, os) &&
+         map_weight(&a->tm_w[1], inner ? p.up : p.down, bf16, p.num_experts, a->inputs, a->features, es, is, os);
+}
+
+}  // namespace um
+
+int64_t experts_um_tiles(const hc_expert_mlp_t& p, int rows, bool inner) {
+  const int64_t pairs = p.tokens * p.top_k, step = inner ? um::kHalf : 2 * um::kHalf, features = inner ? p.inner : p.hidden;
+  return std::min(pairs, pairs / rows + p.num_experts) * ((features + step - 1) / step);
+}
+
+cudaError_t launch_experts_few(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s) {
+  return p.dtype == HC_F16 ? launch_rows<__half>(p, u, num_sms, s) : launch_rows<__nv_bfloat16>(p, u, num_sms, s);
+}
+
+unsigned int read_experts_few_wait_timeouts(bool reset) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_few_wait_timeouts, sizeof(v)) != cudaSuccess) return 0xffffffffu;
+  if (reset) {
+    const unsigned int z = 0;
+    cudaMemcpyToSymbol(g_few_wait_timeouts, &z, sizeof(z));
+  }
+  return v;
+}
+
+}  // namespace hc

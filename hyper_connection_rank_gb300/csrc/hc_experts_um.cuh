@@ -1,0 +1,208 @@
+// What the tensor-core kernels of the experts' products share (hc_experts_few.cu,
+// hc_experts_many.cu): arguments, the ring's barriers, the division of the work
+// into pieces, the gathering of rows, and the inner product's activation.
+//
+// Both products of the layer run through one kernel of either form,
+//
+//   inner  h = silu(x gate) * (x up), rows of x gathered by the list of pairs
+//   outer  o = h down, rows of h in the list's order
+//
+// A tile is a number of pairs of one expert by two halves of 128 features: the
+// gate's and the up projection's for the inner product, 256 features for the outer
+// one. A stage of a CTA's ring holds 64 inputs (a row of 128 bytes, in 128-byte
+// swizzle) of pairs and of weights. Weights come by TMA in either layout, with
+// their inputs or their outputs contiguous: the MMA's descriptor says which. Rows
+// of h come by TMA, too; rows of x by 16-byte copies of gathering warps (TMA's
+// gather of four rows took some 40 ns each, so that 128 rows of 128 bytes came at
+// a third of the tensor cores' pace).
+#pragma once
+
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "hc_async.cuh"
+#include "hc_common.cuh"
+#include "hc_experts.cuh"
+#include "hc_tc.cuh"
+#include "hc_vec.cuh"
+
+namespace hc {
+namespace um {
+
+constexpr int kHalf = 128;  // features of half a tile
+constexpr int kBK = 64;     // inputs of a stage: one 128-byte row
+constexpr int kHalfBytes = kHalf * kBK * 2;
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxStages = 6;
+
+struct Args {
+  CUtensorMap tm_rows;         // outer: h, a box of 64 inputs and a CTA's pairs
+  CUtensorMap tm_w[2];         // the halves: gate and up, or down twice
+  const int32_t *bounds, *order;
+  const void* x;               // inner: rows that are gathered, and their step
+  int64_t x_step;
+  void* out;                   // inner: h in the list's order; outer: o at the pairs' places
+  uint8_t* exps;               // (many, outer) an exponent for each 16 elements of o
+  int64_t out_step, exp_step;  // elements from row to row of out, and of exps
+  float* part;                 // (few) [2 * CTAs][2 halves][rows][128], for tiles that a cut goes through
+  unsigned int* tickets;       // (few) of each tile: pieces that have been written
+  int experts, top_k, inputs, features, kblocks, fblocks, k_major;
+};
+
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+  uint32_t tmem_base, last;
+  int32_t bounds[kMaxExperts + 1], tiles[kMaxExperts + 1];  // tiles: of the experts before each
+  int32_t red[32];
+};
+
+// Arrive on `bar` when this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Ordinary writes into shared memory (cp.async's among them) that this thread knows of, before the tensor core reads them.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// silu(g) * u. The approximate exponential and quotient are within 2^-21, T's rounding at least 2^-12.
+__device__ __forceinline__ float gated(float g, float u) { return __fdividef(g * u, 1.0f + __expf(-g)); }
+
+// A finite value too large for T becomes its largest one: h of fp16 can pass 65504 where its products with down do not.
+template <typename T> __device__ __forceinline__ float saturate(float v) { return v; }
+template <> __device__ __forceinline__ float saturate<__half>(float v) {
+  const float m = fabsf(v);
+  return m > 65504.0f && m < INFINITY ? copysignf(65504.0f, v) : v;
+}
+
+// The pieces of work of a CTA (or a pair of them), the same for all its warps: with kSplit an equal run of all tiles' blocks
+// of inputs laid end to end, otherwise whole tiles in turn.
+template <int kRows, bool kSplit> struct Pieces {
+  const Args& a;
+  const Bars& b;
+  int64_t at, end, units, ctas;
+
+  __device__ __forceinline__ Pieces(const Args& args, const Bars& bars, int cta, int count) : a(args), b(bars) {
+    const int total = b.tiles[a.experts] * a.fblocks;
+    units = static_cast<int64_t>(total) * a.kblocks;
+    ctas = min(static_cast<int64_t>(count), kSplit ? units : total);  // that have work, at least a unit each
+    at = end = 0;
+    if (cta < ctas) {
+      at = kSplit ? first_unit(cta) : cta;
+      end = kSplit ? first_unit(cta + 1) : total;
+    }
+  }
+  __device__ __forceinline__ int64_t first_unit(int64_t cta) const { return cta * units / ctas; }
+  __device__ __forceinline__ int cta_of(int64_t unit) const { return static_cast<int>(((unit + 1) * ctas - 1) / units); }
+
+  int tile, k0, k1;                  // blocks of inputs k0 .. k1 - 1 of this tile
+  int expert, first, rows, feature;  // its pairs in the list, its first feature (of either half)
+
+  __device__ __forceinline__ bool next(int features) {
+    if (at >= end) return false;
+    if (kSplit) {
+      tile = static_cast<int>(at / a.kblocks);
+      k0 = static_cast<int>(at - static_cast<int64_t>(tile) * a.kblocks);
+      k1 = static_cast<int>(min(static_cast<int64_t>(a.kblocks), k0 + (end - at)));
+      at += k1 - k0;
+    } else {
+      tile = static_cast<int>(at);
+      k0 = 0;
+      k1 = a.kblocks;
+      at += ctas;
+    }
+    const int m = tile / a.fblocks;
+    feature = (tile - m * a.fblocks) * features;
+    int lo = 0, hi = a.experts - 1;  // the last expert whose tiles begin at m or before (empty ones have none)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (b.tiles[mid] <= m) lo = mid;
+      else hi = mid - 1;
+    }
+    expert = lo;
+    first = b.bounds[lo] + (m - b.tiles[lo]) * kRows;
+    rows = min(kRows, b.bounds[lo + 1] - first);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == a.kblocks; }
+};
+
+// Tiles of each expert, summed up, and the bounds.
+template <int kRows, int kThreads> __device__ __forceinline__ void count_tiles(const Args& a, Bars* b) {
+  constexpr int kEach = (kMaxExperts + kThreads - 1) / kThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int e = threadIdx.x; e <= a.experts; e += kThreads) b->bounds[e] = a.bounds[e];
+  __syncthreads();
+  int n[kEach], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = threadIdx.x * kEach + i;
+    n[i] = e < a.experts ? (b->bounds[e + 1] - b->bounds[e] + kRows - 1) / kRows : 0;
+    sum += n[i];
+  }
+  int upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) b->red[warp] = upto;
+  __syncthreads();
+  int before = upto - sum;
+  for (int w = 0; w < warp; ++w) before += b->red[w];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = threadIdx.x * kEach + i;
+    if (e <= a.experts) b->tiles[e] = before;
+    before += n[i];
+  }
+  __syncthreads();
+}
+
+// A weight's half of 128 features from n, 64 inputs from k, into 16 KB.
+__device__ __forceinline__ void load_half(uint8_t* to, const CUtensorMap* map, bool k_major, int k, int n, int expert,
+                                          uint64_t* bar) {
+  if (k_major) {
+    tma_load_3d(to, map, k, n, expert, bar);
+  } else {
+    tma_load_3d(to, map, n, k, expert, bar);
+    tma_load_3d(to + kHalfBytes / 2, map, n + 64, k, expert, bar);
+  }
+}
+
+// A gathering warp's part of a tile: 32 rows of x, from place `first` of the list, `rows` of them (past those any row will
+// do: nobody looks at the results, but one is read, so it has to be a row). A lane has the same 16 bytes of eight rows.
+template <typename T> struct Gather {
+  const T* src[8];
+
+  __device__ __forceinline__ void begin(const Args& a, int first, int rows, int group) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = group * 32 + 4 * i + (lane >> 3);
+      const int pair = a.order[first + max(0, min(r, rows - 1))];
+      src[i] = static_cast<const T*>(a.x) + static_cast<int64_t>(pair / a.top_k) * a.x_step + (lane & 7) * 8;
+    }
+  }
+  // Inputs from k into the stage's rows at `to`, zeros past the last one; arrives on `bar` when they have landed.
+  __device__ __forceinline__ void copy(const Args& a, uint32_t to, int k, int group, uint64_t* bar) const {
+    const int lane = threadIdx.x & 31, chunk = lane & 7;
+    const int left = a.inputs - (k + chunk * 8);  // elements of this chunk and after it
+    const uint32_t bytes = left <= 0 ? 0u : left >= 8 ? 16u : static_cast<uint32_t>(left * 2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = group * 32 + 4 * i + (lane >> 3);
+      cp_async16_zfill(to + r * 128 + ((chunk ^ (r & 7)) << 4), bytes ? src[i] + k : src[i] - chunk * 8, bytes);
+    }
+    cp_async_arrive(bar);
+  }
+};
+
+// Host side: maps of the rows (64 elements and box_rows rows to a box) and of a weight, its contiguous axis first.
+bool map_rows(CUtensorMap* m, const void* base, bool bf16, int64_t cols, int64_t rows, int64_t step, int box_rows);
+bool map_weight(CUtensorMap* m, const void* base, bool bf16, int experts, int inputs, int outputs, int64_t es, int64_t is,
+                int64_t os);
+// The arguments of either product but for what the forms add.
+bool fill_args(Args* a, const hc_expert_mlp_t& p, const ExpertUm& u, bool inner, int box_rows);
+
+}  // namespace um
+}  // namespace hc

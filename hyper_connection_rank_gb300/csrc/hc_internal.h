@@ -90,8 +90,9 @@ cudaError_t launch_prefill(const Problem& p);
 unsigned int read_pf_wait_timeouts(bool reset);
 // Attention over a paged cache (hc_attn_tile.cu).
 unsigned int read_tile_wait_timeouts(bool reset);
-// The experts' products (hc_experts_um.cu).
-unsigned int read_experts_wait_timeouts(bool reset);
+// The experts' products (hc_experts_few.cu, hc_experts_many.cu).
+unsigned int read_experts_few_wait_timeouts(bool reset);
+unsigned int read_experts_many_wait_timeouts(bool reset);
 
 // Tensor (TMA) maps (hc_tmap.cu): the driver's encoder (nullptr if the
 // driver lacks it), and a map over a row-major [outer, inner] matrix of 16-bit

@@ -72,7 +72,7 @@ def check(hc, args, flags=0, what="", **kw):
 @pytest.mark.parametrize("tokens,experts,k,hidden,inner", [
     (1, 1, 1, 64, 64), (1, 8, 3, 128, 64), (1, 16, 8, 640, 192), (2, 3, 3, 72, 136), (5, 40, 2, 320, 200), (7, 4, 1, 1000, 88),
     (33, 4, 2, 264, 72), (61, 64, 6, 256, 128), (100, 5, 2, 136, 264), (131, 3, 1, 128, 448), (257, 2, 2, 200, 64),
-    (300, 6, 3, 512, 384)])
+    (300, 6, 3, 512, 384), (520, 4, 1, 64, 520), (900, 3, 2, 136, 712)])
 def test_mlp_sizes(hc, tokens, experts, k, hidden, inner, rows_out, dtype):
     """Every form (tiles of 32, 64 and 128 pairs; float32), tiles that are not full, widths that no tile divides."""
     check(hc, layer(1, tokens, experts, k, hidden, inner, dtype, rows_out), what="mlp")
@@ -86,14 +86,14 @@ def test_mlp_odd_widths(hc, tokens, experts, k, hidden, inner, dtype):
         check(hc, layer(2, tokens, experts, k, hidden, inner, dtype, rows_out), what="odd")
 
 
-@pytest.mark.parametrize("tokens", [1, 20, 200])
+@pytest.mark.parametrize("tokens", [1, 20, 60, 200, 500])
 def test_mlp_general_agrees(hc, tokens):
     args = layer(3, tokens, 4, 2, 192, 128, F16)
     check(hc, args, flags=hc.HC_FLAG_FORCE_GENERAL, what="general")
     check(hc, args, what="tensor cores")
 
 
-@pytest.mark.parametrize("tokens", [3, 90, 300])
+@pytest.mark.parametrize("tokens", [3, 90, 150, 700])
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=ids)
 def test_mlp_rows_without_experts(hc, tokens, dtype):
     """Entries outside the experts take no part, whatever their weights; a row without any other is zero."""
@@ -118,7 +118,7 @@ def test_mlp_nobody(hc):
     assert hc.expert_mlp(x[:0], gate, up, down, e[:0], w[:0]).shape == (0, 128)
 
 
-@pytest.mark.parametrize("tokens,experts", [(90, 16), (200, 3)])
+@pytest.mark.parametrize("tokens,experts", [(90, 16), (200, 3), (300, 4)])
 def test_mlp_one_expert_takes_all(hc, tokens, experts):
     """All tokens at one expert among several, the same expert twice for a token, experts in the order of no list."""
     x, gate, up, down, e, w = layer(6, tokens, experts, 2, 192, 136, BF16)
@@ -129,7 +129,7 @@ def test_mlp_one_expert_takes_all(hc, tokens, experts):
     check(hc, (x, gate, up, down, e, w), what="both ways")
 
 
-@pytest.mark.parametrize("tokens", [4, 150])
+@pytest.mark.parametrize("tokens", [4, 60, 150, 300])
 def test_mlp_strides(hc, tokens):
     """Rows of x and of out with room between them, experts with room between them, one matrix for gate and up."""
     args = layer(7, tokens, 3, 2, 136, 72, F16, spare=24)
@@ -155,7 +155,7 @@ def test_mlp_shared_expert(hc):
     within(y, want, tol)
 
 
-@pytest.mark.parametrize("tokens", [2, 60, 200])
+@pytest.mark.parametrize("tokens", [2, 120, 300, 700])
 def test_mlp_bad_values_stay(hc, tokens):
     """An infinity or a NaN reaches the tokens that have it or choose its expert, and no other's results."""
     x, gate, up, down, e, w = layer(9, tokens, 4, 1, 128, 64, BF16)
@@ -171,7 +171,7 @@ def test_mlp_bad_values_stay(hc, tokens):
 
 def test_mlp_large_inner_values(hc):
     """float16 inner values past 65504 are cut to it, in every form alike."""
-    for tokens in (2, 60, 200):
+    for tokens in (2, 60, 200, 500):
         x, gate, up, down, e, w = layer(10, tokens, 2, 1, 64, 64, F16)
         x, gate, up, down = (torch.full_like(t, v) for t, v in ((x, 4.0), (gate, 1.0), (up, 8.0), (down, 2.0 ** -12)))
         y = hc.expert_mlp(*on_gpu((x, gate, up, down, e, w)))
@@ -179,7 +179,7 @@ def test_mlp_large_inner_values(hc):
         assert (y.float() - 64 * 65504 * 2.0 ** -12).abs().max() <= 1024 * 2.0 ** -11
 
 
-@pytest.mark.parametrize("tokens", [1, 50, 400])
+@pytest.mark.parametrize("tokens", [1, 50, 250, 900])
 def test_mlp_deterministic_and_captured(hc, tokens):
     """The same bits again, on another stream, in a captured graph, and with two graphs that share a workspace."""
     args = on_gpu(layer(11, tokens, 12, 4, 640, 256, BF16))
