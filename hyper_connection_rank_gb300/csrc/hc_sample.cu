@@ -14,7 +14,9 @@
 // (1 each, or the weights) reaches a target: a histogram over 2048 equal steps of
 // the exponent, merged over the cluster, then histograms over the logits' bits
 // within the step that the target falls into, until one value is left; among
-// elements of that value the index decides.
+// elements of that value the index decides. If no more than 2048 elements reach
+// that step, they are listed and sorted by one CTA instead, which then finishes the
+// row by itself.
 //
 // Weights are integers, 2^43 for the largest logit: integer sums have one result
 // in any order, whatever threads, warps and CTAs make of it, and a row of 409600
@@ -26,6 +28,8 @@
 // tokens; fp64 runs at 1/64 of the rate here).
 //
 // REPLACE_MEASURED
+#include <algorithm>
+
 #include "hc_async.cuh"
 #include "hc_common.cuh"
 #include "hc_experts_internal.h"
@@ -66,17 +70,29 @@ struct SampleArgs {
   int32_t* tokens;
   float* logprobs;
   int64_t stride;
+  int64_t rows;
   int vocab, slice, top_k, dtype;
   float temperature, top_p, min_p;
+  bool undecided;  // only rows whose token is kUndecided
 };
+constexpr int kUndecided = -2;  // stands in tokens until a row's second kernel has run
 
 struct Shared {
   u64 table[64];
   u64 exchange[2][kMaxCluster];
   u64 red[kWarps];
   u64 border[4];  // where a target falls: bin, value before it, value in it
-  uint32_t lo[kBins], hi[kBins];
+  union {
+    struct {
+      uint32_t lo[kBins], hi[kBins];
+    };
+    u64 list[kBins];  // of candidates, (key falling, index rising) as rising integers
+  };
+  uint32_t listed;
 };
+constexpr int kCandidates = kBins;
+// The candidates of all CTAs come to lie where the first one's slice was.
+constexpr int kMinSlice = kCandidates * sizeof(u64) / sizeof(float);
 
 __device__ __forceinline__ uint32_t key_of(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);  // (-0 becomes 0)
@@ -109,6 +125,38 @@ __device__ __forceinline__ u64 warp_scan_u64(u64 v) {
     if (lane >= o) v += w;
   }
   return v;
+}
+
+// floor(f * v) for f in 0 .. 1, exactly.
+__device__ __forceinline__ u64 part_of(float f, u64 v) {
+  if (!(f > 0.0f)) return 0;
+  const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+  const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;  // f = m 2^(max(e, 1) - 150)
+  const int down = 150 - static_cast<int>(e ? e : 1);                  // at least 23
+  const u64 lo = m * v, hi = __umul64hi(m, v);
+  if (down < 64) return hi << (64 - down) | lo >> down;
+  return down < 128 ? hi >> (down - 64) : 0;
+}
+// The least integer that is not below f * v, at least 1.
+__device__ __forceinline__ u64 reach(float f, u64 v) {
+  const u64 n = part_of(f, v);
+  if (n == 0) return 1;
+  // (whether the product is an integer: compare n / f the other way round, in whole numbers)
+  const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+  const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+  const int down = 150 - static_cast<int>(e ? e : 1);
+  const u64 lo = m * v, hi = __umul64hi(m, v);
+  const bool whole = down < 64 ? (lo & ((1ull << down) - 1)) == 0 : lo == 0 && (hi & ((1ull << (down - 64)) - 1)) == 0;
+  return n + (whole ? 0 : 1);
+}
+
+// log(w / total) by what the others have, so that a token with nearly all of the sum keeps its digits; or, of a smaller one,
+// from the logarithm of its weight in units (log2_w), of which w may have few digits left.
+__device__ __forceinline__ float log_share(u64 w, double log2_w, u64 total) {
+  if (w >= total / 2) return -log1pf(static_cast<float>(total - w) / static_cast<float>(w));
+  const int e = 63 - __clzll(total);
+  const float rest = log2f(static_cast<float>(total) * __uint_as_float((127u - e) << 23));  // total = 2^(e + rest)
+  return 0.69314718f * (static_cast<float>(log2_w - e) - rest);
 }
 
 // One row, as a thread sees it.
@@ -177,6 +225,16 @@ struct Row {
     return static_cast<u64>(w) >> (j >> 6);
   }
 
+  // The logarithm of the weight of a token of row r.
+  __device__ __forceinline__ double log2_units(const SampleArgs& a, int64_t r, int token) const {
+    const int64_t at = r * a.stride + token;
+    const float x = a.dtype == HC_F32   ? static_cast<const float*>(a.logits)[at]
+                    : a.dtype == HC_F16 ? __half2float(static_cast<const __half*>(a.logits)[at])
+                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at]);
+    if (x == m) return kOneBits;
+    return kOneBits + (static_cast<double>(x) - static_cast<double>(m)) * (static_cast<double>(ch) + static_cast<double>(cl));
+  }
+
   __device__ __forceinline__ void add(int bin, u64 v) {
     const uint32_t lo = static_cast<uint32_t>(v);
     const uint32_t old = atomicAdd(&sh.lo[bin], lo);
@@ -235,10 +293,40 @@ struct Row {
     cluster_sync_all();
   }
 
+  // The elements that a step can hold of those that stay are in steps 0 .. bin. Lists them in the first CTA's memory and
+  // returns their number, or -1 if they are too many (then the histogram is empty again).
+  __device__ __forceinline__ int list(int bin) {
+    if (threadIdx.x == 0) sh.listed = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const float x = xs[i];
+      if (step(x) > bin) continue;
+      const uint32_t at = atomicAdd(&sh.listed, 1u);
+      if (at < kCandidates) sh.list[at] = static_cast<u64>(~key_of(x)) << 32 | static_cast<uint32_t>(base + i);
+    }
+    __syncthreads();
+    const uint32_t have = sh.listed;
+    const u64* counts = gather(have);
+    u64 before = 0, all = 0;
+    for (int r = 0; r < ctas; ++r) {
+      if (r < rank) before += counts[r];
+      all += counts[r];
+    }
+    if (all > kCandidates) {
+      for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
+      return -1;
+    }
+    const uint32_t to = mapa_shared(smem_addr(xs), 0) + static_cast<uint32_t>(before) * 8;
+    for (uint32_t i = threadIdx.x; i < have; i += kThreads) st_cluster(to + 8 * i, sh.list[i]);
+    cluster_sync_all();
+    return static_cast<int>(all);
+  }
+
   // The first element, in the order of falling logits and rising indexes, at which the values cumulated over what stays
   // reach a target becomes the last one that stays. With `mass` the values are the weights and the target is p times
-  // their sum, otherwise they are 1 and the target is k.
-  __device__ __forceinline__ void cut(bool mass, double p, u64 k) {
+  // their sum, otherwise they are 1 and the target is k. If the elements down to the target's step are few, they are listed
+  // instead (see list()) and their number is returned; *total is the sum of the values. Otherwise -1.
+  __device__ __forceinline__ int cut(bool mass, float p, u64 k, u64* total) {
     u64 want = 0;
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const float x = xs[i];
@@ -246,15 +334,16 @@ struct Row {
       const u64 v = mass ? weight(x) : 1;
       if (v != 0) add(step(x), v);
     }
-    find([&](u64 total) {
-      want = k;
-      if (mass) {
-        const double t = ceil(p * static_cast<double>(total));
-        want = t < 1.0 ? 1 : static_cast<u64>(t);
-      }
-      want = min(want, total);
+    find([&](u64 all) {
+      *total = all;
+      want = min(mass ? reach(p, all) : k, all);
       return want;
     });
+    if (cut_key == 0) {
+      const int listed = list(static_cast<int>(sh.border[0]));
+      if (listed >= 0) return listed;
+      __syncthreads();
+    }
     const int bin = static_cast<int>(sh.border[0]);
     want -= sh.border[1];
     // the keys of that step
@@ -292,6 +381,7 @@ struct Row {
     if (take < have) last = nth(high, take);
     cut_key = high;
     cut_index = last;
+    return -1;
   }
 
   // The index of the take-th element with this key.
@@ -357,18 +447,99 @@ __device__ __forceinline__ u64 load_slice(const T* row, int base, int n, float* 
   return best;
 }
 
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem);
-  float* xs = reinterpret_cast<float*>(smem + sizeof(Shared));
+// Sort `n` (a power of two) integers in shared memory.
+__device__ __forceinline__ void sort(u64* v, int n) {
+  for (int size = 2; size <= n; size *= 2) {
+    for (int apart = size / 2; apart > 0; apart /= 2) {
+      for (int t = threadIdx.x; t < n / 2; t += kThreads) {
+        const int i = 2 * t - (t & (apart - 1)), j = i + apart;
+        const bool up = (i & size) == 0;
+        const u64 x = v[i], y = v[j];
+        if ((x > y) == up) {
+          v[i] = y;
+          v[j] = x;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The sum of the values of all threads before this one, and (in *all) of all of them.
+__device__ __forceinline__ u64 block_scan_u64(Shared& sh, u64 v, u64* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const u64 upto = warp_scan_u64(v);
+  __syncthreads();
+  if (lane == 31) sh.red[warp] = upto;
+  __syncthreads();
+  u64 before = upto - v, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sh.red[w];
+    sum += sh.red[w];
+  }
+  *all = sum;
+  return before;
+}
+
+// The rest of a row whose candidates the first CTA has listed, `count` of them: sorted, the first k stay (k > 0), of those
+// the ones before which less than p of the sum lies (p < 1; the sum is `total` without a k), of those the ones not below
+// `least`; sorted by index, the token.
+__device__ __forceinline__ void finish_list(const SampleArgs& a, const Row& row, u64* list, int count, u64 k, float p, u64 total,
+                                            u64 least, float u, int64_t r) {
+  constexpr int kEach = kCandidates / kThreads;
+  Shared& sh = row.sh;
+  int size = 2;
+  while (size < count) size *= 2;
+  for (int i = count + threadIdx.x; i < size; i += kThreads) list[i] = ~0ull;
+  __syncthreads();
+  sort(list, size);
+  u64 w[kEach], sum = 0, all;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int i = threadIdx.x * kEach + j;
+    w[j] = i < count && (k == 0 || i < k) ? row.weight(value_of(~static_cast<uint32_t>(list[i] >> 32))) : 0;
+    sum += w[j];
+  }
+  u64 before = block_scan_u64(sh, sum, &all);
+  const u64 goal = p < 1.0f ? reach(p, k > 0 ? all : total) : ~0ull;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int i = threadIdx.x * kEach + j;
+    const bool stays = before < goal && w[j] >= least;
+    before += w[j];
+    if (i < size) {
+      // the index, and where the weight is
+      if (!stays) w[j] = 0;
+      sh.list[i] = w[j];
+      list[i] = stays ? list[i] << 32 | static_cast<uint32_t>(i) : ~0ull;
+    }
+  }
+  __syncthreads();
+  sort(list, size);
+  sum = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int i = threadIdx.x * kEach + j;
+    w[j] = i < size && list[i] != ~0ull ? sh.list[static_cast<uint32_t>(list[i])] : 0;
+    sum += w[j];
+  }
+  before = block_scan_u64(sh, sum, &all);
+  const u64 want = min(all, part_of(u, all) + 1);
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    if (before < want && want <= before + w[j]) {
+      a.tokens[r] = static_cast<int>(list[threadIdx.x * kEach + j] >> 32);
+      if (a.logprobs)
+        a.logprobs[r] = log_share(w[j], row.log2_units(a, r, static_cast<int>(list[threadIdx.x * kEach + j] >> 32)), all);
+    }
+    before += w[j];
+  }
+}
+
+__device__ __forceinline__ void sample_row(const SampleArgs& a, Shared& sh, float* xs, int64_t r, int rank, int ctas, int* turn) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t r = blockIdx.x / ctas;
-  const int rank = static_cast<int>(blockIdx.x % ctas);
   const int base = rank * a.slice, n = max(0, min(a.slice, a.vocab - base));
-  for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
-  if (tid < 64) sh.table[tid] = kExp2[tid];
-  pdl_wait();
-  pdl_trigger();
   u64 best;
   if (a.dtype == HC_F32)
     best = load_slice(static_cast<const float*>(a.logits) + r * a.stride, base, n, xs);
@@ -378,15 +549,16 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
     best = load_slice(static_cast<const __nv_bfloat16*>(a.logits) + r * a.stride, base, n, xs);
   const float t = a.temperatures ? a.temperatures[r] : a.temperature;
   const float p = a.top_ps ? a.top_ps[r] : a.top_p;
-  const float least = a.min_ps ? a.min_ps[r] : a.min_p;
+  const float min_p = a.min_ps ? a.min_ps[r] : a.min_p;
   const int k = a.top_ks ? a.top_ks[r] : a.top_k;
   float u = a.uniform[r];
   u = u > 0.0f ? fminf(u, 1.0f) : 0.0f;
 
-  // (every CTA of the cluster has begun before anything is stored into its shared memory)
+  // (every CTA of the cluster has begun, and its histogram is empty, before anything is stored into its shared memory)
   cluster_sync_all();
-  Row row = {sh, xs, n, base, rank, ctas, 0, 0.0f, 0.0f, 0.0f, 0u, 0xffffffffu};
+  Row row = {sh, xs, n, base, rank, ctas, *turn, 0.0f, 0.0f, 0.0f, 0u, 0xffffffffu};
   best = row.cluster_max(best);
+  *turn = row.turn;
   row.m = value_of(static_cast<uint32_t>(best >> 32));
   const int first = static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
   const bool none = row.m == -INFINITY;
@@ -400,14 +572,26 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
   const double c = 1.4426950408889634 / static_cast<double>(t);
   row.ch = static_cast<float>(c);
   row.cl = isinf(row.ch) ? 0.0f : static_cast<float>(c - static_cast<double>(row.ch));
-  if (k > 0 && k < a.vocab) row.cut(false, 0.0, static_cast<u64>(k));
-  if (p < 1.0f) row.cut(true, static_cast<double>(p), 0);
-  const u64 floor_w = least > 0.0f ? static_cast<u64>(ceil(static_cast<double>(fminf(least, 1.0f)) * static_cast<double>(kOne))) : 1;
+  const u64 least =
+      min_p > 0.0f ? static_cast<u64>(ceil(static_cast<double>(fminf(min_p, 1.0f)) * static_cast<double>(kOne))) : 1;
+  const bool cut_k = k > 0 && k < a.vocab;
+  u64 total = 0;
+  int listed = -1;
+  if (cut_k) listed = row.cut(false, 0.0f, static_cast<u64>(k), &total);
+  if (listed < 0 && p < 1.0f) listed = row.cut(true, p, 0, &total);
+  *turn = row.turn;
+  if (listed >= 0) {
+    if (rank == 0) finish_list(a, row, reinterpret_cast<u64*>(xs), listed, cut_k ? k : 0, p, total, least, u, r);
+    __syncthreads();
+    // the histogram for the next row
+    for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
+    return;
+  }
   const auto kept = [&](int i) -> u64 {
     const float x = xs[i];
     if (!row.stays(x, base + i)) return 0;
     const u64 w = row.weight(x);
-    return w >= floor_w ? w : 0;
+    return w >= least ? w : 0;
   };
 
   // a warp's sum over a run of elements, which its lanes take in turn
@@ -425,13 +609,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
     all += sh.red[w];
   }
   const u64* totals = row.gather(all);
-  u64 total = 0;
+  *turn = row.turn;
+  total = 0;
   for (int i = 0; i < ctas; ++i) {
     if (i < rank) before += totals[i];
     total += totals[i];
   }
   // the first element whose cumulated weight passes uniform * total, so is at least the next integer
-  const u64 want = min(total, static_cast<u64>(static_cast<double>(u) * static_cast<double>(total)) + 1);
+  const u64 want = min(total, part_of(u, total) + 1);
   if (!(before < want && want <= before + mine)) return;
   // in one warp: its lanes sum a run each (begun at another place each, for the sake of the memory banks)
   const int run = (hi - lo + 31) / 32, l0 = min(hi, lo + lane * run), ln = min(hi, l0 + run) - l0;
@@ -454,12 +639,240 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
     if (hit != 0) {
       if (lane == __ffs(hit) - 1) {
         a.tokens[r] = base + r0 + i;
-        // -log(sum / w) by what the others have, so that a token with nearly all of the weight keeps its digits
-        if (a.logprobs) a.logprobs[r] = -log1pf(static_cast<float>(total - w) / static_cast<float>(w));
+        if (a.logprobs) a.logprobs[r] = log_share(w, row.log2_units(a, r, base + r0 + i), total);
       }
       return;
     }
     before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
+  float* xs = reinterpret_cast<float*>(smem + sizeof(Shared));
+  const int rank = static_cast<int>(blockIdx.x % ctas), clusters = gridDim.x / ctas;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
+  if (threadIdx.x < 64) sh.table[threadIdx.x] = kExp2[threadIdx.x];
+  pdl_wait();
+  pdl_trigger();
+  int turn = 0;
+  for (int64_t r = blockIdx.x / ctas; r < a.rows; r += clusters) {
+    if (a.undecided && a.tokens[r] != kUndecided) continue;  // (read by all before the first exchange, written after the last)
+    sample_row(a, sh, xs, r, rank, ctas, &turn);
+    __syncthreads();
+  }
+}
+
+// ----------------------------------------------------------- the whole distribution --
+//
+// Where nothing is filtered, a row need not be kept, nor its largest logit known before its weights: warps read chunks of
+// 1024 logits and leave each chunk's sum in units of the power of two that its own largest weight lies above. With
+// x c = n + i / 16 + f (c in two fp32 parts, n whole), 2^(x c) = 2^n T[i] (1 + q), T and the result in 31 bits, each weight to
+// within 2^-30 of itself (equal logits have equal weights). Chunks' sums are then shifted to the row's largest n and added,
+// and the chunk in which they pass uniform * sum is read again by one warp.
+//
+// Rows with anything that this does not hold for (an infinite largest logit, one above 512 log2 units in size, where c's
+// parts no longer reach, no logit at all, a temperature of 0) keep kUndecided and are the other kernel's.
+
+constexpr int kStreamThreads = 256, kStreamWarps = kStreamThreads / 32;
+constexpr int kChunk = 1024, kPerLane = kChunk / 32;
+constexpr int kMaxChunks = kSampleMaxVocab / kChunk + 1;
+constexpr int64_t kStreamLeast = 1 << 20;  // logits of a call, below which one kernel is less than two
+constexpr int kUnitBits = 13;              // a chunk's largest weight is 2^43 to 2^44 units, 409600 of them below 2^63
+
+// 2^(30 + i / 16), rounded.
+__device__ const int kExp2Few[16] = {
+    1073741824, 1121280436, 1170923762, 1222764986, 1276901417, 1333434672, 1392470869, 1454120821,
+    1518500250, 1585730000, 1655936265, 1729250827, 1805811301, 1885761398, 1969251188, 2056437387};
+
+struct Weigh {
+  const int* table;  // in shared memory
+  float ch, cl;
+
+  // n of a logit.
+  __device__ __forceinline__ int exponent(float x) const {
+    const float p = fmaxf(__fmul_rn(x, ch), -65536.0f);
+    return (__float_as_int(p + kMagic) - kMagicBits) >> 4;
+  }
+  // Units of a logit's weight, the chunk's n being `top`. (Minus infinity and NaN have p = -65536, so none.)
+  __device__ __forceinline__ u64 units(float x, int top) const {
+    const float p = fmaxf(__fmul_rn(x, ch), -65536.0f);
+    const float pl = fmaf(x, cl, fmaf(x, ch, -p));
+    const float kf = p + kMagic;
+    const int k = __float_as_int(kf) - kMagicBits;
+    const float f = p - (kf - kMagic);  // exact, at most 1/32
+    const float h = __fmul_rn(f, kLn2);
+    // 2^(f + pl) - 1 = h + (f ln2 - h) + pl ln2 (1 + h) + f^2 (...)
+    float e = fmaf(f, kLn2, -h);
+    e = fmaf(f, kLn2Tail, e);
+    e = fmaf(fmaf(pl, h, pl), kLn2, e);
+    const float g = fmaf(f, fmaf(f, fmaf(f, 1.3333558e-03f, 9.6181291e-03f), 5.5504109e-02f), 2.4022651e-01f);
+    e = fmaf(f * f, g, e);
+    const int q = __float2int_rn(h * 4294967296.0f) + __float2int_rn(e * 4294967296.0f);  // in units of 2^-32
+    const int t = table[k & 15];
+    const uint32_t m = static_cast<uint32_t>(t + __mulhi(t, q));
+    const int down = top - (k >> 4);  // at least 0
+    const uint32_t by = max((1u << kUnitBits) >> min(down, 31), 1u);
+    const uint32_t rest = down > kUnitBits ? (down < kUnitBits + 32 ? m >> (down - kUnitBits) : 0u) : m;
+    return static_cast<u64>(rest) * by;
+  }
+
+  static constexpr float kMagic = 786432.0f;  // 1.5 2^19: a sum with it ends at multiples of 1/16
+  static constexpr int kMagicBits = 0x49400000;
+  static constexpr float kLn2 = 0.69314718f, kLn2Tail = -1.9046542e-09f;
+};
+
+// kCount elements of a row of n from `at` on, minus infinity outside. Aligned: `at` is at a 16-byte boundary.
+template <typename T, int kCount> __device__ __forceinline__ void load_inside(const T* row, int at, float* x) {
+  constexpr int kVec = 16 / sizeof(T);
+#pragma unroll
+  for (int v = 0; v < kCount / kVec; ++v) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + at + v * kVec));
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) x[v * kVec + j] = Ty<T>::to_f(e[j]);
+  }
+}
+template <typename T, int kCount> __device__ __forceinline__ void load_edge(const T* row, int at, int n, float* x) {
+#pragma unroll
+  for (int j = 0; j < kCount; ++j) x[j] = at + j >= 0 && at + j < n ? Ty<T>::to_f(row[at + j]) : -INFINITY;
+}
+
+template <typename T> __global__ void __launch_bounds__(kStreamThreads, 3) stream_kernel(SampleArgs a, int ctas) {
+  __shared__ u64 sums[kMaxChunks];
+  __shared__ int tops[kMaxChunks];
+  __shared__ int table[16];
+  __shared__ u64 red[kStreamWarps], exchange[2][kMaxCluster];
+  __shared__ u64 chosen_before;
+  __shared__ int chosen;
+  constexpr int kVec = 16 / sizeof(T);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 16) table[tid] = kExp2Few[tid];
+  if (tid == 0) chosen = -1;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const int64_t r = blockIdx.x / ctas;
+  const int rank = static_cast<int>(blockIdx.x % ctas);
+  const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+  // chunks begin at 16-byte boundaries, the first one up to a vector before the row
+  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const int chunks = (a.vocab + shift + kChunk - 1) / kChunk, each = (chunks + ctas - 1) / ctas;
+  const int c0 = min(chunks, rank * each), c1 = min(chunks, c0 + each);
+  const float t = a.temperatures ? a.temperatures[r] : a.temperature;
+  if (rank == 0 && tid == 0) a.tokens[r] = kUndecided;
+  const double scale = 1.4426950408889634 / static_cast<double>(t);
+  Weigh weigh = {table, static_cast<float>(scale), 0.0f};
+  weigh.cl = static_cast<float>(scale - static_cast<double>(weigh.ch));
+  if (!(t > 0.0f) || !(weigh.ch < 1e30f) || !(weigh.ch > 1e-30f)) return;  // (all CTAs of the row)
+  const auto chunk_top = [&](const float* x) {
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < kPerLane; ++i) top = fmaxf(top, x[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top;
+  };
+  float most = -INFINITY;  // of the chunks that this warp has seen
+  for (int k = c0 + warp; k < c1; k += kStreamWarps) {
+    float x[kPerLane];
+    const int at = k * kChunk - shift + lane * kVec;
+    if (k * kChunk >= shift && (k + 1) * kChunk - shift <= a.vocab) {
+#pragma unroll
+      for (int v = 0; v < kPerLane / kVec; ++v) load_inside<T, kVec>(row, at + v * 32 * kVec, x + v * kVec);
+    } else {
+#pragma unroll
+      for (int v = 0; v < kPerLane / kVec; ++v) load_edge<T, kVec>(row, at + v * 32 * kVec, a.vocab, x + v * kVec);
+    }
+    const float top = chunk_top(x);
+    most = fmaxf(most, top);
+    const int n = weigh.exponent(top);
+    u64 sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) sum += weigh.units(x[i], n);
+    sum = warp_sum_u64(sum);
+    if (lane == 0) {
+      sums[k - c0] = sum;
+      tops[k - c0] = n;
+    }
+  }
+  int turn = 0;
+  // every CTA has begun before anything is stored into its shared memory
+  cluster_sync_all();
+  const auto gather = [&](u64 v) -> const u64* {
+    turn ^= 1;
+    if (tid < ctas) st_cluster(mapa_shared(smem_addr(&exchange[turn][rank]), tid), v);
+    cluster_sync_all();
+    return exchange[turn];
+  };
+  if (lane == 0) red[warp] = key_of(most);
+  __syncthreads();
+  u64 highest = 0;
+  for (int w = 0; w < kStreamWarps; ++w) highest = max(highest, red[w]);
+  __syncthreads();
+  const u64* all = gather(highest);
+  for (int i = 0; i < ctas; ++i) highest = max(highest, all[i]);
+  most = value_of(static_cast<uint32_t>(highest));
+  if (!(fabsf(most) * weigh.ch <= 512.0f)) return;
+  const int top = weigh.exponent(most);
+  const auto down = [&](u64 v, int n) -> u64 { return top - n < 64 ? v >> (top - n) : 0; };
+  constexpr int kEach = (kMaxChunks + kStreamThreads - 1) / kStreamThreads;
+  u64 v[kEach], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int k = tid * kEach + i;
+    v[i] = k < c1 - c0 ? down(sums[k], tops[k]) : 0;
+    sum += v[i];
+  }
+  const u64 upto = warp_scan_u64(sum);
+  if (lane == 31) red[warp] = upto;
+  __syncthreads();
+  u64 before = upto - sum, mine = 0;
+  for (int w = 0; w < kStreamWarps; ++w) {
+    if (w < warp) before += red[w];
+    mine += red[w];
+  }
+  const u64* totals = gather(mine);
+  u64 total = 0;
+  for (int i = 0; i < ctas; ++i) {
+    if (i < rank) before += totals[i];
+    total += totals[i];
+  }
+  float u = a.uniform[r];
+  u = u > 0.0f ? fminf(u, 1.0f) : 0.0f;
+  const u64 want = min(total, part_of(u, total) + 1);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (before < want && want <= before + v[i]) {
+      chosen = tid * kEach + i;
+      chosen_before = before;
+    }
+    before += v[i];
+  }
+  __syncthreads();
+  if (chosen < 0 || warp != 0) return;
+  // the chunk again, a run of 32 to a lane
+  const int at = (c0 + chosen) * kChunk - shift + lane * kPerLane, n = tops[chosen];
+  float x[kPerLane];
+  if (at >= 0 && at + kPerLane <= a.vocab) load_inside<T, kPerLane>(row, at, x);
+  else load_edge<T, kPerLane>(row, at, a.vocab, x);
+  u64 part = 0;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) part += weigh.units(x[i], n);
+  u64 run = warp_scan_u64(part) - part;
+  // (its sums are shifted like the chunk's, so that the last one is the chunk's)
+  u64 from = chosen_before + down(run, n);
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const u64 w = weigh.units(x[i], n);
+    run += w;
+    const u64 to = chosen_before + down(run, n);
+    if (from < want && want <= to) {
+      a.tokens[r] = at + i;
+      if (a.logprobs) a.logprobs[r] = log_share(down(w, n), static_cast<double>(x[i]) * scale + (43 - top), total);
+    }
+    from = to;
   }
 }
 
@@ -471,12 +884,27 @@ cudaError_t launch_token_sample(const hc_token_sample_t& p, int num_sms, cudaStr
   while (static_cast<int64_t>(ctas) * kMaxSlice < p.vocab) ctas *= 2;
   while (ctas < kMaxCluster && p.rows * ctas * 2 <= num_sms && p.vocab / (2 * ctas) >= 2048) ctas *= 2;
   const int slice = ((p.vocab + ctas - 1) / ctas + 31) / 32 * 32;
-  const SampleArgs a = {p.logits, p.uniform, p.temperatures, p.top_ps, p.min_ps, p.top_ks, p.tokens_out, p.logprobs_out,
-                        p.logits_stride, p.vocab, slice, p.top_k, p.dtype, p.temperature, p.top_p, p.min_p};
-  const size_t smem = sizeof(Shared) + static_cast<size_t>(slice) * sizeof(float);
+  SampleArgs a = {p.logits, p.uniform, p.temperatures, p.top_ps, p.min_ps, p.top_ks, p.tokens_out, p.logprobs_out,
+                  p.logits_stride, p.rows, p.vocab, slice, p.top_k, p.dtype, p.temperature, p.top_p, p.min_p, false};
+  int64_t clusters = p.rows;
+  const bool whole = p.top_ks == nullptr && (p.top_k <= 0 || p.top_k >= p.vocab) && p.top_ps == nullptr && !(p.top_p < 1.0f) &&
+                     p.min_ps == nullptr && !(p.min_p > 0.0f);
+  if (whole && p.rows * p.vocab >= kStreamLeast) {
+    int split = 1;
+    while (split < kMaxCluster && p.rows * split * 2 <= 2 * num_sms && p.vocab / (2 * split) >= 4 * kChunk) split *= 2;
+    const dim3 grid(static_cast<unsigned>(p.rows * split)), block(kStreamThreads);
+    cudaError_t e;
+    if (p.dtype == HC_F32) e = launch_pdl(stream_kernel<float>, grid, block, 0, s, split, a, split);
+    else if (p.dtype == HC_F16) e = launch_pdl(stream_kernel<__half>, grid, block, 0, s, split, a, split);
+    else e = launch_pdl(stream_kernel<__nv_bfloat16>, grid, block, 0, s, split, a, split);
+    if (e != cudaSuccess) return e;
+    a.undecided = true;
+    clusters = std::min<int64_t>(p.rows, std::max(1, num_sms / ctas));
+  }
+  const size_t smem = sizeof(Shared) + static_cast<size_t>(std::max(slice, kMinSlice)) * sizeof(float);
   const cudaError_t e = ensure_smem<sample_kernel>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(sample_kernel, dim3(static_cast<unsigned>(p.rows * ctas)), dim3(kThreads), smem, s, ctas, a, ctas);
+  return launch_pdl(sample_kernel, dim3(static_cast<unsigned>(clusters * ctas)), dim3(kThreads), smem, s, ctas, a, ctas);
 }
 
 }  // namespace hc

@@ -120,6 +120,8 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     rows, vocab = logits.shape
 
     def each(v):
+        # (numbers reach the kernel as float32; 0.7 instead of its float32 would move sums by 1e-9 of themselves)
+        v = v if isinstance(v, (torch.Tensor, int)) else torch.full((rows,), v)
         return v.tolist() if isinstance(v, torch.Tensor) else [v] * rows
 
     got = []

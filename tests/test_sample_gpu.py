@@ -193,3 +193,54 @@ def test_captured_and_on_a_stream(hc):
     torch.cuda.synchronize()
     for a, b, c in zip(want, got, other):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=ids)
+@pytest.mark.parametrize("rows,vocab,scale", [(40, 50001, 2.0), (300, 4099, 3.0), (8, 262144, 1.0), (600, 2047, 0.3), (3, 400001, 6.0)])
+def test_whole_distribution(hc, rows, vocab, scale, dtype):
+    """Large calls that filter nothing: sums in fp32 first, rows that they cannot decide by exact ones."""
+    x = rnd(30, rows, vocab + 5, dtype=dtype, scale=scale)[:, 3:vocab + 3]
+    check(hc, x, uniforms(31, rows))
+    check(hc, x, uniforms(32, rows), temperature=0.7)
+    t = 0.2 + uniforms(33, rows)
+    t[::7] = 0.0
+    check(hc, x, uniforms(34, rows), temperature=t)
+
+
+def test_whole_distribution_odd_rows(hc):
+    n, vocab = 64, 20000
+    x = rnd(35, n, vocab, scale=2.0)
+    x[0] = -math.inf
+    x[1] = math.nan
+    x[2, 5:] = -math.inf
+    x[3, ::2] = math.nan
+    x[4, 1024:19000] = -math.inf
+    x[5] = 0.0
+    x[6] = 1e30 * x[6]
+    x[7] -= 1e6
+    u = uniforms(36, n)
+    u[8:12] = torch.tensor([0.0, 1.0, 1.0 - 2.0 ** -24, 2.0 ** -24])
+    check(hc, x, u)
+    check(hc, x, u, temperature=0.01)
+    x[12, 777], x[12, 15000] = math.inf, math.inf
+    got = hc.token_sample(x.cuda(), torch.full((n,), 0.75).cuda())
+    assert got[12] == 15000 and got[0] == -1
+    t = torch.ones(n)
+    t[5], t[13], t[14] = math.inf, 1e-38, math.nan
+    got = hc.token_sample(x.cuda(), torch.full((n,), 0.5).cuda(), temperature=t.cuda())
+    assert got[5] == vocab // 2 and got[13] == int(x[13].argmax()) and got[14] == int(x[14].argmax())
+    y = torch.zeros(64, vocab).cuda()
+    assert hc.token_sample(y, (torch.arange(64) / 64).cuda()).tolist() == [i * vocab // 64 for i in range(64)]
+
+
+@pytest.mark.parametrize("k", [2, 100, 1000, 2040, 2049, 3000])
+def test_listed_candidates(hc, k):
+    """Around the number of tokens that one CTA sorts by itself, with equal logits at the border, with and without top_p."""
+    x = rnd(37, 6, 30000, scale=2.0)
+    x[3] = x[3].mul(2).round()
+    x[4] = x[4].mul(50).round() / 50
+    u = uniforms(38, 6)
+    check(hc, x, u, top_k=k)
+    check(hc, x, u, top_k=k, top_p=0.8, min_p=0.01)
+    check(hc, x, u, top_p=0.02 + k / 40000)
+    check(hc, x, u, temperature=0.3, top_p=0.9)
