@@ -2,13 +2,11 @@
 // kernels for any shape, stride and type, and the sum over a token's experts.
 //
 //   lists_kernel    a CTA per expert: bounds and the sorted list of pairs
-//   inner_kernel    h = silu(x gate) * (x up), a row for each pair, in the list's order
-//   outer_kernel    o = h down, a row for each pair, at the pair's own place
+//   general_kernel  h = silu(x gate) * (x up), a row for each pair, in the list's order;
+//                   then o = h down, a row for each pair, at the pair's own place
 //   combine_kernel  out_t = sum_j weights[t, j] o[t top_k + j], in the order of j
-//
-// The general products run on the CUDA cores in fp32, in tiles of 32 pairs and 64
-// features with 16 inputs at a time in shared memory.
 #include <algorithm>
+#include <type_traits>
 
 #include "hc_async.cuh"
 #include "hc_common.cuh"
@@ -91,41 +89,20 @@ lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, ExpertList
 }
 
 // ------------------------------------------------------- general products --
+//
+// On the CUDA cores in fp32, for float32 and for any type, stride and alignment. A CTA has up to 24 pairs of one expert
+// and 64 features of gate and up (128 of down, as two halves of 64). Its four warps share the inputs among them, eight at a
+// time; a lane has two features of both matrices. A weight is used by one lane alone, so it goes from global memory to a
+// register, eight inputs ahead (where inputs are contiguous, by way of the warp's shared memory, so that eight lanes read
+// neighbouring inputs of a feature: a feature to a lane took three times as long); rows come through a warp's own shared memory, four inputs of a row to a broadcast load for
+// 16 multiply-adds. Sums of the four warps are added at the end, so that a sum of n products is four of n / 4 (one of n
+// was off by twice as much).
+//
+// Bound: the CUDA cores' multiply-adds with rows to spare, the weights' bytes without. REPLACE_MEASURED_GENERAL
 
-constexpr int kTM = 32, kTN = 64, kTK = 16, kGenThreads = 256;
-
-// Element (row, col) of the tile that this thread holds: rows rm, rm + 16; columns cn .. cn + 3.
-struct Thread {
-  int rm, cn;
-};
-__device__ __forceinline__ Thread my_part() {
-  return Thread{static_cast<int>(threadIdx.x) >> 4, (static_cast<int>(threadIdx.x) & 15) * 4};
-}
-
-// A block of a weight, (kTK inputs, kTN outputs) from (k0, n0), zeros outside.
-template <typename T>
-__device__ __forceinline__ void load_weight(float (*b)[kTN + 4], const T* w, int64_t in_stride, int64_t out_stride, int k0, int n0,
-                                            int inputs, int outputs) {
-  for (int i = threadIdx.x; i < kTK * kTN; i += kGenThreads) {
-    const int k = out_stride == 1 ? i / kTN : i % kTK, n = out_stride == 1 ? i % kTN : i / kTK;
-    b[k][n] = k0 + k < inputs && n0 + n < outputs ? ldf(w + (k0 + k) * in_stride + (n0 + n) * out_stride) : 0.0f;
-  }
-}
-
-__device__ __forceinline__ void multiply(float (*acc)[4], const float (*a)[kTM + 1], const float (*b)[kTN + 4], Thread me) {
-#pragma unroll
-  for (int k = 0; k < kTK; ++k) {
-    const float4 v = *reinterpret_cast<const float4*>(&b[k][me.cn]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float x = a[k][me.rm + 16 * i];
-      acc[i][0] = fmaf(x, v.x, acc[i][0]);
-      acc[i][1] = fmaf(x, v.y, acc[i][1]);
-      acc[i][2] = fmaf(x, v.z, acc[i][2]);
-      acc[i][3] = fmaf(x, v.w, acc[i][3]);
-    }
-  }
-}
+constexpr int kGroup = 4, kGroups = 6, kTM = kGroup * kGroups;  // pairs of a tile, in groups that are left out if empty
+constexpr int kTN = 64, kTK = 8, kGenWarps = 4, kGenThreads = 32 * kGenWarps;
+constexpr int kAcc = kTM * 4;  // sums of a lane
 
 struct GeneralArgs {
   hc_expert_mlp_t p;
@@ -134,80 +111,157 @@ struct GeneralArgs {
   int64_t o_step;
 };
 
-template <typename T> __global__ void __launch_bounds__(kGenThreads) inner_kernel(GeneralArgs g) {
-  __shared__ float a[kTK][kTM + 1];
-  __shared__ __align__(16) float b[2][kTK][kTN + 4];
-  __shared__ int64_t row[kTM];
+template <typename T, bool kInner, bool kByInput> __global__ void __launch_bounds__(kGenThreads, 2) general_kernel(GeneralArgs g) {
+  using In = typename std::conditional<kInner, T, float>::type;
+  extern __shared__ __align__(16) float smem[];
   const hc_expert_mlp_t& p = g.p;
   pdl_wait();
   pdl_trigger();
-  const ExpertTile t = expert_tile(g.lists.bounds, p.num_experts, kTM, blockIdx.x);
+  const ExpertTile t = expert_tile_even(g.lists.bounds, p.num_experts, kTM, blockIdx.x);
   if (t.rows == 0) return;
-  if (threadIdx.x < kTM)
-    row[threadIdx.x] =
-        threadIdx.x < t.rows ? static_cast<int64_t>(g.lists.order[t.first + threadIdx.x] / p.top_k) * p.x_stride : -1;
-  __syncthreads();
-  const T* x = static_cast<const T*>(p.x);
-  const T* gate = static_cast<const T*>(p.gate) + t.expert * p.up_expert_stride;
-  const T* up = static_cast<const T*>(p.up) + t.expert * p.up_expert_stride;
-  const int n0 = blockIdx.y * kTN;
-  const Thread me = my_part();
-  float ga[2][4] = {}, ua[2][4] = {};
-  for (int k0 = 0; k0 < p.hidden; k0 += kTK) {
-    for (int i = threadIdx.x; i < kTM * kTK; i += kGenThreads) {
-      const int m = i / kTK, k = i % kTK;
-      a[k][m] = row[m] >= 0 && k0 + k < p.hidden ? ldf(x + row[m] + k0 + k) : 0.0f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int inputs = kInner ? p.hidden : p.inner, features = kInner ? p.inner : p.hidden;
+  const int n0 = blockIdx.y * kTN * (kInner ? 1 : 2);
+  const int64_t is = kInner ? p.up_in_stride : p.down_in_stride, os = kInner ? p.up_out_stride : p.down_out_stride;
+  const int64_t expert = t.expert * (kInner ? p.up_expert_stride : p.down_expert_stride);
+  // [matrix or half][of the lane's two features]; with kByInput the lane reads input lane % 8 of features lane / 8, + 4, ...
+  const T* w[2][2];
+  bool have[2][2];
+  const int mine = kByInput ? lane / 8 : lane;
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int f = n0 + mine + 32 * j + (kInner ? 0 : kTN * m);
+      have[m][j] = f < features;
+      w[m][j] = static_cast<const T*>(kInner ? (m ? p.up : p.gate) : p.down) + expert + (have[m][j] ? f : 0) * os +
+                (kByInput ? lane % 8 : 0);
     }
-    load_weight(b[0], gate, p.up_in_stride, p.up_out_stride, k0, n0, p.hidden, p.inner);
-    load_weight(b[1], up, p.up_in_stride, p.up_out_stride, k0, n0, p.hidden, p.inner);
-    __syncthreads();
-    multiply(ga, a, b[0], me);
-    multiply(ua, a, b[1], me);
-    __syncthreads();
+  // the lane's six elements of a block of rows: input lane % 8 of rows lane / 8, + 4, ...
+  const In* x[6];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    const int at = t.first + min(lane / 8 + 4 * i, t.rows - 1);
+    x[i] = kInner ? static_cast<const In*>(p.x) + static_cast<int64_t>(g.lists.order[at] / p.top_k) * p.x_stride
+                  : reinterpret_cast<const In*>(g.h) + static_cast<int64_t>(at) * p.inner;
   }
+  float* rows = smem + warp * (2 * kTM * kTK);
+  float* turned = smem + kGenWarps * (2 * kTM * kTK) + warp * (4 * 32 * kTK);  // weights on their way to their lanes
+  const int groups = (t.rows + kGroup - 1) / kGroup;
+  float acc[kTM][2][2] = {};
+  float wn[kTK][2][2], xn[6];
+  const auto load = [&](int k0) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int m = me.rm + 16 * i;
-    if (m >= t.rows) continue;
+    for (int i = 0; i < 6; ++i) xn[i] = k0 + lane % 8 < inputs ? ldf(x[i] + k0 + lane % 8) : 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (n0 + me.cn + j < p.inner)
-        g.h[static_cast<int64_t>(t.first + m) * p.inner + n0 + me.cn + j] =
-            ga[i][j] / (1.0f + expf(-ga[i][j])) * ua[i][j];
+    for (int k = 0; k < kTK; ++k)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (kByInput) {
+            const bool in = k0 + lane % 8 < inputs && n0 + mine + 4 * k + 32 * j + (kInner ? 0 : kTN * m) < features;
+            wn[k][m][j] = in ? ldf(w[m][j] + k0 + 4 * k * os) : 0.0f;
+          } else {
+            wn[k][m][j] = have[m][j] && k0 + k < inputs ? ldf(w[m][j] + (k0 + k) * is) : 0.0f;
+          }
+        }
+  };
+  if (warp * kTK < inputs) load(warp * kTK);
+  int turn = 0;
+  for (int k0 = warp * kTK; k0 < inputs; k0 += kGenWarps * kTK, turn ^= 1) {
+    float* buf = rows + turn * (kTM * kTK);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) buf[(lane / 8 + 4 * i) * kTK + lane % 8] = xn[i];
+    float wc[kTK][2][2];
+    if (kByInput) {
+      // feature f's inputs in 32 bytes, their halves exchanged for every other four features (no bank is hit twice)
+#pragma unroll
+      for (int k = 0; k < kTK; ++k)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            turned[((m * 2 + j) * 32 + 4 * k + lane / 8) * 8 + ((lane % 8) ^ (4 * (k & 1)))] = wn[k][m][j];
+      __syncwarp();
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k4 = 0; k4 < kTK; k4 += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(turned + ((m * 2 + j) * 32 + lane) * 8 + (k4 ^ (lane & 4)));
+            wc[k4][m][j] = v.x, wc[k4 + 1][m][j] = v.y, wc[k4 + 2][m][j] = v.z, wc[k4 + 3][m][j] = v.w;
+          }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kTK; ++k)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) wc[k][m][j] = wn[k][m][j];
+    }
+    __syncwarp();
+    if (k0 + kGenWarps * kTK < inputs) load(k0 + kGenWarps * kTK);
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      if (q < groups) {
+#pragma unroll
+        for (int r = q * kGroup; r < (q + 1) * kGroup; ++r) {
+#pragma unroll
+          for (int k4 = 0; k4 < kTK; k4 += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(buf + r * kTK + k4);
+            const float xs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[r][m][j] = fmaf(xs[k], wc[k4 + k][m][j], acc[r][m][j]);
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kTM; ++r)
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (r < groups * kGroup) smem[(warp * kAcc + (r * 2 + m) * 2 + j) * 32 + lane] = acc[r][m][j];
+  __syncthreads();
+  const auto sum = [&](int r, int m, int f) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGenWarps; ++i) v += smem[(i * kAcc + (r * 2 + m) * 2 + (f >> 5)) * 32 + (f & 31)];
+    return v;
+  };
+  for (int i = threadIdx.x; i < t.rows * kTN; i += kGenThreads) {
+    const int r = i / kTN, f = i % kTN;
+    const int64_t at = t.first + r;
+    const float v0 = sum(r, 0, f), v1 = sum(r, 1, f);
+    if (kInner) {
+      if (n0 + f < features) g.h[at * p.inner + n0 + f] = v0 / (1.0f + expf(-v0)) * v1;
+    } else {
+      float* to = g.o + g.lists.order[at] * g.o_step + n0 + f;
+      if (n0 + f < features) to[0] = v0;
+      if (n0 + f + kTN < features) to[kTN] = v1;
+    }
   }
 }
 
-template <typename T> __global__ void __launch_bounds__(kGenThreads) outer_kernel(GeneralArgs g) {
-  __shared__ float a[kTK][kTM + 1];
-  __shared__ __align__(16) float b[kTK][kTN + 4];
-  const hc_expert_mlp_t& p = g.p;
-  pdl_wait();
-  pdl_trigger();
-  const ExpertTile t = expert_tile(g.lists.bounds, p.num_experts, kTM, blockIdx.x);
-  if (t.rows == 0) return;
-  const T* down = static_cast<const T*>(p.down) + t.expert * p.down_expert_stride;
-  const int n0 = blockIdx.y * kTN;
-  const Thread me = my_part();
-  float acc[2][4] = {};
-  for (int k0 = 0; k0 < p.inner; k0 += kTK) {
-    for (int i = threadIdx.x; i < kTM * kTK; i += kGenThreads) {
-      const int m = i / kTK, k = i % kTK;
-      a[k][m] = m < t.rows && k0 + k < p.inner ? g.h[static_cast<int64_t>(t.first + m) * p.inner + k0 + k] : 0.0f;
-    }
-    load_weight(b, down, p.down_in_stride, p.down_out_stride, k0, n0, p.inner, p.hidden);
-    __syncthreads();
-    multiply(acc, a, b, me);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int m = me.rm + 16 * i;
-    if (m >= t.rows) continue;
-    const int64_t pair = g.lists.order[t.first + m];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (n0 + me.cn + j < p.hidden) g.o[pair * g.o_step + n0 + me.cn + j] = acc[i][j];
-  }
+template <typename T, bool kInner> cudaError_t launch_general(const GeneralArgs& g, unsigned slots, cudaStream_t s) {
+  constexpr size_t smem = sizeof(float) * kGenWarps * kAcc * 32;  // (more than the rows take)
+  const int step = kInner ? kTN : 2 * kTN, features = kInner ? g.p.inner : g.p.hidden;
+  const dim3 grid(slots, (features + step - 1) / step);
+  const auto launch = [&](auto by_input) {
+    constexpr bool kByInput = decltype(by_input)::value;
+    const cudaError_t e = ensure_smem<general_kernel<T, kInner, kByInput>>(smem);
+    return e != cudaSuccess ? e : launch_pdl(general_kernel<T, kInner, kByInput>, grid, dim3(kGenThreads), smem, s, 1, g);
+  };
+  return (kInner ? g.p.up_out_stride : g.p.down_out_stride) == 1 ? launch(std::false_type()) : launch(std::true_type());
 }
 
 // ---------------------------------------------------------------- combine --
@@ -361,9 +415,9 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
   }
   const GeneralArgs g = {a, lists, reinterpret_cast<float*>(ws + l.h), reinterpret_cast<float*>(ws + l.o), l.o_step};
   const unsigned slots = static_cast<unsigned>(expert_slots(pairs, kTM, a.num_experts));
-  e = launch_pdl(inner_kernel<T>, dim3(slots, (a.inner + kTN - 1) / kTN), dim3(kGenThreads), 0, s, 1, g);
+  e = launch_general<T, true>(g, slots, s);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(outer_kernel<T>, dim3(slots, (a.hidden + kTN - 1) / kTN), dim3(kGenThreads), 0, s, 1, g);
+  e = launch_general<T, false>(g, slots, s);
   if (e != cudaSuccess) return e;
   return launch_combine<T, false>(a, ws + l.o, l.o_step, nullptr, 0, s);
 }

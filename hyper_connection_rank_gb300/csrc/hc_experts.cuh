@@ -123,4 +123,13 @@ __device__ __forceinline__ ExpertTile expert_tile(const int32_t* bounds, int exp
   return ExpertTile{lo, first, max(0, min(rows, end - first))};
 }
 
+// The same slots for an expert's rows cut evenly: as many tiles, of no more than `rows` rows.
+__device__ __forceinline__ ExpertTile expert_tile_even(const int32_t* bounds, int experts, int rows, int slot) {
+  const ExpertTile t = expert_tile(bounds, experts, rows, slot);
+  if (t.rows == 0) return t;
+  const int begin = bounds[t.expert], n = bounds[t.expert + 1] - begin, tiles = (n + rows - 1) / rows;
+  const int each = (n + tiles - 1) / tiles, first = begin + (t.first - begin) / rows * each;
+  return ExpertTile{t.expert, first, max(0, min(each, begin + n - first))};
+}
+
 }  // namespace hc
