@@ -207,17 +207,23 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
     for (int q = 0; q < kGroups; ++q) {
       if (q < groups) {
 #pragma unroll
-        for (int r = q * kGroup; r < (q + 1) * kGroup; ++r) {
+        for (int r = q * kGroup; r < (q + 1) * kGroup; r += 2) {
 #pragma unroll
           for (int k4 = 0; k4 < kTK; k4 += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(buf + r * kTK + k4);
-            const float xs[4] = {v.x, v.y, v.z, v.w};
+            float xs[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float4 v = *reinterpret_cast<const float4*>(buf + (r + i) * kTK + k4);
+              xs[i][0] = v.x, xs[i][1] = v.y, xs[i][2] = v.z, xs[i][3] = v.w;
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-              for (int m = 0; m < 2; ++m)
+              for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[r][m][j] = fmaf(xs[k], wc[k4 + k][m][j], acc[r][m][j]);
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) acc[r + i][m][j] = fmaf(xs[i][k], wc[k4 + k][m][j], acc[r + i][m][j]);
           }
         }
       }

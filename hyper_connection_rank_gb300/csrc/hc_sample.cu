@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
 // ----------------------------------------------------------- the whole distribution --
 //
 // Where nothing is filtered, a row need not be kept, nor its largest logit known before its weights: warps read chunks of
-// 1024 logits and leave each chunk's sum in units of the power of two that its own largest weight lies above. With
+// 512 logits and leave each chunk's sum in units of the power of two that its own largest weight lies above. With
 // x c = n + i / 16 + f (c in two fp32 parts, n whole), 2^(x c) = 2^n T[i] (1 + q), T and the result in 31 bits, each weight to
 // within 2^-30 of itself (equal logits have equal weights). Chunks' sums are then shifted to the row's largest n and added,
 // and the chunk in which they pass uniform * sum is read again by one warp.
@@ -675,8 +675,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
 // Rows with anything that this does not hold for (an infinite largest logit, one above 512 log2 units in size, where c's
 // parts no longer reach, no logit at all, a temperature of 0) keep kUndecided and are the other kernel's.
 
-constexpr int kStreamThreads = 256, kStreamWarps = kStreamThreads / 32;
-constexpr int kChunk = 1024, kPerLane = kChunk / 32;
+constexpr int kStreamThreads = 256, kStreamWarps = kStreamThreads / 32, kStreamCtas = 4;  // CTAs to an SM
+constexpr int kChunk = 512, kPerLane = kChunk / 32;
 constexpr int kMaxChunks = kSampleMaxVocab / kChunk + 1;
 constexpr int64_t kStreamLeast = 1 << 20;  // logits of a call, below which one kernel is less than two
 constexpr int kUnitBits = 13;              // a chunk's largest weight is 2^43 to 2^44 units, 409600 of them below 2^63
@@ -686,41 +686,80 @@ __device__ const int kExp2Few[16] = {
     1073741824, 1121280436, 1170923762, 1222764986, 1276901417, 1333434672, 1392470869, 1454120821,
     1518500250, 1585730000, 1655936265, 1729250827, 1805811301, 1885761398, 1969251188, 2056437387};
 
+// Two floats in a register pair: one instruction for both.
+struct Two {
+  unsigned long long v;
+  __device__ __forceinline__ Two(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+  __device__ __forceinline__ explicit Two(float x) : Two(x, x) {}
+  __device__ __forceinline__ float2 get() const {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+};
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.v) : "l"(a.v), "l"(b.v));
+  return c;
+}
+
 struct Weigh {
   const int* table;  // in shared memory
   float ch, cl;
 
-  // n of a logit.
+  static constexpr float kMagic = 786432.0f;  // 1.5 2^19: a sum with it ends at multiples of 1/16, which its low bits count
+  static constexpr float kLn2 = 0.69314718f, kLn2Tail = -1.9046542e-09f, k32 = 4294967296.0f;
+  static constexpr float kMagicWhole = 12582912.0f;  // 1.5 2^23: the same at whole numbers
+
+  // n of a logit, plus a constant.
   __device__ __forceinline__ int exponent(float x) const {
-    const float p = fmaxf(__fmul_rn(x, ch), -65536.0f);
-    return (__float_as_int(p + kMagic) - kMagicBits) >> 4;
+    return __float_as_int(kMagic - fminf(__fmul_rn(x, -ch), 65536.0f)) >> 4;
   }
-  // Units of a logit's weight, the chunk's n being `top`. (Minus infinity and NaN have p = -65536, so none.)
+  // sum += units of two logits' weights, the chunk's n being `top`. (Minus infinity and NaN have x c = -65536, so none.)
+  __device__ __forceinline__ void add_units(float x0, float x1, int top, u64* sum) const {
+    const Two x(x0, x1), c(ch);
+    // all of n, k and f with the other sign: n = -x c, f = -(x c - k / 16), exact and at most 1/32
+    const float2 nn = (x * Two(-ch)).get();
+    const Two n(fminf(nn.x, 65536.0f), fminf(nn.y, 65536.0f));
+    const Two pl = fma2(x, Two(cl), fma2(x, c, n));
+    const Two kf = fma2(n, Two(-1.0f), Two(kMagic));
+    const Two f = n + (kf + Two(-kMagic));
+    const Two h = f * Two(-kLn2);
+    // 2^(x c - k / 16) - 1 = h + (-f ln2 - h) + pl ln2 (1 + h) + f^2 (...), pl what x c has below n
+    Two e = fma2(f, Two(-kLn2), f * Two(kLn2));
+    e = fma2(f, Two(-kLn2Tail), e);
+    e = fma2(fma2(pl, h, pl), Two(kLn2), e);
+    Two g = fma2(f, Two(-1.3333558e-03f), Two(9.6181291e-03f));
+    g = fma2(f, g, Two(-5.5504109e-02f));
+    g = fma2(f, g, Two(2.4022651e-01f));
+    e = fma2(f * f, g, e);
+    const float2 hi = (h * Two(k32)).get(), lo = fma2(e, Two(k32), Two(kMagicWhole)).get(), kk = kf.get();
+    one(hi.x, lo.x, kk.x, top, sum);
+    one(hi.y, lo.y, kk.y, top, sum);
+  }
   __device__ __forceinline__ u64 units(float x, int top) const {
-    const float p = fmaxf(__fmul_rn(x, ch), -65536.0f);
-    const float pl = fmaf(x, cl, fmaf(x, ch, -p));
-    const float kf = p + kMagic;
-    const int k = __float_as_int(kf) - kMagicBits;
-    const float f = p - (kf - kMagic);  // exact, at most 1/32
-    const float h = __fmul_rn(f, kLn2);
-    // 2^(f + pl) - 1 = h + (f ln2 - h) + pl ln2 (1 + h) + f^2 (...)
-    float e = fmaf(f, kLn2, -h);
-    e = fmaf(f, kLn2Tail, e);
-    e = fmaf(fmaf(pl, h, pl), kLn2, e);
-    const float g = fmaf(f, fmaf(f, fmaf(f, 1.3333558e-03f, 9.6181291e-03f), 5.5504109e-02f), 2.4022651e-01f);
-    e = fmaf(f * f, g, e);
-    const int q = __float2int_rn(h * 4294967296.0f) + __float2int_rn(e * 4294967296.0f);  // in units of 2^-32
-    const int t = table[k & 15];
-    const uint32_t m = static_cast<uint32_t>(t + __mulhi(t, q));
-    const int down = top - (k >> 4);  // at least 0
-    const uint32_t by = max((1u << kUnitBits) >> min(down, 31), 1u);
-    const uint32_t rest = down > kUnitBits ? (down < kUnitBits + 32 ? m >> (down - kUnitBits) : 0u) : m;
-    return static_cast<u64>(rest) * by;
+    u64 sum = 0;
+    add_units(x, -INFINITY, top, &sum);
+    return sum;
   }
 
-  static constexpr float kMagic = 786432.0f;  // 1.5 2^19: a sum with it ends at multiples of 1/16
-  static constexpr int kMagicBits = 0x49400000;
-  static constexpr float kLn2 = 0.69314718f, kLn2Tail = -1.9046542e-09f;
+  __device__ __forceinline__ void one(float hi, float lo, float kf, int top, u64* sum) const {
+    const int q = __float2int_rn(hi) + (__float_as_int(lo) - 0x4b400000);  // 2^f - 1 in units of 2^-32
+    const int bits = __float_as_int(kf), t = table[bits & 15];
+    const uint32_t m = static_cast<uint32_t>(t + __mulhi(t, q));
+    const int past = top - (bits >> 4) - kUnitBits;
+    uint32_t rest, by;
+    asm("shr.u32 %0, %1, %2;" : "=r"(rest) : "r"(m), "r"(max(past, 0)));  // (0 from 32 on)
+    asm("shl.b32 %0, %1, %2;" : "=r"(by) : "r"(1), "r"(max(-past, 0)));
+    *sum += static_cast<u64>(rest) * by;
+  }
 };
 
 // kCount elements of a row of n from `at` on, minus infinity outside. Aligned: `at` is at a 16-byte boundary.
@@ -739,7 +778,7 @@ template <typename T, int kCount> __device__ __forceinline__ void load_edge(cons
   for (int j = 0; j < kCount; ++j) x[j] = at + j >= 0 && at + j < n ? Ty<T>::to_f(row[at + j]) : -INFINITY;
 }
 
-template <typename T> __global__ void __launch_bounds__(kStreamThreads, 3) stream_kernel(SampleArgs a, int ctas) {
+template <typename T> __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) stream_kernel(SampleArgs a, int ctas) {
   __shared__ u64 sums[kMaxChunks];
   __shared__ int tops[kMaxChunks];
   __shared__ int table[16];
@@ -748,9 +787,10 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, 3) strea
   __shared__ int chosen;
   constexpr int kVec = 16 / sizeof(T);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ double scale;
+  __shared__ float2 parts;  // of scale
   if (tid < 16) table[tid] = kExp2Few[tid];
   if (tid == 0) chosen = -1;
-  __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int64_t r = blockIdx.x / ctas;
@@ -761,17 +801,19 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, 3) strea
   const int chunks = (a.vocab + shift + kChunk - 1) / kChunk, each = (chunks + ctas - 1) / ctas;
   const int c0 = min(chunks, rank * each), c1 = min(chunks, c0 + each);
   const float t = a.temperatures ? a.temperatures[r] : a.temperature;
-  if (rank == 0 && tid == 0) a.tokens[r] = kUndecided;
-  const double scale = 1.4426950408889634 / static_cast<double>(t);
-  Weigh weigh = {table, static_cast<float>(scale), 0.0f};
-  weigh.cl = static_cast<float>(scale - static_cast<double>(weigh.ch));
+  if (tid == 0) {  // (fp64 is slow enough here that all threads' would show)
+    if (rank == 0) a.tokens[r] = kUndecided;
+    scale = 1.4426950408889634 / static_cast<double>(t);
+    parts = make_float2(static_cast<float>(scale), static_cast<float>(scale - static_cast<double>(static_cast<float>(scale))));
+  }
+  __syncthreads();
+  const Weigh weigh = {table, parts.x, parts.y};
   if (!(t > 0.0f) || !(weigh.ch < 1e30f) || !(weigh.ch > 1e-30f)) return;  // (all CTAs of the row)
   const auto chunk_top = [&](const float* x) {
     float top = x[0];
 #pragma unroll
     for (int i = 1; i < kPerLane; ++i) top = fmaxf(top, x[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(top));
     return top;
   };
   float most = -INFINITY;  // of the chunks that this warp has seen
@@ -790,8 +832,10 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, 3) strea
     const int n = weigh.exponent(top);
     u64 sum = 0;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) sum += weigh.units(x[i], n);
-    sum = warp_sum_u64(sum);
+    for (int i = 0; i < kPerLane; i += 2) weigh.add_units(x[i], x[i + 1], n, &sum);
+    // (below 2^49 a lane)
+    const uint32_t high = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(sum >> 27));
+    sum = (static_cast<u64>(high) << 27) + __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(sum) & 0x7ffffffu);
     if (lane == 0) {
       sums[k - c0] = sum;
       tops[k - c0] = n;
@@ -859,7 +903,7 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, 3) strea
   else load_edge<T, kPerLane>(row, at, a.vocab, x);
   u64 part = 0;
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) part += weigh.units(x[i], n);
+  for (int i = 0; i < kPerLane; i += 2) weigh.add_units(x[i], x[i + 1], n, &part);
   u64 run = warp_scan_u64(part) - part;
   // (its sums are shifted like the chunk's, so that the last one is the chunk's)
   u64 from = chosen_before + down(run, n);
@@ -870,7 +914,7 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, 3) strea
     const u64 to = chosen_before + down(run, n);
     if (from < want && want <= to) {
       a.tokens[r] = at + i;
-      if (a.logprobs) a.logprobs[r] = log_share(down(w, n), static_cast<double>(x[i]) * scale + (43 - top), total);
+      if (a.logprobs) a.logprobs[r] = log_share(down(w, n), static_cast<double>(x[i]) * scale + (43 - (top - weigh.exponent(0.0f))), total);
     }
     from = to;
   }
@@ -891,7 +935,8 @@ cudaError_t launch_token_sample(const hc_token_sample_t& p, int num_sms, cudaStr
                      p.min_ps == nullptr && !(p.min_p > 0.0f);
   if (whole && p.rows * p.vocab >= kStreamLeast) {
     int split = 1;
-    while (split < kMaxCluster && p.rows * split * 2 <= 2 * num_sms && p.vocab / (2 * split) >= 4 * kChunk) split *= 2;
+    while (split < kMaxCluster && p.rows * split <= 2 * kStreamCtas * num_sms && p.vocab / (2 * split) >= 2 * kStreamWarps * kChunk)
+      split *= 2;
     const dim3 grid(static_cast<unsigned>(p.rows * split)), block(kStreamThreads);
     cudaError_t e;
     if (p.dtype == HC_F32) e = launch_pdl(stream_kernel<float>, grid, block, 0, s, split, a, split);
