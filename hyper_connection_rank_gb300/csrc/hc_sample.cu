@@ -77,8 +77,17 @@ struct SampleArgs {
 };
 constexpr int kUndecided = -2;  // stands in tokens until a row's second kernel has run
 
+// What a row's parameters come to.
+struct Params {
+  u64 least;        // units of the least weight that min_p leaves
+  float t, p, u;
+  float ch, cl;     // log2(e) / t in two parts
+  int k, step;      // step: of the histogram, past which min_p leaves nothing
+};
+
 struct Shared {
   u64 table[64];
+  Params params;
   u64 exchange[2][kMaxCluster];
   u64 red[kWarps];
   u64 border[4];  // where a target falls: bin, value before it, value in it
@@ -150,23 +159,70 @@ __device__ __forceinline__ u64 reach(float f, u64 v) {
   return n + (whole ? 0 : 1);
 }
 
-// log(w / total) by what the others have, so that a token with nearly all of the sum keeps its digits; or, of a smaller one,
-// from the logarithm of its weight in units (log2_w), of which w may have few digits left.
+// log(w / total) by what the others have, so that a token with nearly all of the sum keeps its digits; or, of a weight of
+// few units (below kPlainLog), from the logarithm of it (log2_w).
+constexpr u64 kPlainLog = 1ull << 26;
 __device__ __forceinline__ float log_share(u64 w, double log2_w, u64 total) {
   if (w >= total / 2) return -log1pf(static_cast<float>(total - w) / static_cast<float>(w));
+  if (w >= kPlainLog) return logf(static_cast<float>(w) / static_cast<float>(total));
   const int e = 63 - __clzll(total);
   const float rest = log2f(static_cast<float>(total) * __uint_as_float((127u - e) << 23));  // total = 2^(e + rest)
   return 0.69314718f * (static_cast<float>(log2_w - e) - rest);
 }
 
-// One row, as a thread sees it.
-struct Row {
+// The weights of a row.
+struct Scale {
+  const u64* table;  // in shared memory
+  float m, ch, cl;   // largest logit; log2(e) / temperature in two parts
+
+  // The step of the first histogram, never falling as x falls.
+  __device__ __forceinline__ int step(float x) const {
+    return x == m ? 0 : min(kBins - 1, static_cast<int>((m - x) * ch * (kBins / kRange)));
+  }
+
+  __device__ __forceinline__ u64 weight(float x) const {
+    if (x == m) return kOne;
+    const float d = __fsub_rn(m, x), b = __fsub_rn(d, m);
+    const float dl = __fsub_rn(__fsub_rn(m, __fsub_rn(d, b)), __fadd_rn(x, b));
+    const float y = __fmul_rn(d, ch);
+    if (!(y < kRange)) return 0;
+    const float yl = fmaf(d, ch, -y) + fmaf(d, cl, dl * ch);
+    const int j = __float2int_rn(y * 64.0f);
+    const float f = fmaf(static_cast<float>(j), -0.015625f, y);  // exact, at most 1/128
+    const float kLn2 = 0.69314718f, kLn2Tail = -1.9046542e-09f;
+    const float h = __fmul_rn(f, kLn2);
+    const float l = fmaf(f, kLn2, -h) + fmaf(f, kLn2Tail, yl * kLn2);
+    // e^-(h + l) - 1 = -h + (h^2 / 2 - h^3 / 6 + h^4 / 24 - l (1 - h))
+    const float c = fmaf(__fmul_rn(h, h), fmaf(h, fmaf(h, 0.041666668f, -0.16666667f), 0.5f), fmaf(h, l, -l));
+    const int q = __float2int_rn(h * -274877906944.0f) + __float2int_rn(c * 274877906944.0f);  // in units of 2^-38
+    const u64 t = table[j & 63];
+    const long long w =
+        static_cast<long long>(t) + ((static_cast<long long>(static_cast<int>(t >> 13)) * q) >> 25);
+    return static_cast<u64>(w) >> (j >> 6);
+  }
+
+  // The logarithm of the weight of a token of row r.
+  __device__ __forceinline__ double log2_units(const SampleArgs& a, int64_t r, int token) const {
+    const int64_t at = r * a.stride + token;
+    const float x = a.dtype == HC_F32   ? static_cast<const float*>(a.logits)[at]
+                    : a.dtype == HC_F16 ? __half2float(static_cast<const __half*>(a.logits)[at])
+                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at]);
+    if (x == m) return kOneBits;
+    return kOneBits + (static_cast<double>(x) - static_cast<double>(m)) * (static_cast<double>(ch) + static_cast<double>(cl));
+  }
+};
+
+// One row, as a thread of the exact kernel sees it.
+struct Row : Scale {
   Shared& sh;
   const float* xs;       // this CTA's slice
   int n, base;           // its elements, and the first one's index in the row
   int rank, ctas, turn;  // turn: of the exchanges
-  float m, ch, cl;       // largest logit; log2(e) / temperature in two parts
   uint32_t cut_key, cut_index;  // what stays: keys above, and equal ones up to this index
+
+  __device__ __forceinline__ Row(Shared& shared, const float* slice, int count, int first, int cta, int of, int at)
+      : Scale{shared.table, 0.0f, 0.0f, 0.0f}, sh(shared), xs(slice), n(count), base(first), rank(cta), ctas(of), turn(at),
+        cut_key(0u), cut_index(0xffffffffu) {}
 
   // Every CTA's value, in the order of the ranks, in exchange[turn].
   __device__ __forceinline__ const u64* gather(u64 v) {
@@ -197,42 +253,6 @@ struct Row {
   __device__ __forceinline__ bool stays(float x, int index) const {
     const uint32_t k = key_of(x);
     return k > cut_key || (k == cut_key && static_cast<uint32_t>(index) <= cut_index);
-  }
-
-  // The step of the first histogram, never falling as x falls.
-  __device__ __forceinline__ int step(float x) const {
-    return x == m ? 0 : min(kBins - 1, static_cast<int>((m - x) * ch * (kBins / kRange)));
-  }
-
-  __device__ __forceinline__ u64 weight(float x) const {
-    if (x == m) return kOne;
-    const float d = __fsub_rn(m, x), b = __fsub_rn(d, m);
-    const float dl = __fsub_rn(__fsub_rn(m, __fsub_rn(d, b)), __fadd_rn(x, b));
-    const float y = __fmul_rn(d, ch);
-    if (!(y < kRange)) return 0;
-    const float yl = fmaf(d, ch, -y) + fmaf(d, cl, dl * ch);
-    const int j = __float2int_rn(y * 64.0f);
-    const float f = fmaf(static_cast<float>(j), -0.015625f, y);  // exact, at most 1/128
-    const float kLn2 = 0.69314718f, kLn2Tail = -1.9046542e-09f;
-    const float h = __fmul_rn(f, kLn2);
-    const float l = fmaf(f, kLn2, -h) + fmaf(f, kLn2Tail, yl * kLn2);
-    // e^-(h + l) - 1 = -h + (h^2 / 2 - h^3 / 6 + h^4 / 24 - l (1 - h))
-    const float c = fmaf(__fmul_rn(h, h), fmaf(h, fmaf(h, 0.041666668f, -0.16666667f), 0.5f), fmaf(h, l, -l));
-    const int q = __float2int_rn(h * -274877906944.0f) + __float2int_rn(c * 274877906944.0f);  // in units of 2^-38
-    const u64 t = sh.table[j & 63];
-    const long long w =
-        static_cast<long long>(t) + ((static_cast<long long>(static_cast<int>(t >> 13)) * q) >> 25);
-    return static_cast<u64>(w) >> (j >> 6);
-  }
-
-  // The logarithm of the weight of a token of row r.
-  __device__ __forceinline__ double log2_units(const SampleArgs& a, int64_t r, int token) const {
-    const int64_t at = r * a.stride + token;
-    const float x = a.dtype == HC_F32   ? static_cast<const float*>(a.logits)[at]
-                    : a.dtype == HC_F16 ? __half2float(static_cast<const __half*>(a.logits)[at])
-                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at]);
-    if (x == m) return kOneBits;
-    return kOneBits + (static_cast<double>(x) - static_cast<double>(m)) * (static_cast<double>(ch) + static_cast<double>(cl));
   }
 
   __device__ __forceinline__ void add(int bin, u64 v) {
@@ -531,15 +551,36 @@ __device__ __forceinline__ void finish_list(const SampleArgs& a, const Row& row,
     if (before < want && want <= before + w[j]) {
       a.tokens[r] = static_cast<int>(list[threadIdx.x * kEach + j] >> 32);
       if (a.logprobs)
-        a.logprobs[r] = log_share(w[j], row.log2_units(a, r, static_cast<int>(list[threadIdx.x * kEach + j] >> 32)), all);
+        a.logprobs[r] = log_share(w[j], w[j] < kPlainLog ? row.log2_units(a, r, static_cast<int>(list[threadIdx.x * kEach + j] >> 32)) : 0.0, all);
     }
     before += w[j];
   }
 }
 
+__device__ __forceinline__ void row_params(const SampleArgs& a, int64_t r, Params* to) {
+  Params v;
+  v.t = a.temperatures ? a.temperatures[r] : a.temperature;
+  v.p = a.top_ps ? a.top_ps[r] : a.top_p;
+  v.k = a.top_ks ? a.top_ks[r] : a.top_k;
+  const float u = a.uniform[r], min_p = a.min_ps ? a.min_ps[r] : a.min_p;
+  v.u = u > 0.0f ? fminf(u, 1.0f) : 0.0f;
+  const float kLog2e = 1.44269502f, kLog2eTail = 1.9259630e-08f;
+  v.ch = __fdiv_rn(kLog2e, v.t);
+  v.cl = __fdiv_rn(fmaf(-v.ch, v.t, kLog2e) + kLog2eTail, v.t);  // (the remainder of the quotient is exact)
+  if (!(fabsf(v.ch) < 1e30f) || !(fabsf(v.cl) < 1e30f)) v.cl = 0.0f;
+  v.least = 1;
+  v.step = kBins;
+  if (min_p > 0.0f) {
+    v.least = max(__float2ull_ru(fminf(min_p, 1.0f) * static_cast<float>(kOne)), 1ull);  // (the product is exact)
+    v.step = min(kBins, static_cast<int>((0.01f - log2f(fminf(min_p, 1.0f))) * (kBins / kRange)) + 1);
+  }
+  *to = v;
+}
+
 __device__ __forceinline__ void sample_row(const SampleArgs& a, Shared& sh, float* xs, int64_t r, int rank, int ctas, int* turn) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int base = rank * a.slice, n = max(0, min(a.slice, a.vocab - base));
+  if (tid == kThreads - 1) row_params(a, r, &sh.params);
   u64 best;
   if (a.dtype == HC_F32)
     best = load_slice(static_cast<const float*>(a.logits) + r * a.stride, base, n, xs);
@@ -547,16 +588,13 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, Shared& sh, floa
     best = load_slice(static_cast<const __half*>(a.logits) + r * a.stride, base, n, xs);
   else
     best = load_slice(static_cast<const __nv_bfloat16*>(a.logits) + r * a.stride, base, n, xs);
-  const float t = a.temperatures ? a.temperatures[r] : a.temperature;
-  const float p = a.top_ps ? a.top_ps[r] : a.top_p;
-  const float min_p = a.min_ps ? a.min_ps[r] : a.min_p;
-  const int k = a.top_ks ? a.top_ks[r] : a.top_k;
-  float u = a.uniform[r];
-  u = u > 0.0f ? fminf(u, 1.0f) : 0.0f;
-
-  // (every CTA of the cluster has begun, and its histogram is empty, before anything is stored into its shared memory)
+  // (every CTA of the cluster has begun, its histogram is empty and its parameters are there, before anything is stored into
+  // its shared memory)
   cluster_sync_all();
-  Row row = {sh, xs, n, base, rank, ctas, *turn, 0.0f, 0.0f, 0.0f, 0u, 0xffffffffu};
+  const float t = sh.params.t, p = sh.params.p, u = sh.params.u;
+  const int k = sh.params.k;
+  const u64 least = sh.params.least;
+  Row row(sh, xs, n, base, rank, ctas, *turn);
   best = row.cluster_max(best);
   *turn = row.turn;
   row.m = value_of(static_cast<uint32_t>(best >> 32));
@@ -569,11 +607,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, Shared& sh, floa
     }
     return;  // (nothing is on its way to another CTA's memory)
   }
-  const double c = 1.4426950408889634 / static_cast<double>(t);
-  row.ch = static_cast<float>(c);
-  row.cl = isinf(row.ch) ? 0.0f : static_cast<float>(c - static_cast<double>(row.ch));
-  const u64 least =
-      min_p > 0.0f ? static_cast<u64>(ceil(static_cast<double>(fminf(min_p, 1.0f)) * static_cast<double>(kOne))) : 1;
+  row.ch = sh.params.ch;
+  row.cl = sh.params.cl;
   const bool cut_k = k > 0 && k < a.vocab;
   u64 total = 0;
   int listed = -1;
@@ -639,7 +674,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, Shared& sh, floa
     if (hit != 0) {
       if (lane == __ffs(hit) - 1) {
         a.tokens[r] = base + r0 + i;
-        if (a.logprobs) a.logprobs[r] = log_share(w, row.log2_units(a, r, base + r0 + i), total);
+        if (a.logprobs) a.logprobs[r] = log_share(w, w < kPlainLog ? row.log2_units(a, r, base + r0 + i) : 0.0, total);
       }
       return;
     }
@@ -675,7 +710,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
 // Rows with anything that this does not hold for (an infinite largest logit, one above 512 log2 units in size, where c's
 // parts no longer reach, no logit at all, a temperature of 0) keep kUndecided and are the other kernel's.
 
-constexpr int kStreamThreads = 256, kStreamWarps = kStreamThreads / 32, kStreamCtas = 4;  // CTAs to an SM
+constexpr int kStreamThreads = 128, kStreamWarps = kStreamThreads / 32, kStreamCtas = 8;  // CTAs to an SM
 constexpr int kChunk = 512, kPerLane = kChunk / 32;
 constexpr int kMaxChunks = kSampleMaxVocab / kChunk + 1;
 constexpr int64_t kStreamLeast = 1 << 20;  // logits of a call, below which one kernel is less than two
@@ -720,14 +755,14 @@ struct Weigh {
 
   // n of a logit, plus a constant.
   __device__ __forceinline__ int exponent(float x) const {
-    return __float_as_int(kMagic - fminf(__fmul_rn(x, -ch), 65536.0f)) >> 4;
+    return __float_as_int(__fadd_rn(__fmul_rn(x, ch), kMagic)) >> 4;
   }
-  // sum += units of two logits' weights, the chunk's n being `top`. (Minus infinity and NaN have x c = -65536, so none.)
+  // sum += units of two logits' weights, the chunk's n being `top`. (Of minus infinity and of logits far below, kf is so far
+  // from kMagic that nothing is left by the shift to the right, of NaN nothing by the one to the left.)
   __device__ __forceinline__ void add_units(float x0, float x1, int top, u64* sum) const {
     const Two x(x0, x1), c(ch);
     // all of n, k and f with the other sign: n = -x c, f = -(x c - k / 16), exact and at most 1/32
-    const float2 nn = (x * Two(-ch)).get();
-    const Two n(fminf(nn.x, 65536.0f), fminf(nn.y, 65536.0f));
+    const Two n = x * Two(-ch);
     const Two pl = fma2(x, Two(cl), fma2(x, c, n));
     const Two kf = fma2(n, Two(-1.0f), Two(kMagic));
     const Two f = n + (kf + Two(-kMagic));
@@ -920,6 +955,215 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, kStreamC
   }
 }
 
+// ------------------------------------------------------------------ few candidates --
+//
+// Most rows that filter come down to a few tokens, and for those neither a copy of the row nor a histogram of it is needed.
+// Each of a CTA's 1024 threads keeps the largest of its logits. The k-th largest logit is not below the k-th largest of the
+// threads' (which a histogram of those finds, to within a step), and min_p says how far down it goes; threads whose largest
+// reaches that far look through theirs again and list what does. For top_p without top_k the 128-th takes the place of the
+// k-th, and it has to turn out that the listed weights come to p of all. One CTA finishes the row: with no more than 512
+// candidates, each looks at all others. Rows with more keep kUndecided.
+
+constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32;
+constexpr int kPicked = 512;   // candidates at most
+constexpr int kMostK = 400;    // a larger top_k is not tried
+constexpr int kTryP = 128;
+
+struct PickShared {
+  u64 table[64];
+  Params params;
+  u64 tops[kMaxCluster], sums[kMaxCluster];
+  u64 red[kPickWarps];
+  uint32_t hist[kBins];
+  int border;
+  uint32_t listed;
+  u64 list[kPicked], weights[kPicked];
+};
+
+__device__ __forceinline__ uint32_t add_cluster(uint32_t addr, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
+  return old;
+}
+__device__ __forceinline__ void st_cluster32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ u64 pick_sum(PickShared& sh, u64 v) {
+  v = warp_sum_u64(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh.red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum_u64(sh.red[threadIdx.x & 31]);
+}
+
+template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_kernel(SampleArgs a, int ctas) {
+  __shared__ PickShared sh;
+  constexpr int kVec = 16 / sizeof(T), kAhead = 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cluster_arrive_relaxed();
+  const int64_t r = blockIdx.x / ctas;
+  const int rank = static_cast<int>(blockIdx.x % ctas);
+  for (int i = tid; i < kBins; i += kPickThreads) sh.hist[i] = 0;
+  if (tid < 64) sh.table[tid] = kExp2[tid];
+  if (tid == 64) sh.listed = 0;
+  if (tid == 65) sh.border = -1;
+  pdl_wait();
+  pdl_trigger();
+  if (tid == kPickThreads - 1) row_params(a, r, &sh.params);
+  const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+  // vectors begin at 16-byte boundaries, the first one up to 16 bytes before the row
+  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const int vectors = (a.vocab + shift + kVec - 1) / kVec, each = (vectors + ctas - 1) / ctas;
+  const int v0 = min(vectors, rank * each), v1 = min(vectors, v0 + each);
+  // f(index, logit) for all of this thread's elements, indexes rising
+  const auto visit = [&](auto f) {
+    for (int v = v0 + tid; v < v1; v += kAhead * kPickThreads) {
+      const int at = v * kVec - shift, far = at + (kAhead - 1) * kPickThreads * kVec;
+      if (at >= 0 && v + (kAhead - 1) * kPickThreads < v1 && far + kVec <= a.vocab) {
+        float x[kAhead][kVec];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load_inside<T, kVec>(row, at + i * kPickThreads * kVec, x[i]);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) f(at + i * kPickThreads * kVec + j, x[i][j]);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kAhead && v + i * kPickThreads < v1; ++i) {
+          float x[kVec];
+          load_edge<T, kVec>(row, at + i * kPickThreads * kVec, a.vocab, x);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) f(at + i * kPickThreads * kVec + j, x[j]);
+        }
+      }
+    }
+  };
+  float top = -INFINITY;
+  int arg = -1;
+  visit([&](int i, float x) {
+    if (x > top) {  // (not for NaN)
+      top = x;
+      arg = i;
+    }
+  });
+  u64 best = arg < 0 ? 0 : static_cast<u64>(key_of(top)) << 32 | (0xffffffffu - static_cast<uint32_t>(arg));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if (lane == 0) sh.red[warp] = best;
+  __syncthreads();
+  best = sh.red[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+  cluster_wait();  // (every CTA has begun)
+  if (tid < ctas) st_cluster(mapa_shared(smem_addr(&sh.tops[rank]), tid), best);
+  cluster_sync_all();
+  for (int i = 0; i < ctas; ++i) best = max(best, sh.tops[i]);
+  const Params& p = sh.params;
+  const bool none = best == 0;
+  const bool cut_k = p.k > 0 && p.k < a.vocab, cut_p = p.p < 1.0f, cut_m = p.step < kBins && !cut_p;
+  const bool one = none || !(p.t > 0.0f) || p.k == 1 || p.p <= 0.0f;
+  if (one || !(cut_k || cut_p || cut_m) || (cut_k && p.k > kMostK && !cut_m)) {
+    if (rank == 0 && tid == 0) {
+      a.tokens[r] = none ? -1 : one ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : kUndecided;
+      if (a.logprobs && one) a.logprobs[r] = none ? -INFINITY : 0.0f;
+    }
+    return;
+  }
+  const Scale scale = {sh.table, value_of(static_cast<uint32_t>(best >> 32)), p.ch, p.cl};
+  const int mine = arg < 0 ? kBins : scale.step(top);
+  int bin = cut_m ? p.step : kBins;
+  const uint32_t some = cut_k ? p.k : kTryP;
+  if ((cut_k || cut_p) && some <= kMostK) {
+    // the first CTA has the histogram
+    if (arg >= 0) add_cluster(mapa_shared(smem_addr(&sh.hist[mine]), 0), 1u);
+    cluster_sync_all();
+    if (rank == 0) {
+      const uint32_t n0 = sh.hist[2 * tid], n1 = sh.hist[2 * tid + 1];
+      const u64 upto = warp_scan_u64(n0 + n1);
+      if (lane == 31) sh.red[warp] = upto;
+      __syncthreads();
+      uint32_t before = static_cast<uint32_t>(upto) - (n0 + n1);
+      for (int w = 0; w < warp; ++w) before += static_cast<uint32_t>(sh.red[w]);
+      const int at = before < some && some <= before + n0 ? 2 * tid : before + n0 < some && some <= before + n0 + n1 ? 2 * tid + 1 : -1;
+      if (at >= 0)
+        for (int i = 0; i < ctas; ++i) st_cluster32(mapa_shared(smem_addr(&sh.border), i), static_cast<uint32_t>(at));
+    }
+    cluster_sync_all();
+    // (fewer threads than that have a logit: all steps, unless min_p has a say)
+    bin = min(bin, sh.border < 0 ? kBins : sh.border);
+  }
+  if (cut_p && !cut_k) {
+    u64 sum = 0;
+    visit([&](int, float x) { sum += scale.weight(x); });
+    sum = pick_sum(sh, sum);
+    if (tid == 0) st_cluster(mapa_shared(smem_addr(&sh.sums[rank]), 0), sum);
+  }
+  if (mine <= bin) {
+    const uint32_t count = mapa_shared(smem_addr(&sh.listed), 0), list = mapa_shared(smem_addr(sh.list), 0);
+    visit([&](int i, float x) {
+      if (x > -INFINITY && scale.step(x) <= bin) {
+        const uint32_t at = add_cluster(count, 1u);
+        if (at < kPicked) st_cluster(list + 8 * at, static_cast<u64>(~key_of(x)) << 32 | static_cast<uint32_t>(i));
+      }
+    });
+  }
+  cluster_sync_all();
+  if (rank != 0) return;
+  const int count = static_cast<int>(sh.listed);
+  if (count > kPicked) {
+    if (tid == 0) a.tokens[r] = kUndecided;
+    return;
+  }
+  // in order, the first k stay, of those the ones before which less than p of the sum lies, of those the ones not below least
+  const bool have = tid < count;
+  const u64 me = have ? sh.list[tid] : 0;
+  u64 w = have ? scale.weight(value_of(~static_cast<uint32_t>(me >> 32))) : 0;
+  if (have) sh.weights[tid] = w;
+  const u64 listed = pick_sum(sh, w);
+  u64 before = 0;
+  uint32_t place = 0;
+  if (have) {
+#pragma unroll 4
+    for (int j = 0; j < count; ++j)
+      if (sh.list[j] < me) {
+        before += sh.weights[j];
+        ++place;
+      }
+  }
+  u64 goal = ~0ull;
+  if (cut_k && place >= p.k) w = 0;
+  if (cut_p) {
+    u64 total = 0;
+    if (cut_k) {
+      total = pick_sum(sh, w);
+    } else {
+      for (int i = 0; i < ctas; ++i) total += sh.sums[i];
+    }
+    goal = reach(p.p, total);
+    if (!cut_k && listed < goal) {  // (the last one that stays is not among them)
+      if (tid == 0) a.tokens[r] = kUndecided;
+      return;
+    }
+  }
+  if (before >= goal || w < p.least) w = 0;
+  const u64 all = pick_sum(sh, w);  // (with barriers, behind which all have read the weights)
+  if (have) sh.weights[tid] = w;
+  __syncthreads();
+  if (w == 0) return;
+  // in the order of the index, the token
+  const u64 want = min(all, part_of(p.u, all) + 1);
+  before = 0;
+#pragma unroll 4
+  for (int j = 0; j < count; ++j)
+    if (static_cast<uint32_t>(sh.list[j]) < static_cast<uint32_t>(me)) before += sh.weights[j];
+  if (before < want && want <= before + w) {
+    const int token = static_cast<int>(static_cast<uint32_t>(me));
+    a.tokens[r] = token;
+    if (a.logprobs) a.logprobs[r] = log_share(w, w < kPlainLog ? scale.log2_units(a, r, token) : 0.0, all);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_token_sample(const hc_token_sample_t& p, int num_sms, cudaStream_t s) {
@@ -935,7 +1179,8 @@ cudaError_t launch_token_sample(const hc_token_sample_t& p, int num_sms, cudaStr
                      p.min_ps == nullptr && !(p.min_p > 0.0f);
   if (whole && p.rows * p.vocab >= kStreamLeast) {
     int split = 1;
-    while (split < kMaxCluster && p.rows * split <= 2 * kStreamCtas * num_sms && p.vocab / (2 * split) >= 2 * kStreamWarps * kChunk)
+    // (all at once, since the CTAs of a row wait for one another)
+    while (split < kMaxCluster && p.rows * split * 2 <= kStreamCtas * num_sms && p.vocab / (2 * split) >= 4 * kStreamWarps * kChunk)
       split *= 2;
     const dim3 grid(static_cast<unsigned>(p.rows * split)), block(kStreamThreads);
     cudaError_t e;
@@ -943,6 +1188,17 @@ cudaError_t launch_token_sample(const hc_token_sample_t& p, int num_sms, cudaStr
     else if (p.dtype == HC_F16) e = launch_pdl(stream_kernel<__half>, grid, block, 0, s, split, a, split);
     else e = launch_pdl(stream_kernel<__nv_bfloat16>, grid, block, 0, s, split, a, split);
     if (e != cudaSuccess) return e;
+  } else if (!whole) {
+    int split = 1;
+    while (split < kMaxCluster && p.rows * split * 2 <= num_sms && p.vocab / (2 * split) >= kPickThreads * 8) split *= 2;
+    const dim3 grid(static_cast<unsigned>(p.rows * split)), block(kPickThreads);
+    cudaError_t e;
+    if (p.dtype == HC_F32) e = launch_pdl(pick_kernel<float>, grid, block, 0, s, split, a, split);
+    else if (p.dtype == HC_F16) e = launch_pdl(pick_kernel<__half>, grid, block, 0, s, split, a, split);
+    else e = launch_pdl(pick_kernel<__nv_bfloat16>, grid, block, 0, s, split, a, split);
+    if (e != cudaSuccess) return e;
+  }
+  if (!whole || p.rows * p.vocab >= kStreamLeast) {  // what those have left
     a.undecided = true;
     clusters = std::min<int64_t>(p.rows, std::max(1, num_sms / ctas));
   }
