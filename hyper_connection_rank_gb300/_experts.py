@@ -36,7 +36,7 @@ def _rows(name, t, dtype, device):
 
 def _dense(name, t, shape, dtype, device):
     """The address of a contiguous tensor of this shape."""
-    if t.dtype is not dtype or t.get_device() != device or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor of shape {shape} and dtype {dtype} on device {device}")
     return t.data_ptr()
 
@@ -142,6 +142,11 @@ def expert_mlp(x, gate_w, up_w, down_w, experts, weights, *, out=None, workspace
     return out
 
 
+def _choice(name, v, rows, dtype, device):
+    """(address, number) of a parameter that is a tensor (rows,) or a number."""
+    return (_dense(name, v, (rows,), dtype, device), 0) if isinstance(v, torch.Tensor) else (0, v)
+
+
 def token_sample(logits, uniform, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, return_logprob=False, stream=None):
     """Draw every row's next token (hc_token_sample). logits: (rows, vocab), float32, float16 or bfloat16, any row stride;
     uniform: (rows,) float32 random numbers in [0, 1). temperature, top_p, min_p (float32) and top_k (int32): a number for all
@@ -154,16 +159,13 @@ def token_sample(logits, uniform, *, temperature=1.0, top_k=0, top_p=1.0, min_p=
                           return_logprob=return_logprob)
     code, device = _dtype_code(logits), _device(logits)
     rows, vocab, step = _rows("logits", logits, logits.dtype, device)
-    at, number = {}, {}
-    for name, v, dtype in (("temperature", temperature, torch.float32), ("top_p", top_p, torch.float32),
-                           ("min_p", min_p, torch.float32), ("top_k", top_k, torch.int32)):
-        tensor = isinstance(v, torch.Tensor)
-        at[name] = _dense(name, v, (rows,), dtype, device) if tensor else 0
-        number[name] = 0 if tensor else v
+    t_at, t = _choice("temperature", temperature, rows, torch.float32, device)
+    k_at, k = _choice("top_k", top_k, rows, torch.int32, device)
+    p_at, p = _choice("top_p", top_p, rows, torch.float32, device)
+    m_at, m = _choice("min_p", min_p, rows, torch.float32, device)
     tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
     logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device) if return_logprob else None
-    args = _SAMPLE.pack(logits.data_ptr(), _dense("uniform", uniform, (rows,), torch.float32, device), at["temperature"],
-                        at["top_p"], at["min_p"], at["top_k"], tokens.data_ptr(), logprobs.data_ptr() if return_logprob else 0,
-                        rows, step, vocab, number["top_k"], number["temperature"], number["top_p"], number["min_p"], code)
+    args = _SAMPLE.pack(logits.data_ptr(), _dense("uniform", uniform, (rows,), torch.float32, device), t_at, p_at, m_at, k_at,
+                        tokens.data_ptr(), logprobs.data_ptr() if return_logprob else 0, rows, step, vocab, k, t, p, m, code)
     _launch(device, lib().hc_token_sample, args)
     return (tokens, logprobs) if return_logprob else tokens

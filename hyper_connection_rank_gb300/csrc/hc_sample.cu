@@ -1017,36 +1017,41 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
   const int vectors = (a.vocab + shift + kVec - 1) / kVec, each = (vectors + ctas - 1) / ctas;
   const int v0 = min(vectors, rank * each), v1 = min(vectors, v0 + each);
   // f(index, logit) for all of this thread's elements, indexes rising
+  const auto one_vector = [&](int v, auto f) {
+    const int at = v * kVec - shift;
+    float x[kVec];
+    if (at >= 0 && at + kVec <= a.vocab) load_inside<T, kVec>(row, at, x);
+    else load_edge<T, kVec>(row, at, a.vocab, x);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) f(at + j, x[j]);
+  };
   const auto visit = [&](auto f) {
-    for (int v = v0 + tid; v < v1; v += kAhead * kPickThreads) {
-      const int at = v * kVec - shift, far = at + (kAhead - 1) * kPickThreads * kVec;
-      if (at >= 0 && v + (kAhead - 1) * kPickThreads < v1 && far + kVec <= a.vocab) {
-        float x[kAhead][kVec];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) load_inside<T, kVec>(row, at + i * kPickThreads * kVec, x[i]);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) f(at + i * kPickThreads * kVec + j, x[i][j]);
-      } else {
 #pragma unroll 1
-        for (int i = 0; i < kAhead && v + i * kPickThreads < v1; ++i) {
-          float x[kVec];
-          load_edge<T, kVec>(row, at + i * kPickThreads * kVec, a.vocab, x);
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) f(at + i * kPickThreads * kVec + j, x[j]);
-        }
-      }
-    }
+    for (int v = v0 + tid; v < v1; v += kPickThreads) one_vector(v, f);
   };
   float top = -INFINITY;
   int arg = -1;
-  visit([&](int i, float x) {
+  const auto look = [&](int i, float x) {
     if (x > top) {  // (not for NaN)
       top = x;
       arg = i;
     }
-  });
+  };
+  for (int v = v0 + tid; v < v1; v += kAhead * kPickThreads) {
+    const int at = v * kVec - shift;
+    if (at >= 0 && v + (kAhead - 1) * kPickThreads < v1 && at + ((kAhead - 1) * kPickThreads + 1) * kVec <= a.vocab) {
+      float x[kAhead][kVec];  // (all loads before any use)
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) load_inside<T, kVec>(row, at + i * kPickThreads * kVec, x[i]);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) look(at + i * kPickThreads * kVec + j, x[i][j]);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kAhead && v + i * kPickThreads < v1; ++i) one_vector(v + i * kPickThreads, look);
+    }
+  }
   u64 best = arg < 0 ? 0 : static_cast<u64>(key_of(top)) << 32 | (0xffffffffu - static_cast<uint32_t>(arg));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
