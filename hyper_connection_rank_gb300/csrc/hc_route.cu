@@ -91,106 +91,126 @@ template <typename F> __device__ __forceinline__ F warp_total(F v) {
   return v;
 }
 
-// How far an fp32 score can be off. Softmax: expf is within 2 ulp, x - m rounds once (an error of |d| 2^-24 on exp(d),
-// which is below 2^-25 whatever d), the sum adds VPL + 5 roundings and its terms' errors, the quotient 2 more.
-// Sigmoid: expf's 2 ulp count with e / (1 + e), the sum and the quotient half an ulp each.
-template <int VPL> __device__ __forceinline__ float score_error(bool sigmoid, float s) {
-  constexpr float u = 5.9604645e-08f;  // 2^-24
-  return sigmoid ? s * (8 * u) : s * ((VPL + 32) * u) + 0.5f * u;
+// How far an fp32 score can be off, of scores up to 1. Sigmoid: ex2.approx is within 4 u (u = 2^-24), which counts with
+// e / (1 + e), its argument's rounding adds |x| u e / (1 + e)^2, less than u, the sum 1 u, the reciprocal 2 u. Softmax: 4 u,
+// the argument's two roundings less than u, the sum VPL + 5 roundings and its terms' errors, reciprocal and product 3 u.
+constexpr float kU = 5.9604645e-08f;
+template <int VPL> __device__ __forceinline__ float score_error(bool sigmoid) { return sigmoid ? 8 * kU : (VPL + 24) * kU; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // What is left of a row when its experts are chosen: lane i has the i-th.
 struct Choice {
   int id;       // of this lane, -1 past top_k
-  float total;  // of exp(x - m), where the fp32 pass needed it
+  float m;      // the largest logit (softmax)
+  float total;  // of exp(x - m) (softmax whose weights are not divided by their sum)
 };
 
-// Choose in arithmetic F. Returns false if fp32 cannot tell the order.
+// The lane's logits, minus infinity for NaN and where it has none.
+template <int VPL> __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, int first, int count, float* x) {
+  const int64_t at = t * a.stride + first;
+  if (a.dtype == HC_F32) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) x[i] = i < count ? static_cast<const float*>(a.logits)[at + i * a.lanes] : -INFINITY;
+  } else if (a.dtype == HC_F16) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      x[i] = i < count ? __half2float(static_cast<const __half*>(a.logits)[at + i * a.lanes]) : -INFINITY;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      x[i] = i < count ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at + i * a.lanes]) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) x[i] = fmaxf(x[i], -INFINITY);
+}
+
+// The groups that stay, in arithmetic F, c being what is compared: whether this lane's does. `sure` becomes false if fp32
+// values that are each off by `error` cannot tell.
 template <typename F, int VPL>
-__device__ __forceinline__ bool choose(const RouteArgs& a, int64_t t, float m, Choice* out) {
+__device__ __forceinline__ bool keep_group(const RouteArgs& a, const F* c, int group, float error, bool* sure) {
   using Key = typename Num<F>::Key;
-  constexpr bool kFast = sizeof(F) == 4;
-  const int lane = threadIdx.x & 31, group = lane / a.lanes, sub = lane % a.lanes;
-  const int first = group * a.each + sub;
   const bool in = group < a.groups;
-  const bool by_logit = a.bias == nullptr;              // the order of the scores is that of the logits
-  const bool group_scores = a.groups > a.top_groups && !(by_logit && a.best == 1);
-  const bool scores = !by_logit || group_scores || (kFast && !a.sigmoid && !a.renormalise);
-  F v[VPL];
-  F s[VPL];
-  F total = 0;
+  F a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const bool have = in && sub + i * a.lanes < a.each;
-    const F x = have ? F(load_logit(a, t, first + i * a.lanes)) : F(-INFINITY);
-    v[i] = x;
-    s[i] = 0;
-    if (scores) {
-      if (a.sigmoid) {
-        s[i] = sigmoid_of<F>(x);
-      } else {
-        s[i] = m == -INFINITY || !have ? F(0) : exp_below<F>(x, F(m));
-        total += s[i];
-      }
+    a2 = fmax(a2, fmin(a1, c[i]));
+    a1 = fmax(a1, c[i]);
+  }
+  for (int o = 1; o < a.lanes; o <<= 1) {
+    const F b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+    a2 = fmax(fmax(a2, b2), fmin(a1, b1));
+    a1 = fmax(a1, b1);
+  }
+  F value = a.best == 2 && a.each > 1 ? a1 + a2 : a1;
+  if (value != value) value = -INFINITY;
+  Key k = in ? key_of(value) : Key(0), last = 0;
+  bool kept = false;
+  for (int i = 0; i < a.top_groups; ++i) {
+    last = warp_max(k);
+    const int g = __reduce_min_sync(kFull, k == last ? static_cast<unsigned>(group) : 64u);
+    if (group == g) {
+      kept = in;
+      k = 0;
     }
   }
-  if (scores && !a.sigmoid) {
-    total = warp_total(total);
-    const F r = total > F(0) ? F(1) / total : F(0);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] *= r;
+  if constexpr (sizeof(F) == 4) {
+    const float x = value_of(last), y = value_of(warp_max(k));
+    *sure = error == 0.0f || y == -INFINITY || x - y > 2 * a.best * error + 4 * kU * (fabsf(x) + fabsf(y));
   }
-  if (kFast) out->total = static_cast<float>(total);
+  return kept;
+}
+
+// All of a row in fp64.
+template <int VPL> __device__ __noinline__ void choose_exactly(const RouteArgs& a, int64_t t, float m, Choice* out) {
+  const int lane = threadIdx.x & 31, group = lane / a.lanes, sub = lane % a.lanes, first = group * a.each + sub;
+  const int count = group < a.groups && sub < a.each ? (a.each - sub + a.lanes - 1) / a.lanes : 0;
+  const bool by_logit = a.bias == nullptr;
+  double v[VPL], s[VPL], total = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const double x = i < count ? static_cast<double>(load_logit(a, t, first + i * a.lanes)) : -INFINITY;
+    v[i] = x;
+    s[i] = a.sigmoid ? sigmoid_of<double>(x) : m == -INFINITY || i >= count ? 0.0 : exp_below<double>(x, m);
+    total += s[i];
+  }
+  if (!a.sigmoid) {
+    total = warp_total(total);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s[i] = total > 0.0 ? s[i] / total : 0.0;
+  }
   if (!by_logit) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const bool have = in && sub + i * a.lanes < a.each;
-      v[i] = have ? s[i] + F(a.bias[first + i * a.lanes]) : F(-INFINITY);
-      if (v[i] != v[i]) v[i] = F(-INFINITY);
+      v[i] = i < count ? s[i] + static_cast<double>(a.bias[first + i * a.lanes]) : -INFINITY;
+      if (v[i] != v[i]) v[i] = -INFINITY;
     }
   }
-  bool kept = in, sure = true;
+  bool kept = group < a.groups;
   if (a.groups > a.top_groups) {
-    F a1 = -INFINITY, a2 = -INFINITY;
+    if (by_logit && a.best == 2) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const F c = by_logit && a.best == 2 ? (in && sub + i * a.lanes < a.each ? s[i] : F(-INFINITY)) : v[i];
-      a2 = fmax(a2, fmin(a1, c));
-      a1 = fmax(a1, c);
-    }
-    for (int o = 1; o < a.lanes; o <<= 1) {
-      const F b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
-      a2 = fmax(fmax(a2, b2), fmin(a1, b1));
-      a1 = fmax(a1, b1);
-    }
-    F value = a.best == 2 && a.each > 1 ? a1 + a2 : a1;
-    if (value != value) value = -INFINITY;
-    Key k = in ? key_of(value) : Key(0);
-    kept = false;
-    Key last = 0;
-    for (int i = 0; i < a.top_groups; ++i) {
-      last = warp_max(k);
-      const int g = __reduce_min_sync(kFull, k == last ? static_cast<unsigned>(group) : 64u);
-      if (group == g) {
-        kept = in;
-        k = 0;
-      }
-    }
-    if constexpr (kFast) {
-      if (group_scores) {
-        const float x = value_of(last), y = value_of(warp_max(k));
-        const float tol = 4.0f * score_error<VPL>(a.sigmoid, 1.0f) + 2.4e-07f * (fabsf(x) + fabsf(y));
-        sure = y == -INFINITY || x - y > tol;
-      }
+      for (int i = 0; i < VPL; ++i)
+        if (i >= count) s[i] = -INFINITY;
+      kept = keep_group<double, VPL>(a, s, group, 0.0f, nullptr);
+    } else {
+      kept = keep_group<double, VPL>(a, v, group, 0.0f, nullptr);
     }
   }
-  Key key[VPL];
+  unsigned long long key[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) key[i] = kept && sub + i * a.lanes < a.each ? key_of(v[i]) : Key(0);
-  Key mine = 0, next = 0;
-  int id = -1, next_id = -1;
-  for (int j = 0; j <= a.top_k; ++j) {
-    Key top = key[0];
+  for (int i = 0; i < VPL; ++i) key[i] = kept && i < count ? key_of(v[i]) : 0;
+  for (int j = 0; j < a.top_k; ++j) {
+    unsigned long long top = key[0];
     int at = 0;
 #pragma unroll
     for (int i = 1; i < VPL; ++i)
@@ -198,52 +218,139 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, int64_t t, float m, C
         top = key[i];
         at = i;
       }
-    const Key best = warp_max(top);
+    const unsigned long long best = warp_max(top);
     const int e = static_cast<int>(
         __reduce_min_sync(kFull, top == best ? static_cast<unsigned>(first + at * a.lanes) : 0x7fffffffu));
-    if (j == a.top_k) {
-      next = best;
-      next_id = e;
-      break;
-    }
-    if (lane == j) {
-      mine = best;
-      id = e;
-    }
+    if (lane == j) out->id = e;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (first + i * a.lanes == e && in) key[i] = 0;
+      if (i < count && first + i * a.lanes == e) key[i] = 0;
   }
-  out->id = id;
-  if constexpr (kFast) {
-    if (!by_logit) {
-      // each chosen value against the next one in the order
-      Key below = __shfl_down_sync(kFull, mine, 1);
-      int below_id = __shfl_down_sync(kFull, id, 1);
-      if (lane == a.top_k - 1) {
-        below = next;
-        below_id = next_id;
-      }
-      if (lane < a.top_k && below != 0) {
-        const float x = value_of(mine), y = value_of(below);
-        float err[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float l = load_logit(a, t, i ? below_id : id);
-          const float sc = a.sigmoid ? sigmoid_of<float>(l) : total > 0.0f ? exp_below<float>(l, m) / total : 0.0f;
-          err[i] = score_error<VPL>(a.sigmoid, sc);
-        }
-        const float tol = err[0] + err[1] + 5.9604645e-08f * (fabsf(x) + fabsf(y));
-        if (y != -INFINITY && !(x - y > tol)) sure = false;
-      }
-    }
-    return __all_sync(kFull, sure);
-  }
-  return true;
 }
 
-template <int VPL> __device__ __noinline__ void choose_exactly(const RouteArgs& a, int64_t t, float m, Choice* out) {
-  choose<double, VPL>(a, t, m, out);
+// Candidates of which some cannot be told apart in fp32, one to a lane: their order in fp64. Lane i gets the i-th.
+template <int VPL>
+__device__ __noinline__ int order_exactly(const RouteArgs& a, int64_t t, float m, int id, int candidates) {
+  const int lane = threadIdx.x & 31;
+  const bool mine = lane < candidates;
+  double v = mine ? static_cast<double>(load_logit(a, t, id)) : -INFINITY;
+  if (a.bias != nullptr) {
+    if (a.sigmoid) {
+      v = sigmoid_of<double>(v);
+    } else {
+      double total = 0;
+      for (int e = lane; e < a.experts; e += 32) total += m == -INFINITY ? 0.0 : exp_below<double>(load_logit(a, t, e), m);
+      total = warp_total(total);
+      v = m == -INFINITY ? 0.0 : exp_below<double>(v, m) / total;
+    }
+    if (mine) v += static_cast<double>(a.bias[id]);
+    if (v != v) v = -INFINITY;
+  }
+  int rank = 0;
+  for (int i = 0; i < candidates; ++i) {
+    const double w = __shfl_sync(kFull, v, i);
+    const int e = __shfl_sync(kFull, id, i);
+    rank += w > v || (w == v && e < id);
+  }
+  int got = -1;
+  for (int i = 0; i < candidates; ++i) {
+    const int e = __shfl_sync(kFull, id, i), at = __shfl_sync(kFull, rank, i);
+    if (at == lane) got = e;
+  }
+  return got;
+}
+
+// Choose in fp32. Returns false if it takes fp64 for all of the row.
+//
+// What is compared is a key and an index in 32 bits, the key's low bits (as many as an index has) giving way to the index,
+// lower ones first: a maximum over the warp is then a choice, and the next one the largest below it. Two values are told
+// apart if the bounds of what their keys stand for are farther apart than errors reach. Beyond the top_k-th, candidates are
+// taken until one is below it for certain; if there are any, or if two of those chosen cannot be told apart, all of them are
+// ordered in fp64.
+template <int VPL> __device__ __forceinline__ bool choose(const RouteArgs& a, int64_t t, Choice* out) {
+  const int lane = threadIdx.x & 31, group = lane / a.lanes, sub = lane % a.lanes, first = group * a.each + sub;
+  const int count = group < a.groups && sub < a.each ? (a.each - sub + a.lanes - 1) / a.lanes : 0;
+  const bool by_logit = a.bias == nullptr;  // the order of the scores is that of the logits
+  const bool by_group = a.groups > a.top_groups, group_scores = by_group && !(by_logit && a.best == 1);
+  const bool whole = !a.sigmoid && !a.renormalise;  // weights that need the sum over all
+  float v[VPL], s[VPL];
+  load_logits<VPL>(a, t, first, count, v);
+  float m = -INFINITY;
+  if (!a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, v[i]);
+    asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(m));
+  }
+  out->m = m;
+  constexpr float kLog2e = 1.44269504f;
+  if (!by_logit || group_scores || whole) {
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s[i] = reciprocal(1.0f + ex2(v[i] * -kLog2e));
+    } else {
+      float total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        s[i] = v[i] == m ? 1.0f : whole ? expf(v[i] - m) : ex2((v[i] - m) * kLog2e);
+        if (m == -INFINITY || i >= count) s[i] = 0.0f;
+        total += s[i];
+      }
+      total = warp_sum(total);
+      out->total = total;
+      const float r = total > 0.0f ? __frcp_rn(total) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s[i] *= r;
+    }
+  }
+  if (!by_logit) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = i < count ? fmaxf(s[i] + a.bias[first + i * a.lanes], -INFINITY) : -INFINITY;
+  }
+  const float error = score_error<VPL>(a.sigmoid);
+  bool kept = group < a.groups;
+  if (by_group) {
+    bool sure = true;
+    if (by_logit && a.best == 2) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (i >= count) s[i] = -INFINITY;
+      kept = keep_group<float, VPL>(a, s, group, error, &sure);
+    } else {
+      kept = keep_group<float, VPL>(a, v, group, group_scores ? error : 0.0f, &sure);
+    }
+    if (!sure) return false;
+  }
+  const uint32_t low = 0xffffffffu >> __clz(max(a.experts - 1, 1));
+  uint32_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    key[i] = kept && i < count ? (key_of(v[i]) & ~low) | (low - static_cast<uint32_t>(first + i * a.lanes)) : 0u;
+  const auto apart = [&](uint32_t above, uint32_t below) {
+    // (16-bit logits have nothing in those bits, so that equal ones are equal and in order)
+    if (by_logit) return a.dtype != HC_F32 || (above | low) != (below | low);
+    const float x = value_of(above & ~low), y = value_of(below | low);
+    return y == -INFINITY ? x > y : x - y > 2 * error + 2 * kU * (fabsf(x) + fabsf(y));
+  };
+  uint32_t mine = 0, last = 0xffffffffu, kth = 0;
+  int candidates = 0;
+#pragma unroll 1
+  for (int j = 0;; ++j) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) top = max(top, key[i] < last ? key[i] : 0u);
+    last = __reduce_max_sync(kFull, top);
+    if (last == 0 || (j >= a.top_k && apart(kth, last))) break;
+    if (j == 32) return false;
+    if (lane == j) mine = last;
+    if (j == a.top_k - 1) kth = last;
+    candidates = j + 1;
+  }
+  int id = lane < candidates ? static_cast<int>(low - (mine & low)) : -1;
+  const uint32_t next = __shfl_down_sync(kFull, mine, 1);
+  const bool told = lane + 1 >= candidates || apart(mine, next);
+  if (candidates > a.top_k || !__all_sync(kFull, told)) id = order_exactly<VPL>(a, t, m, id, candidates);
+  out->id = id;
+  return true;
 }
 
 // x - m in two parts, so that the weight of a large logit's neighbour keeps its last bits.
@@ -270,12 +377,9 @@ template <int VPL> __global__ void __launch_bounds__(32 * kWarps) route_kernel(R
     }
     return;
   }
-  float m = -INFINITY;
-  for (int e = lane; e < a.experts; e += 32) m = fmaxf(m, load_logit(a, t, e));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
   Choice c;
-  if (!choose<float, VPL>(a, t, m, &c)) choose_exactly<VPL>(a, t, m, &c);
+  if (!choose<VPL>(a, t, &c)) choose_exactly<VPL>(a, t, c.m, &c);
+  const float m = c.m;
   const bool mine = lane < a.top_k;
   const float x = mine ? load_logit(a, t, c.id) : -INFINITY;
   float w;
