@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr unsigned kFull = 0xffffffffu;
+using u64 = unsigned long long;
 
 struct RouteArgs {
   const void* logits;
@@ -134,23 +135,21 @@ template <int VPL> __device__ __forceinline__ void load_logits(const RouteArgs& 
   for (int i = 0; i < VPL; ++i) x[i] = fmaxf(x[i], -INFINITY);
 }
 
-// The groups that stay, in arithmetic F, c being what is compared: whether this lane's does. `sure` becomes false if fp32
-// values that are each off by `error` cannot tell.
-template <typename F, int VPL>
-__device__ __forceinline__ bool keep_group(const RouteArgs& a, const F* c, int group, float error, bool* sure) {
+// The two largest values of a group, from those of its lanes.
+template <typename F> __device__ __forceinline__ void join_best(const RouteArgs& a, F* a1, F* a2) {
+  for (int o = 1; o < a.lanes; o <<= 1) {
+    const F b1 = __shfl_xor_sync(kFull, *a1, o), b2 = __shfl_xor_sync(kFull, *a2, o);
+    *a2 = fmax(fmax(*a2, b2), fmin(*a1, b1));
+    *a1 = fmax(*a1, b1);
+  }
+}
+
+// Whether this lane's group stays, by the two largest of its values in arithmetic F. `sure` becomes false if fp32 values that
+// are each off by `error` cannot tell.
+template <typename F>
+__device__ __forceinline__ bool keep_group(const RouteArgs& a, F a1, F a2, int group, float error, bool* sure) {
   using Key = typename Num<F>::Key;
   const bool in = group < a.groups;
-  F a1 = -INFINITY, a2 = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    a2 = fmax(a2, fmin(a1, c[i]));
-    a1 = fmax(a1, c[i]);
-  }
-  for (int o = 1; o < a.lanes; o <<= 1) {
-    const F b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
-    a2 = fmax(fmax(a2, b2), fmin(a1, b1));
-    a1 = fmax(a1, b1);
-  }
   F value = a.best == 2 && a.each > 1 ? a1 + a2 : a1;
   if (value != value) value = -INFINITY;
   Key k = in ? key_of(value) : Key(0), last = 0;
@@ -170,45 +169,45 @@ __device__ __forceinline__ bool keep_group(const RouteArgs& a, const F* c, int g
   return kept;
 }
 
-// All of a row in fp64.
-template <int VPL> __device__ __noinline__ void choose_exactly(const RouteArgs& a, int64_t t, float m, Choice* out) {
-  const int lane = threadIdx.x & 31, group = lane / a.lanes, sub = lane % a.lanes, first = group * a.each + sub;
-  const int count = group < a.groups && sub < a.each ? (a.each - sub + a.lanes - 1) / a.lanes : 0;
-  const bool by_logit = a.bias == nullptr;
-  double v[VPL], s[VPL], total = 0;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const double x = i < count ? static_cast<double>(load_logit(a, t, first + i * a.lanes)) : -INFINITY;
-    v[i] = x;
-    s[i] = a.sigmoid ? sigmoid_of<double>(x) : m == -INFINITY || i >= count ? 0.0 : exp_below<double>(x, m);
-    total += s[i];
-  }
-  if (!a.sigmoid) {
-    total = warp_total(total);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = total > 0.0 ? s[i] / total : 0.0;
-  }
-  if (!by_logit) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      v[i] = i < count ? s[i] + static_cast<double>(a.bias[first + i * a.lanes]) : -INFINITY;
-      if (v[i] != v[i]) v[i] = -INFINITY;
+// The sum of exp(x - m) over a row in fp64.
+__device__ __forceinline__ double exact_total(const RouteArgs& a, int64_t t, float m) {
+  double total = 0;
+  for (int e = threadIdx.x & 31; e < a.experts; e += 32) total += m == -INFINITY ? 0.0 : exp_below<double>(load_logit(a, t, e), m);
+  return warp_total(total);
+}
+// What is compared, in fp64 (with the logits in place of scores where that is the same order).
+__device__ __forceinline__ double exact_value(const RouteArgs& a, int64_t t, int e, float m, double total, bool logits) {
+  double v = load_logit(a, t, e);
+  if (!logits) v = a.sigmoid ? sigmoid_of<double>(v) : m == -INFINITY ? 0.0 : exp_below<double>(v, m) / total;
+  if (a.bias != nullptr) v += static_cast<double>(a.bias[e]);
+  return v != v ? -INFINITY : v;
+}
+
+// Whether this lane's group stays, in fp64. `pending` has the lane's elements that can be among its group's two largest.
+__device__ __noinline__ bool keep_group_exactly(const RouteArgs& a, int64_t t, float m, int group, int first, u64 pending) {
+  const double total = a.sigmoid ? 1.0 : exact_total(a, t, m);
+  double a1 = -INFINITY, a2 = -INFINITY;
+  while (__any_sync(kFull, pending != 0)) {
+    if (pending != 0) {
+      const double v = exact_value(a, t, first + (__ffsll(pending) - 1) * a.lanes, m, total, false);
+      a2 = fmax(a2, fmin(a1, v));
+      a1 = fmax(a1, v);
+      pending &= pending - 1;
     }
   }
-  bool kept = group < a.groups;
-  if (a.groups > a.top_groups) {
-    if (by_logit && a.best == 2) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i >= count) s[i] = -INFINITY;
-      kept = keep_group<double, VPL>(a, s, group, 0.0f, nullptr);
-    } else {
-      kept = keep_group<double, VPL>(a, v, group, 0.0f, nullptr);
-    }
-  }
+  join_best(a, &a1, &a2);
+  return keep_group<double>(a, a1, a2, group, 0.0f, nullptr);
+}
+
+// All experts of the groups that stay, in fp64.
+template <int VPL>
+__device__ __noinline__ int choose_exactly(const RouteArgs& a, int64_t t, float m, int first, int count, bool logits) {
+  const int lane = threadIdx.x & 31;
+  const double total = a.sigmoid || logits ? 1.0 : exact_total(a, t, m);
   unsigned long long key[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) key[i] = kept && i < count ? key_of(v[i]) : 0;
+  for (int i = 0; i < VPL; ++i) key[i] = i < count ? key_of(exact_value(a, t, first + i * a.lanes, m, total, logits)) : 0;
+  int id = -1;
   for (int j = 0; j < a.top_k; ++j) {
     unsigned long long top = key[0];
     int at = 0;
@@ -221,31 +220,19 @@ template <int VPL> __device__ __noinline__ void choose_exactly(const RouteArgs& 
     const unsigned long long best = warp_max(top);
     const int e = static_cast<int>(
         __reduce_min_sync(kFull, top == best ? static_cast<unsigned>(first + at * a.lanes) : 0x7fffffffu));
-    if (lane == j) out->id = e;
+    if (lane == j) id = e;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (i < count && first + i * a.lanes == e) key[i] = 0;
   }
+  return id;
 }
 
 // Candidates of which some cannot be told apart in fp32, one to a lane: their order in fp64. Lane i gets the i-th.
-template <int VPL>
-__device__ __noinline__ int order_exactly(const RouteArgs& a, int64_t t, float m, int id, int candidates) {
+__device__ __noinline__ int order_exactly(const RouteArgs& a, int64_t t, float m, int id, int candidates, bool logits) {
   const int lane = threadIdx.x & 31;
-  const bool mine = lane < candidates;
-  double v = mine ? static_cast<double>(load_logit(a, t, id)) : -INFINITY;
-  if (a.bias != nullptr) {
-    if (a.sigmoid) {
-      v = sigmoid_of<double>(v);
-    } else {
-      double total = 0;
-      for (int e = lane; e < a.experts; e += 32) total += m == -INFINITY ? 0.0 : exp_below<double>(load_logit(a, t, e), m);
-      total = warp_total(total);
-      v = m == -INFINITY ? 0.0 : exp_below<double>(v, m) / total;
-    }
-    if (mine) v += static_cast<double>(a.bias[id]);
-    if (v != v) v = -INFINITY;
-  }
+  const double total = a.sigmoid || logits ? 1.0 : exact_total(a, t, m);
+  const double v = lane < candidates ? exact_value(a, t, id, m, total, logits) : -INFINITY;
   int rank = 0;
   for (int i = 0; i < candidates; ++i) {
     const double w = __shfl_sync(kFull, v, i);
@@ -260,14 +247,14 @@ __device__ __noinline__ int order_exactly(const RouteArgs& a, int64_t t, float m
   return got;
 }
 
-// Choose in fp32. Returns false if it takes fp64 for all of the row.
+// Choose, in fp32 as far as that can tell.
 //
 // What is compared is a key and an index in 32 bits, the key's low bits (as many as an index has) giving way to the index,
 // lower ones first: a maximum over the warp is then a choice, and the next one the largest below it. Two values are told
 // apart if the bounds of what their keys stand for are farther apart than errors reach. Beyond the top_k-th, candidates are
 // taken until one is below it for certain; if there are any, or if two of those chosen cannot be told apart, all of them are
-// ordered in fp64.
-template <int VPL> __device__ __forceinline__ bool choose(const RouteArgs& a, int64_t t, Choice* out) {
+// ordered in fp64 (with more than 32, all experts).
+template <int VPL> __device__ __forceinline__ void choose(const RouteArgs& a, int64_t t, Choice* out) {
   const int lane = threadIdx.x & 31, group = lane / a.lanes, sub = lane % a.lanes, first = group * a.each + sub;
   const int count = group < a.groups && sub < a.each ? (a.each - sub + a.lanes - 1) / a.lanes : 0;
   const bool by_logit = a.bias == nullptr;  // the order of the scores is that of the logits
@@ -309,16 +296,24 @@ template <int VPL> __device__ __forceinline__ bool choose(const RouteArgs& a, in
   const float error = score_error<VPL>(a.sigmoid);
   bool kept = group < a.groups;
   if (by_group) {
-    bool sure = true;
-    if (by_logit && a.best == 2) {
+    float a1 = -INFINITY, a2 = -INFINITY;
+    const auto value = [&](int i) { return i >= count ? -INFINITY : by_logit && a.best == 2 ? s[i] : v[i]; };
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      a2 = fmaxf(a2, fminf(a1, value(i)));
+      a1 = fmaxf(a1, value(i));
+    }
+    join_best(a, &a1, &a2);
+    bool sure;
+    kept = keep_group<float>(a, a1, a2, group, group_scores ? error : 0.0f, &sure);
+    if (!sure) {
+      const float least = a.best == 2 && a.each > 1 ? a2 : a1, reach = 2 * error + 4 * kU * fabsf(least);
+      u64 pending = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (i >= count) s[i] = -INFINITY;
-      kept = keep_group<float, VPL>(a, s, group, error, &sure);
-    } else {
-      kept = keep_group<float, VPL>(a, v, group, group_scores ? error : 0.0f, &sure);
+        if (i < count && !(value(i) < least - reach)) pending |= 1ull << i;
+      kept = keep_group_exactly(a, t, m, group, first, pending);
     }
-    if (!sure) return false;
   }
   const uint32_t low = 0xffffffffu >> __clz(max(a.experts - 1, 1));
   uint32_t key[VPL];
@@ -340,7 +335,10 @@ template <int VPL> __device__ __forceinline__ bool choose(const RouteArgs& a, in
     for (int i = 0; i < VPL; ++i) top = max(top, key[i] < last ? key[i] : 0u);
     last = __reduce_max_sync(kFull, top);
     if (last == 0 || (j >= a.top_k && apart(kth, last))) break;
-    if (j == 32) return false;
+    if (j == 32) {
+      out->id = choose_exactly<VPL>(a, t, m, first, kept ? count : 0, by_logit);
+      return;
+    }
     if (lane == j) mine = last;
     if (j == a.top_k - 1) kth = last;
     candidates = j + 1;
@@ -348,9 +346,8 @@ template <int VPL> __device__ __forceinline__ bool choose(const RouteArgs& a, in
   int id = lane < candidates ? static_cast<int>(low - (mine & low)) : -1;
   const uint32_t next = __shfl_down_sync(kFull, mine, 1);
   const bool told = lane + 1 >= candidates || apart(mine, next);
-  if (candidates > a.top_k || !__all_sync(kFull, told)) id = order_exactly<VPL>(a, t, m, id, candidates);
+  if (candidates > a.top_k || !__all_sync(kFull, told)) id = order_exactly(a, t, m, id, candidates, by_logit);
   out->id = id;
-  return true;
 }
 
 // x - m in two parts, so that the weight of a large logit's neighbour keeps its last bits.
@@ -378,7 +375,7 @@ template <int VPL> __global__ void __launch_bounds__(32 * kWarps) route_kernel(R
     return;
   }
   Choice c;
-  if (!choose<VPL>(a, t, &c)) choose_exactly<VPL>(a, t, c.m, &c);
+  choose<VPL>(a, t, &c);
   const float m = c.m;
   const bool mine = lane < a.top_k;
   const float x = mine ? load_logit(a, t, c.id) : -INFINITY;
