@@ -27,9 +27,11 @@ using namespace um;
 
 template <int kRows> struct Cfg {
   static constexpr int kStage = 2 * kHalfBytes + kRows * kBK * 2;
-  static constexpr int kStages = kRows == 32 ? 6 : kRows == 64 ? 5 : 4;
+  // (With 32 pairs, as few as let two CTAs share an SM, so that the outer product's are there, with their first weights, when
+  // the inner one's finish.)
+  static constexpr int kStages = kRows == 32 ? 3 : kRows == 64 ? 5 : 4;
   static constexpr int kCols = 4 * kRows;  // of tensor memory: two accumulators of two halves each
-  static constexpr size_t kSmem = kStages * kStage + sizeof(Bars) + 1024;
+  static constexpr size_t kSmem = kStages * kStage + 1024;  // and the bars
 };
 template <int kRows, bool kInner> constexpr int kThreads = 192 + (kInner ? kRows : 0);
 
@@ -64,27 +66,44 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = b->tmem_base;
-  pdl_wait();
-  pdl_trigger();
+  // The outer product needs the inner one's results for its rows only. What comes before that was there when this kernel
+  // began: the inner product's CTAs let it begin after they had waited for the lists, and the weights are older.
+  if (kInner) {
+    pdl_wait();
+    pdl_trigger();
+  }
   count_tiles<kRows, kThreads<kRows, kInner>>(a, b);
-  Pieces<kRows, true> p(a, *b, blockIdx.x, gridDim.x);
+  Pieces<kRows, true> p(a, b, blockIdx.x, gridDim.x);
   bool ok = true;
 
   if (warp == 0) {
     if (lane == 0) {
+      const auto weights = [&](int st, int k, const Pieces<kRows, true>& p) {
+        uint8_t* w = smem + st * C::kStage;
+        mbar_arrive_expect_tx(&b->full[st], kInner ? 2 * kHalfBytes : C::kStage);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          load_half(w + h * kHalfBytes, &a.tm_w[h], a.k_major, k * kBK, p.feature + (kInner ? 0 : h * kHalf), p.expert,
+                    &b->full[st]);
+      };
+      int early = 0;  // stages whose weights are on their way before the wait
+      if (!kInner) {
+        Pieces<kRows, true> q = p;
+        while (early < C::kStages && q.next(kStep))
+          for (int k = q.k0; k < q.k1 && early < C::kStages; ++k) weights(early++, k, q);
+        pdl_wait();
+        pdl_trigger();
+      }
       int it = 0;
       while (ok && p.next(kStep)) {
         for (int k = p.k0; k < p.k1; ++k, ++it) {
           const int st = it % C::kStages;
-          ok = mbar_wait(&b->empty[st], ((it / C::kStages) & 1) ^ 1, &g_few_wait_timeouts);
-          if (!ok) break;
-          uint8_t* w = smem + st * C::kStage;
-          mbar_arrive_expect_tx(&b->full[st], kInner ? 2 * kHalfBytes : C::kStage);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            load_half(w + h * kHalfBytes, &a.tm_w[h], a.k_major, k * kBK, p.feature + (kInner ? 0 : h * kHalf), p.expert,
-                      &b->full[st]);
-          if (!kInner) tma_load_2d(w + 2 * kHalfBytes, &a.tm_rows, k * kBK, p.first, &b->full[st]);
+          if (it >= early) {
+            ok = mbar_wait(&b->empty[st], ((it / C::kStages) & 1) ^ 1, &g_few_wait_timeouts);
+            if (!ok) break;
+            weights(st, k, p);
+          }
+          if (!kInner) tma_load_2d(smem + st * C::kStage + 2 * kHalfBytes, &a.tm_rows, k * kBK, p.first, &b->full[st]);
         }
       }
     }
@@ -122,6 +141,7 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
       }
     }
   } else if (warp < 6) {
+    if (!kInner) pdl_wait();  // (where its results go, others may still read until then)
     const int quarter = warp & 3;  // of the lanes of tensor memory, which a warp's place decides
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int me = quarter * 32 + lane;
@@ -138,76 +158,76 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-              // this thread has feature `me` of both halves, a column for each pair
-              const bool whole = p.whole();
-              const int f = p.feature + me;
-              const auto put = [&](int c, float v0, float v1) {
-                const int64_t to = static_cast<int64_t>(__shfl_sync(0xffffffffu, place[c / 32], c % 32)) * a.out_step;
-                if (kInner) {
-                  if (f < a.features) stf(static_cast<T*>(a.out) + to + f, saturate<T>(gated(v0, v1)));
-                } else {
-                  if (f < a.features) static_cast<float*>(a.out)[to + f] = v0;
-                  if (f + kHalf < a.features) static_cast<float*>(a.out)[to + f + kHalf] = v1;
-                }
-              };
-              float* part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (p.k0 > 0 ? 0 : 1)) * (2 * kRows * kHalf) + me;
-      #pragma unroll
-              for (int c0 = 0; c0 < kRows; c0 += 16) {
-                if (c0 < p.rows) {
-                  float v[2][16];
-                  tmem_ld16(d + c0, v[0]);
-                  tmem_ld16(d + kRows + c0, v[1]);
-      #pragma unroll
-                  for (int c = 0; c < 16; ++c) {
-                    if (c0 + c < p.rows) {
-                      if (whole) {
-                        put(c0 + c, v[0][c], v[1][c]);
-                      } else {
-                        __stcg(part + (c0 + c) * kHalf, v[0][c]);
-                        __stcg(part + (kRows + c0 + c) * kHalf, v[1][c]);
-                      }
-                    }
-                  }
-                }
+      // this thread has feature `me` of both halves, a column for each pair
+      const bool whole = p.whole();
+      const int f = p.feature + me;
+      const auto put = [&](int c, float v0, float v1) {
+        const int64_t to = static_cast<int64_t>(__shfl_sync(0xffffffffu, place[c / 32], c % 32)) * a.out_step;
+        if (kInner) {
+          if (f < a.features) stf(static_cast<T*>(a.out) + to + f, saturate<T>(gated(v0, v1)));
+        } else {
+          if (f < a.features) static_cast<float*>(a.out)[to + f] = v0;
+          if (f + kHalf < a.features) static_cast<float*>(a.out)[to + f + kHalf] = v1;
+        }
+      };
+      float* part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (p.k0 > 0 ? 0 : 1)) * (2 * kRows * kHalf) + me;
+#pragma unroll
+      for (int c0 = 0; c0 < kRows; c0 += 16) {
+        if (c0 < p.rows) {
+          float v[2][16];
+          tmem_ld16(d + c0, v[0]);
+          tmem_ld16(d + kRows + c0, v[1]);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            if (c0 + c < p.rows) {
+              if (whole) {
+                put(c0 + c, v[0][c], v[1][c]);
+              } else {
+                __stcg(part + (c0 + c) * kHalf, v[0][c]);
+                __stcg(part + (kRows + c0 + c) * kHalf, v[1][c]);
               }
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&b->acc_empty[buf]);
-              if (!whole) {
-                const int64_t unit = static_cast<int64_t>(p.tile) * a.kblocks;
-                const int c0 = p.cta_of(unit), c1 = p.cta_of(unit + a.kblocks - 1);
-                __threadfence();
-                named_bar_sync(1, 128);
-                if (warp == 2 && lane == 0) b->last = atomicAdd(&a.tickets[p.tile], 1u) == static_cast<unsigned>(c1 - c0);
-                named_bar_sync(1, 128);
-                const bool last = b->last != 0;
-                if (last) {
-                  __threadfence();
-                  // (sixteen pairs' sums at a time, so that their loads overlap)
-                  for (int b0 = 0; b0 < p.rows; b0 += 16) {
-                    float v0[16] = {}, v1[16] = {};
-                    for (int q = c0; q <= c1; ++q) {
-                      const int slot = p.first_unit(q) > unit ? 0 : 1;
-                      const float* from = a.part + (2 * static_cast<int64_t>(q) + slot) * (2 * kRows * kHalf) + b0 * kHalf + me;
-                      float w0[16], w1[16];
-      #pragma unroll
-                      for (int c = 0; c < 16; ++c) {
-                        w0[c] = b0 + c < p.rows ? __ldcg(from + c * kHalf) : 0.0f;
-                        w1[c] = b0 + c < p.rows ? __ldcg(from + (kRows + c) * kHalf) : 0.0f;
-                      }
-      #pragma unroll
-                      for (int c = 0; c < 16; ++c) {
-                        v0[c] += w0[c];
-                        v1[c] += w1[c];
-                      }
-                    }
-      #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                      if (b0 + c < p.rows) put(b0 + c, v0[c], v1[c]);
-                  }
-                }
-                named_bar_sync(1, 128);  // (`last` is read before it is written again)
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->acc_empty[buf]);
+      if (!whole) {
+        const int64_t unit = static_cast<int64_t>(p.tile) * a.kblocks;
+        const int c0 = p.cta_of(unit), c1 = p.cta_of(unit + a.kblocks - 1);
+        __threadfence();
+        named_bar_sync(1, 128);
+        if (warp == 2 && lane == 0) b->last = atomicAdd(&a.tickets[p.tile], 1u) == static_cast<unsigned>(c1 - c0);
+        named_bar_sync(1, 128);
+        const bool last = b->last != 0;
+        if (last) {
+          __threadfence();
+          // (sixteen pairs' sums at a time, so that their loads overlap)
+          for (int b0 = 0; b0 < p.rows; b0 += 16) {
+            float v0[16] = {}, v1[16] = {};
+            for (int q = c0; q <= c1; ++q) {
+              const int slot = p.first_unit(q) > unit ? 0 : 1;
+              const float* from = a.part + (2 * static_cast<int64_t>(q) + slot) * (2 * kRows * kHalf) + b0 * kHalf + me;
+              float w0[16], w1[16];
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                w0[c] = b0 + c < p.rows ? __ldcg(from + c * kHalf) : 0.0f;
+                w1[c] = b0 + c < p.rows ? __ldcg(from + (kRows + c) * kHalf) : 0.0f;
               }
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                v0[c] += w0[c];
+                v1[c] += w1[c];
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (b0 + c < p.rows) put(b0 + c, v0[c], v1[c]);
+          }
+        }
+        named_bar_sync(1, 128);  // (`last` is read before it is written again)
+      }
     }
   } else if constexpr (kInner) {
     const int group = warp - 6;
@@ -238,9 +258,10 @@ cudaError_t launch_product(Args a, const hc_expert_mlp_t& p, int num_sms, cudaSt
   // (no more CTAs than there can be units of work)
   const int64_t units = experts_um_tiles(p, kRows, kInner) * a.kblocks;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(num_sms, units));
-  const cudaError_t e = ensure_smem<few_kernel<T, kRows, kInner>>(Cfg<kRows>::kSmem);
+  const size_t smem = Cfg<kRows>::kSmem + bars_bytes(a.experts);
+  const cudaError_t e = ensure_smem<few_kernel<T, kRows, kInner>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(few_kernel<T, kRows, kInner>, dim3(grid), dim3(kThreads<kRows, kInner>), Cfg<kRows>::kSmem, s, 1, a);
+  return launch_pdl(few_kernel<T, kRows, kInner>, dim3(grid), dim3(kThreads<kRows, kInner>), smem, s, 1, a);
 }
 
 template <typename T, int kRows>

@@ -35,7 +35,7 @@ constexpr int kGatherWarps = 4;
 // Warps that write results: a tile of the outer product has a quarter of the inner one's MMAs to a result, or less.
 template <bool kInner> constexpr int kResults = kInner ? 4 : 8;
 template <bool kInner> constexpr int kThreads = 64 + 32 * kResults<kInner> + (kInner ? 32 * kGatherWarps : 0);
-constexpr size_t kSmem = kStages * kStage + 8 * kStageOut + sizeof(Bars) + 1024;
+constexpr size_t kSmem = kStages * kStage + 8 * kStageOut + 1024;  // and the bars
 
 // ------------------------------------------------------- pairs of CTAs, as inline PTX
 
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads<kInner>, 1) many_kernel(const __grid_
   pdl_wait();
   pdl_trigger();
   count_tiles<kRows, kThreads<kInner>>(a, b);
-  Pieces<kRows, false> p(a, *b, blockIdx.x / 2, gridDim.x / 2);
+  Pieces<kRows, false> p(a, b, blockIdx.x / 2, gridDim.x / 2);
   bool ok = true;
 
   if (warp == 0) {
@@ -171,56 +171,56 @@ __global__ void __launch_bounds__(kThreads<kInner>, 1) many_kernel(const __grid_
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-              // This thread has pair `me`, a column for each feature. Thirty-two features of the warp's 32 pairs at a time go through
-              // shared memory, so that four lanes write 64 bytes of one row (a row for each lane would be 32 requests an instruction).
-              constexpr int kCols32 = (kInner ? kHalf : 2 * kHalf) / 32 / (kWriters / 4);  // that a warp has, from the first-th on
-              const int part = (warp - 2) / 4, first = part * kCols32;
-              uint8_t* stage = smem + kStages * kStage + (warp - 2) * kStageOut;
-              uint32_t exps[2] = {};
-      #pragma unroll
-              for (int h = 0; h < kCols32; ++h) {
-                const int c0 = (first + h) * 32;
-                uint32_t x[2][16], y[2][16];
-      #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  tmem_ld16_nowait(d + c0 + 16 * i, x[i]);
-                  if (kInner) tmem_ld16_nowait(d + kHalf + c0 + 16 * i, y[i]);
-                }
-      #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  uint4 q[2];
-                  float v[16];
-                  tmem_ld_wait_r(x[i]);
-                  if (kInner) tmem_ld_wait_r(y[i]);
-                  if (kInner) {
-      #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = saturate<T>(gated(__uint_as_float(x[i][j]), __uint_as_float(y[i][j])));
-                    q[0] = V8<T>::pack(v);
-                    q[1] = V8<T>::pack(v + 8);
-                  } else {
-      #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(x[i][j]);
-                    exps[h >> 1] |= BlockFloat::pack(v, reinterpret_cast<uint32_t*>(q)) << (16 * (h & 1) + 8 * i);
-                  }
-      #pragma unroll
-                  for (int j = 0; j < 2; ++j)
-                    *reinterpret_cast<uint4*>(stage + lane * 64 + (((2 * i + j) ^ ((lane >> 1) & 3)) << 4)) = q[j];
-                }
-                __syncwarp();
-                const int chunk = lane & 3, f = p.feature + c0 + chunk * 8;
-      #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int r = 8 * i + (lane >> 2);
-                  const int64_t to = __shfl_sync(0xffffffffu, place, r);
-                  const uint4 q = *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
-                  // (rows of out are 16-byte aligned and padded to a multiple of 16 elements)
-                  if (quarter * 32 + r < rows && f < a.features) st16(static_cast<T*>(a.out) + to * a.out_step + f, q);
-                }
-                __syncwarp();
-              }
-              if (!kInner && me < rows)  // (a row's exponents are padded to whole tiles)
-                *reinterpret_cast<uint2*>(a.exps + static_cast<int64_t>(place) * a.exp_step + p.feature / 16 + 8 * part) =
-                    make_uint2(exps[0], exps[1]);
+      // This thread has pair `me`, a column for each feature. Thirty-two features of the warp's 32 pairs at a time go through
+      // shared memory, so that four lanes write 64 bytes of one row (a row for each lane would be 32 requests an instruction).
+      constexpr int kCols32 = (kInner ? kHalf : 2 * kHalf) / 32 / (kWriters / 4);  // that a warp has, from the first-th on
+      const int part = (warp - 2) / 4, first = part * kCols32;
+      uint8_t* stage = smem + kStages * kStage + (warp - 2) * kStageOut;
+      uint32_t exps[2] = {};
+#pragma unroll
+      for (int h = 0; h < kCols32; ++h) {
+        const int c0 = (first + h) * 32;
+        uint32_t x[2][16], y[2][16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          tmem_ld16_nowait(d + c0 + 16 * i, x[i]);
+          if (kInner) tmem_ld16_nowait(d + kHalf + c0 + 16 * i, y[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint4 q[2];
+          float v[16];
+          tmem_ld_wait_r(x[i]);
+          if (kInner) tmem_ld_wait_r(y[i]);
+          if (kInner) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = saturate<T>(gated(__uint_as_float(x[i][j]), __uint_as_float(y[i][j])));
+            q[0] = V8<T>::pack(v);
+            q[1] = V8<T>::pack(v + 8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(x[i][j]);
+            exps[h >> 1] |= BlockFloat::pack(v, reinterpret_cast<uint32_t*>(q)) << (16 * (h & 1) + 8 * i);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<uint4*>(stage + lane * 64 + (((2 * i + j) ^ ((lane >> 1) & 3)) << 4)) = q[j];
+        }
+        __syncwarp();
+        const int chunk = lane & 3, f = p.feature + c0 + chunk * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + (lane >> 2);
+          const int64_t to = __shfl_sync(0xffffffffu, place, r);
+          const uint4 q = *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
+          // (rows of out are 16-byte aligned and padded to a multiple of 16 elements)
+          if (quarter * 32 + r < rows && f < a.features) st16(static_cast<T*>(a.out) + to * a.out_step + f, q);
+        }
+        __syncwarp();
+      }
+      if (!kInner && me < rows)  // (a row's exponents are padded to whole tiles)
+        *reinterpret_cast<uint2*>(a.exps + static_cast<int64_t>(place) * a.exp_step + p.feature / 16 + 8 * part) =
+            make_uint2(exps[0], exps[1]);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) first_arrive(&b->acc_empty[buf]);
@@ -255,9 +255,10 @@ template <typename T, bool kInner>
 cudaError_t launch_product(const Args& a, const hc_expert_mlp_t& p, int num_sms, cudaStream_t s) {
   const int64_t tiles = experts_um_tiles(p, kRows, kInner);
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(num_sms / 2, tiles));
-  const cudaError_t e = ensure_smem<many_kernel<T, kInner>>(kSmem);
+  const size_t smem = kSmem + bars_bytes(a.experts);
+  const cudaError_t e = ensure_smem<many_kernel<T, kInner>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(many_kernel<T, kInner>, dim3(grid), dim3(kThreads<kInner>), kSmem, s, 2, a);
+  return launch_pdl(many_kernel<T, kInner>, dim3(grid), dim3(kThreads<kInner>), smem, s, 2, a);
 }
 
 template <typename T> cudaError_t launch_both(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s) {

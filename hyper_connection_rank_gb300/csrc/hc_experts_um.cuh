@@ -50,12 +50,13 @@ struct Args {
   int experts, top_k, inputs, features, kblocks, fblocks, k_major;
 };
 
+// Behind it in shared memory: the bounds, and the tiles of the experts before each (num_experts + 1 both).
 struct Bars {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   uint32_t tmem_base, last;
-  int32_t bounds[kMaxExperts + 1], tiles[kMaxExperts + 1];  // tiles: of the experts before each
   int32_t red[32];
 };
+inline size_t bars_bytes(int experts) { return sizeof(Bars) + 2 * (static_cast<size_t>(experts) + 1) * sizeof(int32_t); }
 
 // Arrive on `bar` when this thread's cp.async copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -78,11 +79,12 @@ template <> __device__ __forceinline__ float saturate<__half>(float v) {
 // of inputs laid end to end, otherwise whole tiles in turn.
 template <int kRows, bool kSplit> struct Pieces {
   const Args& a;
-  const Bars& b;
+  const int32_t *bounds, *tiles;
   int64_t at, end, units, ctas;
 
-  __device__ __forceinline__ Pieces(const Args& args, const Bars& bars, int cta, int count) : a(args), b(bars) {
-    const int total = b.tiles[a.experts] * a.fblocks;
+  __device__ __forceinline__ Pieces(const Args& args, const Bars* bars, int cta, int count)
+      : a(args), bounds(reinterpret_cast<const int32_t*>(bars + 1)), tiles(bounds + args.experts + 1) {
+    const int total = tiles[a.experts] * a.fblocks;
     units = static_cast<int64_t>(total) * a.kblocks;
     ctas = min(static_cast<int64_t>(count), kSplit ? units : total);  // that have work, at least a unit each
     at = end = 0;
@@ -115,12 +117,12 @@ template <int kRows, bool kSplit> struct Pieces {
     int lo = 0, hi = a.experts - 1;  // the last expert whose tiles begin at m or before (empty ones have none)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (b.tiles[mid] <= m) lo = mid;
+      if (tiles[mid] <= m) lo = mid;
       else hi = mid - 1;
     }
     expert = lo;
-    first = b.bounds[lo] + (m - b.tiles[lo]) * kRows;
-    rows = min(kRows, b.bounds[lo + 1] - first);
+    first = bounds[lo] + (m - tiles[lo]) * kRows;
+    rows = min(kRows, bounds[lo + 1] - first);
     return true;
   }
   __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == a.kblocks; }
@@ -130,13 +132,14 @@ template <int kRows, bool kSplit> struct Pieces {
 template <int kRows, int kThreads> __device__ __forceinline__ void count_tiles(const Args& a, Bars* b) {
   constexpr int kEach = (kMaxExperts + kThreads - 1) / kThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e <= a.experts; e += kThreads) b->bounds[e] = a.bounds[e];
+  int32_t *bounds = reinterpret_cast<int32_t*>(b + 1), *tiles = bounds + a.experts + 1;
+  for (int e = threadIdx.x; e <= a.experts; e += kThreads) bounds[e] = a.bounds[e];
   __syncthreads();
   int n[kEach], sum = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int e = threadIdx.x * kEach + i;
-    n[i] = e < a.experts ? (b->bounds[e + 1] - b->bounds[e] + kRows - 1) / kRows : 0;
+    n[i] = e < a.experts ? (bounds[e + 1] - bounds[e] + kRows - 1) / kRows : 0;
     sum += n[i];
   }
   int upto = sum;
@@ -152,7 +155,7 @@ template <int kRows, int kThreads> __device__ __forceinline__ void count_tiles(c
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int e = threadIdx.x * kEach + i;
-    if (e <= a.experts) b->tiles[e] = before;
+    if (e <= a.experts) tiles[e] = before;
     before += n[i];
   }
   __syncthreads();
