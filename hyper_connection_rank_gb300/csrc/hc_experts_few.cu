@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
           if (f + kHalf < a.features) static_cast<float*>(a.out)[to + f + kHalf] = v1;
         }
       };
-      float* part = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (p.k0 > 0 ? 0 : 1)) * (2 * kRows * kHalf) + me;
+      float* part = a.part + static_cast<int64_t>(p.place(blockIdx.x)) * (2 * kRows * kHalf) + me;
 #pragma unroll
       for (int c0 = 0; c0 < kRows; c0 += 16) {
         if (c0 < p.rows) {
@@ -194,37 +194,44 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->acc_empty[buf]);
       if (!whole) {
-        const int64_t unit = static_cast<int64_t>(p.tile) * a.kblocks;
-        const int c0 = p.cta_of(unit), c1 = p.cta_of(unit + a.kblocks - 1);
+        uint32_t c0, c1;
+        p.sharers(&c0, &c1);
         __threadfence();
         named_bar_sync(1, 128);
-        if (warp == 2 && lane == 0) b->last = atomicAdd(&a.tickets[p.tile], 1u) == static_cast<unsigned>(c1 - c0);
+        if (warp == 2 && lane == 0) b->last = atomicAdd(&a.tickets[p.tile], 1u) == c1 - c0;
         named_bar_sync(1, 128);
-        const bool last = b->last != 0;
-        if (last) {
+        if (b->last != 0) {
           __threadfence();
-          // (sixteen pairs' sums at a time, so that their loads overlap)
-          for (int b0 = 0; b0 < p.rows; b0 += 16) {
-            float v0[16] = {}, v1[16] = {};
-            for (int q = c0; q <= c1; ++q) {
-              const int slot = p.first_unit(q) > unit ? 0 : 1;
-              const float* from = a.part + (2 * static_cast<int64_t>(q) + slot) * (2 * kRows * kHalf) + b0 * kHalf + me;
-              float w0[16], w1[16];
+          // sums of kAt pairs from kOf CTAs' pieces at a time, so that their loads overlap
+          const auto join = [&](auto at_once, auto pieces) {
+            constexpr int kAt = decltype(at_once)::value, kOf = decltype(pieces)::value;
+            for (int b0 = 0; b0 < p.rows; b0 += kAt) {
+              float v[2][kAt] = {};
+              for (uint32_t q0 = c0; q0 <= c1; q0 += kOf) {
+                float w[kOf][2][kAt];
 #pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                w0[c] = b0 + c < p.rows ? __ldcg(from + c * kHalf) : 0.0f;
-                w1[c] = b0 + c < p.rows ? __ldcg(from + (kRows + c) * kHalf) : 0.0f;
+                for (int q = 0; q < kOf; ++q) {
+                  const float* from = a.part + static_cast<int64_t>(p.place(min(q0 + q, c1))) * (2 * kRows * kHalf) + b0 * kHalf + me;
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < kAt; ++c)
+                      w[q][h][c] = q0 + q <= c1 && b0 + c < p.rows ? __ldcg(from + (h * kRows + c) * kHalf) : 0.0f;
+                }
+#pragma unroll
+                for (int q = 0; q < kOf; ++q)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < kAt; ++c) v[h][c] += w[q][h][c];
               }
 #pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                v0[c] += w0[c];
-                v1[c] += w1[c];
-              }
+              for (int c = 0; c < kAt; ++c)
+                if (b0 + c < p.rows) put(b0 + c, v[0][c], v[1][c]);
             }
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (b0 + c < p.rows) put(b0 + c, v0[c], v1[c]);
-          }
+          };
+          if (p.rows <= 4) join(std::integral_constant<int, 4>(), std::integral_constant<int, 4>());
+          else join(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
         }
         named_bar_sync(1, 128);  // (`last` is read before it is written again)
       }
@@ -255,9 +262,7 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
 
 template <typename T, int kRows, bool kInner>
 cudaError_t launch_product(Args a, const hc_expert_mlp_t& p, int num_sms, cudaStream_t s) {
-  // (no more CTAs than there can be units of work)
-  const int64_t units = experts_um_tiles(p, kRows, kInner) * a.kblocks;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(num_sms, units));
+  const unsigned grid = static_cast<unsigned>(num_sms);
   const size_t smem = Cfg<kRows>::kSmem + bars_bytes(a.experts);
   const cudaError_t e = ensure_smem<few_kernel<T, kRows, kInner>>(smem);
   if (e != cudaSuccess) return e;

@@ -75,42 +75,61 @@ template <> __device__ __forceinline__ float saturate<__half>(float v) {
   return m > 65504.0f && m < INFINITY ? copysignf(65504.0f, v) : v;
 }
 
-// The pieces of work of a CTA (or a pair of them), the same for all its warps: with kSplit an equal run of all tiles' blocks
-// of inputs laid end to end, otherwise whole tiles in turn.
+// The pieces of work of a CTA (or a pair of them), the same for all its warps: whole tiles in turn, or, with kSplit, parts of
+// them. If there are no more tiles than CTAs, a tile is cut into as many parts of its blocks of inputs as leave every CTA at
+// most one (so that few CTAs wait for others' sums, and none twice; two thirds of the SMs can take what the memory gives);
+// otherwise all tiles' blocks, laid end to end, are cut into equal runs. (Units, blocks of inputs, are below 2^31 in number
+// where tiles are split: at most 2^17 pairs, and 2^19 blocks of features and inputs.)
 template <int kRows, bool kSplit> struct Pieces {
   const Args& a;
   const int32_t *bounds, *tiles;
-  int64_t at, end, units, ctas;
+  uint32_t at, end, units, ctas, each, rest, parts;  // parts: of a tile, 0 for runs
 
-  __device__ __forceinline__ Pieces(const Args& args, const Bars* bars, int cta, int count)
+  __device__ __forceinline__ Pieces(const Args& args, const Bars* bars, uint32_t cta, uint32_t count)
       : a(args), bounds(reinterpret_cast<const int32_t*>(bars + 1)), tiles(bounds + args.experts + 1) {
-    const int total = tiles[a.experts] * a.fblocks;
-    units = static_cast<int64_t>(total) * a.kblocks;
-    ctas = min(static_cast<int64_t>(count), kSplit ? units : total);  // that have work, at least a unit each
-    at = end = 0;
-    if (cta < ctas) {
-      at = kSplit ? first_unit(cta) : cta;
-      end = kSplit ? first_unit(cta + 1) : total;
+    const uint32_t total = static_cast<uint32_t>(tiles[a.experts]) * a.fblocks;
+    at = end = parts = 0;
+    if (!kSplit) {
+      ctas = count;
+      at = cta;
+      end = total;
+    } else if (total <= count) {
+      parts = total == 0 ? 1u : min(count / total, static_cast<uint32_t>(a.kblocks));
+      at = cta;
+      end = cta < total * parts ? cta + 1 : cta;
+    } else {
+      units = total * a.kblocks;
+      ctas = count;
+      each = units / ctas;
+      rest = units - each * ctas;
+      at = first_unit(cta);
+      end = first_unit(cta + 1);
     }
   }
-  __device__ __forceinline__ int64_t first_unit(int64_t cta) const { return cta * units / ctas; }
-  __device__ __forceinline__ int cta_of(int64_t unit) const { return static_cast<int>(((unit + 1) * ctas - 1) / units); }
+  // first_unit(cta) = cta * units / ctas
+  __device__ __forceinline__ uint32_t first_unit(uint32_t cta) const { return cta * each + cta * rest / ctas; }
 
   int tile, k0, k1;                  // blocks of inputs k0 .. k1 - 1 of this tile
   int expert, first, rows, feature;  // its pairs in the list, its first feature (of either half)
 
   __device__ __forceinline__ bool next(int features) {
     if (at >= end) return false;
-    if (kSplit) {
-      tile = static_cast<int>(at / a.kblocks);
-      k0 = static_cast<int>(at - static_cast<int64_t>(tile) * a.kblocks);
-      k1 = static_cast<int>(min(static_cast<int64_t>(a.kblocks), k0 + (end - at)));
-      at += k1 - k0;
-    } else {
+    if (!kSplit) {
       tile = static_cast<int>(at);
       k0 = 0;
       k1 = a.kblocks;
       at += ctas;
+    } else if (parts > 0) {
+      tile = static_cast<int>(at / parts);
+      const uint32_t part = at - tile * parts;
+      k0 = static_cast<int>(part * a.kblocks / parts);
+      k1 = static_cast<int>((part + 1) * a.kblocks / parts);
+      ++at;
+    } else {
+      tile = static_cast<int>(at / a.kblocks);
+      k0 = static_cast<int>(at - static_cast<uint32_t>(tile) * a.kblocks);
+      k1 = static_cast<int>(min(static_cast<uint32_t>(a.kblocks), k0 + (end - at)));
+      at += k1 - k0;
     }
     const int m = tile / a.fblocks;
     feature = (tile - m * a.fblocks) * features;
@@ -126,6 +145,22 @@ template <int kRows, bool kSplit> struct Pieces {
     return true;
   }
   __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == a.kblocks; }
+
+  // Where partial sums lie: two places to a CTA, the first for a piece that does not begin its tile (or is a part).
+  __device__ __forceinline__ int place(uint32_t cta) const {
+    return 2 * cta + (parts > 0 || first_unit(cta) > static_cast<uint32_t>(tile) * a.kblocks ? 0 : 1);
+  }
+  // The CTAs that have pieces of this tile, the first and the last.
+  __device__ __forceinline__ void sharers(uint32_t* c0, uint32_t* c1) const {
+    if (parts > 0) {
+      *c0 = tile * parts;
+      *c1 = *c0 + parts - 1;
+    } else {
+      const unsigned long long unit = static_cast<unsigned long long>(tile) * a.kblocks;
+      *c0 = static_cast<uint32_t>(((unit + 1) * ctas - 1) / units);
+      *c1 = static_cast<uint32_t>(((unit + a.kblocks) * ctas - 1) / units);
+    }
+  }
 };
 
 // Tiles of each expert, summed up, and the bounds.
