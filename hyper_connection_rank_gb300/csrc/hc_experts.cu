@@ -276,7 +276,7 @@ template <typename T, bool kInner> cudaError_t launch_general(const GeneralArgs&
 // multiple of sixteen). Bound: bytes, top_k + 1 rows a token.
 constexpr int kCombineWarps = 4;
 template <typename T, bool kInts>
-__global__ void __launch_bounds__(32 * kCombineWarps, 7)
+__global__ void __launch_bounds__(32 * kCombineWarps, kInts ? 7 : 5)
 combine_kernel(hc_expert_mlp_t p, const void* __restrict__ o, int64_t o_step, const uint8_t* __restrict__ exps, int64_t exp_step,
                bool vec) {
   pdl_wait();
@@ -285,47 +285,71 @@ combine_kernel(hc_expert_mlp_t p, const void* __restrict__ o, int64_t o_step, co
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5), t = unit / blocks;
   if (t >= p.tokens) return;
   const int c = static_cast<int>(unit - t * blocks) * 256 + lane * 8;
-  // which of the token's experts take part
-  const int id = lane < p.top_k ? p.experts[t * p.top_k + lane] : -1;
+  // lane j has the j-th expert's number, weight and (floats) planes; those that take part are in `valid`
+  const int64_t first = t * p.top_k;
+  const int id = lane < p.top_k ? p.experts[first + lane] : -1;
+  const float weight = lane < p.top_k ? p.weights[first + lane] : 0.0f;
+  const uint32_t planes = !kInts && exps != nullptr && lane < p.top_k ? exps[(first + lane) * exp_step + (c - lane * 8) / 256] : 1;
   const unsigned valid = __ballot_sync(0xffffffffu, id >= 0 && id < p.num_experts);
   const int count = __popc(valid);
-  if (c < p.hidden) {
-    T* out = static_cast<T*>(p.out) + t * p.out_stride;
-    float sum[8] = {};
-    constexpr int kAhead = kInts ? 8 : 4;
-    unsigned left = valid;
-    for (int j0 = 0; j0 < count; j0 += kAhead) {
-      uint4 q[kAhead][kInts ? 1 : 2];
-      uint32_t exp[kAhead];
-      float by[kAhead];
+  T* out = static_cast<T*>(p.out) + t * p.out_stride;
+  float sum[8] = {};
+  const bool have = c < p.hidden;
+  constexpr int kAhead = kInts ? 8 : 4;
+  const int64_t plane = p.tokens * p.top_k * o_step;
+  unsigned left = valid;
+  for (int j0 = 0; j0 < count; j0 += kAhead) {
+    uint4 q[kAhead][kInts ? 1 : 2], other[kAhead][2];  // other: the second plane, zeros without one
+    uint32_t exp[kAhead];
+    int from[kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (j0 + j < count) {
-          const int64_t pair = t * p.top_k + (__ffs(left) - 1);
-          left &= left - 1;
-          by[j] = p.weights[pair];
-          if constexpr (kInts) {
-            q[j][0] = *reinterpret_cast<const uint4*>(static_cast<const int16_t*>(o) + pair * o_step + c);
-            exp[j] = exps[pair * exp_step + c / 16];
-          } else {
-            q[j][0] = reinterpret_cast<const uint4*>(static_cast<const float*>(o) + pair * o_step + c)[0];
-            q[j][1] = reinterpret_cast<const uint4*>(static_cast<const float*>(o) + pair * o_step + c)[1];
-          }
+    for (int j = 0; j < kAhead; ++j) {
+      from[j] = __ffs(left) - 1;
+      left &= left - 1;
+      const bool take = j0 + j < count && have;
+      const int64_t at = (first + from[j]) * o_step + c;
+      if constexpr (kInts) {
+        if (take) {
+          q[j][0] = *reinterpret_cast<const uint4*>(static_cast<const int16_t*>(o) + at);
+          exp[j] = exps[(first + from[j]) * exp_step + c / 16];
         }
-      }
+      } else {
+        const float* f = static_cast<const float*>(o) + at;
+        exp[j] = __shfl_sync(0xffffffffu, planes, max(from[j], 0));
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (j0 + j < count) {
-          if constexpr (kInts) {
-            BlockFloat::add8(q[j][0], exp[j], by[j], sum);
-          } else {
-            const float* f = reinterpret_cast<const float*>(q[j]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] = fmaf(by[j], f[i], sum[i]);
-          }
+        for (int i = 0; i < 2; ++i) {
+          q[j][i] = take ? reinterpret_cast<const uint4*>(f)[i] : make_uint4(0, 0, 0, 0);
+          other[j][i] = take && exp[j] > 1 ? reinterpret_cast<const uint4*>(f + plane)[i] : make_uint4(0, 0, 0, 0);
         }
       }
     }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (j0 + j < count) {
+        const float by = __shfl_sync(0xffffffffu, weight, from[j]);
+        if constexpr (kInts) {
+          if (have) BlockFloat::add8(q[j][0], exp[j], by, sum);
+        } else {
+          float f[8], g[8];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            *reinterpret_cast<uint4*>(f + 4 * i) = q[j][i];
+            *reinterpret_cast<uint4*>(g + 4 * i) = other[j][i];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] += g[i];
+          for (uint32_t n = 2; n < exp[j] && have; ++n) {  // (of a few tiles only)
+            const float4* h = reinterpret_cast<const float4*>(static_cast<const float*>(o) + n * plane + (first + from[j]) * o_step + c);
+            const float4 x = h[0], y = h[1];
+            f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w, f[4] += y.x, f[5] += y.y, f[6] += y.z, f[7] += y.w;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] = fmaf(by, f[i], sum[i]);
+        }
+      }
+    }
+  }
+  if (have) {
     if (vec) {  // (out's rows are 16-byte aligned and hold whole vectors)
       if constexpr (sizeof(T) == 2) {
         st16(out + c, V8<T>::pack(sum));
@@ -353,14 +377,17 @@ cudaError_t launch_combine(const hc_expert_mlp_t& a, const void* o, int64_t o_st
 // ---------------------------------------------------------------- layout --
 
 struct Plan {
-  int rows;  // pairs to a tile of the tensor cores' products; 0: the general ones
-  int64_t tickets, inner_tickets;
+  int rows;  // pairs to a tile of the tensor cores' products, 32 or 256; 0: the general ones
+  int64_t tickets;
+  int planes;  // of o
   int64_t h_step, o_step, exp_step;
   size_t bounds, order, count, part, h, o, exps, total;
 };
 
-// Which products run, and where their buffers lie in the workspace. Tiles of 32, 64, 128 or 256 pairs by the pairs that an
-// expert has on average: REPLACE_RULE
+// Which products run, and where their buffers lie in the workspace. Tiles of 32 pairs with the weights as the first operand
+// or of 256 with the pairs as the first, by the pairs that an expert has on average: 64 experts of 2560 x 640 (six to a
+// token) took 130 and 147 us at 20 pairs, 142 and 150 at 28, 203 and 158 at 40; 16 of 1280 x 2560 took 78 and 93, 76 and
+// 100, 88 and 111, and 124 and 101 at 80.
 Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   const size_t pairs = static_cast<size_t>(a.tokens) * a.top_k;
   Plan l = {};
@@ -369,7 +396,7 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
                      (a.tokens == 1 || a.x_stride >= a.hidden);
   if (a.dtype != HC_F32 && aligned && steps && !(a.flags & HC_FLAG_FORCE_GENERAL)) {
     const size_t mean = pairs / a.num_experts;
-    l.rows = mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 128 ? 128 : 256;
+    l.rows = mean <= 32 ? 32 : 256;
   }
   size_t at = 0;
   const auto take = [&](size_t bytes) {
@@ -381,17 +408,21 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   l.order = take(pairs * sizeof(int32_t));
   l.h_step = l.rows ? static_cast<int64_t>(align_up(a.inner, 16)) : a.inner;
   l.o_step = static_cast<int64_t>(align_up(a.hidden, 16));
-  const bool few = l.rows > 0 && l.rows < 256;
+  const bool few = l.rows == 32;
   if (few) {
-    l.inner_tickets = experts_um_tiles(a, l.rows, true);
-    l.tickets = l.inner_tickets + experts_um_tiles(a, l.rows, false);
+    l.tickets = experts_um_tiles(a, l.rows, true);
     l.count = take(l.tickets * sizeof(unsigned int));
     l.part = take(static_cast<size_t>(num_sms) * 2 * 2 * l.rows * 128 * sizeof(float));
   }
   l.h = take(pairs * l.h_step * (l.rows ? 2 : 4));
-  l.o = take(pairs * l.o_step * (l.rows && !few ? 2 : 4));
+  l.planes = few ? (pairs <= 4096 ? 4 : 2) : 1;  // (two where runs are cut; four let few tiles be on more SMs)
+  l.o = take(pairs * l.o_step * (l.rows && !few ? 2 : 4) * l.planes);
   if (l.rows && !few) {
     l.exp_step = static_cast<int64_t>(align_up(a.hidden, 256)) / 16;
+    l.exps = take(pairs * l.exp_step);
+  }
+  if (few) {
+    l.exp_step = (a.hidden + 255) / 256;
     l.exps = take(pairs * l.exp_step);
   }
   l.total = at;
@@ -412,11 +443,11 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
   if constexpr (sizeof(T) == 2) {
     if (l.rows) {
       const ExpertUm u = {lists, ws + l.h, ws + l.o, ws + l.exps, l.h_step, l.o_step, l.exp_step,
-                          reinterpret_cast<float*>(ws + l.part), tickets, l.inner_tickets, l.rows};
+                          reinterpret_cast<float*>(ws + l.part), tickets, static_cast<int64_t>(pairs) * l.o_step, l.planes, l.rows};
       e = l.rows == 256 ? launch_experts_many(a, u, num_sms, s) : launch_experts_few(a, u, num_sms, s);
       if (e != cudaSuccess) return e;
       return l.rows == 256 ? launch_combine<T, true>(a, ws + l.o, l.o_step, ws + l.exps, l.exp_step, s)
-                           : launch_combine<T, false>(a, ws + l.o, l.o_step, nullptr, 0, s);
+                           : launch_combine<T, false>(a, ws + l.o, l.o_step, ws + l.exps, l.exp_step, s);
     }
   }
   const GeneralArgs g = {a, lists, reinterpret_cast<float*>(ws + l.h), reinterpret_cast<float*>(ws + l.o), l.o_step};

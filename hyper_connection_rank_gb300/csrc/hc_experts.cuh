@@ -89,12 +89,13 @@ struct BlockFloat {
 struct ExpertUm {
   ExpertLists lists;
   void *h, *o;             // (pairs, inner) of T in the list's order; (pairs, hidden) at the pairs' places
-  uint8_t* exps;           // exponents of o's elements, where it holds 16-bit integers
+  uint8_t* exps;           // many: exponents of o's elements, 16 to one; few: how many planes of o count, for each 256
   int64_t h_step, o_step, exp_step;  // elements from row to row, multiples of 16
-  float* part;             // partial sums
-  unsigned int* tickets;   // of the inner product's tiles, then of the outer one's; zero before the call
-  int64_t inner_tickets;
-  int rows;                // pairs to a tile: 32, 64 and 128 (few, o is float), 256 (many, o is 16-bit integers)
+  float* part;             // partial sums of the inner product
+  unsigned int* tickets;   // of the inner product's tiles; zero before the call
+  int64_t plane;           // elements from plane to plane of o (few)
+  int planes;
+  int rows;                // pairs to a tile: 32 (few, o is float) or 256 (many, o is 16-bit integers)
 };
 int64_t experts_um_tiles(const hc_expert_mlp_t& p, int rows, bool inner);
 cudaError_t launch_experts_few(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s);

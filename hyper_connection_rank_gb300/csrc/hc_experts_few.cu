@@ -25,28 +25,27 @@ namespace {
 
 using namespace um;
 
-template <int kRows> struct Cfg {
-  static constexpr int kStage = 2 * kHalfBytes + kRows * kBK * 2;
-  // (With 32 pairs, as few as let two CTAs share an SM, so that the outer product's are there, with their first weights, when
-  // the inner one's finish.)
-  static constexpr int kStages = kRows == 32 ? 3 : kRows == 64 ? 5 : 4;
-  static constexpr int kCols = 4 * kRows;  // of tensor memory: two accumulators of two halves each
-  static constexpr size_t kSmem = kStages * kStage + 1024;  // and the bars
-};
-template <int kRows, bool kInner> constexpr int kThreads = 192 + (kInner ? kRows : 0);
+constexpr int kRows = 32;  // pairs of a tile
+constexpr int kStage = 2 * kHalfBytes + kRows * kBK * 2;
+// As few stages as let two CTAs share an SM (up to some 470 experts), so that the outer product's are there, with their first
+// weights, when the inner one's finish.
+constexpr int kStages = 3;
+constexpr int kCols = 4 * kRows;  // of tensor memory: two accumulators of two halves each
+constexpr size_t kSmem = kStages * kStage + 1024;  // and the bars
+constexpr int kFetched = 8;  // units of 32 KB
+template <bool kInner> constexpr int kThreads = 192 + (kInner ? 32 : 0);
 
-template <typename T, int kRows, bool kInner>
-__global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const __grid_constant__ Args a) {
-  using C = Cfg<kRows>;
+template <typename T, bool kInner>
+__global__ void __launch_bounds__(kThreads<kInner>, 2) few_kernel(const __grid_constant__ Args a, const __grid_constant__ Args outer) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int kStep = kInner ? kHalf : 2 * kHalf;  // features from tile to tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  Bars* b = reinterpret_cast<Bars*>(smem + C::kStages * C::kStage);
+  Bars* b = reinterpret_cast<Bars*>(smem + kStages * kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0 && lane == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&b->full[i], kInner ? 1 + kRows : 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&b->full[i], kInner ? 1 + 32 : 1);
       mbar_init(&b->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -59,7 +58,7 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
     tma_prefetch_desc(&a.tm_w[1]);
   }
   if (warp == 1) {
-    tmem_alloc(&b->tmem_base, C::kCols);
+    tmem_alloc(&b->tmem_base, kCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -72,15 +71,15 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
     pdl_wait();
     pdl_trigger();
   }
-  count_tiles<kRows, kThreads<kRows, kInner>>(a, b);
+  count_tiles<kRows, kThreads<kInner>>(a, b);
   Pieces<kRows, true> p(a, b, blockIdx.x, gridDim.x);
   bool ok = true;
 
   if (warp == 0) {
     if (lane == 0) {
       const auto weights = [&](int st, int k, const Pieces<kRows, true>& p) {
-        uint8_t* w = smem + st * C::kStage;
-        mbar_arrive_expect_tx(&b->full[st], kInner ? 2 * kHalfBytes : C::kStage);
+        uint8_t* w = smem + st * kStage;
+        mbar_arrive_expect_tx(&b->full[st], kInner ? 2 * kHalfBytes : kStage);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           load_half(w + h * kHalfBytes, &a.tm_w[h], a.k_major, k * kBK, p.feature + (kInner ? 0 : h * kHalf), p.expert,
@@ -89,22 +88,33 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
       int early = 0;  // stages whose weights are on their way before the wait
       if (!kInner) {
         Pieces<kRows, true> q = p;
-        while (early < C::kStages && q.next(kStep))
-          for (int k = q.k0; k < q.k1 && early < C::kStages; ++k) weights(early++, k, q);
+        while (early < kStages && q.next(kStep))
+          for (int k = q.k0; k < q.k1 && early < kStages; ++k) weights(early++, k, q);
         pdl_wait();
         pdl_trigger();
       }
       int it = 0;
       while (ok && p.next(kStep)) {
         for (int k = p.k0; k < p.k1; ++k, ++it) {
-          const int st = it % C::kStages;
+          const int st = it % kStages;
           if (it >= early) {
-            ok = mbar_wait(&b->empty[st], ((it / C::kStages) & 1) ^ 1, &g_few_wait_timeouts);
+            ok = mbar_wait(&b->empty[st], ((it / kStages) & 1) ^ 1, &g_few_wait_timeouts);
             if (!ok) break;
             weights(st, k, p);
           }
-          if (!kInner) tma_load_2d(smem + st * C::kStage + 2 * kHalfBytes, &a.tm_rows, k * kBK, p.first, &b->full[st]);
+          if (!kInner) tma_load_2d(smem + st * kStage + 2 * kHalfBytes, &a.tm_rows, k * kBK, p.first, &b->full[st]);
         }
+      }
+      if (kInner) {
+        // While the last sums are formed and joined, the memory would have nothing to do: the outer product's weights of
+        // this place, past those that its stages hold, go to L2.
+        Pieces<kRows, true> q(outer, b, blockIdx.x, gridDim.x);
+        int unit = 0;
+        while (unit < kFetched && q.next(2 * kHalf))
+          for (int k = q.k0; k < q.k1 && unit < kFetched; ++k, ++unit)
+            if (unit >= kStages)
+              for (int h = 0; h < 2; ++h)
+                prefetch_half(&outer.tm_w[h], outer.k_major, k * kBK, q.feature + h * kHalf, q.expert);
       }
     }
   } else if (warp == 1) {
@@ -122,12 +132,12 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
         tc_fence_after();
         const uint32_t d = tmem + buf * 2 * kRows;
         for (int k = p.k0; k < p.k1; ++k, ++it) {
-          const int st = it % C::kStages;
-          ok = mbar_wait(&b->full[st], (it / C::kStages) & 1, &g_few_wait_timeouts);
+          const int st = it % kStages;
+          ok = mbar_wait(&b->full[st], (it / kStages) & 1, &g_few_wait_timeouts);
           if (!ok) break;
           if (kInner) fence_proxy_async();
           tc_fence_after();
-          const uint64_t so = static_cast<uint64_t>((st * C::kStage) >> 4);
+          const uint64_t so = static_cast<uint64_t>((st * kStage) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk) {
             const uint32_t add = k > p.k0 || kk > 0 ? 1u : 0u;
@@ -148,28 +158,27 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
     for (int acc = 0; ok && p.next(kStep); ++acc) {
       const int buf = acc & 1;
       const uint32_t d = tmem + buf * 2 * kRows + lanes;
-      int place[kRows / 32];  // of the pairs' results, in out
-#pragma unroll
-      for (int i = 0; i < kRows / 32; ++i) {
-        const int at = p.first + min(32 * i + lane, p.rows - 1);
-        place[i] = kInner ? at : a.order[at];
-      }
+      const int at = p.first + min(lane, p.rows - 1), place = kInner ? at : a.order[at];  // of the lane's pair, in out
       ok = mbar_wait(&b->acc_full[buf], (acc >> 1) & 1, &g_few_wait_timeouts);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       // this thread has feature `me` of both halves, a column for each pair
-      const bool whole = p.whole();
+      // (a piece of the outer product goes to a plane of its own, which the sum over a token's experts adds to the others)
+      const bool whole = !kInner || p.whole();
       const int f = p.feature + me;
+      float* o = static_cast<float*>(a.out) + (kInner ? 0 : p.piece() * a.plane);
       const auto put = [&](int c, float v0, float v1) {
-        const int64_t to = static_cast<int64_t>(__shfl_sync(0xffffffffu, place[c / 32], c % 32)) * a.out_step;
+        const int64_t to = static_cast<int64_t>(__shfl_sync(0xffffffffu, place, c)) * a.out_step;
         if (kInner) {
           if (f < a.features) stf(static_cast<T*>(a.out) + to + f, saturate<T>(gated(v0, v1)));
         } else {
-          if (f < a.features) static_cast<float*>(a.out)[to + f] = v0;
-          if (f + kHalf < a.features) static_cast<float*>(a.out)[to + f + kHalf] = v1;
+          if (f < a.features) o[to + f] = v0;
+          if (f + kHalf < a.features) o[to + f + kHalf] = v1;
         }
       };
+      if (!kInner && warp == 2 && lane < p.rows)
+        a.exps[place * a.exp_step + p.feature / (2 * kHalf)] = static_cast<uint8_t>(p.pieces());
       float* part = a.part + static_cast<int64_t>(p.place(blockIdx.x)) * (2 * kRows * kHalf) + me;
 #pragma unroll
       for (int c0 = 0; c0 < kRows; c0 += 16) {
@@ -237,17 +246,16 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
       }
     }
   } else if constexpr (kInner) {
-    const int group = warp - 6;
     Gather<T> g;
     int it = 0;
     while (ok && p.next(kStep)) {
-      g.begin(a, p.first, p.rows, group);
+      g.begin(a, p.first, p.rows, 0);
       for (int k = p.k0; k < p.k1; ++k, ++it) {
-        const int st = it % C::kStages;
-        if (lane == 0) ok = mbar_wait(&b->empty[st], ((it / C::kStages) & 1) ^ 1, &g_few_wait_timeouts);
+        const int st = it % kStages;
+        if (lane == 0) ok = mbar_wait(&b->empty[st], ((it / kStages) & 1) ^ 1, &g_few_wait_timeouts);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        g.copy(a, smem_addr(smem) + st * C::kStage + 2 * kHalfBytes, k * kBK, group, &b->full[st]);
+        g.copy(a, smem_addr(smem) + st * kStage + 2 * kHalfBytes, k * kBK, 0, &b->full[st]);
       }
     }
     cp_async_wait_all();
@@ -256,37 +264,28 @@ __global__ void __launch_bounds__(kThreads<kRows, kInner>, 1) few_kernel(const _
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kCols);
+    tmem_dealloc(tmem, kCols);
   }
 }
 
-template <typename T, int kRows, bool kInner>
-cudaError_t launch_product(Args a, const hc_expert_mlp_t& p, int num_sms, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(num_sms);
-  const size_t smem = Cfg<kRows>::kSmem + bars_bytes(a.experts);
-  const cudaError_t e = ensure_smem<few_kernel<T, kRows, kInner>>(smem);
+template <typename T, bool kInner>
+cudaError_t launch_product(const Args& a, const Args& outer, int num_sms, cudaStream_t s) {
+  const size_t smem = kSmem + bars_bytes(a.experts);
+  const cudaError_t e = ensure_smem<few_kernel<T, kInner>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(few_kernel<T, kRows, kInner>, dim3(grid), dim3(kThreads<kRows, kInner>), smem, s, 1, a);
+  return launch_pdl(few_kernel<T, kInner>, dim3(static_cast<unsigned>(num_sms)), dim3(kThreads<kInner>), smem, s, 1, a, outer);
 }
 
-template <typename T, int kRows>
-cudaError_t launch_both(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
-  for (const bool inner : {true, false}) {
-    Args a;
-    if (!fill_args(&a, p, u, inner, kRows)) return cudaErrorInvalidValue;
-    a.part = u.part;
-    a.tickets = u.tickets + (inner ? 0 : u.inner_tickets);
-    e = inner ? launch_product<T, kRows, true>(a, p, num_sms, s) : launch_product<T, kRows, false>(a, p, num_sms, s);
-    if (e != cudaSuccess) break;
-  }
-  return e;
-}
-
-template <typename T> cudaError_t launch_rows(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s) {
-  if (u.rows == 32) return launch_both<T, 32>(p, u, num_sms, s);
-  if (u.rows == 64) return launch_both<T, 64>(p, u, num_sms, s);
-  return launch_both<T, 128>(p, u, num_sms, s);
+template <typename T> cudaError_t launch_both(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s) {
+  Args inner, outer;
+  if (!fill_args(&inner, p, u, true, kRows) || !fill_args(&outer, p, u, false, kRows)) return cudaErrorInvalidValue;
+  inner.part = u.part;
+  inner.tickets = u.tickets;
+  inner.most_parts = inner.kblocks;
+  outer.plane = u.plane;
+  outer.most_parts = u.planes;
+  const cudaError_t e = launch_product<T, true>(inner, outer, num_sms, s);
+  return e != cudaSuccess ? e : launch_product<T, false>(outer, outer, num_sms, s);
 }
 
 }  // namespace
@@ -351,7 +350,7 @@ int64_t experts_um_tiles(const hc_expert_mlp_t& p, int rows, bool inner) {
 }
 
 cudaError_t launch_experts_few(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s) {
-  return p.dtype == HC_F16 ? launch_rows<__half>(p, u, num_sms, s) : launch_rows<__nv_bfloat16>(p, u, num_sms, s);
+  return p.dtype == HC_F16 ? launch_both<__half>(p, u, num_sms, s) : launch_both<__nv_bfloat16>(p, u, num_sms, s);
 }
 
 unsigned int read_experts_few_wait_timeouts(bool reset) {

@@ -43,11 +43,13 @@ struct Args {
   const void* x;               // inner: rows that are gathered, and their step
   int64_t x_step;
   void* out;                   // inner: h in the list's order; outer: o at the pairs' places
-  uint8_t* exps;               // (many, outer) an exponent for each 16 elements of o
+  uint8_t* exps;               // outer, many: an exponent for each 16 elements of o; few: the planes of each 256
   int64_t out_step, exp_step;  // elements from row to row of out, and of exps
-  float* part;                 // (few) [2 * CTAs][2 halves][rows][128], for tiles that a cut goes through
-  unsigned int* tickets;       // (few) of each tile: pieces that have been written
+  int64_t plane;               // (few, outer) elements from plane to plane of out
+  float* part;                 // (few, inner) [2 * CTAs][2 halves][rows][128], for tiles that a cut goes through
+  unsigned int* tickets;       // (few, inner) of each tile: pieces that have been written
   int experts, top_k, inputs, features, kblocks, fblocks, k_major;
+  int most_parts;              // (few) that a tile may be cut into
 };
 
 // Behind it in shared memory: the bounds, and the tiles of the experts before each (num_experts + 1 both).
@@ -78,12 +80,14 @@ template <> __device__ __forceinline__ float saturate<__half>(float v) {
 // The pieces of work of a CTA (or a pair of them), the same for all its warps: whole tiles in turn, or, with kSplit, parts of
 // them. If there are no more tiles than CTAs, a tile is cut into as many parts of its blocks of inputs as leave every CTA at
 // most one (so that few CTAs wait for others' sums, and none twice; two thirds of the SMs can take what the memory gives);
-// otherwise all tiles' blocks, laid end to end, are cut into equal runs. (Units, blocks of inputs, are below 2^31 in number
+// otherwise all tiles' blocks, laid end to end, are cut into equal runs, of which the pieces of cut tiles come first, so that
+// their sums are joined while whole tiles are still on their way. (Units, blocks of inputs, are below 2^31 in number
 // where tiles are split: at most 2^17 pairs, and 2^19 blocks of features and inputs.)
 template <int kRows, bool kSplit> struct Pieces {
   const Args& a;
   const int32_t *bounds, *tiles;
   uint32_t at, end, units, ctas, each, rest, parts;  // parts: of a tile, 0 for runs
+  uint32_t head, tail;                               // of a run: blocks of its first tile that are not its own, of its last that are
 
   __device__ __forceinline__ Pieces(const Args& args, const Bars* bars, uint32_t cta, uint32_t count)
       : a(args), bounds(reinterpret_cast<const int32_t*>(bars + 1)), tiles(bounds + args.experts + 1) {
@@ -94,7 +98,7 @@ template <int kRows, bool kSplit> struct Pieces {
       at = cta;
       end = total;
     } else if (total <= count) {
-      parts = total == 0 ? 1u : min(count / total, static_cast<uint32_t>(a.kblocks));
+      parts = total == 0 ? 1u : min(count / total, static_cast<uint32_t>(min(a.kblocks, a.most_parts)));
       at = cta;
       end = cta < total * parts ? cta + 1 : cta;
     } else {
@@ -102,8 +106,13 @@ template <int kRows, bool kSplit> struct Pieces {
       ctas = count;
       each = units / ctas;
       rest = units - each * ctas;
-      at = first_unit(cta);
-      end = first_unit(cta + 1);
+      // from here on in tiles: the whole ones are at .. end - 1
+      const uint32_t from = first_unit(cta), to = first_unit(cta + 1);
+      at = from / a.kblocks;
+      end = to / a.kblocks;
+      head = from - at * a.kblocks;
+      tail = to - end * a.kblocks;
+      at += head > 0;
     }
   }
   // first_unit(cta) = cta * units / ctas
@@ -113,23 +122,36 @@ template <int kRows, bool kSplit> struct Pieces {
   int expert, first, rows, feature;  // its pairs in the list, its first feature (of either half)
 
   __device__ __forceinline__ bool next(int features) {
-    if (at >= end) return false;
-    if (!kSplit) {
+    if (kSplit && parts == 0) {
+      if (tail > 0) {
+        tile = static_cast<int>(end);
+        k0 = 0;
+        k1 = static_cast<int>(tail);
+        tail = 0;
+      } else if (head > 0) {
+        tile = static_cast<int>(at - 1);
+        k0 = static_cast<int>(head);
+        k1 = a.kblocks;
+        head = 0;
+      } else {
+        if (at >= end) return false;
+        tile = static_cast<int>(at++);
+        k0 = 0;
+        k1 = a.kblocks;
+      }
+    } else if (at >= end) {
+      return false;
+    } else if (!kSplit) {
       tile = static_cast<int>(at);
       k0 = 0;
       k1 = a.kblocks;
       at += ctas;
-    } else if (parts > 0) {
+    } else {
       tile = static_cast<int>(at / parts);
       const uint32_t part = at - tile * parts;
       k0 = static_cast<int>(part * a.kblocks / parts);
       k1 = static_cast<int>((part + 1) * a.kblocks / parts);
       ++at;
-    } else {
-      tile = static_cast<int>(at / a.kblocks);
-      k0 = static_cast<int>(at - static_cast<uint32_t>(tile) * a.kblocks);
-      k1 = static_cast<int>(min(static_cast<uint32_t>(a.kblocks), k0 + (end - at)));
-      at += k1 - k0;
     }
     const int m = tile / a.fblocks;
     feature = (tile - m * a.fblocks) * features;
@@ -145,6 +167,11 @@ template <int kRows, bool kSplit> struct Pieces {
     return true;
   }
   __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == a.kblocks; }
+
+  // The number of pieces that this piece's tile is in, and which one this is. (Runs are no shorter than a tile, so that at
+  // most one cut goes through it.)
+  __device__ __forceinline__ int pieces() const { return parts > 0 ? parts : whole() ? 1 : 2; }
+  __device__ __forceinline__ int piece() const { return parts > 0 ? (at - 1) % parts : k0 > 0 ? 1 : 0; }
 
   // Where partial sums lie: two places to a CTA, the first for a piece that does not begin its tile (or is a part).
   __device__ __forceinline__ int place(uint32_t cta) const {
@@ -204,6 +231,19 @@ __device__ __forceinline__ void load_half(uint8_t* to, const CUtensorMap* map, b
   } else {
     tma_load_3d(to, map, n, k, expert, bar);
     tma_load_3d(to + kHalfBytes / 2, map, n + 64, k, expert, bar);
+  }
+}
+
+// The same half into L2 only.
+__device__ __forceinline__ void prefetch_half(const CUtensorMap* map, bool k_major, int k, int n, int expert) {
+  const auto fetch = [&](int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(expert) : "memory");
+  };
+  if (k_major) {
+    fetch(k, n);
+  } else {
+    fetch(n, k);
+    fetch(n + 64, k);
   }
 }
 
