@@ -11,6 +11,7 @@
 #include "hc_async.cuh"
 #include "hc_common.cuh"
 #include "hc_experts.cuh"
+#include "hc_two.cuh"
 #include "hc_vec.cuh"
 
 namespace hc {
@@ -102,7 +103,8 @@ lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, ExpertList
 
 constexpr int kGroup = 4, kGroups = 6, kTM = kGroup * kGroups;  // pairs of a tile, in groups that are left out if empty
 constexpr int kTN = 64, kTK = 8, kGenWarps = 4, kGenThreads = 32 * kGenWarps;
-constexpr int kAcc = kTM * 4;  // sums of a lane
+constexpr int kAcc = kTM * 4;       // sums of a lane
+constexpr int kRowStep = kTM + 4;  // rows of an input in shared memory (28 words: eight inputs' rows in different banks)
 
 struct GeneralArgs {
   hc_expert_mlp_t p;
@@ -111,161 +113,200 @@ struct GeneralArgs {
   int64_t o_step;
 };
 
+// Tiles of each expert's pairs (as few as hold them, cut evenly), summed up: upto[e] before expert e. All threads.
+__device__ __forceinline__ void count_even_tiles(const int32_t* bounds, int experts, int* upto) {
+  __shared__ int red[kGenWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = (experts + kGenThreads - 1) / kGenThreads;
+  const int lo = min(experts, static_cast<int>(threadIdx.x) * each), hi = min(experts, lo + each);
+  int mine = 0;
+  for (int e = lo; e < hi; ++e) mine += (bounds[e + 1] - bounds[e] + kTM - 1) / kTM;
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 31) red[warp] = before;
+  __syncthreads();
+  before -= mine;
+  for (int w = 0; w < warp; ++w) before += red[w];
+  for (int e = lo; e < hi; ++e) {
+    upto[e] = before;
+    before += (bounds[e + 1] - bounds[e] + kTM - 1) / kTM;
+  }
+  if (hi == experts) upto[experts] = before;  // (the same from every thread that has the last one or none)
+  __syncthreads();
+}
+
 template <typename T, bool kInner, bool kByInput> __global__ void __launch_bounds__(kGenThreads, 2) general_kernel(GeneralArgs g) {
   using In = typename std::conditional<kInner, T, float>::type;
   extern __shared__ __align__(16) float smem[];
   const hc_expert_mlp_t& p = g.p;
   pdl_wait();
   pdl_trigger();
-  const ExpertTile t = expert_tile_even(g.lists.bounds, p.num_experts, kTM, blockIdx.x);
-  if (t.rows == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int inputs = kInner ? p.hidden : p.inner, features = kInner ? p.inner : p.hidden;
-  const int n0 = blockIdx.y * kTN * (kInner ? 1 : 2);
   const int64_t is = kInner ? p.up_in_stride : p.down_in_stride, os = kInner ? p.up_out_stride : p.down_out_stride;
-  const int64_t expert = t.expert * (kInner ? p.up_expert_stride : p.down_expert_stride);
-  // [matrix or half][of the lane's two features]; with kByInput the lane reads input lane % 8 of features lane / 8, + 4, ...
-  const T* w[2][2];
-  bool have[2][2];
-  const int mine = kByInput ? lane / 8 : lane;
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int f = n0 + mine + 32 * j + (kInner ? 0 : kTN * m);
-      have[m][j] = f < features;
-      w[m][j] = static_cast<const T*>(kInner ? (m ? p.up : p.gate) : p.down) + expert + (have[m][j] ? f : 0) * os +
-                (kByInput ? lane % 8 : 0);
+  constexpr int kStep = kTN * (kInner ? 1 : 2);  // features of a unit
+  int* upto = reinterpret_cast<int*>(smem + kGenWarps * kAcc * 32);
+  count_even_tiles(g.lists.bounds, p.num_experts, upto);
+  const int blocks = (features + kStep - 1) / kStep, units = upto[p.num_experts] * blocks;
+  float* rows = smem + warp * (2 * kTK * kRowStep);
+  float* turned = smem + kGenWarps * (2 * kTK * kRowStep) + warp * (4 * 32 * kTK);  // weights on their way to their lanes
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int tile = unit / blocks, n0 = (unit - tile * blocks) * kStep;
+    int expert = 0;  // the last one whose tiles begin here or before (empty ones have none)
+    for (int hi = p.num_experts - 1; expert < hi;) {
+      const int mid = (expert + hi + 1) >> 1;
+      if (upto[mid] <= tile) expert = mid;
+      else hi = mid - 1;
     }
-  // the lane's six elements of a block of rows: input lane % 8 of rows lane / 8, + 4, ...
-  const In* x[6];
+    const int begin = g.lists.bounds[expert], pairs = g.lists.bounds[expert + 1] - begin;
+    const int each = (pairs + upto[expert + 1] - upto[expert] - 1) / (upto[expert + 1] - upto[expert]);
+    const int first = begin + (tile - upto[expert]) * each, count = min(each, begin + pairs - first);
+    if (count <= 0) continue;  // (even shares can leave the last tile nothing)
+    // [matrix or half][of the lane's two features]; with kByInput the lane reads input lane % 8 of features lane / 8, + 4, ...
+    const T* w[2][2];
+    bool have[2][2];
+    const int mine = kByInput ? lane / 8 : lane;
 #pragma unroll
-  for (int i = 0; i < 6; ++i) {
-    const int at = t.first + min(lane / 8 + 4 * i, t.rows - 1);
-    x[i] = kInner ? static_cast<const In*>(p.x) + static_cast<int64_t>(g.lists.order[at] / p.top_k) * p.x_stride
-                  : reinterpret_cast<const In*>(g.h) + static_cast<int64_t>(at) * p.inner;
-  }
-  float* rows = smem + warp * (2 * kTM * kTK);
-  float* turned = smem + kGenWarps * (2 * kTM * kTK) + warp * (4 * 32 * kTK);  // weights on their way to their lanes
-  const int groups = (t.rows + kGroup - 1) / kGroup;
-  float acc[kTM][2][2] = {};
-  float wn[kTK][2][2], xn[6];
-  const auto load = [&](int k0) {
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int i = 0; i < 6; ++i) xn[i] = k0 + lane % 8 < inputs ? ldf(x[i] + k0 + lane % 8) : 0.0f;
+      for (int j = 0; j < 2; ++j) {
+        const int f = n0 + mine + 32 * j + (kInner ? 0 : kTN * m);
+        have[m][j] = f < features;
+        w[m][j] = static_cast<const T*>(kInner ? (m ? p.up : p.gate) : p.down) +
+                  expert * (kInner ? p.up_expert_stride : p.down_expert_stride) + (have[m][j] ? f : 0) * os + (kByInput ? lane % 8 : 0);
+      }
+    // the lane's six elements of a block of rows: input lane % 8 of rows lane / 8, + 4, ...
+    const In* x[6];
 #pragma unroll
-    for (int k = 0; k < kTK; ++k)
+    for (int i = 0; i < 6; ++i) {
+      const int at = first + min(lane / 8 + 4 * i, count - 1);
+      x[i] = (kInner ? static_cast<const In*>(p.x) + static_cast<int64_t>(g.lists.order[at] / p.top_k) * p.x_stride
+                     : reinterpret_cast<const In*>(g.h) + static_cast<int64_t>(at) * p.inner) + lane % 8;
+    }
+    const int groups = (count + kGroup - 1) / kGroup;
+    Two acc[kTM / 2][2][2];  // of two rows each
+#pragma unroll
+    for (int r = 0; r < kTM / 2; ++r)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (kByInput) {
-            const bool in = k0 + lane % 8 < inputs && n0 + mine + 4 * k + 32 * j + (kInner ? 0 : kTN * m) < features;
-            wn[k][m][j] = in ? ldf(w[m][j] + k0 + 4 * k * os) : 0.0f;
-          } else {
-            wn[k][m][j] = have[m][j] && k0 + k < inputs ? ldf(w[m][j] + (k0 + k) * is) : 0.0f;
-          }
-        }
-  };
-  if (warp * kTK < inputs) load(warp * kTK);
-  int turn = 0;
-  for (int k0 = warp * kTK; k0 < inputs; k0 += kGenWarps * kTK, turn ^= 1) {
-    float* buf = rows + turn * (kTM * kTK);
+        for (int j = 0; j < 2; ++j) acc[r][m][j] = Two(0.0f);
+    float wn[kTK][2][2], xn[6];
+    const auto load = [&](int k0) {
 #pragma unroll
-    for (int i = 0; i < 6; ++i) buf[(lane / 8 + 4 * i) * kTK + lane % 8] = xn[i];
-    float wc[kTK][2][2];
-    if (kByInput) {
-      // feature f's inputs in 32 bytes, their halves exchanged for every other four features (no bank is hit twice)
+      for (int i = 0; i < 6; ++i) xn[i] = k0 + lane % 8 < inputs ? ldf(x[i] + k0) : 0.0f;
 #pragma unroll
       for (int k = 0; k < kTK; ++k)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (kByInput) {
+              const bool in = k0 + lane % 8 < inputs && n0 + mine + 4 * k + 32 * j + (kInner ? 0 : kTN * m) < features;
+              wn[k][m][j] = in ? ldf(w[m][j] + k0 + 4 * k * os) : 0.0f;
+            } else {
+              wn[k][m][j] = have[m][j] && k0 + k < inputs ? ldf(w[m][j] + (k0 + k) * is) : 0.0f;
+            }
+          }
+    };
+    __syncthreads();  // (the last unit's sums are read)
+    if (warp * kTK < inputs) load(warp * kTK);
+    int turn = 0;
+    for (int k0 = warp * kTK; k0 < inputs; k0 += kGenWarps * kTK, turn ^= 1) {
+      float* buf = rows + turn * (kTK * kRowStep);
+#pragma unroll
+      for (int i = 0; i < 6; ++i) buf[lane % 8 * kRowStep + lane / 8 + 4 * i] = xn[i];
+      float wc[kTK][2][2];
+      if (kByInput) {
+        // feature f's inputs in 32 bytes, their halves exchanged for every other four features (no bank is hit twice)
+#pragma unroll
+        for (int k = 0; k < kTK; ++k)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              turned[((m * 2 + j) * 32 + 4 * k + lane / 8) * 8 + ((lane % 8) ^ (4 * (k & 1)))] = wn[k][m][j];
+        __syncwarp();
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            turned[((m * 2 + j) * 32 + 4 * k + lane / 8) * 8 + ((lane % 8) ^ (4 * (k & 1)))] = wn[k][m][j];
-      __syncwarp();
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k4 = 0; k4 < kTK; k4 += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(turned + ((m * 2 + j) * 32 + lane) * 8 + (k4 ^ (lane & 4)));
-            wc[k4][m][j] = v.x, wc[k4 + 1][m][j] = v.y, wc[k4 + 2][m][j] = v.z, wc[k4 + 3][m][j] = v.w;
-          }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kTK; ++k)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) wc[k][m][j] = wn[k][m][j];
-    }
-    __syncwarp();
-    if (k0 + kGenWarps * kTK < inputs) load(k0 + kGenWarps * kTK);
-#pragma unroll
-    for (int q = 0; q < kGroups; ++q) {
-      if (q < groups) {
-#pragma unroll
-        for (int r = q * kGroup; r < (q + 1) * kGroup; r += 2) {
-#pragma unroll
-          for (int k4 = 0; k4 < kTK; k4 += 4) {
-            float xs[2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float4 v = *reinterpret_cast<const float4*>(buf + (r + i) * kTK + k4);
-              xs[i][0] = v.x, xs[i][1] = v.y, xs[i][2] = v.z, xs[i][3] = v.w;
+            for (int k4 = 0; k4 < kTK; k4 += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(turned + ((m * 2 + j) * 32 + lane) * 8 + (k4 ^ (lane & 4)));
+              wc[k4][m][j] = v.x, wc[k4 + 1][m][j] = v.y, wc[k4 + 2][m][j] = v.z, wc[k4 + 3][m][j] = v.w;
             }
+      } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kTK; ++k)
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+            for (int j = 0; j < 2; ++j) wc[k][m][j] = wn[k][m][j];
+      }
+      __syncwarp();
+      if (k0 + kGenWarps * kTK < inputs) load(k0 + kGenWarps * kTK);
 #pragma unroll
-                  for (int j = 0; j < 2; ++j) acc[r + i][m][j] = fmaf(xs[i][k], wc[k4 + k][m][j], acc[r + i][m][j]);
+      for (int q = 0; q < kGroups; ++q) {
+        if (q < groups) {
+#pragma unroll
+          for (int k = 0; k < kTK; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(buf + k * kRowStep + q * kGroup);
+            const Two xs[2] = {Two(v.x, v.y), Two(v.z, v.w)};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[2 * q + i][m][j] = fma2(xs[i], Two(wc[k][m][j]), acc[2 * q + i][m][j]);
           }
         }
       }
     }
-  }
-  __syncthreads();
+    __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kTM; ++r)
+    for (int r = 0; r < kTM / 2; ++r)
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (r < groups * kGroup) smem[(warp * kAcc + (r * 2 + m) * 2 + j) * 32 + lane] = acc[r][m][j];
-  __syncthreads();
-  const auto sum = [&](int r, int m, int f) {
-    float v = 0.0f;
+        for (int j = 0; j < 2; ++j)
+          if (2 * r < groups * kGroup) {
+            const float2 v = acc[r][m][j].get();
+            smem[(warp * kAcc + (2 * r * 2 + m) * 2 + j) * 32 + lane] = v.x;
+            smem[(warp * kAcc + ((2 * r + 1) * 2 + m) * 2 + j) * 32 + lane] = v.y;
+          }
+    __syncthreads();
+    const auto sum = [&](int r, int m, int f) {
+      float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kGenWarps; ++i) v += smem[(i * kAcc + (r * 2 + m) * 2 + (f >> 5)) * 32 + (f & 31)];
-    return v;
-  };
-  for (int i = threadIdx.x; i < t.rows * kTN; i += kGenThreads) {
-    const int r = i / kTN, f = i % kTN;
-    const int64_t at = t.first + r;
-    const float v0 = sum(r, 0, f), v1 = sum(r, 1, f);
-    if (kInner) {
-      if (n0 + f < features) g.h[at * p.inner + n0 + f] = v0 / (1.0f + expf(-v0)) * v1;
-    } else {
-      float* to = g.o + g.lists.order[at] * g.o_step + n0 + f;
-      if (n0 + f < features) to[0] = v0;
-      if (n0 + f + kTN < features) to[kTN] = v1;
+      for (int i = 0; i < kGenWarps; ++i) v += smem[(i * kAcc + (r * 2 + m) * 2 + (f >> 5)) * 32 + (f & 31)];
+      return v;
+    };
+    for (int i = threadIdx.x; i < count * kTN; i += kGenThreads) {
+      const int r = i / kTN, f = i % kTN;
+      const int64_t at = first + r;
+      const float v0 = sum(r, 0, f), v1 = sum(r, 1, f);
+      if (kInner) {
+        if (n0 + f < features) g.h[at * p.inner + n0 + f] = v0 / (1.0f + expf(-v0)) * v1;
+      } else {
+        float* to = g.o + g.lists.order[at] * g.o_step + n0 + f;
+        if (n0 + f < features) to[0] = v0;
+        if (n0 + f + kTN < features) to[kTN] = v1;
+      }
     }
   }
 }
 
-template <typename T, bool kInner> cudaError_t launch_general(const GeneralArgs& g, unsigned slots, cudaStream_t s) {
-  constexpr size_t smem = sizeof(float) * kGenWarps * kAcc * 32;  // (more than the rows take)
-  const int step = kInner ? kTN : 2 * kTN, features = kInner ? g.p.inner : g.p.hidden;
-  const dim3 grid(slots, (features + step - 1) / step);
+template <typename T, bool kInner> cudaError_t launch_general(const GeneralArgs& g, int num_sms, cudaStream_t s) {
+  // (the sums, which take more than the rows and weights before them, and the tiles)
+  const size_t smem = sizeof(float) * kGenWarps * kAcc * 32 + sizeof(int) * (g.p.num_experts + 1);
   const auto launch = [&](auto by_input) {
     constexpr bool kByInput = decltype(by_input)::value;
     const cudaError_t e = ensure_smem<general_kernel<T, kInner, kByInput>>(smem);
-    return e != cudaSuccess ? e : launch_pdl(general_kernel<T, kInner, kByInput>, grid, dim3(kGenThreads), smem, s, 1, g);
+    return e != cudaSuccess ? e : launch_pdl(general_kernel<T, kInner, kByInput>, dim3(2 * num_sms), dim3(kGenThreads), smem, s, 1, g);
   };
   return (kInner ? g.p.up_out_stride : g.p.down_out_stride) == 1 ? launch(std::false_type()) : launch(std::true_type());
 }
@@ -451,10 +492,9 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
     }
   }
   const GeneralArgs g = {a, lists, reinterpret_cast<float*>(ws + l.h), reinterpret_cast<float*>(ws + l.o), l.o_step};
-  const unsigned slots = static_cast<unsigned>(expert_slots(pairs, kTM, a.num_experts));
-  e = launch_general<T, true>(g, slots, s);
+  e = launch_general<T, true>(g, num_sms, s);
   if (e != cudaSuccess) return e;
-  e = launch_general<T, false>(g, slots, s);
+  e = launch_general<T, false>(g, num_sms, s);
   if (e != cudaSuccess) return e;
   return launch_combine<T, false>(a, ws + l.o, l.o_step, nullptr, 0, s);
 }

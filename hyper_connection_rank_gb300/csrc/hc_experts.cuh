@@ -1,5 +1,5 @@
 // What the kernels of the experts' layer share: the list of (token, choice)
-// pairs sorted by expert, and the tiles of its rows.
+// pairs sorted by expert, and the form of the experts' results on their way.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -100,37 +100,5 @@ struct ExpertUm {
 int64_t experts_um_tiles(const hc_expert_mlp_t& p, int rows, bool inner);
 cudaError_t launch_experts_few(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s);
 cudaError_t launch_experts_many(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s);
-
-// Tiles of up to `rows` rows of one expert's part of the list have numbers ("slots") that follow from the bounds without a
-// sum over experts: expert e's tiles are slots bounds[e] / rows + e, ... A slot past an expert's last tile is empty. There
-// are pairs / rows + num_experts slots.
-struct ExpertTile {
-  int expert;
-  int first;  // place in the list of its first row
-  int rows;   // 0: an empty slot
-};
-
-__host__ __device__ constexpr int64_t expert_slots(int64_t pairs, int rows, int experts) { return pairs / rows + experts; }
-
-__device__ __forceinline__ ExpertTile expert_tile(const int32_t* bounds, int experts, int rows, int slot) {
-  int lo = 0, hi = experts - 1;  // the last expert whose first slot is not after this one
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (bounds[mid] / rows + mid <= slot) lo = mid;
-    else hi = mid - 1;
-  }
-  const int begin = bounds[lo], end = bounds[lo + 1];
-  const int first = begin + (slot - (begin / rows + lo)) * rows;
-  return ExpertTile{lo, first, max(0, min(rows, end - first))};
-}
-
-// The same slots for an expert's rows cut evenly: as many tiles, of no more than `rows` rows.
-__device__ __forceinline__ ExpertTile expert_tile_even(const int32_t* bounds, int experts, int rows, int slot) {
-  const ExpertTile t = expert_tile(bounds, experts, rows, slot);
-  if (t.rows == 0) return t;
-  const int begin = bounds[t.expert], n = bounds[t.expert + 1] - begin, tiles = (n + rows - 1) / rows;
-  const int each = (n + tiles - 1) / tiles, first = begin + (t.first - begin) / rows * each;
-  return ExpertTile{t.expert, first, max(0, min(each, begin + n - first))};
-}
 
 }  // namespace hc

@@ -33,6 +33,7 @@
 #include "hc_async.cuh"
 #include "hc_common.cuh"
 #include "hc_experts_internal.h"
+#include "hc_two.cuh"
 
 namespace hc {
 namespace {
@@ -720,30 +721,6 @@ constexpr int kUnitBits = 13;              // a chunk's largest weight is 2^43 t
 __device__ const int kExp2Few[16] = {
     1073741824, 1121280436, 1170923762, 1222764986, 1276901417, 1333434672, 1392470869, 1454120821,
     1518500250, 1585730000, 1655936265, 1729250827, 1805811301, 1885761398, 1969251188, 2056437387};
-
-// Two floats in a register pair: one instruction for both.
-struct Two {
-  unsigned long long v;
-  __device__ __forceinline__ Two(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
-  __device__ __forceinline__ explicit Two(float x) : Two(x, x) {}
-  __device__ __forceinline__ float2 get() const {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-  }
-};
-__device__ __forceinline__ Two operator*(Two a, Two b) {
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-  return a;
-}
-__device__ __forceinline__ Two operator+(Two a, Two b) {
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-  return a;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.v) : "l"(a.v), "l"(b.v));
-  return c;
-}
 
 struct Weigh {
   const int* table;  // in shared memory
