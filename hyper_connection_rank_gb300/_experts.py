@@ -31,7 +31,7 @@ def _rows(name, t, dtype, device):
     (rows, cols), (step, inner) = t.shape, t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return rows, cols, step if rows > 1 else max(step, cols)
+    return rows, cols, step if rows > 1 else cols
 
 
 def _dense(name, t, shape, dtype, device):

@@ -433,8 +433,8 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   const size_t pairs = static_cast<size_t>(a.tokens) * a.top_k;
   Plan l = {};
   // (TMA steps from row to row and from expert to expert, so strides of 0 are not for it)
-  const bool steps = (a.num_experts == 1 || (a.up_expert_stride > 0 && a.down_expert_stride > 0)) &&
-                     (a.tokens == 1 || a.x_stride >= a.hidden);
+  const bool steps = (a.num_experts == 1 || (a.up_expert_stride > 0 && a.down_expert_stride > 0)) && a.up_in_stride > 0 &&
+                     a.up_out_stride > 0 && a.down_in_stride > 0 && a.down_out_stride > 0 && (a.tokens == 1 || a.x_stride >= a.hidden);
   if (a.dtype != HC_F32 && aligned && steps && !(a.flags & HC_FLAG_FORCE_GENERAL)) {
     const size_t mean = pairs / a.num_experts;
     l.rows = mean <= 32 ? 32 : 256;
@@ -456,7 +456,9 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
     l.part = take(static_cast<size_t>(num_sms) * 2 * 2 * l.rows * 128 * sizeof(float));
   }
   l.h = take(pairs * l.h_step * (l.rows ? 2 : 4));
-  l.planes = few ? (pairs <= 4096 ? 4 : 2) : 1;  // (two where runs are cut; four let few tiles be on more SMs)
+  // A plane of o for each piece that a tile of the outer product can be cut into: two where runs are cut, and four where so
+  // few tiles are possible that each can be on three SMs or more.
+  l.planes = few ? ((pairs + l.rows - 1) / l.rows * ((a.hidden + 255) / 256) * 3 <= static_cast<size_t>(num_sms) ? 4 : 2) : 1;
   l.o = take(pairs * l.o_step * (l.rows && !few ? 2 : 4) * l.planes);
   if (l.rows && !few) {
     l.exp_step = static_cast<int64_t>(align_up(a.hidden, 256)) / 16;
