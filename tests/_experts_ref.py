@@ -13,8 +13,9 @@ Experts. A sum of n products in float32 is off by at most 2 (n + 8) v S, S the s
 cores may cut off where they add, which is twice a rounding). With e_g and e_u those errors of the two inner products: silu's
 slope is at most 1.1, and the approximate exponential and quotient are off by 2^-20, so silu(g) is off by
 e_s = 1.1 e_g + 2^-20 |silu(g)| and h = silu(g) u by e_h = e_s (|u| + e_u) + |silu(g)| e_u + 2 v |h|; 16-bit kernels round it
-to T: u |h| more (and in float16 2^-25). o = h down: e_o = sum e_h |down| + 2 (inner + 8) v sum |h| |down|, and where it is
-stored in T, u |o| more. The sum over the chosen: sum |w| e_o + (top_k + 2) v sum |w o|, and the store: u |y| (2^-25).
+to T: u |h| more (and in float16 2^-25). o = h down: e_o = sum e_h |down| + 2 (inner + 8) v sum |h| |down|, and where 16-bit
+kernels keep it as integers of 16 bits with one exponent to sixteen, half a unit more: with the largest of them in 2^(e - 1) ..
+2^e the unit is 2^(e - 15) / (1 - 2^-14), so at most 2^-15 (1 + 2^-13) of the largest (2^-126 where all are below 2^-110). The sum over the chosen: sum |w| e_o + (top_k + 2) v sum |w o|, and the store: u |y| (2^-25).
 
 Tokens. A kernel's weight is off by 2^-37 of itself at most, so is each sum; where a comparison in the reference is closer than
 2^-35 the test would not tell anything, and the reference says so. Log-probabilities: a quotient of two integers rounded to
@@ -79,7 +80,7 @@ def route(logits, top_k, bias=None, scoring="softmax", groups=1, top_groups=None
 
 
 def experts(x, gate, up, down, ids, w, rounded=True, stored=True):
-    """(y, bound). rounded: h is rounded to T; stored: each expert's result is."""
+    """(y, bound). rounded: h is rounded to T; stored: each expert's result is kept in 16 bits with an exponent."""
     dt = x.dtype
     u = U[dt] if dt != torch.float32 else 0.0
     tiny = 2.0 ** -25 if dt == torch.float16 else 0.0
@@ -105,8 +106,9 @@ def experts(x, gate, up, down, ids, w, rounded=True, stored=True):
                 eh = eh + u * (h.abs() + eh) + tiny
             o = h @ d
             eo = eh @ d.abs() + 2 * (inner + 8) * V * (h.abs() @ d.abs())
-            if stored:
-                eo = eo + u * (o.abs() + eo) + tiny
+            if stored and dt != torch.float32:
+                most = torch.nn.functional.pad(o.abs() + eo, (0, -hidden % 16)).view(len(rows), -1, 16).amax(-1, keepdim=True)
+                eo = eo + (2.0 ** -15 * (1 + 2.0 ** -13) * most + 2.0 ** -126).expand(-1, -1, 16).flatten(1)[:, :hidden]
             c = w[rows, j].double()[:, None]
             y[rows] += c * o
             tol[rows] += c.abs() * eo

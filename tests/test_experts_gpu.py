@@ -74,7 +74,7 @@ def check(hc, args, flags=0, what="", **kw):
     (33, 4, 2, 264, 72), (61, 64, 6, 256, 128), (100, 5, 2, 136, 264), (131, 3, 1, 128, 448), (257, 2, 2, 200, 64),
     (300, 6, 3, 512, 384), (520, 4, 1, 64, 520), (900, 3, 2, 136, 712)])
 def test_mlp_sizes(hc, tokens, experts, k, hidden, inner, rows_out, dtype):
-    """Every form (tiles of 32, 64 and 128 pairs; float32), tiles that are not full, widths that no tile divides."""
+    """Every form (tiles of 32 and of 256 pairs; float32), tiles that are not full, widths that no tile divides."""
     check(hc, layer(1, tokens, experts, k, hidden, inner, dtype, rows_out), what="mlp")
 
 

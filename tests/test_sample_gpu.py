@@ -198,7 +198,7 @@ def test_captured_and_on_a_stream(hc):
 @pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=ids)
 @pytest.mark.parametrize("rows,vocab,scale", [(40, 50001, 2.0), (300, 4099, 3.0), (8, 262144, 1.0), (600, 2047, 0.3), (3, 400001, 6.0)])
 def test_whole_distribution(hc, rows, vocab, scale, dtype):
-    """Large calls that filter nothing: sums in fp32 first, rows that they cannot decide by exact ones."""
+    """Large calls that filter nothing, whose rows are read by chunks."""
     x = rnd(30, rows, vocab + 5, dtype=dtype, scale=scale)[:, 3:vocab + 3]
     check(hc, x, uniforms(31, rows))
     check(hc, x, uniforms(32, rows), temperature=0.7)
