@@ -91,19 +91,26 @@ lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, ExpertList
 
 // ------------------------------------------------------- general products --
 //
-// On the CUDA cores in fp32, for float32 and for any type, stride and alignment. A CTA has up to 24 pairs of one expert
-// and 64 features of gate and up (128 of down, as two halves of 64). Its four warps share the inputs among them, eight at a
-// time; a lane has two features of both matrices. A weight is used by one lane alone, so it goes from global memory to a
-// register, eight inputs ahead (where inputs are contiguous, by way of the warp's shared memory, so that eight lanes read
-// neighbouring inputs of a feature: a feature to a lane took three times as long); rows come through a warp's own shared memory, four inputs of a row to a broadcast load for
-// 16 multiply-adds. Sums of the four warps are added at the end, so that a sum of n products is four of n / 4 (one of n
-// was off by twice as much).
+// On the CUDA cores in fp32, for float32 and for any type, stride and alignment. A CTA takes units of up to 24 pairs of one
+// expert (its pairs are cut evenly) and 32 kPer features of gate and up (64 kPer of down, as two halves). Its four warps
+// share the inputs among them, eight at a time; a lane has kPer features of both matrices, and sums of two rows in one packed
+// multiply-add. A weight is used by one lane alone, so it goes from global memory to a register, eight inputs ahead (where
+// inputs are contiguous, by way of the warp's shared memory, so that eight lanes read neighbouring inputs of a feature: a
+// feature to a lane took three times as long). Rows come through a warp's own shared memory, an input of four rows to a
+// broadcast load for 4 kPer multiply-adds of two. Sums of the four warps are added at the end, so that a sum of n products is
+// four of n / 4 (one of n was off by twice as much).
 //
-// Bound: the CUDA cores' multiply-adds with rows to spare, the weights' bytes without. REPLACE_MEASURED_GENERAL
+// Bound: the CUDA cores' multiply-adds with rows to spare, the weights' bytes without. 131 tokens at three of 12 experts of
+// 1280 x 704 in fp32 take 57 and 33 us for the two products, 25 and 21 TFLOP/s, where the busiest SM has half as much again as
+// the average one; 2000 tokens take 529 and 289 us, 41 and 37 TFLOP/s of some 75.
+//
+// Two features to a lane need fewer loads to a multiply-add, one leaves registers for a third CTA to an SM and gives twice
+// as many units: with one and two, 131 tokens took 57 and 62 us (inner) and 33 and 38 (outer; 73 and 90, 41 and 50 with the
+// inputs contiguous), 300 tokens 109 and 107, 60 and 63, 600 tokens 200 and 174, 99 and 101, 2000 tokens 625 and 529, 319
+// and 289. One is for calls that have fewer units of two than two rounds of CTAs.
 
 constexpr int kGroup = 4, kGroups = 6, kTM = kGroup * kGroups;  // pairs of a tile, in groups that are left out if empty
-constexpr int kTN = 64, kTK = 8, kGenWarps = 4, kGenThreads = 32 * kGenWarps;
-constexpr int kAcc = kTM * 4;       // sums of a lane
+constexpr int kTK = 8, kGenWarps = 4, kGenThreads = 32 * kGenWarps;
 constexpr int kRowStep = kTM + 4;  // rows of an input in shared memory (28 words: eight inputs' rows in different banks)
 
 struct GeneralArgs {
@@ -138,7 +145,10 @@ __device__ __forceinline__ void count_even_tiles(const int32_t* bounds, int expe
   __syncthreads();
 }
 
-template <typename T, bool kInner, bool kByInput> __global__ void __launch_bounds__(kGenThreads, 2) general_kernel(GeneralArgs g) {
+template <typename T, bool kInner, bool kByInput, int kPer>
+__global__ void __launch_bounds__(kGenThreads, kPer == 1 ? 3 : 2) general_kernel(GeneralArgs g) {
+  constexpr int kTN = 32 * kPer;
+  constexpr int kAcc = kTM * 2 * kPer;  // sums of a lane
   using In = typename std::conditional<kInner, T, float>::type;
   extern __shared__ __align__(16) float smem[];
   const hc_expert_mlp_t& p = g.p;
@@ -152,7 +162,7 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
   count_even_tiles(g.lists.bounds, p.num_experts, upto);
   const int blocks = (features + kStep - 1) / kStep, units = upto[p.num_experts] * blocks;
   float* rows = smem + warp * (2 * kTK * kRowStep);
-  float* turned = smem + kGenWarps * (2 * kTK * kRowStep) + warp * (4 * 32 * kTK);  // weights on their way to their lanes
+  float* turned = smem + kGenWarps * (2 * kTK * kRowStep) + warp * (2 * kPer * 32 * kTK);  // weights on their way to their lanes
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int tile = unit / blocks, n0 = (unit - tile * blocks) * kStep;
     int expert = 0;  // the last one whose tiles begin here or before (empty ones have none)
@@ -166,13 +176,13 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
     const int first = begin + (tile - upto[expert]) * each, count = min(each, begin + pairs - first);
     if (count <= 0) continue;  // (even shares can leave the last tile nothing)
     // [matrix or half][of the lane's two features]; with kByInput the lane reads input lane % 8 of features lane / 8, + 4, ...
-    const T* w[2][2];
-    bool have[2][2];
+    const T* w[2][kPer];
+    bool have[2][kPer];
     const int mine = kByInput ? lane / 8 : lane;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kPer; ++j) {
         const int f = n0 + mine + 32 * j + (kInner ? 0 : kTN * m);
         have[m][j] = f < features;
         w[m][j] = static_cast<const T*>(kInner ? (m ? p.up : p.gate) : p.down) +
@@ -187,14 +197,14 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
                      : reinterpret_cast<const In*>(g.h) + static_cast<int64_t>(at) * p.inner) + lane % 8;
     }
     const int groups = (count + kGroup - 1) / kGroup;
-    Two acc[kTM / 2][2][2];  // of two rows each
+    Two acc[kTM / 2][2][kPer];  // of two rows each
 #pragma unroll
     for (int r = 0; r < kTM / 2; ++r)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[r][m][j] = Two(0.0f);
-    float wn[kTK][2][2], xn[6];
+        for (int j = 0; j < kPer; ++j) acc[r][m][j] = Two(0.0f);
+    float wn[kTK][2][kPer], xn[6];
     const auto load = [&](int k0) {
 #pragma unroll
       for (int i = 0; i < 6; ++i) xn[i] = k0 + lane % 8 < inputs ? ldf(x[i] + k0) : 0.0f;
@@ -203,7 +213,7 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < kPer; ++j) {
             if (kByInput) {
               const bool in = k0 + lane % 8 < inputs && n0 + mine + 4 * k + 32 * j + (kInner ? 0 : kTN * m) < features;
               wn[k][m][j] = in ? ldf(w[m][j] + k0 + 4 * k * os) : 0.0f;
@@ -219,7 +229,7 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
       float* buf = rows + turn * (kTK * kRowStep);
 #pragma unroll
       for (int i = 0; i < 6; ++i) buf[lane % 8 * kRowStep + lane / 8 + 4 * i] = xn[i];
-      float wc[kTK][2][2];
+      float wc[kTK][2][kPer];
       if (kByInput) {
         // feature f's inputs in 32 bytes, their halves exchanged for every other four features (no bank is hit twice)
 #pragma unroll
@@ -227,16 +237,16 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              turned[((m * 2 + j) * 32 + 4 * k + lane / 8) * 8 + ((lane % 8) ^ (4 * (k & 1)))] = wn[k][m][j];
+            for (int j = 0; j < kPer; ++j)
+              turned[((m * kPer + j) * 32 + 4 * k + lane / 8) * 8 + ((lane % 8) ^ (4 * (k & 1)))] = wn[k][m][j];
         __syncwarp();
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < kPer; ++j)
 #pragma unroll
             for (int k4 = 0; k4 < kTK; k4 += 4) {
-              const float4 v = *reinterpret_cast<const float4*>(turned + ((m * 2 + j) * 32 + lane) * 8 + (k4 ^ (lane & 4)));
+              const float4 v = *reinterpret_cast<const float4*>(turned + ((m * kPer + j) * 32 + lane) * 8 + (k4 ^ (lane & 4)));
               wc[k4][m][j] = v.x, wc[k4 + 1][m][j] = v.y, wc[k4 + 2][m][j] = v.z, wc[k4 + 3][m][j] = v.w;
             }
       } else {
@@ -245,7 +255,7 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) wc[k][m][j] = wn[k][m][j];
+            for (int j = 0; j < kPer; ++j) wc[k][m][j] = wn[k][m][j];
       }
       __syncwarp();
       if (k0 + kGenWarps * kTK < inputs) load(k0 + kGenWarps * kTK);
@@ -261,7 +271,7 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
 #pragma unroll
               for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[2 * q + i][m][j] = fma2(xs[i], Two(wc[k][m][j]), acc[2 * q + i][m][j]);
+                for (int j = 0; j < kPer; ++j) acc[2 * q + i][m][j] = fma2(xs[i], Two(wc[k][m][j]), acc[2 * q + i][m][j]);
           }
         }
       }
@@ -272,17 +282,17 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < kPer; ++j)
           if (2 * r < groups * kGroup) {
             const float2 v = acc[r][m][j].get();
-            smem[(warp * kAcc + (2 * r * 2 + m) * 2 + j) * 32 + lane] = v.x;
-            smem[(warp * kAcc + ((2 * r + 1) * 2 + m) * 2 + j) * 32 + lane] = v.y;
+            smem[(warp * kAcc + (2 * r * 2 + m) * kPer + j) * 32 + lane] = v.x;
+            smem[(warp * kAcc + ((2 * r + 1) * 2 + m) * kPer + j) * 32 + lane] = v.y;
           }
     __syncthreads();
     const auto sum = [&](int r, int m, int f) {
       float v = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kGenWarps; ++i) v += smem[(i * kAcc + (r * 2 + m) * 2 + (f >> 5)) * 32 + (f & 31)];
+      for (int i = 0; i < kGenWarps; ++i) v += smem[(i * kAcc + (r * 2 + m) * kPer + (f >> 5)) * 32 + (f & 31)];
       return v;
     };
     for (int i = threadIdx.x; i < count * kTN; i += kGenThreads) {
@@ -301,14 +311,21 @@ template <typename T, bool kInner, bool kByInput> __global__ void __launch_bound
 }
 
 template <typename T, bool kInner> cudaError_t launch_general(const GeneralArgs& g, int num_sms, cudaStream_t s) {
-  // (the sums, which take more than the rows and weights before them, and the tiles)
-  const size_t smem = sizeof(float) * kGenWarps * kAcc * 32 + sizeof(int) * (g.p.num_experts + 1);
-  const auto launch = [&](auto by_input) {
+  const auto launch = [&](auto by_input, auto per) {
     constexpr bool kByInput = decltype(by_input)::value;
-    const cudaError_t e = ensure_smem<general_kernel<T, kInner, kByInput>>(smem);
-    return e != cudaSuccess ? e : launch_pdl(general_kernel<T, kInner, kByInput>, dim3(2 * num_sms), dim3(kGenThreads), smem, s, 1, g);
+    constexpr int kPer = decltype(per)::value;
+    // (the sums, which take more than the rows and weights before them, and the tiles)
+    const size_t smem = sizeof(float) * kGenWarps * kTM * 2 * kPer * 32 + sizeof(int) * (g.p.num_experts + 1);
+    const cudaError_t e = ensure_smem<general_kernel<T, kInner, kByInput, kPer>>(smem);
+    const dim3 grid((kPer == 1 ? 3 : 2) * num_sms);
+    return e != cudaSuccess ? e : launch_pdl(general_kernel<T, kInner, kByInput, kPer>, grid, dim3(kGenThreads), smem, s, 1, g);
   };
-  return (kInner ? g.p.up_out_stride : g.p.down_out_stride) == 1 ? launch(std::false_type()) : launch(std::true_type());
+  const int64_t pairs = g.p.tokens * g.p.top_k, step = kInner ? 64 : 128, features = kInner ? g.p.inner : g.p.hidden;
+  const int64_t units = (pairs / kTM + std::min<int64_t>(pairs, g.p.num_experts) / 2 + 1) * ((features + step - 1) / step);
+  const auto one = [&](auto by_input) {
+    return units < 4 * num_sms ? launch(by_input, std::integral_constant<int, 1>()) : launch(by_input, std::integral_constant<int, 2>());
+  };
+  return (kInner ? g.p.up_out_stride : g.p.down_out_stride) == 1 ? one(std::false_type()) : one(std::true_type());
 }
 
 // ---------------------------------------------------------------- combine --
