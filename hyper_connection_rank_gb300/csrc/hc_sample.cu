@@ -1,33 +1,32 @@
 // The choice of the next tokens (hc_token_sample).
 //
-// A cluster of CTAs takes a row and reads it once: each CTA keeps its slice of the
-// row in shared memory, where every later pass finds it. The steps are
+// Three kernels. Two are for what most calls ask, and leave what they cannot decide to the third, which decides every row:
+//
+//   pick_kernel    rows that filter, where a few hundred tokens at most stay
+//   stream_kernel  calls that filter nothing, from 2^20 logits on
+//   sample_kernel  any row: all of a small call that filters nothing, otherwise what the others have left undecided
+//
+// In the third a cluster of CTAs takes a row and reads it once: each CTA keeps its slice of the row in shared memory, where
+// every later pass finds it. The steps are
 //
 //   1. the largest logit m and its first index;
 //   2. with top_k, the k-th token in the order (logit falling, index rising);
 //   3. with top_p, the last token of that order that stays;
 //   4. the sum of the weights that stay, per warp, CTA and row;
-//   5. the token: the CTA, the warp, the lane and at last the element in which the
-//      cumulated weight passes uniform * sum.
+//   5. the token: the CTA, the warp, the lane and at last the element in which the cumulated weight passes uniform * sum.
 //
-// Steps 2 and 3 find the first element of the order at which a cumulated value
-// (1 each, or the weights) reaches a target: a histogram over 2048 equal steps of
-// the exponent, merged over the cluster, then histograms over the logits' bits
-// within the step that the target falls into, until one value is left; among
-// elements of that value the index decides. If no more than 2048 elements reach
-// that step, they are listed and sorted by one CTA instead, which then finishes the
-// row by itself.
+// Steps 2 and 3 find the first element of the order at which a cumulated value (1 each, or the weights) reaches a target: a
+// histogram over 2048 equal steps of the exponent, merged over the cluster, then histograms over the logits' bits within the
+// step that the target falls into, until one value is left; among elements of that value the index decides. If no more than
+// 2048 elements reach that step, they are listed and sorted by one CTA instead, which then finishes the row by itself.
 //
-// Weights are integers, 2^43 for the largest logit: integer sums have one result
-// in any order, whatever threads, warps and CTAs make of it, and a row of 409600
-// weights stays below 2^62. A weight is 2^-y with y = (m - x) log2(e) / t formed
-// in two fp32 parts; y = (64 n + i + f) / 64, and 2^-y = 2^-n T[i] (1 + q), where T
-// is a table and q = 2^(-f/64) - 1 a polynomial in fp32 whose leading term is
-// kept apart, so that the whole is good to 2^-38 of itself (fp32's 2^-24 would
-// choose another token than the definition once in some thousand rows of 10^5
-// tokens; fp64 runs at 1/64 of the rate here).
+// Weights are integers, 2^43 for the largest logit: integer sums have one result in any order, whatever threads, warps and
+// CTAs make of it, and a row of 409600 weights stays below 2^62. A weight is 2^-y with y = (m - x) log2(e) / t formed in two
+// fp32 parts; y = (64 n + i + f) / 64, and 2^-y = 2^-n T[i] (1 + q), where T is a table and q = 2^(-f/64) - 1 a polynomial in
+// fp32 whose leading term is kept apart, so that the whole is good to 2^-38 of itself (fp32's 2^-24 would choose another
+// token than the definition once in some thousand rows of 10^5 tokens; fp64 runs at 1/64 of the rate here).
 //
-// REPLACE_MEASURED
+// Bound: latency. A row of 131072 with top_p takes this kernel some 50 us, of which 4 are the row's bytes.
 #include <algorithm>
 
 #include "hc_async.cuh"
@@ -708,6 +707,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
 // within 2^-30 of itself (equal logits have equal weights). Chunks' sums are then shifted to the row's largest n and added,
 // and the chunk in which they pass uniform * sum is read again by one warp.
 //
+// Bound: instructions, some 19 to a logit, two logits in packed ones where there are such. 256 rows of 200003 fp32 logits
+// (205 MB) take 84 us, 2.4 TB/s; their bytes alone would take 30. Weights to within 2^-24 by the exponential unit and fp32
+// sums, with fp64 for what those cannot decide, took longer, since some rows in a call always are too close.
+//
 // Rows with anything that this does not hold for (an infinite largest logit, one above 512 log2 units in size, where c's
 // parts no longer reach, no logit at all, a temperature of 0) keep kUndecided and are the other kernel's.
 
@@ -937,9 +940,15 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, kStreamC
 // Most rows that filter come down to a few tokens, and for those neither a copy of the row nor a histogram of it is needed.
 // Each of a CTA's 1024 threads keeps the largest of its logits. The k-th largest logit is not below the k-th largest of the
 // threads' (which a histogram of those finds, to within a step), and min_p says how far down it goes; threads whose largest
-// reaches that far look through theirs again and list what does. For top_p without top_k the 128-th takes the place of the
-// k-th, and it has to turn out that the listed weights come to p of all. One CTA finishes the row: with no more than 512
-// candidates, each looks at all others. Rows with more keep kUndecided.
+// reaches that far have theirs looked through again, and what reaches as far is listed. For top_p without top_k the 128-th
+// takes the place of the k-th, and it has to turn out that the listed weights come to p of all. One CTA finishes the row:
+// with no more than 512 candidates, each is compared with all others. Rows with more keep kUndecided.
+//
+// Bound: latency, of the logits' bytes (1 to 2 us of them) and of four or five steps of a row's CTAs together. 64 rows of
+// 131072 fp32 logits with top_k, top_p and min_p take 15 us (33.6 MB: 4.9 us): 2.8 until all are read, 1.3 for the largest, 2 for the
+// border, 2 for the list, 3 to finish, and 2 for the next kernel to see that nothing is left. One row of 131072 bf16 logits with
+// top_p takes 20 us, 5 of them for the weights of all. (Dealing out the vectors that are looked through again to all threads
+// took 64 rows from 22 to 15 us; a histogram for each CTA rather than the first one's for all, one row from 23 to 20.)
 
 constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32;
 constexpr int kPicked = 512;   // candidates at most
@@ -951,10 +960,11 @@ struct PickShared {
   Params params;
   u64 tops[kMaxCluster], sums[kMaxCluster];
   u64 red[kPickWarps];
-  uint32_t hist[kBins];
+  alignas(8) uint32_t hist[kBins];
   int border;
-  uint32_t listed;
+  uint32_t listed, looking;
   u64 list[kPicked], weights[kPicked];
+  uint16_t who[kPickThreads];  // threads whose logits are looked through again
 };
 
 __device__ __forceinline__ uint32_t add_cluster(uint32_t addr, uint32_t v) {
@@ -964,6 +974,12 @@ __device__ __forceinline__ uint32_t add_cluster(uint32_t addr, uint32_t v) {
 }
 __device__ __forceinline__ void st_cluster32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint2 ld_cluster2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ u64 pick_sum(PickShared& sh, u64 v) {
@@ -985,6 +1001,7 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
   if (tid < 64) sh.table[tid] = kExp2[tid];
   if (tid == 64) sh.listed = 0;
   if (tid == 65) sh.border = -1;
+  if (tid == 66) sh.looking = 0;
   pdl_wait();
   pdl_trigger();
   if (tid == kPickThreads - 1) row_params(a, r, &sh.params);
@@ -1057,11 +1074,15 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
   int bin = cut_m ? p.step : kBins;
   const uint32_t some = cut_k ? p.k : kTryP;
   if ((cut_k || cut_p) && some <= kMostK) {
-    // the first CTA has the histogram
-    if (arg >= 0) add_cluster(mapa_shared(smem_addr(&sh.hist[mine]), 0), 1u);
+    if (arg >= 0) atomicAdd(&sh.hist[mine], 1u);
     cluster_sync_all();
     if (rank == 0) {
-      const uint32_t n0 = sh.hist[2 * tid], n1 = sh.hist[2 * tid + 1];
+      uint32_t n0 = 0, n1 = 0;
+      for (int i = 0; i < ctas; ++i) {
+        const uint2 n = ld_cluster2(mapa_shared(smem_addr(&sh.hist[2 * tid]), i));
+        n0 += n.x;
+        n1 += n.y;
+      }
       const u64 upto = warp_scan_u64(n0 + n1);
       if (lane == 31) sh.red[warp] = upto;
       __syncthreads();
@@ -1081,14 +1102,26 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
     sum = pick_sum(sh, sum);
     if (tid == 0) st_cluster(mapa_shared(smem_addr(&sh.sums[rank]), 0), sum);
   }
-  if (mine <= bin) {
-    const uint32_t count = mapa_shared(smem_addr(&sh.listed), 0), list = mapa_shared(smem_addr(sh.list), 0);
-    visit([&](int i, float x) {
-      if (x > -INFINITY && scale.step(x) <= bin) {
-        const uint32_t at = add_cluster(count, 1u);
-        if (at < kPicked) st_cluster(list + 8 * at, static_cast<u64>(~key_of(x)) << 32 | static_cast<uint32_t>(i));
-      }
-    });
+  // (their vectors are dealt out to all threads, so that all are on their way at once)
+  const uint32_t ballot = __ballot_sync(0xffffffffu, mine <= bin);
+  uint32_t place0 = lane == 0 && ballot != 0 ? atomicAdd(&sh.looking, __popc(ballot)) : 0u;
+  place0 = __shfl_sync(0xffffffffu, place0, 0);
+  if (mine <= bin) sh.who[place0 + __popc(ballot & ((1u << lane) - 1u))] = static_cast<uint16_t>(tid);
+  __syncthreads();
+  {
+    const uint32_t at_most = mapa_shared(smem_addr(&sh.listed), 0), list = mapa_shared(smem_addr(sh.list), 0);
+    const int turns = (v1 - v0 + kPickThreads - 1) / kPickThreads, items = static_cast<int>(sh.looking) * turns;
+#pragma unroll 1
+    for (int item = tid; item < items; item += kPickThreads) {
+      const int which = item / turns, v = v0 + sh.who[which] + (item - which * turns) * kPickThreads;
+      if (v < v1)
+        one_vector(v, [&](int i, float x) {
+          if (x > -INFINITY && scale.step(x) <= bin) {
+            const uint32_t at = add_cluster(at_most, 1u);
+            if (at < kPicked) st_cluster(list + 8 * at, static_cast<u64>(~key_of(x)) << 32 | static_cast<uint32_t>(i));
+          }
+        });
+    }
   }
   cluster_sync_all();
   if (rank != 0) return;
@@ -1097,21 +1130,29 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
     if (tid == 0) a.tokens[r] = kUndecided;
     return;
   }
-  // in order, the first k stay, of those the ones before which less than p of the sum lies, of those the ones not below least
-  const bool have = tid < count;
-  const u64 me = have ? sh.list[tid] : 0;
+  // In order, the first k stay, of those the ones before which less than p of the sum lies, of those the ones not below least.
+  // `share` neighbouring threads have a candidate, each looks at every share-th other one, and the first has the result.
+  int share = 2;
+  while (share < 32 && 2 * share * count <= kPickThreads) share *= 2;
+  const int mate = tid & (share - 1), own = tid / share;
+  const bool have = own < count && mate == 0;
+  const u64 me = own < count ? sh.list[own] : 0;
   u64 w = have ? scale.weight(value_of(~static_cast<uint32_t>(me >> 32))) : 0;
-  if (have) sh.weights[tid] = w;
+  if (have) sh.weights[own] = w;
   const u64 listed = pick_sum(sh, w);
   u64 before = 0;
   uint32_t place = 0;
-  if (have) {
+  if (own < count) {
 #pragma unroll 4
-    for (int j = 0; j < count; ++j)
+    for (int j = mate; j < count; j += share)
       if (sh.list[j] < me) {
         before += sh.weights[j];
         ++place;
       }
+  }
+  for (int o = 1; o < share; o <<= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    place += __shfl_xor_sync(0xffffffffu, place, o);
   }
   u64 goal = ~0ull;
   if (cut_k && place >= p.k) w = 0;
@@ -1130,16 +1171,18 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
   }
   if (before >= goal || w < p.least) w = 0;
   const u64 all = pick_sum(sh, w);  // (with barriers, behind which all have read the weights)
-  if (have) sh.weights[tid] = w;
+  if (have) sh.weights[own] = w;
   __syncthreads();
-  if (w == 0) return;
   // in the order of the index, the token
   const u64 want = min(all, part_of(p.u, all) + 1);
   before = 0;
+  if (own < count) {
 #pragma unroll 4
-  for (int j = 0; j < count; ++j)
-    if (static_cast<uint32_t>(sh.list[j]) < static_cast<uint32_t>(me)) before += sh.weights[j];
-  if (before < want && want <= before + w) {
+    for (int j = mate; j < count; j += share)
+      if (static_cast<uint32_t>(sh.list[j]) < static_cast<uint32_t>(me)) before += sh.weights[j];
+  }
+  for (int o = 1; o < share; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  if (w != 0 && before < want && want <= before + w) {
     const int token = static_cast<int>(static_cast<uint32_t>(me));
     a.tokens[r] = token;
     if (a.logprobs) a.logprobs[r] = log_share(w, w < kPlainLog ? scale.log2_units(a, r, token) : 0.0, all);
