@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
 // Rows with anything that this does not hold for (an infinite largest logit, one above 512 log2 units in size, where c's
 // parts no longer reach, no logit at all, a temperature of 0) keep kUndecided and are the other kernel's.
 
-constexpr int kStreamThreads = 128, kStreamWarps = kStreamThreads / 32, kStreamCtas = 8;  // CTAs to an SM
+constexpr int kStreamThreads = 128, kStreamWarps = kStreamThreads / 32, kStreamCtas = 7;  // CTAs to an SM
 constexpr int kChunk = 512, kPerLane = kChunk / 32;
 constexpr int kMaxChunks = kSampleMaxVocab / kChunk + 1;
 constexpr int64_t kStreamLeast = 1 << 20;  // logits of a call, below which one kernel is less than two
@@ -832,16 +832,27 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, kStreamC
     return top;
   };
   float most = -INFINITY;  // of the chunks that this warp has seen
+  const auto inside = [&](int k) { return k * kChunk >= shift && (k + 1) * kChunk - shift <= a.vocab; };
+  uint4 next[kPerLane / kVec];  // of the chunk after this one
+  const auto fetch = [&](int k) {
+#pragma unroll
+    for (int v = 0; v < kPerLane / kVec; ++v)
+      next[v] = __ldg(reinterpret_cast<const uint4*>(row + k * kChunk - shift + lane * kVec + v * 32 * kVec));
+  };
+  if (c0 + warp < c1 && inside(c0 + warp)) fetch(c0 + warp);
   for (int k = c0 + warp; k < c1; k += kStreamWarps) {
     float x[kPerLane];
-    const int at = k * kChunk - shift + lane * kVec;
-    if (k * kChunk >= shift && (k + 1) * kChunk - shift <= a.vocab) {
+    if (inside(k)) {
 #pragma unroll
-      for (int v = 0; v < kPerLane / kVec; ++v) load_inside<T, kVec>(row, at + v * 32 * kVec, x + v * kVec);
+      for (int v = 0; v < kPerLane / kVec; ++v)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) x[v * kVec + j] = Ty<T>::to_f(reinterpret_cast<const T*>(&next[v])[j]);
     } else {
 #pragma unroll
-      for (int v = 0; v < kPerLane / kVec; ++v) load_edge<T, kVec>(row, at + v * 32 * kVec, a.vocab, x + v * kVec);
+      for (int v = 0; v < kPerLane / kVec; ++v)
+        load_edge<T, kVec>(row, k * kChunk - shift + lane * kVec + v * 32 * kVec, a.vocab, x + v * kVec);
     }
+    if (k + kStreamWarps < c1 && inside(k + kStreamWarps)) fetch(k + kStreamWarps);
     const float top = chunk_top(x);
     most = fmaxf(most, top);
     const int n = weigh.exponent(top);
