@@ -17,8 +17,9 @@
 //
 // Steps 2 and 3 find the first element of the order at which a cumulated value (1 each, or the weights) reaches a target: a
 // histogram over 2048 equal steps of the exponent, merged over the cluster, then histograms over the logits' bits within the
-// step that the target falls into, until one value is left; among elements of that value the index decides. If no more than
-// 2048 elements reach that step, they are listed and sorted by one CTA instead, which then finishes the row by itself.
+// step that the target falls into, until one value is left; among elements of that value the index decides. But if no more
+// than 2048 elements reach that step, they are listed and sorted by one CTA, which then finishes the row by itself; and if no
+// more than that are in the step, they are, and it tells the others where the target falls.
 //
 // Weights are integers, 2^43 for the largest logit: integer sums have one result in any order, whatever threads, warps and
 // CTAs make of it, and a row of 409600 weights stays below 2^62. A weight is 2^-y with y = (m - x) log2(e) / t formed in two
@@ -212,6 +213,41 @@ struct Scale {
   }
 };
 
+// Sort `n` (a power of two) integers in shared memory.
+__device__ __forceinline__ void sort(u64* v, int n) {
+  for (int size = 2; size <= n; size *= 2) {
+    for (int apart = size / 2; apart > 0; apart /= 2) {
+      for (int t = threadIdx.x; t < n / 2; t += kThreads) {
+        const int i = 2 * t - (t & (apart - 1)), j = i + apart;
+        const bool up = (i & size) == 0;
+        const u64 x = v[i], y = v[j];
+        if ((x > y) == up) {
+          v[i] = y;
+          v[j] = x;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The sum of the values of all threads before this one, and (in *all) of all of them.
+__device__ __forceinline__ u64 block_scan_u64(Shared& sh, u64 v, u64* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const u64 upto = warp_scan_u64(v);
+  __syncthreads();
+  if (lane == 31) sh.red[warp] = upto;
+  __syncthreads();
+  u64 before = upto - v, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sh.red[w];
+    sum += sh.red[w];
+  }
+  *all = sum;
+  return before;
+}
+
 // One row, as a thread of the exact kernel sees it.
 struct Row : Scale {
   Shared& sh;
@@ -313,14 +349,15 @@ struct Row : Scale {
     cluster_sync_all();
   }
 
-  // The elements that a step can hold of those that stay are in steps 0 .. bin. Lists them in the first CTA's memory and
-  // returns their number, or -1 if they are too many (then the histogram is empty again).
-  __device__ __forceinline__ int list(int bin) {
+  // Lists the elements of steps 0 .. bin where the first CTA's slice was, or (`only`) those of step bin that stay in place of
+  // its histogram, and returns their number; or -1 if they are too many (then the histogram is empty again).
+  __device__ __forceinline__ int list(int bin, bool only) {
     if (threadIdx.x == 0) sh.listed = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const float x = xs[i];
-      if (step(x) > bin) continue;
+      const int at_step = step(x);
+      if (at_step > bin || (only && (at_step < bin || !stays(x, base + i)))) continue;
       const uint32_t at = atomicAdd(&sh.listed, 1u);
       if (at < kCandidates) sh.list[at] = static_cast<u64>(~key_of(x)) << 32 | static_cast<uint32_t>(base + i);
     }
@@ -336,10 +373,43 @@ struct Row : Scale {
       for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
       return -1;
     }
-    const uint32_t to = mapa_shared(smem_addr(xs), 0) + static_cast<uint32_t>(before) * 8;
-    for (uint32_t i = threadIdx.x; i < have; i += kThreads) st_cluster(to + 8 * i, sh.list[i]);
+    // (the first CTA's own are the first)
+    const uint32_t to = mapa_shared(only ? smem_addr(sh.list) : smem_addr(xs), 0) + static_cast<uint32_t>(before) * 8;
+    if (!only || rank > 0)
+      for (uint32_t i = threadIdx.x; i < have; i += kThreads) st_cluster(to + 8 * i, sh.list[i]);
     cluster_sync_all();
     return static_cast<int>(all);
+  }
+
+  // The last one that stays is the first of the listed ones of a step at which their cumulated values reach `want`.
+  __device__ __forceinline__ void cut_listed(int count, bool mass, u64 want) {
+    constexpr int kEach = kCandidates / kThreads;
+    if (rank == 0) {
+      int size = 2;
+      while (size < count) size *= 2;
+      for (int i = count + threadIdx.x; i < size; i += kThreads) sh.list[i] = ~0ull;
+      __syncthreads();
+      sort(sh.list, size);
+      u64 v[kEach], sum = 0, all;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int i = threadIdx.x * kEach + j;
+        v[j] = i >= count ? 0 : mass ? weight(value_of(~static_cast<uint32_t>(sh.list[i] >> 32))) : 1;
+        sum += v[j];
+      }
+      u64 before = block_scan_u64(sh, sum, &all);
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        if (before < want && want <= before + v[j])
+          for (int r = 0; r < ctas; ++r) st_cluster(mapa_shared(smem_addr(&sh.border[3]), r), sh.list[threadIdx.x * kEach + j]);
+        before += v[j];
+      }
+    }
+    cluster_sync_all();
+    cut_key = ~static_cast<uint32_t>(sh.border[3] >> 32);
+    cut_index = static_cast<uint32_t>(sh.border[3]);
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
+    __syncthreads();
   }
 
   // The first element, in the order of falling logits and rising indexes, at which the values cumulated over what stays
@@ -359,13 +429,21 @@ struct Row : Scale {
       want = min(mass ? reach(p, all) : k, all);
       return want;
     });
-    if (cut_key == 0) {
-      const int listed = list(static_cast<int>(sh.border[0]));
+    const int bin = static_cast<int>(sh.border[0]);
+    if (cut_key == 0 && (mass || sh.border[1] + sh.border[2] <= kCandidates)) {
+      const int listed = list(bin, false);
       if (listed >= 0) return listed;
       __syncthreads();
     }
-    const int bin = static_cast<int>(sh.border[0]);
     want -= sh.border[1];
+    if (mass || sh.border[2] <= kCandidates) {
+      const int listed = list(bin, true);
+      if (listed >= 0) {
+        cut_listed(listed, mass, want);
+        return -1;
+      }
+      __syncthreads();
+    }
     // the keys of that step
     uint32_t low = 0xffffffffu, high = 0;
     for (int i = threadIdx.x; i < n; i += kThreads) {
@@ -465,41 +543,6 @@ __device__ __forceinline__ u64 load_slice(const T* row, int base, int n, float* 
   const int tail = skip + vecs * kVec;
   if (threadIdx.x < n - tail) put(tail + threadIdx.x, p[tail + threadIdx.x]);
   return best;
-}
-
-// Sort `n` (a power of two) integers in shared memory.
-__device__ __forceinline__ void sort(u64* v, int n) {
-  for (int size = 2; size <= n; size *= 2) {
-    for (int apart = size / 2; apart > 0; apart /= 2) {
-      for (int t = threadIdx.x; t < n / 2; t += kThreads) {
-        const int i = 2 * t - (t & (apart - 1)), j = i + apart;
-        const bool up = (i & size) == 0;
-        const u64 x = v[i], y = v[j];
-        if ((x > y) == up) {
-          v[i] = y;
-          v[j] = x;
-        }
-      }
-      __syncthreads();
-    }
-  }
-}
-
-// The sum of the values of all threads before this one, and (in *all) of all of them.
-__device__ __forceinline__ u64 block_scan_u64(Shared& sh, u64 v, u64* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const u64 upto = warp_scan_u64(v);
-  __syncthreads();
-  if (lane == 31) sh.red[warp] = upto;
-  __syncthreads();
-  u64 before = upto - v, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sh.red[w];
-    sum += sh.red[w];
-  }
-  *all = sum;
-  return before;
 }
 
 // The rest of a row whose candidates the first CTA has listed, `count` of them: sorted, the first k stay (k > 0), of those

@@ -244,3 +244,23 @@ def test_listed_candidates(hc, k):
     check(hc, x, u, top_k=k, top_p=0.8, min_p=0.01)
     check(hc, x, u, top_p=0.02 + k / 40000)
     check(hc, x, u, temperature=0.3, top_p=0.9)
+
+
+@pytest.mark.parametrize("scale", [0.3, 2.0])
+def test_many_that_stay(hc, scale):
+    """Borders among thousands of tokens: steps that hold few and many, equal logits at the border, one border behind another."""
+    x = rnd(39, 5, 130001, scale=scale)
+    x[1] = x[1].mul(8).round() / 8
+    x[2] = x[2].mul(1000).round() / 1000
+    x[3, ::2] = -math.inf
+    x[4, 1000:] -= 40.0 * scale
+    u = uniforms(40, 5)
+    for k in (2500, 20000, 64000, 100000, 130000):
+        check(hc, x, u, top_k=k)
+        check(hc, x, u, top_k=k, top_p=0.7)
+    for p in (0.2, 0.9, 0.999):
+        check(hc, x, u, top_p=p)
+        check(hc, x, u, top_p=p, temperature=0.5)
+    y = rnd(41, 40, 30000, scale=scale, dtype=BF16)
+    check(hc, y, uniforms(42, 40), top_k=5000, top_p=0.9, least=0.5)
+    check(hc, y, uniforms(43, 40), top_p=0.95, least=0.5)
