@@ -82,7 +82,7 @@ template <> __device__ __forceinline__ float saturate<__half>(float v) {
 // most one (so that few CTAs wait for others' sums, and none twice; two thirds of the SMs can take what the memory gives);
 // otherwise all tiles' blocks, laid end to end, are cut into equal runs, of which the pieces of cut tiles come first, so that
 // their sums are joined while whole tiles are still on their way. (Units, blocks of inputs, are below 2^31 in number
-// where tiles are split: at most 2^17 pairs, and 2^19 blocks of features and inputs.)
+// where tiles are split: at most 2^11 tiles of pairs, and 2^19 blocks of features and inputs.)
 template <int kRows, bool kSplit> struct Pieces {
   const Args& a;
   const int32_t *bounds, *tiles;

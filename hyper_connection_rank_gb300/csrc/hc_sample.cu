@@ -27,7 +27,10 @@
 // fp32 whose leading term is kept apart, so that the whole is good to 2^-38 of itself (fp32's 2^-24 would choose another
 // token than the definition once in some thousand rows of 10^5 tokens; fp64 runs at 1/64 of the rate here).
 //
-// Bound: latency. A row of 131072 with top_p takes this kernel some 50 us, of which 4 are the row's bytes.
+// Bound: the third kernel's passes over its slices (five with a border, 50 instructions to a logit in those that weigh) and
+// the histogram's atomics. With pick_kernel's attempt before it, one row of 131072 fp32 logits takes 40 us with a top_k of
+// 20000 and 58 with a top_p that leaves thousands (73 where all logits are within few steps), 64 rows take 105 and 155 (191);
+// with 512 threads to a CTA they took 43, 64 (79), 128 and 189 (228).
 #include <algorithm>
 
 #include "hc_async.cuh"
@@ -40,7 +43,7 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = kSampleMaxVocab / kMaxCluster;  // elements that a CTA keeps
@@ -750,9 +753,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
 // within 2^-30 of itself (equal logits have equal weights). Chunks' sums are then shifted to the row's largest n and added,
 // and the chunk in which they pass uniform * sum is read again by one warp.
 //
-// Bound: instructions, some 19 to a logit, two logits in packed ones where there are such. 256 rows of 200003 fp32 logits
-// (205 MB) take 84 us, 2.4 TB/s; their bytes alone would take 30. Weights to within 2^-24 by the exponential unit and fp32
-// sums, with fp64 for what those cannot decide, took longer, since some rows in a call always are too close.
+// Bound: instructions, some 29 to a logit where two logits share the packed ones. 256 rows of 200003 fp32 logits (205 MB) take
+// 76 us here and 84 with what follows, 2.4 TB/s; their bytes alone would take 30. (With no loads ahead of the chunk that is
+// weighed it was 93. fp32 sums of the exponential unit's weights are quicker, but in every call some rows are then too close to
+// decide, and those rows' exact pass takes longer than all others.)
 //
 // Rows with anything that this does not hold for (an infinite largest logit, one above 512 log2 units in size, where c's
 // parts no longer reach, no logit at all, a temperature of 0) keep kUndecided and are the other kernel's.

@@ -76,10 +76,12 @@ hc_status_t hc_expert_route(const hc_expert_route_t* args, struct CUstream_st* s
  *
  * Numerics: products are summed in fp32. In the fp16/bf16 kernels the inner
  * values silu(.) * (.) are rounded to T for the product with down (the tensor
- * core's operands are 16 bits), and so is each chosen expert's result, where
- * there are many tokens; the sum over the chosen experts is fp32, rounded to T
- * once. fp16 inner values saturate at its largest finite value rather than
- * turn to infinity. Limits: top_k <= 32, num_experts <= 1024, hidden and inner
+ * core's operands are 16 bits). Where experts have many tokens, each chosen
+ * expert's result is kept as 16-bit integers with an exponent for sixteen
+ * neighbours, off by 2^-15 of the largest of them at most (and 0 where all are
+ * below 2^-126); otherwise it is fp32. The sum over the chosen experts is fp32,
+ * rounded to T once. fp16 inner values saturate at its largest finite value
+ * rather than turn to infinity. Limits: top_k <= 32, num_experts <= 1024, hidden and inner
  * <= 65536, tokens * top_k < 2^24. */
 typedef struct {
   const void* x; /* (tokens, hidden) of type dtype */

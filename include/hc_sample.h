@@ -29,11 +29,13 @@ extern "C" {
  * log(w_i / sum). A temperature of 0 (or less, or NaN) takes the largest logit,
  * the first of equal ones, with a log-probability of 0.
  *
- * Weights are formed and added as integers in units of 2^-43, each to within
- * about 2^-38 of its own size, so that sums are exact whatever their order: a
- * result differs from the definition above only where a sum comes within some
- * 2^-38 of what it is compared with. A token whose weight is below 2^-44 is
- * not drawn.
+ * Weights are formed and added as integers, so that sums are exact whatever
+ * their order. In units of 2^-43 of the largest, each is within about 2^-38 of
+ * its own size; in calls that filter nothing and have 2^20 logits or more,
+ * within 2^-30 of it, in units of 2^-43 or less of the largest of each 512
+ * logits. A result differs from the definition above only where a sum comes
+ * within about that much of what it is compared with. A token whose weight is
+ * below 2^-44 is not drawn.
  *
  * Per-row parameters are arrays, or with a NULL pointer one value for all rows.
  * top_k <= 0, top_p >= 1 (or NaN) and min_p <= 0 (or NaN) leave everything;
