@@ -236,8 +236,7 @@ __global__ void __launch_bounds__(kThreads<kInner>, 1) many_kernel(const __grid_
     Gather<T> g;
     int it = 0;
     while (ok && p.next(kStep)) {
-      const int off = min(rank * kCtaRows, p.rows - 1);
-      g.begin(a, p.first + off, p.rows - off, group);
+      g.begin(a, p.first + min(rank * kCtaRows, p.rows - 1), p.rows - rank * kCtaRows, group);
       for (int k = p.k0; k < p.k1; ++k, ++it) {
         const int st = it % kStages;
         if (lane == 0) ok = mbar_wait(&b->empty[st], ((it / kStages) & 1) ^ 1, &g_many_wait_timeouts);

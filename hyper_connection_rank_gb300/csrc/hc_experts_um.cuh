@@ -247,29 +247,41 @@ __device__ __forceinline__ void prefetch_half(const CUtensorMap* map, bool k_maj
   }
 }
 
-// A gathering warp's part of a tile: 32 rows of x, from place `first` of the list, `rows` of them (past those any row will
-// do: nobody looks at the results, but one is read, so it has to be a row). A lane has the same 16 bytes of eight rows.
+// A gathering warp's part of a tile: 32 rows of x, from place `first` of the list, `rows` of them (past those whatever was
+// there: nobody looks at the results). A lane has the same 16 bytes of eight rows.
 template <typename T> struct Gather {
   const T* src[8];
+  uint32_t there;  // a bit for each
+  bool all;        // of the warp's
 
   __device__ __forceinline__ void begin(const Args& a, int first, int rows, int group) {
     const int lane = threadIdx.x & 31;
+    there = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = group * 32 + 4 * i + (lane >> 3);
+      there |= r < rows ? 1u << i : 0u;
       const int pair = a.order[first + max(0, min(r, rows - 1))];
       src[i] = static_cast<const T*>(a.x) + static_cast<int64_t>(pair / a.top_k) * a.x_step + (lane & 7) * 8;
     }
+    all = __all_sync(0xffffffffu, there == 0xffu);
   }
   // Inputs from k into the stage's rows at `to`, zeros past the last one; arrives on `bar` when they have landed.
   __device__ __forceinline__ void copy(const Args& a, uint32_t to, int k, int group, uint64_t* bar) const {
     const int lane = threadIdx.x & 31, chunk = lane & 7;
-    const int left = a.inputs - (k + chunk * 8);  // elements of this chunk and after it
-    const uint32_t bytes = left <= 0 ? 0u : left >= 8 ? 16u : static_cast<uint32_t>(left * 2);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    const auto place = [&](int i) {
       const int r = group * 32 + 4 * i + (lane >> 3);
-      cp_async16_zfill(to + r * 128 + ((chunk ^ (r & 7)) << 4), bytes ? src[i] + k : src[i] - chunk * 8, bytes);
+      return to + r * 128 + ((chunk ^ (r & 7)) << 4);
+    };
+    if (all && k + kBK <= a.inputs) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cp_async16_zfill(place(i), src[i] + k, 16);
+    } else {
+      const int left = a.inputs - (k + chunk * 8);  // elements of this chunk and after it
+      const uint32_t bytes = left <= 0 ? 0u : left >= 8 ? 16u : static_cast<uint32_t>(left * 2);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (there >> i & 1u) cp_async16_zfill(place(i), bytes ? src[i] + k : src[i] - chunk * 8, bytes);
     }
     cp_async_arrive(bar);
   }
