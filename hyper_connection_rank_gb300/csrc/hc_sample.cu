@@ -294,11 +294,17 @@ struct Row : Scale {
     return k > cut_key || (k == cut_key && static_cast<uint32_t>(index) <= cut_index);
   }
 
-  __device__ __forceinline__ void add(int bin, u64 v) {
-    const uint32_t lo = static_cast<uint32_t>(v);
-    const uint32_t old = atomicAdd(&sh.lo[bin], lo);
-    const uint32_t up = static_cast<uint32_t>(v >> 32) + (old + lo < old ? 1u : 0u);
-    if (up != 0) atomicAdd(&sh.hi[bin], up);
+  // Values (not zeros) into the histogram, all lower halves before any upper one.
+  static constexpr int kAtOnce = 4;
+  __device__ __forceinline__ void add(const int* bin, const u64* v) {
+    uint32_t old[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) old[j] = v[j] != 0 ? atomicAdd(&sh.lo[bin[j]], static_cast<uint32_t>(v[j])) : 0u;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const uint32_t lo = static_cast<uint32_t>(v[j]), up = static_cast<uint32_t>(v[j] >> 32) + (old[j] + lo < old[j] ? 1u : 0u);
+      if (up != 0) atomicAdd(&sh.hi[bin[j]], up);
+    }
   }
 
   // The histograms of all CTAs together: into which bin the target falls (border[0]), what lies before it (border[1]) and
@@ -312,9 +318,14 @@ struct Row : Scale {
       v[i] = 0;
       if (i < per && at + i < mine) {
         const int bin = rank * mine + at + i;
-        for (int r = 0; r < ctas; ++r)
-          v[i] += ld_cluster(mapa_shared(smem_addr(&sh.lo[bin]), r)) +
-                  (static_cast<u64>(ld_cluster(mapa_shared(smem_addr(&sh.hi[bin]), r))) << 32);
+        uint32_t lo[kMaxCluster], hi[kMaxCluster];  // (all loads before any use)
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          lo[r] = r < ctas ? ld_cluster(mapa_shared(smem_addr(&sh.lo[bin]), r)) : 0u;
+          hi[r] = r < ctas ? ld_cluster(mapa_shared(smem_addr(&sh.hi[bin]), r)) : 0u;
+        }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) v[i] += lo[r] + (static_cast<u64>(hi[r]) << 32);
       }
       sum += v[i];
     }
@@ -387,7 +398,21 @@ struct Row : Scale {
   // The last one that stays is the first of the listed ones of a step at which their cumulated values reach `want`.
   __device__ __forceinline__ void cut_listed(int count, bool mass, u64 want) {
     constexpr int kEach = kCandidates / kThreads;
-    if (rank == 0) {
+    if (rank == 0 && count <= kThreads) {  // each with all others
+      u64* values = sh.list + kThreads;
+      const bool have = threadIdx.x < count;
+      const u64 me = have ? sh.list[threadIdx.x] : 0, v = !have ? 0 : mass ? weight(value_of(~static_cast<uint32_t>(me >> 32))) : 1;
+      if (have) values[threadIdx.x] = v;
+      __syncthreads();
+      u64 before = 0;
+      if (have) {
+#pragma unroll 4
+        for (int j = 0; j < count; ++j)
+          if (sh.list[j] < me) before += values[j];
+        if (before < want && want <= before + v)
+          for (int r = 0; r < ctas; ++r) st_cluster(mapa_shared(smem_addr(&sh.border[3]), r), me);
+      }
+    } else if (rank == 0) {
       int size = 2;
       while (size < count) size *= 2;
       for (int i = count + threadIdx.x; i < size; i += kThreads) sh.list[i] = ~0ull;
@@ -421,11 +446,17 @@ struct Row : Scale {
   // instead (see list()) and their number is returned; *total is the sum of the values. Otherwise -1.
   __device__ __forceinline__ int cut(bool mass, float p, u64 k, u64* total) {
     u64 want = 0;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const float x = xs[i];
-      if (!stays(x, base + i)) continue;
-      const u64 v = mass ? weight(x) : 1;
-      if (v != 0) add(step(x), v);
+    for (int i0 = threadIdx.x; i0 < n; i0 += kAtOnce * kThreads) {
+      u64 v[kAtOnce];
+      int bin[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = i0 + j * kThreads;
+        const float x = i < n ? xs[i] : -INFINITY;
+        v[j] = i < n && stays(x, base + i) ? (mass ? weight(x) : 1) : 0;
+        bin[j] = step(x);
+      }
+      add(bin, v);
     }
     find([&](u64 all) {
       *total = all;
@@ -433,7 +464,7 @@ struct Row : Scale {
       return want;
     });
     const int bin = static_cast<int>(sh.border[0]);
-    if (cut_key == 0 && (mass || sh.border[1] + sh.border[2] <= kCandidates)) {
+    if (cut_key == 0 && !mass && sh.border[1] + sh.border[2] <= kCandidates) {
       const int listed = list(bin, false);
       if (listed >= 0) return listed;
       __syncthreads();
@@ -465,8 +496,9 @@ struct Row : Scale {
         const float x = xs[i];
         const uint32_t key = key_of(x);
         if (key < low || key > high || !stays(x, base + i)) continue;
-        const u64 v = mass ? weight(x) : 1;
-        if (v != 0) add((high - key) >> shift, v);
+        u64 v[kAtOnce] = {mass ? weight(x) : 1};
+        const int bin[kAtOnce] = {static_cast<int>((high - key) >> shift)};
+        add(bin, v);
       }
       find([&](u64) { return want; });
       const uint32_t j = static_cast<uint32_t>(sh.border[0]);
@@ -678,6 +710,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, Shared& sh, floa
   // a warp's sum over a run of elements, which its lanes take in turn
   const int chunk = (n + kWarps - 1) / kWarps, lo = min(n, warp * chunk), hi = min(n, lo + chunk);
   u64 mine = 0;
+#pragma unroll 4
   for (int i = lo + lane; i < hi; i += 32) mine += kept(i);
   mine = warp_sum_u64(mine);
   __syncthreads();
@@ -699,32 +732,36 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, Shared& sh, floa
   // the first element whose cumulated weight passes uniform * total, so is at least the next integer
   const u64 want = min(total, part_of(u, total) + 1);
   if (!(before < want && want <= before + mine)) return;
-  // in one warp: its lanes sum a run each (begun at another place each, for the sake of the memory banks)
-  const int run = (hi - lo + 31) / 32, l0 = min(hi, lo + lane * run), ln = min(hi, l0 + run) - l0;
-  u64 part = 0;
-  for (int i = 0; i < ln; ++i) {
-    int j = i + lane;
-    j %= ln;
-    part += kept(l0 + j);
-  }
-  u64 upto = before + warp_scan_u64(part);
-  const uint32_t passed = __ballot_sync(0xffffffffu, upto >= want);
-  const int owner = __ffs(passed) - 1;
-  before = __shfl_sync(0xffffffffu, upto - part, owner);
-  const int r0 = __shfl_sync(0xffffffffu, l0, owner), rn = __shfl_sync(0xffffffffu, ln, owner);
-  for (int i0 = 0; i0 < rn; i0 += 32) {
-    const int i = i0 + lane;
-    const u64 w = i < rn ? kept(r0 + i) : 0;
-    upto = before + warp_scan_u64(w);
-    const uint32_t hit = __ballot_sync(0xffffffffu, upto >= want);
-    if (hit != 0) {
-      if (lane == __ffs(hit) - 1) {
-        a.tokens[r] = base + r0 + i;
-        if (a.logprobs) a.logprobs[r] = log_share(w, w < kPlainLog ? row.log2_units(a, r, base + r0 + i) : 0.0, total);
-      }
-      return;
+  // in one warp: 128 elements at a time, until they pass it, then the 32 of those that do
+  for (int i0 = lo; i0 < hi; i0 += 32 * 4) {
+    u64 w[4], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + 32 * j + lane;
+      w[j] = i < hi ? kept(i) : 0;
+      sum += w[j];
     }
-    before = __shfl_sync(0xffffffffu, upto, 31);
+    // (sums below 2^45 a lane)
+    sum = (static_cast<u64>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(sum >> 23))) << 23) +
+          __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(sum) & 0x7fffffu);
+    if (before + sum < want) {
+      before += sum;
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u64 upto = before + warp_scan_u64(w[j]);
+      const uint32_t hit = __ballot_sync(0xffffffffu, upto >= want);
+      if (hit != 0) {
+        const int i = i0 + 32 * j + lane;
+        if (lane == __ffs(hit) - 1) {
+          a.tokens[r] = base + i;
+          if (a.logprobs) a.logprobs[r] = log_share(w[j], w[j] < kPlainLog ? row.log2_units(a, r, base + i) : 0.0, total);
+        }
+        return;
+      }
+      before = __shfl_sync(0xffffffffu, upto, 31);
+    }
   }
 }
 
