@@ -27,11 +27,12 @@
 // fp32 whose leading term is kept apart, so that the whole is good to 2^-38 of itself (fp32's 2^-24 would choose another
 // token than the definition once in some thousand rows of 10^5 tokens; fp64 runs at 1/64 of the rate here).
 //
-// Bound: the third kernel's passes over its slices (five with a border, 50 instructions to a logit in those that weigh) and
-// the histogram's atomics. With pick_kernel's attempt before it, one row of 131072 fp32 logits takes 40 us with a top_k of
-// 20000 and 58 with a top_p that leaves thousands (73 where all logits are within few steps), 64 rows take 105 and 155 (191);
-// with 512 threads to a CTA they took 43, 64 (79), 128 and 189 (228).
+// Bound: the third kernel's passes over its slices (four with a border, 50 instructions to a logit in those that weigh), the
+// histogram's atomics and its CTAs' steps together. With pick_kernel's attempt before it, one row of 131072 fp32 logits takes
+// 35 us with a top_k of 20000 and 41 with a top_p that leaves thousands (59 where all logits are within few steps), 64 rows
+// take 102 and 128 (171). With 512 threads to a CTA they took a tenth to a fifth longer.
 #include <algorithm>
+#include <atomic>
 
 #include "hc_async.cuh"
 #include "hc_common.cuh"
@@ -45,8 +46,11 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
-constexpr int kMaxSlice = kSampleMaxVocab / kMaxCluster;  // elements that a CTA keeps
+// CTAs to a row at most, and to one of no more rows than the device can have clusters of so many together (one to six of
+// 131072 fp32 logits with a top_p that leaves thousands took 47.5 to 49 us with 8 and 40 to 42 with 16, with one that leaves
+// few 18 and 17, a top_k of 20000 of 262144 53 to 56 and 42 to 46).
+constexpr int kCluster = 8, kMaxCluster = 16;
+constexpr int kMaxSlice = kSampleMaxVocab / kCluster;  // elements that a CTA keeps
 constexpr int kOneBits = 43;
 constexpr u64 kOne = 1ull << kOneBits;
 constexpr float kRange = 44.0f;  // weights below 2^-44 count as 0
@@ -1042,8 +1046,8 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, kStreamC
 // Bound: latency, of the logits' bytes (1 to 2 us of them) and of four or five steps of a row's CTAs together. 64 rows of
 // 131072 fp32 logits with top_k, top_p and min_p take 15 us (33.6 MB: 4.9 us): 2.8 until all are read, 1.3 for the largest, 2 for the
 // border, 2 for the list, 3 to finish, and 2 for the next kernel to see that nothing is left. One row of 131072 bf16 logits with
-// top_p takes 20 us, 5 of them for the weights of all. (Dealing out the vectors that are looked through again to all threads
-// took 64 rows from 22 to 15 us; a histogram for each CTA rather than the first one's for all, one row from 23 to 20.)
+// top_p takes 18 us, 3 of them for the weights of all. (Dealing out the vectors that are looked through again to all threads
+// took 64 rows from 22 to 15 us; a histogram for each CTA rather than the first one's for all, one row from 23 to 20 with 8 CTAs.)
 
 constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32;
 constexpr int kPicked = 512;   // candidates at most
@@ -1284,13 +1288,46 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
   }
 }
 
+// How many clusters of kMaxCluster CTAs of a kernel the current device can have at once, 0 if none. Asked once for a device.
+template <auto Kernel> int wide_clusters(int threads, size_t smem) {
+  static std::atomic<int> known[64];  // the number + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev].load(std::memory_order_acquire);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxCluster);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kMaxCluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if ((smem > 0 && ensure_smem<Kernel>(smem) != cudaSuccess) ||
+        cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&clusters, Kernel, &cfg) != cudaSuccess) {
+      clusters = 0;
+      cudaGetLastError();  // (a launch with fewer CTAs has no part in that)
+    }
+    n = clusters + 1;
+    known[dev].store(n, std::memory_order_release);
+  }
+  return n - 1;
+}
+
 }  // namespace
 
 cudaError_t launch_token_sample(const hc_token_sample_t& p, int num_sms, cudaStream_t s) {
   // As few CTAs to a row as its slices allow, and more while rows alone leave SMs idle.
   int ctas = 1;
   while (static_cast<int64_t>(ctas) * kMaxSlice < p.vocab) ctas *= 2;
-  while (ctas < kMaxCluster && p.rows * ctas * 2 <= num_sms && p.vocab / (2 * ctas) >= 2048) ctas *= 2;
+  const auto more = [&](int c, int most, int least) { return p.rows * c * 2 <= num_sms && c < most && p.vocab / (2 * c) >= least; };
+  const auto wide = [&](int clusters) { return p.rows <= clusters ? kMaxCluster : kCluster; };
+  const int most = wide(wide_clusters<sample_kernel>(kThreads, sizeof(Shared) + kMaxSlice * sizeof(float)));
+  while (more(ctas, most, 2048)) ctas *= 2;
   const int slice = ((p.vocab + ctas - 1) / ctas + 31) / 32 * 32;
   SampleArgs a = {p.logits, p.uniform, p.temperatures, p.top_ps, p.min_ps, p.top_ks, p.tokens_out, p.logprobs_out,
                   p.logits_stride, p.rows, p.vocab, slice, p.top_k, p.dtype, p.temperature, p.top_p, p.min_p, false};
@@ -1300,7 +1337,7 @@ cudaError_t launch_token_sample(const hc_token_sample_t& p, int num_sms, cudaStr
   if (whole && p.rows * p.vocab >= kStreamLeast) {
     int split = 1;
     // (all at once, since the CTAs of a row wait for one another)
-    while (split < kMaxCluster && p.rows * split * 2 <= kStreamCtas * num_sms && p.vocab / (2 * split) >= 4 * kStreamWarps * kChunk)
+    while (split < kCluster && p.rows * split * 2 <= kStreamCtas * num_sms && p.vocab / (2 * split) >= 4 * kStreamWarps * kChunk)
       split *= 2;
     const dim3 grid(static_cast<unsigned>(p.rows * split)), block(kStreamThreads);
     cudaError_t e;
@@ -1309,13 +1346,16 @@ cudaError_t launch_token_sample(const hc_token_sample_t& p, int num_sms, cudaStr
     else e = launch_pdl(stream_kernel<__nv_bfloat16>, grid, block, 0, s, split, a, split);
     if (e != cudaSuccess) return e;
   } else if (!whole) {
-    int split = 1;
-    while (split < kMaxCluster && p.rows * split * 2 <= num_sms && p.vocab / (2 * split) >= kPickThreads * 8) split *= 2;
-    const dim3 grid(static_cast<unsigned>(p.rows * split)), block(kPickThreads);
-    cudaError_t e;
-    if (p.dtype == HC_F32) e = launch_pdl(pick_kernel<float>, grid, block, 0, s, split, a, split);
-    else if (p.dtype == HC_F16) e = launch_pdl(pick_kernel<__half>, grid, block, 0, s, split, a, split);
-    else e = launch_pdl(pick_kernel<__nv_bfloat16>, grid, block, 0, s, split, a, split);
+    const auto launch = [&](auto type) {
+      using T = decltype(type);
+      const int most_here = wide(wide_clusters<pick_kernel<T>>(kPickThreads, 0));
+      int split = 1;
+      while (more(split, most_here, kPickThreads * 8)) split *= 2;
+      return launch_pdl(pick_kernel<T>, dim3(static_cast<unsigned>(p.rows * split)), dim3(kPickThreads), 0, s, split, a, split);
+    };
+    const cudaError_t e = p.dtype == HC_F32   ? launch(float())
+                          : p.dtype == HC_F16 ? launch(__half())
+                                              : launch(__nv_bfloat16());
     if (e != cudaSuccess) return e;
   }
   if (!whole || p.rows * p.vocab >= kStreamLeast) {  // what those have left
