@@ -10,11 +10,13 @@
 // tensor cores' cycles). Accumulators take turns, so that a tile is written while
 // the next one is multiplied. Whole tiles are dealt out in turn.
 //
-// 8191 tokens at eight of 64 experts of 2560 x 640 in bf16: 298 us (inner, 1.44 PFLOP/s, 76% of measured) and 163 (outer, 1.32),
+// 8191 tokens at eight of 64 experts of 2560 x 640 in bf16: 298 to 305 us (inner, 1.42 PFLOP/s, 75% of measured) and 164 (outer, 1.31),
 // tensor cores active for 75 and 68% of the cycles; a stage takes 0.32 us where the MMAs take 0.27, and tiles are 90% full. 1301
-// tokens at two of 16 experts of 1280 x 2560 in fp16: 75 and 36 us, 2.8 and 2.9 TB/s of weights; tiles are half full, 20
+// tokens at two of 16 experts of 1280 x 2560 in fp16: 58 and 36 us, 3.6 and 2.9 TB/s of weights; tiles are half full, 20
 // tiles of pairs by 20 and 5 of features are 5.3 and 1.3 rounds of 76 pairs of CTAs, and the first two tiles of each wait for cold
-// weights. (Sending those to L2 earlier, by TMA or by the gathering warps, took 10 to 20% longer: both have no time to spare.)
+// weights. (Sending those to L2 earlier, by TMA or by the gathering warps, took 10 to 20% longer: both have no time to spare.
+// For the same reason the gathering warps copy full tiles without a look at their rows, and nothing for rows that are not
+// there: with copies of some row in their place the inner product took 75 us.)
 //
 // Of the pair, the first CTA issues the MMAs. The second one's stages are made known
 // to it by a warp that waits for them and arrives at the first one's barrier;
