@@ -11,8 +11,8 @@ import struct
 
 import torch
 
-from ._binding import lib
-from ._paged import _device, _dtype_code, _launch, _on_stream, _sized
+from ._binding import check, lib
+from ._paged import _current_device, _current_stream, _device, _dtype_code, _launch, _on_stream, _sized
 
 __all__ = ["expert_route", "expert_mlp", "expert_mlp_workspace_size", "token_sample"]
 
@@ -58,8 +58,8 @@ def expert_route(logits, top_k, *, bias=None, scoring="softmax", groups=1, top_g
         raise ValueError(f"unknown scoring {scoring!r}")
     bias_at = 0 if bias is None else _dense("bias", bias, (experts,), torch.float32, device)
     live_at = 0 if live is None else _dense("live", live, (1,), torch.int32, device)
-    ids = torch.empty((tokens, max(top_k, 0)), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((tokens, max(top_k, 0)), dtype=torch.float32, device=logits.device)
+    ids = logits.new_empty((tokens, max(top_k, 0)), dtype=torch.int32)
+    weights = logits.new_empty((tokens, max(top_k, 0)), dtype=torch.float32)
     args = _ROUTE.pack(logits.data_ptr(), bias_at, live_at, ids.data_ptr(), weights.data_ptr(), tokens, step, experts, top_k,
                        groups, groups if top_groups is None else top_groups, group_best, _SCORING[scoring], bool(renormalise),
                        code, scale)
@@ -122,24 +122,47 @@ def expert_mlp(x, gate_w, up_w, down_w, experts, weights, *, out=None, workspace
                           flags=flags)
     device = _device(x)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
     elif out.shape != x.shape:
         raise ValueError("out must have the shape of x")
     out_step = _rows("out", out, x.dtype, device)[2]
     L = lib()
     args = _mlp_args(x, gate_w, up_w, down_w, experts, weights, flags, out.data_ptr(), out_step, 0, 0, device)
-    if workspace is None:
-        size = _sized(device, L.hc_expert_mlp_workspace_size, args)
-        if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
-    else:
+    if workspace is not None:
         if workspace.get_device() != device:
             raise ValueError(f"workspace must be a CUDA tensor on device {device}")
-        size = workspace.numel() * workspace.element_size()
-    if workspace is not None:
-        args = args[:56] + struct.pack("@PN", workspace.data_ptr(), size) + args[72:]
-    _launch(device, L.hc_expert_mlp, args)
+        _launch(device, L.hc_expert_mlp, _with(args, workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+    elif device == _current_device():
+        _mlp_in_scratch(L, device, args)
+    else:
+        with torch.cuda.device(device):
+            _mlp_in_scratch(L, device, args)
     return out
+
+
+# A block of the current stream's memory without a tensor around it, where this build of torch has that (a third of the time).
+_alloc, _free = (getattr(torch._C, "_cuda_cudaCachingAllocator_raw_" + n, None) for n in ("alloc", "delete"))
+
+
+def _with(args, workspace, size):
+    """_MLP's fields with this workspace."""
+    return args[:56] + struct.pack("@PN", workspace, size) + args[72:]
+
+
+def _mlp_in_scratch(L, device, args):
+    """The call on the current device and stream, with a workspace that goes back to the allocator right behind it."""
+    size, stream = L.hc_expert_mlp_workspace_size(args), _current_stream(device)
+    if not size:  # (no rows, or an error that the call reports)
+        check(L.hc_expert_mlp(args, stream))
+    elif _alloc is None or _free is None:
+        work = torch.empty(size, dtype=torch.uint8, device=device)
+        check(L.hc_expert_mlp(_with(args, work.data_ptr(), size), stream))
+    else:
+        work = _alloc(size, stream)
+        try:
+            check(L.hc_expert_mlp(_with(args, work, size), stream))
+        finally:
+            _free(work)
 
 
 def _choice(name, v, rows, dtype, device):
@@ -163,8 +186,8 @@ def token_sample(logits, uniform, *, temperature=1.0, top_k=0, top_p=1.0, min_p=
     k_at, k = _choice("top_k", top_k, rows, torch.int32, device)
     p_at, p = _choice("top_p", top_p, rows, torch.float32, device)
     m_at, m = _choice("min_p", min_p, rows, torch.float32, device)
-    tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
-    logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device) if return_logprob else None
+    tokens = logits.new_empty((rows,), dtype=torch.int32)
+    logprobs = logits.new_empty((rows,), dtype=torch.float32) if return_logprob else None
     args = _SAMPLE.pack(logits.data_ptr(), _dense("uniform", uniform, (rows,), torch.float32, device), t_at, p_at, m_at, k_at,
                         tokens.data_ptr(), logprobs.data_ptr() if return_logprob else 0, rows, step, vocab, k, t, p, m, code)
     _launch(device, lib().hc_token_sample, args)
