@@ -52,7 +52,8 @@ def route(logits, top_k, bias=None, scoring="softmax", groups=1, top_groups=None
         c = torch.where(torch.isnan(c), -math.inf, c)
         allowed = torch.ones(e, dtype=torch.bool)
         if top_groups < groups:
-            g = (s if bias is None else c).view(groups, -1)
+            # (scores rise with logits, so that of one score to a group the order is theirs, too, where float64 has 1 for several)
+            g = (s if bias is None and group_best == 2 else c).view(groups, -1)
             value = g.sort(-1, descending=True).values[:, :group_best].sum(-1)
             best = sorted(range(groups), key=lambda i: (-value[i].item(), i))[:top_groups]
             allowed = torch.zeros(groups, dtype=torch.bool).index_fill_(0, torch.tensor(best), True).repeat_interleave(e // groups)

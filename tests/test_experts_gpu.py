@@ -263,6 +263,16 @@ def test_route_close_values(hc):
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_large_logits(hc, scoring):
+    """Scores that no type tells from 1 or from 0 are in the order of their logits, and so are groups by their best."""
+    for dtype in (F32, BF16):
+        x = rnd(27, 30, 120, dtype=dtype, scale=50.0)
+        route_check(hc, x, 9, scoring=scoring)
+        route_check(hc, x, 9, scoring=scoring, groups=8, top_groups=3)
+        route_check(hc, x, 9, scoring=scoring, groups=24, top_groups=5, renormalise=False)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_route_odd_values(hc, scoring):
     """Infinities, NaN, rows of nothing, scores too small for float32, experts closed by their bias."""
     x = rnd(24, 8, 40)
