@@ -8,6 +8,7 @@
 #include <cmath>
 
 #include "hc_experts_internal.h"
+#include "hc_two.cuh"
 
 namespace hc {
 
@@ -61,26 +62,28 @@ struct BlockFloat {
 
   // sum += by * (eight of them). An integer n is the low half of the float 2^23 + 2^15 + n, so that a subtraction makes a
   // float of it (a conversion has a quarter of the rate).
-  static __device__ __forceinline__ void add8(const uint4& u, uint32_t e, float by, float* sum) {
+  static __device__ __forceinline__ void add8(const uint4& u, uint32_t e, float by, Two* sum) {
     const float scale = __uint_as_float((e - 14u) << 23) * (1.0f / kShrink);
     const uint32_t q[4] = {u.x, u.y, u.z, u.w};
     uint32_t most = __vmaxs2(__vmaxs2(q[0], q[1]), __vmaxs2(q[2], q[3]));
     uint32_t least = __vmins2(__vmins2(q[0], q[1]), __vmins2(q[2], q[3]));
     if (__vmaxs2(most, 0x7ffe7ffeu) != 0x7ffe7ffeu || __vmins2(least, 0x80028002u) != 0x80028002u) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int n = static_cast<int16_t>(i & 1 ? q[i >> 1] >> 16 : q[i >> 1] & 0xffffu);
-        const float v = n == kNan ? __int_as_float(0x7fc00000) : n == kInf ? INFINITY : n == -kInf ? -INFINITY
-                                                                                                 : static_cast<float>(n) * scale;
-        sum[i] = fmaf(by, v, sum[i]);
+      for (int i = 0; i < 4; ++i) {
+        const auto value = [&](uint32_t bits) {
+          const int n = static_cast<int16_t>(bits);
+          return n == kNan ? __int_as_float(0x7fc00000) : n == kInf ? INFINITY : n == -kInf ? -INFINITY : static_cast<float>(n) * scale;
+        };
+        sum[i] = fma2(Two(by), Two(value(q[i] & 0xffffu), value(q[i] >> 16)), sum[i]);
       }
       return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t biased = q[i >> 1] ^ 0x80008000u;
-      const float n = __uint_as_float(__byte_perm(biased, 0x4b000000u, i & 1 ? 0x7432 : 0x7410)) - 8421376.0f;
-      sum[i] = fmaf(by, n * scale, sum[i]);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t biased = q[i] ^ 0x80008000u;
+      const Two n = Two(__uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7410)), __uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7432))) +
+                    Two(-8421376.0f);
+      sum[i] = fma2(Two(by), n * Two(scale), sum[i]);
     }
   }
 };
