@@ -452,9 +452,10 @@ struct Plan {
 };
 
 // Which products run, and where their buffers lie in the workspace. Tiles of 32 pairs with the weights as the first operand
-// or of 256 with the pairs as the first, by the pairs that an expert has on average: 64 experts of 2560 x 640 (six to a
-// token) took 130 and 147 us at 20 pairs, 142 and 150 at 28, 203 and 158 at 40; 16 of 1280 x 2560 took 78 and 93, 76 and
-// 100, 88 and 111, and 124 and 101 at 80.
+// or of 256 with the pairs as the first, by the pairs that an expert has on average: with 8, 16, 24, 28, 32 and 40 of them, 64
+// experts of 2560 x 640 (six to a token) took 113, 125, 134, 142, 170 and 202 us with 32 and 133, 136, 137, 137, 138 and 140 with
+// 256; 128 of 1024 x 512 (eight to a token) 83, 87, 96, 101, 114 and 139, and 94, 96, 98, 99, 100 and 101; 16 of 1280 x 2560 (two)
+// 63, 75, 71, 76, 84 and 88, and 67, 69, 69, 85, 85 and 85; 8 of 512 x 1024 (two) 21, 24, 25, 22, 22 and 22, and 25 throughout.
 Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   const size_t pairs = static_cast<size_t>(a.tokens) * a.top_k;
   Plan l = {};
@@ -463,7 +464,7 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
                      a.up_out_stride > 0 && a.down_in_stride > 0 && a.down_out_stride > 0 && (a.tokens == 1 || a.x_stride >= a.hidden);
   if (a.dtype != HC_F32 && aligned && steps && !(a.flags & HC_FLAG_FORCE_GENERAL)) {
     const size_t mean = pairs / a.num_experts;
-    l.rows = mean <= 32 ? 32 : 256;
+    l.rows = mean <= 24 ? 32 : 256;
   }
   size_t at = 0;
   const auto take = [&](size_t bytes) {
