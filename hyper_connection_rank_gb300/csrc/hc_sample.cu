@@ -3,7 +3,7 @@
 // Three kernels. Two are for what most calls ask, and leave what they cannot decide to the third, which decides every row:
 //
 //   pick_kernel    rows that filter, where a few hundred tokens at most stay
-//   stream_kernel  calls that filter nothing, from 2^20 logits on
+//   stream_kernel  calls that filter nothing, from 2^21 logits on
 //   sample_kernel  any row: all of a small call that filters nothing, otherwise what the others have left undecided
 //
 // In the third a cluster of CTAs takes a row and reads it once: each CTA keeps its slice of the row in shared memory, where
@@ -805,7 +805,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
 constexpr int kStreamThreads = 128, kStreamWarps = kStreamThreads / 32, kStreamCtas = 7;  // CTAs to an SM
 constexpr int kChunk = 512, kPerLane = kChunk / 32;
 constexpr int kMaxChunks = kSampleMaxVocab / kChunk + 1;
-constexpr int64_t kStreamLeast = 1 << 20;  // logits of a call, below which one kernel is less than two
+// Logits of a call, below which one kernel is less than two: with 8, 16, 32, 64 and 128 rows of 131072 the two took 15, 17, 31,
+// 24 and 38 us and sample_kernel alone 16, 26, 25, 48 and 86, with 64, 128 and 256 rows of 32000 22, 32 and 34, and 17, 26 and 49,
+// with 256 and 512 rows of 4096 16 and 18, and 15 and 29.
+constexpr int64_t kStreamLeast = 1 << 21;
 constexpr int kUnitBits = 13;              // a chunk's largest weight is 2^43 to 2^44 units, 409600 of them below 2^63
 
 // 2^(30 + i / 16), rounded.

@@ -31,7 +31,7 @@ extern "C" {
  *
  * Weights are formed and added as integers, so that sums are exact whatever
  * their order. In units of 2^-43 of the largest, each is within about 2^-38 of
- * its own size; in calls that filter nothing and have 2^20 logits or more,
+ * its own size; in calls that filter nothing and have 2^21 logits or more,
  * within 2^-30 of it, in units of 2^-43 or less of the largest of each 512
  * logits. A result differs from the definition above only where a sum comes
  * within about that much of what it is compared with. A token whose weight is

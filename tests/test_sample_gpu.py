@@ -196,7 +196,8 @@ def test_captured_and_on_a_stream(hc):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=ids)
-@pytest.mark.parametrize("rows,vocab,scale", [(40, 50001, 2.0), (300, 4099, 3.0), (8, 262144, 1.0), (600, 2047, 0.3), (3, 400001, 6.0)])
+@pytest.mark.parametrize("rows,vocab,scale", [(40, 50001, 2.0), (300, 4099, 3.0), (8, 262144, 1.0), (600, 2047, 0.3), (3, 400001, 6.0),
+                                              (44, 50001, 2.0), (600, 4099, 3.0), (1100, 2047, 0.3), (6, 400001, 6.0)])
 def test_whole_distribution(hc, rows, vocab, scale, dtype):
     """Large calls that filter nothing, whose rows are read by chunks."""
     x = rnd(30, rows, vocab + 5, dtype=dtype, scale=scale)[:, 3:vocab + 3]
@@ -207,8 +208,10 @@ def test_whole_distribution(hc, rows, vocab, scale, dtype):
     check(hc, x, uniforms(34, rows), temperature=t)
 
 
-def test_whole_distribution_odd_rows(hc):
-    n, vocab = 64, 20000
+@pytest.mark.parametrize("n", [64, 128])
+def test_whole_distribution_odd_rows(hc, n):
+    """(By the kernel for any row, and by chunks first.)"""
+    vocab = 20000
     x = rnd(35, n, vocab, scale=2.0)
     x[0] = -math.inf
     x[1] = math.nan
@@ -229,8 +232,8 @@ def test_whole_distribution_odd_rows(hc):
     t[5], t[13], t[14] = math.inf, 1e-38, math.nan
     got = hc.token_sample(x.cuda(), torch.full((n,), 0.5).cuda(), temperature=t.cuda())
     assert got[5] == vocab // 2 and got[13] == int(x[13].argmax()) and got[14] == int(x[14].argmax())
-    y = torch.zeros(64, vocab).cuda()
-    assert hc.token_sample(y, (torch.arange(64) / 64).cuda()).tolist() == [i * vocab // 64 for i in range(64)]
+    y = torch.zeros(n, vocab).cuda()
+    assert hc.token_sample(y, (torch.arange(n) / n).cuda()).tolist() == [i * vocab // n for i in range(n)]
 
 
 @pytest.mark.parametrize("k", [2, 100, 1000, 2040, 2049, 3000])
