@@ -1064,6 +1064,7 @@ struct PickShared {
   u64 red[kPickWarps];
   alignas(8) uint32_t hist[kBins];
   int border;
+  uint32_t mass;  // of the largest logits of the threads down to the border, in units of the largest (a float's bits)
   uint32_t listed, looking;
   u64 list[kPicked], weights[kPicked];
   uint16_t who[kPickThreads];  // threads whose logits are looked through again
@@ -1077,6 +1078,10 @@ __device__ __forceinline__ uint32_t add_cluster(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void st_cluster32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+
+// The halves of cluster_sync_all.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_acquire() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint2 ld_cluster2(uint32_t addr) {
   uint2 v;
@@ -1103,6 +1108,7 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
   if (tid < 64) sh.table[tid] = kExp2[tid];
   if (tid == 64) sh.listed = 0;
   if (tid == 65) sh.border = -1;
+  if (tid == 67) sh.mass = 0x7f800000u;
   if (tid == 66) sh.looking = 0;
   pdl_wait();
   pdl_trigger();
@@ -1177,7 +1183,15 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
   const uint32_t some = cut_k ? p.k : kTryP;
   if ((cut_k || cut_p) && some <= kMostK) {
     if (arg >= 0) atomicAdd(&sh.hist[mine], 1u);
-    cluster_sync_all();
+    cluster_arrive();
+    if (cut_p && !cut_k) {  // (while the others come)
+      u64 sum = 0;
+      visit([&](int, float x) { sum += scale.weight(x); });
+      sum = pick_sum(sh, sum);
+      if (tid < ctas) st_cluster(mapa_shared(smem_addr(&sh.sums[rank]), tid), sum);
+    }
+    cluster_wait_acquire();
+    __syncthreads();  // (that sum is read by all)
     if (rank == 0) {
       uint32_t n0 = 0, n1 = 0;
       for (int i = 0; i < ctas; ++i) {
@@ -1185,24 +1199,38 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
         n0 += n.x;
         n1 += n.y;
       }
-      const u64 upto = warp_scan_u64(n0 + n1);
+      // counts, and below them the weights of those logits by their steps, in units of 2^-20 (together at most 2^34 of them)
+      const auto entry = [&](uint32_t n, int step) {
+        return static_cast<u64>(n) << 36 | static_cast<u64>(n * exp2f(20.0f - step * (kRange / kBins)));
+      };
+      const u64 e0 = entry(n0, 2 * tid), e1 = entry(n1, 2 * tid + 1), upto = warp_scan_u64(e0 + e1);
       if (lane == 31) sh.red[warp] = upto;
       __syncthreads();
-      uint32_t before = static_cast<uint32_t>(upto) - (n0 + n1);
-      for (int w = 0; w < warp; ++w) before += static_cast<uint32_t>(sh.red[w]);
+      u64 prior = upto - (e0 + e1);
+      for (int w = 0; w < warp; ++w) prior += sh.red[w];
+      const uint32_t before = static_cast<uint32_t>(prior >> 36);
       const int at = before < some && some <= before + n0 ? 2 * tid : before + n0 < some && some <= before + n0 + n1 ? 2 * tid + 1 : -1;
-      if (at >= 0)
-        for (int i = 0; i < ctas; ++i) st_cluster32(mapa_shared(smem_addr(&sh.border), i), static_cast<uint32_t>(at));
+      if (at >= 0) {
+        const u64 upto_it = prior + e0 + (at & 1 ? e1 : 0);
+        const float mass = static_cast<float>(upto_it & ((1ull << 36) - 1)) * 0x1p-20f;
+        for (int i = 0; i < ctas; ++i) {
+          st_cluster32(mapa_shared(smem_addr(&sh.border), i), static_cast<uint32_t>(at));
+          st_cluster32(mapa_shared(smem_addr(&sh.mass), i), __float_as_uint(mass));
+        }
+      }
     }
     cluster_sync_all();
     // (fewer threads than that have a logit: all steps, unless min_p has a say)
     bin = min(bin, sh.border < 0 ? kBins : sh.border);
   }
+  u64 total = 0;
   if (cut_p && !cut_k) {
-    u64 sum = 0;
-    visit([&](int, float x) { sum += scale.weight(x); });
-    sum = pick_sum(sh, sum);
-    if (tid == 0) st_cluster(mapa_shared(smem_addr(&sh.sums[rank]), 0), sum);
+    for (int i = 0; i < ctas; ++i) total += sh.sums[i];
+    // (most of what would be listed is among those, so there is no hope if p of all is far above them)
+    if (p.p * static_cast<float>(total) > 1.3f * __uint_as_float(sh.mass) * static_cast<float>(kOne)) {
+      if (rank == 0 && tid == 0) a.tokens[r] = kUndecided;
+      return;
+    }
   }
   // (their vectors are dealt out to all threads, so that all are on their way at once)
   const uint32_t ballot = __ballot_sync(0xffffffffu, mine <= bin);
@@ -1259,12 +1287,7 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
   u64 goal = ~0ull;
   if (cut_k && place >= p.k) w = 0;
   if (cut_p) {
-    u64 total = 0;
-    if (cut_k) {
-      total = pick_sum(sh, w);
-    } else {
-      for (int i = 0; i < ctas; ++i) total += sh.sums[i];
-    }
+    if (cut_k) total = pick_sum(sh, w);
     goal = reach(p.p, total);
     if (!cut_k && listed < goal) {  // (the last one that stays is not among them)
       if (tid == 0) a.tokens[r] = kUndecided;
@@ -1353,7 +1376,7 @@ cudaError_t launch_token_sample(const hc_token_sample_t& p, int num_sms, cudaStr
       using T = decltype(type);
       const int most_here = wide(wide_clusters<pick_kernel<T>>(kPickThreads, 0));
       int split = 1;
-      while (more(split, most_here, kPickThreads * 8)) split *= 2;
+      while (more(split, most_here, kPickThreads * 4)) split *= 2;
       return launch_pdl(pick_kernel<T>, dim3(static_cast<unsigned>(p.rows * split)), dim3(kPickThreads), 0, s, split, a, split);
     };
     const cudaError_t e = p.dtype == HC_F32   ? launch(float())
