@@ -29,8 +29,8 @@
 //
 // Bound: the third kernel's passes over its slices (four with a border, 50 instructions to a logit in those that weigh), the
 // histogram's atomics and its CTAs' steps together. With pick_kernel's attempt before it, one row of 131072 fp32 logits takes
-// 35 us with a top_k of 20000 and 41 with a top_p that leaves thousands (59 where all logits are within few steps), 64 rows
-// take 102 and 128 (171). With 512 threads to a CTA they took a tenth to a fifth longer.
+// 35 us with a top_k of 20000 and 37 with a top_p that leaves thousands (56 where all logits are within few steps), 64 rows
+// take 102 and 128 (166). With 512 threads to a CTA they took a tenth to a fifth longer.
 #include <algorithm>
 #include <atomic>
 
@@ -47,8 +47,8 @@ using u64 = unsigned long long;
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 // CTAs to a row at most, and to one of no more rows than the device can have clusters of so many together (one to six of
-// 131072 fp32 logits with a top_p that leaves thousands took 47.5 to 49 us with 8 and 40 to 42 with 16, with one that leaves
-// few 18 and 17, a top_k of 20000 of 262144 53 to 56 and 42 to 46).
+// 131072 fp32 logits with a top_p that leaves thousands take 44 to 45 us with 8 and 36 to 38 with 16, with one that leaves few
+// 18 to 19 with either, a top_k of 20000 of 262144 53 to 55 and 42 to 45).
 constexpr int kCluster = 8, kMaxCluster = 16;
 constexpr int kMaxSlice = kSampleMaxVocab / kCluster;  // elements that a CTA keeps
 constexpr int kOneBits = 43;
@@ -1049,8 +1049,11 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, kStreamC
 // Bound: latency, of the logits' bytes (1 to 2 us of them) and of four or five steps of a row's CTAs together. 64 rows of
 // 131072 fp32 logits with top_k, top_p and min_p take 15 us (33.6 MB: 4.9 us): 2.8 until all are read, 1.3 for the largest, 2 for the
 // border, 2 for the list, 3 to finish, and 2 for the next kernel to see that nothing is left. One row of 131072 bf16 logits with
-// top_p takes 18 us, 3 of them for the weights of all. (Dealing out the vectors that are looked through again to all threads
+// top_p takes 19 us, 3 of them for the weights of all. (Dealing out the vectors that are looked through again to all threads
 // took 64 rows from 22 to 15 us; a histogram for each CTA rather than the first one's for all, one row from 23 to 20 with 8 CTAs.)
+//
+// CTAs to a row, as long as rows leave SMs idle: as many as leave 4096 logits to each (one row of 50001 with min_p takes 7.8 us with
+// eight and 8.7 with the four that 8192 would make it; from 131072 on 8192 or less make no difference).
 
 constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32;
 constexpr int kPicked = 512;   // candidates at most
