@@ -1,6 +1,9 @@
 """Calls of the experts' layer, routing and the choice of tokens that the documentation allows but that ordinary use seldom makes,
 and the refusals that need a GPU."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -145,6 +148,37 @@ def test_sampling_at_once(hc):  # noqa: F811
     torch.cuda.synchronize()
     for i, pair in enumerate(got):
         assert all(torch.equal(y, want[i % len(kinds)]) for y in pair)
+
+
+FIRST_CALLS = """
+import torch, hyper_connection_rank_gb300 as hc
+g = torch.Generator(device="cuda").manual_seed(1)
+rand = lambda *s: torch.randn(*s, generator=g, device="cuda")
+logits, x, weights = rand(3, 70000), rand(40, 64).half(), [rand(8, *s).half() for s in ((64, 32), (64, 32), (32, 64))]
+many, u, scores = rand(900, 64).half(), torch.rand(3, generator=g, device="cuda"), rand(40, 8)
+ids = torch.randint(0, 8, (900, 2), generator=g, device="cuda", dtype=torch.int32)
+share = torch.rand(900, 2, generator=g, device="cuda")
+def run():
+    e, w = hc.expert_route(scores, 2)
+    return [hc.token_sample(logits, u), hc.token_sample(logits, u, top_p=0.9), hc.token_sample(logits, u, top_k=9), e, w,
+            hc.expert_mlp(x, *weights, e, w), hc.expert_mlp(many, *weights, ids, share),
+            hc.expert_mlp(x.float(), *[t.float() for t in weights], e, w)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+print("the same")
+"""
+
+
+def test_first_calls_in_a_capture(hc):  # noqa: F811
+    """A process whose first call of each kind is captured: what is asked of the device once must not disturb the capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and "the same" in got.stdout, got.stderr[-2000:]
 
 
 # ---------------------------------------------------------------------------------------------- refusals --
