@@ -333,12 +333,14 @@ template <typename T, bool kInner> cudaError_t launch_general(const GeneralArgs&
 // ---------------------------------------------------------------- combine --
 
 // A warp has 256 features of a token, eight to a lane, and loads four or eight experts' rows at a time (rows of o are padded to a
-// multiple of sixteen). Bound: bytes, top_k + 1 rows a token: eight experts' rows of 8191 tokens and 2560 features as 16-bit
-// integers (388 MB) take 72 us, 5.4 TB/s.
+// multiple of sixteen). With kPlanes an expert's result is the sum of some planes of o, counts[] of them.
+// Bound: bytes, top_k rows of floats and one of T a token: eight experts' rows of 8191 tokens and 2560 features (713 MB) take 105 us,
+// 6.8 TB/s. (16-bit integers with an exponent for sixteen features took 72 and the product before it 164 instead of 195, but cost
+// the neighbours of a large feature their digits: with one of 1000 times their size 1.4% of theirs.)
 constexpr int kCombineWarps = 4;
-template <typename T, bool kInts>
-__global__ void __launch_bounds__(32 * kCombineWarps, kInts ? 7 : 5)
-combine_kernel(hc_expert_mlp_t p, const void* __restrict__ o, int64_t o_step, const uint8_t* __restrict__ exps, int64_t exp_step,
+template <typename T, bool kPlanes>
+__global__ void __launch_bounds__(32 * kCombineWarps, 5)
+combine_kernel(hc_expert_mlp_t p, const float* __restrict__ o, int64_t o_step, const uint8_t* __restrict__ counts, int64_t count_step,
                bool vec) {
   pdl_wait();
   pdl_trigger();
@@ -346,66 +348,53 @@ combine_kernel(hc_expert_mlp_t p, const void* __restrict__ o, int64_t o_step, co
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5), t = unit / blocks;
   if (t >= p.tokens) return;
   const int c = static_cast<int>(unit - t * blocks) * 256 + lane * 8;
-  // lane j has the j-th expert's number, weight and (floats) planes; those that take part are in `valid`
+  // lane j has the j-th expert's number, weight and planes; those that take part are in `valid`
   const int64_t first = t * p.top_k;
   const int id = lane < p.top_k ? p.experts[first + lane] : -1;
   const float weight = lane < p.top_k ? p.weights[first + lane] : 0.0f;
-  const uint32_t planes = !kInts && exps != nullptr && lane < p.top_k ? exps[(first + lane) * exp_step + (c - lane * 8) / 256] : 1;
+  const int planes = kPlanes && lane < p.top_k ? counts[(first + lane) * count_step + (c - lane * 8) / 256] : 1;
   const unsigned valid = __ballot_sync(0xffffffffu, id >= 0 && id < p.num_experts);
   const int count = __popc(valid);
   T* out = static_cast<T*>(p.out) + t * p.out_stride;
   Two sums[4] = {Two(0.0f), Two(0.0f), Two(0.0f), Two(0.0f)};
   const bool have = c < p.hidden;
-  constexpr int kAhead = kInts ? 8 : 4;
+  constexpr int kAhead = kPlanes ? 4 : 8;
   const int64_t plane = p.tokens * p.top_k * o_step;
   unsigned left = valid;
   for (int j0 = 0; j0 < count; j0 += kAhead) {
-    uint4 q[kAhead][kInts ? 1 : 2], other[kAhead][2];  // other: the second plane, zeros without one
-    uint32_t exp[kAhead];
-    int from[kAhead];
+    float4 q[kAhead][2], other[kPlanes ? kAhead : 1][2];  // other: the second plane, zeros without one
+    int parts[kAhead], from[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      from[j] = __ffs(left) - 1;
+      from[j] = max(__ffs(left) - 1, 0);
       left &= left - 1;
       const bool take = j0 + j < count && have;
-      const int64_t at = (first + from[j]) * o_step + c;
-      if constexpr (kInts) {
-        if (take) {
-          q[j][0] = *reinterpret_cast<const uint4*>(static_cast<const int16_t*>(o) + at);
-          exp[j] = exps[(first + from[j]) * exp_step + c / 16];
-        }
-      } else {
-        const float* f = static_cast<const float*>(o) + at;
-        exp[j] = __shfl_sync(0xffffffffu, planes, max(from[j], 0));
+      const float4* row = reinterpret_cast<const float4*>(o + (first + from[j]) * o_step + c);
+      parts[j] = kPlanes ? __shfl_sync(0xffffffffu, planes, from[j]) : 1;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          q[j][i] = take ? reinterpret_cast<const uint4*>(f)[i] : make_uint4(0, 0, 0, 0);
-          other[j][i] = take && exp[j] > 1 ? reinterpret_cast<const uint4*>(f + plane)[i] : make_uint4(0, 0, 0, 0);
-        }
+      for (int i = 0; i < 2; ++i) {
+        q[j][i] = take ? row[i] : make_float4(0, 0, 0, 0);
+        if constexpr (kPlanes) other[j][i] = take && parts[j] > 1 ? row[plane / 4 + i] : make_float4(0, 0, 0, 0);
       }
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (j0 + j < count) {
-        const float by = __shfl_sync(0xffffffffu, weight, from[j]);
-        if constexpr (kInts) {
-          if (have) BlockFloat::add8(q[j][0], exp[j], by, sums);
-        } else {
-          float f[8], g[8];
+        const Two by(__shfl_sync(0xffffffffu, weight, from[j]));
+        float4 f[2] = {q[j][0], q[j][1]};
+        if constexpr (kPlanes) {
+          const auto add = [&](const float4* g) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            *reinterpret_cast<uint4*>(f + 4 * i) = q[j][i];
-            *reinterpret_cast<uint4*>(g + 4 * i) = other[j][i];
-          }
+            for (int i = 0; i < 2; ++i) f[i].x += g[i].x, f[i].y += g[i].y, f[i].z += g[i].z, f[i].w += g[i].w;
+          };
+          add(other[j]);
+          for (int n = 2; n < parts[j] && have; ++n)  // (of a few tiles only)
+            add(reinterpret_cast<const float4*>(o + n * plane + (first + from[j]) * o_step + c));
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] += g[i];
-          for (uint32_t n = 2; n < exp[j] && have; ++n) {  // (of a few tiles only)
-            const float4* h = reinterpret_cast<const float4*>(static_cast<const float*>(o) + n * plane + (first + from[j]) * o_step + c);
-            const float4 x = h[0], y = h[1];
-            f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w, f[4] += y.x, f[5] += y.y, f[6] += y.z, f[7] += y.w;
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sums[i] = fma2(Two(by), Two(f[2 * i], f[2 * i + 1]), sums[i]);
+        for (int i = 0; i < 2; ++i) {
+          sums[2 * i] = fma2(by, Two(f[i].x, f[i].y), sums[2 * i]);
+          sums[2 * i + 1] = fma2(by, Two(f[i].z, f[i].w), sums[2 * i + 1]);
         }
       }
     }
@@ -432,13 +421,15 @@ combine_kernel(hc_expert_mlp_t p, const void* __restrict__ o, int64_t o_step, co
   }
 }
 
-template <typename T, bool kInts>
-cudaError_t launch_combine(const hc_expert_mlp_t& a, const void* o, int64_t o_step, const uint8_t* exps, int64_t exp_step,
+// counts: NULL where o is one plane.
+template <typename T>
+cudaError_t launch_combine(const hc_expert_mlp_t& a, const float* o, int64_t o_step, const uint8_t* counts, int64_t count_step,
                            cudaStream_t s) {
   const bool vec = a.hidden % 8 == 0 && a.out_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
   const int64_t units = a.tokens * ((a.hidden + 255) / 256);
-  return launch_pdl(combine_kernel<T, kInts>, dim3(static_cast<unsigned>((units + kCombineWarps - 1) / kCombineWarps)),
-                    dim3(32 * kCombineWarps), 0, s, 1, a, o, o_step, exps, exp_step, vec);
+  const dim3 grid(static_cast<unsigned>((units + kCombineWarps - 1) / kCombineWarps)), block(32 * kCombineWarps);
+  return counts != nullptr ? launch_pdl(combine_kernel<T, true>, grid, block, 0, s, 1, a, o, o_step, counts, count_step, vec)
+                           : launch_pdl(combine_kernel<T, false>, grid, block, 0, s, 1, a, o, o_step, counts, count_step, vec);
 }
 
 // ---------------------------------------------------------------- layout --
@@ -447,8 +438,8 @@ struct Plan {
   int rows;  // pairs to a tile of the tensor cores' products, 32 or 256; 0: the general ones
   int64_t tickets;
   int planes;  // of o
-  int64_t h_step, o_step, exp_step;
-  size_t bounds, order, count, part, h, o, exps, total;
+  int64_t h_step, o_step, count_step;
+  size_t bounds, order, tickets_at, part, h, o, counts, total;
 };
 
 // Which products run, and where their buffers lie in the workspace. Tiles of 32 pairs with the weights as the first operand
@@ -479,21 +470,17 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   const bool few = l.rows == 32;
   if (few) {
     l.tickets = experts_um_tiles(a, l.rows, true);
-    l.count = take(l.tickets * sizeof(unsigned int));
+    l.tickets_at = take(l.tickets * sizeof(unsigned int));
     l.part = take(static_cast<size_t>(num_sms) * 2 * 2 * l.rows * 128 * sizeof(float));
   }
   l.h = take(pairs * l.h_step * (l.rows ? 2 : 4));
   // A plane of o for each piece that a tile of the outer product can be cut into: two where runs are cut, and four where so
   // few tiles are possible that each can be on three SMs or more.
   l.planes = few ? ((pairs + l.rows - 1) / l.rows * ((a.hidden + 255) / 256) * 3 <= static_cast<size_t>(num_sms) ? 4 : 2) : 1;
-  l.o = take(pairs * l.o_step * (l.rows && !few ? 2 : 4) * l.planes);
-  if (l.rows && !few) {
-    l.exp_step = static_cast<int64_t>(align_up(a.hidden, 256)) / 16;
-    l.exps = take(pairs * l.exp_step);
-  }
+  l.o = take(pairs * l.o_step * 4 * l.planes);
   if (few) {
-    l.exp_step = (a.hidden + 255) / 256;
-    l.exps = take(pairs * l.exp_step);
+    l.count_step = (a.hidden + 255) / 256;
+    l.counts = take(pairs * l.count_step);
   }
   l.total = at;
   return l;
@@ -503,7 +490,8 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
   const Plan l = make_plan(a, aligned, num_sms);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const ExpertLists lists = {reinterpret_cast<int32_t*>(ws + l.bounds), reinterpret_cast<int32_t*>(ws + l.order)};
-  unsigned int* tickets = reinterpret_cast<unsigned int*>(ws + l.count);
+  unsigned int* tickets = reinterpret_cast<unsigned int*>(ws + l.tickets_at);
+  float* o = reinterpret_cast<float*>(ws + l.o);
   const int pairs = static_cast<int>(a.tokens * a.top_k), count = static_cast<int>(l.tickets);
   cudaError_t e = pairs > 4096 ? launch_pdl(lists_kernel<1024>, dim3(a.num_experts), dim3(1024), 0, s, 1, a.experts, pairs,
                                             a.num_experts, lists, tickets, count)
@@ -512,20 +500,18 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
   if (e != cudaSuccess) return e;
   if constexpr (sizeof(T) == 2) {
     if (l.rows) {
-      const ExpertUm u = {lists, ws + l.h, ws + l.o, ws + l.exps, l.h_step, l.o_step, l.exp_step,
+      uint8_t* counts = l.rows == 32 ? ws + l.counts : nullptr;
+      const ExpertUm u = {lists, ws + l.h, o, counts, l.h_step, l.o_step, l.count_step,
                           reinterpret_cast<float*>(ws + l.part), tickets, static_cast<int64_t>(pairs) * l.o_step, l.planes, l.rows};
       e = l.rows == 256 ? launch_experts_many(a, u, num_sms, s) : launch_experts_few(a, u, num_sms, s);
-      if (e != cudaSuccess) return e;
-      return l.rows == 256 ? launch_combine<T, true>(a, ws + l.o, l.o_step, ws + l.exps, l.exp_step, s)
-                           : launch_combine<T, false>(a, ws + l.o, l.o_step, ws + l.exps, l.exp_step, s);
+      return e != cudaSuccess ? e : launch_combine<T>(a, o, l.o_step, counts, l.count_step, s);
     }
   }
-  const GeneralArgs g = {a, lists, reinterpret_cast<float*>(ws + l.h), reinterpret_cast<float*>(ws + l.o), l.o_step};
+  const GeneralArgs g = {a, lists, reinterpret_cast<float*>(ws + l.h), o, l.o_step};
   e = launch_general<T, true>(g, num_sms, s);
   if (e != cudaSuccess) return e;
   e = launch_general<T, false>(g, num_sms, s);
-  if (e != cudaSuccess) return e;
-  return launch_combine<T, false>(a, ws + l.o, l.o_step, nullptr, 0, s);
+  return e != cudaSuccess ? e : launch_combine<T>(a, o, l.o_step, nullptr, 0, s);
 }
 
 }  // namespace

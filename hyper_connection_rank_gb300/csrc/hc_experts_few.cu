@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads<kInner>, 2) few_kernel(const __grid_c
         }
       };
       if (!kInner && warp == 2 && lane < p.rows)
-        a.exps[place * a.exp_step + p.feature / (2 * kHalf)] = static_cast<uint8_t>(p.pieces());
+        a.counts[place * a.count_step + p.feature / (2 * kHalf)] = static_cast<uint8_t>(p.pieces());
       float* part = a.part + static_cast<int64_t>(p.place(blockIdx.x)) * (2 * kRows * kHalf) + me;
 #pragma unroll
       for (int c0 = 0; c0 < kRows; c0 += 16) {
@@ -331,10 +331,10 @@ bool fill_args(Args* a, const hc_expert_mlp_t& p, const ExpertUm& u, bool inner,
   a->order = u.lists.order;
   a->x = p.x;
   a->x_step = p.x_stride;
-  a->out = inner ? u.h : u.o;
+  a->out = inner ? u.h : static_cast<void*>(u.o);
   a->out_step = inner ? u.h_step : u.o_step;
-  a->exps = u.exps;
-  a->exp_step = u.exp_step;
+  a->counts = u.counts;
+  a->count_step = u.count_step;
   a->experts = p.num_experts;
   a->top_k = p.top_k;
   a->inputs = inner ? p.hidden : p.inner;

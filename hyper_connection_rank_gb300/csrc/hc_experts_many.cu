@@ -10,8 +10,8 @@
 // tensor cores' cycles). Accumulators take turns, so that a tile is written while
 // the next one is multiplied. Whole tiles are dealt out in turn.
 //
-// 8191 tokens at eight of 64 experts of 2560 x 640 in bf16: 298 to 305 us (inner, 1.42 PFLOP/s, 75% of measured) and 164 (outer, 1.31),
-// tensor cores active for 75 and 68% of the cycles; a stage takes 0.32 us where the MMAs take 0.27, and tiles are 90% full. 1301
+// 8191 tokens at eight of 64 experts of 2560 x 640 in bf16: 294 to 305 us (inner, 1.42 PFLOP/s, 75% of measured) and 195 (outer, 1.10:
+// its 671 MB of results leave at 3.4 TB/s beside L2's feed of the stages), the inner one's tensor cores active for 75% of the cycles; a stage takes 0.32 us where the MMAs take 0.27, and tiles are 90% full. 1301
 // tokens at two of 16 experts of 1280 x 2560 in fp16: 58 and 36 us, 3.6 and 2.9 TB/s of weights; tiles are half full, 20
 // tiles of pairs by 20 and 5 of features are 5.3 and 1.3 rounds of 76 pairs of CTAs, and the first two tiles of each wait for cold
 // weights. (Sending those to L2 earlier, by TMA or by the gathering warps, took 10 to 20% longer: both have no time to spare.
@@ -179,12 +179,29 @@ __global__ void __launch_bounds__(kThreads<kInner>, 1) many_kernel(const __grid_
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      // This thread has pair `me`, a column for each feature. Thirty-two features of the warp's 32 pairs at a time go through
-      // shared memory, so that four lanes write 64 bytes of one row (a row for each lane would be 32 requests an instruction).
+      // This thread has pair `me`, a column for each feature. 64 bytes (32 features of h, 16 of o) of the warp's 32 pairs at a
+      // time go through shared memory, so that four lanes write 64 bytes of one row (a row for each lane would be 32 requests an
+      // instruction).
       constexpr int kCols32 = (kInner ? kHalf : 2 * kHalf) / 32 / (kWriters / 4);  // that a warp has, from the first-th on
-      const int part = (warp - 2) / 4, first = part * kCols32;
+      const int first = (warp - 2) / 4 * kCols32;
       uint8_t* stage = smem + kStages * kStage + (warp - 2) * kStageOut;
-      uint32_t exps[2] = {};
+      const int chunk = lane & 3;
+      const auto put = [&](const uint4* q, auto* out, int f0) {
+        constexpr int kEach = 16 / sizeof(*out);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = q[j];
+        __syncwarp();
+        const int f = f0 + chunk * kEach;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + (lane >> 2);
+          const int64_t to = __shfl_sync(0xffffffffu, place, r);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
+          // (rows of out are 16-byte aligned and padded to a multiple of 16 elements)
+          if (quarter * 32 + r < rows && f < a.features) *reinterpret_cast<uint4*>(out + to * a.out_step + f) = v;
+        }
+        __syncwarp();
+      };
 #pragma unroll
       for (int h = 0; h < kCols32; ++h) {
         const int c0 = (first + h) * 32;
@@ -194,41 +211,33 @@ __global__ void __launch_bounds__(kThreads<kInner>, 1) many_kernel(const __grid_
           tmem_ld16_nowait(d + c0 + 16 * i, x[i]);
           if (kInner) tmem_ld16_nowait(d + kHalf + c0 + 16 * i, y[i]);
         }
+        // (all at once: lanes may part below, and the wait is one of the whole warp)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          uint4 q[2];
-          float v[16];
           tmem_ld_wait_r(x[i]);
           if (kInner) tmem_ld_wait_r(y[i]);
-          if (kInner) {
+        }
+        if constexpr (kInner) {
+          uint4 q[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float v[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = saturate<T>(gated(__uint_as_float(x[i][j]), __uint_as_float(y[i][j])));
-            q[0] = V8<T>::pack(v);
-            q[1] = V8<T>::pack(v + 8);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(x[i][j]);
-            exps[h >> 1] |= BlockFloat::pack(v, reinterpret_cast<uint32_t*>(q)) << (16 * (h & 1) + 8 * i);
+            q[2 * i] = V8<T>::pack(v);
+            q[2 * i + 1] = V8<T>::pack(v + 8);
           }
+          put(q, static_cast<T*>(a.out), p.feature + c0);
+        } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<uint4*>(stage + lane * 64 + (((2 * i + j) ^ ((lane >> 1) & 3)) << 4)) = q[j];
-        }
-        __syncwarp();
-        const int chunk = lane & 3, f = p.feature + c0 + chunk * 8;
+          for (int i = 0; i < 2; ++i) {
+            uint4 q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + (lane >> 2);
-          const int64_t to = __shfl_sync(0xffffffffu, place, r);
-          const uint4 q = *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
-          // (rows of out are 16-byte aligned and padded to a multiple of 16 elements)
-          if (quarter * 32 + r < rows && f < a.features) st16(static_cast<T*>(a.out) + to * a.out_step + f, q);
+            for (int j = 0; j < 4; ++j) q[j] = make_uint4(x[i][4 * j], x[i][4 * j + 1], x[i][4 * j + 2], x[i][4 * j + 3]);
+            put(q, static_cast<float*>(a.out), p.feature + c0 + 16 * i);
+          }
         }
-        __syncwarp();
       }
-      if (!kInner && me < rows)  // (a row's exponents are padded to whole tiles)
-        *reinterpret_cast<uint2*>(a.exps + static_cast<int64_t>(place) * a.exp_step + p.feature / 16 + 8 * part) =
-            make_uint2(exps[0], exps[1]);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) first_arrive(&b->acc_empty[buf]);

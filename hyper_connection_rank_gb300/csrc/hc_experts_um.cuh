@@ -43,8 +43,8 @@ struct Args {
   const void* x;               // inner: rows that are gathered, and their step
   int64_t x_step;
   void* out;                   // inner: h in the list's order; outer: o at the pairs' places
-  uint8_t* exps;               // outer, many: an exponent for each 16 elements of o; few: the planes of each 256
-  int64_t out_step, exp_step;  // elements from row to row of out, and of exps
+  uint8_t* counts;             // (few, outer) the planes of each 256 elements of o
+  int64_t out_step, count_step;  // elements from row to row of out, and of counts
   int64_t plane;               // (few, outer) elements from plane to plane of out
   float* part;                 // (few, inner) [2 * CTAs][2 halves][rows][128], for tiles that a cut goes through
   unsigned int* tickets;       // (few, inner) of each tile: pieces that have been written

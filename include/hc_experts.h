@@ -76,11 +76,8 @@ hc_status_t hc_expert_route(const hc_expert_route_t* args, struct CUstream_st* s
  *
  * Numerics: products are summed in fp32. In the fp16/bf16 kernels the inner
  * values silu(.) * (.) are rounded to T for the product with down (the tensor
- * core's operands are 16 bits). Where experts have many tokens, each chosen
- * expert's result is kept as 16-bit integers with an exponent for sixteen
- * neighbours, off by 2^-15 of the largest of them at most (and 0 where all are
- * below 2^-126); otherwise it is fp32. The sum over the chosen experts is fp32,
- * rounded to T once. fp16 inner values saturate at its largest finite value
+ * core's operands are 16 bits). Each chosen expert's result is fp32, and so is
+ * the sum over them, rounded to T once. fp16 inner values saturate at its largest finite value
  * rather than turn to infinity. Limits: top_k <= 32, num_experts <= 1024, hidden and inner
  * <= 65536, tokens * top_k < 2^24. */
 typedef struct {
