@@ -105,7 +105,7 @@ __device__ __forceinline__ void l2_prefetch(const void* src, uint32_t bytes) {
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
-// The same, reading only the first `bytes` (0 or 16) and filling up with zeros;
+// The same, reading only the first `bytes` (0 to 16) and filling up with zeros;
 // src must be a valid address either way.
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");

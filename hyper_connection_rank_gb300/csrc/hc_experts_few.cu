@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kThreads<kInner>, 2) few_kernel(const __grid_c
       for (int c0 = 0; c0 < kRows; c0 += 16) {
         if (c0 < p.rows) {
           float v[2][16];
+          __syncwarp();  // (lanes part where they write, and the loads are the whole warp's)
           tmem_ld16(d + c0, v[0]);
           tmem_ld16(d + kRows + c0, v[1]);
 #pragma unroll
