@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(kGenThreads, kPer == 1 ? 3 : 2) general_kernel
       const int64_t at = first + r;
       const float v0 = sum(r, 0, f), v1 = sum(r, 1, f);
       if (kInner) {
-        if (n0 + f < features) g.h[at * p.inner + n0 + f] = v0 / (1.0f + expf(-v0)) * v1;
+        const float e = expf(-0.5f * fabsf(v0));
+        if (n0 + f < features) g.h[at * p.inner + n0 + f] = silu_times(v0, v1, e, 1.0f / fmaf(e, e, 1.0f));
       } else {
         float* to = g.o + g.lists.order[at] * g.o_step + n0 + f;
         if (n0 + f < features) to[0] = v0;

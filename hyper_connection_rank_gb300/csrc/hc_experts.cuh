@@ -16,6 +16,15 @@ struct ExpertLists {
   int32_t* order;   // [pairs]
 };
 
+// silu(g) u = g u / (1 + e^-g) with e = e^(-|g| / 2) and r = 1 / (1 + e^2): g r u above 0, (g e r)(u e) below. In this order no
+// product overflows where the result does not (g u does: g = -10 and u = 4e37 make -1.8e34), nor does e^-g (from g = -89 on, where
+// u can still be large enough for the result to count). No branch, since lanes must not part between the loads from tensor
+// memory that a warp makes as one.
+__device__ __forceinline__ float silu_times(float g, float u, float e, float r) {
+  const float by = g < 0.0f ? e : 1.0f;
+  return g * by * r * (u * by);
+}
+
 // The products on the tensor cores, for fp16 and bf16 (hc_experts_few.cu, hc_experts_many.cu).
 struct ExpertUm {
   ExpertLists lists;

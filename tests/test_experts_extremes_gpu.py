@@ -3,9 +3,51 @@ import pytest
 import torch
 
 import _experts_ref as R
-from test_experts_gpu import BF16, F16, hc, ids, layer, on_gpu, within  # noqa: F401
+from test_experts_gpu import BF16, F16, F32, hc, ids, layer, on_gpu, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------------ activation --
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=ids)
+@pytest.mark.parametrize("general", [False, True], ids=["", "general"])
+@pytest.mark.parametrize("tokens", [2, 200])
+def test_activation_over_the_whole_range(hc, tokens, general, dtype):  # noqa: F811
+    """silu(g) u where g u overflows, and where exp(-g) does. Every sum has one product, so that g, u and h down are as given.
+
+    silu: the exponential's argument is off by 2 |g| v of the result (v = 2^-24: the constant and the product), exponential and
+    quotient by 8 v, a product 1 v; h and the result are rounded to T (u each, a unit at 2^-126 of subnormal numbers: 2^-133 in bf16
+    and 2^-149 in float32, of h by way of down)."""
+    pairs = [(g, u) for g in (-5.0, -10.0, -30.0, -79.0, -80.5, -88.0, -89.0, -100.0, -120.0, -150.0, -170.0, 5.0, 80.0, 100.0, 300.0)
+             for u in (3e38, -1e38, 4e37, 1e30, 1.0)]
+    pairs += [(-1e20, 1e25), (-1e30, 3e38), (1e20, 1e10), (3e38, 0.5), (-0.0, 3e38), (0.0, -3e38), (-3e38, 1.0)]
+
+    def value(g, u):
+        return g * torch.exp(torch.minimum(g, torch.zeros_like(g))) / (1 + torch.exp(-g.abs())) * u
+
+    # (what is beyond the type is infinite, and an infinity times one of down's zeros is no number)
+    g, u = torch.tensor(pairs).to(dtype).t()
+    fits = value(g.double(), u.double()).abs() < 3.3e38
+    g, u = g[fits], u[fits]
+    inner = -(-len(g) // 8) * 8
+    g, u = (torch.nn.functional.pad(t, (0, inner - len(t))) for t in (g, u))
+    x = torch.zeros(tokens, 128, dtype=dtype)
+    x[:, 3] = 1.0
+    gate, up = torch.zeros(1, 128, inner, dtype=dtype), torch.zeros(1, 128, inner, dtype=dtype)
+    gate[0, 3], up[0, 3] = g, u
+    scale = 2.0 ** -10
+    down = torch.nn.functional.pad(torch.eye(inner, dtype=dtype), (0, 128 - inner))[None] * scale
+    e, w = torch.zeros(tokens, 1, dtype=torch.int32), torch.ones(tokens, 1)
+    y = hc.expert_mlp(*on_gpu((x, gate, up, down, e, w)), flags=hc.HC_FLAG_FORCE_GENERAL if general else 0)
+    g, u = g.double(), u.double()
+    h = value(g, u)
+    unit = {BF16: 2.0 ** -133, F32: 2.0 ** -149}[dtype]
+    of_t = 2 * R.U[dtype]
+    tol = h.abs() * ((2 * g.abs().clamp(max=200) + 12) * R.V + of_t * 1.01) + 2 * unit
+    got = y.double().cpu() / scale
+    assert torch.isfinite(got).all()
+    within(got[:, :inner], h.expand(tokens, -1), (tol + 2 * unit / scale).expand(tokens, -1))
 
 
 # -------------------------------------------------------------------------------------------- unequal features --
