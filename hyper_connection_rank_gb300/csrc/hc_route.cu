@@ -141,18 +141,20 @@ template <typename F> __device__ __forceinline__ void join_best(const RouteArgs&
   }
 }
 
-// Whether this lane's group stays, by the two largest of its values in arithmetic F. `sure` becomes false if fp32 values that
-// are each off by `error` cannot tell.
+// Whether this lane's group stays, by the two largest of its values in arithmetic F. `sure` becomes false if fp32 values cannot tell
+// that are sums of a score, off by `error`, and a bias, rounded at the size of each: two of them that cancel leave a group's value
+// with an error that its own size does not show. So a group's bounds are its value and `best` errors more or less, and 4 u of
+// |a1| + |a2| (u of each, u of their sum, and u for the bounds).
 template <typename F>
 __device__ __forceinline__ bool keep_group(const RouteArgs& a, F a1, F a2, int group, float error, bool* sure) {
   using Key = typename Num<F>::Key;
   const bool in = group < a.groups;
   F value = a.best == 2 && a.each > 1 ? a1 + a2 : a1;
   if (value != value) value = -INFINITY;
-  Key k = in ? key_of(value) : Key(0), last = 0;
+  Key k = in ? key_of(value) : Key(0);
   bool kept = false;
   for (int i = 0; i < a.top_groups; ++i) {
-    last = warp_max(k);
+    const Key last = warp_max(k);
     const int g = __reduce_min_sync(kFull, k == last ? static_cast<unsigned>(group) : 64u);
     if (group == g) {
       kept = in;
@@ -160,8 +162,14 @@ __device__ __forceinline__ bool keep_group(const RouteArgs& a, F a1, F a2, int g
     }
   }
   if constexpr (sizeof(F) == 4) {
-    const float x = value_of(last), y = value_of(warp_max(k));
-    *sure = error == 0.0f || y == -INFINITY || x - y > 2 * a.best * error + 4 * kU * (fabsf(x) + fabsf(y));
+    const float size = value == -INFINITY ? 0.0f : a.best == 2 && a.each > 1 ? fabsf(a1) + fabsf(a2) : fabsf(a1);
+    const float reach = a.best * error + 4 * kU * size;
+    const bool bounded = reach < INFINITY;
+    float out = !in || kept ? -INFINITY : bounded ? value + reach : INFINITY;  // the upper bound of those that go
+    float stay = !(in && kept) ? -INFINITY : bounded ? reach - value : INFINITY;  // minus the lower one of those that stay
+    asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(out));
+    asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(stay));
+    *sure = error == 0.0f || out == -INFINITY || -stay > out;
   }
   return kept;
 }

@@ -1,9 +1,11 @@
 """The experts' layer and routing at the ends of their types' ranges. Bounds: _experts_ref.py, or derived here."""
+import math
+
 import pytest
 import torch
 
 import _experts_ref as R
-from test_experts_gpu import BF16, F16, F32, hc, ids, layer, on_gpu, within  # noqa: F401
+from test_experts_gpu import BF16, F16, F32, hc, ids, layer, on_gpu, route_check, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +65,30 @@ def test_small_features_beside_large_ones(hc, tokens, factor, dtype):  # noqa: F
     y = hc.expert_mlp(*on_gpu((x, gate, up, down, e, w)))
     want, tol = R.experts(x, gate, up, down, e, w, stored=False)
     within(y, want, tol)
+
+
+# -------------------------------------------------------------------------------------------------- routing --
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,each", [(2, 2), (8, 4), (3, 7)])
+@pytest.mark.parametrize("large", [30.0, 100.0, 1000.0, 1e5])
+def test_biases_that_cancel(hc, large, groups, each, scoring):  # noqa: F811
+    """A group's two best values are a large one and its negative but for little: their sum keeps only what float32 has at the
+    large one's size, and the groups are closer than that. (float64 orders them as the real numbers do down to some 1e-16 of the
+    large one, a hundredth of the smallest steps here.)"""
+    g = torch.Generator().manual_seed(62)
+    n, step = 300, large * 2.0 ** -26
+    at = torch.randint(-30, 31, (n, groups, each), generator=g)
+    # (the two that count are the first two; their places add up to another number in every group)
+    at[:, :, 1] = torch.rand(n, 60, generator=g).argsort(1)[:, :groups] - 30 - at[:, :, 0]
+    x = torch.rand(n, 1, 1, generator=g) * 0.5 + at * step
+    bias = torch.full((groups, each), -4 * large)
+    bias[:, 0], bias[:, 1] = large, -large
+    for top in (1, groups - 1):
+        route_check(hc, x.reshape(n, -1).contiguous(), 2, bias=bias.flatten(), scoring=scoring, groups=groups, top_groups=top,
+                    group_best=2)
+        closed = bias.clone()
+        for value in (-1e9, -math.inf):  # a group that only goes along where no other is left, and does not blur the others
+            closed[1] = value
+            route_check(hc, x.reshape(n, -1).contiguous(), 2, bias=closed.flatten(), scoring=scoring, groups=groups, top_groups=top,
+                        group_best=2)
