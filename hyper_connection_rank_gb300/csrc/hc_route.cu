@@ -5,7 +5,7 @@
 // over the warp of keys that have the value's upper bits and the index.
 //
 // Order: which of two values is the larger must not hang on a rounding. Without a bias the order is that of the logits
-// themselves, exactly. Otherwise values are formed in fp32 first; a comparison is trusted if the difference is larger than
+// themselves, exactly (but beside a logit of plus infinity all others of a softmax have the score 0). Otherwise values are formed in fp32 first; a comparison is trusted if the difference is larger than
 // both errors, which `score_error` bounds by the arithmetic below, and values that fp32 cannot tell apart (groups, neighbours
 // in the order, the last that is taken and the first that is not) are ordered by themselves in fp64, which runs at 1/64 of
 // fp32's rate here: doing all rows that way would cost ten times the rest.
@@ -180,9 +180,14 @@ __device__ __forceinline__ double exact_total(const RouteArgs& a, int64_t t, flo
   for (int e = threadIdx.x & 31; e < a.experts; e += 32) total += m == -INFINITY ? 0.0 : exp_below<double>(load_logit(a, t, e), m);
   return warp_total(total);
 }
+// What stands for a score where logits are compared: the logit, but for the zeros beside an infinite one in a softmax.
+__device__ __forceinline__ float order_logit(const RouteArgs& a, float x, float m) {
+  return !a.sigmoid && m == INFINITY && x != INFINITY ? 0.0f : x;
+}
 // What is compared, in fp64 (with the logits in place of scores where that is the same order).
 __device__ __forceinline__ double exact_value(const RouteArgs& a, int64_t t, int e, float m, double total, bool logits) {
-  double v = load_logit(a, t, e);
+  const float x = load_logit(a, t, e);
+  double v = logits ? order_logit(a, x, m) : x;
   if (!logits) v = a.sigmoid ? sigmoid_of<double>(v) : m == -INFINITY ? 0.0 : exp_below<double>(v, m) / total;
   if (a.bias != nullptr) v += static_cast<double>(a.bias[e]);
   return v != v ? -INFINITY : v;
@@ -294,7 +299,10 @@ template <int VPL> __device__ __forceinline__ void choose(const RouteArgs& a, in
       for (int i = 0; i < VPL; ++i) s[i] *= r;
     }
   }
-  if (!by_logit) {
+  if (by_logit) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = order_logit(a, v[i], m);
+  } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) v[i] = i < count ? fmaxf(s[i] + a.bias[first + i * a.lanes], -INFINITY) : -INFINITY;
   }

@@ -43,7 +43,9 @@ extern "C" {
  * A NaN among the logits counts as minus infinity, a NaN among the biases as
  * a bias of minus infinity. An expert whose logit is minus infinity has the
  * score 0; a token without any other logit has scores of 0, and weights of 0.
- * Logits of plus infinity share a softmax among them. live: the rows from
+ * Logits of plus infinity share a softmax among them, and all others have the
+ * score 0. Where a bias is given or two values of a group count, scores below
+ * 1e-300 are 0. live: the rows from
  * live[0] on are no token's: they get experts of -1 and weights of 0 (NULL: all
  * rows are tokens'). Limits: experts <= 1024, groups <= 32, top_k <= 32. */
 typedef struct {

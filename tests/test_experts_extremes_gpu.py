@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import _experts_ref as R
-from test_experts_gpu import BF16, F16, F32, hc, ids, layer, on_gpu, route_check, within  # noqa: F401
+from test_experts_gpu import BF16, F16, F32, hc, ids, layer, on_gpu, rnd, route_check, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,30 @@ def test_biases_that_cancel(hc, large, groups, each, scoring):  # noqa: F811
             closed[1] = value
             route_check(hc, x.reshape(n, -1).contiguous(), 2, bias=closed.flatten(), scoring=scoring, groups=groups, top_groups=top,
                         group_best=2)
+
+
+def test_infinite_logits_leave_equal_scores(hc):  # noqa: F811
+    """Beside a logit of plus infinity all others have the score 0 of a softmax: equal, so in the order of their index, whether a
+    bias of zeros or none is given."""
+    x = rnd(63, 6, 24)
+    x[0, 0] = math.inf
+    x[1, [3, 17]] = math.inf
+    x[2, 5], x[2, 9], x[2, 2] = math.inf, -math.inf, math.nan
+    x[3, 23], x[3, :6] = math.inf, -math.inf
+    x[4, :] = math.inf
+    for dtype in (F32, F16, BF16):
+        r = x.to(dtype)
+        for k in (1, 3, 24):
+            for bias in (None, torch.zeros(24).cuda()):
+                e, w = hc.expert_route(r.cuda(), k, bias=bias)
+                for t in range(5):
+                    high = (r[t] == math.inf).nonzero().flatten().tolist()
+                    order = high + [i for i in range(24) if i not in high]
+                    assert e[t].tolist() == order[:k], (dtype, k, t)
+                    share = torch.tensor([1.0 / min(k, len(high)) if i in high else 0.0 for i in order[:k]])
+                    assert torch.equal(w[t].cpu(), share)
+        # groups of four: those with an infinite logit by their number of them, the others equal
+        for best in (1, 2):
+            for bias in (None, torch.zeros(24).cuda()):
+                e, _ = hc.expert_route(r[1:2].cuda(), 12, bias=bias, groups=6, top_groups=3, group_best=best)
+                assert e[0].tolist() == [3, 17] + [i for i in (*range(8), *range(16, 20)) if i not in (3, 17)]
