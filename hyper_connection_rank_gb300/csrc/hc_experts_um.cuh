@@ -67,11 +67,13 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 // Ordinary writes into shared memory (cp.async's among them) that this thread knows of, before the tensor core reads them.
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// silu(g) u. The approximate exponential and quotient and the products are within (1.25 |g| + 12) 2^-24 of it for g < 0 (the
-// argument's rounding counts), within 2^-20 above; from |g| = 174 on e is subnormal and keeps fewer digits.
+// silu(g) u. The approximate exponential and reciprocal and the products are within (1.5 |g| + 16) 2^-24 of it for g < 0 (the
+// argument's rounding counts), within 2^-20 above; from g = -174 on, where it is below 2^-251 u, it is 0.
 __device__ __forceinline__ float gated(float g, float u) {
-  const float e = __expf(-0.5f * fabsf(g));
-  return silu_times(g, u, e, __fdividef(1.0f, fmaf(e, e, 1.0f)));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(g) * -0.72134752f));  // e^(-|g| / 2)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, e, 1.0f)));
+  return silu_times(g, u, e, r);
 }
 
 // A finite value too large for T becomes its largest one: h of fp16 can pass 65504 where its products with down do not.
