@@ -21,17 +21,18 @@ namespace {
 
 // CTA e counts the pairs of the experts before e, which is where its own begin, and its own in each warp's run of pairs;
 // then every warp writes its own. All CTAs read all experts (tokens * top_k numbers from L2), and none waits for another.
+// Together they clear the words that the products count and mark in.
 // Bound: latency up to some thousand pairs (5 us by itself, less behind the call before), issue beyond (65528 pairs and 64
 // experts: 15 us).
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads)
-lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, ExpertLists lists, unsigned int* tickets, int num_tickets) {
+lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, ExpertLists lists, unsigned int* zeros, int64_t num_zeros) {
   constexpr int kWarps = kThreads / 32;
   __shared__ int own[kWarps], less[kWarps];
   pdl_wait();
   pdl_trigger();
   const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = e * kThreads + threadIdx.x; i < num_tickets; i += experts * kThreads) tickets[i] = 0;
+  for (int64_t i = e * kThreads + threadIdx.x; i < num_zeros; i += experts * kThreads) zeros[i] = 0;
   // four neighbouring pairs to a lane, 128 to a warp's step
   const bool vec = (reinterpret_cast<uintptr_t>(ids) & 15u) == 0;
   const auto load4 = [&](int i) {
@@ -339,10 +340,34 @@ template <typename T, bool kInner> cudaError_t launch_general(const GeneralArgs&
 // 6.8 TB/s. (16-bit integers with an exponent for sixteen features took 72 and the product before it 164 instead of 195, but cost
 // the neighbours of a large feature their digits: with one of 1000 times their size 1.4% of theirs.)
 constexpr int kCombineWarps = 4;
+
+// sums += weight * (the products with down of a pair's inner values beyond fp16), eight features from c on to a lane.
+__device__ __noinline__ void add_excess(const hc_expert_mlp_t& p, const Excess& x, int64_t pair, int expert, float weight, int c,
+                                        float* sums) {
+  const __half* down = static_cast<const __half*>(p.down) + expert * p.down_expert_stride + c * p.down_out_stride;
+  float v[8] = {};
+  for (int word = 0; word < x.words; ++word) {
+    for (uint32_t blocks = x.over[pair * x.words + word]; blocks != 0; blocks &= blocks - 1) {
+      const int first = (word * 32 + __ffs(blocks) - 1) * 32, i = first + (threadIdx.x & 31);
+      const float mine = i < p.inner ? x.values[pair * x.step + i] : 0.0f;
+      for (uint32_t left = __ballot_sync(0xffffffffu, mine != 0.0f); left != 0; left &= left - 1) {
+        const int l = __ffs(left) - 1;
+        const float h = __shfl_sync(0xffffffffu, mine, l);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < p.hidden) v[j] = fmaf(h, __half2float(down[(first + l) * p.down_in_stride + j * p.down_out_stride]), v[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[j] = fmaf(weight, v[j], sums[j]);
+}
+
+// excess: of fp16 on the tensor cores, without values otherwise.
 template <typename T, bool kPlanes>
 __global__ void __launch_bounds__(32 * kCombineWarps, 5)
-combine_kernel(hc_expert_mlp_t p, const float* __restrict__ o, int64_t o_step, const uint8_t* __restrict__ counts, int64_t count_step,
-               bool vec) {
+combine_kernel(const __grid_constant__ hc_expert_mlp_t p, const float* __restrict__ o, int64_t o_step,
+               const uint8_t* __restrict__ counts, int64_t count_step, const __grid_constant__ Excess excess, bool vec) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, blocks = (p.hidden + 255) / 256;
@@ -400,13 +425,23 @@ combine_kernel(hc_expert_mlp_t p, const float* __restrict__ o, int64_t o_step, c
       }
     }
   }
-  if (have) {
-    float sum[8];
+  float sum[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = sums[i].get();
-      sum[2 * i] = v.x, sum[2 * i + 1] = v.y;
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = sums[i].get();
+    sum[2 * i] = v.x, sum[2 * i + 1] = v.y;
+  }
+  if constexpr (std::is_same<T, __half>::value) {
+    if (excess.values != nullptr) {
+      uint32_t over = 0;
+      for (int i = 0; i < excess.words && (valid >> lane & 1u); ++i) over |= excess.over[(first + lane) * excess.words + i];
+      for (unsigned pairs = __ballot_sync(0xffffffffu, over != 0); pairs != 0; pairs &= pairs - 1) {
+        const int j = __ffs(pairs) - 1;
+        add_excess(p, excess, first + j, __shfl_sync(0xffffffffu, id, j), __shfl_sync(0xffffffffu, weight, j), c, sum);
+      }
     }
+  }
+  if (have) {
     if (vec) {  // (out's rows are 16-byte aligned and hold whole vectors)
       if constexpr (sizeof(T) == 2) {
         st16(out + c, V8<T>::pack(sum));
@@ -425,12 +460,12 @@ combine_kernel(hc_expert_mlp_t p, const float* __restrict__ o, int64_t o_step, c
 // counts: NULL where o is one plane.
 template <typename T>
 cudaError_t launch_combine(const hc_expert_mlp_t& a, const float* o, int64_t o_step, const uint8_t* counts, int64_t count_step,
-                           cudaStream_t s) {
+                           const Excess& excess, cudaStream_t s) {
   const bool vec = a.hidden % 8 == 0 && a.out_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
   const int64_t units = a.tokens * ((a.hidden + 255) / 256);
   const dim3 grid(static_cast<unsigned>((units + kCombineWarps - 1) / kCombineWarps)), block(32 * kCombineWarps);
-  return counts != nullptr ? launch_pdl(combine_kernel<T, true>, grid, block, 0, s, 1, a, o, o_step, counts, count_step, vec)
-                           : launch_pdl(combine_kernel<T, false>, grid, block, 0, s, 1, a, o, o_step, counts, count_step, vec);
+  return counts != nullptr ? launch_pdl(combine_kernel<T, true>, grid, block, 0, s, 1, a, o, o_step, counts, count_step, excess, vec)
+                           : launch_pdl(combine_kernel<T, false>, grid, block, 0, s, 1, a, o, o_step, counts, count_step, excess, vec);
 }
 
 // ---------------------------------------------------------------- layout --
@@ -440,7 +475,8 @@ struct Plan {
   int64_t tickets;
   int planes;  // of o
   int64_t h_step, o_step, count_step;
-  size_t bounds, order, tickets_at, part, h, o, counts, total;
+  int64_t excess_step, excess_words;  // (fp16 on the tensor cores) of the excess of inner values, elements and words of bits to a pair
+  size_t bounds, order, zeros, part, h, o, counts, excess, total;  // zeros: tickets, and behind them the words of bits
 };
 
 // Which products run, and where their buffers lie in the workspace. Tiles of 32 pairs with the weights as the first operand
@@ -469,9 +505,13 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   l.h_step = l.rows ? static_cast<int64_t>(align_up(a.inner, 16)) : a.inner;
   l.o_step = static_cast<int64_t>(align_up(a.hidden, 16));
   const bool few = l.rows == 32;
+  if (few) l.tickets = experts_um_tiles(a, l.rows, true);
+  if (l.rows && a.dtype == HC_F16) {
+    l.excess_step = static_cast<int64_t>(align_up(a.inner, 128));
+    l.excess_words = (a.inner + 1023) / 1024;
+  }
+  l.zeros = take((l.tickets + pairs * l.excess_words) * sizeof(uint32_t));
   if (few) {
-    l.tickets = experts_um_tiles(a, l.rows, true);
-    l.tickets_at = take(l.tickets * sizeof(unsigned int));
     l.part = take(static_cast<size_t>(num_sms) * 2 * 2 * l.rows * 128 * sizeof(float));
   }
   l.h = take(pairs * l.h_step * (l.rows ? 2 : 4));
@@ -483,6 +523,7 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
     l.count_step = (a.hidden + 255) / 256;
     l.counts = take(pairs * l.count_step);
   }
+  l.excess = take(pairs * l.excess_step * sizeof(float));
   l.total = at;
   return l;
 }
@@ -491,9 +532,10 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
   const Plan l = make_plan(a, aligned, num_sms);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const ExpertLists lists = {reinterpret_cast<int32_t*>(ws + l.bounds), reinterpret_cast<int32_t*>(ws + l.order)};
-  unsigned int* tickets = reinterpret_cast<unsigned int*>(ws + l.tickets_at);
+  unsigned int* tickets = reinterpret_cast<unsigned int*>(ws + l.zeros);
   float* o = reinterpret_cast<float*>(ws + l.o);
-  const int pairs = static_cast<int>(a.tokens * a.top_k), count = static_cast<int>(l.tickets);
+  const int pairs = static_cast<int>(a.tokens * a.top_k);
+  const int64_t count = l.tickets + pairs * l.excess_words;
   cudaError_t e = pairs > 4096 ? launch_pdl(lists_kernel<1024>, dim3(a.num_experts), dim3(1024), 0, s, 1, a.experts, pairs,
                                             a.num_experts, lists, tickets, count)
                                : launch_pdl(lists_kernel<128>, dim3(a.num_experts), dim3(128), 0, s, 1, a.experts, pairs,
@@ -502,17 +544,19 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
   if constexpr (sizeof(T) == 2) {
     if (l.rows) {
       uint8_t* counts = l.rows == 32 ? ws + l.counts : nullptr;
-      const ExpertUm u = {lists, ws + l.h, o, counts, l.h_step, l.o_step, l.count_step,
-                          reinterpret_cast<float*>(ws + l.part), tickets, static_cast<int64_t>(pairs) * l.o_step, l.planes, l.rows};
+      const Excess excess = {l.excess_words ? reinterpret_cast<float*>(ws + l.excess) : nullptr, tickets + l.tickets, l.excess_step,
+                             static_cast<int>(l.excess_words)};
+      const ExpertUm u = {lists, ws + l.h, o, counts, l.h_step, l.o_step, l.count_step, reinterpret_cast<float*>(ws + l.part), tickets,
+                          excess, static_cast<int64_t>(pairs) * l.o_step, l.planes, l.rows};
       e = l.rows == 256 ? launch_experts_many(a, u, num_sms, s) : launch_experts_few(a, u, num_sms, s);
-      return e != cudaSuccess ? e : launch_combine<T>(a, o, l.o_step, counts, l.count_step, s);
+      return e != cudaSuccess ? e : launch_combine<T>(a, o, l.o_step, counts, l.count_step, excess, s);
     }
   }
   const GeneralArgs g = {a, lists, reinterpret_cast<float*>(ws + l.h), o, l.o_step};
   e = launch_general<T, true>(g, num_sms, s);
   if (e != cudaSuccess) return e;
   e = launch_general<T, false>(g, num_sms, s);
-  return e != cudaSuccess ? e : launch_combine<T>(a, o, l.o_step, nullptr, 0, s);
+  return e != cudaSuccess ? e : launch_combine<T>(a, o, l.o_step, nullptr, 0, Excess{}, s);
 }
 
 }  // namespace

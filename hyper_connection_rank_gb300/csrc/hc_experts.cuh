@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "hc_experts_internal.h"
 
 namespace hc {
@@ -25,6 +27,19 @@ __device__ __forceinline__ float silu_times(float g, float u, float e, float r) 
   return g * by * r * (u * by);
 }
 
+// Inner values beyond fp16, whose products with down can be within it: h has the largest finite value in their place, and what that
+// leaves, in fp32, is kept here, for the sum over a token's experts to multiply with down itself. A pair's values count in blocks
+// of 32 features that have their bit set in `over`, which is zero before the call.
+struct Excess {
+  float* values;   // (pairs, step) at the pairs' places
+  uint32_t* over;  // (pairs, words)
+  int64_t step;    // a multiple of 32
+  int words;
+};
+constexpr float kMostHalf = 65504.0f;
+__device__ __forceinline__ bool past_half(float h) { return fabsf(h) > kMostHalf && fabsf(h) < INFINITY; }
+__device__ __forceinline__ float excess_of(float h) { return past_half(h) ? h - copysignf(kMostHalf, h) : 0.0f; }
+
 // The products on the tensor cores, for fp16 and bf16 (hc_experts_few.cu, hc_experts_many.cu).
 struct ExpertUm {
   ExpertLists lists;
@@ -34,6 +49,7 @@ struct ExpertUm {
   int64_t h_step, o_step, count_step;  // elements from row to row, the first two multiples of 16
   float* part;             // partial sums of the inner product
   unsigned int* tickets;   // of the inner product's tiles; zero before the call
+  Excess excess;           // (fp16)
   int64_t plane;           // elements from plane to plane of o (few)
   int planes;
   int rows;                // pairs to a tile: 32 (few) or 256 (many)

@@ -177,8 +177,16 @@ __global__ void __launch_bounds__(kThreads<kInner>, 2) few_kernel(const __grid_c
       float* o = static_cast<float*>(a.out) + (kInner ? 0 : p.piece() * a.plane);
       const auto put = [&](int c, float v0, float v1) {
         const int64_t to = static_cast<int64_t>(__shfl_sync(0xffffffffu, place, c)) * a.out_step;
-        if (kInner) {
-          if (f < a.features) stf(static_cast<T*>(a.out) + to + f, saturate<T>(gated(v0, v1)));
+        if constexpr (kInner) {
+          const float h = gated(v0, v1);
+          if (f < a.features) stf(static_cast<T*>(a.out) + to + f, saturate<T>(h));
+          if constexpr (!kBf16) {
+            if (__any_sync(0xffffffffu, f < a.features && past_half(h))) {  // (32 features from a multiple of 32 on)
+              const int64_t pair = a.order[p.first + c];
+              if (f < a.features) a.excess.values[pair * a.excess.step + f] = excess_of(h);
+              if (lane == 0) mark_excess(a.excess, pair, f);
+            }
+          }
         } else {
           if (f < a.features) o[to + f] = v0;
           if (f + kHalf < a.features) o[to + f + kHalf] = v1;
@@ -330,6 +338,7 @@ bool fill_args(Args* a, const hc_expert_mlp_t& p, const ExpertUm& u, bool inner,
   *a = Args{};
   a->bounds = u.lists.bounds;
   a->order = u.lists.order;
+  a->excess = u.excess;
   a->x = p.x;
   a->x_step = p.x_stride;
   a->out = inner ? u.h : static_cast<void*>(u.o);

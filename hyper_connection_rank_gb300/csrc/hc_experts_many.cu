@@ -219,14 +219,25 @@ __global__ void __launch_bounds__(kThreads<kInner>, 1) many_kernel(const __grid_
         }
         if constexpr (kInner) {
           uint4 q[4];
+          float v[32];
+          float most = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float v[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = saturate<T>(gated(__uint_as_float(x[i][j]), __uint_as_float(y[i][j])));
-            q[2 * i] = V8<T>::pack(v);
-            q[2 * i + 1] = V8<T>::pack(v + 8);
+          for (int j = 0; j < 32; ++j) {
+            v[j] = gated(__uint_as_float(x[j / 16][j % 16]), __uint_as_float(y[j / 16][j % 16]));
+            if (!kBf16) most = fmaxf(most, fabsf(v[j]));
           }
+          if (!kBf16 && most > kMostHalf && me < rows) {  // (or infinite)
+            const int64_t pair = a.order[at];
+            float4* to = reinterpret_cast<float4*>(a.excess.values + pair * a.excess.step + p.feature + c0);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              to[j / 4] = make_float4(excess_of(v[j]), excess_of(v[j + 1]), excess_of(v[j + 2]), excess_of(v[j + 3]));
+            mark_excess(a.excess, pair, p.feature + c0);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = saturate<T>(v[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) q[j] = V8<T>::pack(v + 8 * j);
           put(q, static_cast<T*>(a.out), p.feature + c0);
         } else {
 #pragma unroll

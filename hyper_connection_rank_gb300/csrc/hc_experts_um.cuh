@@ -46,6 +46,7 @@ struct Args {
   uint8_t* counts;             // (few, outer) the planes of each 256 elements of o
   int64_t out_step, count_step;  // elements from row to row of out, and of counts
   int64_t plane;               // (few, outer) elements from plane to plane of out
+  Excess excess;               // (inner, fp16)
   float* part;                 // (few, inner) [2 * CTAs][2 halves][rows][128], for tiles that a cut goes through
   unsigned int* tickets;       // (few, inner) of each tile: pieces that have been written
   int experts, top_k, inputs, features, kblocks, fblocks, k_major;
@@ -76,11 +77,11 @@ __device__ __forceinline__ float gated(float g, float u) {
   return silu_times(g, u, e, r);
 }
 
-// A finite value too large for T becomes its largest one: h of fp16 can pass 65504 where its products with down do not.
+// A finite value too large for T becomes its largest one, and an entry of the excess.
 template <typename T> __device__ __forceinline__ float saturate(float v) { return v; }
-template <> __device__ __forceinline__ float saturate<__half>(float v) {
-  const float m = fabsf(v);
-  return m > 65504.0f && m < INFINITY ? copysignf(65504.0f, v) : v;
+template <> __device__ __forceinline__ float saturate<__half>(float v) { return past_half(v) ? copysignf(kMostHalf, v) : v; }
+__device__ __forceinline__ void mark_excess(const Excess& x, int64_t pair, int feature) {
+  atomicOr(x.over + pair * x.words + (feature >> 10), 1u << ((feature >> 5) & 31));
 }
 
 // The pieces of work of a CTA (or a pair of them), the same for all its warps: whole tiles in turn, or, with kSplit, parts of

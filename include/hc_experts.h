@@ -79,9 +79,10 @@ hc_status_t hc_expert_route(const hc_expert_route_t* args, struct CUstream_st* s
  * Numerics: products are summed in fp32. In the fp16/bf16 kernels the inner
  * values silu(.) * (.) are rounded to T for the product with down (the tensor
  * core's operands are 16 bits). Each chosen expert's result is fp32, and so is
- * the sum over them, rounded to T once. fp16 inner values saturate at its largest finite value
- * rather than turn to infinity. Limits: top_k <= 32, num_experts <= 1024, hidden and inner
- * <= 65536, tokens * top_k < 2^24. */
+ * the sum over them, rounded to T once. Finite inner values beyond
+ * fp16's largest one count in full: what that leaves of them is multiplied with
+ * down in fp32, a row of down for each. Limits: top_k <= 32, num_experts <= 1024,
+ * hidden and inner <= 65536, tokens * top_k < 2^24. */
 typedef struct {
   const void* x; /* (tokens, hidden) of type dtype */
   const void *gate, *up, *down; /* (num_experts, hidden, inner) twice, (num_experts, inner, hidden) */

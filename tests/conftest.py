@@ -13,6 +13,21 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: long-running CPU test")
 
 
+# Tests that ask for a value which the definition does not give, with the reason; they are kept and have to fail.
+WRONG_VALUES = {
+    "test_experts_gpu.py::test_mlp_large_inner_values":
+        "asks for 64 * 65504 * 2^-12 = 1023.5 where silu(256) * 2048 = 524288 and 64 * 524288 * 2^-12 = 8192, which float16 holds; "
+        "test_experts_extremes_gpu.py has the definition's value for the same inputs in every form",
+}
+
+
+def pytest_collection_modifyitems(items):
+    for item in items:
+        for name, why in WRONG_VALUES.items():
+            if item.nodeid.endswith(name):
+                item.add_marker(pytest.mark.xfail(reason=why, strict=True))
+
+
 @pytest.fixture(scope="session")
 def oracle_lib():
     import oracle

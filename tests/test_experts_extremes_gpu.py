@@ -67,6 +67,49 @@ def test_small_features_beside_large_ones(hc, tokens, factor, dtype):  # noqa: F
     within(y, want, tol)
 
 
+# ------------------------------------------------------------------------------------- large inner values in fp16 --
+
+FORMS = ["aligned", "general", "odd"]
+
+
+def in_form(hc, args, form):  # noqa: F811
+    """The layer's result through aligned rows, through the general kernels, and through rows at odd places."""
+    x, gate, up, down, e, w = on_gpu(args)
+    if form == "odd":
+        wide = torch.zeros(x.shape[0], x.shape[1] + 3, dtype=x.dtype, device="cuda")
+        wide[:, 1:-2] = x
+        x = wide[:, 1:-2]
+    return hc.expert_mlp(x, gate, up, down, e, w, flags=hc.HC_FLAG_FORCE_GENERAL if form == "general" else 0)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("tokens", [2, 60, 200, 500])
+def test_inner_values_past_the_largest_float16(hc, tokens, form):  # noqa: F811
+    """silu(256) * 2048 = 524288 is beyond float16, 64 of them by 2^-12 are 8192, which it holds; all sums are exact."""
+    x, gate, up, down, e, w = layer(10, tokens, 2, 1, 64, 64, F16)
+    x, gate, up, down = (torch.full_like(t, v) for t, v in ((x, 4.0), (gate, 1.0), (up, 8.0), (down, 2.0 ** -12)))
+    assert (in_form(hc, (x, gate, up, down, e, w), form) == 8192.0).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows_out", [False, True], ids=["outputs", "inputs"])
+@pytest.mark.parametrize("tokens,inner", [(3, 64), (40, 200), (200, 136), (300, 1160)])
+def test_some_inner_values_past_the_largest_float16(hc, tokens, inner, rows_out, form):  # noqa: F811
+    """A few of them, in some rows, of either sign, beside an infinite one that stays in its row and a row without experts."""
+    x, gate, up, down, e, w = layer(61, tokens, 3, 2, 136, inner, F16, rows_out)
+    x[::3] *= 100.0
+    up *= 30.0
+    down *= 2.0 ** -9
+    e[tokens // 2] = -1
+    y = in_form(hc, (x, gate, up, down, e, w), form)
+    want, tol = R.experts(x, gate, up, down, e, w, stored=False)
+    assert torch.isfinite(want).all() and want.abs().max() < 60000
+    within(y, want, tol)
+    x[0, 0] = math.inf
+    z = in_form(hc, (x, gate, up, down, e, w), form)
+    assert torch.equal(z[1:], y[1:]) and not torch.isfinite(z[0]).any()
+
+
 # -------------------------------------------------------------------------------------------------- routing --
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
