@@ -140,13 +140,14 @@ def _sized(device, f, *args):
 def _on_stream(stream, f, *args, out=None, workspace=None, **kw):
     """f's call with another stream as the current one, so that what it allocates comes from that stream's memory: a block that
     was freed on this stream may still be in use by kernels queued here. Results are the caller's, who may free them on this
-    stream; memory that the caller gave is not handed out again before the other stream is done with it."""
+    stream; memory that the caller gave, inputs among it (another call's results may have no other reference), is not handed out
+    again before the other stream is done with it."""
     if stream.device.index != args[0].get_device():
         raise ValueError("the stream and the tensors are on different devices")
-    for name, t in (("out", out), ("workspace", workspace)):
-        if t is not None:
+    kw.update((name, t) for name, t in (("out", out), ("workspace", workspace)) if t is not None)
+    for t in (*args, *kw.values()):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
             t.record_stream(stream)
-            kw[name] = t
     here = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
         got = f(*args, **kw)
