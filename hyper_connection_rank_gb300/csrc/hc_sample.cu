@@ -828,8 +828,9 @@ struct Weigh {
   __device__ __forceinline__ int exponent(float x) const {
     return __float_as_int(__fadd_rn(__fmul_rn(x, ch), kMagic)) >> 4;
   }
-  // sum += units of two logits' weights, the chunk's n being `top`. (Of minus infinity and of logits far below, kf is so far
-  // from kMagic that nothing is left by the shift to the right, of NaN nothing by the one to the left.)
+  // sum += units of two logits' weights, the chunk's n being `top`, that of a number or of minus infinity. (Of minus infinity and of
+  // logits far below, kf is so far from kMagic that nothing is left by the shift to the right, of NaN nothing by the one to the
+  // left; in a chunk of nothing else the sum says nothing, and its n lets nothing of it count.)
   __device__ __forceinline__ void add_units(float x0, float x1, int top, u64* sum) const {
     const Two x(x0, x1), c(ch);
     // all of n, k and f with the other sign: n = -x c, f = -(x c - k / 16), exact and at most 1/32
@@ -920,7 +921,7 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, kStreamC
 #pragma unroll
     for (int i = 1; i < kPerLane; ++i) top = fmaxf(top, x[i]);
     asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(top));
-    return top;
+    return fmaxf(top, -INFINITY);  // (of nothing but NaN, too)
   };
   float most = -INFINITY;  // of the chunks that this warp has seen
   const auto inside = [&](int k) { return k * kChunk >= shift && (k + 1) * kChunk - shift <= a.vocab; };
@@ -977,7 +978,8 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, kStreamC
   most = value_of(static_cast<uint32_t>(highest));
   if (!(fabsf(most) * weigh.ch <= 512.0f)) return;
   const int top = weigh.exponent(most);
-  const auto down = [&](u64 v, int n) -> u64 { return top - n < 64 ? v >> (top - n) : 0; };
+  // (n is at most top, and far below it in a chunk without any logit above minus infinity)
+  const auto down = [&](u64 v, int n) -> u64 { return static_cast<unsigned>(top - n) < 64 ? v >> (top - n) : 0; };
   constexpr int kEach = (kMaxChunks + kStreamThreads - 1) / kStreamThreads;
   u64 v[kEach], sum = 0;
 #pragma unroll
