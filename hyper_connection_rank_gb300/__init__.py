@@ -16,14 +16,14 @@ The other layer between two blocks is a feed-forward layer of experts
 """
 from ._binding import (HC_FLAG_FORCE_GENERAL, HC_FLAG_WEIGHTS_STATIC, HC_PATH_DECODE, HC_PATH_GENERAL,
                        HC_PATH_NONE, HC_PATH_PREFILL, PATH_NAMES, HcError, attrs_default, debug_sigmoid_exact,
-                       debug_sigmoid_table, debug_sigmoid_table_f16, debug_wait_timeout, debug_wait_timeouts, engram_gate, inv_rms, load_library, lowrank_mix, path,
+                       debug_sigmoid_table, debug_sigmoid_table_f16, debug_wait_timeout, debug_wait_timeouts, debug_wait_together, engram_gate, inv_rms, load_library, lowrank_mix, path,
                        workspace_size)
 from ._experts import expert_mlp, expert_mlp_workspace_size, expert_route, token_sample
 from ._paged import (page_compact, page_copy, page_extend, page_fork, page_release, paged_attention,
                      paged_attention_workspace_size, rotary, rotary_append, rotary_frequencies)
 
 __all__ = ["lowrank_mix", "inv_rms", "engram_gate", "path", "workspace_size", "attrs_default", "load_library", "debug_wait_timeouts",
-           "debug_wait_timeout", "debug_sigmoid_exact", "debug_sigmoid_table_f16", "debug_sigmoid_table",
+           "debug_wait_timeout", "debug_wait_together", "debug_sigmoid_exact", "debug_sigmoid_table_f16", "debug_sigmoid_table",
            "HcError", "HC_FLAG_WEIGHTS_STATIC", "HC_FLAG_FORCE_GENERAL", "HC_PATH_NONE", "HC_PATH_DECODE",
            "HC_PATH_PREFILL", "HC_PATH_GENERAL", "PATH_NAMES", "rotary_frequencies", "rotary", "rotary_append",
            "paged_attention", "paged_attention_workspace_size", "page_copy", "page_fork", "page_extend", "page_release",

@@ -28,7 +28,7 @@ DTYPE_CODES = {torch.float32: HC_F32, torch.float16: HC_F16, torch.bfloat16: HC_
 # Every symbol the headers in include/ declare.
 EXPORTS = ("hc_attrs_default", "hc_lowrank_mix_path", "hc_lowrank_mix_workspace_size", "hc_lowrank_mix",
            "hc_status_string", "hc_last_error", "hc_debug_wait_timeouts", "hc_debug_sigmoid_exact",
-           "hc_debug_sigmoid_table", "hc_debug_sigmoid_table_f16", "hc_debug_sigmoid_table_f16_bytes", "hc_debug_wait_timeout", "hc_debug_phase_clocks", "hc_debug_sync_probe", "hc_lowrank_mix_decode_noalloc", "hc_inv_rms",
+           "hc_debug_sigmoid_table", "hc_debug_sigmoid_table_f16", "hc_debug_sigmoid_table_f16_bytes", "hc_debug_wait_timeout", "hc_debug_wait_together", "hc_debug_phase_clocks", "hc_debug_sync_probe", "hc_lowrank_mix_decode_noalloc", "hc_inv_rms",
            "hc_engram_gate", "hc_rotary", "hc_rotary_append", "hc_paged_attention", "hc_paged_attention_workspace_size",
            "hc_pages_workspace_size", "hc_page_copy", "hc_page_fork", "hc_page_extend", "hc_page_release",
            "hc_page_compact", "hc_expert_route", "hc_expert_mlp", "hc_expert_mlp_workspace_size", "hc_token_sample")
@@ -80,6 +80,8 @@ def load_library(path: str = LIB_PATH):
         L.hc_debug_sigmoid_table_f16.restype = ci
         L.hc_debug_wait_timeout.argtypes = [vp, ctypes.c_longlong, vp]
         L.hc_debug_wait_timeout.restype = ci
+        L.hc_debug_wait_together.argtypes = [vp, u32, ctypes.c_longlong, vp]
+        L.hc_debug_wait_together.restype = ci
         L.hc_debug_phase_clocks.argtypes = [vp, sz]
         L.hc_debug_phase_clocks.restype = sz
         L.hc_debug_sync_probe.argtypes = [ci, ci, ci, sz, vp, sz, vp]
@@ -212,6 +214,15 @@ def debug_wait_timeout(limit_cycles: int = 2_000_000, device="cuda"):
     out = torch.zeros(32, dtype=torch.float32, device=device)
     s = torch.cuda.current_stream(out.device)
     check(lib().hc_debug_wait_timeout(_ptr(out), int(limit_cycles), s.cuda_stream))
+    return out
+
+
+def debug_wait_together(stuck: int = 0, limit_cycles: int = 2_000_000, device="cuda"):
+    """Run the check of waits that end together (hc_debug_wait_together):
+    returns the 128 floats of its four warps, NaN in all if one gave up."""
+    out = torch.zeros(128, dtype=torch.float32, device=device)
+    s = torch.cuda.current_stream(out.device)
+    check(lib().hc_debug_wait_together(_ptr(out), int(stuck), int(limit_cycles), s.cuda_stream))
     return out
 
 

@@ -272,6 +272,16 @@ hc_status_t hc_debug_wait_timeout(float* out, long long limit_cycles, struct CUs
   return HC_OK;
 }
 
+hc_status_t hc_debug_wait_together(float* out, unsigned int stuck, long long limit_cycles, struct CUstream_st* stream) {
+  if (out == nullptr) return hc::set_error(HC_ERR_INVALID_ARG, "null output pointer");
+  if (stuck > 15u) return hc::set_error(HC_ERR_INVALID_ARG, "stuck must lie in [0, 15]");
+  if (limit_cycles < 1000 || limit_cycles > 4000000000LL)
+    return hc::set_error(HC_ERR_INVALID_ARG, "limit_cycles must lie in [1e3, 4e9]");
+  const cudaError_t e = hc::launch_wait_together_probe(out, stuck, limit_cycles, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return hc::set_error(HC_ERR_CUDA, cudaGetErrorString(e));
+  return HC_OK;
+}
+
 size_t hc_debug_sigmoid_table_f16_bytes(void) { return hc::sigmoid_table16_bytes(); }
 
 hc_status_t hc_debug_sigmoid_table_f16(float* g_out, void* table, size_t table_bytes, struct CUstream_st* stream) {

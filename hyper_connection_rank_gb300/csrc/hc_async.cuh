@@ -144,6 +144,23 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The same barrier, and whether `ok` is true for all of them. Warps that have to
+// go the same way after bounded waits of their own ask here: each comes, whether
+// its wait ended or gave up, so that none is left waiting for one that has gone.
+__device__ __forceinline__ bool named_bar_all(uint32_t id, uint32_t nthreads, bool ok) {
+  uint32_t all;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(nthreads), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return all != 0;
+}
+
 // Arrive at hardware barrier `id` (expecting `nthreads`) without waiting.
 __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

@@ -162,12 +162,18 @@ __global__ void __launch_bounds__(kThreads<kInner>, 2) few_kernel(const __grid_c
     const int quarter = warp & 3;  // of the lanes of tensor memory, which a warp's place decides
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int me = quarter * 32 + lane;
+    const auto meet = [] {  // (of the four warps)
+      __syncwarp();
+      named_bar_sync(1, 128);
+    };
     for (int acc = 0; ok && p.next(kStep); ++acc) {
       const int buf = acc & 1;
       const uint32_t d = tmem + buf * 2 * kRows + lanes;
       const int at = p.first + min(lane, p.rows - 1), place = kInner ? at : a.order[at];  // of the lane's pair, in out
       ok = mbar_wait(&b->acc_full[buf], (acc >> 1) & 1, &g_few_wait_timeouts);
-      ok = __all_sync(0xffffffffu, ok);
+      // The inner product's four warps meet below where a piece of a cut tile is joined, so there they go on as one; whole tiles
+      // come behind all of those, and a warp that leaves at one of them leaves nobody waiting.
+      ok = kInner && !p.whole() ? named_bar_all(1, 128, ok) : __all_sync(0xffffffffu, ok) != 0;
       if (!ok) break;
       tc_fence_after();
       // this thread has feature `me` of both halves, a column for each pair
@@ -222,9 +228,9 @@ __global__ void __launch_bounds__(kThreads<kInner>, 2) few_kernel(const __grid_c
         uint32_t c0, c1;
         p.sharers(&c0, &c1);
         __threadfence();
-        named_bar_sync(1, 128);
+        meet();
         if (warp == 2 && lane == 0) b->last = atomicAdd(&a.tickets[p.tile], 1u) == c1 - c0;
-        named_bar_sync(1, 128);
+        meet();
         if (b->last != 0) {
           __threadfence();
           // sums of kAt pairs from kOf CTAs' pieces at a time, so that their loads overlap
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(kThreads<kInner>, 2) few_kernel(const __grid_c
           if (p.rows <= 4) join(std::integral_constant<int, 4>(), std::integral_constant<int, 4>());
           else join(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
         }
-        named_bar_sync(1, 128);  // (`last` is read before it is written again)
+        meet();  // (`last` is read before it is written again)
       }
     }
   } else if constexpr (kInner) {
@@ -368,6 +374,27 @@ int64_t experts_um_tiles(const hc_expert_mlp_t& p, int rows, bool inner) {
 
 cudaError_t launch_experts_few(const hc_expert_mlp_t& p, const ExpertUm& u, int num_sms, cudaStream_t s) {
   return p.dtype == HC_F16 ? launch_both<__half>(p, u, num_sms, s) : launch_both<__nv_bfloat16>(p, u, num_sms, s);
+}
+
+// Four warps wait by themselves, those in `stuck` for an mbarrier that nothing arrives on, and go on as one.
+__global__ void __launch_bounds__(128) wait_together_probe(float* out, unsigned int stuck, long long limit) {
+  __shared__ uint64_t bars[2];
+  if (threadIdx.x == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) mbar_arrive(&bars[0]);
+  const bool ok = mbar_wait_limit(&bars[stuck >> (threadIdx.x >> 5) & 1u], 0, &g_few_wait_timeouts, limit);
+  const bool all = named_bar_all(1, 128, ok);
+  if (all) named_bar_sync(1, 128);
+  out[threadIdx.x] = all ? 1.0f : __int_as_float(0x7fc00000);
+}
+
+cudaError_t launch_wait_together_probe(float* out, unsigned int stuck, long long limit_cycles, cudaStream_t s) {
+  wait_together_probe<<<1, 128, 0, s>>>(out, stuck, limit_cycles);
+  return cudaGetLastError();
 }
 
 unsigned int read_experts_few_wait_timeouts(bool reset) {

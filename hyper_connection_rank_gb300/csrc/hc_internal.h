@@ -60,6 +60,7 @@ size_t set_phase_clocks(void* buf, size_t bytes);
 cudaError_t launch_sync_probe(int mode, int ctas, int rounds, size_t smem, unsigned int* scratch, cudaStream_t s);
 // One CTA whose bounded wait on an mbarrier that nothing completes runs out.
 cudaError_t launch_wait_timeout_probe(float* out, long long limit_cycles, cudaStream_t s);
+cudaError_t launch_wait_together_probe(float* out, unsigned int stuck, long long limit_cycles, cudaStream_t s);
 // Every 16-bit code through the fast rounded sigmoid and the accurate one.
 cudaError_t launch_sigmoid_codes(hc_dtype_t dt, uint16_t* fast, uint16_t* acc, cudaStream_t s);
 cudaError_t launch_sigmoid_table_codes(float* g, cudaStream_t s);

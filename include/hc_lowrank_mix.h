@@ -217,6 +217,14 @@ size_t hc_debug_phase_clocks(void* buf, size_t bytes);
  * range, HC_ERR_CUDA if the launch fails. */
 hc_status_t hc_debug_wait_timeout(float* out, long long limit_cycles, struct CUstream_st* stream);
 
+/* Diagnostic: the same for warps that go on together. Four warps of one CTA wait
+ * each by itself, those whose bit is set in `stuck` (0 .. 15) on an mbarrier that
+ * nothing arrives on, and then ask, as the experts' products do, whether all of
+ * them may go on. out[0..127] becomes 1.0f if no wait gave up, and NaN for every
+ * warp otherwise; each thread that gave up counts in hc_debug_wait_timeouts. The
+ * rest is as above. */
+hc_status_t hc_debug_wait_together(float* out, unsigned int stuck, long long limit_cycles, struct CUstream_st* stream);
+
 /* Diagnostic, with no counterpart on the page that defines the block: check of
  * the fast sigmoid the fp16/bf16 kernels use where the contract rounds
  * sigmoid(z) to T for a z that is itself a value of T (the ScaledSiLU gate and
