@@ -363,11 +363,13 @@ __device__ __noinline__ void add_excess(const hc_expert_mlp_t& p, const Excess& 
   for (int j = 0; j < 8; ++j) sums[j] = fmaf(weight, v[j], sums[j]);
 }
 
-// excess: of fp16 on the tensor cores, without values otherwise.
+// excess: of fp16 on the tensor cores, without values otherwise. gave_up: of the tensor cores' products, whether a wait has given
+// up (then all results become NaN), NULL otherwise.
 template <typename T, bool kPlanes>
 __global__ void __launch_bounds__(32 * kCombineWarps, 5)
 combine_kernel(const __grid_constant__ hc_expert_mlp_t p, const float* __restrict__ o, int64_t o_step,
-               const uint8_t* __restrict__ counts, int64_t count_step, const __grid_constant__ Excess excess, bool vec) {
+               const uint8_t* __restrict__ counts, int64_t count_step, const __grid_constant__ Excess excess,
+               const unsigned int* gave_up, bool vec) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, blocks = (p.hidden + 255) / 256;
@@ -383,7 +385,7 @@ combine_kernel(const __grid_constant__ hc_expert_mlp_t p, const float* __restric
   const int count = __popc(valid);
   T* out = static_cast<T*>(p.out) + t * p.out_stride;
   Two sums[4] = {Two(0.0f), Two(0.0f), Two(0.0f), Two(0.0f)};
-  const bool have = c < p.hidden;
+  const bool have = c < p.hidden, lost = gave_up != nullptr && *gave_up != 0;
   constexpr int kAhead = kPlanes ? 4 : 8;
   const int64_t plane = p.tokens * p.top_k * o_step;
   unsigned left = valid;
@@ -428,7 +430,7 @@ combine_kernel(const __grid_constant__ hc_expert_mlp_t p, const float* __restric
   float sum[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 v = sums[i].get();
+    const float2 v = lost ? make_float2(NAN, NAN) : sums[i].get();
     sum[2 * i] = v.x, sum[2 * i + 1] = v.y;
   }
   if constexpr (std::is_same<T, __half>::value) {
@@ -460,12 +462,14 @@ combine_kernel(const __grid_constant__ hc_expert_mlp_t p, const float* __restric
 // counts: NULL where o is one plane.
 template <typename T>
 cudaError_t launch_combine(const hc_expert_mlp_t& a, const float* o, int64_t o_step, const uint8_t* counts, int64_t count_step,
-                           const Excess& excess, cudaStream_t s) {
+                           const Excess& excess, const unsigned int* gave_up, cudaStream_t s) {
   const bool vec = a.hidden % 8 == 0 && a.out_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
   const int64_t units = a.tokens * ((a.hidden + 255) / 256);
   const dim3 grid(static_cast<unsigned>((units + kCombineWarps - 1) / kCombineWarps)), block(32 * kCombineWarps);
-  return counts != nullptr ? launch_pdl(combine_kernel<T, true>, grid, block, 0, s, 1, a, o, o_step, counts, count_step, excess, vec)
-                           : launch_pdl(combine_kernel<T, false>, grid, block, 0, s, 1, a, o, o_step, counts, count_step, excess, vec);
+  return counts != nullptr ? launch_pdl(combine_kernel<T, true>, grid, block, 0, s, 1, a, o, o_step, counts, count_step, excess, gave_up,
+                                        vec)
+                           : launch_pdl(combine_kernel<T, false>, grid, block, 0, s, 1, a, o, o_step, counts, count_step, excess, gave_up,
+                                        vec);
 }
 
 // ---------------------------------------------------------------- layout --
@@ -476,7 +480,7 @@ struct Plan {
   int planes;  // of o
   int64_t h_step, o_step, count_step;
   int64_t excess_step, excess_words;  // (fp16 on the tensor cores) of the excess of inner values, elements and words of bits to a pair
-  size_t bounds, order, zeros, part, h, o, counts, excess, total;  // zeros: tickets, and behind them the words of bits
+  size_t bounds, order, zeros, part, h, o, counts, excess, total;  // zeros: whether a wait gave up, tickets, and the words of bits
 };
 
 // Which products run, and where their buffers lie in the workspace. Tiles of 32 pairs with the weights as the first operand
@@ -510,7 +514,7 @@ Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
     l.excess_step = static_cast<int64_t>(align_up(a.inner, 128));
     l.excess_words = (a.inner + 1023) / 1024;
   }
-  l.zeros = take((l.tickets + pairs * l.excess_words) * sizeof(uint32_t));
+  l.zeros = take((1 + l.tickets + pairs * l.excess_words) * sizeof(uint32_t));
   if (few) {
     l.part = take(static_cast<size_t>(num_sms) * 2 * 2 * l.rows * 128 * sizeof(float));
   }
@@ -532,14 +536,14 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
   const Plan l = make_plan(a, aligned, num_sms);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const ExpertLists lists = {reinterpret_cast<int32_t*>(ws + l.bounds), reinterpret_cast<int32_t*>(ws + l.order)};
-  unsigned int* tickets = reinterpret_cast<unsigned int*>(ws + l.zeros);
+  unsigned int *zeros = reinterpret_cast<unsigned int*>(ws + l.zeros), *tickets = zeros + 1;
   float* o = reinterpret_cast<float*>(ws + l.o);
   const int pairs = static_cast<int>(a.tokens * a.top_k);
-  const int64_t count = l.tickets + pairs * l.excess_words;
+  const int64_t count = 1 + l.tickets + pairs * l.excess_words;
   cudaError_t e = pairs > 4096 ? launch_pdl(lists_kernel<1024>, dim3(a.num_experts), dim3(1024), 0, s, 1, a.experts, pairs,
-                                            a.num_experts, lists, tickets, count)
+                                            a.num_experts, lists, zeros, count)
                                : launch_pdl(lists_kernel<128>, dim3(a.num_experts), dim3(128), 0, s, 1, a.experts, pairs,
-                                            a.num_experts, lists, tickets, count);
+                                            a.num_experts, lists, zeros, count);
   if (e != cudaSuccess) return e;
   if constexpr (sizeof(T) == 2) {
     if (l.rows) {
@@ -547,16 +551,16 @@ template <typename T> cudaError_t launch(const hc_expert_mlp_t& a, bool aligned,
       const Excess excess = {l.excess_words ? reinterpret_cast<float*>(ws + l.excess) : nullptr, tickets + l.tickets, l.excess_step,
                              static_cast<int>(l.excess_words)};
       const ExpertUm u = {lists, ws + l.h, o, counts, l.h_step, l.o_step, l.count_step, reinterpret_cast<float*>(ws + l.part), tickets,
-                          excess, static_cast<int64_t>(pairs) * l.o_step, l.planes, l.rows};
+                          excess, zeros, static_cast<int64_t>(pairs) * l.o_step, l.planes, l.rows};
       e = l.rows == 256 ? launch_experts_many(a, u, num_sms, s) : launch_experts_few(a, u, num_sms, s);
-      return e != cudaSuccess ? e : launch_combine<T>(a, o, l.o_step, counts, l.count_step, excess, s);
+      return e != cudaSuccess ? e : launch_combine<T>(a, o, l.o_step, counts, l.count_step, excess, zeros, s);
     }
   }
   const GeneralArgs g = {a, lists, reinterpret_cast<float*>(ws + l.h), o, l.o_step};
   e = launch_general<T, true>(g, num_sms, s);
   if (e != cudaSuccess) return e;
   e = launch_general<T, false>(g, num_sms, s);
-  return e != cudaSuccess ? e : launch_combine<T>(a, o, l.o_step, nullptr, 0, Excess{}, s);
+  return e != cudaSuccess ? e : launch_combine<T>(a, o, l.o_step, nullptr, 0, Excess{}, nullptr, s);
 }
 
 }  // namespace

@@ -50,6 +50,7 @@ struct ExpertUm {
   float* part;             // partial sums of the inner product
   unsigned int* tickets;   // of the inner product's tiles; zero before the call
   Excess excess;           // (fp16)
+  unsigned int* gave_up;   // becomes 1 if a wait gave up; zero before the call
   int64_t plane;           // elements from plane to plane of o (few)
   int planes;
   int rows;                // pairs to a tile: 32 (few) or 256 (many)

@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(kThreads<kInner>, 2) few_kernel(const __grid_c
     }
     cp_async_wait_all();
   }
+  if (!ok) *a.gave_up = 1u;
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -345,6 +346,7 @@ bool fill_args(Args* a, const hc_expert_mlp_t& p, const ExpertUm& u, bool inner,
   a->bounds = u.lists.bounds;
   a->order = u.lists.order;
   a->excess = u.excess;
+  a->gave_up = u.gave_up;
   a->x = p.x;
   a->x_step = p.x_stride;
   a->out = inner ? u.h : static_cast<void*>(u.o);

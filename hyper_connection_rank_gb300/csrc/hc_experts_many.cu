@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kThreads<kInner>, 1) many_kernel(const __grid_
     }
     cp_async_wait_all();
   }
+  if (!ok) *a.gave_up = 1u;
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // (nothing is on its way to the other CTA any more)

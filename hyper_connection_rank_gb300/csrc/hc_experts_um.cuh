@@ -48,6 +48,7 @@ struct Args {
   int64_t plane;               // (few, outer) elements from plane to plane of out
   Excess excess;               // (inner, fp16)
   float* part;                 // (few, inner) [2 * CTAs][2 halves][rows][128], for tiles that a cut goes through
+  unsigned int* gave_up;       // becomes 1 if a wait gave up
   unsigned int* tickets;       // (few, inner) of each tile: pieces that have been written
   int experts, top_k, inputs, features, kblocks, fblocks, k_major;
   int most_parts;              // (few) that a tile may be cut into
