@@ -19,8 +19,10 @@
 // there: with copies of some row in their place the inner product took 75 us.)
 //
 // Of the pair, the first CTA issues the MMAs. The second one's stages are made known
-// to it by a warp that waits for them and arrives at the first one's barrier;
-// releases come by commits that arrive in both. All waits are bounded (see
+// to it by a warp that waits for them and arrives at the first one's barrier, behind
+// a fence that releases its CTA's shared memory to the cluster; the MMAs' thread
+// waits with acquire at that scope. Releases of stages come by commits that arrive
+// in both. All waits are bounded (see
 // hc_async.cuh).
 #include <algorithm>
 
@@ -70,9 +72,15 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-// Arrive at the first CTA's barrier.
+// Arrive at the first CTA's barrier, in order after tensor-memory loads before a tc_fence_before ...
 __device__ __forceinline__ void first_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_addr(bar), 0)) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_addr(bar), 0)) : "memory");
+}
+// ... or after the writes into this CTA's shared memory that this thread knows of (a releasing arrival would wait for all others, too,
+// and take twice as long as a stage).
+__device__ __forceinline__ void first_release(uint64_t* bar) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  first_arrive(bar);
 }
 
 template <typename T, bool kInner>
@@ -134,7 +142,7 @@ __global__ void __launch_bounds__(kThreads<kInner>, 1) many_kernel(const __grid_
           ok = mbar_wait(&b->full[st], (it / kStages) & 1, &g_many_wait_timeouts);
           if (!ok) break;
           if (kInner) fence_proxy_async();
-          first_arrive(&b->full[st]);
+          first_release(&b->full[st]);
         }
       }
     } else if (lane == 0) {
@@ -152,7 +160,7 @@ __global__ void __launch_bounds__(kThreads<kInner>, 1) many_kernel(const __grid_
         const uint32_t d = tmem + buf * kAccCols;
         for (int k = p.k0; k < p.k1; ++k, ++it) {
           const int st = it % kStages;
-          ok = mbar_wait(&b->full[st], (it / kStages) & 1, &g_many_wait_timeouts);
+          ok = mbar_wait_cluster(&b->full[st], (it / kStages) & 1, &g_many_wait_timeouts);
           if (!ok) break;
           if (kInner) fence_proxy_async();
           tc_fence_after();
