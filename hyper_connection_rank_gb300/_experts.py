@@ -79,7 +79,7 @@ def _weight(name, t, dtype, device):
         i = 1
     if i == 1 and o == 1:
         i, o = (max(shape[2], 1), 1) if shape[1] == 1 else (1, max(shape[1], 1))
-    return shape, (es, i, o)
+    return shape, (es if shape[0] > 1 else 0, i, o)
 
 
 def _mlp_args(x, gate_w, up_w, down_w, experts, weights, flags, out, out_step, work, size, device):

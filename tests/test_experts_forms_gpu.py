@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import _experts_ref as R
-from test_experts_gpu import BF16, F16, hc, ids, layer, within  # noqa: F401
+from test_experts_gpu import BF16, F16, hc, ids, layer, on_gpu, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,16 @@ def test_widths_that_eight_does_not_divide(hc, hidden, inner, tokens, rows_out, 
                       out=out[:, :hidden])
     within(y, *R.experts(*args, stored=False))
     assert (out[:, hidden:] == 7.0).all()
+
+
+# ------------------------------------------------------------------------------------------- a single expert --
+
+def test_strides_of_a_single_expert_say_nothing(hc):  # noqa: F811
+    """gate and up of one expert out of buffers whose experts lie at different steps."""
+    for tokens in (3, 70):
+        x, gate, up, down, e, w = layer(64, tokens, 1, 1, 64, 32, BF16)
+        g = torch.zeros(2, 64, 32, dtype=BF16, device="cuda")[:1].copy_(gate)
+        u = torch.zeros(2, 100, 32, dtype=BF16, device="cuda")[:1, :64].copy_(up)
+        assert g.stride() != u.stride()
+        y = hc.expert_mlp(x.cuda(), g, u, *on_gpu((down, e, w)))
+        within(y, *R.experts(x, gate, up, down, e, w))
