@@ -128,6 +128,12 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   return v;
 }
 
+// A barrier of a row's CTAs. Its instructions are the whole warp's, whose lanes part before it where they store for themselves.
+__device__ __forceinline__ void row_sync() {
+  __syncwarp();
+  cluster_sync_all();
+}
+
 __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -271,7 +277,7 @@ struct Row : Scale {
   __device__ __forceinline__ const u64* gather(u64 v) {
     turn ^= 1;
     if (threadIdx.x < ctas) st_cluster(mapa_shared(smem_addr(&sh.exchange[turn][rank]), threadIdx.x), v);
-    cluster_sync_all();
+    row_sync();
     return sh.exchange[turn];
   }
   // The same value for all threads of the CTA: the largest one.
@@ -314,7 +320,7 @@ struct Row : Scale {
   // The histograms of all CTAs together: into which bin the target falls (border[0]), what lies before it (border[1]) and
   // in it (border[2]). target(total) gives the target. The histogram is empty again afterwards.
   template <class F> __device__ __forceinline__ void find(F target) {
-    cluster_sync_all();
+    row_sync();
     const int mine = kBins / ctas, per = max(1, mine / kThreads), at = threadIdx.x * per;
     u64 v[kBins / kThreads], sum = 0;
 #pragma unroll
@@ -364,7 +370,7 @@ struct Row : Scale {
       }
       before += v[i];
     }
-    cluster_sync_all();
+    row_sync();
   }
 
   // Lists the elements of steps 0 .. bin where the first CTA's slice was, or (`only`) those of step bin that stay in place of
@@ -395,7 +401,7 @@ struct Row : Scale {
     const uint32_t to = mapa_shared(only ? smem_addr(sh.list) : smem_addr(xs), 0) + static_cast<uint32_t>(before) * 8;
     if (!only || rank > 0)
       for (uint32_t i = threadIdx.x; i < have; i += kThreads) st_cluster(to + 8 * i, sh.list[i]);
-    cluster_sync_all();
+    row_sync();
     return static_cast<int>(all);
   }
 
@@ -437,7 +443,7 @@ struct Row : Scale {
         before += v[j];
       }
     }
-    cluster_sync_all();
+    row_sync();
     cut_key = ~static_cast<uint32_t>(sh.border[3] >> 32);
     cut_index = static_cast<uint32_t>(sh.border[3]);
     for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
@@ -672,7 +678,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& a, Shared& sh, floa
     best = load_slice(static_cast<const __nv_bfloat16*>(a.logits) + r * a.stride, base, n, xs);
   // (every CTA of the cluster has begun, its histogram is empty and its parameters are there, before anything is stored into
   // its shared memory)
-  cluster_sync_all();
+  row_sync();
   const float t = sh.params.t, p = sh.params.p, u = sh.params.u;
   const int k = sh.params.k;
   const u64 least = sh.params.least;
@@ -961,11 +967,11 @@ template <typename T> __global__ void __launch_bounds__(kStreamThreads, kStreamC
   }
   int turn = 0;
   // every CTA has begun before anything is stored into its shared memory
-  cluster_sync_all();
+  row_sync();
   const auto gather = [&](u64 v) -> const u64* {
     turn ^= 1;
     if (tid < ctas) st_cluster(mapa_shared(smem_addr(&exchange[turn][rank]), tid), v);
-    cluster_sync_all();
+    row_sync();
     return exchange[turn];
   };
   if (lane == 0) red[warp] = key_of(most);
@@ -1084,9 +1090,15 @@ __device__ __forceinline__ void st_cluster32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// The halves of cluster_sync_all.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait_acquire() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The halves of row_sync.
+__device__ __forceinline__ void row_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void row_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 __device__ __forceinline__ uint2 ld_cluster2(uint32_t addr) {
   uint2 v;
@@ -1169,7 +1181,7 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
   for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
   cluster_wait();  // (every CTA has begun)
   if (tid < ctas) st_cluster(mapa_shared(smem_addr(&sh.tops[rank]), tid), best);
-  cluster_sync_all();
+  row_sync();
   for (int i = 0; i < ctas; ++i) best = max(best, sh.tops[i]);
   const Params& p = sh.params;
   const bool none = best == 0;
@@ -1188,14 +1200,14 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
   const uint32_t some = cut_k ? p.k : kTryP;
   if ((cut_k || cut_p) && some <= kMostK) {
     if (arg >= 0) atomicAdd(&sh.hist[mine], 1u);
-    cluster_arrive();
+    row_arrive();
     if (cut_p && !cut_k) {  // (while the others come)
       u64 sum = 0;
       visit([&](int, float x) { sum += scale.weight(x); });
       sum = pick_sum(sh, sum);
       if (tid < ctas) st_cluster(mapa_shared(smem_addr(&sh.sums[rank]), tid), sum);
     }
-    cluster_wait_acquire();
+    row_wait();
     __syncthreads();  // (that sum is read by all)
     if (rank == 0) {
       uint32_t n0 = 0, n1 = 0;
@@ -1224,7 +1236,7 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
         }
       }
     }
-    cluster_sync_all();
+    row_sync();
     // (fewer threads than that have a logit: all steps, unless min_p has a say)
     bin = min(bin, sh.border < 0 ? kBins : sh.border);
   }
@@ -1258,7 +1270,7 @@ template <typename T> __global__ void __launch_bounds__(kPickThreads, 1) pick_ke
         });
     }
   }
-  cluster_sync_all();
+  row_sync();
   if (rank != 0) return;
   const int count = static_cast<int>(sh.listed);
   if (count > kPicked) {
