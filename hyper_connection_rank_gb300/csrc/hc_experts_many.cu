@@ -10,9 +10,10 @@
 // tensor cores' cycles). Accumulators take turns, so that a tile is written while
 // the next one is multiplied. Whole tiles are dealt out in turn.
 //
-// 8191 tokens at eight of 64 experts of 2560 x 640 in bf16: 294 to 305 us (inner, 1.42 PFLOP/s, 75% of measured) and 195 (outer, 1.10:
-// its 671 MB of results leave at 3.4 TB/s beside L2's feed of the stages), the inner one's tensor cores active for 75% of the cycles; a stage takes 0.32 us where the MMAs take 0.27, and tiles are 90% full. 1301
-// tokens at two of 16 experts of 1280 x 2560 in fp16: 58 and 36 us, 3.6 and 2.9 TB/s of weights; tiles are half full, 20
+// 8191 tokens at eight of 64 experts of 2560 x 640 in bf16: 294 to 307 us (inner, 1.42 PFLOP/s, 75% of measured; tensor cores active
+// for 74% of the cycles) and 195 (outer, 1.10; 55%: 671 MB of results leave at 3.4 TB/s beside L2's feed of the stages); a stage takes
+// 0.32 us where the MMAs take 0.27, and tiles are 90% full. 1301 tokens at two of 16 experts of 1280 x 2560 in fp16: 60 and
+// 39 us, 3.5 and 2.7 TB/s of weights; tiles are half full, 20
 // tiles of pairs by 20 and 5 of features are 5.3 and 1.3 rounds of 76 pairs of CTAs, and the first two tiles of each wait for cold
 // weights. (Sending those to L2 earlier, by TMA or by the gathering warps, took 10 to 20% longer: both have no time to spare.
 // For the same reason the gathering warps copy full tiles without a look at their rows, and nothing for rows that are not

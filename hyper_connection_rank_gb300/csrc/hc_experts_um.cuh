@@ -7,6 +7,10 @@
 //   inner  h = silu(x gate) * (x up), rows of x gathered by the list of pairs
 //   outer  o = h down, rows of h in the list's order
 //
+// h is rounded to T, which the tensor core's operands are: results are off by 2.3e-3 of their size against 64 bits in bf16 and
+// 2.9e-4 in fp16, where rounding them alone costs 1.65e-3 and 2.1e-4. (What the rounding takes off as a second operand
+// would give that back for twice the outer product's MMAs, which where experts have many pairs set its pace.)
+//
 // A tile is a number of pairs of one expert by two halves of 128 features: the
 // gate's and the up projection's for the inner product, 256 features for the outer
 // one. A stage of a CTA's ring holds 64 inputs (a row of 128 bytes, in 128-byte

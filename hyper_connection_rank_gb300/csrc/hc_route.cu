@@ -10,8 +10,9 @@
 // in the order, the last that is taken and the first that is not) are ordered by themselves in fp64, which runs at 1/64 of
 // fp32's rate here: doing all rows that way would cost ten times the rest.
 //
-// Bound: issue slots and latency, not bytes. 8191 tokens and 256 experts in eight groups, two of whose values count, take 15.8
-// us with their bias (8.9 MB: 1.3 us), 54% of the ALU's slots; one token and 128 experts 3.3 us, a launch. (A maximum and then the
+// Bound: latency, not bytes. 8191 tokens and 256 experts in eight groups, two of whose values count, take 15.7 us with their bias
+// (8.9 MB: 1.3 us): issue slots are active in 41% of the cycles (58% of those in which an SM has warps), the ALU in 54% of the
+// latter; a warp's top_k maxima wait for one another, and 2048 CTAs of 64 registers a thread are 1.7 rounds. One token and 128 experts 3.3 us, a launch. (A maximum and then the
 // lowest index that has it: 27 us. All of a row again in fp64 where two neighbours are too close: 19.)
 #include <cmath>
 

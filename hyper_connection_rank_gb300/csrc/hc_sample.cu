@@ -800,8 +800,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int ctas
 // within 2^-30 of itself (equal logits have equal weights). Chunks' sums are then shifted to the row's largest n and added,
 // and the chunk in which they pass uniform * sum is read again by one warp.
 //
-// Bound: instructions, some 29 to a logit where two logits share the packed ones. 256 rows of 200003 fp32 logits (205 MB) take
-// 76 us here and 84 with what follows, 2.4 TB/s; their bytes alone would take 30. (With no loads ahead of the chunk that is
+// Bound: latency of some 29 instructions to a logit, where two logits share the packed ones. 256 rows of 200003 fp32 logits (205 MB) take
+// 76 us here and 84 with what follows, 2.4 TB/s; their bytes alone would take 30. Issue slots are active in 51% of the cycles (58% of
+// those in which an SM has warps); a warp waits longest for the pipe of the packed instructions, which hold it twice as long, and
+// for its own last result, and 20 of the 28 warps that fit an SM are there on average. (With no loads ahead of the chunk that is
 // weighed it was 93. fp32 sums of the exponential unit's weights are quicker, but in every call some rows are then too close to
 // decide, and those rows' exact pass takes longer than all others.)
 //
