@@ -487,9 +487,9 @@ struct Plan {
 
 // Which products run, and where their buffers lie in the workspace. Tiles of 32 pairs with the weights as the first operand
 // or of 256 with the pairs as the first, by the pairs that an expert has on average: with 8, 16, 24, 28, 32 and 40 of them, 64
-// experts of 2560 x 640 (six to a token) took 113, 125, 134, 142, 170 and 202 us with 32 and 133, 136, 137, 137, 138 and 140 with
-// 256; 128 of 1024 x 512 (eight to a token) 83, 87, 96, 101, 114 and 139, and 94, 96, 98, 99, 100 and 101; 16 of 1280 x 2560 (two)
-// 63, 75, 71, 76, 84 and 88, and 67, 69, 69, 85, 85 and 85; 8 of 512 x 1024 (two) 21, 24, 25, 22, 22 and 22, and 25 throughout.
+// experts of 2560 x 640 (six to a token) took 111, 121, 131, 137, 164 and 194 us with 32 and 128, 133, 135, 136, 139 and 143 with
+// 256; 128 of 1024 x 512 (eight to a token) 81, 84, 93, 99, 110 and 135, and 90, 92, 95, 96, 98 and 100; 16 of 1280 x 2560 (two)
+// 63, 75, 70, 75, 84 and 87, and 65, 66, 66, 86, 86 and 86; 8 of 512 x 1024 (two) 20, 24, 25, 22, 22 and 22, and 23 throughout.
 Plan make_plan(const hc_expert_mlp_t& a, bool aligned, int num_sms) {
   const size_t pairs = static_cast<size_t>(a.tokens) * a.top_k;
   Plan l = {};
