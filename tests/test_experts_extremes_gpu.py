@@ -110,6 +110,38 @@ def test_some_inner_values_past_the_largest_float16(hc, tokens, inner, rows_out,
     assert torch.equal(z[1:], y[1:]) and not torch.isfinite(z[0]).any()
 
 
+@pytest.mark.parametrize("tokens", [30, 300])
+def test_excess_of_a_captured_call(hc, tokens):  # noqa: F811
+    """Values past float16 in some replays and not in others, in a workspace that held anything before; the same expert several
+    times for a token, widths that eight does not divide, more than 1024 inner values."""
+    hidden, inner, k = 131, 1050, 5
+    x, gate, up, down, e, w = layer(65, tokens, 4, 4, 136, 1056, F16)
+    e, w = torch.cat((e, e[:, :1]), 1), torch.cat((w, w[:, 1:2]), 1)
+    down = down * 2.0 ** -9
+    gpu = on_gpu((x, gate, up, down, e, w))
+    cut = lambda x, g, u, d, e, w: (x[:, :hidden], g[:, :hidden, :inner], u[:, :hidden, :inner], d[:, :inner, :hidden], e, w)  # noqa: E731
+    args = cut(*gpu)
+    assert args[4].shape[1] == k
+    work = torch.empty(hc.expert_mlp_workspace_size(*args), dtype=torch.uint8, device="cuda").random_(0, 256)
+    hc.expert_mlp(*args, workspace=work)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = hc.expert_mlp(*args, workspace=work)
+    for by in (300.0, 1.0, 200.0):
+        scaled = x.clone()
+        scaled[1::4] = scaled[1::4] * by
+        gpu[0].copy_(scaled)
+        graph.replay()
+        cpu = cut(scaled, gate, up, down, e, w)
+        want, tol = R.experts(*cpu, stored=False)
+        past = max((v @ gate[0, :hidden, :inner].double() * (v @ up[0, :hidden, :inner].double())).abs().max() for v in [cpu[0].double()])
+        assert (past > 65504) == (by > 1)
+        within(y, want, tol)
+        first = y.clone()
+        graph.replay()
+        assert torch.equal(first, y)
+
+
 # -------------------------------------------------------------------------------------------------- routing --
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
