@@ -78,7 +78,7 @@ hc_status_t hc_expert_route(const hc_expert_route_t* args, struct CUstream_st* s
  *
  * Numerics: products are summed in fp32. In the fp16/bf16 kernels the inner
  * values silu(.) * (.) are rounded to T for the product with down (the tensor
- * core's operands are 16 bits). Each chosen expert's result is fp32, and so is
+ * core's operands are 16 bits; a value below 2^-251 of its x up is 0). Each chosen expert's result is fp32, and so is
  * the sum over them, rounded to T once. Finite inner values beyond
  * fp16's largest one count in full: what that leaves of them is multiplied with
  * down in fp32, a row of down for each. Limits: top_k <= 32, num_experts <= 1024,
